@@ -60,7 +60,11 @@ enum {
     QW_ERR_CUDA = -6,               /* a CUDA runtime call failed */
     QW_ERR_TIMEOUT = -7,            /* (device) a pipeline wait exceeded its limit */
     QW_ERR_BAD_CODES = -8,          /* (device) qpack_w4 saw a code outside [-8, 7] */
-    QW_ERR_BAD_INDEX = -9           /* (device) embed_gather_w8 saw a row id outside [0, V) */
+    QW_ERR_BAD_INDEX = -9,          /* (device) an id outside its range: embed_gather_w8 a row id,
+                                       the paged cache a page id, a length beyond its page table or
+                                       token offsets out of order, token_logprobs a token */
+    QW_ERR_NO_PAGES = -10,          /* kv_pool_extend: fewer free pages than needed */
+    QW_ERR_HOST_MEMORY = -11        /* kv_pool_*: no host memory */
 };
 
 enum { QW_MODE_W4A16 = 0, QW_MODE_W4A8 = 1, QW_MODE_W8A16 = 2, QW_MODE_W4A8_FUSED = 3 };
@@ -255,6 +259,161 @@ size_t attn_int8qk_workspace_bytes(int T, int S, int Hq, int Hkv, int d);
 int attn_int8qk_workspace_layout(int T, int S, int Hq, int Hkv, int d, size_t *offsets);
 int attn_int8qk_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, int T, int S, int Hq,
                         int Hkv, int d, uint16_t *out, void *ws, size_t ws_bytes, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The paged key-value cache of one layer: pages of `page` tokens, each page holding every
+ * KV head's rows of those tokens.  Row (page p, KV head g, token r) of K and of V starts at
+ * element p * page_stride + g * head_stride + r * token_stride of k and of v (the same
+ * strides for both) and has d contiguous elements.  Any page size >= 1; d = 64, 128 or 256;
+ * rows start on 16-byte boundaries.
+ *   QW_KV_F16, QW_KV_BF16: 16-bit values.
+ *   QW_KV_INT8: int8 codes with a binary32 scale a row, value = code * scale; k_scale and
+ *     v_scale [num_pages][Hkv][page], dense.  The activations beside it are fp16.
+ *
+ * A batch: sequence b's keys are, in order, the pages page_table[b][0 ..] (int32
+ * [B][max_pages]); seq_lens[b] (int32 [B]) is its length WITH this step's new tokens, which
+ * are its last positions and are rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of q, k, v and
+ * out (int32 [B + 1], ascending, from 0).  All in device memory; nothing is read on the host,
+ * so a captured graph follows lengths that change.  Pages of different sequences may be the
+ * same (a shared prefix), except those that kv_append writes to.
+ * ------------------------------------------------------------------------ */
+enum { QW_KV_F16 = 0, QW_KV_BF16 = 1, QW_KV_INT8 = 2 };
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;       /* QW_KV_INT8 */
+    int dtype, num_pages, page, Hkv, d;
+    long long page_stride, head_stride, token_stride;   /* elements */
+} qw_kv_cache_t;
+typedef struct {
+    const int32_t *page_table, *seq_lens, *cu_tokens;
+    int B, max_pages;
+} qw_kv_batch_t;
+
+/* ------------------------------------------------------------------------
+ * kv_append -- writes the new tokens' rows of K and V into their pages.
+ *   k, v: [T][Hkv][d] with the given token and head strides in elements (multiples of 8;
+ *   slices of a fused projection's output are fine), fp16 or bf16 as the cache (QW_KV_INT8:
+ *   fp16; each row is quantized as quant_act_int8 does it: scale = amax / 127, code =
+ *   rne(x / scale), a row of zeros scale 0), 16-byte aligned.
+ * A token whose page is missing (a position before 0 or past the table, a page id outside
+ * [0, num_pages)) is skipped and sets QW_ERR_BAD_INDEX.  One launch, async.  Returns QW_OK,
+ * QW_ERR_INVALID_ARG, QW_ERR_UNSUPPORTED_SHAPE, QW_ERR_ALIGNMENT, QW_ERR_ARCH or QW_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int kv_append(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const uint16_t *k, const uint16_t *v, int T,
+              long long k_token_stride, long long k_head_stride, long long v_token_stride,
+              long long v_head_stride, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_copy_pages -- for every pair (source, destination) of pages (int32 [n][2], device,
+ * 8-byte aligned), in every layer of up to four pools (K, V and their scales): the
+ * destination's bytes become the source's.
+ * No page may be a destination twice, nor both a source and a destination (the pairs of
+ * kv_pool_extend and kv_pool_compact are so).  A pair naming a page outside its pool is
+ * skipped and sets QW_ERR_BAD_INDEX.
+ *   base: the pool's first page; page p of layer l is the page_bytes bytes at
+ *   base + l * layer_stride + p * page_stride (strides in bytes, all multiples of 4; 16
+ *   bytes at a time where they and base allow).
+ * One launch for all pools and layers, async.  Returns as kv_append.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *base;
+    int layers, num_pages;
+    long long layer_stride, page_stride, page_bytes;
+} qw_page_pool_t;
+int kv_copy_pages(const qw_page_pool_t *pools, int n_pools, const int32_t *pairs, int n, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * attn_paged -- attention of each sequence's new tokens (one in a decode step, a few in a
+ * speculative verify, any number) over its cache, which already holds them:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax over the visible j of (q[t][h] . k_j) * scale,
+ * query head h reading KV head h / (Hq / Hkv).  The token at position i sees key j when
+ * j <= i and, if window > 0, also j > i - window or j < sinks (the first tokens that stay
+ * visible).  A token that sees nothing gives a row of zeros.
+ *   q [T][Hq][d] with token and head strides in elements (multiples of 8), 16-byte aligned,
+ *   fp16 or bf16 as the cache (QW_KV_INT8: fp16); out [T][Hq][d] dense, the same type,
+ *   16-byte aligned; rows of no sequence are left as they are.
+ *   lse: NULL, or binary32 [T][Hq]: the natural logarithm of the sum of exponentials
+ *   (-inf for a token that sees nothing), with which parts over other keys can be joined.
+ *   max_new >= 1: the most new tokens of a sequence.  A hint: it sets how many query rows a
+ *   CTA takes at a time, and with it the workspace; more tokens are still computed, at the
+ *   price of reading the keys again.
+ *   ws: attn_paged_workspace_bytes(d, Hq, Hkv, max_new) bytes, 256-byte aligned, zero-filled
+ *   once (the first attn_paged_workspace_zero_bytes stay zero after every call); shared by
+ *   attn_paged calls of any shape, not by calls that may run concurrently nor by other
+ *   entry points.
+ * Values of keys that a token does not see never reach its row, whatever they hold.  A page
+ * id outside [0, num_pages) reads as rows of zeros, a length beyond the page table as the
+ * table's end, and either sets QW_ERR_BAD_INDEX.  Results are bit-identical between calls
+ * (on devices with the same number of SMs).  One launch, async.  Returns as kv_append, or
+ * QW_ERR_WORKSPACE.
+ * ------------------------------------------------------------------------ */
+size_t attn_paged_workspace_bytes(int d, int Hq, int Hkv, int max_new);
+size_t attn_paged_workspace_zero_bytes(int d, int Hq, int Hkv, int max_new);
+int attn_paged(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const uint16_t *q, int T, int Hq,
+               long long q_token_stride, long long q_head_stride, int max_new, int window, int sinks, float scale,
+               uint16_t *out, float *lse, void *ws, size_t ws_bytes, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_pool -- which pages hold which sequence, on the host (no device access; calls on one
+ * pool are serialized by a lock).  Pages carry reference counts: a fork shares its parent's
+ * pages, and kv_pool_extend gives a sequence a page of its own before it writes to a shared,
+ * partly filled one.  Free pages are handed out lowest first.
+ *   kv_pool_create    a pool of num_pages pages of `page` tokens.
+ *   kv_pool_add       *seq = a new sequence of length 0.
+ *   kv_pool_extend    lengthens a sequence by n_tokens; pair: room for one (source,
+ *                     destination) pair, *n_pairs 0 or 1: a copy that has to be enqueued
+ *                     (kv_copy_pages) before the new tokens are written.  QW_ERR_NO_PAGES
+ *                     leaves everything as it was.  The pairs of several extends may go into
+ *                     one copy if no sequence was forked, truncated or freed between them.
+ *   kv_pool_truncate  shortens it (rejected tokens), kv_pool_free gives it up,
+ *   kv_pool_fork      *child = a new sequence with the same pages and length.
+ *   kv_pool_compact   moves live pages into the lowest free ones, at most `cap` of them
+ *                     (*n_pairs pairs to copy before anything else; page tables written
+ *                     earlier are stale).  With cap >= the live pages the live ones end up
+ *                     first.
+ *   kv_pool_table     host arrays table [B][max_pages] (unused entries 0) and lens [B] of B
+ *                     sequences.
+ *   kv_pool_pages     a sequence's length and page count; kv_pool_free_pages how many pages
+ *                     are free (>= 0), or an error.
+ * Return QW_OK, QW_ERR_INVALID_ARG (also for a sequence that does not exist),
+ * QW_ERR_UNSUPPORTED_SHAPE, QW_ERR_NO_PAGES or QW_ERR_HOST_MEMORY.
+ * ------------------------------------------------------------------------ */
+typedef struct kv_pool kv_pool_t;
+int kv_pool_create(int num_pages, int page, kv_pool_t **out);
+void kv_pool_destroy(kv_pool_t *pool);
+int kv_pool_add(kv_pool_t *pool, int *seq);
+int kv_pool_extend(kv_pool_t *pool, int seq, int n_tokens, int32_t *pair, int *n_pairs);
+int kv_pool_truncate(kv_pool_t *pool, int seq, int len);
+int kv_pool_fork(kv_pool_t *pool, int seq, int *child);
+int kv_pool_free(kv_pool_t *pool, int seq);
+int kv_pool_compact(kv_pool_t *pool, int32_t *pairs, int cap, int *n_pairs);
+int kv_pool_table(kv_pool_t *pool, const int32_t *seqs, int B, int max_pages, int32_t *table, int32_t *lens);
+int kv_pool_pages(kv_pool_t *pool, int seq, int *len, int *pages);
+int kv_pool_free_pages(kv_pool_t *pool);
+
+/* ------------------------------------------------------------------------
+ * token_logprobs -- per row of an [M, N] logit matrix (the lm_head's output, with or without
+ * a mask of -inf), in one pass:
+ *   lse[m]          logsumexp(x)                       (-inf when every logit is -inf)
+ *   entropy[m]      -sum p log p, natural logarithm    (0 when every logit is -inf)
+ *   logprob[m][c]   x[tokens[m][c]] - lse for C given tokens (a token outside [0, N): NaN,
+ *                   and QW_ERR_BAD_INDEX)
+ *   top_logprob, top_idx [m][k]   the k most likely tokens, most likely first, equal logits
+ *                   by the smaller index (-0 equals +0)
+ *   logits: fp16, bf16 or binary32 (dtype QW_F16, QW_BF16, QW_F32), row m at
+ *   logits + m * row_stride elements; any alignment and any 1 <= N <= 2^30.  -inf is a
+ *   probability of 0; NaN and +inf give NaN sums.  0 <= k <= min(64, N).
+ *   tokens [M][C]: token_bytes 4 (int32) or 8 (int64); C may be 0.
+ *   ws: token_logprobs_workspace_bytes(M, N, k, dtype) bytes, 256-byte aligned, zero-filled
+ *   once (the first ..._zero_bytes stay zero after every call); shared as attn_paged's.
+ * One launch, async.  Sums in binary32, joined in a fixed order.  Returns as attn_paged.
+ * ------------------------------------------------------------------------ */
+enum { QW_F16 = 0, QW_BF16 = 1, QW_F32 = 2 };
+size_t token_logprobs_workspace_bytes(int M, int N, int k, int dtype);
+size_t token_logprobs_workspace_zero_bytes(int M, int N, int k, int dtype);
+int token_logprobs(const void *logits, int dtype, int M, int N, long long row_stride, const void *tokens,
+                   int token_bytes, int C, int k, float *logprob, float *entropy, float *lse, float *top_logprob,
+                   int32_t *top_idx, void *ws, size_t ws_bytes, qw_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * qgemm_w4a8_fused -- the W4A8 layer from fp16 activations: y is bit-identical

@@ -10,12 +10,18 @@ Entry points (same names as the C ABI):
     qgemm_w4a8_fused(x, packed, N, K) -> y
     qgemm_w8a16(x, packed, N, K) -> y
     embed_gather_w8(ids, packed, V, D) -> out        topk_logits(logits, k) -> (vals, idx)
+    kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_tokens)
+    attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens) -> out
+    kv_copy_pages(pairs, *pools)                     KvPool: pages of sequences, on the host
+    token_logprobs(logits, tokens, k) -> TokenLogprobs
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +38,10 @@ QW_ERR_CUDA = -6
 QW_ERR_TIMEOUT = -7
 QW_ERR_BAD_CODES = -8
 QW_ERR_BAD_INDEX = -9
+QW_ERR_NO_PAGES = -10
+QW_ERR_HOST_MEMORY = -11
+QW_KV_F16, QW_KV_BF16, QW_KV_INT8 = 0, 1, 2
+QW_F16, QW_BF16, QW_F32 = 0, 1, 2
 MODE_W4A16, MODE_W4A8, MODE_W8A16, MODE_W4A8_FUSED = 0, 1, 2, 3
 
 # every function the header declares: name -> (restype, argtypes)
@@ -45,6 +55,23 @@ class Plan(ctypes.Structure):
                 ("act_stages", _i), ("act_block", _i), ("fused", _i), ("decode_teams", _i),
                 ("decode_row_blocks", _i)]
 
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("dtype", _i), ("num_pages", _i),
+                ("page", _i), ("Hkv", _i), ("d", _i), ("page_stride", _ll), ("head_stride", _ll),
+                ("token_stride", _ll)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    _fields_ = [("page_table", _p), ("seq_lens", _p), ("cu_tokens", _p), ("B", _i), ("max_pages", _i)]
+
+
+class PagePoolDesc(ctypes.Structure):
+    _fields_ = [("base", _p), ("layers", _i), ("num_pages", _i), ("layer_stride", _ll), ("page_stride", _ll),
+                ("page_bytes", _ll)]
+
+
+_ip = ctypes.POINTER(ctypes.c_int)
 
 SIGNATURES = {
     "qpack_w4_bytes": (_sz, [_i, _i]),
@@ -69,6 +96,26 @@ SIGNATURES = {
     "attn_int8qk_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "attn_int8qk_workspace_layout": (_i, [_i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)]),
     "attn_int8qk_prefill": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _sz, _p]),
+    "kv_append": (_i, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _p, _p, _i, _ll, _ll, _ll, _ll, _p]),
+    "kv_copy_pages": (_i, [ctypes.POINTER(PagePoolDesc), _i, _p, _i, _p]),
+    "attn_paged_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "attn_paged_workspace_zero_bytes": (_sz, [_i, _i, _i, _i]),
+    "attn_paged": (_i, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _p, _i, _i, _ll, _ll, _i, _i, _i,
+                        ctypes.c_float, _p, _p, _p, _sz, _p]),
+    "kv_pool_create": (_i, [_i, _i, ctypes.POINTER(_p)]),
+    "kv_pool_destroy": (None, [_p]),
+    "kv_pool_add": (_i, [_p, _ip]),
+    "kv_pool_extend": (_i, [_p, _i, _i, _p, _ip]),
+    "kv_pool_truncate": (_i, [_p, _i, _i]),
+    "kv_pool_fork": (_i, [_p, _i, _ip]),
+    "kv_pool_free": (_i, [_p, _i]),
+    "kv_pool_compact": (_i, [_p, _p, _i, _ip]),
+    "kv_pool_table": (_i, [_p, _p, _i, _i, _p, _p]),
+    "kv_pool_pages": (_i, [_p, _i, _ip, _ip]),
+    "kv_pool_free_pages": (_i, [_p]),
+    "token_logprobs_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "token_logprobs_workspace_zero_bytes": (_sz, [_i, _i, _i, _i]),
+    "token_logprobs": (_i, [_p, _i, _i, _i, _ll, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "qw_last_error_string": (ctypes.c_char_p, []),
     "qw_device_error": (_i, [_p]),
     "qw_num_kernel_launches": (_ll, []),
@@ -431,6 +478,273 @@ def topk_logits(logits, k: int):
         _check(lib().topk_logits(_ptr(logits), M, N, k, _ptr(vals), _ptr(idx), _ptr(buf), buf.numel(),
                                  _stream(logits)))
     return vals, idx
+
+
+# ------------------------------------------------------------ paged cache --
+_KV_TYPES = {torch.float16: QW_KV_F16, torch.bfloat16: QW_KV_BF16, torch.int8: QW_KV_INT8}
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on the current stream of `dev`, with `dev` current."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _scratch(ws, dev, kind, query, *args):
+    """(buffer, bytes) of `ws`, or of the default workspace of this kind of call and stream."""
+    if ws is None:
+        key = (dev, torch.cuda.current_stream(dev).cuda_stream, kind)
+        ws = _default_ws.get(key)
+        if ws is None:
+            ws = _default_ws.setdefault(key, Workspace(dev))
+    if dev.index == torch.cuda.current_device():
+        need = int(query(*args))
+    else:
+        with torch.cuda.device(dev):
+            need = int(query(*args))
+    return ws.get_bytes(need)
+
+
+def _kv_cache(k_pages, v_pages, k_scale, v_scale):
+    """The descriptor of one layer's cache (k_pages, v_pages [pages, Hkv, page, d])."""
+    dtype = _KV_TYPES.get(k_pages.dtype)
+    if dtype is None or v_pages.dtype != k_pages.dtype:
+        raise TypeError("k_pages and v_pages must both be float16, bfloat16 or int8")
+    if not (k_pages.is_cuda and v_pages.device == k_pages.device):
+        raise TypeError("k_pages and v_pages must be CUDA tensors on one device")
+    shape, stride = k_pages.shape, k_pages.stride()
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("k_pages and v_pages must have one shape [pages, Hkv, page, d]")
+    if v_pages.stride() != stride or stride[3] != 1:
+        raise ValueError("k_pages and v_pages must have the same strides, the last dimension contiguous")
+    ks = vs = None
+    if dtype == QW_KV_INT8:
+        for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(s, torch.float32, name, 3)
+            _need_shape(s, shape[:3], name)
+            if s.device != k_pages.device:
+                raise ValueError(f"{name} is on {s.device}, the cache on {k_pages.device}")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("only an int8 cache has scales")
+    return KvCacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, dtype, shape[0], shape[2], shape[1], shape[3],
+                       stride[0], stride[1], stride[2])
+
+
+def _kv_batch(page_table, seq_lens, cu_tokens, dev):
+    for t, name, nd in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1), (cu_tokens, "cu_tokens", 1)):
+        if t.dtype != torch.int32 or t.dim() != nd or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {nd} dimension(s) on {dev}")
+    B = page_table.shape[0]
+    if seq_lens.shape[0] != B or cu_tokens.shape[0] != B + 1:
+        raise ValueError("page_table [B, max_pages], seq_lens [B] and cu_tokens [B + 1] disagree")
+    return KvBatchDesc(page_table.data_ptr(), seq_lens.data_ptr(), cu_tokens.data_ptr(), B, page_table.shape[1])
+
+
+def _rows(t, name, cache, dev, heads=None):
+    """Checks new tokens' rows [T, heads, d] (strided, d contiguous); returns the two strides."""
+    want = torch.bfloat16 if cache.dtype == QW_KV_BF16 else torch.float16
+    if t.dtype != want or t.device != dev:
+        raise TypeError(f"{name} must be {want} on {dev}, got {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.shape[2] != cache.d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads or 'Hq'}, {cache.d}], got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return s[0], s[1]
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_tokens, k_scale=None, v_scale=None):
+    """Writes the new tokens' k and v [T, Hkv, d] into their pages (k_pages, v_pages
+    [pages, Hkv, page, d]; an int8 cache has scales [pages, Hkv, page] float32 and quantizes
+    each row).  Sequence b's new tokens are rows cu_tokens[b] .. cu_tokens[b + 1] - 1 and its
+    last positions; seq_lens counts them already."""
+    dev = k_pages.device
+    c = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    b = _kv_batch(page_table, seq_lens, cu_tokens, dev)
+    kt, kh = _rows(k, "k", c, dev, c.Hkv)
+    vt, vh = _rows(v, "v", c, dev, c.Hkv)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same number of tokens")
+    _launch(dev, lib().kv_append, c, b, k.data_ptr(), v.data_ptr(), k.shape[0], kt, kh, vt, vh)
+
+
+def kv_copy_pages(pairs, *pools):
+    """For every (source, destination) of pairs (int32 [n, 2], device): copies the page in
+    each pool and layer.  A pool is a tensor whose leading dimensions are [pages] or
+    [layers, pages] -- 4 or 5 dimensions for K and V, 3 or 4 (float32) for the scales of an
+    int8 cache -- and whose pages are dense.  No page may be a destination twice, nor both a
+    source and a destination."""
+    _need(pairs, torch.int32, "pairs", 2)
+    if pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    if not 1 <= len(pools) <= 4:
+        raise ValueError("one to four pools")
+    desc = (PagePoolDesc * len(pools))()
+    for i, x in enumerate(pools):
+        if x.device != pairs.device:
+            raise ValueError(f"pool {i} is on {x.device}, the pairs on {pairs.device}")
+        inner = 2 if x.dtype == torch.float32 else 3
+        lead = x.dim() - inner
+        if lead not in (1, 2):
+            raise ValueError(f"pool {i}: [pages, ...] or [layers, pages, ...] with {inner} dimensions a page")
+        es, shape, stride = x.element_size(), x.shape, x.stride()
+        dense = 1
+        for st, n in sorted(zip(stride[lead:], shape[lead:])):
+            if n != 1 and st != dense:
+                raise ValueError(f"pool {i}: a page must be one dense block")
+            dense *= n
+        layers, layer_stride = (1, 0) if lead == 1 else (shape[0], stride[0])
+        desc[i] = PagePoolDesc(x.data_ptr(), layers, shape[lead - 1], layer_stride * es, stride[lead - 1] * es,
+                               dense * es)
+    _launch(pairs.device, lib().kv_copy_pages, desc, len(pools), pairs.data_ptr(), pairs.shape[0])
+
+
+def attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, max_new: int = 1, window: int = 0, sinks: int = 0,
+               scale: float | None = None, k_scale=None, v_scale=None, out=None, lse=None,
+               ws: Workspace | None = None):
+    """Attention of the new tokens q [T, Hq, d] over the paged cache, which holds them
+    already: out [T, Hq, d].  The token at position i sees keys j <= i and, with window > 0,
+    j > i - window or j < sinks.  max_new: the most new tokens of a sequence (a hint).
+    scale: 1 / sqrt(d) unless given.  lse: a float32 [T, Hq] tensor to fill with the log of
+    the sum of exponentials; then (out, lse) is returned."""
+    dev = k_pages.device
+    c = _kv_cache(k_pages, v_pages, k_scale, v_scale)
+    b = _kv_batch(page_table, seq_lens, cu_tokens, dev)
+    qt, qh = _rows(q, "q", c, dev)
+    T, Hq, d = q.shape
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(q.shape)} on {dev}")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        _need_shape(lse, (T, Hq), "lse")
+        if lse.device != dev:
+            raise ValueError(f"lse is on {lse.device}, the cache on {dev}")
+    L = lib()
+    buf, nbytes = _scratch(ws, dev, "paged", L.attn_paged_workspace_bytes, d, Hq, c.Hkv, max_new)
+    _launch(dev, L.attn_paged, c, b, q.data_ptr(), T, Hq, qt, qh, max_new, window, sinks,
+            1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if buf is None else buf.data_ptr(), nbytes)
+    return out if lse is None else (out, lse)
+
+
+class KvPool:
+    """Which pages hold which sequence (host side, include/qgemm.h kv_pool_*).  Sequences are
+    small integers.  Copies come back as [source, destination] lists; enqueue them with
+    kv_copy_pages before the step writes its tokens."""
+
+    def __init__(self, num_pages: int, page: int):
+        h = ctypes.c_void_p()
+        _check(lib().kv_pool_create(num_pages, page, ctypes.byref(h)))
+        self._h = h
+        self.num_pages, self.page = num_pages, page
+
+    def __del__(self):
+        h, self._h = getattr(self, "_h", None), None
+        if h:
+            lib().kv_pool_destroy(h)
+
+    def add(self) -> int:
+        s = ctypes.c_int()
+        _check(lib().kv_pool_add(self._h, ctypes.byref(s)))
+        return s.value
+
+    def extend(self, seq: int, n_tokens: int) -> list:
+        """Lengthens the sequence; returns the pages to copy first: [] or [[src, dst]]."""
+        pair, n = (ctypes.c_int32 * 2)(), ctypes.c_int()
+        _check(lib().kv_pool_extend(self._h, seq, n_tokens, pair, ctypes.byref(n)))
+        return [list(pair)] if n.value else []
+
+    def truncate(self, seq: int, length: int):
+        _check(lib().kv_pool_truncate(self._h, seq, length))
+
+    def fork(self, seq: int) -> int:
+        s = ctypes.c_int()
+        _check(lib().kv_pool_fork(self._h, seq, ctypes.byref(s)))
+        return s.value
+
+    def free(self, seq: int):
+        _check(lib().kv_pool_free(self._h, seq))
+
+    def compact(self, most: int | None = None) -> list:
+        """Moves live pages into the lowest free ones; returns the pages to copy."""
+        cap = self.num_pages if most is None else most
+        pairs, n = (ctypes.c_int32 * (2 * max(cap, 1)))(), ctypes.c_int()
+        _check(lib().kv_pool_compact(self._h, pairs, cap, ctypes.byref(n)))
+        return [[pairs[2 * i], pairs[2 * i + 1]] for i in range(n.value)]
+
+    def length(self, seq: int) -> int:
+        n = ctypes.c_int()
+        _check(lib().kv_pool_pages(self._h, seq, ctypes.byref(n), None))
+        return n.value
+
+    def pages(self, seq: int) -> int:
+        n = ctypes.c_int()
+        _check(lib().kv_pool_pages(self._h, seq, None, ctypes.byref(n)))
+        return n.value
+
+    def free_pages(self) -> int:
+        n = int(lib().kv_pool_free_pages(self._h))
+        if n < 0:
+            _check(n)
+        return n
+
+    def table(self, seqs, max_pages: int | None = None, pin: bool = False):
+        """CPU int32 tensors (page_table [B, max_pages], seq_lens [B]) of the sequences."""
+        seqs = [int(s) for s in seqs]
+        width = max([self.pages(s) for s in seqs], default=0) if max_pages is None else max_pages
+        table = torch.empty((len(seqs), width), dtype=torch.int32, pin_memory=pin)
+        lens = torch.empty((len(seqs),), dtype=torch.int32, pin_memory=pin)
+        ids = (ctypes.c_int32 * max(len(seqs), 1))(*seqs)
+        _check(lib().kv_pool_table(self._h, ids, len(seqs), width, table.data_ptr(), lens.data_ptr()))
+        return table, lens
+
+
+# ------------------------------------------------------- token probabilities --
+class TokenLogprobs(NamedTuple):
+    logprob: torch.Tensor               # [M, C] (or [M]) of the given tokens
+    entropy: torch.Tensor               # [M]
+    lse: torch.Tensor                   # [M] logsumexp
+    top_logprob: torch.Tensor | None    # [M, k], most likely first
+    top_idx: torch.Tensor | None        # [M, k] int32
+
+
+_LOGIT_TYPES = {torch.float16: QW_F16, torch.bfloat16: QW_BF16, torch.float32: QW_F32}
+
+
+def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> TokenLogprobs:
+    """Log probabilities of given tokens (int32 or int64 [M] or [M, C]), entropy, logsumexp
+    and the k (<= 64) most likely tokens of each row of logits [M, N] (fp16, bf16 or float32;
+    rows may be strided), in one pass over the logits."""
+    dtype = _LOGIT_TYPES.get(logits.dtype)
+    if dtype is None or not logits.is_cuda:
+        raise TypeError("logits must be a float16, bfloat16 or float32 CUDA tensor")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [M, N] with contiguous rows")
+    dev = logits.device
+    M, N = logits.shape
+    if tokens.dtype not in (torch.int32, torch.int64) or tokens.device != dev:
+        raise TypeError(f"tokens must be int32 or int64 on {dev}")
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != M or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous [M] or [M, C]")
+    C = 1 if tokens.dim() == 1 else tokens.shape[1]
+    f32 = dict(dtype=torch.float32, device=dev)
+    logprob = torch.empty(tokens.shape, **f32)
+    entropy, lse = torch.empty((2, M), **f32)
+    top = torch.empty((M, k), **f32) if k > 0 else None
+    idx = torch.empty((M, k), dtype=torch.int32, device=dev) if k > 0 else None
+    L = lib()
+    buf, nbytes = _scratch(ws, dev, "logprobs", L.token_logprobs_workspace_bytes, M, N, k, dtype)
+    _launch(dev, L.token_logprobs, logits.data_ptr(), dtype, M, N, logits.stride(0), tokens.data_ptr(),
+            tokens.element_size(), C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+            None if top is None else top.data_ptr(), None if idx is None else idx.data_ptr(),
+            None if buf is None else buf.data_ptr(), nbytes)
+    return TokenLogprobs(logprob, entropy, lse, top, idx)
 
 
 def qgemm_w4a16_noalloc(x, packed, N: int, K: int, y=None):

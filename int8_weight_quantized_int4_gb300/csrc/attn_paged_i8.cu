@@ -1,0 +1,8 @@
+// attn_paged_i8.cu -- the paged attention kernels of one cache type (see attn_paged.cuh)
+#include "attn_paged.cuh"
+
+namespace qw {
+cudaError_t launch_attn_paged_i8(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st) {
+  return paged_launch<kPagedI8>(a, d, rw, sms, st);
+}
+}  // namespace qw

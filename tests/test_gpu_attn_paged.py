@@ -1,0 +1,252 @@
+"""attn_paged on the GPU against its definition in binary64, with error bounds derived in
+_decode_ref.Cache.tolerances.  Every slot of the cache that holds no key of the batch is NaN
+(and, int8, has a NaN scale)."""
+import pytest
+import torch
+
+from tests._decode_ref import DEV, Cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+    import int8_weight_quantized_int4_gb300 as q
+    return q
+
+
+def check(q, c, window=0, sinks=0, max_new=None, scale=None, **kw):
+    ref = c.reference(window, sinks, scale)
+    tol, lse_tol = c.tolerances(ref)
+    lse = torch.full((c.T, c.Hq), 7.0, device=DEV)
+    out, got_lse = q.attn_paged(c.q, *c.args(), max_new=max_new or max(c.news + [1]), window=window, sinks=sinks,
+                                scale=scale, lse=lse, **c.kw, **kw)
+    assert q.device_error() == 0
+    assert got_lse is lse
+    err = (out.double() - ref[0]).abs()
+    assert bool((err <= tol).all()), (float((err / tol).max()), float(err.max()))
+    empty = torch.isinf(ref[1])
+    assert torch.equal(torch.isneginf(lse), empty)
+    assert bool((out[empty] == 0).all())
+    d = (lse.double() - ref[1])[~empty].abs()
+    assert bool((d <= lse_tol[~empty]).all()), float((d / lse_tol[~empty]).max())
+    return out, lse
+
+
+HEADS = [("fp16", 256, 24, 4, 16, False), ("bf16", 128, 32, 8, 64, True), ("int8", 256, 24, 4, 16, False),
+         ("fp16", 64, 64, 8, 1, False), ("bf16", 256, 8, 8, 48, False), ("int8", 128, 16, 1, 7, False),
+         ("int8", 64, 6, 2, 32, False), ("fp16", 128, 40, 10, 33, True), ("bf16", 64, 16, 1, 128, False)]
+
+
+@pytest.mark.parametrize("kind,d,Hq,Hkv,page,nhd", HEADS)
+@pytest.mark.parametrize("lens", [[1], [15], [16], [17], [129], [1003], [0, 1, 2, 63, 64, 65, 300]])
+def test_one_token(q, kind, d, Hq, Hkv, page, nhd, lens):
+    c = Cache(lens, [min(1, n) for n in lens], Hq, Hkv, d, page, kind, nhd, seed=len(lens) + d)
+    check(q, c)
+
+
+@pytest.mark.parametrize("kind,d,Hq,Hkv,page,nhd", HEADS)
+@pytest.mark.parametrize("lens,news", [
+    ([5, 77, 300, 9, 18], [5, 3, 6, 1, 2]), ([40, 0, 33], [40, 0, 2]), ([130], [130]), ([700, 10], [9, 10])])
+def test_several_tokens(q, kind, d, Hq, Hkv, page, nhd, lens, news):
+    c = Cache(lens, news, Hq, Hkv, d, page, kind, nhd, seed=sum(news) + d)
+    out, _ = check(q, c)
+    # a wrong hint changes the work's split, not the result
+    check(q, c, max_new=1)
+
+
+@pytest.mark.parametrize("kind,d,Hq,Hkv,page,nhd", HEADS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (100, 1), (130, 64), (64, 300), (5000, 4)])
+def test_window_and_sinks(q, kind, d, Hq, Hkv, page, nhd, window, sinks):
+    c = Cache([1, 100, 101, 260, 777], [1, 3, 1, 2, 4], Hq, Hkv, d, page, kind, nhd, seed=window)
+    check(q, c, window, sinks)
+
+
+@pytest.mark.parametrize("kind,d,Hq,Hkv,page", [("fp16", 256, 24, 4, 16), ("bf16", 128, 8, 2, 64), ("int8", 256, 6, 1, 16),
+                                               ("int8", 64, 4, 4, 16), ("fp16", 64, 2, 1, 80)])
+def test_long_context_is_split_and_joined(q, kind, d, Hq, Hkv, page):
+    """One long sequence over every SM, beside short ones: items cut across CTAs."""
+    c = Cache([20011, 3, 70, 1], [1, 1, 2, 1], Hq, Hkv, d, page, kind, seed=3)
+    a, la = check(q, c)
+    for _ in range(5):                                   # joined in a fixed order: the same bits
+        lse = torch.empty_like(la)
+        b, lb = q.attn_paged(c.q, *c.args(), max_new=2, lse=lse, **c.kw)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+    check(q, c, window=9000, sinks=500)
+
+
+def test_many_short_sequences(q):
+    """More items than a CTA lists at a time (several lists a CTA)."""
+    lens = [1 + (i * 7) % 40 for i in range(1500)]
+    c = Cache(lens, [1] * 1500, 16, 8, 64, 16, "fp16", seed=5)
+    check(q, c)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "int8"])
+def test_large_scores_and_scale(q, kind):
+    """Scores that differ by hundreds (the reference moves many times), another scale, and a
+    negative one."""
+    c = Cache([513, 64], [2, 1], 8, 2, 128, 16, kind, seed=8)
+    c.q.mul_(6.0)
+    check(q, c, scale=0.5)
+    check(q, c, scale=-0.25)
+    check(q, c, scale=0.0)
+
+
+@pytest.mark.parametrize("v_scale", [2.0 ** -13, 2.0 ** 8])
+def test_int8_values_of_any_size(q, v_scale):
+    """The weight carries the value's scale: small scales must not lose its bits."""
+    c = Cache([700], [1], 8, 2, 128, 16, "int8", seed=4, v_scale=v_scale)
+    check(q, c)
+
+
+def test_zero_scale_rows(q):
+    c = Cache([50, 3], [1, 1], 4, 2, 64, 16, "int8", seed=4)
+    for b, j in ((0, 7), (0, 49), (1, 0), (1, 1), (1, 2)):
+        pid, off = c.row(b, j)
+        for s, x in ((c.kw["k_scale"], c.k64), (c.kw["v_scale"], c.v64)):
+            s[pid, :, off] = 0.0
+            x[pid, :, off] = 0.0
+    check(q, c)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_hidden_values_never_reach_a_row(q, kind, value):
+    """A key that one new token sees and another does not (a later token; a key that leaves
+    the window between them) may hold anything: only the rows that see it are affected."""
+    for window, sinks, hidden, sees in ((0, 0, 59, lambda t: t == 4), (20, 0, 36, lambda t: t == 0),
+                                        (20, 2, 37, lambda t: t <= 1)):
+        c = Cache([60], [5], 12, 2, 128, 16, kind, seed=2)
+        pid, off = c.row(0, hidden)
+        clean = c.reference(window, sinks)
+        tol, _ = c.tolerances(clean)
+        c.v[pid, 0, off, 10:14] = value
+        c.k[pid, 1, off, 3] = value
+        out = q.attn_paged(c.q, *c.args(), max_new=5, window=window, sinks=sinks)
+        assert q.device_error() == 0
+        for t in range(5):
+            if not sees(t):
+                assert bool(((out[t].double() - clean[0][t]).abs() <= tol[t]).all()), (window, t)
+            else:
+                assert not bool(torch.isfinite(out[t, :6, 10:14]).any())
+
+
+def test_int8_hidden_scales(q):
+    c = Cache([60], [5], 4, 1, 64, 16, "int8", seed=2)
+    clean = c.reference()
+    tol, _ = c.tolerances(clean)
+    pid, off = c.row(0, 59)
+    c.kw["k_scale"][pid, 0, off] = float("nan")
+    c.kw["v_scale"][pid, 0, off] = float("inf")
+    out = q.attn_paged(c.q, *c.args(), max_new=5, **c.kw)
+    assert bool(((out[:4].double() - clean[0][:4]).abs() <= tol[:4]).all())
+
+
+def test_shared_prefix_pages(q):
+    c = Cache([64, 64], [1, 1], 8, 2, 64, 16, "fp16", seed=6)
+    c.table[1, :3] = c.table[0, :3]
+    check(q, c)
+
+
+def test_bad_pages_and_lengths(q):
+    """A page id out of range reads as zeros, a length past the table as the table's end."""
+    c = Cache([60, 40], [1, 1], 4, 2, 64, 16, "fp16", seed=6)
+    good = c.table.clone()
+    c.table[0, 1], c.table[1, 2] = c.k.shape[0], -5
+    out = q.attn_paged(c.q, *c.args())
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and q.device_error() == 0
+    zero = int(c.k.shape[0] - 1)
+    used = set(good.flatten().tolist())
+    zero = next(p for p in range(c.k.shape[0]) if p not in used)
+    c.k[zero], c.v[zero] = 0.0, 0.0
+    c.k64[zero], c.v64[zero] = 0.0, 0.0
+    c.table[0, 1], c.table[1, 2] = zero, zero
+    ref = c.reference()
+    tol, _ = c.tolerances(ref)
+    assert bool(((out.double() - ref[0]).abs() <= tol).all())
+    c = Cache([64], [1], 4, 2, 64, 16, "fp16", seed=6)
+    want = q.attn_paged(c.q, *c.args())
+    c.lens[0] = 1 << 30
+    got = q.attn_paged(c.q, *c.args())
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and torch.equal(got, want)
+
+
+def test_offsets_out_of_order(q):
+    """Offsets beyond q or descending: clamped, reported, nothing read or written outside."""
+    c = Cache([40, 40, 40], [1, 1, 1], 4, 2, 64, 16, "fp16", seed=6)
+    c.cu.copy_(torch.tensor([0, 900, -3, 2], device=DEV))
+    out = torch.full_like(c.q, 3.0).contiguous()
+    q.attn_paged(c.q, *c.args(), out=out)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX
+
+
+def test_rows_of_no_sequence_are_left(q):
+    c = Cache([30, 30], [1, 1], 4, 2, 64, 16, "fp16", seed=6)
+    c.cu[2] = 1
+    out = torch.full(c.q.shape, 3.0, dtype=torch.float16, device=DEV)
+    q.attn_paged(c.q, *c.args(), out=out)
+    assert q.device_error() == 0 and bool((out[1] == 3.0).all()) and not bool((out[0] == 3.0).all())
+
+
+def test_graph_follows_lengths(q):
+    """A captured step replays with longer contexts: lengths are read on the device."""
+    c = Cache([400, 900], [1, 1], 24, 4, 256, 16, "fp16", seed=9)
+    ws = q.Workspace(torch.device("cuda:0"))
+    out = torch.empty(c.q.shape, dtype=torch.float16, device=DEV)
+    q.attn_paged(c.q, *c.args(), out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.attn_paged(c.q, *c.args(), out=out, ws=ws)
+    for lens in ([1, 900], [400, 17], [333, 801]):
+        c.lens_list = lens
+        c.lens.copy_(torch.tensor(lens))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = c.reference()
+        tol, _ = c.tolerances(ref)
+        assert bool(((out.double() - ref[0]).abs() <= tol).all())
+    assert q.device_error() == 0
+
+
+def test_another_stream(q):
+    c = Cache([500, 20], [1, 1], 24, 4, 256, 16, "fp16", seed=9)
+    want = q.attn_paged(c.q, *c.args())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = q.attn_paged(c.q, *c.args())
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_binding_refusals(q):
+    c = Cache([20], [1], 4, 2, 64, 16, "fp16")
+    a = c.args()
+    with pytest.raises(TypeError):
+        q.attn_paged(c.q.bfloat16(), *a)
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q[..., :32], *a)
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, c.k, c.v[:, :, :8], *a[2:])
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, c.k, c.v, a[2].long(), *a[3:])
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, c.k, c.v, a[2], a[3], a[4][:1])
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, *a, k_scale=torch.zeros(1, device=DEV))
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, *a, out=torch.empty(1, 4, 64, device=DEV))
+    with pytest.raises(ValueError):
+        q.attn_paged(c.q, *a, lse=torch.empty(1, 3, device=DEV))
+    with pytest.raises(q.QgemmError):
+        q.attn_paged(c.q[:, :3].contiguous(), *a)           # 2 KV heads do not divide 3
+    with pytest.raises(q.QgemmError):
+        q.attn_paged(c.q, *a, window=-1)
+    T0 = q.attn_paged(c.q[:0], c.k, c.v, a[2], a[3], torch.zeros_like(a[4]))
+    assert T0.shape == (0, 4, 64) and q.device_error() == 0
