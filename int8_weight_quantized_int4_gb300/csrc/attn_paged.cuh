@@ -1,6 +1,6 @@
 // attn_paged.cuh -- attention of each sequence's new tokens over a paged key-value cache.
 //
-// For query head h of new token t at position pos of its sequence, KV head g = h / G
+// For query head h of a new token at position pos of its sequence, KV head g = h / G
 // (G = Hq / Hkv), over the keys j it can see (j <= pos and, with a window W, j > pos - W or
 // j < sinks):
 //   x_j = q . k_j * scale,  p_j = e^(x_j - m),  out = sum_j p_j v_j / sum_j p_j.
@@ -10,20 +10,22 @@
 // What bounds it: reading K and V, 2 S d e bytes a (sequence, KV head) for 4 S d flops a
 // query row -- a few rows a KV head (G x new tokens), so 1..64 flops a byte, far below the
 // ridge of any matrix unit here (warp-level MMA: 606 TFLOP/s measured against 6.7 TB/s, 90
-// flops a byte).  So the design is about keeping loads in flight:
-//   - The G heads and the new tokens of a sequence that share a KV head are the rows of one
-//     16-row MMA tile (RW tiles for more rows), so K and V are read once for all of them.
-//   - A CTA of RW x KW warps owns an SM.  Each of its KW groups streams its own strips of 16
-//     keys through its own ring of shared-memory stages (cp.async, 16 bytes a thread; rows
-//     beyond the visible keys are zero-filled, not read) and waits only for itself: no
-//     CTA-wide barrier between the strips of a sequence.  The RW warps of a group share its
-//     strips, one row tile each.
-//   - Work is split evenly over the SMs whatever the lengths: the visible keys of every
-//     (sequence, row block, KV head) item are cut into units of 16 KW keys, the units of all
-//     items laid end to end and cut into one equal range a CTA (every CTA finds its own range
-//     from the lengths on the device, so a captured graph follows growing contexts).  An item
-//     that a range border cuts leaves partial sums (m, l, O) in the workspace, and the last
-//     CTA to finish it joins them in CTA order: results do not depend on arrival order.
+// flops a byte).  So the design is about keeping loads in flight and instructions few:
+//   - The G heads and the new tokens of a sequence that share a KV head are the columns of an
+//     MMA whose rows are keys (S^T = K Q^T) and then channels (O^T = V^T P^T), so K and V are
+//     read once for all of them and eight columns (the common case, G <= 8) cost half of what
+//     a 16-row query tile would, in instructions and in accumulator registers.
+//   - A CTA owns an SM.  Each of its KW groups streams its own strips of 16 keys through its
+//     own ring of half stages (the K rows, then the V rows of a strip; cp.async, 16 bytes a
+//     thread; rows beyond the visible keys are zero-filled, not read) and waits only for
+//     itself: no CTA-wide barrier between the strips of a sequence.  For more than 16 columns
+//     the RW warps of a group share its strips, 16 columns each.
+//   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
+//     (sequence, column block, KV head) item are laid end to end and cut into one equal range
+//     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
+//     follows growing contexts).  An item that a range border cuts leaves partial sums (m, l,
+//     O) in the workspace, and the last CTA to finish it joins them in CTA order: results do
+//     not depend on arrival order.
 //   - The ring runs ahead across item borders, so the next item's keys arrive while one item
 //     is being finished.
 //
@@ -43,39 +45,47 @@
 namespace qw {
 
 constexpr int kPagedMaxSegs = 32;       // work segments listed at a time
-constexpr int kStrip = 16;              // keys a group handles per step: the MMA's K of P.V
-constexpr int kRedStride = 40;          // floats a row of the 32-column exchange buffer
-                                        // (8 rows x 4 column pairs on distinct banks)
+constexpr int kStrip = 16;              // keys of a strip: the MMA's rows of S^T, its depth of O^T
 constexpr int kPagedSmem = 227 * 1024;
 
 struct PagedSeg {
-  int b, g, rb;                 // sequence, KV head, row block
-  int u0, u1;                   // units of the item [u0, u1)
-  int nsu, first;               // units of the sinks, unit of the first windowed key
-  int lo, hi;                   // visible keys of the row block: [lo, hi) and below `sinks`
-  int pos0, rows;               // position of the sequence's first new token; its query rows
+  int b, g, rb;                 // sequence, KV head, column block
+  int u0, u1;                   // strips of the item [u0, u1)
+  int nsu, first;               // strips of the sinks, strip of the first windowed key
+  int lo, hi;                   // visible keys of the column block: [lo, hi) and below `sinks`
+  int pos0, rows;               // position of the sequence's first new token; its query columns
   int tok0;                     // its first row in q and out
-  int c0, c1;                   // CTAs holding the item's first and last unit
+  int c0, c1;                   // CTAs holding the item's first and last strip
 };
 
-template <int D, int KV, int RW>
+// Shapes.  NB: MMA column tiles (of 8) a warp; RW: warps a group (column blocks of 8 NB RW).
+// The warps a CTA has are what the registers allow: accumulators take D NB / 4 registers a
+// thread and the Q fragments D NB / 8 more (in shared memory where D NB = 512).
+template <int D, int KV, int NB, int RW>
 struct PagedShape {
   static constexpr int kES = KV == kPagedI8 ? 1 : 2;
-  static constexpr int kKW = KV != kPagedI8 && D == 256 && RW == 1 ? 4 : 8 / RW;
+  static constexpr int kMaxWarps = D * NB == 512 ? 8 : D * NB == 256 ? 12 : 16;
+  static constexpr int kKW = kMaxWarps / RW;
   static constexpr int kWarps = RW * kKW;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRows = 16 * RW;
-  static constexpr int kUnit = kStrip * kKW;
+  static constexpr int kCols = 8 * NB;                 // columns a warp
+  static constexpr int kRows = kCols * RW;             // columns a CTA takes at a time
   static constexpr int kRowBytes = D * kES;
-  static constexpr int kStageBytes = 2 * kStrip * kRowBytes + (KV == kPagedI8 ? 2 * kStrip * 4 : 0);
-  static constexpr int kQBytes = RW * D * 32;
-  static constexpr int kRedBytes = kWarps * 16 * kRedStride * 4;
-  static constexpr int kQRed = kQBytes > kRedBytes ? kQBytes : kRedBytes;   // Q and the exchange share it
-  static constexpr int kFixed = kQRed + 2 * kWarps * 16 * 4 + kPagedMaxSegs * (int)sizeof(PagedSeg) + 256;
-  static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kStageBytes);
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kFixed + kStages * kKW * kStageBytes;
-  static_assert(kStages >= 3, "a ring of at least three stages");
+  static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
+  static constexpr bool kQRegs = D * NB <= 256;
+  static constexpr int kQBytes = kQRegs ? 0 : kRows * D * 2;
+  // the exchange at an item's end: SW channels at a time, rows of SW + 4 floats (column pairs
+  // 2 c and channels r8 of a warp's lanes fall on distinct banks)
+  static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
+  static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
+  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kPagedMaxSegs * (int)sizeof(PagedSeg) + 256;
+  static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
+  static constexpr int kRing = kFit > 8 ? 8 : kFit;    // half stages a group
+  static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
+  static_assert(kRing >= (RW > 1 ? 3 : 2), "K and V of a strip in flight");
+  // what an item costs beside its strips (its Q, the join of the groups: about 1.5 us, in
+  // which an SM reads some 64 KB), in strips
+  static constexpr int kItemCost = 65536 / (2 * kStrip * kRowBytes);
   static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 };
 
@@ -139,6 +149,13 @@ __device__ __forceinline__ uint32_t strip_off(int r, int c) {
   else return (uint32_t)(r * RB + ((c ^ ((r >> 1) & 3)) << 4));      // 64-byte rows: two a bank line
 }
 
+// 8 x 8 matrix of 16-bit elements, a row pair a lane, transposed across the warp.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Whether a strip of 16 value rows (16-bit) holds an infinity or a NaN; whole warp.
 template <int D, bool BF>
 __device__ __noinline__ bool strip_nonfinite(uint32_t vst, int lane) {
@@ -151,37 +168,31 @@ __device__ __noinline__ bool strip_nonfinite(uint32_t vst, int lane) {
   }
   return __any_sync(0xffffffffu, bad);
 }
-// acc += P . V of one strip over the visible keys alone (score above -inf), term by term.
-// p: the A fragments, s: the scores (tile t, element e: row r8 + 8 (e / 2), key 8 t + 2 c4 + (e & 1)).
-template <int D, bool BF>
-__device__ __forceinline__ void add_visible(float (&acc)[D / 8][4], const uint32_t (&p)[4], const float (&s)[2][4],
-                                            uint32_t vst, int lane) {
+// acc += V^T P^T of one strip over the visible keys alone (score above -inf), term by term.
+// pk[nb][h]: the packed weights of keys r8 + 8 h and columns 2 c4, 2 c4 + 1; s: their scores.
+template <int D, int NB, bool BF>
+__device__ __forceinline__ void add_visible(float (&acc)[D / 16][NB][4], const uint32_t (&pk)[NB][2],
+                                            const float (&s)[NB][4], uint32_t vst, int lane) {
+  const int c4 = lane & 3, r8 = lane >> 2;
 #pragma unroll 1
   for (int j = 0; j < kStrip; ++j) {
-    const int src = (lane & ~3) | ((j & 7) >> 1), t = j >> 3, e = j & 1;
-    float w[2];
-    bool see[2];
+    const int src = (j & 7) * 4 + c4, h = j >> 3;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const uint32_t pw = __shfl_sync(0xffffffffu, t ? p[2 + hh] : p[hh], src) >> (16 * e);
-      const float sv = __shfl_sync(0xffffffffu, t ? (e ? s[1][2 * hh + 1] : s[1][2 * hh])
-                                                  : (e ? s[0][2 * hh + 1] : s[0][2 * hh]), src);
-      w[hh] = BF ? __uint_as_float(pw << 16) : __half2float(__ushort_as_half((unsigned short)pw));
-      see[hh] = sv != -INFINITY;
-    }
+    for (int nb = 0; nb < NB; ++nb) {
+      const uint32_t pw = __shfl_sync(0xffffffffu, h ? pk[nb][1] : pk[nb][0], src);
+      const float s0 = __shfl_sync(0xffffffffu, h ? s[nb][2] : s[nb][0], src);
+      const float s1 = __shfl_sync(0xffffffffu, h ? s[nb][3] : s[nb][1], src);
+      const float w0 = BF ? __uint_as_float(pw << 16) : __half2float(__ushort_as_half((unsigned short)pw));
+      const float w1 = BF ? __uint_as_float(pw & 0xffff0000u) : __half2float(__ushort_as_half((unsigned short)(pw >> 16)));
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      uint32_t v;
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(v) : "r"(vst + strip_off<D * 2>(j, n) + 4 * (lane & 3)) : "memory");
-      const float v0 = BF ? __uint_as_float(v << 16) : __half2float(__ushort_as_half((unsigned short)v));
-      const float v1 = BF ? __uint_as_float(v & 0xffff0000u) : __half2float(__ushort_as_half((unsigned short)(v >> 16)));
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-        if (see[hh]) {
-          acc[n][2 * hh] = fmaf(w[hh], v0, acc[n][2 * hh]);
-          acc[n][2 * hh + 1] = fmaf(w[hh], v1, acc[n][2 * hh + 1]);
-        }
+      for (int n = 0; n < D / 8; ++n) {              // channel 8 n + r8: rows r8 (+ 8) of tile n / 2
+        unsigned short v;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(vst + strip_off<D * 2>(j, n) + 2 * r8) : "memory");
+        const float f = BF ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+        float(&a)[4] = acc[n / 2][nb];
+        if (s0 != -INFINITY) a[2 * (n & 1)] = fmaf(w0, f, a[2 * (n & 1)]);
+        if (s1 != -INFINITY) a[2 * (n & 1) + 1] = fmaf(w1, f, a[2 * (n & 1) + 1]);
+      }
     }
   }
 }
@@ -204,55 +215,69 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &a, int b) {
 struct PagedSpan {
   int lo, hi, nsu, first, n;
 };
-// The keys that row block rb can see and their units.
-template <int ROWS, int UNIT>
+// The keys that column block rb can see and their strips.
+template <int ROWS>
 __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedSeq &s, int rb) {
   PagedSpan p;
   const int rows = s.nq * a.G, pos0 = s.len - s.nq;
   const int t0 = rb * ROWS / a.G, t1 = (min(rows, rb * ROWS + ROWS) - 1) / a.G;
   p.hi = max(pos0 + t1 + 1, 0);
   p.lo = a.window > 0 ? max(pos0 + t0 - a.window + 1, 0) : 0;
-  p.first = p.lo / UNIT;
-  p.nsu = min((min(a.sinks, p.hi) + UNIT - 1) / UNIT, p.first);
-  p.n = max(p.nsu + (p.hi + UNIT - 1) / UNIT - p.first, 1);      // an item with no key still writes its rows
+  p.first = p.lo / kStrip;
+  p.nsu = min((min(a.sinks, p.hi) + kStrip - 1) / kStrip, p.first);
+  p.n = max(p.nsu + (p.hi + kStrip - 1) / kStrip - p.first, 1);      // an item with no key still writes its rows
   return p;
 }
 
-template <int D, int KV, int RW>
-__global__ void __launch_bounds__(PagedShape<D, KV, RW>::kThreads, 1)
+// a / b (a >= 0, b > 0), in 32 bits where both fit
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0ull) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
+template <int D, int KV, int NB, int RW>
+__global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     attn_paged_kernel(const __grid_constant__ PagedArgs a) {
-  using P = PagedShape<D, KV, RW>;
+  using P = PagedShape<D, KV, NB, RW>;
   constexpr bool BF = KV == kPagedBf16;
   constexpr bool I8 = KV == kPagedI8;
-  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, U = P::kUnit, RB = P::kRowBytes;
-  constexpr int ST = P::kStages;
+  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
+  constexpr int R = P::kRing, SW = P::kSW;
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t ring_s = smem_u32(smem);
-  uint8_t *fixed = smem + ST * KW * P::kStageBytes;
-  uint4 *qf = reinterpret_cast<uint4 *>(fixed);                       // [RW][D/16][32] A fragments
-  float *red = reinterpret_cast<float *>(fixed);                      // [KW][RW][16][kRedStride]
-  float *sm_m = reinterpret_cast<float *>(fixed + P::kQRed);          // [KW][ROWS]
-  float *sm_l = sm_m + P::kWarps * 16;
-  PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_l + P::kWarps * 16);
+  uint8_t *fixed = smem + R * KW * P::kHalf;
+  uint32_t *qsm = reinterpret_cast<uint32_t *>(fixed);                // [RW][D/16][32][NB][2] B fragments
+  float *red = reinterpret_cast<float *>(fixed + P::kQBytes);         // [KW][RW][COLS][SW + 4]
+  float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
+  float *sm_l = sm_m + P::kWarps * COLS;
+  PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_l + P::kWarps * COLS);
   int *ctl = reinterpret_cast<int *>(segs + kPagedMaxSegs);           // [0..63]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kw = warp / RW;
   const int c4 = lane & 3, r8 = lane >> 2;
+  uint8_t *ring = smem + kw * R * P::kHalf;                           // this group's half stages
+  const uint32_t ring_s = smem_u32(ring);
 
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this CTA's range of units
+  // ---- this CTA's range.  Every item takes kItemCost places and one for each strip; the
+  // places of all items, in order, are cut into equal ranges.
+  constexpr int IC = P::kItemCost;
   long long total = 0, pre = 0, mine = 0;
   const int per = (a.B + NT - 1) / NT;
   const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
   auto cost = [&](const PagedSeq &s) {
     long long c = 0;
-    for (int rb = 0, n = (s.nq * a.G + ROWS - 1) / ROWS; rb < n; ++rb) c += paged_span<ROWS, U>(a, s, rb).n;
+    for (int rb = 0, n = (s.nq * a.G + ROWS - 1) / ROWS; rb < n; ++rb) c += paged_span<ROWS>(a, s, rb).n + IC;
     return c * a.Hkv;
   };
-  for (int b = b_lo; b < b_hi; ++b) mine += cost(paged_seq(a, b));
+  PagedSeq own{};                                                     // per == 1: this thread's sequence
+  for (int b = b_lo; b < b_hi; ++b) {
+    own = paged_seq(a, b);
+    mine += cost(own);
+  }
+  if (tid == 0) ctl[4] = 0;
   {
     long long inc = mine;
 #pragma unroll
@@ -263,343 +288,482 @@ __global__ void __launch_bounds__(PagedShape<D, KV, RW>::kThreads, 1)
     long long *ws = reinterpret_cast<long long *>(red);
     if (lane == 31) ws[warp] = inc;
     __syncthreads();
+#pragma unroll
     for (int w = 0; w < P::kWarps; ++w) {
       if (w < warp) pre += ws[w];
       total += ws[w];
     }
     pre += inc - mine;
   }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)a.min_units);
+  const long long share = max(paged_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_strips);
   const long long begin = share * blockIdx.x, end = min(total, begin + share);
   if (begin >= end) return;                                           // whole CTA
-  // the sequence holding `begin`: ctl[0] its index, ctl[2..3] the offset in it
-  if (begin >= pre && begin < pre + mine) {
-    long long off = begin - pre;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const long long c = cost(paged_seq(a, b));
-      if (off < c) break;
-      off -= c;
+  // one segment: the strips of the item that starts at place `at` which lie in this range
+  auto emit = [&](PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head, long long at) {
+    g.b = b;
+    g.rb = rb;
+    g.g = head;
+    g.u0 = (int)max(begin - at - IC, 0ll);
+    g.u1 = (int)min(end - at - IC, (long long)p.n);
+    g.nsu = p.nsu;
+    g.first = p.first;
+    g.lo = p.lo;
+    g.hi = p.hi;
+    g.pos0 = s.len - s.nq;
+    g.rows = s.nq * a.G;
+    g.tok0 = s.tok0;
+    g.c0 = (int)paged_div(at + IC, share);
+    g.c1 = (int)paged_div(at + IC + p.n - 1, share);
+  };
+  // Up to a sequence a thread and kPagedMaxSegs segments: every thread lists its own
+  // sequence's (in any order); otherwise thread 0 walks, a list at a time.
+  if (pre < end && begin < pre + mine) {
+    long long at = pre;
+    if (per == 1)
+      for (int rb = 0, n = (own.nq * a.G + ROWS - 1) / ROWS; rb < n && at < end; ++rb) {
+        const PagedSpan p = paged_span<ROWS>(a, own, rb);
+        const int each = p.n + IC;
+        int head = begin > at ? (int)min(paged_div(begin - at, each), (long long)a.Hkv) : 0;
+        long long x = at + (long long)head * each;
+        for (; head < a.Hkv && x + IC < end; ++head, x += each)
+          if (x + each > begin) {
+            const int i = atomicAdd(ctl + 4, 1);
+            if (i < kPagedMaxSegs) emit(segs[i], own, p, b_lo, rb, head, x);
+          }
+        at += (long long)a.Hkv * each;
+      }
+    if (begin >= pre) {                                 // the owner of the range's first place
+      long long off = begin - pre;
+      int b = b_lo;
+      for (; b + 1 < b_hi; ++b) {
+        const long long c = cost(paged_seq(a, b));
+        if (off < c) break;
+        off -= c;
+      }
+      ctl[0] = b;
+      *reinterpret_cast<long long *>(ctl + 2) = off;
     }
-    ctl[0] = b;
-    *reinterpret_cast<long long *>(ctl + 2) = off;
   }
   __syncthreads();
-  // the walk's state, kept by thread 0: sequence, offset in it, units done
+  const bool walk = per > 1 || ctl[4] > kPagedMaxSegs;
+  // the walk's state, kept by thread 0: sequence, offset in it, places done
   int wb = ctl[0];
   long long woff = *reinterpret_cast<long long *>(ctl + 2), wpos = begin;
 
-  float acc[D / 8][4];
+  float acc[D / 16][NB][4];
   for (;;) {
-    // ---- list the next segments
-    __syncthreads();
-    if (tid == 0) {
-      int n = 0;
-      while (wpos < end && n < kPagedMaxSegs) {
-        const PagedSeq s = paged_seq(a, wb);
-        const int rows = s.nq * a.G, nrb = (rows + ROWS - 1) / ROWS;
-        long long off = woff;
-        int rb = 0;
-        PagedSpan p{};
-        for (; rb < nrb; ++rb) {
-          p = paged_span<ROWS, U>(a, s, rb);
-          if (off < (long long)p.n * a.Hkv) break;
-          off -= (long long)p.n * a.Hkv;
+    if (walk) {
+      // ---- list the next segments
+      __syncthreads();
+      if (tid == 0) {
+        int n = 0;
+        while (wpos < end && n < kPagedMaxSegs) {
+          const PagedSeq s = paged_seq(a, wb);
+          const int nrb = (s.nq * a.G + ROWS - 1) / ROWS;
+          long long off = woff;
+          int rb = 0;
+          PagedSpan p{};
+          for (; rb < nrb; ++rb) {
+            p = paged_span<ROWS>(a, s, rb);
+            if (off < (long long)(p.n + IC) * a.Hkv) break;
+            off -= (long long)(p.n + IC) * a.Hkv;
+          }
+          if (rb == nrb) {
+            ++wb;
+            woff = 0;
+            continue;
+          }
+          const int head = (int)paged_div(off, p.n + IC), in = (int)(off - (long long)head * (p.n + IC));
+          PagedSeg &g = segs[n];
+          emit(g, s, p, wb, rb, head, wpos - in);
+          if (g.u0 < g.u1) ++n;                         // (a range may end among an item's first places)
+          wpos += p.n + IC - in;
+          woff += p.n + IC - in;
         }
-        if (rb == nrb) {
-          ++wb;
-          woff = 0;
-          continue;
-        }
-        PagedSeg &g = segs[n++];
-        g.b = wb;
-        g.rb = rb;
-        g.g = (int)(off / p.n);
-        g.u0 = (int)(off % p.n);
-        g.u1 = (int)min((long long)p.n, g.u0 + (end - wpos));
-        g.nsu = p.nsu;
-        g.first = p.first;
-        g.lo = p.lo;
-        g.hi = p.hi;
-        g.pos0 = s.len - s.nq;
-        g.rows = rows;
-        g.tok0 = s.tok0;
-        g.c0 = (int)((wpos - g.u0) / share);
-        g.c1 = (int)((wpos - g.u0 + p.n - 1) / share);
-        wpos += g.u1 - g.u0;
-        woff += g.u1 - g.u0;
+        ctl[4] = n;
+        ctl[5] = wpos < end;
       }
-      ctl[4] = n;
-      ctl[5] = wpos < end;
+      __syncthreads();
     }
-    __syncthreads();
     const int nseg = ctl[4];
-    const bool more = ctl[5] != 0;
+    const bool more = walk && ctl[5] != 0;
+    if (nseg == 0) break;                               // (only places of no strip)
 
-    // ---- the ring: this group's strips, ahead of the arithmetic
-    int ls = 0, lu = segs[0].u0, lstage = 0;
+    // ---- the ring: this group's strips (u0 + kw, + KW, ..), ahead of the arithmetic, each as
+    // two half stages: its K rows, then its V rows
+    int ls = 0, lu = segs[0].u0 + kw, lbuf = 0;
+    bool lv = false;
+    while (ls < nseg && lu >= segs[ls].u1)
+      if (++ls < nseg) lu = segs[ls].u0 + kw;
+    // of the strip being loaded: this lane's row offset (lane & 15; -1: not read) and scale
+    long long off = -1;
+    long long soff = -1;
     auto load_next = [&]() {
       if (ls < nseg) {
         const PagedSeg &g = segs[ls];
-        const int unit = lu < g.nsu ? lu : g.first + lu - g.nsu;
-        const int key0 = unit * U + kw * kStrip;
-        const uint32_t st = ring_s + (uint32_t)((lstage * KW + kw) * P::kStageBytes);
-        // lane r (and r + 16): row r of the strip -- its element offset, -1 when not read
-        long long off = -1;
-        int srow = -1;
-        {
-          const int key = key0 + (lane & 15);
+        const uint32_t st = ring_s + (uint32_t)(lbuf * P::kHalf);
+        if (!lv) {
+          const int unit = lu < g.nsu ? lu : g.first + lu - g.nsu;
+          const int key = unit * kStrip + (lane & 15);
+          off = soff = -1;
           if (key < g.hi && (key >= g.lo || key < a.sinks)) {
             const int pi = key / a.page, po = key - pi * a.page;
             const int pid = __ldg(a.table + (size_t)g.b * a.max_pages + pi);
             if ((unsigned)pid < (unsigned)a.npages) {
-              off = pid * a.page_stride + g.g * a.head_stride + po * a.tok_stride;
-              srow = 1;
-              if constexpr (I8) {
-                if (rw == 0) {
-                  const float *sc = (lane < 16 ? a.ks : a.vs) + ((size_t)pid * a.Hkv + g.g) * a.page + po;
-                  cp_async4(st + 2 * kStrip * RB + lane * 4, sc, 4);
-                }
-              }
+              off = (pid * a.page_stride + g.g * a.head_stride + po * a.tok_stride) * P::kES;
+              if constexpr (I8) soff = ((long long)pid * a.Hkv + g.g) * a.page + po;
             } else {
               atomicCAS(a.err, 0, -9);
             }
           }
-          if constexpr (I8)
-            if (rw == 0 && srow < 0) cp_async4(st + 2 * kStrip * RB + lane * 4, a.ks, 0);
         }
+        const uint8_t *base = lv ? a.v : a.k;
+        if constexpr (I8)
+          if (rw == 0 && lane < 16)
+            cp_async4(st + kStrip * RB + lane * 4, (lv ? a.vs : a.ks) + (soff >= 0 ? soff : 0), soff >= 0 ? 4u : 0u);
         constexpr int CH = RB / 16;                        // 16-byte chunks a row
-        constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;     // rows a warp instruction covers
+        constexpr int RPI = 32 / CH;                       // rows a warp instruction covers
         constexpr int NI = kStrip / RPI;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           if (NI >= RW ? (i % RW != rw) : (rw >= NI || i != rw)) continue;
           const int r = i * RPI + (CH < 32 ? lane / CH : 0), c = lane % CH;
           const long long o = __shfl_sync(0xffffffffu, off, r);
-          const uint32_t d = st + strip_off<RB>(r, c), nb = o >= 0 ? 16u : 0u;
-          const size_t so = o >= 0 ? (size_t)o * P::kES + c * 16 : 0;
-          cp_async16(d, a.k + so, nb);
-          cp_async16(d + kStrip * RB, a.v + so, nb);
+          cp_async16(st + strip_off<RB>(r, c), base + (o >= 0 ? o + c * 16 : 0), o >= 0 ? 16u : 0u);
         }
-        if (++lu == g.u1 && ++ls < nseg) lu = segs[ls].u0;
+        if (lv) {
+          lu += KW;
+          while (ls < nseg && lu >= segs[ls].u1)
+            if (++ls < nseg) lu = segs[ls].u0 + kw;
+        }
+        lv = !lv;
       }
       cp_async_commit();
-      lstage = lstage + 1 == ST ? 0 : lstage + 1;
+      lbuf = lbuf + 1 == R ? 0 : lbuf + 1;
     };
-#pragma unroll 1
-    for (int i = 0; i < ST - 1; ++i) load_next();
+    // One warp a group refills a buffer as soon as it has read it (R loads ahead); several
+    // warps refill it after the next half's barrier (R - 1 ahead).
+    constexpr int kAhead = RW == 1 ? R : R - 1;
+    int buf = 0;
+    auto acquire = [&]() {                                 // the next half: its shared address
+      cp_async_wait<kAhead - 1>();
+      if constexpr (RW == 1) {
+        __syncwarp();
+      } else {
+        named_bar_sync(1 + kw, 32 * RW);
+        load_next();
+      }
+      const int b = buf;
+      buf = buf + 1 == R ? 0 : buf + 1;
+      return b * P::kHalf;
+    };
+    auto release = [&]() {
+      if constexpr (RW == 1) {
+        __syncwarp();
+        load_next();
+      }
+    };
 
-    int stage = 0;
+    // ---- Q as B fragments: column r8 of tile nb, channels 2 c4, + 1, + 8, + 9 of each 16
+    // (int8: 4 c4 .. 4 c4 + 3, the order in which the codes of a word are widened).  Loaded
+    // while the item before is joined.
+    uint32_t qr[P::kQRegs ? D / 16 : 1][NB][2];
+    auto load_q = [&](const PagedSeg &g) {
+      const int row0 = g.rb * ROWS;
+      if constexpr (P::kQRegs) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int gr = row0 + rw * COLS + nb * 8 + r8;
+          const bool in = gr < g.rows;
+          const int tok = in ? gr / a.G : 0, hd = in ? gr - tok * a.G : 0;
+          const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + (I8 ? 4 : 2) * c4;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            if constexpr (I8) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + ks * 16));
+              qr[ks][nb][0] = in ? v.x : 0u;
+              qr[ks][nb][1] = in ? v.y : 0u;
+            } else {
+              const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
+              const uint32_t y = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8));
+              qr[ks][nb][0] = in ? x : 0u;
+              qr[ks][nb][1] = in ? y : 0u;
+            }
+          }
+        }
+      } else {
+        // thread: column tid % ROWS, words tid / ROWS, + NT / ROWS, .. of its D / 2
+        static_assert(NT % ROWS == 0, "whole columns");
+        constexpr int WS = NT / ROWS, NW = D / 2 / WS;
+        static_assert(D / 2 % WS == 0, "whole words");
+        const int col = tid % ROWS, gr = row0 + col;
+        const bool in = gr < g.rows;
+        const int tok = in ? gr / a.G : 0, hd = in ? gr - tok * a.G : 0;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(
+            a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head);
+        // fragment place of word w (channels 2 w, 2 w + 1): lane 4 (col % 8) + c, half h
+        uint32_t *dst = qsm + (((col / COLS) * (D / 16) * 32 + 4 * (col % 8)) * NB + col % COLS / 8) * 2;
+#pragma unroll
+        for (int i0 = 0; i0 < NW; i0 += 8) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8 && i0 + i < NW; ++i) v[i] = __ldg(src + tid / ROWS + (i0 + i) * WS);
+#pragma unroll
+          for (int i = 0; i < 8 && i0 + i < NW; ++i) {
+            const int w = tid / ROWS + (i0 + i) * WS, ks = w / 8, j = w % 8;
+            const int c = I8 ? j / 2 : j % 4, h = I8 ? j % 2 : j / 4;
+            dst[(ks * 32 + c) * NB * 2 + h] = in ? v[i] : 0u;
+          }
+        }
+      }
+    };
+
+    load_q(segs[0]);
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i) load_next();
+
     for (int sg = 0; sg < nseg; ++sg) {
       const PagedSeg &g = segs[sg];
       const int row0 = g.rb * ROWS;
-      // ---- Q rows as A fragments
-      for (int i = tid; i < RW * (D / 16) * 32; i += NT) {
-        const int ln = i & 31, ks = (i >> 5) % (D / 16), w = i / (32 * (D / 16));
-        uint32_t f[4] = {0u, 0u, 0u, 0u};
+      if constexpr (!P::kQRegs) __syncthreads();
+      // positions of this lane's columns (-1: no such column)
+      int pos[NB][2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int gr = row0 + w * 16 + (ln >> 2) + 8 * hh;
-          if (gr < g.rows) {
-            const uint16_t *src = a.q + (long long)(g.tok0 + gr / a.G) * a.q_tok + (long long)(g.g * a.G + gr % a.G) * a.q_head + ks * 16;
-            if constexpr (I8) {       // k = 2c, 2c+1 and 2c+8, 2c+9 are channels 4c .. 4c+3
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 4 * (ln & 3)));
-              f[hh] = v.x;
-              f[2 + hh] = v.y;
-            } else {
-              f[hh] = __ldg(reinterpret_cast<const uint32_t *>(src + 2 * (ln & 3)));
-              f[2 + hh] = __ldg(reinterpret_cast<const uint32_t *>(src + 2 * (ln & 3) + 8));
-            }
-          }
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int gr = row0 + rw * COLS + nb * 8 + 2 * c4 + e;
+          pos[nb][e] = gr < g.rows ? g.pos0 + gr / a.G : -1;
         }
-        qf[i] = make_uint4(f[0], f[1], f[2], f[3]);
-      }
-      __syncthreads();
-      // positions of this lane's two rows (-1: no such row)
-      int pos[2];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int gr = row0 + rw * 16 + r8 + 8 * hh;
-        pos[hh] = gr < g.rows ? g.pos0 + gr / a.G : -1;
-      }
       const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + ROWS) - 1) / a.G;
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
+      for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][nb][e] = 0.0f;
+      float m[NB][2], l[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.0f;
+      }
 
 #pragma unroll 1
-      for (int u = g.u0; u < g.u1; ++u) {
-        cp_async_wait<ST - 2>();
-        if constexpr (RW == 1) __syncwarp();
-        else named_bar_sync(1 + kw, 32 * RW);
-        load_next();
-        const uint32_t kst = ring_s + (uint32_t)((stage * KW + kw) * P::kStageBytes), vst = kst + kStrip * RB;
-        const float *sc = reinterpret_cast<const float *>(smem + (stage * KW + kw) * P::kStageBytes + 2 * kStrip * RB);
-        const int unit = u < g.nsu ? u : g.first + u - g.nsu;
-        const int key0 = unit * U + kw * kStrip;
-        stage = stage + 1 == ST ? 0 : stage + 1;
-        if (key0 >= g.hi) continue;                      // nothing of this strip is visible
-        // ---- scores of 16 rows x 16 keys
-        float s[2][4] = {};
+      for (int u = g.u0 + kw; u < g.u1; u += KW) {
+        const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
         const int mi = lane >> 3;
-        const int krow = (lane & 7) + (mi >> 1) * 8;
-        if constexpr (!I8) {
+        // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
+        constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
+        float sp[CN][NB][4] = {};
+        float ksc[2] = {a.scale_log2, a.scale_log2};
+        {
+          const int hb = acquire();
+          const uint32_t kst = ring_s + (uint32_t)hb;
+          if constexpr (!I8) {
+            // A tile: matrices (keys 0-7, 8-15) x (channels 0-7, 8-15) of each 16
+            const int krow = (lane & 7) + (mi & 1) * 8;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t kf[4];
-            ldsm4(kf, kst + strip_off<RB>(krow, ks * 2 + (mi & 1)));
-            const uint4 q4 = qf[(rw * (D / 16) + ks) * 32 + lane];
-            const uint32_t af[4] = {q4.x, q4.y, q4.z, q4.w};
-            mma16816<BF>(s[0], af, kf[0], kf[1]);
-            mma16816<BF>(s[1], af, kf[2], kf[3]);
-          }
-        } else {
+            for (int ks = 0; ks < D / 16; ++ks) {
+              uint32_t kf[4];
+              ldsm4(kf, kst + strip_off<RB>(krow, ks * 2 + (mi >> 1)));
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            uint32_t kf[4];
-            ldsm4(kf, kst + strip_off<RB>(krow, kk * 2 + (mi & 1)));
+              for (int nb = 0; nb < NB; ++nb) {
+                uint32_t b0, b1;
+                if constexpr (P::kQRegs) {
+                  b0 = qr[ks][nb][0];
+                  b1 = qr[ks][nb][1];
+                } else {
+                  const uint2 v = reinterpret_cast<const uint2 *>(qsm)[((rw * (D / 16) + ks) * 32 + lane) * NB + nb];
+                  b0 = v.x;
+                  b1 = v.y;
+                }
+                mma16816<BF>(sp[ks % CN][nb], kf, b0, b1);
+              }
+            }
+          } else {
+            const float *sc = reinterpret_cast<const float *>(ring + hb + kStrip * RB);
+            ksc[0] *= sc[r8];
+            ksc[1] *= sc[r8 + 8];
+            // matrices: (keys 0-7, 8-15) x (channels 0-15, 16-31); a word holds four channels
+            const int krow = (lane & 7) + (mi & 1) * 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 q4 = qf[(rw * (D / 16) + kk * 2 + h) * 32 + lane];
-              const uint32_t af[4] = {q4.x, q4.y, q4.z, q4.w};
-              const uint32_t u0 = kf[h] ^ 0x80808080u, u1 = kf[2 + h] ^ 0x80808080u;
-              mma16816<false>(s[0], af, codes_f16<0x4140>(u0), codes_f16<0x4342>(u0));
-              mma16816<false>(s[1], af, codes_f16<0x4140>(u1), codes_f16<0x4342>(u1));
+            for (int kk = 0; kk < D / 32; ++kk) {
+              uint32_t kf[4];
+              ldsm4(kf, kst + strip_off<RB>(krow, kk * 2 + (mi >> 1)));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t u0 = kf[2 * h] ^ 0x80808080u, u1 = kf[2 * h + 1] ^ 0x80808080u;
+                const uint32_t af[4] = {codes_f16<0x4140>(u0), codes_f16<0x4140>(u1), codes_f16<0x4342>(u0), codes_f16<0x4342>(u1)};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  uint32_t b0, b1;
+                  if constexpr (P::kQRegs) {
+                    b0 = qr[kk * 2 + h][nb][0];
+                    b1 = qr[kk * 2 + h][nb][1];
+                  } else {
+                    const uint2 v = reinterpret_cast<const uint2 *>(qsm)[((rw * (D / 16) + kk * 2 + h) * 32 + lane) * NB + nb];
+                    b0 = v.x;
+                    b1 = v.y;
+                  }
+                  mma16816<false>(sp[(kk * 2 + h) % CN][nb], af, b0, b1);
+                }
+              }
             }
           }
+          release();
         }
-        // ---- weights: element (tile t, e): row r8 + 8 (e / 2), key key0 + 8 t + 2 c4 + (e & 1)
+        float s[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = sp[0][nb][e];
+#pragma unroll
+            for (int i = 1; i < CN; ++i) x += sp[i][nb][e];
+            s[nb][e] = x * ksc[e >> 1];
+          }
         const bool masked = key0 + kStrip - 1 > pmin ||
                             (a.window > 0 && key0 <= pmax - a.window && key0 + kStrip > a.sinks);
-        float vs[2][2], lvs[2][2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if constexpr (I8) {
-              const int j = 8 * t + 2 * c4 + e;
-              const float ksc = sc[j] * a.scale_log2;
-              s[t][e] *= ksc;
-              s[t][2 + e] *= ksc;
-              vs[t][e] = sc[kStrip + j];
-              lvs[t][e] = fmaxf(paged_lg2(fabsf(vs[t][e])), -64.0f);
-            } else {
-              s[t][e] *= a.scale_log2;
-              s[t][2 + e] *= a.scale_log2;
-              vs[t][e] = 1.0f;
-              lvs[t][e] = 0.0f;
-            }
-          }
         if (masked) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = key0 + 8 * t + 2 * c4 + (e & 1), ps = pos[e >> 1];
-              if (j > ps || (a.window > 0 && j <= ps - a.window && j >= a.sinks)) s[t][e] = -INFINITY;
+              const int j = key0 + r8 + 8 * (e >> 1), ps = pos[nb][e & 1];
+              if (j > ps || (a.window > 0 && j <= ps - a.window && j >= a.sinks)) s[nb][e] = -INFINITY;
             }
         }
-        float top[2];
+        const int hb = acquire();
+        const uint32_t vst = ring_s + (uint32_t)hb;
+        float vsc[2] = {1.0f, 1.0f}, lvs[2] = {0.0f, 0.0f};
+        if constexpr (I8) {
+          const float *sc = reinterpret_cast<const float *>(ring + hb + kStrip * RB);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float x = fmaxf(fmaxf(s[0][2 * hh] + lvs[0][0], s[0][2 * hh + 1] + lvs[0][1]),
-                          fmaxf(s[1][2 * hh] + lvs[1][0], s[1][2 * hh + 1] + lvs[1][1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          top[hh] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          for (int h = 0; h < 2; ++h) {
+            vsc[h] = sc[r8 + 8 * h];
+            lvs[h] = fmaxf(paged_lg2(fabsf(vsc[h])), -64.0f);
+          }
         }
-        // the reference moves only when a weight passes it by 2^8 (a weight then fits fp16)
-        const bool up = top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f;
+        // ---- weights.  The reference moves only when a weight passes it by 2^8 (a weight
+        // then still fits fp16), so the largest score of a strip is seldom needed exactly.
+        bool up = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up |= s[nb][e] + lvs[e >> 1] > m[nb][e & 1] + 8.0f;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float f = 1.0f;
-            if (top[hh] > m[hh] + 8.0f) {
-              f = paged_ex2(m[hh] - top[hh]);
-              m[hh] = top[hh];
-            }
-            l[hh] *= f;
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-              acc[t][2 * hh] *= f;
-              acc[t][2 * hh + 1] *= f;
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(s[nb][e] + lvs[0], s[nb][2 + e] + lvs[1]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              float f = 1.0f;
+              if (top > m[nb][e] + 8.0f) {
+                f = paged_ex2(m[nb][e] - top);
+                m[nb][e] = top;
+              }
+              l[nb][e] *= f;
+#pragma unroll
+              for (int t = 0; t < D / 16; ++t) {
+                acc[t][nb][e] *= f;
+                acc[t][nb][2 + e] *= f;
+              }
             }
+        }
+        uint32_t pk[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float ref0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], ref1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float p0 = paged_ex2(s[nb][2 * h] - ref0), p1 = paged_ex2(s[nb][2 * h + 1] - ref1);
+            l[nb][0] += p0;
+            l[nb][1] += p1;
+            if constexpr (I8) {          // (a hidden key's weight is 0 whatever its value's scale holds)
+              p0 = s[nb][2 * h] == -INFINITY ? 0.0f : p0 * vsc[h];
+              p1 = s[nb][2 * h + 1] == -INFINITY ? 0.0f : p1 * vsc[h];
+            }
+            pk[nb][h] = pack2<BF>(p0, p1);
           }
         }
-        uint32_t pf[4];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float ref = m[hh] == -INFINITY ? 0.0f : m[hh];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float p0 = paged_ex2(s[t][2 * hh] - ref), p1 = paged_ex2(s[t][2 * hh + 1] - ref);
-            l[hh] += p0 + p1;
-            // (a hidden key's weight is 0 whatever its value's scale holds)
-            if constexpr (I8)
-              pf[2 * t + hh] = pack2<false>(s[t][2 * hh] == -INFINITY ? 0.0f : p0 * vs[t][0],
-                                            s[t][2 * hh + 1] == -INFINITY ? 0.0f : p1 * vs[t][1]);
-            else
-              pf[2 * t + hh] = pack2<BF>(p0, p1);
-          }
-        }
-        // ---- P . V
-        const int vrow = (lane & 7) + (mi & 1) * 8;
+        // ---- O^T += V^T P^T
         if constexpr (!I8) {
-          // rows at several positions: a key hidden from some rows has weight 0 there, and 0
+          // columns at several positions: a key hidden from some has weight 0 there, and 0
           // times an infinite or NaN value would reach them through the MMA.  Strips that
           // hold such a value are summed without the hidden products.
           if (masked && pmin != pmax && strip_nonfinite<D, BF>(vst, lane)) {
-            add_visible<D, BF>(acc, pf, s, vst, lane);
+            add_visible<D, NB, BF>(acc, pk, s, vst, lane);
+            release();
             continue;
           }
+        }
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          pf[nb][0] = movm_t(pk[nb][0]);
+          pf[nb][1] = movm_t(pk[nb][1]);
+        }
+        const int vrow = (lane & 7) + (mi >> 1) * 8;
+        if constexpr (!I8) {
+          // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + strip_off<RB>(vrow, dt * 2 + (mi >> 1)));
-            mma16816<BF>(acc[2 * dt], pf, vf[0], vf[1]);
-            mma16816<BF>(acc[2 * dt + 1], pf, vf[2], vf[3]);
+            ldsm4_t(vf, vst + strip_off<RB>(vrow, dt * 2 + (mi & 1)));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<BF>(acc[dt][nb], vf, pf[nb][0], pf[nb][1]);
           }
         } else {
-          // a transposed 16-bit element holds two channels: the even and the odd ones go to
-          // two tiles (tile 2c: channels 16 c + 0, 2, .. 14; tile 2c + 1: 1, 3, .. 15)
+          // a transposed 16-bit element holds two channels: rows 0-7 of tile dt are the even
+          // channels of its 16, rows 8-15 the odd ones
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + strip_off<RB>(vrow, kk * 2 + (mi >> 1)));
+            ldsm4_t(vf, vst + strip_off<RB>(vrow, kk * 2 + (mi & 1)));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t u0 = vf[2 * h] ^ 0x80808080u, u1 = vf[2 * h + 1] ^ 0x80808080u;
-              mma16816<false>(acc[4 * kk + 2 * h], pf, codes_f16<0x4240>(u0), codes_f16<0x4240>(u1));
-              mma16816<false>(acc[4 * kk + 2 * h + 1], pf, codes_f16<0x4341>(u0), codes_f16<0x4341>(u1));
+              const uint32_t u0 = vf[h] ^ 0x80808080u, u1 = vf[2 + h] ^ 0x80808080u;
+              const uint32_t af[4] = {codes_f16<0x4240>(u0), codes_f16<0x4341>(u0), codes_f16<0x4240>(u1), codes_f16<0x4341>(u1)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816<false>(acc[2 * kk + h][nb], af, pf[nb][0], pf[nb][1]);
             }
           }
         }
+        release();
       }
 
       // ---- join the CTA's groups: out rows, or partial sums of a cut item
+      if constexpr (P::kQRegs)
+        if (sg + 1 < nseg) load_q(segs[sg + 1]);
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
-        l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-        if (c4 == 0) {
-          sm_m[kw * ROWS + rw * 16 + r8 + 8 * hh] = m[hh];
-          sm_l[kw * ROWS + rw * 16 + r8 + 8 * hh] = l[hh];
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
+          if (r8 == 0) {
+            sm_m[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = m[nb][e];
+            sm_l[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = l[nb][e];
+          }
         }
-      }
       __syncthreads();                                   // also: Q is no longer read
-      float f[2];
+      float f[NB][2];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float M = -INFINITY;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + rw * 16 + r8 + 8 * hh]);
-        f[hh] = m[hh] == -INFINITY ? 0.0f : paged_ex2(m[hh] - M);
-      }
+        for (int e = 0; e < 2; ++e) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + rw * COLS + nb * 8 + 2 * c4 + e]);
+          f[nb][e] = m[nb][e] == -INFINITY ? 0.0f : paged_ex2(m[nb][e] - M);
+        }
       const bool cut = g.c0 != g.c1;
       float *part = a.part + (size_t)(2 * blockIdx.x + (g.c0 == (int)blockIdx.x ? 1 : 0)) * P::kPartFloats;
       const int nrows = min(ROWS, g.rows - row0);
-      // row sums: M and L of each row (thread r)
+      // column sums: M and L of each column (thread r)
       float M = -INFINITY, L = 0.0f;
       if (tid < nrows) {
         for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
@@ -616,35 +780,39 @@ __global__ void __launch_bounds__(PagedShape<D, KV, RW>::kThreads, 1)
         }
       }
       __syncthreads();
+      if constexpr (!P::kQRegs)
+        if (sg + 1 < nseg) load_q(segs[sg + 1]);
       if (tid < nrows) sm_l[tid] = L == 0.0f ? 0.0f : 1.0f / L;      // no key: a row of zeros
 #pragma unroll
-      for (int sl = 0; sl < D / 32; ++sl) {
-        float *w = red + (warp * 16) * kRedStride;
+      for (int sl = 0; sl < D / SW; ++sl) {
+        float *w = red + warp * COLS * (SW + 4);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float(&x)[4] = acc[4 * sl + t];
-          if constexpr (!I8) {
-            *reinterpret_cast<float2 *>(w + r8 * kRedStride + 8 * t + 2 * c4) = make_float2(x[0] * f[0], x[1] * f[0]);
-            *reinterpret_cast<float2 *>(w + (r8 + 8) * kRedStride + 8 * t + 2 * c4) = make_float2(x[2] * f[1], x[3] * f[1]);
-          } else if (t % 2 == 0) {
-            const float(&y)[4] = acc[4 * sl + t + 1];
-            *reinterpret_cast<float4 *>(w + r8 * kRedStride + 8 * t + 4 * c4) =
-                make_float4(x[0] * f[0], y[0] * f[0], x[1] * f[0], y[1] * f[0]);
-            *reinterpret_cast<float4 *>(w + (r8 + 8) * kRedStride + 8 * t + 4 * c4) =
-                make_float4(x[2] * f[1], y[2] * f[1], x[3] * f[1], y[3] * f[1]);
+        for (int t = 0; t < SW / 16; ++t)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float(&x)[4] = acc[sl * (SW / 16) + t][nb];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float *dst = w + (nb * 8 + 2 * c4 + e) * (SW + 4) + 16 * t;
+              if constexpr (!I8) {
+                dst[r8] = x[e] * f[nb][e];
+                dst[r8 + 8] = x[2 + e] * f[nb][e];
+              } else {
+                *reinterpret_cast<float2 *>(dst + 2 * r8) = make_float2(x[e] * f[nb][e], x[2 + e] * f[nb][e]);
+              }
+            }
           }
-        }
         __syncthreads();
-        for (int i = tid; i < nrows * 16; i += NT) {
-          const int r = i >> 4, cp = i & 15;
+        for (int i = tid; i < nrows * (SW / 2); i += NT) {
+          const int r = i / (SW / 2), cp = i % (SW / 2);
           float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int w2 = 0; w2 < KW; ++w2) {
-            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * RW + (r >> 4)) * 16 + (r & 15)) * kRedStride + 2 * cp);
+            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * RW + r / COLS) * COLS + r % COLS) * (SW + 4) + 2 * cp);
             o.x += v.x;
             o.y += v.y;
           }
-          const int col = 32 * sl + 2 * cp;
+          const int col = SW * sl + 2 * cp;
           if (cut) {
             *reinterpret_cast<float2 *>(part + 2 * ROWS + (size_t)r * D + col) = o;
           } else {
@@ -661,8 +829,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, RW>::kThreads, 1)
       // ---- a cut item: the last CTA to finish it joins the parts, in CTA order
       __threadfence();
       __syncthreads();
+      const int n = g.c1 - g.c0 + 1;
       if (tid == 0) {
-        const int n = g.c1 - g.c0 + 1;
         const int old = atom_add_acq_rel_gpu(a.counters + g.c0, 1);
         ctl[6] = old == n - 1;
         if (old == n - 1) a.counters[g.c0] = 0;          // zero again for the next call
@@ -670,58 +838,92 @@ __global__ void __launch_bounds__(PagedShape<D, KV, RW>::kThreads, 1)
       __syncthreads();
       if (ctl[6] == 0) continue;
       __threadfence();
-      const float *p0 = a.part + (size_t)(2 * g.c0 + 1) * P::kPartFloats;         // the first part: slot 1
-      auto slot = [&](int i) { return i == 0 ? p0 : a.part + (size_t)(2 * (g.c0 + i)) * P::kPartFloats; };
-      const int n = g.c1 - g.c0 + 1;
-      for (int i = tid; i < nrows * (D / 4); i += NT) {
-        const int r = i / (D / 4), col = 4 * (i % (D / 4));
-        float Mx = -INFINITY;
-        for (int k = 0; k < n; ++k) Mx = fmaxf(Mx, __ldcg(slot(k) + r));
-        float Ls = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-          const float *s = slot(k);
-          const float mk = __ldcg(s + r), lk = __ldcg(s + ROWS + r);
-          const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + 2 * ROWS + (size_t)r * D + col));
-          const float wgt = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
-          Ls += lk * wgt;
-          o.x += v.x * wgt;
-          o.y += v.y * wgt;
-          o.z += v.z * wgt;
-          o.w += v.w * wgt;
+      // the first part is in its CTA's slot 1, the others in their slots 0
+      auto slot = [&](int i) { return a.part + (size_t)(2 * (g.c0 + i) + (i == 0 ? 1 : 0)) * P::kPartFloats; };
+      // `chunk` columns at a time: their parts' m and l in shared memory, then each part's weight
+      const int chunk = min(nrows, P::kRedBytes / 8 / n);
+      float *mm = red, *ll = red + chunk * n;
+      for (int r0 = 0; r0 < nrows; r0 += chunk) {
+        const int nr = min(chunk, nrows - r0);
+        for (int i = tid; i < n * nr; i += NT) {
+          const int k = i / nr, r = i - k * nr;
+          const float *s = slot(k) + r0 + r;
+          mm[k * nr + r] = __ldcg(s);
+          ll[k * nr + r] = __ldcg(s + ROWS);
         }
-        const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-        const int gr = row0 + r;
-        const long long orow = (long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G;
-        *reinterpret_cast<uint2 *>(a.out + orow * D + col) =
-            make_uint2(pack2<BF>(o.x * inv, o.y * inv), pack2<BF>(o.z * inv, o.w * inv));
-        if (a.lse && col == 0)
-          a.lse[orow] = Ls > 0.0f || Ls != Ls ? (Mx + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+        __syncthreads();
+        if (tid < nr) {
+          float Mx = -INFINITY, Ls = 0.0f;
+          for (int k = 0; k < n; ++k) Mx = fmaxf(Mx, mm[k * nr + tid]);
+          for (int k = 0; k < n; ++k) {
+            const float mk = mm[k * nr + tid], w = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
+            Ls += ll[k * nr + tid] * w;
+            mm[k * nr + tid] = w;
+          }
+          const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+          for (int k = 0; k < n; ++k) mm[k * nr + tid] *= inv;
+          const int gr = row0 + r0 + tid;
+          if (a.lse)
+            a.lse[(long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G] =
+                Ls > 0.0f || Ls != Ls ? (Mx + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
+        constexpr int NI = 4;                            // results a thread works on at a time
+        for (int i0 = tid; i0 < nr * (D / 4); i0 += NI * NT) {
+          float4 o[NI] = {};
+#pragma unroll 2
+          for (int k = 0; k < n; ++k) {
+            const float *s = slot(k) + 2 * ROWS + (size_t)r0 * D;
+#pragma unroll
+            for (int x = 0; x < NI; ++x) {
+              const int i = i0 + x * NT;
+              if (i < nr * (D / 4)) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(s) + i);
+                const float w = mm[k * nr + i / (D / 4)];
+                o[x].x += v.x * w;
+                o[x].y += v.y * w;
+                o[x].z += v.z * w;
+                o[x].w += v.w * w;
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < NI; ++x) {
+            const int i = i0 + x * NT;
+            if (i < nr * (D / 4)) {
+              const int gr = row0 + r0 + i / (D / 4);
+              uint16_t *dst = a.out + ((long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G) * D + 4 * (i % (D / 4));
+              *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF>(o[x].x, o[x].y), pack2<BF>(o[x].z, o[x].w));
+            }
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
     if (!more) break;
   }
 }
 
-template <int D, int KV, int RW>
+template <int D, int KV, int NB, int RW>
 cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
-  using P = PagedShape<D, KV, RW>;
-  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, RW>);
+  using P = PagedShape<D, KV, NB, RW>;
+  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, NB, RW>);
   cudaError_t e = ensure_smem_attr(f, P::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(f, dim3(sms), dim3(P::kThreads), P::kSmem, st, a);
   count_launch();
   return e;
 }
+// cols: the columns a CTA takes at a time (paged_columns)
 template <int KV>
-cudaError_t paged_launch(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st) {
-#define QW_PAGED(DD)                                                     \
-  case DD:                                                               \
-    return rw == 1   ? paged_launch_one<DD, KV, 1>(a, sms, st)           \
-           : rw == 2 ? paged_launch_one<DD, KV, 2>(a, sms, st)           \
-                     : paged_launch_one<DD, KV, 4>(a, sms, st);
+cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
+#define QW_PAGED(DD)                                                      \
+  case DD:                                                                \
+    return cols == 8    ? paged_launch_one<DD, KV, 1, 1>(a, sms, st)      \
+           : cols == 16 ? paged_launch_one<DD, KV, 2, 1>(a, sms, st)      \
+           : cols == 32 ? paged_launch_one<DD, KV, 2, 2>(a, sms, st)      \
+           : cols == 48 ? paged_launch_one<DD, KV, 2, 3>(a, sms, st)      \
+                        : paged_launch_one<DD, KV, 2, 4>(a, sms, st);
   switch (d) {
     QW_PAGED(64)
     QW_PAGED(128)

@@ -2,7 +2,7 @@
 #include "attn_paged.cuh"
 
 namespace qw {
-cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st) {
-  return paged_launch<kPagedBf16>(a, d, rw, sms, st);
+cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
+  return paged_launch<kPagedBf16>(a, d, cols, sms, st);
 }
 }  // namespace qw

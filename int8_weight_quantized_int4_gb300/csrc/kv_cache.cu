@@ -239,16 +239,16 @@ const void *append_kernel(int d) {
                     : reinterpret_cast<const void *>(kv_append_kernel<256, I8>);
 }
 
-// ---- attention: row tiles a CTA handles, and the workspace for them
-// One tile of 16 query rows when the step's rows (new tokens x heads a KV head) fit, two or
-// four when they do not, so that K and V are read once for all of a sequence's rows.
-int paged_row_tiles(int max_new, int G) {
-  const long long rows = (long long)max_new * G;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+// ---- attention: the query columns a CTA takes at a time, and the workspace for them
+// The fewest that hold a step's columns (new tokens x heads a KV head), so that K and V are
+// read once for all of a sequence's columns.
+int paged_columns(int max_new, int G) {
+  const long long n = (long long)max_new * G;
+  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 48 ? 48 : 64;
 }
 constexpr size_t kPagedCounterBytes = 4096;      // one counter a CTA
-size_t paged_ws(int d, int rw, int sms) {
-  return kPagedCounterBytes + (size_t)2 * sms * (16 * rw) * (d + 2) * 4;
+size_t paged_ws(int d, int cols, int sms) {
+  return kPagedCounterBytes + (size_t)2 * sms * cols * (d + 2) * 4;
 }
 int check_heads(int d, int Hq, int Hkv, int max_new) {
   if (Hq < 1 || Hkv < 1 || max_new < 1) return bad(QW_ERR_INVALID_ARG, "Hq, Hkv and max_new must be positive");
@@ -353,7 +353,7 @@ int kv_copy_pages(const qw_page_pool_t *pools, int n_pools, const int32_t *pairs
 size_t attn_paged_workspace_bytes(int d, int Hq, int Hkv, int max_new) {
   int sms = 0;
   if (check_heads(d, Hq, Hkv, max_new) || device_info(&sms, nullptr)) return 0;
-  return paged_ws(d, paged_row_tiles(max_new, Hq / Hkv), sms);
+  return paged_ws(d, paged_columns(max_new, Hq / Hkv), sms);
 }
 size_t attn_paged_workspace_zero_bytes(int d, int Hq, int Hkv, int max_new) {
   return check_heads(d, Hq, Hkv, max_new) ? 0 : kPagedCounterBytes;
@@ -378,8 +378,8 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   int sms = 0;
   if ((rc = device_info(&sms, &a.err))) return rc;
   a.G = Hq / c->Hkv;
-  const int rw = paged_row_tiles(max_new, a.G);
-  const size_t need = paged_ws(c->d, rw, sms);
+  const int cols = paged_columns(max_new, a.G);
+  const size_t need = paged_ws(c->d, cols, sms);
   if (sms * 4 > (int)kPagedCounterBytes) return bad(QW_ERR_ARCH, "more than %zu SMs", kPagedCounterBytes / 4);
   if (!ws || ws_bytes < need)
     return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
@@ -408,14 +408,14 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.cap = b->max_pages * c->page;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
-  a.min_units = 1;
+  a.min_strips = 4;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.counters = static_cast<int *>(ws);
   a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kPagedCounterBytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = c->dtype == QW_KV_F16    ? launch_attn_paged_f16(a, c->d, rw, sms, st)
-                  : c->dtype == QW_KV_BF16 ? launch_attn_paged_bf16(a, c->d, rw, sms, st)
-                                           : launch_attn_paged_i8(a, c->d, rw, sms, st);
+  cudaError_t e = c->dtype == QW_KV_F16    ? launch_attn_paged_f16(a, c->d, cols, sms, st)
+                  : c->dtype == QW_KV_BF16 ? launch_attn_paged_bf16(a, c->d, cols, sms, st)
+                                           : launch_attn_paged_i8(a, c->d, cols, sms, st);
   if (e != cudaSuccess) return bad(QW_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
   return QW_OK;
 }

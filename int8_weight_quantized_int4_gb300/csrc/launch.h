@@ -107,7 +107,6 @@ cudaError_t launch_attn(const AttnLaunch &L, cudaStream_t st);
 
 // Paged key-value cache (kv_cache.cu, attn_paged*.cu).  Cache types:
 enum { kPagedF16 = 0, kPagedBf16 = 1, kPagedI8 = 2 };
-constexpr int kPagedMaxRows = 64;       // query rows a CTA handles at a time (4 row tiles)
 struct PagedArgs {
   const uint16_t *q;            // [T][Hq][d], token and head strides q_tok, q_head (elements)
   uint16_t *out;                // [T][Hq][d] dense
@@ -119,15 +118,15 @@ struct PagedArgs {
   int B, T, Hq, Hkv, G, page, npages, max_pages;
   int cap;                      // keys the page table can name: max_pages * page
   int window, sinks;            // window 0: every key up to the position; sinks 0 without one
-  int min_units;                // fewest units a CTA takes
+  int min_strips;               // fewest strips of 16 keys a CTA takes
   float scale_log2;             // softmax scale * log2(e)
   float *part;                  // [2 CTAs][rows (d + 2)] partial sums (workspace)
   int *counters;                // [CTAs] arrivals, zero between calls (workspace)
   int *err;
 };
-cudaError_t launch_attn_paged_f16(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st);
-cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st);
-cudaError_t launch_attn_paged_i8(const PagedArgs &a, int d, int rw, int sms, cudaStream_t st);
+cudaError_t launch_attn_paged_f16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
+cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
+cudaError_t launch_attn_paged_i8(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
 
 cudaError_t launch_gemm_w4a16(const GemmArgs &a, cudaStream_t st);
 // W4A8 (token scales in the epilogue): act8, int8 codes widened in the kernel (token
