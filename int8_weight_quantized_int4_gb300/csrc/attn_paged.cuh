@@ -58,6 +58,17 @@ struct PagedSeg {
   int c0, c1;                   // CTAs holding the item's first and last strip
 };
 
+// A CTA's list of work and the state to list the rest, in shared memory.
+struct PagedCtl {
+  int nseg, more;               // segments listed; whether others follow
+  int njoin;                    // cut items this CTA was the last to finish
+  PagedSeg join[2];
+  int b;                        // walk: sequence
+  long long off, pos;           // walk: place in the sequence, in all
+  long long begin, end, share;  // the range
+  int part[16];
+};
+
 // Shapes.  NB: MMA column tiles (of 8) a warp; RW: warps a group (column blocks of 8 NB RW).
 // The warps a CTA has are what the registers allow: accumulators take D NB / 4 registers a
 // thread and the Q fragments D NB / 8 more (in shared memory where D NB = 512).
@@ -78,7 +89,7 @@ struct PagedShape {
   // 2 c and channels r8 of a warp's lanes fall on distinct banks)
   static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
   static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
-  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kPagedMaxSegs * (int)sizeof(PagedSeg) + 256;
+  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
   static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
   static constexpr int kRing = kFit > 8 ? 8 : kFit;    // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
@@ -197,6 +208,18 @@ __device__ __forceinline__ void add_visible(float (&acc)[D / 16][NB][4], const u
   }
 }
 
+// Chunk s of a row, s = 2 k + h (k the MMA step, h this lane's half): the offsets of steps
+// 0 .. 3; step k is 128 (k / 4) bytes past step k % 4 (the swizzle permutes 128 bytes).
+template <int RB>
+struct LaneOffs {
+  uint32_t x[RB >= 128 ? 4 : 2];
+  __device__ __forceinline__ LaneOffs(int row, int half) {
+#pragma unroll
+    for (int k = 0; k < (RB >= 128 ? 4 : 2); ++k) x[k] = strip_off<RB>(row, 2 * k + half);
+  }
+  __device__ __forceinline__ uint32_t operator()(int k) const { return x[k % (RB >= 128 ? 4 : 2)] + (uint32_t)(k / 4 * 128); }
+};
+
 // --------------------------------------------------------------- the schedule --
 // Sequence b's new tokens and keys, clamped to what the buffers hold (a length beyond the
 // page table or offsets out of order record QW_ERR_BAD_INDEX).
@@ -229,10 +252,284 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedS
   return p;
 }
 
+__device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head,
+                                          int G) {
+  g.b = b;
+  g.rb = rb;
+  g.g = head;
+  g.nsu = p.nsu;
+  g.first = p.first;
+  g.lo = p.lo;
+  g.hi = p.hi;
+  g.pos0 = s.len - s.nq;
+  g.rows = s.nq * G;
+  g.tok0 = s.tok0;
+}
+
 // a / b (a >= 0, b > 0), in 32 bits where both fit
 __device__ __forceinline__ long long paged_div(long long a, long long b) {
   if (((unsigned long long)(a | b) >> 32) == 0ull) return (unsigned)a / (unsigned)b;
   return a / b;
+}
+
+// One segment: the strips of the item that starts at place `at` which lie in the range.
+template <int IC>
+__device__ __forceinline__ void paged_emit(PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head,
+                                           long long at, long long begin, long long end, long long share, int G) {
+  g.u0 = (int)max(begin - at - IC, 0ll);
+  g.u1 = (int)min(end - at - IC, (long long)p.n);
+  g.c0 = g.u0 == 0 ? (int)blockIdx.x : (int)paged_div(at + IC, share);
+  g.c1 = g.u1 == p.n ? (int)blockIdx.x : (int)paged_div(at + IC + p.n - 1, share);
+  paged_fill(g, s, p, b, rb, head, G);
+}
+
+// Lists the range's next segments (one thread).
+template <int ROWS, int IC>
+__device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, PagedCtl *ctl) {
+  int n = 0, b = ctl->b;
+  long long off = ctl->off, pos = ctl->pos;
+  const long long end = ctl->end;
+  while (pos < end && n < kPagedMaxSegs) {
+    const PagedSeq s = paged_seq(a, b);
+    const int nrb = (s.nq * a.G + ROWS - 1) / ROWS;
+    long long o = off;
+    int rb = 0;
+    PagedSpan p{};
+    for (; rb < nrb; ++rb) {
+      p = paged_span<ROWS>(a, s, rb);
+      if (o < (long long)(p.n + IC) * a.Hkv) break;
+      o -= (long long)(p.n + IC) * a.Hkv;
+    }
+    if (rb == nrb) {
+      ++b;
+      off = 0;
+      continue;
+    }
+    const int head = (int)paged_div(o, p.n + IC), in = (int)(o - (long long)head * (p.n + IC));
+    PagedSeg &g = segs[n];
+    paged_emit<IC>(g, s, p, b, rb, head, pos - in, ctl->begin, end, ctl->share, a.G);
+    if (g.u0 < g.u1) ++n;                               // (a range may end among an item's first places)
+    pos += p.n + IC - in;
+    off += p.n + IC - in;
+  }
+  ctl->nseg = n;
+  ctl->more = pos < end;
+  ctl->b = b;
+  ctl->off = off;
+  ctl->pos = pos;
+}
+
+// This CTA's work: its first segments and the state to list the others; false: none.  Every
+// item takes IC places and one for each strip; the places of all items, in order, are cut into
+// equal ranges -- or, where that costs little more than the equal share (`whole`), each item
+// gets CTAs of its own: no CTA then finishes two items one after the other, which is what a
+// short call would wait for.
+template <int ROWS, int IC, int NW>
+__device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *segs, PagedCtl *ctl, float *scratch) {
+  constexpr int NT = 32 * NW;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.B + NT - 1) / NT;
+  const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
+  auto blocks = [&](const PagedSeq &s) { return (s.nq * a.G + ROWS - 1) / ROWS; };
+  auto cost = [&](const PagedSeq &s) {
+    long long c = 0;
+    for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_span<ROWS>(a, s, rb).n + IC;
+    return c * a.Hkv;
+  };
+  PagedSeq own{};                                       // per == 1: this thread's sequence
+  long long mine = 0;
+  int items = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    own = paged_seq(a, b);
+    mine += cost(own);
+    items = min(items + blocks(own) * a.Hkv, 1 << 20);
+  }
+  if (tid == 0) {
+    ctl->nseg = 0;
+    ctl->more = 0;
+    ctl->njoin = 0;
+  }
+  long long total = 0, pre = 0;
+  {
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    items = __reduce_add_sync(0xffffffffu, items);
+    longlong2 *ws = reinterpret_cast<longlong2 *>(scratch);
+    if (lane == 31) ws[warp] = make_longlong2(inc, items);
+    __syncthreads();
+    items = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const longlong2 v = ws[w];
+      if (w < warp) pre += v.x;
+      total += v.x;
+      items += (int)v.y;
+    }
+    pre += inc - mine;
+  }
+  const int grid = gridDim.x, me = blockIdx.x;
+  const long long share = max(paged_div(total + grid - 1, grid), (long long)a.min_strips);
+  // strips a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
+  long long size = 0;
+  if (per == 1 && items < grid)
+    size = max(paged_div(total - (long long)IC * items + grid - items - 1, grid - items), (long long)a.min_strips);
+  if (size > 0 && size <= share + 2 * IC) {
+    const int sz = (int)min(size, 1ll << 30);
+    int parts = 0, pp = 0;
+    for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += (paged_span<ROWS>(a, own, rb).n + sz - 1) / sz * a.Hkv;
+    int inc = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) ctl->part[warp] = inc;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) pp += w < warp ? ctl->part[w] : 0;
+    pp += inc - parts;
+    if (me >= pp && me < pp + parts) {                  // one thread, if any
+      int at = pp;
+      for (int rb = 0, n = blocks(own); rb < n; ++rb) {
+        const PagedSpan p = paged_span<ROWS>(a, own, rb);
+        const int np = (p.n + sz - 1) / sz;
+        if (me < at + np * a.Hkv) {
+          PagedSeg &g = segs[0];
+          const int head = (me - at) / np, j = me - at - head * np, len = (p.n + np - 1) / np;
+          g.u0 = j * len;
+          g.u1 = min(p.n, g.u0 + len);
+          g.c0 = me - j;
+          g.c1 = g.c0 + np - 1;
+          paged_fill(g, own, p, b_lo, rb, head, a.G);
+          ctl->nseg = 1;
+          break;
+        }
+        at += np * a.Hkv;
+      }
+    }
+    __syncthreads();
+    return ctl->nseg != 0;
+  }
+  const long long begin = share * me, end = min(total, begin + share);
+  if (begin >= end) return false;
+  // Up to a sequence a thread and kPagedMaxSegs segments: every thread lists its own
+  // sequence's (in any order); otherwise thread 0 walks, a list at a time.
+  if (pre < end && begin < pre + mine) {
+    long long at = pre;
+    if (per == 1)
+      for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
+        const PagedSpan p = paged_span<ROWS>(a, own, rb);
+        const int each = p.n + IC;
+        int head = begin > at ? (int)min(paged_div(begin - at, each), (long long)a.Hkv) : 0;
+        long long x = at + (long long)head * each;
+        for (; head < a.Hkv && x + IC < end; ++head, x += each)
+          if (x + each > begin) {
+            const int i = atomicAdd(&ctl->nseg, 1);
+            if (i < kPagedMaxSegs) paged_emit<IC>(segs[i], own, p, b_lo, rb, head, x, begin, end, share, a.G);
+          }
+        at += (long long)a.Hkv * each;
+      }
+    if (begin >= pre) {                                 // the owner of the range's first place
+      long long off = begin - pre;
+      int b = b_lo;
+      for (; b + 1 < b_hi; ++b) {
+        const long long c = cost(paged_seq(a, b));
+        if (off < c) break;
+        off -= c;
+      }
+      ctl->b = b;
+      ctl->off = off;
+      ctl->pos = ctl->begin = begin;
+      ctl->end = end;
+      ctl->share = share;
+    }
+  }
+  __syncthreads();
+  if (per > 1 || ctl->nseg > kPagedMaxSegs) {
+    __syncthreads();
+    if (tid == 0) paged_walk<ROWS, IC>(a, segs, ctl);
+    __syncthreads();
+  }
+  return ctl->nseg != 0;
+}
+
+// Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
+template <int D, int KV, int NB, int RW>
+__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g, float *red) {
+  using P = PagedShape<D, KV, NB, RW>;
+  constexpr int NT = P::kThreads, ROWS = P::kRows;
+  constexpr bool BF = KV == kPagedBf16;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int row0 = g.rb * ROWS, nrows = min(ROWS, g.rows - row0), n = g.c1 - g.c0 + 1;
+  // the first part is in its CTA's slot 1, the others in their slots 0
+  auto slot = [&](int i) { return a.part + (size_t)(2 * (g.c0 + i) + (i == 0 ? 1 : 0)) * P::kPartFloats; };
+  // `chunk` columns at a time: their parts' m and l in shared memory, then each part's weight
+  const int chunk = min(nrows, P::kRedBytes / 8 / n);
+  float *mm = red, *ll = red + chunk * n;
+  for (int r0 = 0; r0 < nrows; r0 += chunk) {
+    const int nr = min(chunk, nrows - r0);
+    for (int i = tid; i < n * nr; i += NT) {
+      const int k = i / nr, r = i - k * nr;
+      const float *s = slot(k) + r0 + r;
+      mm[k * nr + r] = __ldcg(s);
+      ll[k * nr + r] = __ldcg(s + ROWS);
+    }
+    __syncthreads();
+    // eight lanes a column
+    for (int r = tid >> 3; r < (nr + 3) / 4 * 4; r += NT / 8) {       // whole warps
+      const int e = lane & 7;
+      float Mx = -INFINITY, Ls = 0.0f;
+      if (r < nr)
+        for (int k = e; k < n; k += 8) Mx = fmaxf(Mx, mm[k * nr + r]);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
+      if (r < nr)
+        for (int k = e; k < n; k += 8) {
+          const float mk = mm[k * nr + r], w = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
+          Ls += ll[k * nr + r] * w;
+          mm[k * nr + r] = w;
+        }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+      if (r < nr)
+        for (int k = e; k < n; k += 8) mm[k * nr + r] *= inv;
+      if (a.lse && r < nr && e == 0) {
+        const int gr = row0 + r0 + r;
+        a.lse[(long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G] =
+            Ls > 0.0f || Ls != Ls ? (Mx + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < nr * (D / 4); i += NT) {
+      const int r = i / (D / 4);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k0 = 0; k0 < n; k0 += 8) {            // eight parts in flight
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (k0 + x < n)
+            v[x] = __ldcg(reinterpret_cast<const float4 *>(slot(k0 + x) + 2 * ROWS + (size_t)r0 * D) + i);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (k0 + x < n) {
+            const float w = mm[(k0 + x) * nr + r];
+            o.x += v[x].x * w;
+            o.y += v[x].y * w;
+            o.z += v[x].z * w;
+            o.w += v[x].w * w;
+          }
+      }
+      const int gr = row0 + r0 + r;
+      uint16_t *dst = a.out + ((long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G) * D + 4 * (i % (D / 4));
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF>(o.x, o.y), pack2<BF>(o.z, o.w));
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, int KV, int NB, int RW>
@@ -250,7 +547,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
   float *sm_l = sm_m + P::kWarps * COLS;
   PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_l + P::kWarps * COLS);
-  int *ctl = reinterpret_cast<int *>(segs + kPagedMaxSegs);           // [0..63]
+  PagedCtl *ctl = reinterpret_cast<PagedCtl *>(segs + kPagedMaxSegs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rw = warp % RW, kw = warp / RW;
@@ -258,136 +555,19 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   uint8_t *ring = smem + kw * R * P::kHalf;                           // this group's half stages
   const uint32_t ring_s = smem_u32(ring);
 
+  // this lane's row and half of the four matrices it addresses: K as keys x channels, V
+  // transposed (channels x keys)
+  const LaneOffs<RB> koff((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4), voff((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- this CTA's range.  Every item takes kItemCost places and one for each strip; the
-  // places of all items, in order, are cut into equal ranges.
-  constexpr int IC = P::kItemCost;
-  long long total = 0, pre = 0, mine = 0;
-  const int per = (a.B + NT - 1) / NT;
-  const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
-  auto cost = [&](const PagedSeq &s) {
-    long long c = 0;
-    for (int rb = 0, n = (s.nq * a.G + ROWS - 1) / ROWS; rb < n; ++rb) c += paged_span<ROWS>(a, s, rb).n + IC;
-    return c * a.Hkv;
-  };
-  PagedSeq own{};                                                     // per == 1: this thread's sequence
-  for (int b = b_lo; b < b_hi; ++b) {
-    own = paged_seq(a, b);
-    mine += cost(own);
-  }
-  if (tid == 0) ctl[4] = 0;
-  {
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    long long *ws = reinterpret_cast<long long *>(red);
-    if (lane == 31) ws[warp] = inc;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < P::kWarps; ++w) {
-      if (w < warp) pre += ws[w];
-      total += ws[w];
-    }
-    pre += inc - mine;
-  }
-  const long long share = max(paged_div(total + gridDim.x - 1, gridDim.x), (long long)a.min_strips);
-  const long long begin = share * blockIdx.x, end = min(total, begin + share);
-  if (begin >= end) return;                                           // whole CTA
-  // one segment: the strips of the item that starts at place `at` which lie in this range
-  auto emit = [&](PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head, long long at) {
-    g.b = b;
-    g.rb = rb;
-    g.g = head;
-    g.u0 = (int)max(begin - at - IC, 0ll);
-    g.u1 = (int)min(end - at - IC, (long long)p.n);
-    g.nsu = p.nsu;
-    g.first = p.first;
-    g.lo = p.lo;
-    g.hi = p.hi;
-    g.pos0 = s.len - s.nq;
-    g.rows = s.nq * a.G;
-    g.tok0 = s.tok0;
-    g.c0 = (int)paged_div(at + IC, share);
-    g.c1 = (int)paged_div(at + IC + p.n - 1, share);
-  };
-  // Up to a sequence a thread and kPagedMaxSegs segments: every thread lists its own
-  // sequence's (in any order); otherwise thread 0 walks, a list at a time.
-  if (pre < end && begin < pre + mine) {
-    long long at = pre;
-    if (per == 1)
-      for (int rb = 0, n = (own.nq * a.G + ROWS - 1) / ROWS; rb < n && at < end; ++rb) {
-        const PagedSpan p = paged_span<ROWS>(a, own, rb);
-        const int each = p.n + IC;
-        int head = begin > at ? (int)min(paged_div(begin - at, each), (long long)a.Hkv) : 0;
-        long long x = at + (long long)head * each;
-        for (; head < a.Hkv && x + IC < end; ++head, x += each)
-          if (x + each > begin) {
-            const int i = atomicAdd(ctl + 4, 1);
-            if (i < kPagedMaxSegs) emit(segs[i], own, p, b_lo, rb, head, x);
-          }
-        at += (long long)a.Hkv * each;
-      }
-    if (begin >= pre) {                                 // the owner of the range's first place
-      long long off = begin - pre;
-      int b = b_lo;
-      for (; b + 1 < b_hi; ++b) {
-        const long long c = cost(paged_seq(a, b));
-        if (off < c) break;
-        off -= c;
-      }
-      ctl[0] = b;
-      *reinterpret_cast<long long *>(ctl + 2) = off;
-    }
-  }
-  __syncthreads();
-  const bool walk = per > 1 || ctl[4] > kPagedMaxSegs;
-  // the walk's state, kept by thread 0: sequence, offset in it, places done
-  int wb = ctl[0];
-  long long woff = *reinterpret_cast<long long *>(ctl + 2), wpos = begin;
+  if (!paged_schedule<ROWS, P::kItemCost, P::kWarps>(a, segs, ctl, red)) return;       // whole CTA
 
   float acc[D / 16][NB][4];
   for (;;) {
-    if (walk) {
-      // ---- list the next segments
-      __syncthreads();
-      if (tid == 0) {
-        int n = 0;
-        while (wpos < end && n < kPagedMaxSegs) {
-          const PagedSeq s = paged_seq(a, wb);
-          const int nrb = (s.nq * a.G + ROWS - 1) / ROWS;
-          long long off = woff;
-          int rb = 0;
-          PagedSpan p{};
-          for (; rb < nrb; ++rb) {
-            p = paged_span<ROWS>(a, s, rb);
-            if (off < (long long)(p.n + IC) * a.Hkv) break;
-            off -= (long long)(p.n + IC) * a.Hkv;
-          }
-          if (rb == nrb) {
-            ++wb;
-            woff = 0;
-            continue;
-          }
-          const int head = (int)paged_div(off, p.n + IC), in = (int)(off - (long long)head * (p.n + IC));
-          PagedSeg &g = segs[n];
-          emit(g, s, p, wb, rb, head, wpos - in);
-          if (g.u0 < g.u1) ++n;                         // (a range may end among an item's first places)
-          wpos += p.n + IC - in;
-          woff += p.n + IC - in;
-        }
-        ctl[4] = n;
-        ctl[5] = wpos < end;
-      }
-      __syncthreads();
-    }
-    const int nseg = ctl[4];
-    const bool more = walk && ctl[5] != 0;
-    if (nseg == 0) break;                               // (only places of no strip)
+    const int nseg = ctl->nseg;
+    const bool more = ctl->more != 0;
 
     // ---- the ring: this group's strips (u0 + kw, + KW, ..), ahead of the arithmetic, each as
     // two half stages: its K rows, then its V rows
@@ -424,12 +604,16 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         constexpr int CH = RB / 16;                        // 16-byte chunks a row
         constexpr int RPI = 32 / CH;                       // rows a warp instruction covers
         constexpr int NI = kStrip / RPI;
+        // (computed here again for each half: kept, these would take eight registers)
+        int ln = lane;
+        asm volatile("" : "+r"(ln));
+        const int lr = ln / CH, lc = ln % CH;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           if (NI >= RW ? (i % RW != rw) : (rw >= NI || i != rw)) continue;
-          const int r = i * RPI + (CH < 32 ? lane / CH : 0), c = lane % CH;
+          const int r = i * RPI + lr;
           const long long o = __shfl_sync(0xffffffffu, off, r);
-          cp_async16(st + strip_off<RB>(r, c), base + (o >= 0 ? o + c * 16 : 0), o >= 0 ? 16u : 0u);
+          cp_async16(st + strip_off<RB>(r, lc), base + (o >= 0 ? o + lc * 16 : 0), o >= 0 ? 16u : 0u);
         }
         if (lv) {
           lu += KW;
@@ -473,21 +657,19 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       if constexpr (P::kQRegs) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          // (a column past the last repeats the first: its sums are its own and unused)
           const int gr = row0 + rw * COLS + nb * 8 + r8;
-          const bool in = gr < g.rows;
-          const int tok = in ? gr / a.G : 0, hd = in ? gr - tok * a.G : 0;
+          const int tok = gr < g.rows ? gr / a.G : 0, hd = gr < g.rows ? gr - tok * a.G : 0;
           const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + (I8 ? 4 : 2) * c4;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             if constexpr (I8) {
               const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + ks * 16));
-              qr[ks][nb][0] = in ? v.x : 0u;
-              qr[ks][nb][1] = in ? v.y : 0u;
+              qr[ks][nb][0] = v.x;
+              qr[ks][nb][1] = v.y;
             } else {
-              const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
-              const uint32_t y = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8));
-              qr[ks][nb][0] = in ? x : 0u;
-              qr[ks][nb][1] = in ? y : 0u;
+              qr[ks][nb][0] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
+              qr[ks][nb][1] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8));
             }
           }
         }
@@ -497,8 +679,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         constexpr int WS = NT / ROWS, NW = D / 2 / WS;
         static_assert(D / 2 % WS == 0, "whole words");
         const int col = tid % ROWS, gr = row0 + col;
-        const bool in = gr < g.rows;
-        const int tok = in ? gr / a.G : 0, hd = in ? gr - tok * a.G : 0;
+        const int tok = gr < g.rows ? gr / a.G : 0, hd = gr < g.rows ? gr - tok * a.G : 0;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(
             a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head);
         // fragment place of word w (channels 2 w, 2 w + 1): lane 4 (col % 8) + c, half h
@@ -512,7 +693,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           for (int i = 0; i < 8 && i0 + i < NW; ++i) {
             const int w = tid / ROWS + (i0 + i) * WS, ks = w / 8, j = w % 8;
             const int c = I8 ? j / 2 : j % 4, h = I8 ? j % 2 : j / 4;
-            dst[(ks * 32 + c) * NB * 2 + h] = in ? v[i] : 0u;
+            dst[(ks * 32 + c) * NB * 2 + h] = v[i];
           }
         }
       }
@@ -552,7 +733,6 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll 1
       for (int u = g.u0 + kw; u < g.u1; u += KW) {
         const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
-        const int mi = lane >> 3;
         // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
         constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
         float sp[CN][NB][4] = {};
@@ -562,11 +742,10 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           const uint32_t kst = ring_s + (uint32_t)hb;
           if constexpr (!I8) {
             // A tile: matrices (keys 0-7, 8-15) x (channels 0-7, 8-15) of each 16
-            const int krow = (lane & 7) + (mi & 1) * 8;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               uint32_t kf[4];
-              ldsm4(kf, kst + strip_off<RB>(krow, ks * 2 + (mi >> 1)));
+              ldsm4(kf, kst + koff(ks));
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 uint32_t b0, b1;
@@ -586,11 +765,10 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
             ksc[0] *= sc[r8];
             ksc[1] *= sc[r8 + 8];
             // matrices: (keys 0-7, 8-15) x (channels 0-15, 16-31); a word holds four channels
-            const int krow = (lane & 7) + (mi & 1) * 8;
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) {
               uint32_t kf[4];
-              ldsm4(kf, kst + strip_off<RB>(krow, kk * 2 + (mi >> 1)));
+              ldsm4(kf, kst + koff(kk));
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t u0 = kf[2 * h] ^ 0x80808080u, u1 = kf[2 * h + 1] ^ 0x80808080u;
@@ -706,13 +884,12 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           pf[nb][0] = movm_t(pk[nb][0]);
           pf[nb][1] = movm_t(pk[nb][1]);
         }
-        const int vrow = (lane & 7) + (mi >> 1) * 8;
         if constexpr (!I8) {
           // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + strip_off<RB>(vrow, dt * 2 + (mi & 1)));
+            ldsm4_t(vf, vst + voff(dt));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) mma16816<BF>(acc[dt][nb], vf, pf[nb][0], pf[nb][1]);
           }
@@ -722,7 +899,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + strip_off<RB>(vrow, kk * 2 + (mi & 1)));
+            ldsm4_t(vf, vst + voff(kk));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t u0 = vf[h] ^ 0x80808080u, u1 = vf[2 + h] ^ 0x80808080u;
@@ -827,81 +1004,26 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       if (!cut) continue;
 
       // ---- a cut item: the last CTA to finish it joins the parts, in CTA order
-      __threadfence();
+      // (the barrier and thread 0's release and acquire order every thread's accesses)
       __syncthreads();
       const int n = g.c1 - g.c0 + 1;
       if (tid == 0) {
         const int old = atom_add_acq_rel_gpu(a.counters + g.c0, 1);
-        ctl[6] = old == n - 1;
-        if (old == n - 1) a.counters[g.c0] = 0;          // zero again for the next call
-      }
-      __syncthreads();
-      if (ctl[6] == 0) continue;
-      __threadfence();
-      // the first part is in its CTA's slot 1, the others in their slots 0
-      auto slot = [&](int i) { return a.part + (size_t)(2 * (g.c0 + i) + (i == 0 ? 1 : 0)) * P::kPartFloats; };
-      // `chunk` columns at a time: their parts' m and l in shared memory, then each part's weight
-      const int chunk = min(nrows, P::kRedBytes / 8 / n);
-      float *mm = red, *ll = red + chunk * n;
-      for (int r0 = 0; r0 < nrows; r0 += chunk) {
-        const int nr = min(chunk, nrows - r0);
-        for (int i = tid; i < n * nr; i += NT) {
-          const int k = i / nr, r = i - k * nr;
-          const float *s = slot(k) + r0 + r;
-          mm[k * nr + r] = __ldcg(s);
-          ll[k * nr + r] = __ldcg(s + ROWS);
+        if (old == n - 1) {
+          a.counters[g.c0] = 0;                          // zero again for the next call
+          ctl->join[ctl->njoin++] = g;                   // (a range cuts two items at most)
         }
-        __syncthreads();
-        if (tid < nr) {
-          float Mx = -INFINITY, Ls = 0.0f;
-          for (int k = 0; k < n; ++k) Mx = fmaxf(Mx, mm[k * nr + tid]);
-          for (int k = 0; k < n; ++k) {
-            const float mk = mm[k * nr + tid], w = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
-            Ls += ll[k * nr + tid] * w;
-            mm[k * nr + tid] = w;
-          }
-          const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-          for (int k = 0; k < n; ++k) mm[k * nr + tid] *= inv;
-          const int gr = row0 + r0 + tid;
-          if (a.lse)
-            a.lse[(long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G] =
-                Ls > 0.0f || Ls != Ls ? (Mx + log2f(Ls)) * 0.6931471805599453f : -INFINITY;
-        }
-        __syncthreads();
-        constexpr int NI = 4;                            // results a thread works on at a time
-        for (int i0 = tid; i0 < nr * (D / 4); i0 += NI * NT) {
-          float4 o[NI] = {};
-#pragma unroll 2
-          for (int k = 0; k < n; ++k) {
-            const float *s = slot(k) + 2 * ROWS + (size_t)r0 * D;
-#pragma unroll
-            for (int x = 0; x < NI; ++x) {
-              const int i = i0 + x * NT;
-              if (i < nr * (D / 4)) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(s) + i);
-                const float w = mm[k * nr + i / (D / 4)];
-                o[x].x += v.x * w;
-                o[x].y += v.y * w;
-                o[x].z += v.z * w;
-                o[x].w += v.w * w;
-              }
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < NI; ++x) {
-            const int i = i0 + x * NT;
-            if (i < nr * (D / 4)) {
-              const int gr = row0 + r0 + i / (D / 4);
-              uint16_t *dst = a.out + ((long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G) * D + 4 * (i % (D / 4));
-              *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF>(o[x].x, o[x].y), pack2<BF>(o[x].z, o[x].w));
-            }
-          }
-        }
-        __syncthreads();
       }
     }
     if (!more) break;
+    __syncthreads();
+    if (tid == 0) paged_walk<ROWS, P::kItemCost>(a, segs, ctl);
+    __syncthreads();
+    if (ctl->nseg == 0) break;                             // (only places of no strip were left)
   }
+  // ---- the cut items that this CTA was the last to finish
+  __syncthreads();
+  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB, RW>(a, ctl->join[i], red);
 }
 
 template <int D, int KV, int NB, int RW>
