@@ -89,7 +89,7 @@ struct PagedShape {
   // 2 c and channels r8 of a warp's lanes fall on distinct banks)
   static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
   static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
-  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
+  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
   static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
   static constexpr int kRing = kFit > 8 ? 8 : kFit;    // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
@@ -146,6 +146,9 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t u) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x64646464u), "n"(SEL));
   return h2_as_u32(__hsub2(u32_as_h2(r), u32_as_h2(0x64806480u)));
+}
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 4-byte asynchronous copy (zero-filled when src_bytes is 0)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t src_bytes) {
@@ -221,6 +224,20 @@ struct LaneOffs {
 };
 
 // --------------------------------------------------------------- the schedule --
+// a / b for 0 <= a, 0 < b.  Below 2^22 (every schedule of up to 64 M keys) by a binary32
+// quotient, at most one off, and its remainder: a tenth of the instructions of the general
+// division, which a short call would wait for.
+static __device__ __noinline__ long long paged_div64(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 22) != 0ull) return paged_div64(a, b);
+  const int x = (int)a, y = (int)b;
+  int q = (int)__fdividef((float)x, (float)y);
+  const int r = x - q * y;
+  q += r >= y;
+  q -= r < 0;
+  return q;
+}
+
 // Sequence b's new tokens and keys, clamped to what the buffers hold (a length beyond the
 // page table or offsets out of order record QW_ERR_BAD_INDEX).
 struct PagedSeq {
@@ -243,7 +260,7 @@ template <int ROWS>
 __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedSeq &s, int rb) {
   PagedSpan p;
   const int rows = s.nq * a.G, pos0 = s.len - s.nq;
-  const int t0 = rb * ROWS / a.G, t1 = (min(rows, rb * ROWS + ROWS) - 1) / a.G;
+  const int t0 = (int)paged_div(rb * ROWS, a.G), t1 = (int)paged_div(min(rows, rb * ROWS + ROWS) - 1, a.G);
   p.hi = max(pos0 + t1 + 1, 0);
   p.lo = a.window > 0 ? max(pos0 + t0 - a.window + 1, 0) : 0;
   p.first = p.lo / kStrip;
@@ -266,11 +283,6 @@ __device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const
   g.tok0 = s.tok0;
 }
 
-// a / b (a >= 0, b > 0), in 32 bits where both fit
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-  if (((unsigned long long)(a | b) >> 32) == 0ull) return (unsigned)a / (unsigned)b;
-  return a / b;
-}
 
 // One segment: the strips of the item that starts at place `at` which lie in the range.
 template <int IC>
@@ -289,12 +301,14 @@ __device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, P
   int n = 0, b = ctl->b;
   long long off = ctl->off, pos = ctl->pos;
   const long long end = ctl->end;
+#pragma unroll 1
   while (pos < end && n < kPagedMaxSegs) {
     const PagedSeq s = paged_seq(a, b);
     const int nrb = (s.nq * a.G + ROWS - 1) / ROWS;
     long long o = off;
     int rb = 0;
     PagedSpan p{};
+#pragma unroll 1
     for (; rb < nrb; ++rb) {
       p = paged_span<ROWS>(a, s, rb);
       if (o < (long long)(p.n + IC) * a.Hkv) break;
@@ -333,12 +347,14 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
   auto blocks = [&](const PagedSeq &s) { return (s.nq * a.G + ROWS - 1) / ROWS; };
   auto cost = [&](const PagedSeq &s) {
     long long c = 0;
+#pragma unroll 1
     for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_span<ROWS>(a, s, rb).n + IC;
     return c * a.Hkv;
   };
   PagedSeq own{};                                       // per == 1: this thread's sequence
   long long mine = 0;
   int items = 0;
+#pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
     own = paged_seq(a, b);
     mine += cost(own);
@@ -380,7 +396,8 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
   if (size > 0 && size <= share + 2 * IC) {
     const int sz = (int)min(size, 1ll << 30);
     int parts = 0, pp = 0;
-    for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += (paged_span<ROWS>(a, own, rb).n + sz - 1) / sz * a.Hkv;
+#pragma unroll 1
+    for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += (int)paged_div(paged_span<ROWS>(a, own, rb).n + sz - 1, sz) * a.Hkv;
     int inc = parts;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -394,12 +411,13 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     pp += inc - parts;
     if (me >= pp && me < pp + parts) {                  // one thread, if any
       int at = pp;
+#pragma unroll 1
       for (int rb = 0, n = blocks(own); rb < n; ++rb) {
         const PagedSpan p = paged_span<ROWS>(a, own, rb);
-        const int np = (p.n + sz - 1) / sz;
+        const int np = (int)paged_div(p.n + sz - 1, sz);
         if (me < at + np * a.Hkv) {
           PagedSeg &g = segs[0];
-          const int head = (me - at) / np, j = me - at - head * np, len = (p.n + np - 1) / np;
+          const int head = (int)paged_div(me - at, np), j = me - at - head * np, len = (int)paged_div(p.n + np - 1, np);
           g.u0 = j * len;
           g.u1 = min(p.n, g.u0 + len);
           g.c0 = me - j;
@@ -421,11 +439,13 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
   if (pre < end && begin < pre + mine) {
     long long at = pre;
     if (per == 1)
+#pragma unroll 1
       for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
         const PagedSpan p = paged_span<ROWS>(a, own, rb);
         const int each = p.n + IC;
         int head = begin > at ? (int)min(paged_div(begin - at, each), (long long)a.Hkv) : 0;
         long long x = at + (long long)head * each;
+#pragma unroll 1
         for (; head < a.Hkv && x + IC < end; ++head, x += each)
           if (x + each > begin) {
             const int i = atomicAdd(&ctl->nseg, 1);
@@ -436,6 +456,7 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     if (begin >= pre) {                                 // the owner of the range's first place
       long long off = begin - pre;
       int b = b_lo;
+#pragma unroll 1
       for (; b + 1 < b_hi; ++b) {
         const long long c = cost(paged_seq(a, b));
         if (off < c) break;
@@ -449,12 +470,14 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     }
   }
   __syncthreads();
-  if (per > 1 || ctl->nseg > kPagedMaxSegs) {
-    __syncthreads();
-    if (tid == 0) paged_walk<ROWS, IC>(a, segs, ctl);
-    __syncthreads();
+  if (per == 1 && ctl->nseg <= kPagedMaxSegs) return ctl->nseg != 0;
+  __syncthreads();
+  if (tid == 0) {
+    ctl->nseg = 0;                                      // nothing listed yet
+    ctl->more = 1;
   }
-  return ctl->nseg != 0;
+  __syncthreads();
+  return true;
 }
 
 // Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
@@ -470,8 +493,10 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
   // `chunk` columns at a time: their parts' m and l in shared memory, then each part's weight
   const int chunk = min(nrows, P::kRedBytes / 8 / n);
   float *mm = red, *ll = red + chunk * n;
+#pragma unroll 1
   for (int r0 = 0; r0 < nrows; r0 += chunk) {
     const int nr = min(chunk, nrows - r0);
+#pragma unroll 1
     for (int i = tid; i < n * nr; i += NT) {
       const int k = i / nr, r = i - k * nr;
       const float *s = slot(k) + r0 + r;
@@ -480,14 +505,17 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
     }
     __syncthreads();
     // eight lanes a column
+#pragma unroll 1
     for (int r = tid >> 3; r < (nr + 3) / 4 * 4; r += NT / 8) {       // whole warps
       const int e = lane & 7;
       float Mx = -INFINITY, Ls = 0.0f;
       if (r < nr)
+#pragma unroll 1
         for (int k = e; k < n; k += 8) Mx = fmaxf(Mx, mm[k * nr + r]);
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
       if (r < nr)
+#pragma unroll 1
         for (int k = e; k < n; k += 8) {
           const float mk = mm[k * nr + r], w = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
           Ls += ll[k * nr + r] * w;
@@ -497,6 +525,7 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
       for (int o = 1; o < 8; o <<= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
       const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
       if (r < nr)
+#pragma unroll 1
         for (int k = e; k < n; k += 8) mm[k * nr + r] *= inv;
       if (a.lse && r < nr && e == 0) {
         const int gr = row0 + r0 + r;
@@ -505,9 +534,11 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
       }
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < nr * (D / 4); i += NT) {
       const int r = i / (D / 4);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
       for (int k0 = 0; k0 < n; k0 += 8) {            // eight parts in flight
         float4 v[8];
 #pragma unroll
@@ -546,7 +577,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   float *red = reinterpret_cast<float *>(fixed + P::kQBytes);         // [KW][RW][COLS][SW + 4]
   float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
   float *sm_l = sm_m + P::kWarps * COLS;
-  PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_l + P::kWarps * COLS);
+  long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * COLS);   // [ROWS]
+  PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_row + ROWS);
   PagedCtl *ctl = reinterpret_cast<PagedCtl *>(segs + kPagedMaxSegs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -566,6 +598,12 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 
   float acc[D / 16][NB][4];
   for (;;) {
+    if (ctl->nseg == 0) {                                // the whole CTA
+      __syncthreads();
+      if (tid == 0) paged_walk<ROWS, P::kItemCost>(a, segs, ctl);
+      __syncthreads();
+      if (ctl->nseg == 0) break;                         // (only places of no strip were left)
+    }
     const int nseg = ctl->nseg;
     const bool more = ctl->more != 0;
 
@@ -575,9 +613,10 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     bool lv = false;
     while (ls < nseg && lu >= segs[ls].u1)
       if (++ls < nseg) lu = segs[ls].u0 + kw;
-    // of the strip being loaded: this lane's row offset (lane & 15; -1: not read) and scale
-    long long off = -1;
-    long long soff = -1;
+    // Of the strip being loaded: byte offset of row lane & 15 (-1: not read) and, int8, of its
+    // scale; the rows that are read; whether the strip lies in one page and is read whole.
+    long long off = -1, soff = -1;
+    bool plain = false;
     auto load_next = [&]() {
       if (ls < nseg) {
         const PagedSeg &g = segs[ls];
@@ -587,7 +626,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           const int key = unit * kStrip + (lane & 15);
           off = soff = -1;
           if (key < g.hi && (key >= g.lo || key < a.sinks)) {
-            const int pi = key / a.page, po = key - pi * a.page;
+            const int pi = (int)paged_div(key, a.page), po = key - pi * a.page;
             const int pid = __ldg(a.table + (size_t)g.b * a.max_pages + pi);
             if ((unsigned)pid < (unsigned)a.npages) {
               off = (pid * a.page_stride + g.g * a.head_stride + po * a.tok_stride) * P::kES;
@@ -596,6 +635,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
               atomicCAS(a.err, 0, -9);
             }
           }
+          plain = a.strip_pages && __all_sync(0xffffffffu, off >= 0);
         }
         const uint8_t *base = lv ? a.v : a.k;
         if constexpr (I8)
@@ -608,15 +648,26 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         int ln = lane;
         asm volatile("" : "+r"(ln));
         const int lr = ln / CH, lc = ln % CH;
+        if (plain) {                                       // rows at equal distances
+          const long long o0 = __shfl_sync(0xffffffffu, off, 0);
+          const long long step = RPI * a.tok_stride * P::kES;
+          const uint8_t *src = base + o0 + lr * a.tok_stride * P::kES + lc * 16;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (NI >= RW ? (i % RW != rw) : (rw >= NI || i != rw)) continue;
-          const int r = i * RPI + lr;
-          const long long o = __shfl_sync(0xffffffffu, off, r);
-          cp_async16(st + strip_off<RB>(r, lc), base + (o >= 0 ? o + lc * 16 : 0), o >= 0 ? 16u : 0u);
+          for (int i = 0; i < NI; ++i) {
+            if (NI >= RW ? (i % RW == rw) : (i == rw)) cp_async16_full(st + strip_off<RB>(i * RPI + lr, lc), src);
+            src += step;
+          }
+        } else {
+#pragma unroll 1
+          for (int i = rw; i < NI; i += RW) {
+            const int r = i * RPI + lr;
+            const long long o = __shfl_sync(0xffffffffu, off, r);
+            cp_async16(st + strip_off<RB>(r, lc), base + (o >= 0 ? o + lc * 16 : 0), o >= 0 ? 16u : 0u);
+          }
         }
         if (lv) {
           lu += KW;
+#pragma unroll 1
           while (ls < nseg && lu >= segs[ls].u1)
             if (++ls < nseg) lu = segs[ls].u0 + kw;
         }
@@ -868,15 +919,12 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           }
         }
         // ---- O^T += V^T P^T
+        bool odd = false;
         if constexpr (!I8) {
           // columns at several positions: a key hidden from some has weight 0 there, and 0
           // times an infinite or NaN value would reach them through the MMA.  Strips that
           // hold such a value are summed without the hidden products.
-          if (masked && pmin != pmax && strip_nonfinite<D, BF>(vst, lane)) {
-            add_visible<D, NB, BF>(acc, pk, s, vst, lane);
-            release();
-            continue;
-          }
+          odd = masked && pmin != pmax && strip_nonfinite<D, BF>(vst, lane);
         }
         uint32_t pf[NB][2];
 #pragma unroll
@@ -884,7 +932,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           pf[nb][0] = movm_t(pk[nb][0]);
           pf[nb][1] = movm_t(pk[nb][1]);
         }
-        if constexpr (!I8) {
+        if (!I8 && odd) {
+          if constexpr (!I8) add_visible<D, NB, BF>(acc, pk, s, vst, lane);
+        } else if constexpr (!I8) {
           // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
@@ -940,9 +990,12 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       const bool cut = g.c0 != g.c1;
       float *part = a.part + (size_t)(2 * blockIdx.x + (g.c0 == (int)blockIdx.x ? 1 : 0)) * P::kPartFloats;
       const int nrows = min(ROWS, g.rows - row0);
-      // column sums: M and L of each column (thread r)
+      // column sums: M and L of each column (thread r), and its row of out
       float M = -INFINITY, L = 0.0f;
       if (tid < nrows) {
+        const int tok = (row0 + tid) / a.G;
+        const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.g * a.G + row0 + tid - tok * a.G;
+        sm_row[tid] = orow;
         for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
         for (int w = 0; w < KW; ++w) {
           const float mw = sm_m[w * ROWS + tid];
@@ -952,8 +1005,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           part[tid] = M;
           part[ROWS + tid] = L;
         } else if (a.lse) {
-          const int gr = row0 + tid;
-          a.lse[(long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G] = L > 0.0f || L != L ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          a.lse[orow] = L > 0.0f || L != L ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
         }
       }
       __syncthreads();
@@ -980,6 +1032,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
             }
           }
         __syncthreads();
+#pragma unroll 1
         for (int i = tid; i < nrows * (SW / 2); i += NT) {
           const int r = i / (SW / 2), cp = i % (SW / 2);
           float2 o = make_float2(0.0f, 0.0f);
@@ -994,9 +1047,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
             *reinterpret_cast<float2 *>(part + 2 * ROWS + (size_t)r * D + col) = o;
           } else {
             const float inv = sm_l[r];
-            const int gr = row0 + r;
-            uint16_t *dst = a.out + ((long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G) * D + col;
-            *reinterpret_cast<uint32_t *>(dst) = pack2<BF>(o.x * inv, o.y * inv);
+            *reinterpret_cast<uint32_t *>(a.out + sm_row[r] * D + col) = pack2<BF>(o.x * inv, o.y * inv);
           }
         }
         __syncthreads();
@@ -1017,9 +1068,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     }
     if (!more) break;
     __syncthreads();
-    if (tid == 0) paged_walk<ROWS, P::kItemCost>(a, segs, ctl);
+    if (tid == 0) ctl->nseg = 0;
     __syncthreads();
-    if (ctl->nseg == 0) break;                             // (only places of no strip were left)
   }
   // ---- the cut items that this CTA was the last to finish
   __syncthreads();

@@ -408,6 +408,7 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.cap = b->max_pages * c->page;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
+  a.strip_pages = c->page % 16 == 0;
   a.min_strips = 12;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.counters = static_cast<int *>(ws);
