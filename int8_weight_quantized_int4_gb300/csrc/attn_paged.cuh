@@ -64,8 +64,8 @@ struct PagedCtl {
   int njoin;                    // cut items this CTA was the last to finish
   PagedSeg join[2];
   int b;                        // walk: sequence
-  long long off, pos;           // walk: place in the sequence, in all
-  long long begin, end, share;  // the range
+  int off, pos;                 // walk: place in the sequence, in all
+  int begin, end, share;        // the range
   int part[16];
 };
 
@@ -224,16 +224,13 @@ struct LaneOffs {
 };
 
 // --------------------------------------------------------------- the schedule --
-// a / b for 0 <= a, 0 < b.  Below 2^22 (every schedule of up to 64 M keys) by a binary32
-// quotient, at most one off, and its remainder: a tenth of the instructions of the general
-// division, which a short call would wait for.
-static __device__ __noinline__ long long paged_div64(long long a, long long b) { return a / b; }
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-  if (((unsigned long long)(a | b) >> 22) != 0ull) return paged_div64(a, b);
-  const int x = (int)a, y = (int)b;
-  int q = (int)__fdividef((float)x, (float)y);
-  const int r = x - q * y;
-  q += r >= y;
+// a / b for 0 <= a, 0 < b.  Below 2^22 by a binary32 quotient, at most one off, and its
+// remainder: a fraction of the general division's latency, which a short call waits for.
+__device__ __forceinline__ int paged_div(int a, int b) {
+  if ((unsigned)(a | b) >> 22) return (int)((unsigned)a / (unsigned)b);
+  int q = (int)__fdividef((float)a, (float)b);
+  const int r = a - q * b;
+  q += r >= b;
   q -= r < 0;
   return q;
 }
@@ -260,7 +257,7 @@ template <int ROWS>
 __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedSeq &s, int rb) {
   PagedSpan p;
   const int rows = s.nq * a.G, pos0 = s.len - s.nq;
-  const int t0 = (int)paged_div(rb * ROWS, a.G), t1 = (int)paged_div(min(rows, rb * ROWS + ROWS) - 1, a.G);
+  const int t0 = paged_div(rb * ROWS, a.G), t1 = paged_div(min(rows, rb * ROWS + ROWS) - 1, a.G);
   p.hi = max(pos0 + t1 + 1, 0);
   p.lo = a.window > 0 ? max(pos0 + t0 - a.window + 1, 0) : 0;
   p.first = p.lo / kStrip;
@@ -284,47 +281,52 @@ __device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const
 }
 
 
+// Places are counted in 2^shift strips (shift is 0 unless all keys of a call could pass 2^30
+// places): an item takes IC of them and paged_places(n) for its n strips.
+__device__ __forceinline__ int paged_places(const PagedArgs &a, int n) { return (n + (1 << a.shift) - 1) >> a.shift; }
+
 // One segment: the strips of the item that starts at place `at` which lie in the range.
 template <int IC>
-__device__ __forceinline__ void paged_emit(PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head,
-                                           long long at, long long begin, long long end, long long share, int G) {
-  g.u0 = (int)max(begin - at - IC, 0ll);
-  g.u1 = (int)min(end - at - IC, (long long)p.n);
-  g.c0 = g.u0 == 0 ? (int)blockIdx.x : (int)paged_div(at + IC, share);
-  g.c1 = g.u1 == p.n ? (int)blockIdx.x : (int)paged_div(at + IC + p.n - 1, share);
-  paged_fill(g, s, p, b, rb, head, G);
+__device__ __forceinline__ void paged_emit(const PagedArgs &a, PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b,
+                                           int rb, int head, int at, int begin, int end, int share) {
+  const int n = paged_places(a, p.n), u0 = max(begin - at - IC, 0), u1 = min(end - at - IC, n);
+  g.u0 = u0 << a.shift;
+  g.u1 = u1 == n ? p.n : u1 << a.shift;
+  g.c0 = u0 == 0 ? (int)blockIdx.x : paged_div(at + IC, share);
+  g.c1 = u1 == n ? (int)blockIdx.x : paged_div(at + IC + n - 1, share);
+  paged_fill(g, s, p, b, rb, head, a.G);
 }
 
 // Lists the range's next segments (one thread).
 template <int ROWS, int IC>
 __device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, PagedCtl *ctl) {
-  int n = 0, b = ctl->b;
-  long long off = ctl->off, pos = ctl->pos;
-  const long long end = ctl->end;
+  int n = 0, b = ctl->b, off = ctl->off, pos = ctl->pos;
+  const int end = ctl->end;
 #pragma unroll 1
   while (pos < end && n < kPagedMaxSegs) {
     const PagedSeq s = paged_seq(a, b);
     const int nrb = (s.nq * a.G + ROWS - 1) / ROWS;
-    long long o = off;
-    int rb = 0;
+    int o = off, rb = 0, each = 1;
     PagedSpan p{};
 #pragma unroll 1
     for (; rb < nrb; ++rb) {
       p = paged_span<ROWS>(a, s, rb);
-      if (o < (long long)(p.n + IC) * a.Hkv) break;
-      o -= (long long)(p.n + IC) * a.Hkv;
+      each = paged_places(a, p.n) + IC;
+      if (o < each * a.Hkv) break;
+      o -= each * a.Hkv;
     }
     if (rb == nrb) {
       ++b;
       off = 0;
       continue;
     }
-    const int head = (int)paged_div(o, p.n + IC), in = (int)(o - (long long)head * (p.n + IC));
-    PagedSeg &g = segs[n];
-    paged_emit<IC>(g, s, p, b, rb, head, pos - in, ctl->begin, end, ctl->share, a.G);
-    if (g.u0 < g.u1) ++n;                               // (a range may end among an item's first places)
-    pos += p.n + IC - in;
-    off += p.n + IC - in;
+    const int head = paged_div(o, each), in = o - head * each;
+    if (pos - in + IC < end) {                          // (a range may end among an item's first places)
+      paged_emit<IC>(a, segs[n], s, p, b, rb, head, pos - in, ctl->begin, end, ctl->share);
+      ++n;
+    }
+    pos += each - in;
+    off += each - in;
   }
   ctl->nseg = n;
   ctl->more = pos < end;
@@ -333,151 +335,144 @@ __device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, P
   ctl->pos = pos;
 }
 
-// This CTA's work: its first segments and the state to list the others; false: none.  Every
-// item takes IC places and one for each strip; the places of all items, in order, are cut into
-// equal ranges -- or, where that costs little more than the equal share (`whole`), each item
-// gets CTAs of its own: no CTA then finishes two items one after the other, which is what a
-// short call would wait for.
+// This CTA's work: its first segments and the state to list the others; false: none.  The
+// places of all items, in order, are cut into equal ranges -- or, where that costs little more
+// than the equal share, each item gets CTAs of its own: no CTA then finishes two items one
+// after the other, which is what a short call would wait for.  Up to 32 sequences one warp
+// does it, a sequence a lane; otherwise the CTA, one or more sequences a thread.
 template <int ROWS, int IC, int NW>
-__device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *segs, PagedCtl *ctl, float *scratch) {
+__device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *segs, PagedCtl *ctl) {
   constexpr int NT = 32 * NW;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per = (a.B + NT - 1) / NT;
-  const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
-  auto blocks = [&](const PagedSeq &s) { return (s.nq * a.G + ROWS - 1) / ROWS; };
-  auto cost = [&](const PagedSeq &s) {
-    long long c = 0;
-#pragma unroll 1
-    for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_span<ROWS>(a, s, rb).n + IC;
-    return c * a.Hkv;
-  };
-  PagedSeq own{};                                       // per == 1: this thread's sequence
-  long long mine = 0;
-  int items = 0;
-#pragma unroll 1
-  for (int b = b_lo; b < b_hi; ++b) {
-    own = paged_seq(a, b);
-    mine += cost(own);
-    items = min(items + blocks(own) * a.Hkv, 1 << 20);
-  }
   if (tid == 0) {
-    ctl->nseg = 0;
-    ctl->more = 0;
-    ctl->njoin = 0;
+    ctl->nseg = ctl->more = ctl->njoin = 0;
   }
-  long long total = 0, pre = 0;
-  {
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    items = __reduce_add_sync(0xffffffffu, items);
-    longlong2 *ws = reinterpret_cast<longlong2 *>(scratch);
-    if (lane == 31) ws[warp] = make_longlong2(inc, items);
-    __syncthreads();
-    items = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const longlong2 v = ws[w];
-      if (w < warp) pre += v.x;
-      total += v.x;
-      items += (int)v.y;
-    }
-    pre += inc - mine;
-  }
-  const int grid = gridDim.x, me = blockIdx.x;
-  const long long share = max(paged_div(total + grid - 1, grid), (long long)a.min_strips);
-  // strips a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
-  long long size = 0;
-  if (per == 1 && items < grid)
-    size = max(paged_div(total - (long long)IC * items + grid - items - 1, grid - items), (long long)a.min_strips);
-  if (size > 0 && size <= share + 2 * IC) {
-    const int sz = (int)min(size, 1ll << 30);
-    int parts = 0, pp = 0;
+  if (a.B > 32 || warp == 0) {
+    const int per = a.B > 32 ? (a.B + NT - 1) / NT : 1;
+    const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
+    auto blocks = [&](const PagedSeq &s) { return (s.nq * a.G + ROWS - 1) / ROWS; };
+    auto cost = [&](const PagedSeq &s) {
+      int c = 0;
 #pragma unroll 1
-    for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += (int)paged_div(paged_span<ROWS>(a, own, rb).n + sz - 1, sz) * a.Hkv;
-    int inc = parts;
+      for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_places(a, paged_span<ROWS>(a, s, rb).n) + IC;
+      return c * a.Hkv;
+    };
+    // sums before this thread and over all (of the warp, or through shared memory)
+    auto scan = [&](int v, int &before, int &all) {
+      int inc = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) ctl->part[warp] = inc;
-    __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      before = inc - v;
+      all = __shfl_sync(0xffffffffu, inc, 31);
+      if (a.B > 32) {
+        __syncthreads();
+        if (lane == 0) ctl->part[warp] = all;
+        __syncthreads();
+        all = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) pp += w < warp ? ctl->part[w] : 0;
-    pp += inc - parts;
-    if (me >= pp && me < pp + parts) {                  // one thread, if any
-      int at = pp;
-#pragma unroll 1
-      for (int rb = 0, n = blocks(own); rb < n; ++rb) {
-        const PagedSpan p = paged_span<ROWS>(a, own, rb);
-        const int np = (int)paged_div(p.n + sz - 1, sz);
-        if (me < at + np * a.Hkv) {
-          PagedSeg &g = segs[0];
-          const int head = (int)paged_div(me - at, np), j = me - at - head * np, len = (int)paged_div(p.n + np - 1, np);
-          g.u0 = j * len;
-          g.u1 = min(p.n, g.u0 + len);
-          g.c0 = me - j;
-          g.c1 = g.c0 + np - 1;
-          paged_fill(g, own, p, b_lo, rb, head, a.G);
-          ctl->nseg = 1;
-          break;
+        for (int w = 0; w < NW; ++w) {
+          const int x = ctl->part[w];
+          before += w < warp ? x : 0;
+          all += x;
         }
-        at += np * a.Hkv;
       }
+    };
+    PagedSeq own{};                                     // per == 1: this thread's sequence
+    int mine = 0, items = 0;
+#pragma unroll 1
+    for (int b = b_lo; b < b_hi; ++b) {
+      own = paged_seq(a, b);
+      mine += cost(own);
+      items += blocks(own) * a.Hkv;
+    }
+    int pre, total, dummy, all_items;
+    scan(mine, pre, total);
+    scan(min(items, 1 << 16), dummy, all_items);
+    const int grid = gridDim.x, me = blockIdx.x;
+    const int share = max(paged_div(total + grid - 1, grid), a.min_places);
+    // strips a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
+    const int left = grid - all_items;
+    const int size = per == 1 && left > 0 && a.shift == 0 ? max(paged_div(total - IC * all_items + left - 1, left), a.min_places) : 0;
+    if (size > 0 && size <= share + 2 * IC) {
+      int parts = 0, pp;
+#pragma unroll 1
+      for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += paged_div(paged_span<ROWS>(a, own, rb).n + size - 1, size) * a.Hkv;
+      scan(parts, pp, dummy);
+      if (me >= pp && me < pp + parts) {                // one thread, if any
+        int at = pp;
+#pragma unroll 1
+        for (int rb = 0, n = blocks(own); rb < n; ++rb) {
+          const PagedSpan p = paged_span<ROWS>(a, own, rb);
+          const int np = paged_div(p.n + size - 1, size);
+          if (me < at + np * a.Hkv) {
+            PagedSeg &g = segs[0];
+            const int head = paged_div(me - at, np), j = me - at - head * np, len = paged_div(p.n + np - 1, np);
+            g.u0 = j * len;
+            g.u1 = min(p.n, g.u0 + len);
+            g.c0 = me - j;
+            g.c1 = g.c0 + np - 1;
+            paged_fill(g, own, p, b_lo, rb, head, a.G);
+            ctl->nseg = 1;
+            break;
+          }
+          at += np * a.Hkv;
+        }
+      }
+    } else {
+      const int begin = (int)min((long long)share * me, (long long)total), end = min(total - begin, share) + begin;
+      // Up to a sequence a thread and kPagedMaxSegs segments: every thread lists its own
+      // sequence's (in any order); otherwise thread 0 walks, a list at a time.
+      if (begin < end && pre < end && begin < pre + mine) {
+        int at = pre;
+        if (per == 1) {
+#pragma unroll 1
+          for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
+            const PagedSpan p = paged_span<ROWS>(a, own, rb);
+            const int each = paged_places(a, p.n) + IC;
+            int head = begin > at ? min(paged_div(begin - at, each), a.Hkv) : 0;
+            int x = at + head * each;
+#pragma unroll 1
+            for (; head < a.Hkv && x + IC < end; ++head, x += each)
+              if (x + each > begin) {
+                const int i = atomicAdd(&ctl->nseg, 1);
+                if (i < kPagedMaxSegs) paged_emit<IC>(a, segs[i], own, p, b_lo, rb, head, x, begin, end, share);
+              }
+            at += a.Hkv * each;
+          }
+        }
+        if (begin >= pre) {                             // the owner of the range's first place
+          int off = begin - pre, b = b_lo;
+          if (per > 1) {
+#pragma unroll 1
+            for (; b + 1 < b_hi; ++b) {
+              const int c = cost(paged_seq(a, b));
+              if (off < c) break;
+              off -= c;
+            }
+            ctl->more = 1;
+          }
+          ctl->b = b;
+          ctl->off = off;
+          ctl->pos = ctl->begin = begin;
+          ctl->end = end;
+          ctl->share = share;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (ctl->nseg > kPagedMaxSegs) {                      // too many: walk instead
+    __syncthreads();
+    if (tid == 0) {
+      ctl->nseg = 0;
+      ctl->more = 1;
     }
     __syncthreads();
-    return ctl->nseg != 0;
   }
-  const long long begin = share * me, end = min(total, begin + share);
-  if (begin >= end) return false;
-  // Up to a sequence a thread and kPagedMaxSegs segments: every thread lists its own
-  // sequence's (in any order); otherwise thread 0 walks, a list at a time.
-  if (pre < end && begin < pre + mine) {
-    long long at = pre;
-    if (per == 1)
-#pragma unroll 1
-      for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
-        const PagedSpan p = paged_span<ROWS>(a, own, rb);
-        const int each = p.n + IC;
-        int head = begin > at ? (int)min(paged_div(begin - at, each), (long long)a.Hkv) : 0;
-        long long x = at + (long long)head * each;
-#pragma unroll 1
-        for (; head < a.Hkv && x + IC < end; ++head, x += each)
-          if (x + each > begin) {
-            const int i = atomicAdd(&ctl->nseg, 1);
-            if (i < kPagedMaxSegs) paged_emit<IC>(segs[i], own, p, b_lo, rb, head, x, begin, end, share, a.G);
-          }
-        at += (long long)a.Hkv * each;
-      }
-    if (begin >= pre) {                                 // the owner of the range's first place
-      long long off = begin - pre;
-      int b = b_lo;
-#pragma unroll 1
-      for (; b + 1 < b_hi; ++b) {
-        const long long c = cost(paged_seq(a, b));
-        if (off < c) break;
-        off -= c;
-      }
-      ctl->b = b;
-      ctl->off = off;
-      ctl->pos = ctl->begin = begin;
-      ctl->end = end;
-      ctl->share = share;
-    }
-  }
-  __syncthreads();
-  if (per == 1 && ctl->nseg <= kPagedMaxSegs) return ctl->nseg != 0;
-  __syncthreads();
-  if (tid == 0) {
-    ctl->nseg = 0;                                      // nothing listed yet
-    ctl->more = 1;
-  }
-  __syncthreads();
-  return true;
+  return ctl->nseg != 0 || ctl->more != 0;
 }
 
 // Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
@@ -594,7 +589,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  if (!paged_schedule<ROWS, P::kItemCost, P::kWarps>(a, segs, ctl, red)) return;       // whole CTA
+  if (!paged_schedule<ROWS, P::kItemCost, P::kWarps>(a, segs, ctl)) return;       // whole CTA
 
   float acc[D / 16][NB][4];
   for (;;) {
@@ -626,7 +621,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           const int key = unit * kStrip + (lane & 15);
           off = soff = -1;
           if (key < g.hi && (key >= g.lo || key < a.sinks)) {
-            const int pi = (int)paged_div(key, a.page), po = key - pi * a.page;
+            const int pi = paged_div(key, a.page), po = key - pi * a.page;
             const int pid = __ldg(a.table + (size_t)g.b * a.max_pages + pi);
             if ((unsigned)pid < (unsigned)a.npages) {
               off = (pid * a.page_stride + g.g * a.head_stride + po * a.tok_stride) * P::kES;

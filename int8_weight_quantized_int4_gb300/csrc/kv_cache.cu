@@ -409,7 +409,15 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
   a.strip_pages = c->page % 16 == 0;
-  a.min_strips = 12;
+  // every sequence's column blocks and their strips, were all contexts as long as the page
+  // table; up to 41 places more an item, and counts to spare
+  long long most = ((long long)T * a.G / cols + b->B) * c->Hkv;
+  if (most > (1ll << 28)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
+  const long long blocks = most;
+  for (most = blocks * (a.cap / 16 + 64); most > (1ll << 30); most = blocks * ((a.cap / 16 >> a.shift) + 64)) {
+    if (++a.shift > 24) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
+  }
+  a.min_places = 12;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.counters = static_cast<int *>(ws);
   a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kPagedCounterBytes);

@@ -119,7 +119,8 @@ struct PagedArgs {
   int cap;                      // keys the page table can name: max_pages * page
   int window, sinks;            // window 0: every key up to the position; sinks 0 without one
   int strip_pages;              // page % 16 == 0: a strip of 16 keys lies in one page
-  int min_strips;               // fewest strips of 16 keys a CTA takes
+  int shift;                    // the schedule counts keys in 2^shift strips of 16
+  int min_places;               // fewest of them a CTA takes
   float scale_log2;             // softmax scale * log2(e)
   float *part;                  // [2 CTAs][rows (d + 2)] partial sums (workspace)
   int *counters;                // [CTAs] arrivals, zero between calls (workspace)
