@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -481,80 +482,119 @@ def topk_logits(logits, k: int):
 
 
 # ------------------------------------------------------------ paged cache --
+# These calls run once a layer and token, so their marshalling is kept short: device indices
+# instead of device objects, descriptors packed by struct (native layout, as the C structs),
+# the raw handle of the current stream.
 _KV_TYPES = {torch.float16: QW_KV_F16, torch.bfloat16: QW_KV_BF16, torch.int8: QW_KV_INT8}
+_ACT_TYPES = (torch.float16, torch.bfloat16, torch.float16)       # by cache type
+_pack_cache = struct.Struct("@PPPPiiiiiqqq").pack
+_pack_batch = struct.Struct("@PPPii").pack
+_pack_pool = struct.Struct("@Piiqqq").pack
+assert struct.calcsize("@PPPPiiiiiqqq") == ctypes.sizeof(KvCacheDesc)
+assert struct.calcsize("@PPPii0q") == ctypes.sizeof(KvBatchDesc)
+assert struct.calcsize("@Piiqqq") == ctypes.sizeof(PagePoolDesc)
+_i32, _f32 = torch.int32, torch.float32
 
 
-def _launch(dev, fn, *args):
-    """fn(*args, stream) on the current stream of `dev`, with `dev` current."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_step = {}
+
+
+def _step_fn(name):
+    """The entry point with its descriptors taken as packed bytes."""
+    fn = _step.get(name)
+    if fn is None:
+        lib()
+        fn = getattr(ctypes.CDLL(LIB_PATH), name)
+        fn.restype, args = SIGNATURES[name]
+        fn.argtypes = [ctypes.c_char_p if isinstance(x, type) and issubclass(x, ctypes._Pointer) else x for x in args]
+        _step[name] = fn
+    return fn
+
+
+def _run(index, fn, *args):
+    """fn(*args) with device `index` current; raises on an error code."""
+    if index == _current_device():
+        rc = fn(*args)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc:
+        _check(rc)
 
 
-def _scratch(ws, dev, kind, query, *args):
-    """(buffer, bytes) of `ws`, or of the default workspace of this kind of call and stream."""
+def _scratch(ws, index, stream, kind, query, *args):
+    """(pointer, bytes) of `ws`, or of the default workspace of this kind of call and stream."""
     if ws is None:
-        key = (dev, torch.cuda.current_stream(dev).cuda_stream, kind)
-        ws = _default_ws.get(key)
+        ws = _default_ws.get((index, stream, kind))
         if ws is None:
-            ws = _default_ws.setdefault(key, Workspace(dev))
-    if dev.index == torch.cuda.current_device():
-        need = int(query(*args))
+            ws = _default_ws.setdefault((index, stream, kind), Workspace(torch.device("cuda", index)))
+    if index == _current_device():
+        need = query(*args)
     else:
-        with torch.cuda.device(dev):
-            need = int(query(*args))
-    return ws.get_bytes(need)
+        with torch.cuda.device(index):
+            need = query(*args)
+    buf, nbytes = ws.get_bytes(need)
+    return (None if buf is None else buf.data_ptr()), nbytes
 
 
-def _kv_cache(k_pages, v_pages, k_scale, v_scale):
-    """The descriptor of one layer's cache (k_pages, v_pages [pages, Hkv, page, d])."""
+def _kv_cache(k_pages, v_pages, k_scale, v_scale, index):
+    """(packed descriptor, cache type, Hkv, d) of one layer's cache, [pages, Hkv, page, d]."""
     dtype = _KV_TYPES.get(k_pages.dtype)
-    if dtype is None or v_pages.dtype != k_pages.dtype:
+    if dtype is None or v_pages.dtype is not k_pages.dtype:
         raise TypeError("k_pages and v_pages must both be float16, bfloat16 or int8")
-    if not (k_pages.is_cuda and v_pages.device == k_pages.device):
+    if index < 0 or v_pages.get_device() != index:
         raise TypeError("k_pages and v_pages must be CUDA tensors on one device")
     shape, stride = k_pages.shape, k_pages.stride()
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have one shape [pages, Hkv, page, d]")
     if v_pages.stride() != stride or stride[3] != 1:
         raise ValueError("k_pages and v_pages must have the same strides, the last dimension contiguous")
-    ks = vs = None
+    ks = vs = 0
+    pages, heads, page, d = shape
     if dtype == QW_KV_INT8:
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _need(s, torch.float32, name, 3)
-            _need_shape(s, shape[:3], name)
-            if s.device != k_pages.device:
-                raise ValueError(f"{name} is on {s.device}, the cache on {k_pages.device}")
+            if s.shape != shape[:3] or s.get_device() != index:
+                raise ValueError(f"{name} must be {tuple(shape[:3])} on the cache's device")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("only an int8 cache has scales")
-    return KvCacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, dtype, shape[0], shape[2], shape[1], shape[3],
-                       stride[0], stride[1], stride[2])
+    return (_pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, dtype, pages, page, heads, d, stride[0],
+                        stride[1], stride[2]), dtype, heads, d)
 
 
-def _kv_batch(page_table, seq_lens, cu_tokens, dev):
-    for t, name, nd in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1), (cu_tokens, "cu_tokens", 1)):
-        if t.dtype != torch.int32 or t.dim() != nd or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {nd} dimension(s) on {dev}")
-    B = page_table.shape[0]
-    if seq_lens.shape[0] != B or cu_tokens.shape[0] != B + 1:
+def _kv_batch(table, lens, cu, index):
+    """The packed descriptor of a batch."""
+    if not (table.dtype is lens.dtype is cu.dtype is _i32):
+        raise ValueError("page_table, seq_lens and cu_tokens must be int32")
+    if not (table.get_device() == lens.get_device() == cu.get_device() == index):
+        raise ValueError("page_table, seq_lens and cu_tokens must be on the cache's device")
+    if table.dim() != 2 or not (table.is_contiguous() and lens.is_contiguous() and cu.is_contiguous()):
+        raise ValueError("page_table [B, max_pages], seq_lens [B] and cu_tokens [B + 1] must be contiguous")
+    B, width = table.shape
+    if lens.dim() != 1 or cu.dim() != 1 or lens.shape[0] != B or cu.shape[0] != B + 1:
         raise ValueError("page_table [B, max_pages], seq_lens [B] and cu_tokens [B + 1] disagree")
-    return KvBatchDesc(page_table.data_ptr(), seq_lens.data_ptr(), cu_tokens.data_ptr(), B, page_table.shape[1])
+    return _pack_batch(table.data_ptr(), lens.data_ptr(), cu.data_ptr(), B, width)
 
 
-def _rows(t, name, cache, dev, heads=None):
-    """Checks new tokens' rows [T, heads, d] (strided, d contiguous); returns the two strides."""
-    want = torch.bfloat16 if cache.dtype == QW_KV_BF16 else torch.float16
-    if t.dtype != want or t.device != dev:
-        raise TypeError(f"{name} must be {want} on {dev}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[2] != cache.d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {heads or 'Hq'}, {cache.d}], got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return s[0], s[1]
+def _rows(t, name, dtype, d, index, heads):
+    """Checks new tokens' rows [T, heads, d] (strided, d contiguous); returns (T, heads, strides)."""
+    want = _ACT_TYPES[dtype]
+    if t.dtype is not want or t.get_device() != index:
+        raise TypeError(f"{name} must be {want} on the cache's device, got {t.dtype} on {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, {d}]")
+    T, h, dt = t.shape
+    st, sh, sd = t.stride()
+    if dt != d or (heads and h != heads) or sd != 1:
+        raise ValueError(f"{name} must be [T, {heads or 'Hq'}, {d}] with the last dimension contiguous")
+    return T, h, st, sh
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_tokens, k_scale=None, v_scale=None):
@@ -562,14 +602,14 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_tokens, k_scale=N
     [pages, Hkv, page, d]; an int8 cache has scales [pages, Hkv, page] float32 and quantizes
     each row).  Sequence b's new tokens are rows cu_tokens[b] .. cu_tokens[b + 1] - 1 and its
     last positions; seq_lens counts them already."""
-    dev = k_pages.device
-    c = _kv_cache(k_pages, v_pages, k_scale, v_scale)
-    b = _kv_batch(page_table, seq_lens, cu_tokens, dev)
-    kt, kh = _rows(k, "k", c, dev, c.Hkv)
-    vt, vh = _rows(v, "v", c, dev, c.Hkv)
-    if v.shape[0] != k.shape[0]:
+    index = k_pages.get_device()
+    cache, dtype, heads, d = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
+    T, _, kt, kh = _rows(k, "k", dtype, d, index, heads)
+    Tv, _, vt, vh = _rows(v, "v", dtype, d, index, heads)
+    if Tv != T:
         raise ValueError("k and v must have the same number of tokens")
-    _launch(dev, lib().kv_append, c, b, k.data_ptr(), v.data_ptr(), k.shape[0], kt, kh, vt, vh)
+    _run(index, _step_fn("kv_append"), cache, batch, k.data_ptr(), v.data_ptr(), T, kt, kh, vt, vh, _raw_stream(index))
 
 
 def kv_copy_pages(pairs, *pools):
@@ -578,29 +618,29 @@ def kv_copy_pages(pairs, *pools):
     [layers, pages] -- 4 or 5 dimensions for K and V, 3 or 4 (float32) for the scales of an
     int8 cache -- and whose pages are dense.  No page may be a destination twice, nor both a
     source and a destination."""
-    _need(pairs, torch.int32, "pairs", 2)
-    if pairs.shape[1] != 2:
-        raise ValueError("pairs must be [n, 2]")
+    index = pairs.get_device()
+    if pairs.dtype is not _i32 or index < 0:
+        raise TypeError("pairs must be an int32 CUDA tensor")
+    if pairs.dim() != 2 or pairs.shape[1] != 2 or not pairs.is_contiguous():
+        raise ValueError("pairs must be a contiguous [n, 2]")
     if not 1 <= len(pools) <= 4:
         raise ValueError("one to four pools")
-    desc = (PagePoolDesc * len(pools))()
+    desc = b""
     for i, x in enumerate(pools):
-        if x.device != pairs.device:
+        if x.get_device() != index:
             raise ValueError(f"pool {i} is on {x.device}, the pairs on {pairs.device}")
-        inner = 2 if x.dtype == torch.float32 else 3
-        lead = x.dim() - inner
-        if lead not in (1, 2):
-            raise ValueError(f"pool {i}: [pages, ...] or [layers, pages, ...] with {inner} dimensions a page")
-        es, shape, stride = x.element_size(), x.shape, x.stride()
+        shape, stride, es = x.shape, x.stride(), x.element_size()
+        lead = len(shape) - (2 if x.dtype is _f32 else 3)
+        if lead != 1 and lead != 2:
+            raise ValueError(f"pool {i}: [pages, ...] or [layers, pages, ...] before a page's dimensions")
         dense = 1
         for st, n in sorted(zip(stride[lead:], shape[lead:])):
             if n != 1 and st != dense:
                 raise ValueError(f"pool {i}: a page must be one dense block")
             dense *= n
-        layers, layer_stride = (1, 0) if lead == 1 else (shape[0], stride[0])
-        desc[i] = PagePoolDesc(x.data_ptr(), layers, shape[lead - 1], layer_stride * es, stride[lead - 1] * es,
-                               dense * es)
-    _launch(pairs.device, lib().kv_copy_pages, desc, len(pools), pairs.data_ptr(), pairs.shape[0])
+        desc += _pack_pool(x.data_ptr(), shape[0] if lead == 2 else 1, shape[lead - 1],
+                           stride[0] * es if lead == 2 else 0, stride[lead - 1] * es, dense * es)
+    _run(index, _step_fn("kv_copy_pages"), desc, len(pools), pairs.data_ptr(), pairs.shape[0], _raw_stream(index))
 
 
 def attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, max_new: int = 1, window: int = 0, sinks: int = 0,
@@ -611,25 +651,22 @@ def attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, max_new: in
     j > i - window or j < sinks.  max_new: the most new tokens of a sequence (a hint).
     scale: 1 / sqrt(d) unless given.  lse: a float32 [T, Hq] tensor to fill with the log of
     the sum of exponentials; then (out, lse) is returned."""
-    dev = k_pages.device
-    c = _kv_cache(k_pages, v_pages, k_scale, v_scale)
-    b = _kv_batch(page_table, seq_lens, cu_tokens, dev)
-    qt, qh = _rows(q, "q", c, dev)
-    T, Hq, d = q.shape
+    index = k_pages.get_device()
+    cache, dtype, heads, d = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
+    T, Hq, qt, qh = _rows(q, "q", dtype, d, index, 0)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
-    elif out.dtype != q.dtype or out.shape != q.shape or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(q.shape)} on {dev}")
-    if lse is not None:
-        _need(lse, torch.float32, "lse", 2)
-        _need_shape(lse, (T, Hq), "lse")
-        if lse.device != dev:
-            raise ValueError(f"lse is on {lse.device}, the cache on {dev}")
-    L = lib()
-    buf, nbytes = _scratch(ws, dev, "paged", L.attn_paged_workspace_bytes, d, Hq, c.Hkv, max_new)
-    _launch(dev, L.attn_paged, c, b, q.data_ptr(), T, Hq, qt, qh, max_new, window, sinks,
-            1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-            None if buf is None else buf.data_ptr(), nbytes)
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    elif out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(q.shape)} on the cache's device")
+    if lse is not None and (lse.dtype is not _f32 or lse.shape != (T, Hq) or lse.get_device() != index
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {(T, Hq)} on the cache's device")
+    stream = _raw_stream(index)
+    buf, nbytes = _scratch(ws, index, stream, "paged", _step_fn("attn_paged_workspace_bytes"), d, Hq, heads, max_new)
+    _run(index, _step_fn("attn_paged"), cache, batch, q.data_ptr(), T, Hq, qt, qh, max_new, window, sinks,
+         d ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), buf, nbytes,
+         stream)
     return out if lse is None else (out, lse)
 
 
@@ -720,30 +757,41 @@ _LOGIT_TYPES = {torch.float16: QW_F16, torch.bfloat16: QW_BF16, torch.float32: Q
 def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> TokenLogprobs:
     """Log probabilities of given tokens (int32 or int64 [M] or [M, C]), entropy, logsumexp
     and the k (<= 64) most likely tokens of each row of logits [M, N] (fp16, bf16 or float32;
-    rows may be strided), in one pass over the logits."""
+    rows may be strided), in one pass over the logits.  (The float results are views of one
+    buffer.)"""
     dtype = _LOGIT_TYPES.get(logits.dtype)
-    if dtype is None or not logits.is_cuda:
+    index = logits.get_device()
+    if dtype is None or index < 0:
         raise TypeError("logits must be a float16, bfloat16 or float32 CUDA tensor")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+    if logits.dim() != 2:
         raise ValueError("logits must be [M, N] with contiguous rows")
-    dev = logits.device
     M, N = logits.shape
-    if tokens.dtype not in (torch.int32, torch.int64) or tokens.device != dev:
-        raise TypeError(f"tokens must be int32 or int64 on {dev}")
-    if tokens.dim() not in (1, 2) or tokens.shape[0] != M or not tokens.is_contiguous():
+    row, col = logits.stride()
+    if col != 1 and N > 1:
+        raise ValueError("logits must be [M, N] with contiguous rows")
+    tt = tokens.dtype
+    if tt is not torch.int64 and tt is not _i32 or tokens.get_device() != index:
+        raise TypeError("tokens must be int32 or int64 on the logits' device")
+    shape = tokens.shape
+    if len(shape) not in (1, 2) or shape[0] != M or not tokens.is_contiguous():
         raise ValueError("tokens must be a contiguous [M] or [M, C]")
-    C = 1 if tokens.dim() == 1 else tokens.shape[1]
-    f32 = dict(dtype=torch.float32, device=dev)
-    logprob = torch.empty(tokens.shape, **f32)
-    entropy, lse = torch.empty((2, M), **f32)
-    top = torch.empty((M, k), **f32) if k > 0 else None
-    idx = torch.empty((M, k), dtype=torch.int32, device=dev) if k > 0 else None
-    L = lib()
-    buf, nbytes = _scratch(ws, dev, "logprobs", L.token_logprobs_workspace_bytes, M, N, k, dtype)
-    _launch(dev, L.token_logprobs, logits.data_ptr(), dtype, M, N, logits.stride(0), tokens.data_ptr(),
-            tokens.element_size(), C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
-            None if top is None else top.data_ptr(), None if idx is None else idx.data_ptr(),
-            None if buf is None else buf.data_ptr(), nbytes)
+    C = 1 if len(shape) == 1 else shape[1]
+    if k < 0:
+        raise ValueError("k must not be negative")
+    # entropy [M], lse [M], logprob [M, C], top_logprob [M, k]
+    buf = torch.empty(M * (2 + C + k), dtype=_f32, device=logits.device)
+    entropy, lse, logprob = buf[:M], buf[M:2 * M], buf[2 * M:(2 + C) * M].view(shape)
+    top = idx = None
+    p = buf.data_ptr()
+    ptop = pidx = None
+    if k:
+        top = buf[(2 + C) * M:].view(M, k)
+        idx = torch.empty((M, k), dtype=_i32, device=logits.device)
+        ptop, pidx = p + 4 * M * (2 + C), idx.data_ptr()
+    stream = _raw_stream(index)
+    wbuf, nbytes = _scratch(ws, index, stream, "logprobs", _step_fn("token_logprobs_workspace_bytes"), M, N, k, dtype)
+    _run(index, _step_fn("token_logprobs"), logits.data_ptr(), dtype, M, N, row, tokens.data_ptr(),
+         4 if tt is _i32 else 8, C, k, p + 8 * M, p, p + 4 * M, ptop, pidx, wbuf, nbytes, stream)
     return TokenLogprobs(logprob, entropy, lse, top, idx)
 
 
