@@ -757,8 +757,7 @@ _LOGIT_TYPES = {torch.float16: QW_F16, torch.bfloat16: QW_BF16, torch.float32: Q
 def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> TokenLogprobs:
     """Log probabilities of given tokens (int32 or int64 [M] or [M, C]), entropy, logsumexp
     and the k (<= 64) most likely tokens of each row of logits [M, N] (fp16, bf16 or float32;
-    rows may be strided), in one pass over the logits.  (The float results are views of one
-    buffer.)"""
+    rows may be strided), in one pass over the logits."""
     dtype = _LOGIT_TYPES.get(logits.dtype)
     index = logits.get_device()
     if dtype is None or index < 0:
@@ -778,20 +777,18 @@ def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> T
     C = 1 if len(shape) == 1 else shape[1]
     if k < 0:
         raise ValueError("k must not be negative")
-    # entropy [M], lse [M], logprob [M, C], top_logprob [M, k]
-    buf = torch.empty(M * (2 + C + k), dtype=_f32, device=logits.device)
-    entropy, lse, logprob = buf[:M], buf[M:2 * M], buf[2 * M:(2 + C) * M].view(shape)
-    top = idx = None
-    p = buf.data_ptr()
-    ptop = pidx = None
+    dev, empty = logits.device, torch.empty
+    entropy, lse = empty(M, dtype=_f32, device=dev), empty(M, dtype=_f32, device=dev)
+    logprob = empty(shape, dtype=_f32, device=dev)
+    top = idx = ptop = pidx = None
     if k:
-        top = buf[(2 + C) * M:].view(M, k)
-        idx = torch.empty((M, k), dtype=_i32, device=logits.device)
-        ptop, pidx = p + 4 * M * (2 + C), idx.data_ptr()
+        top, idx = empty((M, k), dtype=_f32, device=dev), empty((M, k), dtype=_i32, device=dev)
+        ptop, pidx = top.data_ptr(), idx.data_ptr()
     stream = _raw_stream(index)
     wbuf, nbytes = _scratch(ws, index, stream, "logprobs", _step_fn("token_logprobs_workspace_bytes"), M, N, k, dtype)
     _run(index, _step_fn("token_logprobs"), logits.data_ptr(), dtype, M, N, row, tokens.data_ptr(),
-         4 if tt is _i32 else 8, C, k, p + 8 * M, p, p + 4 * M, ptop, pidx, wbuf, nbytes, stream)
+         4 if tt is _i32 else 8, C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ptop, pidx, wbuf, nbytes,
+         stream)
     return TokenLogprobs(logprob, entropy, lse, top, idx)
 
 

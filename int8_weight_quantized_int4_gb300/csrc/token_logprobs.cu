@@ -8,11 +8,14 @@
 // A thread keeps (r, s, t) while it streams its 16-byte vectors; r moves only when a vector
 // brings a new maximum.  All sums in binary32, joined in a fixed order.
 //
-// The k most likely come from the same pass: the k-th largest of the threads' maxima is a
-// lower bound T of the k-th largest element, so the elements above T lie in fewer than k
-// threads, which read their own elements again (from L1 and L2) and list them; elements
-// equal to T fill up, lowest index first.  A row is cut into slices (one CTA each); the last
-// slice of a row to finish joins the sums and selects among the slices' lists the same way.
+// The k most likely come from the same pass.  Each warp's j-th largest thread maximum, j =
+// ceil(k / warps), is passed by j threads of that warp, so the smallest of these, T, is a lower
+// bound of the k-th largest element: the elements from T on lie in a few threads, which read
+// the quarters of their elements that reach T again (from L2) and list them as
+// (value, column) composites -- distinct, ties ordered by column.  A list that overflows
+// (many equal logits) gives a higher bound, the k-th largest of what it holds, and is filled
+// again.  A row is cut into slices (one CTA each); the last slice of a row to finish joins the
+// sums and selects among the slices' lists the same way.
 //
 // What bounds it: the read of the logits (HBM), at about six operations and one ex2 an
 // element; for few rows the launch and two chains of block-wide steps.
@@ -32,9 +35,9 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpMaxK = 64;
 constexpr int kLpMaxSlices = 128;                 // kLpMaxSlices k candidates: at most 32 a thread
-constexpr int kLpListA = 2048;                    // elements above T
-constexpr int kLpListB = 256;                     // elements equal to T
-static_assert(kLpMaxSlices * kLpMaxK <= kLpListA / kLpMaxK * kLpThreads, "a joining thread's share, k times, fits list A");
+constexpr int kLpList = 512;                      // listed elements
+constexpr int kLpPerSm = 4;                       // CTAs an SM holds (64 registers a thread)
+constexpr int kLpUnroll = 4;                      // vectors in flight a thread; maxima kept apart
 
 struct LpArgs {
   const void *logits;
@@ -52,12 +55,11 @@ struct LpArgs {
 
 struct LpSmem {
   float red[3][kLpWarps];
-  unsigned long long lista[kLpListA];
-  unsigned listb[kLpListB];
-  alignas(16) unsigned long long key[kLpThreads];
+  unsigned wkey[kLpWarps];
+  unsigned long long list[kLpList];
   unsigned long long sel[kLpMaxK];
   unsigned long long T;
-  int na, nb, last, scan[kLpWarps];
+  int n, last;
 };
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -95,31 +97,21 @@ __device__ __forceinline__ float lp_float<__nv_bfloat16>(__nv_bfloat16 x) { retu
 
 // A row as 16-byte vectors: vector v holds columns v VE - pad .. v VE - pad + VE - 1, where
 // pad is how many elements the row starts past a 16-byte boundary.  Only the first and last
-// vectors can reach past the row; they are read element by element.
+// vectors can reach past the row; their elements are read one by one.
 template <typename T>
 struct LpRow {
   static constexpr int VE = LpVec<T>::VE;
+  static constexpr bool kBf = sizeof(T) == 2 && !__is_same(T, __half);
   const T *row;
-  int pad, N, nvec;
+  int pad, N, nvec, in0, in1;                     // whole vectors: [in0, in1)
   __device__ __forceinline__ LpRow(const T *r, int n) : row(r), N(n) {
     pad = (int)((reinterpret_cast<uintptr_t>(r) / sizeof(T)) % VE);
     nvec = (int)(((long long)n + pad + VE - 1) / VE);
+    in0 = pad > 0 ? 1 : 0;
+    in1 = max((int)(((long long)n + pad) / VE), in0);
   }
   __device__ __forceinline__ int col(int v) const { return v * VE - pad; }
-  __device__ __forceinline__ bool inner(int v) const { return col(v) >= 0 && col(v) + VE <= N; }
-  __device__ __forceinline__ uint4 raw(int v) const {
-    if (inner(v)) return __ldg(reinterpret_cast<const uint4 *>(row + col(v)));
-    alignas(16) T e[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      const int c = col(v) + i;
-      if (c >= 0 && c < N) e[i] = row[c];
-      else if constexpr (sizeof(T) == 4) e[i] = -INFINITY;
-      else *reinterpret_cast<uint16_t *>(&e[i]) = sizeof(T) == 2 && LpRow::kBf ? 0xff80u : 0xfc00u;   // -inf
-    }
-    return *reinterpret_cast<const uint4 *>(e);
-  }
-  static constexpr bool kBf = sizeof(T) == 2 && !__is_same(T, __half);
+  __device__ __forceinline__ uint4 raw(int v) const { return __ldg(reinterpret_cast<const uint4 *>(row + col(v))); }
 };
 template <typename T>
 __device__ __forceinline__ void lp_unpack(const uint4 &w, float (&x)[LpVec<T>::VE]) {
@@ -176,125 +168,81 @@ __device__ __forceinline__ LpSum lp_block(LpSum a, LpSmem &sm) {
   return a;
 }
 
-// sm.T = the k-th largest of n keys (k <= n), each thread counting for its own keys.
-__device__ __forceinline__ void kth_largest(const unsigned long long *key, int n, int k, LpSmem &sm) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const unsigned long long mine = key[i];
-    int above = 0, equal = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      above += key[j] > mine;
-      equal += key[j] == mine;
+// A lower bound of the k-th largest of the elements whose largest each thread holds in
+// `key` (0: none), from the first `warps` warps, all of whose lanes hold one.
+__device__ __forceinline__ unsigned lp_bound(unsigned key, int warps, int k, LpSmem &sm) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = warps > 0 ? (k + warps - 1) / warps : 33;
+  unsigned best = 0u;
+  if (w < warps && j <= 32)
+    for (int i = 0; i < j; ++i) {                 // the warp's largest, one lane at a time
+      best = __reduce_max_sync(0xffffffffu, key);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, key == best)) - 1) key = 0u;
     }
-    if (above < k && k <= above + equal) sm.T = mine;
+  if (lane == 0) sm.wkey[w] = best;
+  __syncthreads();
+  unsigned T = 0u;
+  if (j <= 32) {
+    T = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < kLpWarps; ++i)
+      if (i < warps) T = min(T, sm.wkey[i]);
+  }
+  return T;
+}
+// sm.T = the k-th largest of the (distinct) elements of a full list.
+__device__ __forceinline__ void lp_raise(int k, LpSmem &sm) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < kLpList; i += kLpThreads) {
+    const unsigned long long mine = sm.list[i];
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < kLpList; ++j) above += sm.list[j] > mine;
+    if (above == k - 1) sm.T = mine;
   }
   __syncthreads();
 }
-// The k largest of list[0 .. n) (distinct, n >= k or all of them), largest first, into sel.
-__device__ __forceinline__ void rank_list(const unsigned long long *list, int n, int k, unsigned long long *sel) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const unsigned long long mine = list[i];
-    int above = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) above += list[j] > mine;
-    if (above < k) sel[above] = mine;
+// Lists the elements from T on that `visit(T, put)` puts -- every thread its own --, raising T
+// while they do not fit, and writes the k largest, largest first, to sm.sel (0 past the last).
+template <typename F>
+__device__ __forceinline__ void lp_select(unsigned long long T, int k, LpSmem &sm, const F &visit) {
+  if ((int)threadIdx.x < k) sm.sel[threadIdx.x] = 0ull;
+  if (threadIdx.x == 0) sm.n = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (;;) {
+    visit(T, [&](unsigned long long p) {
+      const int at = atomicAdd(&sm.n, 1);
+      if (at < kLpList) sm.list[at] = p;
+    });
+    __syncthreads();
+    if (sm.n <= kLpList) break;
+    lp_raise(k, sm);
+    T = sm.T;
+    if (threadIdx.x == 0) sm.n = 0;
+    __syncthreads();
   }
+  const int n = sm.n;
+  // rank: 4 threads an element while that many are free
+  const int sub = n <= kLpThreads / 4 ? 4 : 1;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kLpThreads / sub) {
+    const int i = i0 + (int)threadIdx.x / sub, e = (int)threadIdx.x % sub;
+    const unsigned long long mine = i < n ? sm.list[i] : 0ull;
+    int above = 0;
+    if (i < n)
+#pragma unroll 4
+      for (int j = e; j < n; j += sub) above += sm.list[j] > mine;
+    if (sub == 4) {
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+    }
+    if (i < n && e == 0 && above < k) sm.sel[above] = mine;
+  }
+  __syncthreads();
 }
 __device__ __forceinline__ unsigned long long lp_pair(unsigned key, int col) {
   return ((unsigned long long)key << 32) | (0xffffffffu - (unsigned)col);
-}
-
-// The slice's k best (key, column) pairs, best first, in sm.sel; 0 where the slice has
-// fewer elements.  mymax: the key of this thread's largest element (0: it has none).
-template <typename T>
-__device__ void lp_slice_topk(const LpRow<T> &R, int v0, int v1, int k, unsigned mymax, LpSmem &sm) {
-  constexpr int VE = LpVec<T>::VE;
-  sm.key[threadIdx.x] = mymax;
-  if (threadIdx.x < k) sm.sel[threadIdx.x] = 0ull;
-  if (threadIdx.x == 0) sm.na = sm.nb = 0;
-  __syncthreads();
-  kth_largest(sm.key, kLpThreads, k, sm);
-  unsigned T32 = (unsigned)sm.T;
-  for (;;) {
-    if (mymax >= T32 && mymax != 0u) {
-      for (int v = v0 + (int)threadIdx.x; v < v1; v += kLpThreads) {
-        float x[VE];
-        lp_unpack<T>(R.raw(v), x);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int c = R.col(v) + e;
-          const unsigned key = order_key32(x[e]);
-          if (key < T32 || c < 0 || c >= R.N) continue;
-          if (key > T32) {
-            const int at = atomicAdd(&sm.na, 1);
-            if (at < kLpListA) sm.lista[at] = lp_pair(key, c);
-          } else {
-            const int at = atomicAdd(&sm.nb, 1);
-            if (at < kLpListB) sm.listb[at] = (unsigned)c;
-          }
-        }
-      }
-    }
-    __syncthreads();
-    if (sm.na <= kLpListA) break;
-    // more above T than the list holds (they crowd into few threads): the k-th largest of
-    // those listed is a higher lower bound; take its key and list again
-    kth_largest(sm.lista, kLpListA, k, sm);
-    T32 = (unsigned)(sm.T >> 32);
-    __syncthreads();
-    if (threadIdx.x == 0) sm.na = sm.nb = 0;
-    __syncthreads();
-  }
-  const int na = sm.na, nb = sm.nb;
-  rank_list(sm.lista, na, k, sm.sel);
-  const int want = k - na;
-  if (want > 0 && T32 != 0u) {
-    if (nb <= kLpListB) {                         // few equal to T: rank them by column
-      if ((int)threadIdx.x < nb) {
-        const unsigned c = sm.listb[threadIdx.x];
-        int before = 0;
-        for (int j = 0; j < nb; ++j) before += sm.listb[j] < c;
-        if (before < want) sm.sel[na + before] = lp_pair(T32, (int)c);
-      }
-    } else {                                      // many: the first `want`, in column order
-      int got = 0;
-      for (int base = v0; base < v1 && got < want; base += kLpThreads) {
-        const int v = base + (int)threadIdx.x;
-        unsigned hit = 0;
-        if (v < v1) {
-          float x[VE];
-          lp_unpack<T>(R.raw(v), x);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const int c = R.col(v) + e;
-            if (c >= 0 && c < R.N && order_key32(x[e]) == T32) hit |= 1u << e;
-          }
-        }
-        int inc = __popc(hit);
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        if (lane == 31) sm.scan[w] = inc;
-        __syncthreads();
-        int at = got + inc - __popc(hit), all = 0;
-        for (int i = 0; i < kLpWarps; ++i) {
-          if (i < w) at += sm.scan[i];
-          all += sm.scan[i];
-        }
-        while (hit && at < want) {
-          const int e = __ffs(hit) - 1;
-          hit &= hit - 1;
-          sm.sel[na + at++] = lp_pair(T32, R.col(v) + e);
-        }
-        got += all;
-        __syncthreads();
-      }
-    }
-  }
-  __syncthreads();
 }
 
 // The row's results from its sums and (k > 0) its k best pairs in sm.sel.
@@ -323,7 +271,7 @@ __device__ __forceinline__ void lp_write(const LpArgs &a, int m, const T *row, c
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 5) token_logprobs_kernel(const __grid_constant__ LpArgs a) {
+__global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(const __grid_constant__ LpArgs a) {
   constexpr int VE = LpVec<T>::VE;
   __shared__ LpSmem sm;
   const int S = gridDim.x, sl = blockIdx.x;
@@ -334,38 +282,91 @@ __global__ void __launch_bounds__(kLpThreads, 5) token_logprobs_kernel(const __g
     const LpRow<T> R(row, a.N);
     const int v0 = min(sl * a.vps, R.nvec), v1 = min(v0 + a.vps, R.nvec);
     LpSum z{kNoRef, 0.0f, 0.0f};
-    float top = -INFINITY;
-    constexpr int UN = 4;                         // vectors in flight a thread
-    auto take = [&](const uint4 &w) {
-      float x[VE];
-      lp_unpack<T>(w, x);
-      float vm = x[0];
+    float top = -INFINITY, quarter[kLpUnroll];
 #pragma unroll
-      for (int e = 1; e < VE; ++e) vm = fmaxf(vm, x[e]);
-      if (vm > top) {
-        top = vm;
-        lp_move(z, vm * kLog2e);
-      }
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float y = max_nan(fmaf(x[e], kLog2e, -z.r), -150.0f);      // 2^-150 is 0; -inf stays out of y 2^y
-        const float p = lp_ex2(y);
-        z.s += p;
-        z.t = fmaf(y, p, z.t);
+    for (int i = 0; i < kLpUnroll; ++i) quarter[i] = -INFINITY;
+    const int w0 = max(v0, R.in0), w1 = min(v1, R.in1);
+    auto raise = [&](float x) {                   // a new largest element: the reference follows
+      if (x > top) {
+        top = x;
+        lp_move(z, x * kLog2e);
       }
     };
-    int v = v0 + (int)threadIdx.x;
-    const bool some = v < v1;
-    for (; v + (UN - 1) * kLpThreads < v1; v += UN * kLpThreads) {
-      uint4 w[UN];
+    auto add = [&](float x) {
+      const float y = max_nan(fmaf(x, kLog2e, -z.r), -150.0f);     // 2^-150 is 0; -inf stays out of y 2^y
+      const float p = lp_ex2(y);
+      z.s += p;
+      z.t = fmaf(y, p, z.t);
+    };
+    // the elements of the row's cut vectors: thread 0 takes those of its slice, once
+    auto edges = [&](auto f) {
+      if (threadIdx.x != 0) return;
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {
+        const int v = end ? R.in1 : 0;
+        if (v < v0 || v >= v1 || (end ? v >= R.nvec : R.in0 == 0) ) continue;
+#pragma unroll 1
+        for (int c = max(R.col(v), 0); c < min(R.col(v) + VE, R.N); ++c) f(lp_float(row[c]), c);
+      }
+    };
+#pragma unroll 1
+    for (int v = w0 + (int)threadIdx.x; v < w1; v += kLpUnroll * kLpThreads) {
+      uint4 w[kLpUnroll];
 #pragma unroll
-      for (int i = 0; i < UN; ++i) w[i] = R.raw(v + i * kLpThreads);
+      for (int i = 0; i < kLpUnroll; ++i)
+        if (v + i * kLpThreads < w1) w[i] = R.raw(v + i * kLpThreads);
 #pragma unroll
-      for (int i = 0; i < UN; ++i) take(w[i]);
+      for (int i = 0; i < kLpUnroll; ++i) {
+        if (v + i * kLpThreads >= w1) break;
+        float x[VE];
+        lp_unpack<T>(w[i], x);
+        float vm = x[0];
+#pragma unroll
+        for (int e = 1; e < VE; ++e) vm = fmaxf(vm, x[e]);
+        quarter[i] = fmaxf(quarter[i], vm);
+        raise(vm);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) add(x[e]);
+      }
     }
-    for (; v < v1; v += kLpThreads) take(R.raw(v));
+    edges([&](float x, int) {
+      raise(x);
+      add(x);
+    });
     z = lp_block(z, sm);
-    if (a.k > 0) lp_slice_topk<T>(R, v0, v1, a.k, some ? order_key32(top) : 0u, sm);
+    if (a.k > 0) {
+      unsigned reach = 0u;                        // order keys of the quarters
+      const unsigned bound = lp_bound(w0 + (int)threadIdx.x < w1 ? order_key32(top) : 0u, min((w1 - w0) / 32, kLpWarps), a.k, sm);
+      lp_select((unsigned long long)bound << 32, a.k, sm, [&](unsigned long long B, auto put) {
+        const unsigned key0 = (unsigned)(B >> 32);
+        reach = 0u;
+#pragma unroll
+        for (int i = 0; i < kLpUnroll; ++i) reach |= order_key32(quarter[i]) >= key0 ? 1u << i : 0u;
+        auto offer = [&](float x, int c) {
+          const unsigned long long p = lp_pair(order_key32(x), c);
+          if (p >= B) put(p);
+        };
+#pragma unroll 1
+        for (int v = w0 + (int)threadIdx.x; v < w1 && reach; v += kLpUnroll * kLpThreads) {
+          uint4 w[kLpUnroll];
+#pragma unroll
+          for (int i = 0; i < kLpUnroll; ++i)
+            if (v + i * kLpThreads < w1 && (reach >> i & 1u)) w[i] = R.raw(v + i * kLpThreads);
+#pragma unroll 1
+          for (int i = 0; i < kLpUnroll; ++i) {
+            if (v + i * kLpThreads < w1 && (reach >> i & 1u)) {
+              float x[VE];
+              lp_unpack<T>(w[0], x);
+#pragma unroll
+              for (int e = 0; e < VE; ++e) offer(x[e], R.col(v + i * kLpThreads) + e);
+            }
+#pragma unroll
+            for (int j = 0; j + 1 < kLpUnroll; ++j) w[j] = w[j + 1];
+          }
+        }
+        edges(offer);
+      });
+    }
     if (S > 1) {
       // ---- publish; the last slice of the row joins
       unsigned long long *cand = a.cand + (size_t)m * S * a.k;
@@ -389,22 +390,16 @@ __global__ void __launch_bounds__(kLpThreads, 5) token_logprobs_kernel(const __g
       z = lp_block(z, sm);
       if (a.k > 0) {
         const int total = S * a.k;
-        unsigned long long best = 0ull;
-        for (int i = threadIdx.x; i < total; i += kLpThreads) best = max(best, __ldcg(cand + i));
-        sm.key[threadIdx.x] = best;
-        if ((int)threadIdx.x < a.k) sm.sel[threadIdx.x] = 0ull;
-        if (threadIdx.x == 0) sm.na = 0;
-        __syncthreads();
-        kth_largest(sm.key, kLpThreads, a.k, sm);
-        const unsigned long long T64 = sm.T;
-        if (best >= T64 && best != 0ull)
+        unsigned best = 0u;
+        for (int i = threadIdx.x; i < total; i += kLpThreads) best = max(best, (unsigned)(__ldcg(cand + i) >> 32));
+        const unsigned bound = lp_bound(best, min(total / 32, kLpWarps), a.k, sm);
+        lp_select((unsigned long long)bound << 32, a.k, sm, [&](unsigned long long B, auto put) {
+          if (best < (unsigned)(B >> 32)) return;
           for (int i = threadIdx.x; i < total; i += kLpThreads) {
             const unsigned long long p = __ldcg(cand + i);
-            if (p >= T64 && p != 0ull) sm.lista[atomicAdd(&sm.na, 1)] = p;
+            if (p >= B && p != 0ull) put(p);
           }
-        __syncthreads();
-        rank_list(sm.lista, sm.na, a.k, sm.sel);
-        __syncthreads();
+        });
       }
     }
     lp_write<T>(a, m, row, z, sm);
@@ -424,11 +419,11 @@ int bad(int code, const char *fmt, ...) {
 }
 bool at(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// Slices a row is cut into: enough CTAs to fill the SMs at 5 CTAs each, but at least two
+// Slices a row is cut into: enough CTAs to fill the SMs twice, but at least two
 // vectors a thread (a shorter slice costs more in the join than it saves).
-// (several slices only where M < 5 SMs: one counter a row)
-constexpr size_t kLpCounterBytes = 4096;
-constexpr int kLpPerSm = 5;
+// (several slices only where M < 8 SMs: one counter a row)
+constexpr size_t kLpCounterBytes = 8192;
+constexpr int kLpFill = 8;                        // CTAs an SM to aim for
 struct LpPlan {
   int S, vps;
   size_t counters, part, cand;
@@ -438,7 +433,7 @@ LpPlan lp_plan(int M, int N, int es, int k, int sms) {
   LpPlan p{};
   const int ve = 16 / es;
   const long long nvec = ((long long)N + ve - 1 + ve - 1) / ve;     // whatever the row's alignment
-  long long S = ((long long)kLpPerSm * sms + M - 1) / (M > 0 ? M : 1);
+  long long S = ((long long)kLpFill * sms + M - 1) / (M > 0 ? M : 1);
   const long long most = (nvec + 2 * kLpThreads - 1) / (2 * kLpThreads);
   if (S > most) S = most;
   if (S > kLpMaxSlices) S = kLpMaxSlices;
@@ -494,7 +489,7 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
   LpArgs a{};
   int sms = 0;
   if ((rc = device_info(&sms, &a.err))) return rc;
-  if ((size_t)kLpPerSm * sms * 4 > kLpCounterBytes) return bad(QW_ERR_ARCH, "more SMs than counters (%d)", sms);
+  if ((size_t)kLpFill * sms * 4 > kLpCounterBytes) return bad(QW_ERR_ARCH, "more SMs than counters (%d)", sms);
   const LpPlan p = lp_plan(M, N, dtype == QW_F32 ? 4 : 2, k, sms);
   const size_t need = p.counters + p.part + p.cand;
   if (need > 0 && (!ws || ws_bytes < need))
