@@ -5,20 +5,26 @@
 //   s = sum 2^y_j,  t = sum y_j 2^y_j
 //   logsumexp = (r + log2 s) ln 2      log p_j = (y_j - log2 s) ln 2
 //   entropy   = (log2 s - t / s) ln 2  (both terms are >= 0 up to rounding: no cancellation)
-// A thread keeps (r, s, t) while it streams its 16-byte vectors; r moves only when a vector
-// brings a new maximum.  All sums in binary32, joined in a fixed order.
+// A thread keeps (r, s, t) while it streams its 16-byte vectors; all sums in binary32, joined
+// in a fixed order.
 //
 // The k most likely come from the same pass.  Each warp's j-th largest thread maximum, j =
 // ceil(k / warps), is passed by j threads of that warp, so the smallest of these, T, is a lower
-// bound of the k-th largest element: the elements from T on lie in a few threads, which read
-// the quarters of their elements that reach T again (from L2) and list them as
+// bound of the k-th largest element: the blocks of vectors whose maximum (kept in shared
+// memory) reaches T are read again (from L2), and their elements from T on listed as
 // (value, column) composites -- distinct, ties ordered by column.  A list that overflows
 // (many equal logits) gives a higher bound, the k-th largest of what it holds, and is filled
-// again.  A row is cut into slices (one CTA each); the last slice of a row to finish joins the
-// sums and selects among the slices' lists the same way.
+// again.
 //
-// What bounds it: the read of the logits (HBM), at about six operations and one ex2 an
-// element; for few rows the launch and two chains of block-wide steps.
+// Five CTAs of 128 threads an SM.  The vectors of all rows, laid end to end with a few places
+// more for what a row costs by itself, are cut into one equal range a CTA, so the SMs finish
+// together whatever the numbers of rows and columns; the last CTA to finish a cut row joins
+// its parts' sums and selects among their lists the same way.  Each block of four vectors a
+// thread is loaded while the one before is summed, across row borders too.
+//
+// What bounds it: the read of the logits (HBM); close to it the instructions, about six an
+// element (pairs go through two-wide binary32 operations) and some 500 a warp and row; for few
+// rows the launch and two chains of block-wide steps.
 #include <float.h>
 #include <stdarg.h>
 #include <stdint.h>
@@ -31,25 +37,31 @@
 
 namespace qw {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpPerSm = 5;                       // CTAs an SM (up to 96 registers a thread)
 constexpr int kLpMaxK = 64;
-constexpr int kLpMaxSlices = 128;                 // kLpMaxSlices k candidates: at most 32 a thread
+constexpr int kLpLogUnroll = 2, kLpUnroll = 1 << kLpLogUnroll;      // vectors of a block a thread
+constexpr int kLpBlock = kLpUnroll * kLpThreads;  // vectors of a block
+constexpr int kLpMaxima = 16;                     // block maxima a thread keeps (of 2^g blocks for long rows)
+constexpr int kLpBlocks = 256;                    // listed blocks of threads
 constexpr int kLpList = 512;                      // listed elements
-constexpr int kLpPerSm = 4;                       // CTAs an SM holds (64 registers a thread)
-constexpr int kLpUnroll = 4;                      // vectors in flight a thread; maxima kept apart
+constexpr int kLpMinBlocks = 2;                   // blocks of vectors a CTA takes at least
+constexpr int kLpRowCost = 256;                   // places of a row beside its vectors
 
 struct LpArgs {
   const void *logits;
   const void *tokens;                             // [M][C] int32 or int64
   long long row_stride;                           // elements
   int M, N, C, k, tok64;
-  int vps;                                        // vectors of a slice
+  int nv;                                         // vectors of a row, whatever its alignment
+  long long share;                                // places a CTA
+  int S, step;                                    // or, S > 0: CTAs a row and vectors of each
   float *logprob, *entropy, *lse, *top_lp;
   int *top_idx;
-  float *part;                                    // [M][S][4]: r, s, t
-  unsigned long long *cand;                       // [M][S][k]
-  int *counters;                                  // [M], zero between calls
+  float *part;                                    // [CTAs][2][4]: r, s, t of a cut row's part
+  unsigned long long *cand;                       // [CTAs][2][k]
+  int *counters;                                  // [CTAs], zero between calls
   int *err;
 };
 
@@ -59,7 +71,8 @@ struct LpSmem {
   unsigned long long list[kLpList];
   unsigned long long sel[kLpMaxK];
   unsigned long long T;
-  int n, last;
+  int block[kLpBlocks];
+  int n, nblock, first, parts;
 };
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -82,6 +95,14 @@ __device__ __forceinline__ float key_value32(unsigned k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+template <typename T>
+struct LpTwo {
+  using type = __half2;
+};
+template <>
+struct LpTwo<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
 template <typename T>
 struct LpVec {
   static constexpr int VE = 16 / sizeof(T);
@@ -130,6 +151,18 @@ __device__ __forceinline__ void lp_unpack(const uint4 &w, float (&x)[LpVec<T>::V
     }
   }
 }
+// The largest element of a vector (16-bit types: two at a time; NaN ignored).
+template <typename T>
+__device__ __forceinline__ float lp_max(const uint4 &w) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else {
+    using T2 = typename LpTwo<T>::type;
+    const T2 *e = reinterpret_cast<const T2 *>(&w);
+    const T2 hi = __hmax2(__hmax2(e[0], e[1]), __hmax2(e[2], e[3]));
+    return fmaxf(lp_float(hi.x), lp_float(hi.y));
+  }
+}
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e30f;                  // the reference of a sum of nothing
@@ -137,6 +170,32 @@ constexpr float kNoRef = -1e30f;                  // the reference of a sum of n
 struct LpSum {
   float r, s, t;
 };
+// two binary32 values in a register pair
+__device__ __forceinline__ unsigned long long pair2(float a, float b) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 both2(unsigned long long a) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void lp_move(LpSum &a, float r) {       // to the reference r
   const float d = a.r - r, f = lp_ex2(d);
   a.t = a.s == 0.0f ? 0.0f : (a.t + d * a.s) * f;
@@ -149,23 +208,31 @@ __device__ __forceinline__ LpSum lp_join(LpSum a, LpSum b) {
   lp_move(b, r);
   return LpSum{r, a.s + b.s, a.t + b.t};
 }
-// over the CTA, in a fixed order; valid in every thread
-__device__ __forceinline__ LpSum lp_block(LpSum a, LpSmem &sm) {
+// to the largest reference among 2^n lanes, then plain sums (xor shuffles: a fixed order)
+template <int LANES>
+__device__ __forceinline__ LpSum lp_lanes(LpSum a) {
+  float r = a.r;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = lp_join(a, LpSum{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                         __shfl_xor_sync(0xffffffffu, a.t, o)});
-  const int w = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
+  for (int o = LANES / 2; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+  lp_move(a, r);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
+  }
+  return a;
+}
+// over the CTA; valid in every thread
+__device__ __forceinline__ LpSum lp_block(LpSum a, LpSmem &sm) {
+  a = lp_lanes<32>(a);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
     sm.red[0][w] = a.r;
     sm.red[1][w] = a.s;
     sm.red[2][w] = a.t;
   }
   __syncthreads();
-  a = LpSum{sm.red[0][0], sm.red[1][0], sm.red[2][0]};
-#pragma unroll
-  for (int i = 1; i < kLpWarps; ++i) a = lp_join(a, LpSum{sm.red[0][i], sm.red[1][i], sm.red[2][i]});
-  return a;
+  return lp_lanes<kLpWarps>(LpSum{sm.red[0][lane % kLpWarps], sm.red[1][lane % kLpWarps], sm.red[2][lane % kLpWarps]});
 }
 
 // A lower bound of the k-th largest of the elements whose largest each thread holds in
@@ -223,21 +290,18 @@ __device__ __forceinline__ void lp_select(unsigned long long T, int k, LpSmem &s
     __syncthreads();
   }
   const int n = sm.n;
-  // rank: 4 threads an element while that many are free
-  const int sub = n <= kLpThreads / 4 ? 4 : 1;
+  // rank: eight threads an element
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += kLpThreads / sub) {
-    const int i = i0 + (int)threadIdx.x / sub, e = (int)threadIdx.x % sub;
+  for (int i0 = 0; i0 < n; i0 += kLpThreads / 8) {
+    const int i = i0 + (int)threadIdx.x / 8;
     const unsigned long long mine = i < n ? sm.list[i] : 0ull;
     int above = 0;
     if (i < n)
 #pragma unroll 4
-      for (int j = e; j < n; j += sub) above += sm.list[j] > mine;
-    if (sub == 4) {
-      above += __shfl_xor_sync(0xffffffffu, above, 1);
-      above += __shfl_xor_sync(0xffffffffu, above, 2);
-    }
-    if (i < n && e == 0 && above < k) sm.sel[above] = mine;
+      for (int j = threadIdx.x % 8; j < n; j += 8) above += sm.list[j] > mine;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (i < n && threadIdx.x % 8 == 0 && above < k) sm.sel[above] = mine;
   }
   __syncthreads();
 }
@@ -245,24 +309,35 @@ __device__ __forceinline__ unsigned long long lp_pair(unsigned key, int col) {
   return ((unsigned long long)key << 32) | (0xffffffffu - (unsigned)col);
 }
 
-// The row's results from its sums and (k > 0) its k best pairs in sm.sel.
+__device__ __forceinline__ long long lp_token_id(const LpArgs &a, int m, int c) {
+  const long long i = (long long)m * a.C + c;
+  return a.tok64 ? __ldg(reinterpret_cast<const long long *>(a.tokens) + i) : __ldg(reinterpret_cast<const int *>(a.tokens) + i);
+}
+// The logit of the row's given token c; NaN when there is no such token.
 template <typename T>
-__device__ __forceinline__ void lp_write(const LpArgs &a, int m, const T *row, const LpSum &z, const LpSmem &sm) {
+__device__ __forceinline__ float lp_token(const LpArgs &a, int m, const T *row, int c) {
+  const long long tok = lp_token_id(a, m, c);
+  if (tok >= 0 && tok < a.N) return lp_float(row[tok]);
+  atomicCAS(a.err, 0, -9);
+  return __uint_as_float(0x7fc00000u);
+}
+// The row's results from its sums and (k > 0) its k best pairs in sm.sel; xtok: token
+// threadIdx.x's logit, where `given`.
+template <typename T>
+__device__ __forceinline__ void lp_write(const LpArgs &a, int m, const T *row, const LpSum &z, const LpSmem &sm, bool given,
+                                         float xtok) {
   const float ls = log2f(z.s);
   const bool none = z.s == 0.0f;                  // every logit -inf
   if (threadIdx.x == 0) {
     a.lse[m] = none ? -INFINITY : (z.r + ls) * kLn2;
     a.entropy[m] = none ? 0.0f : fmaxf(ls - z.t / z.s, z.s != z.s ? z.s : 0.0f) * kLn2;
   }
-  auto lp = [&](float x) { return none ? -INFINITY : (fmaf(x, kLog2e, -z.r) - ls) * kLn2; };
-  for (int c = threadIdx.x; c < a.C; c += kLpThreads) {
-    const long long i = (long long)m * a.C + c;
-    const long long tok = a.tok64 ? reinterpret_cast<const long long *>(a.tokens)[i] : reinterpret_cast<const int *>(a.tokens)[i];
-    float y = __uint_as_float(0x7fc00000u);       // no such token: NaN
-    if (tok >= 0 && tok < a.N) y = lp(lp_float(row[tok]));
-    else atomicCAS(a.err, 0, -9);
-    a.logprob[i] = y;
-  }
+  // (a token that does not exist stays NaN)
+  auto lp = [&](float x) { return none ? (x != x ? x : -INFINITY) : (fmaf(x, kLog2e, -z.r) - ls) * kLn2; };
+#pragma unroll 1
+  for (int c = threadIdx.x; c < a.C; c += kLpThreads)
+    a.logprob[(long long)m * a.C + c] = lp(given && c == (int)threadIdx.x ? xtok : lp_token<T>(a, m, row, c));
+#pragma unroll 1
   for (int i = threadIdx.x; i < a.k; i += kLpThreads) {
     const unsigned long long p = sm.sel[i];
     a.top_lp[(long long)m * a.k + i] = lp(key_value32((unsigned)(p >> 32)));
@@ -270,140 +345,240 @@ __device__ __forceinline__ void lp_write(const LpArgs &a, int m, const T *row, c
   }
 }
 
-template <typename T>
+// TOP: the k most likely are wanted too
+template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(const __grid_constant__ LpArgs a) {
   constexpr int VE = LpVec<T>::VE;
   __shared__ LpSmem sm;
-  const int S = gridDim.x, sl = blockIdx.x;
+  __shared__ float maxima[TOP ? kLpMaxima * kLpThreads : 1];
+  const int tid = threadIdx.x, me = blockIdx.x, nv = a.nv;
+  const long long span = nv + kLpRowCost;
+  long long begin = a.share * me, end = min(begin + a.share, span * a.M);
+  if (a.S > 0) {
+    const int r = me / a.S, u = (me - r * a.S) * a.step;
+    begin = r * span + kLpRowCost + u;
+    end = begin + min(a.step, nv - u);
+  }
   griddep_wait();
   griddep_launch_dependents();
-  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
+
+  // ---- the copies, a block of vectors ahead of the sums: row lm (its places from lat)
+  int lm = a.S > 0 ? me / a.S : (int)(begin / span);
+  long long lat = lm * span;
+  const int m0 = lm;
+  const uint8_t *lsrc = nullptr;                  // the row's 16-byte boundary
+  int lv = 0, lend = 0;
+  auto open = [&]() {                             // the whole vectors of the row that lie in the range
+    const LpRow<T> R(static_cast<const T *>(a.logits) + (long long)lm * a.row_stride, a.N);
+    lsrc = reinterpret_cast<const uint8_t *>(R.row) - R.pad * (int)sizeof(T);
+    lv = max((int)max(begin - lat - kLpRowCost, 0ll), R.in0);
+    lend = min((int)min(end - lat - kLpRowCost, (long long)nv), R.in1);
+  };
+  open();
+  auto fetch = [&](uint4 (&w)[kLpUnroll]) {
+    while (lv >= lend) {
+      lat += span;
+      if (lat + kLpRowCost >= end) return;
+      ++lm;
+      open();
+    }
+    const uint4 *src = reinterpret_cast<const uint4 *>(lsrc) + lv + tid;
+#pragma unroll
+    for (int i = 0; i < kLpUnroll; ++i)
+      if (lv + tid + i * kLpThreads < lend) w[i] = __ldg(src + i * kLpThreads);
+    lv += kLpBlock;
+    if (lv > lend) lv = lend;
+  };
+  uint4 w[kLpUnroll];
+  fetch(w);
+
+  long long at = m0 * span;
+  int m = m0;
+  long long tok = -1;
+  if (tid < a.C) tok = lp_token_id(a, m, tid);
+#pragma unroll 1
+  for (; at + kLpRowCost < end; ++m, at += span) {
+    const int u0 = (int)max(begin - at - kLpRowCost, 0ll), u1 = (int)min(end - at - kLpRowCost, (long long)nv);
     const T *row = static_cast<const T *>(a.logits) + (long long)m * a.row_stride;
     const LpRow<T> R(row, a.N);
-    const int v0 = min(sl * a.vps, R.nvec), v1 = min(v0 + a.vps, R.nvec);
-    LpSum z{kNoRef, 0.0f, 0.0f};
-    float top = -INFINITY, quarter[kLpUnroll];
-#pragma unroll
-    for (int i = 0; i < kLpUnroll; ++i) quarter[i] = -INFINITY;
-    const int w0 = max(v0, R.in0), w1 = min(v1, R.in1);
-    auto raise = [&](float x) {                   // a new largest element: the reference follows
-      if (x > top) {
-        top = x;
-        lp_move(z, x * kLog2e);
+    const int w0 = max(u0, R.in0), w1 = min(u1, R.in1);
+    // an element of the row's cut vectors, by a thread of its own (loaded ahead of its use):
+    // threads 0 .. those before the first whole vector, 32 .. those past the last
+    int ec = -1;
+    if (tid < VE) {
+      if (u0 == 0 && R.in0 > 0 && tid < min(VE - R.pad, R.N)) ec = tid;
+    } else if (tid >= 32 && tid < 32 + VE) {
+      if (u0 <= R.in1 && R.in1 < min(u1, R.nvec) && R.col(R.in1) + tid - 32 < R.N) ec = R.col(R.in1) + tid - 32;
+    }
+    const T ex0 = row[max(ec, 0)];
+    // the given tokens' logits likewise, thread c's token c of the row (the token itself was
+    // loaded a row ahead)
+    const bool known = tid < a.C && tok >= 0 && tok < a.N;
+    const T xt0 = row[known ? tok : 0];
+    if (tid < a.C && m + 1 < a.M) tok = lp_token_id(a, m + 1, tid);
+
+    // ---- the sums, over even and odd elements.  The reference starts at the largest of the
+    // warp's first blocks and moves when a block passes it by 2^4 (y stays below 4: nothing
+    // overflows, and little cancels in log2 s - t / s).
+    float top = -INFINITY, r = kNoRef;            // this thread's largest element
+    unsigned long long nr2 = 0ull, s2 = pair2(0.0f, 0.0f), t2 = s2;
+    const unsigned long long e2 = pair2(kLog2e, kLog2e);
+    auto raise = [&](float x) {
+      const float q = x * kLog2e;
+      if (q > r + 4.0f) {
+        const float d = r - q, f = lp_ex2(d);
+        t2 = mul2(fma2(pair2(d, d), s2, t2), pair2(f, f));
+        s2 = mul2(s2, pair2(f, f));
+        r = q;
+        nr2 = pair2(-q, -q);
       }
     };
-    auto add = [&](float x) {
-      const float y = max_nan(fmaf(x, kLog2e, -z.r), -150.0f);     // 2^-150 is 0; -inf stays out of y 2^y
-      const float p = lp_ex2(y);
-      z.s += p;
-      z.t = fmaf(y, p, z.t);
+    auto add = [&](float x0, float x1) {
+      const float2 y = both2(fma2(pair2(x0, x1), e2, nr2));
+      const float y0 = max_nan(y.x, -150.0f), y1 = max_nan(y.y, -150.0f);       // 2^-150 is 0; -inf stays out of y 2^y
+      const unsigned long long p2 = pair2(lp_ex2(y0), lp_ex2(y1));
+      s2 = add2(s2, p2);
+      t2 = fma2(pair2(y0, y1), p2, t2);
     };
-    // the elements of the row's cut vectors: thread 0 takes those of its slice, once
-    auto edges = [&](auto f) {
-      if (threadIdx.x != 0) return;
+    int g = 0;                                    // log2 of the blocks behind a kept maximum
+    if (TOP)
+      while ((w1 - w0 - 1) / kLpBlock >> g >= kLpMaxima) ++g;
+    float run = -INFINITY;
 #pragma unroll 1
-      for (int end = 0; end < 2; ++end) {
-        const int v = end ? R.in1 : 0;
-        if (v < v0 || v >= v1 || (end ? v >= R.nvec : R.in0 == 0) ) continue;
-#pragma unroll 1
-        for (int c = max(R.col(v), 0); c < min(R.col(v) + VE, R.N); ++c) f(lp_float(row[c]), c);
-      }
-    };
-#pragma unroll 1
-    for (int v = w0 + (int)threadIdx.x; v < w1; v += kLpUnroll * kLpThreads) {
-      uint4 w[kLpUnroll];
+    for (int v = w0, blk = 0; v < w1; v += kLpBlock, ++blk) {
+      uint4 x4[kLpUnroll];
+      fetch(x4);
+      float bm = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kLpUnroll; ++i)
-        if (v + i * kLpThreads < w1) w[i] = R.raw(v + i * kLpThreads);
-#pragma unroll
-      for (int i = 0; i < kLpUnroll; ++i) {
-        if (v + i * kLpThreads >= w1) break;
-        float x[VE];
-        lp_unpack<T>(w[i], x);
-        float vm = x[0];
-#pragma unroll
-        for (int e = 1; e < VE; ++e) vm = fmaxf(vm, x[e]);
-        quarter[i] = fmaxf(quarter[i], vm);
-        raise(vm);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) add(x[e]);
+        if (v + tid + i * kLpThreads < w1) bm = fmaxf(bm, lp_max<T>(w[i]));
+      top = fmaxf(top, bm);
+      if (TOP) {
+        run = (blk & ((1 << g) - 1)) == 0 ? bm : fmaxf(run, bm);
+        maxima[(blk >> g) * kLpThreads + tid] = run;
       }
+      if (blk == 0) {                             // (whole warp)
+        r = fmaxf(key_value32(__reduce_max_sync(0xffffffffu, order_key32(bm))) * kLog2e, kNoRef);
+        nr2 = pair2(-r, -r);
+      } else {
+        raise(bm);
+      }
+#pragma unroll
+      for (int i = 0; i < kLpUnroll; ++i)
+        if (v + tid + i * kLpThreads < w1) {
+          float x[VE];
+          lp_unpack<T>(w[i], x);
+#pragma unroll
+          for (int e = 0; e < VE; e += 2) add(x[e], x[e + 1]);
+        }
+#pragma unroll
+      for (int i = 0; i < kLpUnroll; ++i) w[i] = x4[i];
     }
-    edges([&](float x, int) {
-      raise(x);
-      add(x);
-    });
-    z = lp_block(z, sm);
-    if (a.k > 0) {
-      unsigned reach = 0u;                        // order keys of the quarters
-      const unsigned bound = lp_bound(w0 + (int)threadIdx.x < w1 ? order_key32(top) : 0u, min((w1 - w0) / 32, kLpWarps), a.k, sm);
+    const float ex1 = lp_float(ex0);
+    if (ec >= 0) {
+      raise(ex1);
+      add(ex1, -INFINITY);
+    }
+    const float2 ss = both2(s2), tt = both2(t2);
+    LpSum z = lp_block(LpSum{r, ss.x + ss.y, tt.x + tt.y}, sm);
+    if (TOP) {
+      const unsigned bound = lp_bound(w0 + tid < w1 ? order_key32(top) : 0u, min(max(w1 - w0, 0) / 32, kLpWarps), a.k, sm);
       lp_select((unsigned long long)bound << 32, a.k, sm, [&](unsigned long long B, auto put) {
         const unsigned key0 = (unsigned)(B >> 32);
-        reach = 0u;
-#pragma unroll
-        for (int i = 0; i < kLpUnroll; ++i) reach |= order_key32(quarter[i]) >= key0 ? 1u << i : 0u;
         auto offer = [&](float x, int c) {
           const unsigned long long p = lp_pair(order_key32(x), c);
           if (p >= B) put(p);
         };
+        // element e of kept maximum b: vector j of its 4 2^g, b = (first block >> g) threads + thread
+        auto element = [&](int b, int j, int e) {
+          const int v = w0 + (((b / kLpThreads) << g) * kLpUnroll + j) * kLpThreads + b % kLpThreads;
+          if (v < w1) offer(lp_float(row[R.col(v) + e]), R.col(v) + e);
+        };
+        const int kept = w0 < w1 ? ((w1 - w0 - 1) / kLpBlock >> g) + 1 : 0, eg = kLpLogUnroll + g;
+        if (tid == 0) sm.nblock = 0;
+        __syncthreads();
 #pragma unroll 1
-        for (int v = w0 + (int)threadIdx.x; v < w1 && reach; v += kLpUnroll * kLpThreads) {
-          uint4 w[kLpUnroll];
-#pragma unroll
-          for (int i = 0; i < kLpUnroll; ++i)
-            if (v + i * kLpThreads < w1 && (reach >> i & 1u)) w[i] = R.raw(v + i * kLpThreads);
-#pragma unroll 1
-          for (int i = 0; i < kLpUnroll; ++i) {
-            if (v + i * kLpThreads < w1 && (reach >> i & 1u)) {
-              float x[VE];
-              lp_unpack<T>(w[0], x);
-#pragma unroll
-              for (int e = 0; e < VE; ++e) offer(x[e], R.col(v + i * kLpThreads) + e);
-            }
-#pragma unroll
-            for (int j = 0; j + 1 < kLpUnroll; ++j) w[j] = w[j + 1];
+        for (int b = tid; b < kept * kLpThreads; b += kLpThreads)
+          if (w0 + (b / kLpThreads << g) * kLpBlock + tid < w1 && order_key32(maxima[b]) >= key0) {
+            const int i = atomicAdd(&sm.nblock, 1);
+            if (i < kLpBlocks) sm.block[i] = b;
           }
+        __syncthreads();
+        if (sm.nblock <= kLpBlocks) {             // a thread an element of a listed block
+#pragma unroll 4
+          for (int i = tid; i < (sm.nblock << eg) * VE; i += kLpThreads) {
+            const int q = i / VE;
+            element(sm.block[q >> eg], q & ((1 << eg) - 1), i % VE);
+          }
+        } else {                                  // many (equal logits): every thread its own
+#pragma unroll 1
+          for (int b = tid; b < kept * kLpThreads; b += kLpThreads)
+            if (order_key32(maxima[b]) >= key0) {
+#pragma unroll 1
+              for (int q = 0; q < VE << eg; ++q) element(b, q / VE, q % VE);
+            }
         }
-        edges(offer);
+        if (ec >= 0) offer(ex1, ec);
       });
     }
-    if (S > 1) {
-      // ---- publish; the last slice of the row joins
-      unsigned long long *cand = a.cand + (size_t)m * S * a.k;
-      if (threadIdx.x == 0) *reinterpret_cast<float4 *>(a.part + ((size_t)m * S + sl) * 4) = make_float4(z.r, z.s, z.t, 0.0f);
-      if ((int)threadIdx.x < a.k) cand[(size_t)sl * a.k + threadIdx.x] = sm.sel[threadIdx.x];
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const int old = atom_add_acq_rel_gpu(a.counters + m, 1);
-        sm.last = old == S - 1;
-        if (sm.last) a.counters[m] = 0;           // zero again for the next call
+    float xt = lp_float(xt0);
+    if (u0 > 0 || u1 < nv) {
+      // ---- a cut row: the last CTA to finish it joins its parts, in order
+      if (tid == 0) {
+        int c0 = me, c1 = me;
+        if (a.S > 0) {
+          c0 = m * a.S;
+          c1 = c0 + a.S - 1;
+        } else {
+          if (u0 > 0) c0 = (int)((at + kLpRowCost) / a.share);
+          if (u1 < nv) c1 = (int)((at + kLpRowCost + nv - 1) / a.share);
+        }
+        sm.first = c0;
+        sm.parts = c1 - c0 + 1;
+        *reinterpret_cast<float4 *>(a.part + (size_t)(2 * me + (c0 == me)) * 4) = make_float4(z.r, z.s, z.t, 0.0f);
       }
       __syncthreads();
-      if (!sm.last) continue;
-      __threadfence();
+      const int c0 = sm.first, parts = sm.parts;
+      auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)); };   // the first part: its CTA's slot 1
+      if (TOP && tid < a.k) a.cand[slot(me - c0) * a.k + tid] = sm.sel[tid];
+      __syncthreads();                            // (thread 0's release and acquire order every thread's accesses)
+      if (tid == 0) {
+        const int old = atom_add_acq_rel_gpu(a.counters + c0, 1);
+        sm.n = old == parts - 1;
+        if (sm.n) a.counters[c0] = 0;             // zero again for the next call
+      }
+      __syncthreads();
+      const bool last = sm.n != 0;
+      __syncthreads();
+      if (!last) continue;
       z = LpSum{kNoRef, 0.0f, 0.0f};
-      if ((int)threadIdx.x < S) {
-        const float4 q = __ldcg(reinterpret_cast<const float4 *>(a.part + ((size_t)m * S + threadIdx.x) * 4));
-        z = LpSum{q.x, q.y, q.z};
+      for (int i = tid; i < parts; i += kLpThreads) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(a.part + slot(i) * 4));
+        z = lp_join(z, LpSum{q.x, q.y, q.z});
       }
       z = lp_block(z, sm);
-      if (a.k > 0) {
-        const int total = S * a.k;
+      if (TOP) {
+        const int total = parts * a.k;
+        auto pair = [&](int i) {
+          const int q = i / a.k;
+          return __ldcg(a.cand + slot(q) * a.k + i - q * a.k);
+        };
         unsigned best = 0u;
-        for (int i = threadIdx.x; i < total; i += kLpThreads) best = max(best, (unsigned)(__ldcg(cand + i) >> 32));
+#pragma unroll 4
+        for (int i = tid; i < total; i += kLpThreads) best = max(best, (unsigned)(pair(i) >> 32));
         const unsigned bound = lp_bound(best, min(total / 32, kLpWarps), a.k, sm);
         lp_select((unsigned long long)bound << 32, a.k, sm, [&](unsigned long long B, auto put) {
           if (best < (unsigned)(B >> 32)) return;
-          for (int i = threadIdx.x; i < total; i += kLpThreads) {
-            const unsigned long long p = __ldcg(cand + i);
+#pragma unroll 4
+          for (int i = tid; i < total; i += kLpThreads) {
+            const unsigned long long p = pair(i);
             if (p >= B && p != 0ull) put(p);
           }
         });
       }
     }
-    lp_write<T>(a, m, row, z, sm);
-    __syncthreads();                              // sm free for the next row
+    lp_write<T>(a, m, row, z, sm, tid < a.C && known, xt);
+    __syncthreads();                              // sm is free for the next row
   }
 }
 
@@ -419,32 +594,36 @@ int bad(int code, const char *fmt, ...) {
 }
 bool at(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// Slices a row is cut into: enough CTAs to fill the SMs twice, but at least two
-// vectors a thread (a shorter slice costs more in the join than it saves).
-// (several slices only where M < 8 SMs: one counter a row)
-constexpr size_t kLpCounterBytes = 8192;
-constexpr int kLpFill = 8;                        // CTAs an SM to aim for
+// One range a CTA over the places of all rows; at least two blocks of vectors (fewer, and the
+// join costs a short call more than the CTAs save).
+constexpr size_t kLpCounterBytes = 8192;          // a counter a CTA, at a fixed place: calls of any shape share a workspace
 struct LpPlan {
-  int S, vps;
-  size_t counters, part, cand;
+  int grid, nv, S, step;
+  long long share;
+  size_t part, cand;
 };
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 LpPlan lp_plan(int M, int N, int es, int k, int sms) {
   LpPlan p{};
   const int ve = 16 / es;
-  const long long nvec = ((long long)N + ve - 1 + ve - 1) / ve;     // whatever the row's alignment
-  long long S = ((long long)kLpFill * sms + M - 1) / (M > 0 ? M : 1);
-  const long long most = (nvec + 2 * kLpThreads - 1) / (2 * kLpThreads);
-  if (S > most) S = most;
-  if (S > kLpMaxSlices) S = kLpMaxSlices;
-  if (S < 1) S = 1;
-  p.vps = (int)((nvec + S - 1) / S);
-  p.S = (int)((nvec + p.vps - 1) / p.vps);
-  if (p.S > 1) {
-    p.counters = kLpCounterBytes;      // a fixed place: calls of any M share a workspace
-    p.part = up((size_t)M * p.S * 16);
-    p.cand = up((size_t)M * p.S * k * 8);
+  p.nv = (int)(((long long)N + 2 * ve - 2) / ve); // whatever the row's alignment
+  const long long total = ((long long)p.nv + kLpRowCost) * M, most = (long long)kLpPerSm * sms;
+  p.share = (total + most - 1) / most;
+  if (p.share < kLpMinBlocks * kLpBlock) p.share = kLpMinBlocks * kLpBlock;
+  p.grid = (int)((total + p.share - 1) / p.share);
+  // Equal parts of each row instead, one a CTA, where a CTA of the ranges would finish two rows
+  // one after the other and that costs more than the CTAs left over (a row's end takes a CTA
+  // about as long as 700 vectors, 4000 with the top k).
+  const int end = k > 0 ? 4000 : 700;
+  long long S = most / M, fit = (p.nv + kLpMinBlocks * kLpBlock - 1) / (kLpMinBlocks * kLpBlock);
+  if (S > fit) S = fit;
+  if (S >= 1 && (p.nv + S - 1) / S + end <= p.share + 2 * end) {
+    p.step = (int)((p.nv + S - 1) / S);
+    p.S = (p.nv + p.step - 1) / p.step;
+    p.grid = p.S * M;
   }
+  p.part = up((size_t)p.grid * 2 * 16);
+  p.cand = up((size_t)p.grid * 2 * k * 8);
   return p;
 }
 int lp_shape(int M, int N, int C, int k, int dtype) {
@@ -466,12 +645,12 @@ size_t token_logprobs_workspace_bytes(int M, int N, int k, int dtype) {
   int sms = 0;
   if (lp_shape(M, N, 0, k, dtype) || M == 0 || device_info(&sms, nullptr)) return 0;
   const LpPlan p = lp_plan(M, N, dtype == QW_F32 ? 4 : 2, k, sms);
-  return p.counters + p.part + p.cand;
+  return kLpCounterBytes + p.part + p.cand;
 }
 size_t token_logprobs_workspace_zero_bytes(int M, int N, int k, int dtype) {
   int sms = 0;
   if (lp_shape(M, N, 0, k, dtype) || M == 0 || device_info(&sms, nullptr)) return 0;
-  return lp_plan(M, N, dtype == QW_F32 ? 4 : 2, k, sms).counters;
+  return kLpCounterBytes;
 }
 
 int token_logprobs(const void *logits, int dtype, int M, int N, long long row_stride, const void *tokens,
@@ -489,10 +668,10 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
   LpArgs a{};
   int sms = 0;
   if ((rc = device_info(&sms, &a.err))) return rc;
-  if ((size_t)kLpFill * sms * 4 > kLpCounterBytes) return bad(QW_ERR_ARCH, "more SMs than counters (%d)", sms);
   const LpPlan p = lp_plan(M, N, dtype == QW_F32 ? 4 : 2, k, sms);
-  const size_t need = p.counters + p.part + p.cand;
-  if (need > 0 && (!ws || ws_bytes < need))
+  const size_t need = kLpCounterBytes + p.part + p.cand;
+  if ((size_t)kLpPerSm * sms * 4 > kLpCounterBytes) return bad(QW_ERR_ARCH, "more SMs than counters (%d)", sms);
+  if ((!ws || ws_bytes < need))
     return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.logits = logits;
@@ -503,19 +682,23 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
   a.C = C;
   a.k = k;
   a.tok64 = token_bytes == 8;
-  a.vps = p.vps;
+  a.nv = p.nv;
+  a.share = p.share;
+  a.S = p.S;
+  a.step = p.step;
   a.logprob = logprob;
   a.entropy = entropy;
   a.lse = lse;
   a.top_lp = top_logprob;
   a.top_idx = top_idx;
   a.counters = reinterpret_cast<int *>(w);
-  a.part = reinterpret_cast<float *>(w + p.counters);
-  a.cand = reinterpret_cast<unsigned long long *>(w + p.counters + p.part);
-  const void *f = dtype == QW_F16    ? reinterpret_cast<const void *>(token_logprobs_kernel<__half>)
-                  : dtype == QW_BF16 ? reinterpret_cast<const void *>(token_logprobs_kernel<__nv_bfloat16>)
-                                     : reinterpret_cast<const void *>(token_logprobs_kernel<float>);
-  cudaError_t e = launch_pdl(f, dim3(p.S, M < 65535 ? M : 65535), dim3(kLpThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  a.part = reinterpret_cast<float *>(w + kLpCounterBytes);
+  a.cand = reinterpret_cast<unsigned long long *>(w + kLpCounterBytes + p.part);
+#define QW_LP(T) (k > 0 ? reinterpret_cast<const void *>(token_logprobs_kernel<T, true>) \
+                       : reinterpret_cast<const void *>(token_logprobs_kernel<T, false>))
+  const void *f = dtype == QW_F16 ? QW_LP(__half) : dtype == QW_BF16 ? QW_LP(__nv_bfloat16) : QW_LP(float);
+#undef QW_LP
+  cudaError_t e = launch_pdl(f, dim3(p.grid), dim3(kLpThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
   count_launch();
   if (e != cudaSuccess) return bad(QW_ERR_CUDA, "log probability kernel launch: %s", cudaGetErrorString(e));
   return QW_OK;
