@@ -19,7 +19,10 @@
 //     own ring of half stages (the K rows, then the V rows of a strip; cp.async, 16 bytes a
 //     thread; rows beyond the visible keys are zero-filled, not read) and waits only for
 //     itself: no CTA-wide barrier between the strips of a sequence.  For more than 16 columns
-//     the RW warps of a group share its strips, 16 columns each.
+//     the RW warps of a group share its strips, 16 columns each; where 16 columns of d = 256
+//     would fill a thread's registers, two warps halve the channels (of both products: the
+//     halves' scores meet in shared memory), which lets twelve warps hide each other's waits
+//     where six could not.
 //   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
 //     (sequence, column block, KV head) item are laid end to end and cut into one equal range
 //     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
@@ -69,31 +72,33 @@ struct PagedCtl {
   int part[16];
 };
 
-// Shapes.  NB: MMA column tiles (of 8) a warp; RW: warps a group (column blocks of 8 NB RW).
-// The warps a CTA has are what the registers allow: accumulators take D NB / 4 registers a
-// thread and the Q fragments D NB / 8 more (in shared memory where D NB = 512).
+// Shapes.  NB: MMA column tiles (of 8) a warp; RW: warps a group side by side (column blocks of
+// 8 NB RW); DS: warps that share the channels.  The warps a CTA has are what the registers
+// allow: accumulators take D NB / 4 / DS registers a thread and the Q fragments half of that.
 template <int D, int KV, int NB, int RW>
 struct PagedShape {
   static constexpr int kES = KV == kPagedI8 ? 1 : 2;
-  static constexpr int kMaxWarps = D * NB == 512 ? 8 : D * NB == 256 ? 12 : 16;
-  static constexpr int kKW = kMaxWarps / RW;
-  static constexpr int kWarps = RW * kKW;
+  static constexpr int kDS = D * NB == 512 ? 2 : 1;
+  static constexpr int kGW = RW * kDS;                 // warps a group
+  static constexpr int kMaxWarps = D * NB >= 256 ? 12 : 16;
+  static constexpr int kKW = kMaxWarps / kGW;
+  static constexpr int kWarps = kGW * kKW;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCols = 8 * NB;                 // columns a warp
   static constexpr int kRows = kCols * RW;             // columns a CTA takes at a time
   static constexpr int kRowBytes = D * kES;
   static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
-  static constexpr bool kQRegs = D * NB <= 256;
-  static constexpr int kQBytes = kQRegs ? 0 : kRows * D * 2;
-  // the exchange at an item's end: SW channels at a time, rows of SW + 4 floats (column pairs
-  // 2 c and channels r8 of a warp's lanes fall on distinct banks)
+  // the exchange at an item's end: SW channels of each warp at a time, rows of SW + 4 floats
+  // (column pairs 2 c and channels r8 of a warp's lanes fall on distinct banks); in between it
+  // holds the halves' scores
   static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
   static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
-  static constexpr int kFixed = kQBytes + kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
+  static_assert(kDS == 1 || kWarps * NB * 512 <= kRedBytes, "room for the scores");
+  static constexpr int kFixed = kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
   static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
-  static constexpr int kRing = kFit > 8 ? 8 : kFit;    // half stages a group
+  static constexpr int kRing = kFit > 12 ? 12 : kFit;  // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
-  static_assert(kRing >= (RW > 1 ? 3 : 2), "K and V of a strip in flight");
+  static_assert(kRing >= (kGW > 1 ? 3 : 2), "K and V of a strip in flight");
   // what an item costs beside its strips (its Q, the join of the groups: about 1.5 us, in
   // which an SM reads some 64 KB), in strips
   static constexpr int kItemCost = 65536 / (2 * kStrip * kRowBytes);
@@ -184,9 +189,10 @@ __device__ __noinline__ bool strip_nonfinite(uint32_t vst, int lane) {
 }
 // acc += V^T P^T of one strip over the visible keys alone (score above -inf), term by term.
 // pk[nb][h]: the packed weights of keys r8 + 8 h and columns 2 c4, 2 c4 + 1; s: their scores.
-template <int D, int NB, bool BF>
-__device__ __forceinline__ void add_visible(float (&acc)[D / 16][NB][4], const uint32_t (&pk)[NB][2],
-                                            const float (&s)[NB][4], uint32_t vst, int lane) {
+// n0: the warp's first chunk of 8 channels.
+template <int D, int DT, int NB, bool BF>
+__device__ __forceinline__ void add_visible(float (&acc)[DT][NB][4], const uint32_t (&pk)[NB][2],
+                                            const float (&s)[NB][4], uint32_t vst, int n0, int lane) {
   const int c4 = lane & 3, r8 = lane >> 2;
 #pragma unroll 1
   for (int j = 0; j < kStrip; ++j) {
@@ -199,9 +205,9 @@ __device__ __forceinline__ void add_visible(float (&acc)[D / 16][NB][4], const u
       const float w0 = BF ? __uint_as_float(pw << 16) : __half2float(__ushort_as_half((unsigned short)pw));
       const float w1 = BF ? __uint_as_float(pw & 0xffff0000u) : __half2float(__ushort_as_half((unsigned short)(pw >> 16)));
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {              // channel 8 n + r8: rows r8 (+ 8) of tile n / 2
+      for (int n = 0; n < 2 * DT; ++n) {             // channel 8 n + r8: rows r8 (+ 8) of tile n / 2
         unsigned short v;
-        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(vst + strip_off<D * 2>(j, n) + 2 * r8) : "memory");
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(vst + strip_off<D * 2>(j, n0 + n) + 2 * r8) : "memory");
         const float f = BF ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
         float(&a)[4] = acc[n / 2][nb];
         if (s0 != -INFINITY) a[2 * (n & 1)] = fmaf(w0, f, a[2 * (n & 1)]);
@@ -565,11 +571,11 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   constexpr bool BF = KV == kPagedBf16;
   constexpr bool I8 = KV == kPagedI8;
   constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
-  constexpr int R = P::kRing, SW = P::kSW;
+  constexpr int R = P::kRing, SW = P::kSW, DS = P::kDS, GW = P::kGW;
+  constexpr int DT = D / 16 / DS;                       // 16-channel tiles a warp
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *fixed = smem + R * KW * P::kHalf;
-  uint32_t *qsm = reinterpret_cast<uint32_t *>(fixed);                // [RW][D/16][32][NB][2] B fragments
-  float *red = reinterpret_cast<float *>(fixed + P::kQBytes);         // [KW][RW][COLS][SW + 4]
+  float *red = reinterpret_cast<float *>(fixed);                      // [KW][RW][DS][COLS][SW + 4]
   float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
   float *sm_l = sm_m + P::kWarps * COLS;
   long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * COLS);   // [ROWS]
@@ -577,7 +583,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   PagedCtl *ctl = reinterpret_cast<PagedCtl *>(segs + kPagedMaxSegs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rw = warp % RW, kw = warp / RW;
+  const int gi = warp % GW, kw = warp / GW, rw = gi / DS, dh = gi % DS;
   const int c4 = lane & 3, r8 = lane >> 2;
   uint8_t *ring = smem + kw * R * P::kHalf;                           // this group's half stages
   const uint32_t ring_s = smem_u32(ring);
@@ -585,13 +591,14 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   // this lane's row and half of the four matrices it addresses: K as keys x channels, V
   // transposed (channels x keys)
   const LaneOffs<RB> koff((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4), voff((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+  const uint32_t half = (uint32_t)(dh * (RB / 2));      // this warp's channels in a row (DS = 2: a multiple of 128 bytes)
 
   griddep_wait();
   griddep_launch_dependents();
 
   if (!paged_schedule<ROWS, P::kItemCost, P::kWarps>(a, segs, ctl)) return;       // whole CTA
 
-  float acc[D / 16][NB][4];
+  float acc[DT][NB][4];
   for (;;) {
     if (ctl->nseg == 0) {                                // the whole CTA
       __syncthreads();
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         }
         const uint8_t *base = lv ? a.v : a.k;
         if constexpr (I8)
-          if (rw == 0 && lane < 16)
+          if (gi == 0 && lane < 16)
             cp_async4(st + kStrip * RB + lane * 4, (lv ? a.vs : a.ks) + (soff >= 0 ? soff : 0), soff >= 0 ? 4u : 0u);
         constexpr int CH = RB / 16;                        // 16-byte chunks a row
         constexpr int RPI = 32 / CH;                       // rows a warp instruction covers
@@ -645,16 +652,16 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         const int lr = ln / CH, lc = ln % CH;
         if (plain) {                                       // rows at equal distances
           const long long o0 = __shfl_sync(0xffffffffu, off, 0);
-          const long long step = RPI * a.tok_stride * P::kES;
-          const uint8_t *src = base + o0 + lr * a.tok_stride * P::kES + lc * 16;
+          const long long step = GW * RPI * a.tok_stride * P::kES;
+          const uint8_t *src = base + o0 + (gi * RPI + lr) * a.tok_stride * P::kES + lc * 16;
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            if (NI >= RW ? (i % RW == rw) : (i == rw)) cp_async16_full(st + strip_off<RB>(i * RPI + lr, lc), src);
+          for (int i = 0; i < (NI + GW - 1) / GW; ++i) {
+            if (NI % GW == 0 || i * GW + gi < NI) cp_async16_full(st + strip_off<RB>((i * GW + gi) * RPI + lr, lc), src);
             src += step;
           }
         } else {
 #pragma unroll 1
-          for (int i = rw; i < NI; i += RW) {
+          for (int i = gi; i < NI; i += GW) {
             const int r = i * RPI + lr;
             const long long o = __shfl_sync(0xffffffffu, off, r);
             cp_async16(st + strip_off<RB>(r, lc), base + (o >= 0 ? o + lc * 16 : 0), o >= 0 ? 16u : 0u);
@@ -673,14 +680,14 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     };
     // One warp a group refills a buffer as soon as it has read it (R loads ahead); several
     // warps refill it after the next half's barrier (R - 1 ahead).
-    constexpr int kAhead = RW == 1 ? R : R - 1;
+    constexpr int kAhead = GW == 1 ? R : R - 1;
     int buf = 0;
     auto acquire = [&]() {                                 // the next half: its shared address
       cp_async_wait<kAhead - 1>();
-      if constexpr (RW == 1) {
+      if constexpr (GW == 1) {
         __syncwarp();
       } else {
-        named_bar_sync(1 + kw, 32 * RW);
+        named_bar_sync(1 + kw, 32 * GW);
         load_next();
       }
       const int b = buf;
@@ -688,7 +695,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       return b * P::kHalf;
     };
     auto release = [&]() {
-      if constexpr (RW == 1) {
+      if constexpr (GW == 1) {
         __syncwarp();
         load_next();
       }
@@ -697,49 +704,24 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     // ---- Q as B fragments: column r8 of tile nb, channels 2 c4, + 1, + 8, + 9 of each 16
     // (int8: 4 c4 .. 4 c4 + 3, the order in which the codes of a word are widened).  Loaded
     // while the item before is joined.
-    uint32_t qr[P::kQRegs ? D / 16 : 1][NB][2];
+    uint32_t qr[DT][NB][2];
     auto load_q = [&](const PagedSeg &g) {
       const int row0 = g.rb * ROWS;
-      if constexpr (P::kQRegs) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          // (a column past the last repeats the first: its sums are its own and unused)
-          const int gr = row0 + rw * COLS + nb * 8 + r8;
-          const int tok = gr < g.rows ? gr / a.G : 0, hd = gr < g.rows ? gr - tok * a.G : 0;
-          const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + (I8 ? 4 : 2) * c4;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            if constexpr (I8) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + ks * 16));
-              qr[ks][nb][0] = v.x;
-              qr[ks][nb][1] = v.y;
-            } else {
-              qr[ks][nb][0] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
-              qr[ks][nb][1] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8));
-            }
-          }
-        }
-      } else {
-        // thread: column tid % ROWS, words tid / ROWS, + NT / ROWS, .. of its D / 2
-        static_assert(NT % ROWS == 0, "whole columns");
-        constexpr int WS = NT / ROWS, NW = D / 2 / WS;
-        static_assert(D / 2 % WS == 0, "whole words");
-        const int col = tid % ROWS, gr = row0 + col;
+      for (int nb = 0; nb < NB; ++nb) {
+        // (a column past the last repeats the first: its sums are its own and unused)
+        const int gr = row0 + rw * COLS + nb * 8 + r8;
         const int tok = gr < g.rows ? gr / a.G : 0, hd = gr < g.rows ? gr - tok * a.G : 0;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(
-            a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head);
-        // fragment place of word w (channels 2 w, 2 w + 1): lane 4 (col % 8) + c, half h
-        uint32_t *dst = qsm + (((col / COLS) * (D / 16) * 32 + 4 * (col % 8)) * NB + col % COLS / 8) * 2;
+        const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + dh * (D / 2) + (I8 ? 4 : 2) * c4;
 #pragma unroll
-        for (int i0 = 0; i0 < NW; i0 += 8) {
-          uint32_t v[8];
-#pragma unroll
-          for (int i = 0; i < 8 && i0 + i < NW; ++i) v[i] = __ldg(src + tid / ROWS + (i0 + i) * WS);
-#pragma unroll
-          for (int i = 0; i < 8 && i0 + i < NW; ++i) {
-            const int w = tid / ROWS + (i0 + i) * WS, ks = w / 8, j = w % 8;
-            const int c = I8 ? j / 2 : j % 4, h = I8 ? j % 2 : j / 4;
-            dst[(ks * 32 + c) * NB * 2 + h] = v[i];
+        for (int ks = 0; ks < DT; ++ks) {
+          if constexpr (I8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + ks * 16));
+            qr[ks][nb][0] = v.x;
+            qr[ks][nb][1] = v.y;
+          } else {
+            qr[ks][nb][0] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16));
+            qr[ks][nb][1] = __ldg(reinterpret_cast<const uint32_t *>(src + ks * 16 + 8));
           }
         }
       }
@@ -752,7 +734,6 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
     for (int sg = 0; sg < nseg; ++sg) {
       const PagedSeg &g = segs[sg];
       const int row0 = g.rb * ROWS;
-      if constexpr (!P::kQRegs) __syncthreads();
       // positions of this lane's columns (-1: no such column)
       int pos[NB][2];
 #pragma unroll
@@ -762,9 +743,10 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           const int gr = row0 + rw * COLS + nb * 8 + 2 * c4 + e;
           pos[nb][e] = gr < g.rows ? g.pos0 + gr / a.G : -1;
         }
+      const bool idle = RW > 1 && row0 + rw * COLS >= g.rows;
       const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + ROWS) - 1) / a.G;
 #pragma unroll
-      for (int t = 0; t < D / 16; ++t)
+      for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -779,32 +761,29 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll 1
       for (int u = g.u0 + kw; u < g.u1; u += KW) {
         const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
+        if (idle) {                                       // no column: only its share of the copies
+          acquire();
+          release();
+          if constexpr (DS == 2) named_bar_sync(1 + kw, 32 * GW);
+          acquire();
+          release();
+          continue;
+        }
         // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
         constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
         float sp[CN][NB][4] = {};
         float ksc[2] = {a.scale_log2, a.scale_log2};
         {
           const int hb = acquire();
-          const uint32_t kst = ring_s + (uint32_t)hb;
+          const uint32_t kst = ring_s + (uint32_t)hb + half;
           if constexpr (!I8) {
             // A tile: matrices (keys 0-7, 8-15) x (channels 0-7, 8-15) of each 16
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
+            for (int ks = 0; ks < DT; ++ks) {
               uint32_t kf[4];
               ldsm4(kf, kst + koff(ks));
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                uint32_t b0, b1;
-                if constexpr (P::kQRegs) {
-                  b0 = qr[ks][nb][0];
-                  b1 = qr[ks][nb][1];
-                } else {
-                  const uint2 v = reinterpret_cast<const uint2 *>(qsm)[((rw * (D / 16) + ks) * 32 + lane) * NB + nb];
-                  b0 = v.x;
-                  b1 = v.y;
-                }
-                mma16816<BF>(sp[ks % CN][nb], kf, b0, b1);
-              }
+              for (int nb = 0; nb < NB; ++nb) mma16816<BF>(sp[ks % CN][nb], kf, qr[ks][nb][0], qr[ks][nb][1]);
             }
           } else {
             const float *sc = reinterpret_cast<const float *>(ring + hb + kStrip * RB);
@@ -812,7 +791,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
             ksc[1] *= sc[r8 + 8];
             // matrices: (keys 0-7, 8-15) x (channels 0-15, 16-31); a word holds four channels
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
+            for (int kk = 0; kk < DT / 2; ++kk) {
               uint32_t kf[4];
               ldsm4(kf, kst + koff(kk));
 #pragma unroll
@@ -820,18 +799,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
                 const uint32_t u0 = kf[2 * h] ^ 0x80808080u, u1 = kf[2 * h + 1] ^ 0x80808080u;
                 const uint32_t af[4] = {codes_f16<0x4140>(u0), codes_f16<0x4140>(u1), codes_f16<0x4342>(u0), codes_f16<0x4342>(u1)};
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                  uint32_t b0, b1;
-                  if constexpr (P::kQRegs) {
-                    b0 = qr[kk * 2 + h][nb][0];
-                    b1 = qr[kk * 2 + h][nb][1];
-                  } else {
-                    const uint2 v = reinterpret_cast<const uint2 *>(qsm)[((rw * (D / 16) + kk * 2 + h) * 32 + lane) * NB + nb];
-                    b0 = v.x;
-                    b1 = v.y;
-                  }
-                  mma16816<false>(sp[(kk * 2 + h) % CN][nb], af, b0, b1);
-                }
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<false>(sp[(kk * 2 + h) % CN][nb], af, qr[kk * 2 + h][nb][0], qr[kk * 2 + h][nb][1]);
               }
             }
           }
@@ -842,11 +811,29 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float x = sp[0][nb][e];
+            s[nb][e] = sp[0][nb][e];
 #pragma unroll
-            for (int i = 1; i < CN; ++i) x += sp[i][nb][e];
-            s[nb][e] = x * ksc[e >> 1];
+            for (int i = 1; i < CN; ++i) s[nb][e] += sp[i][nb][e];
           }
+        if constexpr (DS == 2) {
+          // the other half's scores (read before the values' barrier, written again after it)
+          float4 *xs = reinterpret_cast<float4 *>(red) + ((kw * RW + rw) * 2 * NB) * 32 + lane;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) xs[(dh * NB + nb) * 32] = make_float4(s[nb][0], s[nb][1], s[nb][2], s[nb][3]);
+          named_bar_sync(1 + kw, 32 * GW);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float4 o = xs[((dh ^ 1) * NB + nb) * 32];
+            s[nb][0] += o.x;
+            s[nb][1] += o.y;
+            s[nb][2] += o.z;
+            s[nb][3] += o.w;
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nb][e] *= ksc[e >> 1];
         const bool masked = key0 + kStrip - 1 > pmin ||
                             (a.window > 0 && key0 <= pmax - a.window && key0 + kStrip > a.sinks);
         if (masked) {
@@ -875,7 +862,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up |= s[nb][e] + lvs[e >> 1] > m[nb][e & 1] + 8.0f;
+          for (int e = 0; e < 4; ++e) up |= (I8 ? s[nb][e] + lvs[e >> 1] : s[nb][e]) > m[nb][e & 1] + 8.0f;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -891,7 +878,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
               }
               l[nb][e] *= f;
 #pragma unroll
-              for (int t = 0; t < D / 16; ++t) {
+              for (int t = 0; t < DT; ++t) {
                 acc[t][nb][e] *= f;
                 acc[t][nb][2 + e] *= f;
               }
@@ -928,13 +915,13 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           pf[nb][1] = movm_t(pk[nb][1]);
         }
         if (!I8 && odd) {
-          if constexpr (!I8) add_visible<D, NB, BF>(acc, pk, s, vst, lane);
+          if constexpr (!I8) add_visible<D, DT, NB, BF>(acc, pk, s, vst, dh * 2 * DT, lane);
         } else if constexpr (!I8) {
           // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
+          for (int dt = 0; dt < DT; ++dt) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + voff(dt));
+            ldsm4_t(vf, vst + half + voff(dt));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) mma16816<BF>(acc[dt][nb], vf, pf[nb][0], pf[nb][1]);
           }
@@ -942,9 +929,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           // a transposed 16-bit element holds two channels: rows 0-7 of tile dt are the even
           // channels of its 16, rows 8-15 the odd ones
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
+          for (int kk = 0; kk < DT / 2; ++kk) {
             uint32_t vf[4];
-            ldsm4_t(vf, vst + voff(kk));
+            ldsm4_t(vf, vst + half + voff(kk));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t u0 = vf[h] ^ 0x80808080u, u1 = vf[2 + h] ^ 0x80808080u;
@@ -958,15 +945,14 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       }
 
       // ---- join the CTA's groups: out rows, or partial sums of a cut item
-      if constexpr (P::kQRegs)
-        if (sg + 1 < nseg) load_q(segs[sg + 1]);
+      if (sg + 1 < nseg) load_q(segs[sg + 1]);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
-          if (r8 == 0) {
+          if (r8 == 0 && dh == 0) {
             sm_m[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = m[nb][e];
             sm_l[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = l[nb][e];
           }
@@ -1004,11 +990,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         }
       }
       __syncthreads();
-      if constexpr (!P::kQRegs)
-        if (sg + 1 < nseg) load_q(segs[sg + 1]);
       if (tid < nrows) sm_l[tid] = L == 0.0f ? 0.0f : 1.0f / L;      // no key: a row of zeros
 #pragma unroll
-      for (int sl = 0; sl < D / SW; ++sl) {
+      for (int sl = 0; sl < 16 * DT / SW; ++sl) {
         float *w = red + warp * COLS * (SW + 4);
 #pragma unroll
         for (int t = 0; t < SW / 16; ++t)
@@ -1028,16 +1012,16 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           }
         __syncthreads();
 #pragma unroll 1
-        for (int i = tid; i < nrows * (SW / 2); i += NT) {
-          const int r = i / (SW / 2), cp = i % (SW / 2);
+        for (int i = tid; i < nrows * (DS * SW / 2); i += NT) {
+          const int r = i / (DS * SW / 2), hc = i % (DS * SW / 2) / (SW / 2), cp = i % (SW / 2);
           float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int w2 = 0; w2 < KW; ++w2) {
-            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * RW + r / COLS) * COLS + r % COLS) * (SW + 4) + 2 * cp);
+            const float2 v = *reinterpret_cast<const float2 *>(red + (((w2 * RW + r / COLS) * DS + hc) * COLS + r % COLS) * (SW + 4) + 2 * cp);
             o.x += v.x;
             o.y += v.y;
           }
-          const int col = SW * sl + 2 * cp;
+          const int col = hc * (D / 2) + SW * sl + 2 * cp;
           if (cut) {
             *reinterpret_cast<float2 *>(part + 2 * ROWS + (size_t)r * D + col) = o;
           } else {
