@@ -18,11 +18,14 @@
 //   - A CTA owns an SM.  Each of its KW groups streams its own strips of 16 keys through its
 //     own ring of half stages (the K rows, then the V rows of a strip; cp.async, 16 bytes a
 //     thread; rows beyond the visible keys are zero-filled, not read) and waits only for
-//     itself: no CTA-wide barrier between the strips of a sequence.  For more than 16 columns
-//     the RW warps of a group share its strips, 16 columns each; where 16 columns of d = 256
-//     would fill a thread's registers, two warps halve the channels (of both products: the
-//     halves' scores meet in shared memory), which lets twelve warps hide each other's waits
-//     where six could not.
+//     itself: no CTA-wide barrier between the strips of a sequence.  A group is one warp, but
+//     where 16 columns of d = 256 would fill a thread's registers, two warps halve the channels
+//     (of both products: the halves' scores meet in shared memory), which lets twelve warps
+//     hide each other's waits where six could not.
+//   - More than 16 columns are taken in blocks of 16, as items of their own: the blocks of a
+//     sequence run at about the same time and find its keys in L2.  (Groups of two to four
+//     warps with 16 columns each, reading a strip once for all of them, took 188 to 421 us
+//     where this takes 184: 16 sequences of up to 16384, 6 to 36 columns, d = 256.)
 //   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
 //     (sequence, column block, KV head) item are laid end to end and cut into one equal range
 //     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
@@ -72,29 +75,27 @@ struct PagedCtl {
   int part[16];
 };
 
-// Shapes.  NB: MMA column tiles (of 8) a warp; RW: warps a group side by side (column blocks of
-// 8 NB RW); DS: warps that share the channels.  The warps a CTA has are what the registers
-// allow: accumulators take D NB / 4 / DS registers a thread and the Q fragments half of that.
-template <int D, int KV, int NB, int RW>
+// Shapes.  NB: MMA column tiles (of 8) a warp; GW: warps of a group, which share the channels.
+// The warps a CTA has are what the registers allow: accumulators take D NB / 4 / GW registers a
+// thread and the Q fragments half of that.
+template <int D, int KV, int NB>
 struct PagedShape {
   static constexpr int kES = KV == kPagedI8 ? 1 : 2;
-  static constexpr int kDS = D * NB == 512 ? 2 : 1;
-  static constexpr int kGW = RW * kDS;                 // warps a group
+  static constexpr int kGW = D * NB == 512 ? 2 : 1;
   static constexpr int kMaxWarps = D * NB >= 256 ? 12 : 16;
   static constexpr int kKW = kMaxWarps / kGW;
   static constexpr int kWarps = kGW * kKW;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCols = 8 * NB;                 // columns a warp
-  static constexpr int kRows = kCols * RW;             // columns a CTA takes at a time
+  static constexpr int kRows = 8 * NB;                 // columns of an item
   static constexpr int kRowBytes = D * kES;
   static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
   // the exchange at an item's end: SW channels of each warp at a time, rows of SW + 4 floats
   // (column pairs 2 c and channels r8 of a warp's lanes fall on distinct banks); in between it
   // holds the halves' scores
-  static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
-  static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
-  static_assert(kDS == 1 || kWarps * NB * 512 <= kRedBytes, "room for the scores");
-  static constexpr int kFixed = kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
+  static constexpr int kSW = D == 64 || kWarps * kRows * 68 * 4 <= 28 * 1024 ? 64 : 32;
+  static constexpr int kRedBytes = kWarps * kRows * (kSW + 4) * 4;
+  static_assert(kGW == 1 || kWarps * NB * 512 <= kRedBytes, "room for the scores");
+  static constexpr int kFixed = kRedBytes + 2 * kWarps * kRows * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
   static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
   static constexpr int kRing = kFit > 12 ? 12 : kFit;  // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
@@ -482,9 +483,9 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
 }
 
 // Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
-template <int D, int KV, int NB, int RW>
+template <int D, int KV, int NB>
 __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g, float *red) {
-  using P = PagedShape<D, KV, NB, RW>;
+  using P = PagedShape<D, KV, NB>;
   constexpr int NT = P::kThreads, ROWS = P::kRows;
   constexpr bool BF = KV == kPagedBf16;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -564,26 +565,26 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
   }
 }
 
-template <int D, int KV, int NB, int RW>
-__global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
+template <int D, int KV, int NB>
+__global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
     attn_paged_kernel(const __grid_constant__ PagedArgs a) {
-  using P = PagedShape<D, KV, NB, RW>;
+  using P = PagedShape<D, KV, NB>;
   constexpr bool BF = KV == kPagedBf16;
   constexpr bool I8 = KV == kPagedI8;
-  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
-  constexpr int R = P::kRing, SW = P::kSW, DS = P::kDS, GW = P::kGW;
-  constexpr int DT = D / 16 / DS;                       // 16-channel tiles a warp
+  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, RB = P::kRowBytes;
+  constexpr int R = P::kRing, SW = P::kSW, GW = P::kGW;
+  constexpr int DT = D / 16 / GW;                       // 16-channel tiles a warp
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *fixed = smem + R * KW * P::kHalf;
-  float *red = reinterpret_cast<float *>(fixed);                      // [KW][RW][DS][COLS][SW + 4]
+  float *red = reinterpret_cast<float *>(fixed);                      // [KW][GW][ROWS][SW + 4]
   float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
-  float *sm_l = sm_m + P::kWarps * COLS;
-  long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * COLS);   // [ROWS]
+  float *sm_l = sm_m + P::kWarps * ROWS;
+  long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * ROWS);   // [ROWS]
   PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_row + ROWS);
   PagedCtl *ctl = reinterpret_cast<PagedCtl *>(segs + kPagedMaxSegs);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gi = warp % GW, kw = warp / GW, rw = gi / DS, dh = gi % DS;
+  const int gi = warp % GW, kw = warp / GW;             // place in its group, group
   const int c4 = lane & 3, r8 = lane >> 2;
   uint8_t *ring = smem + kw * R * P::kHalf;                           // this group's half stages
   const uint32_t ring_s = smem_u32(ring);
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   // this lane's row and half of the four matrices it addresses: K as keys x channels, V
   // transposed (channels x keys)
   const LaneOffs<RB> koff((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4), voff((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
-  const uint32_t half = (uint32_t)(dh * (RB / 2));      // this warp's channels in a row (DS = 2: a multiple of 128 bytes)
+  const uint32_t half = (uint32_t)(gi * (RB / 2));      // this warp's channels in a row (GW = 2: a multiple of 128 bytes)
 
   griddep_wait();
   griddep_launch_dependents();
@@ -710,9 +711,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // (a column past the last repeats the first: its sums are its own and unused)
-        const int gr = row0 + rw * COLS + nb * 8 + r8;
+        const int gr = row0 + nb * 8 + r8;
         const int tok = gr < g.rows ? gr / a.G : 0, hd = gr < g.rows ? gr - tok * a.G : 0;
-        const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + dh * (D / 2) + (I8 ? 4 : 2) * c4;
+        const uint16_t *src = a.q + (long long)(g.tok0 + tok) * a.q_tok + (long long)(g.g * a.G + hd) * a.q_head + gi * (D / 2) + (I8 ? 4 : 2) * c4;
 #pragma unroll
         for (int ks = 0; ks < DT; ++ks) {
           if constexpr (I8) {
@@ -740,10 +741,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int gr = row0 + rw * COLS + nb * 8 + 2 * c4 + e;
+          const int gr = row0 + nb * 8 + 2 * c4 + e;
           pos[nb][e] = gr < g.rows ? g.pos0 + gr / a.G : -1;
         }
-      const bool idle = RW > 1 && row0 + rw * COLS >= g.rows;
       const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + ROWS) - 1) / a.G;
 #pragma unroll
       for (int t = 0; t < DT; ++t)
@@ -761,14 +761,6 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll 1
       for (int u = g.u0 + kw; u < g.u1; u += KW) {
         const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
-        if (idle) {                                       // no column: only its share of the copies
-          acquire();
-          release();
-          if constexpr (DS == 2) named_bar_sync(1 + kw, 32 * GW);
-          acquire();
-          release();
-          continue;
-        }
         // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
         constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
         float sp[CN][NB][4] = {};
@@ -815,15 +807,15 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
 #pragma unroll
             for (int i = 1; i < CN; ++i) s[nb][e] += sp[i][nb][e];
           }
-        if constexpr (DS == 2) {
+        if constexpr (GW == 2) {
           // the other half's scores (read before the values' barrier, written again after it)
-          float4 *xs = reinterpret_cast<float4 *>(red) + ((kw * RW + rw) * 2 * NB) * 32 + lane;
+          float4 *xs = reinterpret_cast<float4 *>(red) + kw * 2 * NB * 32 + lane;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) xs[(dh * NB + nb) * 32] = make_float4(s[nb][0], s[nb][1], s[nb][2], s[nb][3]);
+          for (int nb = 0; nb < NB; ++nb) xs[(gi * NB + nb) * 32] = make_float4(s[nb][0], s[nb][1], s[nb][2], s[nb][3]);
           named_bar_sync(1 + kw, 32 * GW);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const float4 o = xs[((dh ^ 1) * NB + nb) * 32];
+            const float4 o = xs[((gi ^ 1) * NB + nb) * 32];
             s[nb][0] += o.x;
             s[nb][1] += o.y;
             s[nb][2] += o.z;
@@ -915,7 +907,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           pf[nb][1] = movm_t(pk[nb][1]);
         }
         if (!I8 && odd) {
-          if constexpr (!I8) add_visible<D, DT, NB, BF>(acc, pk, s, vst, dh * 2 * DT, lane);
+          if constexpr (!I8) add_visible<D, DT, NB, BF>(acc, pk, s, vst, gi * 2 * DT, lane);
         } else if constexpr (!I8) {
           // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
@@ -952,9 +944,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
-          if (r8 == 0 && dh == 0) {
-            sm_m[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = m[nb][e];
-            sm_l[kw * ROWS + rw * COLS + nb * 8 + 2 * c4 + e] = l[nb][e];
+          if (r8 == 0 && gi == 0) {
+            sm_m[kw * ROWS + nb * 8 + 2 * c4 + e] = m[nb][e];
+            sm_l[kw * ROWS + nb * 8 + 2 * c4 + e] = l[nb][e];
           }
         }
       __syncthreads();                                   // also: Q is no longer read
@@ -965,7 +957,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + rw * COLS + nb * 8 + 2 * c4 + e]);
+          for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + nb * 8 + 2 * c4 + e]);
           f[nb][e] = m[nb][e] == -INFINITY ? 0.0f : paged_ex2(m[nb][e] - M);
         }
       const bool cut = g.c0 != g.c1;
@@ -993,7 +985,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
       if (tid < nrows) sm_l[tid] = L == 0.0f ? 0.0f : 1.0f / L;      // no key: a row of zeros
 #pragma unroll
       for (int sl = 0; sl < 16 * DT / SW; ++sl) {
-        float *w = red + warp * COLS * (SW + 4);
+        float *w = red + warp * ROWS * (SW + 4);
 #pragma unroll
         for (int t = 0; t < SW / 16; ++t)
 #pragma unroll
@@ -1012,12 +1004,12 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
           }
         __syncthreads();
 #pragma unroll 1
-        for (int i = tid; i < nrows * (DS * SW / 2); i += NT) {
-          const int r = i / (DS * SW / 2), hc = i % (DS * SW / 2) / (SW / 2), cp = i % (SW / 2);
+        for (int i = tid; i < nrows * (GW * SW / 2); i += NT) {
+          const int r = i / (GW * SW / 2), hc = i % (GW * SW / 2) / (SW / 2), cp = i % (SW / 2);
           float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int w2 = 0; w2 < KW; ++w2) {
-            const float2 v = *reinterpret_cast<const float2 *>(red + (((w2 * RW + r / COLS) * DS + hc) * COLS + r % COLS) * (SW + 4) + 2 * cp);
+            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * GW + hc) * ROWS + r) * (SW + 4) + 2 * cp);
             o.x += v.x;
             o.y += v.y;
           }
@@ -1052,29 +1044,24 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, RW>::kThreads, 1)
   }
   // ---- the cut items that this CTA was the last to finish
   __syncthreads();
-  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB, RW>(a, ctl->join[i], red);
+  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB>(a, ctl->join[i], red);
 }
 
-template <int D, int KV, int NB, int RW>
+template <int D, int KV, int NB>
 cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
-  using P = PagedShape<D, KV, NB, RW>;
-  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, NB, RW>);
+  using P = PagedShape<D, KV, NB>;
+  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, NB>);
   cudaError_t e = ensure_smem_attr(f, P::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(f, dim3(sms), dim3(P::kThreads), P::kSmem, st, a);
   count_launch();
   return e;
 }
-// cols: the columns a CTA takes at a time (paged_columns)
+// cols: the columns of an item, 8 or 16 (paged_columns)
 template <int KV>
 cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
-#define QW_PAGED(DD)                                                      \
-  case DD:                                                                \
-    return cols == 8    ? paged_launch_one<DD, KV, 1, 1>(a, sms, st)      \
-           : cols == 16 ? paged_launch_one<DD, KV, 2, 1>(a, sms, st)      \
-           : cols == 32 ? paged_launch_one<DD, KV, 2, 2>(a, sms, st)      \
-           : cols == 48 ? paged_launch_one<DD, KV, 2, 3>(a, sms, st)      \
-                        : paged_launch_one<DD, KV, 2, 4>(a, sms, st);
+#define QW_PAGED(DD) \
+  case DD: return cols == 8 ? paged_launch_one<DD, KV, 1>(a, sms, st) : paged_launch_one<DD, KV, 2>(a, sms, st);
   switch (d) {
     QW_PAGED(64)
     QW_PAGED(128)

@@ -239,13 +239,9 @@ const void *append_kernel(int d) {
                     : reinterpret_cast<const void *>(kv_append_kernel<256, I8>);
 }
 
-// ---- attention: the query columns a CTA takes at a time, and the workspace for them
-// The fewest that hold a step's columns (new tokens x heads a KV head), so that K and V are
-// read once for all of a sequence's columns.
-int paged_columns(int max_new, int G) {
-  const long long n = (long long)max_new * G;
-  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 48 ? 48 : 64;
-}
+// ---- attention: the query columns of an item, and the workspace for them.  Eight where a
+// step's columns (new tokens x heads a KV head) fit (half the MMAs of 16), else blocks of 16.
+int paged_columns(int max_new, int G) { return (long long)max_new * G <= 8 ? 8 : 16; }
 constexpr size_t kPagedCounterBytes = 4096;      // one counter a CTA
 size_t paged_ws(int d, int cols, int sms) {
   return kPagedCounterBytes + (size_t)2 * sms * cols * (d + 2) * 4;
