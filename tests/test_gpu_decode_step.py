@@ -1,0 +1,69 @@
+"""The cache's operators together, as examples/decode_step.py runs them: the same logits
+whichever way a sequence's tokens entered the cache (a prompt at once, token by token, a
+verify step, after a fork with copy on write, after a compaction)."""
+import os
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def ex():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import decode_step
+    yield decode_step
+    sys.path.remove(os.path.join(ROOT, "examples"))
+
+
+def near(a, b, cache):
+    """Both come from fp16 layers whose GEMMs and attention may sum in another order: a step
+    (2^-10) at each of the 5 roundings of two layers, on the scale of the largest logit; with
+    the int8 cache such a step can also move a code, 1 / 127 of its row's largest value, in a
+    few of the values that a weight averages: four times that."""
+    a, b = a.float(), b.float()
+    steps = 2 * 5 * (4 if cache == "int8" else 1)
+    return float((a - b).abs().max()) <= steps * 2.0 ** -10 * float(b.abs().max())
+
+
+@pytest.mark.parametrize("cache", ["fp16", "int8"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 3)])
+def test_one_sequence_many_ways(ex, cache, window, sinks):
+    toks = [(53 * i + 7) % 1024 for i in range(50)]
+    m = ex.Decoder(cache=cache)
+    a = m.pool.add()
+    whole = m.step([a], [toks], window, sinks)                       # the prompt at once
+    b = m.pool.add()
+    single = torch.cat([m.step([b], [[t]], window, sinks) for t in toks])
+    assert near(single, whole, cache)
+    c = m.pool.add()
+    m.step([c], [toks[:37]], window, sinks)
+    verify = m.step([c], [toks[37:43]], window, sinks)               # six tokens, then four rejected
+    assert near(verify, whole[37:43], cache)
+    m.pool.truncate(c, 39)
+    f = m.pool.fork(c)                                               # shares a partly filled page
+    two = m.step([c, f], [toks[39:41], [999]], window, sinks)
+    assert near(two[:2], whole[39:41], cache)
+    m.pool.free(a)
+    m.pool.free(b)
+    m.pool.free(f)
+    before = {s: m.pool.table([s])[0].tolist() for s in (c,)}
+    m.compact()
+    assert m.pool.table([c])[0].tolist() != before[c]
+    rest = m.step([c], [toks[41:]], window, sinks)
+    assert near(rest, whole[41:], cache)
+
+
+@pytest.mark.parametrize("cache", ["fp16", "int8"])
+def test_example_runs(ex, cache, capsys):
+    model, out, logits = ex.main(cache)
+    assert len(out) == 4 and all(len(o) == 24 for o in out) and len({o[0] for o in out}) == 4
+    assert torch.isfinite(logits.float()).all() and logits.shape == (2, model.vocab)
+    assert "verify" in capsys.readouterr().out
