@@ -100,9 +100,10 @@ struct PagedShape {
   static constexpr int kRing = kFit > 12 ? 12 : kFit;  // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
   static_assert(kRing >= (kGW > 1 ? 3 : 2), "K and V of a strip in flight");
-  // what an item costs beside its strips (its Q, the join of the groups: about 1.5 us, in
-  // which an SM reads some 64 KB), in strips
-  static constexpr int kItemCost = 65536 / (2 * kStrip * kRowBytes);
+  // What an item costs beside its strips, in strips: the groups that wait for the last one, its
+  // join and the next Q take an SM about the time of 192 KB (64 x 8k bf16: 202 us with 64 KB,
+  // 196 with 128, 193 with 192, 188 with 256; 4 x 128k int8: 119, 117, 117, 124).
+  static constexpr int kItemCost = 196608 / (2 * kStrip * kRowBytes);
   static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 };
 

@@ -406,11 +406,11 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.sinks = window > 0 ? sinks : 0;
   a.strip_pages = c->page % 16 == 0;
   // every sequence's column blocks and their strips, were all contexts as long as the page
-  // table; up to 41 places more an item, and counts to spare
+  // table; up to 96 places more an item
   long long most = ((long long)T * a.G / cols + b->B) * c->Hkv;
   if (most > (1ll << 28)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   const long long blocks = most;
-  for (most = blocks * (a.cap / 16 + 64); most > (1ll << 30); most = blocks * ((a.cap / 16 >> a.shift) + 64)) {
+  for (most = blocks * (a.cap / 16 + 128); most > (1ll << 30); most = blocks * ((a.cap / 16 >> a.shift) + 128)) {
     if (++a.shift > 24) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   }
   a.min_places = 12;
