@@ -265,7 +265,11 @@ template <int ROWS>
 __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedSeq &s, int rb) {
   PagedSpan p;
   const int rows = s.nq * a.G, pos0 = s.len - s.nq;
-  const int t0 = paged_div(rb * ROWS, a.G), t1 = paged_div(min(rows, rb * ROWS + ROWS) - 1, a.G);
+  int t0 = 0, t1 = s.nq - 1;                            // its first and last token
+  if (rows > ROWS) {
+    t0 = paged_div(rb * ROWS, a.G);
+    t1 = paged_div(min(rows, rb * ROWS + ROWS) - 1, a.G);
+  }
   p.hi = max(pos0 + t1 + 1, 0);
   p.lo = a.window > 0 ? max(pos0 + t0 - a.window + 1, 0) : 0;
   p.first = p.lo / kStrip;
@@ -389,16 +393,25 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
       }
     };
     PagedSeq own{};                                     // per == 1: this thread's sequence
+    PagedSpan first{};                                  // and its first block's keys
     int mine = 0, items = 0;
 #pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) {
       own = paged_seq(a, b);
-      mine += cost(own);
-      items += blocks(own) * a.Hkv;
+      const int n = blocks(own);
+      if (n == 1) {
+        first = paged_span<ROWS>(a, own, 0);
+        mine += (paged_places(a, first.n) + IC) * a.Hkv;
+      } else {
+        mine += cost(own);
+      }
+      items += n * a.Hkv;
     }
+    auto span = [&](int rb) { return blocks(own) == 1 ? first : paged_span<ROWS>(a, own, rb); };
     int pre, total, dummy, all_items;
     scan(mine, pre, total);
-    scan(min(items, 1 << 16), dummy, all_items);
+    if (a.B > 32) scan(min(items, 1 << 16), dummy, all_items);
+    else all_items = __reduce_add_sync(0xffffffffu, min(items, 1 << 16));
     const int grid = gridDim.x, me = blockIdx.x;
     const int share = max(paged_div(total + grid - 1, grid), a.min_places);
     // strips a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
@@ -407,13 +420,13 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     if (size > 0 && size <= share + 2 * IC) {
       int parts = 0, pp;
 #pragma unroll 1
-      for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += paged_div(paged_span<ROWS>(a, own, rb).n + size - 1, size) * a.Hkv;
+      for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += paged_div(span(rb).n + size - 1, size) * a.Hkv;
       scan(parts, pp, dummy);
       if (me >= pp && me < pp + parts) {                // one thread, if any
         int at = pp;
 #pragma unroll 1
         for (int rb = 0, n = blocks(own); rb < n; ++rb) {
-          const PagedSpan p = paged_span<ROWS>(a, own, rb);
+          const PagedSpan p = span(rb);
           const int np = paged_div(p.n + size - 1, size);
           if (me < at + np * a.Hkv) {
             PagedSeg &g = segs[0];
@@ -438,7 +451,7 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
         if (per == 1) {
 #pragma unroll 1
           for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
-            const PagedSpan p = paged_span<ROWS>(a, own, rb);
+            const PagedSpan p = span(rb);
             const int each = paged_places(a, p.n) + IC;
             int head = begin > at ? min(paged_div(begin - at, each), a.Hkv) : 0;
             int x = at + head * each;
