@@ -22,10 +22,11 @@
 //     where 16 columns of d = 256 would fill a thread's registers, two warps halve the channels
 //     (of both products: the halves' scores meet in shared memory), which lets twelve warps
 //     hide each other's waits where six could not.
-//   - More than 16 columns are taken in blocks of 16, as items of their own: the blocks of a
-//     sequence run at about the same time and find its keys in L2.  (Groups of two to four
-//     warps with 16 columns each, reading a strip once for all of them, took 188 to 421 us
-//     where this takes 184: 16 sequences of up to 16384, 6 to 36 columns, d = 256.)
+//   - More than 16 columns are dealt to the groups in blocks of 16: the groups of different
+//     blocks stream the same strips at the same time, the first from HBM and the others from
+//     L2.  (As items of their own the blocks came too far apart: 5 % L2 hits and 170 us where
+//     this takes 154; groups of two to four warps with 16 columns each, reading a strip
+//     once for all of them, took 188 to 421: 16 sequences of up to 16384, 6 to 36 columns, d = 256.)
 //   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
 //     (sequence, column block, KV head) item are laid end to end and cut into one equal range
 //     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
@@ -55,7 +56,8 @@ constexpr int kStrip = 16;              // keys of a strip: the MMA's rows of S^
 constexpr int kPagedSmem = 227 * 1024;
 
 struct PagedSeg {
-  int b, g, rb;                 // sequence, KV head, column block
+  int b, g, rb;                 // sequence, KV head, block of kRows columns
+  int nblk;                     // blocks of kCols columns in it
   int u0, u1;                   // strips of the item [u0, u1)
   int nsu, first;               // strips of the sinks, strip of the first windowed key
   int lo, hi;                   // visible keys of the column block: [lo, hi) and below `sinks`
@@ -86,16 +88,20 @@ struct PagedShape {
   static constexpr int kKW = kMaxWarps / kGW;
   static constexpr int kWarps = kGW * kKW;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRows = 8 * NB;                 // columns of an item
+  static constexpr int kCols = 8 * NB;                 // columns a group
+  // columns of an item, at most (kernels of 8 are called for up to 8: then the blocks' logic is
+  // left out, 1 to 3 us a call)
+  static constexpr int kRows = NB == 1 ? kCols : 4 * kCols;
+  static_assert(kKW >= 4, "a group a block");
   static constexpr int kRowBytes = D * kES;
   static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
   // the exchange at an item's end: SW channels of each warp at a time, rows of SW + 4 floats
   // (column pairs 2 c and channels r8 of a warp's lanes fall on distinct banks); in between it
   // holds the halves' scores
-  static constexpr int kSW = D == 64 || kWarps * kRows * 68 * 4 <= 28 * 1024 ? 64 : 32;
-  static constexpr int kRedBytes = kWarps * kRows * (kSW + 4) * 4;
+  static constexpr int kSW = D == 64 || kWarps * kCols * 68 * 4 <= 28 * 1024 ? 64 : 32;
+  static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
   static_assert(kGW == 1 || kWarps * NB * 512 <= kRedBytes, "room for the scores");
-  static constexpr int kFixed = kRedBytes + 2 * kWarps * kRows * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
+  static constexpr int kFixed = kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
   static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
   static constexpr int kRing = kFit > 12 ? 12 : kFit;  // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
@@ -278,6 +284,12 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedS
   return p;
 }
 
+// Blocks of a group's columns in block rb of a sequence's `rows` columns.
+template <int ROWS>
+__device__ __forceinline__ int paged_blocks(int rows, int rb) {
+  return ROWS == 8 ? 1 : (min(rows - rb * ROWS, ROWS) + ROWS / 4 - 1) / (ROWS / 4);
+}
+template <int ROWS>
 __device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head,
                                           int G) {
   g.b = b;
@@ -289,24 +301,38 @@ __device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const
   g.hi = p.hi;
   g.pos0 = s.len - s.nq;
   g.rows = s.nq * G;
+  g.nblk = paged_blocks<ROWS>(g.rows, rb);
   g.tok0 = s.tok0;
 }
 
 
-// Places are counted in 2^shift strips (shift is 0 unless all keys of a call could pass 2^30
-// places): an item takes IC of them and paged_places(n) for its n strips.
-__device__ __forceinline__ int paged_places(const PagedArgs &a, int n) { return (n + (1 << a.shift) - 1) >> a.shift; }
+// Places: a strip takes as many as its item has column blocks w (its groups' work), an item IC
+// more by itself.  They are counted in units of 2^shift (shift is 0 unless all keys of a call
+// could pass 2^30 places).
+__device__ __forceinline__ int paged_places(const PagedArgs &a, int n, int w) { return (n * w + (1 << a.shift) - 1) >> a.shift; }
+// the strips that end within the first x places of an item's strips
+__device__ __forceinline__ int paged_strips(const PagedArgs &a, int x, int w) { return w == 1 ? x << a.shift : paged_div(x << a.shift, w); }
 
-// One segment: the strips of the item that starts at place `at` which lie in the range.
-template <int IC>
-__device__ __forceinline__ void paged_emit(const PagedArgs &a, PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b,
+// One segment: the strips of the item that starts at place `at` which lie in the range; false
+// if there are none.
+template <int ROWS, int IC>
+__device__ __forceinline__ bool paged_emit(const PagedArgs &a, PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b,
                                            int rb, int head, int at, int begin, int end, int share) {
-  const int n = paged_places(a, p.n), u0 = max(begin - at - IC, 0), u1 = min(end - at - IC, n);
-  g.u0 = u0 << a.shift;
-  g.u1 = u1 == n ? p.n : u1 << a.shift;
-  g.c0 = u0 == 0 ? (int)blockIdx.x : paged_div(at + IC, share);
-  g.c1 = u1 == n ? (int)blockIdx.x : paged_div(at + IC + n - 1, share);
-  paged_fill(g, s, p, b, rb, head, a.G);
+  const int w = paged_blocks<ROWS>(s.nq * a.G, rb), n = paged_places(a, p.n, w), x1 = min(end - at - IC, n);
+  const int u0 = paged_strips(a, max(begin - at - IC, 0), w), u1 = x1 == n ? p.n : paged_strips(a, x1, w);
+  if (u0 >= u1) return false;
+  g.u0 = u0;
+  g.u1 = u1;
+  g.c0 = u0 == 0 ? (int)blockIdx.x : paged_div(at + IC + paged_places(a, 1, w) - 1, share);
+  g.c1 = u1 == p.n ? (int)blockIdx.x : paged_div(at + IC + n - 1, share);
+  paged_fill<ROWS>(g, s, p, b, rb, head, a.G);
+  return true;
+}
+// Parts of an item of n strips when CTAs of their own take `size` places, and their strips.
+__device__ __forceinline__ int paged_parts(const PagedArgs &a, int n, int w, int size, int &len) {
+  const int np = paged_div(paged_places(a, n, w) + size - 1, size);
+  len = paged_div(n + np - 1, np);
+  return paged_div(n + len - 1, len);
 }
 
 // Lists the range's next segments (one thread).
@@ -323,7 +349,7 @@ __device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, P
 #pragma unroll 1
     for (; rb < nrb; ++rb) {
       p = paged_span<ROWS>(a, s, rb);
-      each = paged_places(a, p.n) + IC;
+      each = paged_places(a, p.n, paged_blocks<ROWS>(s.nq * a.G, rb)) + IC;
       if (o < each * a.Hkv) break;
       o -= each * a.Hkv;
     }
@@ -333,10 +359,8 @@ __device__ __forceinline__ void paged_walk(const PagedArgs &a, PagedSeg *segs, P
       continue;
     }
     const int head = paged_div(o, each), in = o - head * each;
-    if (pos - in + IC < end) {                          // (a range may end among an item's first places)
-      paged_emit<IC>(a, segs[n], s, p, b, rb, head, pos - in, ctl->begin, end, ctl->share);
-      ++n;
-    }
+    // (a range may end among an item's first places)
+    if (pos - in + IC < end && paged_emit<ROWS, IC>(a, segs[n], s, p, b, rb, head, pos - in, ctl->begin, end, ctl->share)) ++n;
     pos += each - in;
     off += each - in;
   }
@@ -366,7 +390,7 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     auto cost = [&](const PagedSeq &s) {
       int c = 0;
 #pragma unroll 1
-      for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_places(a, paged_span<ROWS>(a, s, rb).n) + IC;
+      for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_places(a, paged_span<ROWS>(a, s, rb).n, paged_blocks<ROWS>(s.nq * a.G, rb)) + IC;
       return c * a.Hkv;
     };
     // sums before this thread and over all (of the warp, or through shared memory)
@@ -401,7 +425,7 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
       const int n = blocks(own);
       if (n == 1) {
         first = paged_span<ROWS>(a, own, 0);
-        mine += (paged_places(a, first.n) + IC) * a.Hkv;
+        mine += (paged_places(a, first.n, paged_blocks<ROWS>(own.nq * a.G, 0)) + IC) * a.Hkv;
       } else {
         mine += cost(own);
       }
@@ -414,28 +438,30 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     else all_items = __reduce_add_sync(0xffffffffu, min(items, 1 << 16));
     const int grid = gridDim.x, me = blockIdx.x;
     const int share = max(paged_div(total + grid - 1, grid), a.min_places);
-    // strips a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
+    // places a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
     const int left = grid - all_items;
     const int size = per == 1 && left > 0 && a.shift == 0 ? max(paged_div(total - IC * all_items + left - 1, left), a.min_places) : 0;
     if (size > 0 && size <= share + 2 * IC) {
       int parts = 0, pp;
 #pragma unroll 1
-      for (int rb = 0, n = blocks(own); rb < n; ++rb) parts += paged_div(span(rb).n + size - 1, size) * a.Hkv;
+      for (int rb = 0, n = blocks(own), len; rb < n; ++rb)
+        parts += paged_parts(a, span(rb).n, paged_blocks<ROWS>(own.nq * a.G, rb), size, len) * a.Hkv;
       scan(parts, pp, dummy);
       if (me >= pp && me < pp + parts) {                // one thread, if any
         int at = pp;
 #pragma unroll 1
         for (int rb = 0, n = blocks(own); rb < n; ++rb) {
           const PagedSpan p = span(rb);
-          const int np = paged_div(p.n + size - 1, size);
+          int len;
+          const int np = paged_parts(a, p.n, paged_blocks<ROWS>(own.nq * a.G, rb), size, len);
           if (me < at + np * a.Hkv) {
             PagedSeg &g = segs[0];
-            const int head = paged_div(me - at, np), j = me - at - head * np, len = paged_div(p.n + np - 1, np);
+            const int head = paged_div(me - at, np), j = me - at - head * np;
             g.u0 = j * len;
             g.u1 = min(p.n, g.u0 + len);
             g.c0 = me - j;
             g.c1 = g.c0 + np - 1;
-            paged_fill(g, own, p, b_lo, rb, head, a.G);
+            paged_fill<ROWS>(g, own, p, b_lo, rb, head, a.G);
             ctl->nseg = 1;
             break;
           }
@@ -452,14 +478,17 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
 #pragma unroll 1
           for (int rb = 0, n = blocks(own); rb < n && at < end; ++rb) {
             const PagedSpan p = span(rb);
-            const int each = paged_places(a, p.n) + IC;
+            const int each = paged_places(a, p.n, paged_blocks<ROWS>(own.nq * a.G, rb)) + IC;
             int head = begin > at ? min(paged_div(begin - at, each), a.Hkv) : 0;
             int x = at + head * each;
 #pragma unroll 1
             for (; head < a.Hkv && x + IC < end; ++head, x += each)
               if (x + each > begin) {
-                const int i = atomicAdd(&ctl->nseg, 1);
-                if (i < kPagedMaxSegs) paged_emit<IC>(a, segs[i], own, p, b_lo, rb, head, x, begin, end, share);
+                PagedSeg g;
+                if (paged_emit<ROWS, IC>(a, g, own, p, b_lo, rb, head, x, begin, end, share)) {
+                  const int i = atomicAdd(&ctl->nseg, 1);
+                  if (i < kPagedMaxSegs) segs[i] = g;
+                }
               }
             at += a.Hkv * each;
           }
@@ -585,15 +614,15 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
   using P = PagedShape<D, KV, NB>;
   constexpr bool BF = KV == kPagedBf16;
   constexpr bool I8 = KV == kPagedI8;
-  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, RB = P::kRowBytes;
+  constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
   constexpr int R = P::kRing, SW = P::kSW, GW = P::kGW;
   constexpr int DT = D / 16 / GW;                       // 16-channel tiles a warp
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *fixed = smem + R * KW * P::kHalf;
-  float *red = reinterpret_cast<float *>(fixed);                      // [KW][GW][ROWS][SW + 4]
-  float *sm_m = red + P::kRedBytes / 4;                               // [KW][ROWS]
-  float *sm_l = sm_m + P::kWarps * ROWS;
-  long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * ROWS);   // [ROWS]
+  float *red = reinterpret_cast<float *>(fixed);                      // [KW][GW][COLS][SW + 4]
+  float *sm_m = red + P::kRedBytes / 4;                               // [KW][COLS]
+  float *sm_l = sm_m + P::kWarps * COLS;
+  long long *sm_row = reinterpret_cast<long long *>(sm_l + P::kWarps * COLS);   // [ROWS]
   PagedSeg *segs = reinterpret_cast<PagedSeg *>(sm_row + ROWS);
   PagedCtl *ctl = reinterpret_cast<PagedCtl *>(segs + kPagedMaxSegs);
 
@@ -624,12 +653,30 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
     const int nseg = ctl->nseg;
     const bool more = ctl->more != 0;
 
-    // ---- the ring: this group's strips (u0 + kw, + KW, ..), ahead of the arithmetic, each as
-    // two half stages: its K rows, then its V rows
-    int ls = 0, lu = segs[0].u0 + kw, lbuf = 0;
+    // Group kw of an item of nblk column blocks takes block kw % nblk and its strips
+    // u0 + kw / nblk, + KW / nblk, .. (the groups left over take none).
+    auto deal = [&](const PagedSeg &g, int &first, int &step) {
+      const int n = ROWS == COLS ? 1 : g.nblk;
+      step = n == 1 ? KW : n == 2 ? KW / 2 : n == 3 ? KW / 3 : KW / 4;
+      first = n == 1 ? kw : n == 2 ? kw >> 1 : n == 3 ? (kw * 11) >> 5 : kw >> 2;     // kw / n, kw < 16
+      const int block = kw - first * n;
+      if (first >= step) first = 1 << 28;
+      first += g.u0;
+      return block;
+    };
+    // ---- the ring: this group's strips, ahead of the arithmetic, each as two half stages: its
+    // K rows, then its V rows
+    int ls = -1, lu = 0, lend = 0, lstep = KW, lbuf = 0;
     bool lv = false;
-    while (ls < nseg && lu >= segs[ls].u1)
-      if (++ls < nseg) lu = segs[ls].u0 + kw;
+    auto advance = [&]() {                                 // to the next segment with a strip
+#pragma unroll 1
+      while (ls < nseg && lu >= lend)
+        if (++ls < nseg) {
+          deal(segs[ls], lu, lstep);
+          lend = segs[ls].u1;
+        }
+    };
+    advance();
     // Of the strip being loaded: byte offset of row lane & 15 (-1: not read) and, int8, of its
     // scale; the rows that are read; whether the strip lies in one page and is read whole.
     long long off = -1, soff = -1;
@@ -683,10 +730,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
           }
         }
         if (lv) {
-          lu += KW;
-#pragma unroll 1
-          while (ls < nseg && lu >= segs[ls].u1)
-            if (++ls < nseg) lu = segs[ls].u0 + kw;
+          lu += lstep;
+          advance();
         }
         lv = !lv;
       }
@@ -721,7 +766,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
     // while the item before is joined.
     uint32_t qr[DT][NB][2];
     auto load_q = [&](const PagedSeg &g) {
-      const int row0 = g.rb * ROWS;
+      int first, step;
+      const int row0 = g.rb * ROWS + deal(g, first, step) * COLS;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         // (a column past the last repeats the first: its sums are its own and unused)
@@ -748,7 +794,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
 
     for (int sg = 0; sg < nseg; ++sg) {
       const PagedSeg &g = segs[sg];
-      const int row0 = g.rb * ROWS;
+      int u, step;
+      const int block = deal(g, u, step);
+      const int row0 = g.rb * ROWS + block * COLS;         // the group's first column
       // positions of this lane's columns (-1: no such column)
       int pos[NB][2];
 #pragma unroll
@@ -758,7 +806,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
           const int gr = row0 + nb * 8 + 2 * c4 + e;
           pos[nb][e] = gr < g.rows ? g.pos0 + gr / a.G : -1;
         }
-      const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + ROWS) - 1) / a.G;
+      const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + COLS) - 1) / a.G;
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -773,7 +821,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
       }
 
 #pragma unroll 1
-      for (int u = g.u0 + kw; u < g.u1; u += KW) {
+      for (; u < g.u1; u += step) {
         const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
         // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
         constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
@@ -959,11 +1007,13 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], o);
           if (r8 == 0 && gi == 0) {
-            sm_m[kw * ROWS + nb * 8 + 2 * c4 + e] = m[nb][e];
-            sm_l[kw * ROWS + nb * 8 + 2 * c4 + e] = l[nb][e];
+            sm_m[kw * COLS + nb * 8 + 2 * c4 + e] = m[nb][e];
+            sm_l[kw * COLS + nb * 8 + 2 * c4 + e] = l[nb][e];
           }
         }
       __syncthreads();                                   // also: Q is no longer read
+      // bit w: group w takes the item's first block; shifted by b, its block b
+      const unsigned groups = ROWS == COLS || g.nblk == 1 ? 0xffffu : g.nblk == 2 ? 0x5555u : g.nblk == 3 ? 0x9249u : 0x1111u;
       float f[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -971,22 +1021,28 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + nb * 8 + 2 * c4 + e]);
+          for (int w = 0; w < KW; ++w)
+            if (ROWS == COLS || ((groups << block >> w) & 1u)) M = fmaxf(M, sm_m[w * COLS + nb * 8 + 2 * c4 + e]);
           f[nb][e] = m[nb][e] == -INFINITY ? 0.0f : paged_ex2(m[nb][e] - M);
         }
       const bool cut = g.c0 != g.c1;
       float *part = a.part + (size_t)(2 * blockIdx.x + (g.c0 == (int)blockIdx.x ? 1 : 0)) * P::kPartFloats;
-      const int nrows = min(ROWS, g.rows - row0);
+      const int first = g.rb * ROWS, nrows = min(ROWS, g.rows - first);
       // column sums: M and L of each column (thread r), and its row of out
       float M = -INFINITY, L = 0.0f;
       if (tid < nrows) {
-        const int tok = (row0 + tid) / a.G;
-        const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.g * a.G + row0 + tid - tok * a.G;
+        const int tok = (first + tid) / a.G;
+        const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.g * a.G + first + tid - tok * a.G;
         sm_row[tid] = orow;
-        for (int w = 0; w < KW; ++w) M = fmaxf(M, sm_m[w * ROWS + tid]);
+        const unsigned mine = groups << (tid / COLS);
+        const int cl = tid % COLS;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+          if (ROWS == COLS || (mine >> w & 1u)) M = fmaxf(M, sm_m[w * COLS + cl]);
+#pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const float mw = sm_m[w * ROWS + tid];
-          if (mw != -INFINITY) L += sm_l[w * ROWS + tid] * paged_ex2(mw - M);
+          const float mw = ROWS == COLS || (mine >> w & 1u) ? sm_m[w * COLS + cl] : -INFINITY;
+          if (mw != -INFINITY) L += sm_l[w * COLS + cl] * paged_ex2(mw - M);
         }
         if (cut) {
           part[tid] = M;
@@ -999,7 +1055,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
       if (tid < nrows) sm_l[tid] = L == 0.0f ? 0.0f : 1.0f / L;      // no key: a row of zeros
 #pragma unroll
       for (int sl = 0; sl < 16 * DT / SW; ++sl) {
-        float *w = red + warp * ROWS * (SW + 4);
+        float *w = red + warp * COLS * (SW + 4);
 #pragma unroll
         for (int t = 0; t < SW / 16; ++t)
 #pragma unroll
@@ -1021,9 +1077,11 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
         for (int i = tid; i < nrows * (GW * SW / 2); i += NT) {
           const int r = i / (GW * SW / 2), hc = i % (GW * SW / 2) / (SW / 2), cp = i % (SW / 2);
           float2 o = make_float2(0.0f, 0.0f);
+          const unsigned mine = groups << (r / COLS);
 #pragma unroll
           for (int w2 = 0; w2 < KW; ++w2) {
-            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * GW + hc) * ROWS + r) * (SW + 4) + 2 * cp);
+            if (ROWS != COLS && !(mine >> w2 & 1u)) continue;
+            const float2 v = *reinterpret_cast<const float2 *>(red + ((w2 * GW + hc) * COLS + r % COLS) * (SW + 4) + 2 * cp);
             o.x += v.x;
             o.y += v.y;
           }
@@ -1071,7 +1129,7 @@ cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
   count_launch();
   return e;
 }
-// cols: the columns of an item, 8 or 16 (paged_columns)
+// cols: the columns of an item, 8 or 64 (paged_columns)
 template <int KV>
 cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
 #define QW_PAGED(DD) \

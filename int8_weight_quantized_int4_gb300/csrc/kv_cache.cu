@@ -240,8 +240,9 @@ const void *append_kernel(int d) {
 }
 
 // ---- attention: the query columns of an item, and the workspace for them.  Eight where a
-// step's columns (new tokens x heads a KV head) fit (half the MMAs of 16), else blocks of 16.
-int paged_columns(int max_new, int G) { return (long long)max_new * G <= 8 ? 8 : 16; }
+// step's columns (new tokens x heads a KV head) fit (half the MMAs of 16), else up to four blocks
+// of 16.
+int paged_columns(int max_new, int G) { return (long long)max_new * G <= 8 ? 8 : 64; }
 constexpr size_t kPagedCounterBytes = 4096;      // one counter a CTA
 size_t paged_ws(int d, int cols, int sms) {
   return kPagedCounterBytes + (size_t)2 * sms * cols * (d + 2) * 4;
@@ -405,12 +406,12 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
   a.strip_pages = c->page % 16 == 0;
-  // every sequence's column blocks and their strips, were all contexts as long as the page
-  // table; up to 96 places more an item
+  // every item's places, were all contexts as long as the page table: four for each strip of 16
+  // keys, and up to 96 more
   long long most = ((long long)T * a.G / cols + b->B) * c->Hkv;
   if (most > (1ll << 28)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   const long long blocks = most;
-  for (most = blocks * (a.cap / 16 + 128); most > (1ll << 30); most = blocks * ((a.cap / 16 >> a.shift) + 128)) {
+  for (most = blocks * (a.cap / 4 + 128); most > (1ll << 30); most = blocks * ((a.cap / 4 >> a.shift) + 128)) {
     if (++a.shift > 24) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   }
   a.min_places = 12;
