@@ -54,6 +54,7 @@ namespace qw {
 constexpr int kPagedMaxSegs = 32;       // work segments listed at a time
 constexpr int kStrip = 16;              // keys of a strip: the MMA's rows of S^T, its depth of O^T
 constexpr int kPagedSmem = 227 * 1024;
+constexpr float kNoScore = -3.402823466e38f;   // the reference of a sum of nothing: the lowest finite score
 
 struct PagedSeg {
   int b, g, rb;                 // sequence, KV head, block of kRows columns
@@ -553,7 +554,7 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
 #pragma unroll 1
     for (int r = tid >> 3; r < (nr + 3) / 4 * 4; r += NT / 8) {       // whole warps
       const int e = lane & 7;
-      float Mx = -INFINITY, Ls = 0.0f;
+      float Mx = kNoScore, Ls = 0.0f;
       if (r < nr)
 #pragma unroll 1
         for (int k = e; k < n; k += 8) Mx = fmaxf(Mx, mm[k * nr + r]);
@@ -562,7 +563,7 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
       if (r < nr)
 #pragma unroll 1
         for (int k = e; k < n; k += 8) {
-          const float mk = mm[k * nr + r], w = mk == -INFINITY ? 0.0f : paged_ex2(mk - Mx);
+          const float w = paged_ex2(mm[k * nr + r] - Mx);
           Ls += ll[k * nr + r] * w;
           mm[k * nr + r] = w;
         }
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
           const int key = unit * kStrip + (lane & 15);
           off = soff = -1;
           if (key < g.hi && (key >= g.lo || key < a.sinks)) {
-            const int pi = paged_div(key, a.page), po = key - pi * a.page;
+            const int pi = a.page_shift >= 0 ? key >> a.page_shift : paged_div(key, a.page), po = key - pi * a.page;
             const int pid = __ldg(a.table + (size_t)g.b * a.max_pages + pi);
             if ((unsigned)pid < (unsigned)a.npages) {
               off = (pid * a.page_stride + g.g * a.head_stride + po * a.tok_stride) * P::kES;
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
       float m[NB][2], l[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        m[nb][0] = m[nb][1] = -INFINITY;
+        m[nb][0] = m[nb][1] = kNoScore;
         l[nb][0] = l[nb][1] = 0.0f;
       }
 
@@ -941,10 +942,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
         uint32_t pk[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float ref0 = m[nb][0] == -INFINITY ? 0.0f : m[nb][0], ref1 = m[nb][1] == -INFINITY ? 0.0f : m[nb][1];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float p0 = paged_ex2(s[nb][2 * h] - ref0), p1 = paged_ex2(s[nb][2 * h + 1] - ref1);
+            float p0 = paged_ex2(s[nb][2 * h] - m[nb][0]), p1 = paged_ex2(s[nb][2 * h + 1] - m[nb][1]);
             l[nb][0] += p0;
             l[nb][1] += p1;
             if constexpr (I8) {          // (a hidden key's weight is 0 whatever its value's scale holds)
@@ -1019,17 +1019,17 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float M = -INFINITY;
+          float M = kNoScore;
 #pragma unroll
           for (int w = 0; w < KW; ++w)
             if (ROWS == COLS || ((groups << block >> w) & 1u)) M = fmaxf(M, sm_m[w * COLS + nb * 8 + 2 * c4 + e]);
-          f[nb][e] = m[nb][e] == -INFINITY ? 0.0f : paged_ex2(m[nb][e] - M);
+          f[nb][e] = paged_ex2(m[nb][e] - M);
         }
       const bool cut = g.c0 != g.c1;
       float *part = a.part + (size_t)(2 * blockIdx.x + (g.c0 == (int)blockIdx.x ? 1 : 0)) * P::kPartFloats;
       const int first = g.rb * ROWS, nrows = min(ROWS, g.rows - first);
       // column sums: M and L of each column (thread r), and its row of out
-      float M = -INFINITY, L = 0.0f;
+      float M = kNoScore, L = 0.0f;
       if (tid < nrows) {
         const int tok = (first + tid) / a.G;
         const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.g * a.G + first + tid - tok * a.G;
@@ -1041,8 +1041,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
           if (ROWS == COLS || (mine >> w & 1u)) M = fmaxf(M, sm_m[w * COLS + cl]);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const float mw = ROWS == COLS || (mine >> w & 1u) ? sm_m[w * COLS + cl] : -INFINITY;
-          if (mw != -INFINITY) L += sm_l[w * COLS + cl] * paged_ex2(mw - M);
+          if (ROWS == COLS || (mine >> w & 1u)) L += sm_l[w * COLS + cl] * paged_ex2(sm_m[w * COLS + cl] - M);
         }
         if (cut) {
           part[tid] = M;

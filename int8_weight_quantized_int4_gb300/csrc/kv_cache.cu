@@ -405,6 +405,8 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.cap = b->max_pages * c->page;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
+  a.page_shift = (c->page & (c->page - 1)) == 0 ? 0 : -1;
+  while (a.page_shift >= 0 && c->page >> a.page_shift > 1) ++a.page_shift;
   a.strip_pages = c->page % 16 == 0;
   // every item's places, were all contexts as long as the page table: four for each strip of 16
   // keys, and up to 96 more

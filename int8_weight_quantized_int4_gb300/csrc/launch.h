@@ -118,6 +118,7 @@ struct PagedArgs {
   int B, T, Hq, Hkv, G, page, npages, max_pages;
   int cap;                      // keys the page table can name: max_pages * page
   int window, sinks;            // window 0: every key up to the position; sinks 0 without one
+  int page_shift;               // log2(page), -1 where page is no power of two
   int strip_pages;              // page % 16 == 0: a strip of 16 keys lies in one page
   int shift;                    // the schedule counts keys in 2^shift strips of 16
   int min_places;               // fewest of them a CTA takes

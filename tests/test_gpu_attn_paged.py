@@ -97,6 +97,25 @@ def test_large_scores_and_scale(q, kind):
     check(q, c, scale=0.0)
 
 
+def test_scores_near_the_lowest(q):
+    """Every visible score near binary32's lowest value (-1.96 * 2^127 in base 2, the same for
+    all keys): the weights are still equal.  Equal scores leave only the rounding of a 16-bit
+    output and of binary32 sums."""
+    c = Cache([300, 37], [1, 2], 8, 2, 64, 16, "bf16", seed=8)
+    c.q.fill_(2.0 ** 60)
+    for b, n in enumerate(c.lens_list):
+        for j in range(n):
+            pid, off = c.row(b, j)
+            c.k[pid, :, off] = -2.0 ** 61
+            c.k64[pid, :, off] = -2.0 ** 61
+    ref = c.reference(scale=1.36)
+    out, lse = q.attn_paged(c.q, *c.args(), max_new=2, scale=1.36, lse=torch.empty(c.T, 8, device=DEV), **c.kw)
+    assert q.device_error() == 0
+    tol = 2.0 ** -9 * ref[0].abs() * (1 + 2.0 ** -6) + 400 * 2.0 ** -24 * ref[3]
+    assert bool(((out.double() - ref[0]).abs() <= 2 * tol).all())
+    assert bool(((lse.double() / ref[1] - 1).abs() <= 2.0 ** -20).all())
+
+
 @pytest.mark.parametrize("v_scale", [2.0 ** -13, 2.0 ** 8])
 def test_int8_values_of_any_size(q, v_scale):
     """The weight carries the value's scale: small scales must not lose its bits."""
