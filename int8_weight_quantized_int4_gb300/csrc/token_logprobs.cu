@@ -1,10 +1,13 @@
 // token_logprobs.cu -- log probabilities of given tokens, entropy and the k most likely
 // tokens of each row of a logit matrix, in one pass over the logits.
 //
-// In base 2, with y_j = x_j log2(e) - r for a reference r near the row's largest x log2(e):
+// With y_j = (x_j - r) log2(e) for a reference r near the row's largest x:
 //   s = sum 2^y_j,  t = sum y_j 2^y_j
-//   logsumexp = (r + log2 s) ln 2      log p_j = (y_j - log2 s) ln 2
+//   logsumexp = r + log2 s ln 2        log p_j = (x_j - r) - log2 s ln 2
 //   entropy   = (log2 s - t / s) ln 2  (both terms are >= 0 up to rounding: no cancellation)
+// The difference is taken first: x log2(e) - r log2(e) in one step saves an operation a pair, but
+// then the rounding of r log2(e) moves every y by up to |r| 2^-24, and far from zero (a whole
+// row masked with -1e30 or the type's lowest value) that is more than the exponents hold.
 // A thread keeps (r, s, t) while it streams its 16-byte vectors; all sums in binary32, joined
 // in a fixed order.
 //
@@ -165,7 +168,7 @@ __device__ __forceinline__ float lp_max(const uint4 &w) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNoRef = -1e30f;                  // the reference of a sum of nothing
+constexpr float kNoRef = -3.402823466e38f;        // the reference of a sum of nothing: the lowest finite logit
 
 struct LpSum {
   float r, s, t;
@@ -196,8 +199,11 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// y moved from reference a to b: far below the exponents' range nothing is left, and no
+// infinity may meet a zero (a reference +inf leaves NaN: its own sum is one)
+__device__ __forceinline__ float lp_shift(float a, float b) { return fmaxf((a - b) * kLog2e, -1000.0f); }
 __device__ __forceinline__ void lp_move(LpSum &a, float r) {       // to the reference r
-  const float d = a.r - r, f = lp_ex2(d);
+  const float d = lp_shift(a.r, r), f = lp_ex2(d);
   a.t = a.s == 0.0f ? 0.0f : (a.t + d * a.s) * f;
   a.s *= f;
   a.r = r;
@@ -329,11 +335,11 @@ __device__ __forceinline__ void lp_write(const LpArgs &a, int m, const T *row, c
   const float ls = log2f(z.s);
   const bool none = z.s == 0.0f;                  // every logit -inf
   if (threadIdx.x == 0) {
-    a.lse[m] = none ? -INFINITY : (z.r + ls) * kLn2;
+    a.lse[m] = none ? -INFINITY : fmaf(ls, kLn2, z.r);
     a.entropy[m] = none ? 0.0f : fmaxf(ls - z.t / z.s, z.s != z.s ? z.s : 0.0f) * kLn2;
   }
   // (a token that does not exist stays NaN)
-  auto lp = [&](float x) { return none ? (x != x ? x : -INFINITY) : (fmaf(x, kLog2e, -z.r) - ls) * kLn2; };
+  auto lp = [&](float x) { return none ? (x != x ? x : -INFINITY) : fmaf(-ls, kLn2, x - z.r); };
 #pragma unroll 1
   for (int c = threadIdx.x; c < a.C; c += kLpThreads)
     a.logprob[(long long)m * a.C + c] = lp(given && c == (int)threadIdx.x ? xtok : lp_token<T>(a, m, row, c));
@@ -418,23 +424,22 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(co
     if (tid < a.C && m + 1 < a.M) tok = lp_token_id(a, m + 1, tid);
 
     // ---- the sums, over even and odd elements.  The reference starts at the largest of the
-    // warp's first blocks and moves when a block passes it by 2^4 (y stays below 4: nothing
+    // warp's first blocks and moves when a block passes it by 4 (y stays below 6: nothing
     // overflows, and little cancels in log2 s - t / s).
     float top = -INFINITY, r = kNoRef;            // this thread's largest element
-    unsigned long long nr2 = 0ull, s2 = pair2(0.0f, 0.0f), t2 = s2;
+    unsigned long long nr2 = pair2(-kNoRef, -kNoRef), s2 = pair2(0.0f, 0.0f), t2 = s2;
     const unsigned long long e2 = pair2(kLog2e, kLog2e);
     auto raise = [&](float x) {
-      const float q = x * kLog2e;
-      if (q > r + 4.0f) {
-        const float d = r - q, f = lp_ex2(d);
+      if (x > r + 4.0f) {
+        const float d = lp_shift(r, x), f = lp_ex2(d);
         t2 = mul2(fma2(pair2(d, d), s2, t2), pair2(f, f));
         s2 = mul2(s2, pair2(f, f));
-        r = q;
-        nr2 = pair2(-q, -q);
+        r = x;
+        nr2 = pair2(-x, -x);
       }
     };
     auto add = [&](float x0, float x1) {
-      const float2 y = both2(fma2(pair2(x0, x1), e2, nr2));
+      const float2 y = both2(mul2(add2(pair2(x0, x1), nr2), e2));
       const float y0 = max_nan(y.x, -150.0f), y1 = max_nan(y.y, -150.0f);       // 2^-150 is 0; -inf stays out of y 2^y
       const unsigned long long p2 = pair2(lp_ex2(y0), lp_ex2(y1));
       s2 = add2(s2, p2);
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(co
         maxima[(blk >> g) * kLpThreads + tid] = run;
       }
       if (blk == 0) {                             // (whole warp)
-        r = fmaxf(key_value32(__reduce_max_sync(0xffffffffu, order_key32(bm))) * kLog2e, kNoRef);
+        r = fmaxf(key_value32(__reduce_max_sync(0xffffffffu, order_key32(bm))), kNoRef);
         nr2 = pair2(-r, -r);
       } else {
         raise(bm);

@@ -120,6 +120,50 @@ def test_all_masked_row(q):
     assert r.top_idx[1].tolist() == [0, 1, 2, 3, 4] and bool((r.top_logprob[1] == -math.inf).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("left", [0, 1, 20, 200])
+@pytest.mark.parametrize("low", ["lowest", -1.0e9, -1.0e30])
+def test_masked_with_large_finite_values(q, dtype, left, low):
+    """Masks of the type's lowest value or another large one: with `left` tokens besides, the
+    others have no probability; alone, they are equally likely."""
+    low = torch.finfo(dtype).min if low == "lowest" else low
+    for M, N in ((3, 40000), (770, 2001)):
+        x, tok = rand(M, N, dtype, seed=left)
+        g = torch.Generator(device=DEV).manual_seed(left)
+        keep = torch.zeros(M, N, dtype=torch.bool, device=DEV)
+        keep.scatter_(1, torch.argsort(torch.rand(M, N, generator=g, device=DEV))[:, :left], True)
+        check_far(q, x.masked_fill(~keep, low), tok, 20)
+
+
+def check_far(q, x, tok, k):
+    """Against logits less their row's maximum, m (exact in binary64): log p = (x - m) - log s
+    has one rounding of x - m (2 e |x - m|, <= 2 e (|log p| + log N)), the others' as in check."""
+    r = q.token_logprobs(x, tok, k=k)
+    assert q.device_error() == 0
+    m = x.double().amax(1, keepdim=True)
+    lp, ent, lse, top, idx = logprobs_reference(x.double() - m, tok[:, None], k)
+    ds = 2.0 ** -21 + (x.shape[1] / 256 + 41) * E
+    far = math.log(x.shape[1]) + 2
+
+    def near(got, want, tol, what):
+        err = (got.double() - want).abs()
+        assert bool((err <= tol).all()), (what, float((err / tol).max()))
+    near(r.lse, lse + m[:, 0], ds + 4 * E * (lse + m[:, 0]).abs() + 4 * E * m[:, 0].abs(), "lse")
+    near(r.entropy, ent, ds * (2 + ent) + 8 * E * (1 + ent), "entropy")
+    near(r.logprob, lp[:, 0], ds + 4 * E * (lp[:, 0].abs() + far), "logprob")
+    near(r.top_logprob, top, ds + 4 * E * (top.abs() + far), "top")
+    assert torch.equal(r.top_idx, idx)
+
+
+@pytest.mark.parametrize("shift", [1.0e6, -1.0e6, 1.0e8, -1.0e12])
+def test_far_from_zero(q, shift):
+    """binary32 logits a long way from zero: the differences between them are what counts."""
+    step = max(1.0, 2.0 ** math.ceil(math.log2(abs(shift) * 2.0 ** -23)))       # distinct after rounding
+    for M, N in ((2, 30000), (770, 2001)):
+        x, tok = rand(M, N, torch.float32, seed=4)
+        check_far(q, (x.double() * step + shift).float(), tok, 20)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_large_values_in_few_places(q, dtype):
     """The best logits crowded where one thread reads them (its list overflows and the
