@@ -335,8 +335,9 @@ int kv_copy_pages(const qw_page_pool_t *pools, int n_pools, const int32_t *pairs
  *   lse: NULL, or binary32 [T][Hq]: the natural logarithm of the sum of exponentials
  *   (-inf for a token that sees nothing), with which parts over other keys can be joined.
  *   max_new >= 1: the most new tokens of a sequence.  A hint: max_new * Hq / Hkv <= 8 selects
- *   items of 8 query columns (a column: one head of one new token) instead of 16; a sequence
- *   with more columns is computed in several items all the same.
+ *   the kernel that takes 8 query columns (a column: one head of one new token) at a time
+ *   instead of up to 64 in blocks of 16; a sequence with more columns is computed piece by
+ *   piece all the same.  The workspace's size depends on it.
  *   ws: attn_paged_workspace_bytes(d, Hq, Hkv, max_new) bytes, 256-byte aligned, zero-filled
  *   once (the first attn_paged_workspace_zero_bytes stay zero after every call); shared by
  *   attn_paged calls of any shape, not by calls that may run concurrently nor by other
@@ -401,8 +402,9 @@ int kv_pool_free_pages(kv_pool_t *pool);
  *   top_logprob, top_idx [m][k]   the k most likely tokens, most likely first, equal logits
  *                   by the smaller index (-0 equals +0)
  *   logits: fp16, bf16 or binary32 (dtype QW_F16, QW_BF16, QW_F32), row m at
- *   logits + m * row_stride elements; any alignment and any 1 <= N <= 2^30.  -inf (and any
- *   logit below -2.3e38) is a probability of 0; NaN and +inf give NaN sums.  0 <= k <= min(64, N).
+ *   logits + m * row_stride elements; any alignment and any 1 <= N <= 2^30.  -inf is a
+ *   probability of 0 (a mask of the type's lowest value likewise, but a row of nothing else
+ *   is uniform); NaN and +inf give NaN sums.  0 <= k <= min(64, N).
  *   tokens [M][C]: token_bytes 4 (int32) or 8 (int64); C may be 0.
  *   ws: token_logprobs_workspace_bytes(M, N, k, dtype) bytes, 256-byte aligned, zero-filled
  *   once (the first ..._zero_bytes stay zero after every call); shared as attn_paged's.

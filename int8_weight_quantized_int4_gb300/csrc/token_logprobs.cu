@@ -25,9 +25,13 @@
 // its parts' sums and selects among their lists the same way.  Each block of four vectors a
 // thread is loaded while the one before is summed, across row borders too.
 //
-// What bounds it: the read of the logits (HBM); close to it the instructions, about six an
-// element (pairs go through two-wide binary32 operations) and some 500 a warp and row; for few
-// rows the launch and two chains of block-wide steps.
+// What bounds it: the read of the logits (HBM); close to it the instructions, about ten a 16-bit
+// element with everything counted (pairs go through two-wide binary32 operations), and some 500
+// a warp and row; for few rows the launch and two chains of block-wide steps (the part's sums
+// and list, then the join's).
+//
+// Measured: 2048 rows of 50257 bf16 (206 MB), no alternatives: 42.2 us, 4.9 TB/s; 64 of 128257
+// binary32 with 20 alternatives: 17.4 us, 1.9 TB/s; one of 248320 fp16 with 20: 12.2 us.
 #include <float.h>
 #include <stdarg.h>
 #include <stdint.h>
