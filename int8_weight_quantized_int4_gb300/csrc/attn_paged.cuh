@@ -15,7 +15,7 @@
 //     MMA whose rows are keys (S^T = K Q^T) and then channels (O^T = V^T P^T), so K and V are
 //     read once for all of them and eight columns (the common case, G <= 8) cost half of what
 //     a 16-row query tile would, in instructions and in accumulator registers.
-//   - A CTA owns an SM.  Each of its KW groups streams its own strips of 16 keys through its
+//   - One CTA, or up to four (paged_launch), share an SM.  Each of its KW groups streams its own strips of 16 keys through its
 //     own ring of half stages (the K rows, then the V rows of a strip; cp.async, 16 bytes a
 //     thread; rows beyond the visible keys are zero-filled, not read) and waits only for
 //     itself: no CTA-wide barrier between the strips of a sequence.  A group is one warp, but
@@ -37,11 +37,11 @@
 //     is being finished.
 //
 // Measured (K and V rows read / time): 64 ragged contexts of up to 8190, 32/8 heads of 128, bf16:
-// 190.7 us, 6.07 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 113.6 us, 5.88 TB/s (the
+// 181 us, 6.4 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 113.6 us, 5.88 TB/s (the
 // codes' conversion to fp16 takes half of the issue slots); 16 of up to 16384 with up to 6 new
 // tokens, fp16: 148.5 us, 4.76 TB/s (36 columns: the strip is read once from HBM and up to
 // twice more from L2, and the columns' exponents and products take the rest); a window of
-// 1024, 48 contexts, 64/8 heads of 64, fp16: 31.6 us, 3.17 TB/s (items of 66 strips: their
+// 1024, 48 contexts, 64/8 heads of 64, fp16: 27.2 us, 3.7 TB/s (items of 66 strips: their
 // starts and joins); one context of 1003, 24/4 heads of 256, fp16: 12.1 us, nearly all of it the
 // chain launch -> lengths -> page table -> keys -> exchange -> partial sums -> join.
 //
@@ -88,13 +88,13 @@ struct PagedCtl {
 };
 
 // Shapes.  NB: MMA column tiles (of 8) a warp; GW: warps of a group, which share the channels.
-// The warps a CTA has are what the registers allow: accumulators take D NB / 4 / GW registers a
-// thread and the Q fragments half of that.
-template <int D, int KV, int NB>
+// The warps an SM has are what the registers allow: accumulators take D NB / 4 / GW registers a
+// thread and the Q fragments half of that.  CTAS: CTAs that share it.
+template <int D, int KV, int NB, int CTAS>
 struct PagedShape {
   static constexpr int kES = KV == kPagedI8 ? 1 : 2;
   static constexpr int kGW = D * NB == 512 ? 2 : 1;
-  static constexpr int kMaxWarps = D * NB >= 256 ? 12 : 16;
+  static constexpr int kMaxWarps = (D * NB >= 256 ? 12 : 16) / CTAS;
   static constexpr int kKW = kMaxWarps / kGW;
   static constexpr int kWarps = kGW * kKW;
   static constexpr int kThreads = 32 * kWarps;
@@ -102,7 +102,7 @@ struct PagedShape {
   // columns of an item, at most (kernels of 8 are called for up to 8: then the blocks' logic is
   // left out, 1 to 3 us a call)
   static constexpr int kRows = NB == 1 ? kCols : 4 * kCols;
-  static_assert(kKW >= 4, "a group a block");
+  static_assert(NB == 1 || kKW >= 4, "a group a block");
   static constexpr int kRowBytes = D * kES;
   static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
   // the exchange at an item's end: SW channels of each warp at a time, rows of SW + 4 floats
@@ -112,14 +112,15 @@ struct PagedShape {
   static constexpr int kRedBytes = kWarps * kCols * (kSW + 4) * 4;
   static_assert(kGW == 1 || kWarps * NB * 512 <= kRedBytes, "room for the scores");
   static constexpr int kFixed = kRedBytes + 2 * kWarps * kCols * 4 + kRows * 8 + kPagedMaxSegs * (int)sizeof(PagedSeg) + (int)sizeof(PagedCtl);
-  static constexpr int kFit = (kPagedSmem - kFixed) / (kKW * kHalf);
+  static constexpr int kFit = (kPagedSmem / CTAS - (CTAS - 1) * 1024 / CTAS - kFixed) / (kKW * kHalf);
   static constexpr int kRing = kFit > 12 ? 12 : kFit;  // half stages a group
   static constexpr int kSmem = kFixed + kRing * kKW * kHalf;
   static_assert(kRing >= (kGW > 1 ? 3 : 2), "K and V of a strip in flight");
   // What an item costs beside its strips, in strips: the groups that wait for the last one, its
-  // join and the next Q take an SM about the time of 192 KB (64 x 8k bf16: 202 us with 64 KB,
-  // 196 with 128, 193 with 192, 188 with 256; 4 x 128k int8: 119, 117, 117, 124).
-  static constexpr int kItemCost = 196608 / (2 * kStrip * kRowBytes);
+  // join and the next Q take an SM about the time of 192 KB (64 x 8k bf16, one CTA an SM: 202 us
+  // with 64 KB, 196 with 128, 193 with 192, 188 with 256; 4 x 128k int8: 119, 117, 117, 124; four CTAs,
+  // 200 x 700: 63 with 128, 58 with 192, 57 with 288, and 48 x 1024 of d = 64: 19.8, 19.4, 22.3).
+  static constexpr int kItemCost = 196608 / CTAS / (2 * kStrip * kRowBytes);
   static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 };
 
@@ -297,7 +298,7 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedArgs &a, const PagedS
 // Blocks of a group's columns in block rb of a sequence's `rows` columns.
 template <int ROWS>
 __device__ __forceinline__ int paged_blocks(int rows, int rb) {
-  return ROWS == 8 ? 1 : (min(rows - rb * ROWS, ROWS) + ROWS / 4 - 1) / (ROWS / 4);
+  return ROWS == 8 ? 1 : (min(rows - rb * ROWS, ROWS) + 15) / 16;
 }
 template <int ROWS>
 __device__ __forceinline__ void paged_fill(PagedSeg &g, const PagedSeq &s, const PagedSpan &p, int b, int rb, int head,
@@ -536,9 +537,9 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
 }
 
 // Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
-template <int D, int KV, int NB>
+template <int D, int KV, int NB, int CTAS>
 __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g, float *red) {
-  using P = PagedShape<D, KV, NB>;
+  using P = PagedShape<D, KV, NB, CTAS>;
   constexpr int NT = P::kThreads, ROWS = P::kRows;
   constexpr bool BF = KV == kPagedBf16;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -618,10 +619,10 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
   }
 }
 
-template <int D, int KV, int NB>
-__global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
+template <int D, int KV, int NB, int CTAS>
+__global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
     attn_paged_kernel(const __grid_constant__ PagedArgs a) {
-  using P = PagedShape<D, KV, NB>;
+  using P = PagedShape<D, KV, NB, CTAS>;
   constexpr bool BF = KV == kPagedBf16;
   constexpr bool I8 = KV == kPagedI8;
   constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
@@ -1124,28 +1125,42 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB>::kThreads, 1)
   }
   // ---- the cut items that this CTA was the last to finish
   __syncthreads();
-  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB>(a, ctl->join[i], red);
+  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB, CTAS>(a, ctl->join[i], red);
 }
 
-template <int D, int KV, int NB>
+template <int D, int KV, int NB, int CTAS>
 cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
-  using P = PagedShape<D, KV, NB>;
-  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, NB>);
+  using P = PagedShape<D, KV, NB, CTAS>;
+  const void *f = reinterpret_cast<const void *>(attn_paged_kernel<D, KV, NB, CTAS>);
   cudaError_t e = ensure_smem_attr(f, P::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(f, dim3(sms), dim3(P::kThreads), P::kSmem, st, a);
+  e = launch_pdl(f, dim3(sms * CTAS), dim3(P::kThreads), P::kSmem, st, a);
   count_launch();
   return e;
 }
-// cols: the columns of an item, 8 or 64 (paged_columns)
+// cols: the columns of an item, 8 or 64 (paged_columns).
+//
+// Several CTAs share an SM where there are many items (one CTA's exchange and join then overlap
+// the others' strips), one has it alone where there are few (a short call waits for one item,
+// which more warps finish sooner).  Measured, one against several: 64 x 8k of 8 heads of 128, bf16:
+// 192 and 181 us; 200 x 700: 82 and 58; 48 windows of 1024 of 8 heads of 64: 31.5 and 27.1; 64 x 3000
+// of 4 heads of 256: 74.2 and 71.1 (int8 49.5 and 45.2); and 16 x 3000 of 4 heads of 256 (64 items):
+// 28.5 and 26.8, 4 x 3000: 14.4 and 15.4; 2 x 3000 of 8 heads of 128: 11.3 and 12.9; 4 x 128k of 4
+// heads of 256, int8: 113.6 and 117.6.  Sixteen columns of d = 256 leave no registers for it
+// (48 x 16k, 24 columns: 299 and 382 us).
 template <int KV>
 cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
-#define QW_PAGED(DD) \
-  case DD: return cols == 8 ? paged_launch_one<DD, KV, 1>(a, sms, st) : paged_launch_one<DD, KV, 2>(a, sms, st);
+  const bool many = 3ll * a.B * a.Hkv > sms;
+#define QW_PAGED(DD, C1, C2)                                               \
+  case DD:                                                                 \
+    return cols == 8 ? many ? paged_launch_one<DD, KV, 1, C1>(a, sms, st)  \
+                            : paged_launch_one<DD, KV, 1, 1>(a, sms, st)   \
+                     : many ? paged_launch_one<DD, KV, 2, C2>(a, sms, st)  \
+                            : paged_launch_one<DD, KV, 2, 1>(a, sms, st);
   switch (d) {
-    QW_PAGED(64)
-    QW_PAGED(128)
-    QW_PAGED(256)
+    QW_PAGED(64, 4, 4)
+    QW_PAGED(128, 4, 2)
+    QW_PAGED(256, 2, 1)
   }
 #undef QW_PAGED
   return cudaErrorInvalidValue;

@@ -79,6 +79,20 @@ def test_long_context_is_split_and_joined(q, kind, d, Hq, Hkv, page):
     check(q, c, window=9000, sinks=500)
 
 
+@pytest.mark.parametrize("kind,d", [(k, d) for k in ("fp16", "bf16", "int8") for d in (64, 128, 256)])
+@pytest.mark.parametrize("G,new", [(6, 1), (4, 4), (5, 13)])
+def test_many_sequences(q, kind, d, G, new):
+    """More items than a third of the SMs: several CTAs an SM, of 8, 16 and up to 64 columns;
+    long and short contexts, so that ranges cut items and hold many."""
+    lens = [1 + (i * 37) % 90 for i in range(40)] + [2200, 1, 700]
+    news = [min(n, 1 + (i * 5) % new) for i, n in enumerate(lens)]
+    c = Cache(lens, news, 2 * G, 2, d, 16 if d == 64 else 48, kind, nhd=d == 128, seed=d + new)
+    a, la = check(q, c, max_new=new)
+    b, lb = check(q, c, max_new=new)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+    check(q, c, window=70, sinks=3, max_new=new)
+
+
 def test_many_short_sequences(q):
     """More items than a CTA lists at a time (several lists a CTA)."""
     lens = [1 + (i * 7) % 40 for i in range(1500)]
