@@ -104,7 +104,7 @@ struct PagedShape {
   static constexpr int kRows = NB == 1 ? kCols : 4 * kCols;
   static_assert(NB == 1 || kKW >= 4, "a group a block");
   static constexpr int kRowBytes = D * kES;
-  static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? kStrip * 4 : 0);
+  static constexpr int kHalf = kStrip * kRowBytes + (KV == kPagedI8 ? 2 * kStrip * 4 : 0);      // (whole 128 bytes)
   // the exchange at an item's end: SW channels of each warp at a time, rows of SW + 4 floats
   // (column pairs 2 c and channels r8 of a warp's lanes fall on distinct banks); in between it
   // holds the halves' scores
@@ -725,12 +725,22 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
         const int lr = ln / CH, lc = ln % CH;
         if (plain) {                                       // rows at equal distances
           const long long o0 = __shfl_sync(0xffffffffu, off, 0);
-          const long long step = GW * RPI * a.tok_stride * P::kES;
           const uint8_t *src = base + o0 + (gi * RPI + lr) * a.tok_stride * P::kES + lc * 16;
+          // row i of this lane: the swizzle changes by bits of i alone (stages start on 128 bytes)
+          constexpr int NR = GW * RPI;
+          static_assert(NI % GW == 0 && (RB >= 128 || NR % 8 == 0) && P::kHalf % (RB < 128 ? RB : 128) == 0, "");
+          const uint32_t dst = st + strip_off<RB>(gi * RPI + lr, lc);
+          if (a.tok_stride == D) {                         // one after the other: no address to compute
 #pragma unroll
-          for (int i = 0; i < (NI + GW - 1) / GW; ++i) {
-            if (NI % GW == 0 || i * GW + gi < NI) cp_async16_full(st + strip_off<RB>((i * GW + gi) * RPI + lr, lc), src);
-            src += step;
+            for (int i = 0; i < NI / GW; ++i)
+              cp_async16_full((dst ^ (((i * NR) & 7) << 4)) + i * NR * RB, src + i * NR * RB);
+          } else {
+            const long long step = NR * a.tok_stride * P::kES;
+#pragma unroll
+            for (int i = 0; i < NI / GW; ++i) {
+              cp_async16_full((dst ^ (((i * NR) & 7) << 4)) + i * NR * RB, src);
+              src += step;
+            }
           }
         } else {
 #pragma unroll 1
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
       for (; u < g.u1; u += step) {
         const int key0 = (u < g.nsu ? u : g.first + u - g.nsu) * kStrip;
         // ---- S^T = K Q^T: element e of tile nb: key r8 + 8 (e / 2), column 2 c4 + (e & 1)
-        constexpr int CN = NB == 1 ? 4 : 2;                // independent sums (MMA latency)
+        constexpr int CN = NB == 1 ? 2 : 1;                // independent sums (MMA latency)
         float sp[CN][NB][4] = {};
         float ksc[2] = {a.scale_log2, a.scale_log2};
         {
