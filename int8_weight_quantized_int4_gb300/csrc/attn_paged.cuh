@@ -79,8 +79,9 @@ struct PagedSeg {
 // A CTA's list of work and the state to list the rest, in shared memory.
 struct PagedCtl {
   int nseg, more;               // segments listed; whether others follow
-  int njoin;                    // cut items this CTA was the last to finish
-  PagedSeg join[2];
+  int njoin, last;              // groups of parts this CTA was the last to finish
+  PagedSeg join[2];             // their items
+  int group[2];                 // and the first part of each
   int b;                        // walk: sequence
   int off, pos;                 // walk: place in the sequence, in all
   int begin, end, share;        // the range
@@ -536,16 +537,26 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
   return ctl->nseg != 0 || ctl->more != 0;
 }
 
-// Joins the parts of a cut item, in CTA order (the last CTA to finish it; all its threads).
+// More than 16 parts of a cut item are joined in groups of 2^this, then the groups: one CTA
+// reading 152 parts took longer than all the rest (131k keys of one KV head of 128: 51 us, in
+// groups of 16 31; of 256 with 64 columns, 60k keys: 207 and 89).
+__device__ __forceinline__ int paged_group(int parts) { return parts <= 16 ? 4 : parts <= 64 ? 3 : parts <= 256 ? 4 : 5; }
+
+// Joins n parts of a cut item, first, first + step, .., in order (all threads of the last CTA to
+// finish them): the item's rows, or (not FINAL) one part in place of the first.
 template <int D, int KV, int NB, int CTAS>
-__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g, float *red) {
+__device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g, int first, int step, int n, bool final,
+                                           float *red) {
   using P = PagedShape<D, KV, NB, CTAS>;
   constexpr int NT = P::kThreads, ROWS = P::kRows;
   constexpr bool BF = KV == kPagedBf16;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int row0 = g.rb * ROWS, nrows = min(ROWS, g.rows - row0), n = g.c1 - g.c0 + 1;
-  // the first part is in its CTA's slot 1, the others in their slots 0
-  auto slot = [&](int i) { return a.part + (size_t)(2 * (g.c0 + i) + (i == 0 ? 1 : 0)) * P::kPartFloats; };
+  const int row0 = g.rb * ROWS, nrows = min(ROWS, g.rows - row0);
+  // the item's first part is in its CTA's slot 1, the others in their slots 0
+  auto slot = [&](int i) {
+    const int k = first + i * step;
+    return a.part + (size_t)(2 * (g.c0 + k) + (k == 0 ? 1 : 0)) * P::kPartFloats;
+  };
   // `chunk` columns at a time: their parts' m and l in shared memory, then each part's weight
   const int chunk = min(nrows, P::kRedBytes / 8 / n);
   float *mm = red, *ll = red + chunk * n;
@@ -579,6 +590,13 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
         }
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      if (!final) {
+        if (r < nr && e == 0) {
+          slot(0)[r0 + r] = Mx;
+          slot(0)[ROWS + r0 + r] = Ls;
+        }
+        continue;
+      }
       const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
       if (r < nr)
 #pragma unroll 1
@@ -610,6 +628,10 @@ __device__ __forceinline__ void paged_join(const PagedArgs &a, const PagedSeg &g
             o.z += v[x].z * w;
             o.w += v[x].w * w;
           }
+      }
+      if (!final) {
+        reinterpret_cast<float4 *>(slot(0) + 2 * ROWS + (size_t)r0 * D)[i] = o;
+        continue;
       }
       const int gr = row0 + r0 + r;
       uint16_t *dst = a.out + ((long long)(g.tok0 + gr / a.G) * a.Hq + g.g * a.G + gr % a.G) * D + 4 * (i % (D / 4));
@@ -1116,14 +1138,16 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
       }
       if (!cut) continue;
 
-      // ---- a cut item: the last CTA to finish it joins the parts, in CTA order
+      // ---- a cut item: the last CTA to finish a group of its parts joins them, in CTA order
       // (the barrier and thread 0's release and acquire order every thread's accesses)
       __syncthreads();
-      const int n = g.c1 - g.c0 + 1;
       if (tid == 0) {
-        const int old = atom_add_acq_rel_gpu(a.counters + g.c0, 1);
-        if (old == n - 1) {
-          a.counters[g.c0] = 0;                          // zero again for the next call
+        const int n = g.c1 - g.c0 + 1, lg = paged_group(n), head = ((int)blockIdx.x - g.c0) >> lg << lg;
+        // (a CTA's first and last part may each begin a group: two counters)
+        int *counter = a.counters + kPagedMaxCtas + 2 * (g.c0 + head) + (head == 0 ? 1 : 0);
+        if (atom_add_acq_rel_gpu(counter, 1) == min(1 << lg, n - head) - 1) {
+          *counter = 0;                                  // zero again for the next call
+          ctl->group[ctl->njoin] = head;
           ctl->join[ctl->njoin++] = g;                   // (a range cuts two items at most)
         }
       }
@@ -1133,9 +1157,35 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
     if (tid == 0) ctl->nseg = 0;
     __syncthreads();
   }
-  // ---- the cut items that this CTA was the last to finish
+  // ---- the groups that this CTA was the last to finish; the last of an item's groups: the item
   __syncthreads();
-  for (int i = 0; i < ctl->njoin; ++i) paged_join<D, KV, NB, CTAS>(a, ctl->join[i], red);
+#pragma unroll 1
+  for (int i = 0; i < ctl->njoin; ++i) {
+    const PagedSeg &g = ctl->join[i];
+    const int n = g.c1 - g.c0 + 1, lg = paged_group(n), groups = (n + (1 << lg) - 1) >> lg;
+    if (groups == 1) {                                   // (apart, with its constants: 0.3 us a short call)
+      paged_join<D, KV, NB, CTAS>(a, g, 0, 1, n, true, red);
+      continue;
+    }
+    int first = ctl->group[i], step = 1, count = min(1 << lg, n - first);
+    bool final = false;
+#pragma unroll 1
+    for (;;) {
+      paged_join<D, KV, NB, CTAS>(a, g, first, step, count, final, red);
+      if (final) break;
+      if (tid == 0) {                                    // (the join ends with a barrier)
+        ctl->last = atom_add_acq_rel_gpu(a.counters + g.c0, 1) == groups - 1;
+        if (ctl->last) a.counters[g.c0] = 0;
+      }
+      __syncthreads();
+      final = ctl->last != 0;
+      __syncthreads();
+      if (!final) break;
+      first = 0;
+      step = 1 << lg;
+      count = groups;
+    }
+  }
 }
 
 template <int D, int KV, int NB, int CTAS>

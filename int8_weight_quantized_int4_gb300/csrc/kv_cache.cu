@@ -248,7 +248,7 @@ const void *append_kernel(int d) {
 // step's columns (new tokens x heads a KV head) fit (half the MMAs of 16), else up to four blocks
 // of 16.
 int paged_columns(int max_new, int G) { return (long long)max_new * G <= 8 ? 8 : 64; }
-constexpr size_t kPagedCounterBytes = 4096;      // one counter a CTA
+constexpr size_t kPagedCounterBytes = 3 * kPagedMaxCtas * 4;   // three counters a CTA
 constexpr int kPagedCtas = 4;                    // CTAs an SM, at most
 size_t paged_ws(int d, int cols, int sms) {
   return kPagedCounterBytes + (size_t)2 * kPagedCtas * sms * cols * (d + 2) * 4;
@@ -383,7 +383,7 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.G = Hq / c->Hkv;
   const int cols = paged_columns(max_new, a.G);
   const size_t need = paged_ws(c->d, cols, sms);
-  if (kPagedCtas * sms * 4 > (int)kPagedCounterBytes) return bad(QW_ERR_ARCH, "more than %zu SMs", kPagedCounterBytes / 4 / kPagedCtas);
+  if (kPagedCtas * sms > kPagedMaxCtas) return bad(QW_ERR_ARCH, "more than %d SMs", kPagedMaxCtas / kPagedCtas);
   if (!ws || ws_bytes < need)
     return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
   a.q = q;

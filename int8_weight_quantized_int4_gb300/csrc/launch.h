@@ -107,6 +107,7 @@ cudaError_t launch_attn(const AttnLaunch &L, cudaStream_t st);
 
 // Paged key-value cache (kv_cache.cu, attn_paged*.cu).  Cache types:
 enum { kPagedF16 = 0, kPagedBf16 = 1, kPagedI8 = 2 };
+constexpr int kPagedMaxCtas = 1024;
 struct PagedArgs {
   const uint16_t *q;            // [T][Hq][d], token and head strides q_tok, q_head (elements)
   uint16_t *out;                // [T][Hq][d] dense
@@ -124,7 +125,8 @@ struct PagedArgs {
   int min_places;               // fewest of them a CTA takes
   float scale_log2;             // softmax scale * log2(e)
   float *part;                  // [2 CTAs][rows (d + 2)] partial sums (workspace)
-  int *counters;                // [CTAs] arrivals, zero between calls (workspace)
+  int *counters;                // [kPagedMaxCtas] arrivals of an item's groups of parts, then [kPagedMaxCtas][2]
+                                //   of a group's parts; zero between calls (workspace)
   int *err;
 };
 cudaError_t launch_attn_paged_f16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);

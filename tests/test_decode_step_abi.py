@@ -89,7 +89,7 @@ def test_attn_refusals():
     assert call(T=(1 << 31) - 1) == q.QW_ERR_UNSUPPORTED_SHAPE
     assert call(T=0, qp=N0, out=N0, ws=N0) == q.QW_OK
     assert L.attn_paged_workspace_bytes(96, 8, 4, 1) == 0 and L.attn_paged_workspace_bytes(128, 6, 4, 1) == 0
-    assert L.attn_paged_workspace_zero_bytes(128, 8, 4, 1) == 4096
+    assert L.attn_paged_workspace_zero_bytes(128, 8, 4, 1) == 12288
 
 
 def test_copy_refusals():

@@ -79,6 +79,19 @@ def test_long_context_is_split_and_joined(q, kind, d, Hq, Hkv, page):
     check(q, c, window=9000, sinks=500)
 
 
+@pytest.mark.parametrize("kind,d,G,new", [("bf16", 128, 16, 1), ("fp16", 256, 16, 3), ("int8", 128, 12, 4),
+                                          ("fp16", 64, 7, 2), ("int8", 256, 5, 1)])
+def test_long_context_of_one_head(q, kind, d, G, new):
+    """One KV head over every SM: its parts are joined in groups, and the groups."""
+    for n in (2999, 33000):
+        c = Cache([n], [new], G, 1, d, 16, kind, seed=n)
+        a, la = check(q, c)
+        for _ in range(5):
+            lse = torch.empty_like(la)
+            b, lb = q.attn_paged(c.q, *c.args(), max_new=new, lse=lse, **c.kw)
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+
+
 @pytest.mark.parametrize("kind,d", [(k, d) for k in ("fp16", "bf16", "int8") for d in (64, 128, 256)])
 @pytest.mark.parametrize("G,new", [(6, 1), (4, 4), (5, 13)])
 def test_many_sequences(q, kind, d, G, new):
