@@ -422,6 +422,9 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   for (most = blocks * (a.cap / 4 + 128); most > (1ll << 30); most = blocks * ((a.cap / 4 >> a.shift) + 128)) {
     if (++a.shift > 24) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   }
+  // A CTA takes 12 places at least: with 6, one context of 1000 keys (8 heads of 128) takes 10.7 us
+  // instead of 11.3 but one of 4000 14.8 instead of 13.6 (more parts to join); with 24, 1000 keys of
+  // 4 heads of 256 with 12 columns 18.6 instead of 15.4, with 36 columns 22.6 instead of 24.7.
   a.min_places = 12;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.counters = static_cast<int *>(ws);
