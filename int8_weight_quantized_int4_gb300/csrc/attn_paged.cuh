@@ -37,12 +37,12 @@
 //     is being finished.
 //
 // Measured (K and V rows read / time): 64 ragged contexts of up to 8190, 32/8 heads of 128, bf16:
-// 181 us, 6.4 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 113.6 us, 5.88 TB/s (the
+// 176 to 181 us, 6.4 to 6.6 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 111 us, 6.0 TB/s (the
 // codes' conversion to fp16 takes half of the issue slots); 16 of up to 16384 with up to 6 new
-// tokens, fp16: 148.5 us, 4.76 TB/s (36 columns: the strip is read once from HBM and up to
-// twice more from L2, and the columns' exponents and products take the rest); a window of
-// 1024, 48 contexts, 64/8 heads of 64, fp16: 27.2 us, 3.7 TB/s (items of 66 strips: their
-// starts and joins); one context of 1003, 24/4 heads of 256, fp16: 12.1 us, nearly all of it the
+// tokens, fp16: 149 us, 4.74 TB/s (up to 36 columns: a strip is read once from HBM and up to
+// twice more from L2, whose 31 bytes a clock an SM are the bound); a window of
+// 1024, 48 contexts, 64/8 heads of 64, fp16: 26.9 us, 3.7 TB/s (items of 66 strips: their
+// starts and joins); one context of 1003, 24/4 heads of 256, fp16: 12.2 us, nearly all of it the
 // chain launch -> lengths -> page table -> keys -> exchange -> partial sums -> join.
 //
 // Roundings: p is rounded to the values' 16-bit type for the P.V product (fp16 2^-11, bf16

@@ -168,7 +168,7 @@ __device__ __forceinline__ void copy_piece(const uint8_t *src, uint8_t *dst, uns
 
 // One warp a piece of 256 vectors of one page of one layer of one pool (eight loads in
 // flight a lane); the pieces of all pools and layers in one launch.  1000 pages of 16 layers
-// (int8 K and V and their scales, 2.13 GB read and written) in 311 us: 6.84 TB/s, the rate of a
+// (int8 K and V and their scales, 2.13 GB read and written) in 312 us: 6.83 TB/s, the rate of a
 // plain copy; one page of 16 layers in 2.3 us, its launch.
 __global__ void __launch_bounds__(32 * kCopyWarps) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
   const int lane = threadIdx.x & 31;

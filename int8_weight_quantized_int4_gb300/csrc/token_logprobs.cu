@@ -30,8 +30,8 @@
 // a warp and row; for few rows the launch and two chains of block-wide steps (the part's sums
 // and list, then the join's).
 //
-// Measured: 2048 rows of 50257 bf16 (206 MB), no alternatives: 42.2 us, 4.9 TB/s; 64 of 128257
-// binary32 with 20 alternatives: 17.4 us, 1.9 TB/s; one of 248320 fp16 with 20: 12.2 us.
+// Measured: 2048 rows of 50257 bf16 (206 MB), no alternatives: 41.9 us, 4.9 TB/s; 64 of 128257
+// binary32 with 20 alternatives: 17.2 us, 1.9 TB/s; one of 248320 fp16 with 20: 12.2 us.
 #include <float.h>
 #include <stdarg.h>
 #include <stdint.h>
