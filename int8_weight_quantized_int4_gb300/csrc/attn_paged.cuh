@@ -24,9 +24,10 @@
 //     hide each other's waits where six could not.
 //   - More than 16 columns are dealt to the groups in blocks of 16: the groups of different
 //     blocks stream the same strips at the same time, the first from HBM and the others from
-//     L2.  (As items of their own the blocks came too far apart: 5 % L2 hits and 170 us where
-//     this takes 154; groups of two to four warps with 16 columns each, reading a strip
-//     once for all of them, took 188 to 421: 16 sequences of up to 16384, 6 to 36 columns, d = 256.)
+//     L2.  (16 sequences of up to 16384, 6 to 36 columns, d = 256: 149 us.  As items of their
+//     own the blocks came too far apart, 5 % L2 hits and 21 us more; groups of two to four warps
+//     with 16 columns each, reading a strip once for all of them, took 188 to 421 us, rings
+//     shared through counting barriers 151 at best.)
 //   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
 //     (sequence, column block, KV head) item are laid end to end and cut into one equal range
 //     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
