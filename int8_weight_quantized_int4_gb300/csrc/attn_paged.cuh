@@ -396,6 +396,7 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
   if (tid == 0) {
     ctl->nseg = ctl->more = ctl->njoin = 0;
   }
+  __syncwarp();                  // before the first warp's other lanes count up (shuffles order no memory)
   if (a.B > 32 || warp == 0) {
     const int per = a.B > 32 ? (a.B + NT - 1) / NT : 1;
     const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);

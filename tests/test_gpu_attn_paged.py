@@ -106,6 +106,21 @@ def test_many_sequences(q, kind, d, G, new):
     check(q, c, window=70, sinks=3, max_new=new)
 
 
+@pytest.mark.parametrize("lens", [[700], [3, 900, 0, 45, 2100, 1, 16], [1 + (i * 131) % 700 for i in range(32)]])
+def test_short_schedules_repeat(q, lens):
+    """Up to 32 sequences, whose schedule one warp makes: every launch lists all its work, so
+    rows that were NaN before are the same each time."""
+    c = Cache(lens, [min(1, n) for n in lens], 16, 4, 128, 16, "bf16", seed=len(lens))
+    want, _ = check(q, c)
+    out = torch.empty(100, *want.shape, dtype=want.dtype, device=DEV)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        for o in out:
+            q.attn_paged(c.q, *c.args(), out=o)
+        assert bool((out.view(torch.int16) == want.contiguous().view(torch.int16)).all())
+    assert q.device_error() == 0
+
+
 def test_many_short_sequences(q):
     """More items than a CTA lists at a time (several lists a CTA)."""
     lens = [1 + (i * 7) % 40 for i in range(1500)]
