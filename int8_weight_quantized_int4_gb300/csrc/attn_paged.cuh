@@ -852,6 +852,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
           pos[nb][e] = gr < g.rows ? g.pos0 + gr / a.G : -1;
         }
       const int pmin = g.pos0 + row0 / a.G, pmax = g.pos0 + (min(g.rows, row0 + COLS) - 1) / a.G;
+      // whether the item's columns, whose keys are loaded together, lie at several positions
+      const bool mixed = g.rb * ROWS / a.G != (min(g.rows, g.rb * ROWS + ROWS) - 1) / a.G;
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1001,10 +1003,11 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
         // ---- O^T += V^T P^T
         bool odd = false;
         if constexpr (!I8) {
-          // columns at several positions: a key hidden from some has weight 0 there, and 0
-          // times an infinite or NaN value would reach them through the MMA.  Strips that
-          // hold such a value are summed without the hidden products.
-          odd = masked && pmin != pmax && strip_nonfinite<D, BF>(vst, lane);
+          // an item's columns at several positions: a key hidden from some (this group's may
+          // all be at one) has weight 0 there, and 0 times an infinite or NaN value would reach
+          // them through the MMA.  Strips that hold such a value are summed without the hidden
+          // products.
+          odd = masked && mixed && strip_nonfinite<D, BF>(vst, lane);
         }
         uint32_t pf[NB][2];
 #pragma unroll

@@ -197,6 +197,35 @@ def test_hidden_values_never_reach_a_row(q, kind, value):
                 assert not bool(torch.isfinite(out[t, :6, 10:14]).any())
 
 
+@pytest.mark.parametrize("kind,d", [("fp16", 64), ("bf16", 128), ("fp16", 256), ("bf16", 256)])
+@pytest.mark.parametrize("G,new", [(16, 2), (16, 4), (32, 2), (6, 3), (6, 6), (8, 3), (8, 5), (12, 2), (64, 3)])
+def test_hidden_values_of_other_blocks(q, kind, d, G, new):
+    """Columns in blocks of 16: a block that lies in one token shares its strips with blocks of
+    other tokens, whose keys it does not see.  Every key that some token does not see holds an
+    infinity or a NaN in turn; the rows that do not see it stay as they were."""
+    n, window = 70, 37
+    for win, sinks in ((0, 0), (window, 0), (window, 2)):
+        c = Cache([n, 33], [new, 1], 2 * G, 2, d, 16, kind, seed=G + new)
+        clean = c.reference(win, sinks)
+        tol, _ = c.tolerances(clean)
+        first = n - new                                      # position of the first new token
+        keys = list(range(first + 1, n)) + ([j for j in range(first - win + 1, n - win)] if win else [])
+        for i, j in enumerate(keys):
+            pid, off = c.row(0, j)
+            kept = c.v[pid, :, off].clone()
+            c.v[pid, :, off, 5:9] = (float("inf"), float("nan"), float("-inf"))[i % 3]
+            out = q.attn_paged(c.q, *c.args(), max_new=new, window=win, sinks=sinks)
+            c.v[pid, :, off] = kept
+            for t in range(new):
+                at = first + t
+                if j <= at and (not win or j > at - win or j < sinks):
+                    assert not bool(torch.isfinite(out[t, :, 5:9]).any())
+                else:
+                    assert bool(((out[t].double() - clean[0][t]).abs() <= tol[t]).all()), (win, j, t)
+            assert bool(((out[new:].double() - clean[0][new:]).abs() <= tol[new:]).all())
+    assert q.device_error() == 0
+
+
 def test_int8_hidden_scales(q):
     c = Cache([60], [5], 4, 1, 64, 16, "int8", seed=2)
     clean = c.reference()
