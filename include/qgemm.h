@@ -344,7 +344,8 @@ int kv_copy_pages(const qw_page_pool_t *pools, int n_pools, const int32_t *pairs
  *   entry points.
  * Values of keys that a token does not see never reach its row, whatever they hold.  A page
  * id outside [0, num_pages) reads as rows of zeros, a length beyond the page table as the
- * table's end, and either sets QW_ERR_BAD_INDEX.  Results are bit-identical between calls
+ * table's end, offsets outside 0 .. T as the nearest of these; each sets QW_ERR_BAD_INDEX, as
+ * do offsets that descend, which leave the call's rows unspecified.  Results are bit-identical between calls
  * (on devices with the same number of SMs).  One launch, async.  Returns as kv_append, or
  * QW_ERR_WORKSPACE.
  * ------------------------------------------------------------------------ */

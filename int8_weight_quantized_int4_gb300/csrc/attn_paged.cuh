@@ -407,13 +407,16 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
       for (int rb = 0, n = blocks(s); rb < n; ++rb) c += paged_places(a, paged_span<ROWS>(a, s, rb).n, paged_blocks<ROWS>(s.nq * a.G, rb)) + IC;
       return c * a.Hkv;
     };
+    // Sums stop past kPagedMaxPlaces.  Offsets in order stay below it (the host's shift); sequences
+    // whose offsets overlap could name more tokens than there are, and pass 2^31.
+    auto add = [](int x, int y) { return (int)min((unsigned)x + (unsigned)y, kPagedMaxPlaces + 1u); };
     // sums before this thread and over all (of the warp, or through shared memory)
     auto scan = [&](int v, int &before, int &all) {
       int inc = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
+        if (lane >= o) inc = add(inc, t);
       }
       before = inc - v;
       all = __shfl_sync(0xffffffffu, inc, 31);
@@ -425,8 +428,8 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           const int x = ctl->part[w];
-          before += w < warp ? x : 0;
-          all += x;
+          before = add(before, w < warp ? x : 0);
+          all = add(all, x);
         }
       }
     };
@@ -439,9 +442,9 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
       const int n = blocks(own);
       if (n == 1) {
         first = paged_span<ROWS>(a, own, 0);
-        mine += (paged_places(a, first.n, paged_blocks<ROWS>(own.nq * a.G, 0)) + IC) * a.Hkv;
+        mine = add(mine, (paged_places(a, first.n, paged_blocks<ROWS>(own.nq * a.G, 0)) + IC) * a.Hkv);
       } else {
-        mine += cost(own);
+        mine = add(mine, cost(own));
       }
       items += n * a.Hkv;
     }
@@ -455,7 +458,9 @@ __device__ __forceinline__ bool paged_schedule(const PagedArgs &a, PagedSeg *seg
     // places a CTA takes when items have CTAs of their own (the items' parts then fit the grid)
     const int left = grid - all_items;
     const int size = per == 1 && left > 0 && a.shift == 0 ? max(paged_div(total - IC * all_items + left - 1, left), a.min_places) : 0;
-    if (size > 0 && size <= share + 2 * IC) {
+    if (total > (int)kPagedMaxPlaces) {
+      // offsets that overlap (recorded by paged_seq): no places to cut, so nothing is computed
+    } else if (size > 0 && size <= share + 2 * IC) {
       int parts = 0, pp;
 #pragma unroll 1
       for (int rb = 0, n = blocks(own), len; rb < n; ++rb)

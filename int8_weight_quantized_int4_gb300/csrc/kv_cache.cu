@@ -419,7 +419,7 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   long long most = ((long long)T * a.G / cols + b->B) * c->Hkv;
   if (most > (1ll << 28)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   const long long blocks = most;
-  for (most = blocks * (a.cap / 4 + 128); most > (1ll << 30); most = blocks * ((a.cap / 4 >> a.shift) + 128)) {
+  for (most = blocks * (a.cap / 4 + 128); most > (long long)kPagedMaxPlaces; most = blocks * ((a.cap / 4 >> a.shift) + 128)) {
     if (++a.shift > 24) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns");
   }
   // A CTA takes 12 places at least: with 6, one context of 1000 keys (8 heads of 128) takes 10.7 us

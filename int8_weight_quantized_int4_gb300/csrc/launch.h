@@ -108,6 +108,7 @@ cudaError_t launch_attn(const AttnLaunch &L, cudaStream_t st);
 // Paged key-value cache (kv_cache.cu, attn_paged*.cu).  Cache types:
 enum { kPagedF16 = 0, kPagedBf16 = 1, kPagedI8 = 2 };
 constexpr int kPagedMaxCtas = 1024;
+constexpr unsigned kPagedMaxPlaces = 1u << 30;   // of all items of a call
 struct PagedArgs {
   const uint16_t *q;            // [T][Hq][d], token and head strides q_tok, q_head (elements)
   uint16_t *out;                // [T][Hq][d] dense
@@ -121,8 +122,8 @@ struct PagedArgs {
   int window, sinks;            // window 0: every key up to the position; sinks 0 without one
   int page_shift;               // log2(page), -1 where page is no power of two
   int strip_pages;              // page % 16 == 0: a strip of 16 keys lies in one page
-  int shift;                    // the schedule counts keys in 2^shift strips of 16
-  int min_places;               // fewest of them a CTA takes
+  int shift;                    // the schedule counts places (a strip of 16 keys for a block of columns) in 2^shift
+  int min_places;               // fewest of those units a CTA takes
   float scale_log2;             // softmax scale * log2(e)
   float *part;                  // [2 CTAs][rows (d + 2)] partial sums (workspace)
   int *counters;                // [kPagedMaxCtas] arrivals of an item's groups of parts, then [kPagedMaxCtas][2]

@@ -275,6 +275,42 @@ def test_offsets_out_of_order(q):
     assert q.device_error() == q.QW_ERR_BAD_INDEX
 
 
+@pytest.mark.parametrize("cu,left", [([1, 3, 2, 4], [0, 4, 5]), ([-7, 1, 1, 2], [2, 3, 4, 5]),
+                                     ([5, 900, 900, 900], [0, 1, 2, 3, 4]), ([6, -2, -2, 0], [0, 1, 2, 3, 4, 5])])
+def test_offsets_stay_inside(q, cu, left):
+    """Offsets that descend or leave 0 .. T write no row outside q's nor one of no sequence."""
+    c = Cache([40, 40, 40], [2, 2, 2], 4, 2, 64, 16, "fp16", seed=6)
+    c.cu.copy_(torch.tensor(cu, device=DEV))
+    big = torch.full((c.T + 16, 4, 64), 3.0, dtype=torch.float16, device=DEV)
+    lse = torch.full((c.T + 16, 4), 3.0, device=DEV)
+    q.attn_paged(c.q, *c.args(), max_new=2, out=big[8:8 + c.T], lse=lse[8:8 + c.T])
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and q.device_error() == 0
+    keep = torch.ones(c.T + 16, dtype=torch.bool, device=DEV)
+    keep[8:8 + c.T] = False
+    keep[[8 + t for t in left]] = True
+    assert bool((big[keep] == 3.0).all()) and bool((lse[keep] == 3.0).all())
+    assert bool(torch.isfinite(big.float()).all()) and not bool((big[~keep] == 3.0).any())
+
+
+def test_overlapping_offsets_past_2_to_31_places(q):
+    """Offsets that descend can name each token many times: 128 sequences of all 4096 tokens, 64
+    heads and 4096 strips would be 17 * 2^30 places.  Nothing is computed, and the next call,
+    with the same workspace, is right."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    T, H, B = 4096, 64, 256
+    k = torch.randn(1, H, 1024, 64, device=DEV).half()
+    table = torch.zeros(B, 64, **i32)
+    lens = torch.full((B,), 65536, **i32)
+    cu = torch.tensor([0, T] * (B // 2) + [0], **i32)
+    qq = torch.randn(T, H, 64, device=DEV).half()
+    ws = q.Workspace(torch.device("cuda:0"))
+    out = torch.full_like(qq, 3.0)
+    q.attn_paged(qq, k, k, table, lens, cu, out=out, ws=ws)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and bool((out == 3.0).all())
+    c = Cache([40, 3000], [1, 1], 64, 64, 64, 16, "fp16", seed=6)
+    check(q, c, ws=ws)
+
+
 def test_rows_of_no_sequence_are_left(q):
     c = Cache([30, 30], [1, 1], 4, 2, 64, 16, "fp16", seed=6)
     c.cu[2] = 1
