@@ -92,6 +92,80 @@ def test_long_context_of_one_head(q, kind, d, G, new):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
 
 
+def count_case(kind, d, lens, news, Hkv, G, page, seed=0):
+    """A batch whose scores are all 0 and whose values count: strip s (16 keys) of a sequence is 1
+    in channel s % d of even heads and s // d % d of odd ones, else 0.  Returns (q, args, scales)."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pid = torch.randperm(sum(need) + 2, generator=g).to(DEV)
+    act = torch.bfloat16 if kind == "bf16" else torch.float16
+    store = torch.int8 if kind == "int8" else act
+    v = torch.zeros(sum(need) + 2, Hkv, page, d, dtype=store, device=DEV)
+    k = torch.randint(-3, 4, v.shape, device=DEV).to(store)
+    table = torch.zeros(len(lens), max(need), dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = pid[at:at + need[b]]
+        strip = torch.arange(need[b] * page, device=DEV) // 16
+        for h in range(Hkv):
+            one = torch.nn.functional.one_hot((strip // d if h % 2 else strip) % d, d).to(store)
+            v[pid[at:at + need[b]], h] = one.view(need[b], page, d)
+        at += need[b]
+    cu = [0]
+    for x in news:
+        cu.append(cu[-1] + x)
+    qq = torch.randn(cu[-1], Hkv * G, d, generator=g).to(act).to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    kw = {}
+    if kind == "int8":
+        kw = {s: torch.full(v.shape[:3], 1.0, device=DEV) for s in ("k_scale", "v_scale")}
+    return qq, (k, v, table, torch.tensor(lens, **i32), torch.tensor(cu, **i32)), kw
+
+
+@pytest.mark.parametrize("kind,d,Hkv,G,new", [("bf16", 128, 2, 8, 1), ("fp16", 256, 4, 6, 1), ("fp16", 256, 2, 6, 6),
+                                              ("int8", 256, 2, 6, 1), ("int8", 128, 2, 9, 7), ("fp16", 64, 2, 16, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9000, 500)])
+def test_every_strip_counts_once(q, kind, d, Hkv, G, new, window, sinks):
+    """With scores of 0 every visible key weighs 1 / n.  A strip that is skipped or taken twice
+    moves its channel by 16 keys of at most 2060 (n / d or 16 d of them), 2^-8, and the log of the sum by
+    16 / n >= 2^-13.  All sums are of whole numbers below 2^24, scaled by powers of two; what rounds is
+    the output (u), the quotient and the logarithms (a few 2^-24)."""
+    u = torch.finfo(torch.bfloat16 if kind == "bf16" else torch.float16).eps / 2
+    for lens in ([20011], [33000], [131071], [20011, 3, 33000, 700, 16], [3001] * 60):
+        news = [min(new, n) for n in lens]
+        qq, args, kw = count_case(kind, d, lens, news, Hkv, G, 32, seed=len(lens))
+        lse = torch.empty(qq.shape[:2], device=DEV)
+        out, _ = q.attn_paged(qq, *args, max_new=new, window=window, sinks=sinks, scale=0.0, lse=lse, **kw)
+        assert q.device_error() == 0
+        t = 0
+        for n, m in zip(lens, news):
+            for at in range(n - m, n):
+                key = torch.arange(at + 1, device=DEV)
+                if window:
+                    key = key[(key > at - window) | (key < sinks)]
+                for h in range(Hkv):
+                    c = (key // 16 // d if h % 2 else key // 16) % d
+                    want = torch.bincount(c, minlength=d).double() / key.numel()
+                    got = out[t, h * G:(h + 1) * G].double()
+                    assert bool(((got - want).abs() <= u * want * 1.01 + 2.0 ** -25).all()), (n, at, h)
+                ln = torch.tensor(float(key.numel()), dtype=torch.float64).log().item()
+                assert float((lse[t].double() - ln).abs().max()) <= 16 * 2.0 ** -24 * (1 + ln), (n, at)
+                t += 1
+
+
+@pytest.mark.parametrize("kind,d,G,new", [("fp16", 256, 6, 1), ("bf16", 128, 4, 13), ("int8", 64, 16, 2), ("int8", 128, 8, 1)])
+@pytest.mark.parametrize("extra", [1 << 15, 1 << 18, (1 << 20) - 64])
+def test_wide_page_tables(q, kind, d, G, new, extra):
+    """Tables that could name up to 2^30 keys: the schedule counts places in larger units."""
+    lens = [1 + (i * 37) % 90 for i in range(30)] + [5200, 1, 700]
+    news = [min(n, 1 + (i * 5) % new) for i, n in enumerate(lens)]
+    c = Cache(lens, news, 2 * G, 2, d, 1024, kind, seed=d + new, extra_pages=extra)
+    a, la = check(q, c, max_new=new)
+    b, lb = check(q, c, max_new=new)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+    check(q, c, window=300, sinks=3, max_new=new)
+
+
 @pytest.mark.parametrize("kind,d", [(k, d) for k in ("fp16", "bf16", "int8") for d in (64, 128, 256)])
 @pytest.mark.parametrize("G,new", [(6, 1), (4, 4), (5, 13)])
 def test_many_sequences(q, kind, d, G, new):
