@@ -505,10 +505,14 @@ int qw_get_option(int option);
  *                         itself fails.
  *   qw_num_kernel_launches  number of kernels this library has enqueued in
  *                         this process (all devices, all threads).
+ *   qw_stream_capture_id  0 when `stream` is not being captured into a graph, else a
+ *                         number of the capture, unique in the process: workspaces that
+ *                         a capture allocates and zero-fills belong to it alone.
  * ------------------------------------------------------------------------ */
 const char *qw_last_error_string(void);
 int qw_device_error(qw_stream_t stream);
 long long qw_num_kernel_launches(void);
+unsigned long long qw_stream_capture_id(qw_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Measurement and verification tools (not on the GEMM's path).

@@ -120,6 +120,7 @@ SIGNATURES = {
     "qw_last_error_string": (ctypes.c_char_p, []),
     "qw_device_error": (_i, [_p]),
     "qw_num_kernel_launches": (_ll, []),
+    "qw_stream_capture_id": (ctypes.c_ulonglong, [_p]),
     "qw_set_option": (_i, [_i, _i]),
     "qw_get_option": (_i, [_i]),
     "qw_diag_mma_peak": (_i, [_i, _i, _i, _i, _p, ctypes.POINTER(ctypes.c_double), _p]),
@@ -256,34 +257,72 @@ def workspace_bytes(mode: int, M: int, N: int, K: int) -> int:
     return int(lib().qgemm_workspace_bytes(mode, M, N, K))
 
 
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+def _capture_id(index):
+    """A number of the graph being captured on device `index`'s current stream, 0 without one."""
+    if index == _current_device() and not _is_capturing():
+        return 0
+    return int(lib().qw_stream_capture_id(_raw_stream(index)))
+
+
 class Workspace:
-    """A zero-initialised device workspace that grows on demand (one per stream)."""
+    """A zero-initialised device workspace that grows on demand (one per stream).
+
+    A buffer that a graph was captured with stays allocated as long as the Workspace lives,
+    whatever later calls need; the Workspace has to outlive the graph.  A capture that finds no
+    large enough buffer gets one of its own from the graph's memory, zero-filled at every
+    replay (a call of the same sizes before the capture saves that)."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._index = self.device.index if self.device.type == "cuda" else -1    # -1: host memory
+        self._held = []                     # buffers that graphs were captured with
+        self._own = (0, None)               # the latest capture and the buffer of its own
 
     def get(self, mode: int, M: int, N: int, K: int):
         with torch.cuda.device(self.device):
             need = workspace_bytes(mode, M, N, K)
-        if need == 0:
-            return None, 0
-        if self.buf is None or self.buf.numel() < need:
-            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        return self.buf, self.buf.numel()
+        return self.get_bytes(need)
 
     def get_bytes(self, need: int):
-        """The buffer, grown to at least `need` bytes (zero-filled when grown)."""
+        """A buffer of at least `need` bytes (zero-filled when it is made)."""
         if need == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() < need:
-            self.buf = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        return self.buf, self.buf.numel()
+        index = self._index
+        capture = _capture_id(_current_device() if index is None else index) if index != -1 else 0
+        buf = self.buf
+        fits = buf is not None and buf.numel() >= need
+        if not capture:
+            if not fits:
+                buf = self.buf = self._zeros(need)
+        elif fits:
+            if not any(x is buf for x in self._held):
+                self._held.append(buf)
+        else:
+            owner, buf = self._own
+            if owner != capture or buf.numel() < need:
+                buf = self._zeros(need)
+                self._own = (capture, buf)
+        return buf, buf.numel()
+
+    def _zeros(self, n):
+        return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def zero(self):
-        """Zero-fill the buffer again (needed after a call that ended in QW_ERR_TIMEOUT)."""
-        if self.buf is not None:
-            self.buf.zero_()
+        """Zero-fill the buffers again (needed after a call that ended in QW_ERR_TIMEOUT)."""
+        for x in {id(x): x for x in (self.buf, *self._held) if x is not None}.values():
+            x.zero_()
 
 
 _default_ws = {}
@@ -496,12 +535,6 @@ assert struct.calcsize("@Piiqqq") == ctypes.sizeof(PagePoolDesc)
 _i32, _f32 = torch.int32, torch.float32
 
 
-def _raw_stream(index):
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _step = {}
 
 
@@ -529,7 +562,8 @@ def _run(index, fn, *args):
 
 
 def _scratch(ws, index, stream, kind, query, *args):
-    """(pointer, bytes) of `ws`, or of the default workspace of this kind of call and stream."""
+    """(buffer, pointer, bytes) of `ws`, or of the default workspace of this kind of call and
+    stream.  The caller keeps the buffer until its call is enqueued."""
     if ws is None:
         ws = _default_ws.get((index, stream, kind))
         if ws is None:
@@ -540,7 +574,7 @@ def _scratch(ws, index, stream, kind, query, *args):
         with torch.cuda.device(index):
             need = query(*args)
     buf, nbytes = ws.get_bytes(need)
-    return (None if buf is None else buf.data_ptr()), nbytes
+    return buf, (None if buf is None else buf.data_ptr()), nbytes
 
 
 def _kv_cache(k_pages, v_pages, k_scale, v_scale, index):
@@ -663,9 +697,10 @@ def attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, max_new: in
                             or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor {(T, Hq)} on the cache's device")
     stream = _raw_stream(index)
-    buf, nbytes = _scratch(ws, index, stream, "paged", _step_fn("attn_paged_workspace_bytes"), d, Hq, heads, max_new)
+    buf, pbuf, nbytes = _scratch(ws, index, stream, "paged", _step_fn("attn_paged_workspace_bytes"), d, Hq, heads,
+                                 max_new)
     _run(index, _step_fn("attn_paged"), cache, batch, q.data_ptr(), T, Hq, qt, qh, max_new, window, sinks,
-         d ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), buf, nbytes,
+         d ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), pbuf, nbytes,
          stream)
     return out if lse is None else (out, lse)
 
@@ -785,9 +820,10 @@ def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> T
         top, idx = empty((M, k), dtype=_f32, device=dev), empty((M, k), dtype=_i32, device=dev)
         ptop, pidx = top.data_ptr(), idx.data_ptr()
     stream = _raw_stream(index)
-    wbuf, nbytes = _scratch(ws, index, stream, "logprobs", _step_fn("token_logprobs_workspace_bytes"), M, N, k, dtype)
+    buf, pbuf, nbytes = _scratch(ws, index, stream, "logprobs", _step_fn("token_logprobs_workspace_bytes"), M, N, k,
+                                 dtype)
     _run(index, _step_fn("token_logprobs"), logits.data_ptr(), dtype, M, N, row, tokens.data_ptr(),
-         4 if tt is _i32 else 8, C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ptop, pidx, wbuf, nbytes,
+         4 if tt is _i32 else 8, C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ptop, pidx, pbuf, nbytes,
          stream)
     return TokenLogprobs(logprob, entropy, lse, top, idx)
 

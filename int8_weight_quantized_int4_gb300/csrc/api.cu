@@ -598,6 +598,17 @@ int qw_device_error(qw_stream_t stream) {
 
 long long qw_num_kernel_launches(void) { return g_launches.load(std::memory_order_relaxed); }
 
+unsigned long long qw_stream_capture_id(qw_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &id);
+  if (e != cudaSuccess) {
+    cudaGetLastError();                 // (a legacy stream during another's capture, or no device)
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 int qw_set_option(int option, int value) {
   if (option == QW_OPT_WEIGHTS_IMMUTABLE && (value == 0 || value == 1)) {
     g_opt_weights_immutable.store(value, std::memory_order_relaxed);

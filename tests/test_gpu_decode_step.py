@@ -67,3 +67,49 @@ def test_example_runs(ex, cache, capsys):
     assert len(out) == 4 and all(len(o) == 24 for o in out) and len({o[0] for o in out}) == 4
     assert torch.isfinite(logits.float()).all() and logits.shape == (2, model.vocab)
     assert "verify" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("first", [0, 1])
+def test_decode_and_verify_graphs_in_turn(ex, own, first):
+    """A decode step and a verify step, each captured into a graph of its own, with no workspace
+    given or with one that only the smaller step has sized, then replayed in turn: the eager
+    calls' bits.  The verify step's attention needs eight times the workspace."""
+    q, dev = ex.q, ex.DEV
+    g = torch.Generator(device=dev).manual_seed(3)
+    k, v = torch.randn(2, 400, 2, 16, 128, generator=g, device=dev).half()
+    lens = torch.tensor([3000, 70, 1500], dtype=torch.int32, device=dev)
+    table = torch.stack([torch.randperm(400, generator=g, device=dev)[:190].int() for _ in range(3)])
+    ws = [q.Workspace(dev), q.Workspace(dev)] if own else [None, None]
+
+    def step(new, vocab):
+        cu = torch.arange(0, 3 * new + 1, new, dtype=torch.int32, device=dev)
+        x = torch.randn(3 * new, 16, 128, generator=g, device=dev).half()
+        y = torch.randn(3 * new, vocab, generator=g, device=dev).half()
+        tok = torch.zeros(3 * new, dtype=torch.int32, device=dev)
+
+        def run():
+            return (q.attn_paged(x, k, v, table, lens, cu, max_new=new, ws=ws[0]),
+                    *q.token_logprobs(y, tok, k=8, ws=ws[1]))
+        return run
+    steps = [step(1, 3000), step(6, 70000)]
+    if own:
+        steps[0]()
+    torch.cuda.synchronize()
+    graphs, outs = [None, None], [None, None]
+    for i in (first, 1 - first):
+        graphs[i] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[i]):
+            outs[i] = steps[i]()
+    junk = [torch.full((1 << 22,), 0x3f, dtype=torch.uint8, device=dev) for _ in range(8)]   # over what was given back
+    want = [s() for s in steps]
+    for i in (1 - first, first, 0, 1, 1, 0):
+        for o in outs[i]:
+            o.fill_(-1)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs[i], want[i]):
+            assert torch.equal(a, b)
+        again = steps[i]()
+        assert all(torch.equal(a, b) for a, b in zip(again, want[i]))
+    assert q.device_error() == 0 and len(junk) == 8

@@ -1,0 +1,69 @@
+"""Workspace's bookkeeping, on host buffers: what a captured graph holds stays allocated, and a
+capture gets no buffer that only its own replay would zero."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+import int8_weight_quantized_int4_gb300 as q
+
+
+@pytest.fixture
+def capture(monkeypatch):
+    """A switch: the number of the graph being captured, 0 for none."""
+    now = [0]
+    monkeypatch.setattr(q, "_capture_id", lambda index: now[0], raising=False)
+
+    def switch(n):
+        now[0] = n
+    return switch
+
+
+def host_workspace():
+    ws = q.Workspace("cpu")
+    ws._index = 0                       # as a device's, so that captures are asked for
+    return ws
+
+
+def test_growth_keeps_the_buffer_a_graph_was_captured_with(capture):
+    ws = host_workspace()
+    small, _ = ws.get_bytes(100)
+    capture(1)
+    assert ws.get_bytes(100)[0] is small
+    capture(0)
+    alive = weakref.ref(small)
+    del small
+    big, n = ws.get_bytes(1000)
+    gc.collect()
+    assert n == 1000 and ws.get_bytes(100)[0] is big
+    assert alive() is not None and alive().data_ptr() != big.data_ptr()
+
+
+def test_growth_without_a_capture_gives_the_buffer_back(capture):
+    ws = host_workspace()
+    alive = weakref.ref(ws.get_bytes(100)[0])
+    ws.get_bytes(1000)
+    gc.collect()
+    assert alive() is None
+
+
+def test_a_buffer_made_in_a_capture_serves_that_graph_only(capture):
+    """Its zero-fill is a node of the graph: no other graph, and no eager call, may rely on it."""
+    ws = host_workspace()
+    capture(1)
+    a, n = ws.get_bytes(100)
+    assert n == 100 and not a.any() and ws.get_bytes(100)[0] is a
+    a.fill_(1)
+    capture(2)
+    b, _ = ws.get_bytes(100)
+    assert b is not a and not b.any()
+    assert ws.get_bytes(200)[1] == 200
+    capture(0)
+    c, _ = ws.get_bytes(100)
+    assert c is not a and c is not b and not c.any()
+    capture(3)
+    assert ws.get_bytes(100)[0] is c                             # one made before serves every graph
+    assert ws.get_bytes(200)[1] == 200
+    capture(0)
+    assert ws.get_bytes(100)[0] is c
