@@ -276,7 +276,8 @@ def _capture_id(index):
 
 
 class Workspace:
-    """A zero-initialised device workspace that grows on demand (one per stream).
+    """A zero-initialised device workspace that grows on demand (one per stream).  Each kind of
+    call has a buffer of its own in it, whose layout the others do not know.
 
     A buffer that a graph was captured with stays allocated as long as the Workspace lives,
     whatever later calls need; the Workspace has to outlive the graph.  A capture that finds no
@@ -285,35 +286,39 @@ class Workspace:
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
-        self.buf = None
+        self.buf = None                     # the buffer of the latest call
+        self._bufs = {}                     # by kind of call
         self._index = self.device.index if self.device.type == "cuda" else -1    # -1: host memory
         self._held = []                     # buffers that graphs were captured with
-        self._own = (0, None)               # the latest capture and the buffer of its own
+        self._own = (0, {})                 # the latest capture and the buffers of its own, by kind
 
     def get(self, mode: int, M: int, N: int, K: int):
         with torch.cuda.device(self.device):
             need = workspace_bytes(mode, M, N, K)
         return self.get_bytes(need)
 
-    def get_bytes(self, need: int):
-        """A buffer of at least `need` bytes (zero-filled when it is made)."""
+    def get_bytes(self, need: int, kind: str = "gemm"):
+        """A buffer of at least `need` bytes for calls of a kind (zero-filled when it is made)."""
         if need == 0:
             return None, 0
         index = self._index
         capture = _capture_id(_current_device() if index is None else index) if index != -1 else 0
-        buf = self.buf
+        buf = self._bufs.get(kind)
         fits = buf is not None and buf.numel() >= need
         if not capture:
             if not fits:
-                buf = self.buf = self._zeros(need)
+                buf = self._bufs[kind] = self._zeros(need)
         elif fits:
             if not any(x is buf for x in self._held):
                 self._held.append(buf)
         else:
-            owner, buf = self._own
-            if owner != capture or buf.numel() < need:
-                buf = self._zeros(need)
-                self._own = (capture, buf)
+            if self._own[0] != capture:
+                self._own = (capture, {})
+            buf = self._own[1].get(kind)
+            if buf is None or buf.numel() < need:
+                buf = self._own[1][kind] = self._zeros(need)
+            return buf, buf.numel()
+        self.buf = buf
         return buf, buf.numel()
 
     def _zeros(self, n):
@@ -321,7 +326,7 @@ class Workspace:
 
     def zero(self):
         """Zero-fill the buffers again (needed after a call that ended in QW_ERR_TIMEOUT)."""
-        for x in {id(x): x for x in (self.buf, *self._held) if x is not None}.values():
+        for x in {id(x): x for x in (*self._bufs.values(), *self._held)}.values():
             x.zero_()
 
 
@@ -446,7 +451,7 @@ def attn_int8qk_prefill(q, k, v, out=None, ws: Workspace | None = None):
         key = (q.device, torch.cuda.current_stream(q.device).cuda_stream, "attn")
         ws = _default_ws.setdefault(key, Workspace(q.device))
     with torch.cuda.device(q.device):
-        wbuf, wbytes = ws.get_bytes(int(lib().attn_int8qk_workspace_bytes(T, S, Hq, Hkv, d)))
+        wbuf, wbytes = ws.get_bytes(int(lib().attn_int8qk_workspace_bytes(T, S, Hq, Hkv, d)), "int8qk")
         _check(lib().attn_int8qk_prefill(_ptr(q), _ptr(k), _ptr(v), T, S, Hq, Hkv, d, _ptr(out), _ptr(wbuf),
                                          wbytes, _stream(q)))
     return out
@@ -458,7 +463,7 @@ def attn_int8qk_intermediates(ws: Workspace, T: int, S: int, Hq: int, Hkv: int, 
     V^T [Hkv,d,S]); codes as fp16 tensors holding the int8 values."""
     off = (ctypes.c_size_t * 6)()
     _check(lib().attn_int8qk_workspace_layout(T, S, Hq, Hkv, d, off))
-    b = ws.buf
+    b = ws._bufs["int8qk"]
 
     def view(o, n, dt, shape):
         return b[o:o + n * torch.tensor([], dtype=dt).element_size()].view(dt).view(shape)
@@ -495,7 +500,7 @@ def qgemm_lm_head_topk(mode: int, x, packed, N: int, K: int, k: int, y=None, val
         ws = _default_ws.setdefault(key, Workspace(x.device))
     with torch.cuda.device(x.device):
         need = int(lib().qgemm_lm_head_topk_workspace_bytes(mode, M, N, K, k))
-        wbuf, wbytes = ws.get_bytes(need)
+        wbuf, wbytes = ws.get_bytes(need, "lm_head_topk")
         _check(lib().qgemm_lm_head_topk(mode, _ptr(x), _ptr(packed), M, N, K, k, _ptr(y), _ptr(vals),
                                         _ptr(idx), _ptr(wbuf), wbytes, _stream(x)))
     return y, vals, idx
@@ -573,7 +578,7 @@ def _scratch(ws, index, stream, kind, query, *args):
     else:
         with torch.cuda.device(index):
             need = query(*args)
-    buf, nbytes = ws.get_bytes(need)
+    buf, nbytes = ws.get_bytes(need, kind)
     return buf, (None if buf is None else buf.data_ptr()), nbytes
 
 

@@ -113,3 +113,32 @@ def test_decode_and_verify_graphs_in_turn(ex, own, first):
         again = steps[i]()
         assert all(torch.equal(a, b) for a, b in zip(again, want[i]))
     assert q.device_error() == 0 and len(junk) == 8
+
+
+def test_one_workspace_for_every_kind_of_call(ex):
+    """Log probabilities leave their parts where attention keeps its counters, the GEMM and the
+    prefill attention write there too: a Workspace keeps them apart."""
+    q, dev = ex.q, ex.DEV
+    g = torch.Generator(device=dev).manual_seed(4)
+    shared = q.Workspace(dev)
+    k, v = torch.randn(2, 300, 2, 16, 128, generator=g, device=dev).half()
+    table = torch.randperm(300, generator=g, device=dev)[None, :250].int().contiguous()
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([4000], [0, 3]))
+    x = torch.randn(3, 16, 128, generator=g, device=dev).half()
+    y = torch.randn(700, 3000, generator=g, device=dev).half()
+    tok = torch.zeros(700, dtype=torch.int32, device=dev)
+    w4, w8 = (ex._weights(5120, 1024, torch.Generator().manual_seed(bits), bits) for bits in (4, 8))
+    z = torch.randn(20, 1024, generator=g, device=dev).half()
+    p = torch.randn(256, 6, 256, generator=g, device=dev).half()
+    calls = [lambda ws: q.attn_paged(x, k, v, table, lens, cu, max_new=3, ws=ws),
+             lambda ws: q.token_logprobs(y, tok, k=64, ws=ws),
+             lambda ws: q.qgemm_w4a16(z, w4, 5120, 1024, ws=ws),
+             lambda ws: q.qgemm_lm_head_topk(q.MODE_W8A16, z, w8, 5120, 1024, 20, ws=ws),
+             lambda ws: q.attn_int8qk_prefill(p, p[:, :2].contiguous(), p[:, 2:4].contiguous(), ws=ws)]
+    want = [f(q.Workspace(dev)) for f in calls]
+    for i in (0, 1, 0, 2, 0, 3, 0, 4, 0, 1, 2, 1, 3, 2, 4, 3, 1, 4, 2, 3):
+        got = calls[i](shared)
+        for a, b in zip(got if isinstance(got, tuple) else (got,), want[i] if isinstance(want[i], tuple) else (want[i],)):
+            assert torch.equal(a, b), i
+    torch.cuda.synchronize()
+    assert q.device_error() == 0

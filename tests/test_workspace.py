@@ -1,5 +1,6 @@
-"""Workspace's bookkeeping, on host buffers: what a captured graph holds stays allocated, and a
-capture gets no buffer that only its own replay would zero."""
+"""Workspace's bookkeeping, on host buffers: what a captured graph holds stays allocated, a
+capture gets no buffer that only its own replay would zero, and kinds of calls do not share
+one."""
 import gc
 import weakref
 
@@ -67,3 +68,38 @@ def test_a_buffer_made_in_a_capture_serves_that_graph_only(capture):
     assert ws.get_bytes(200)[1] == 200
     capture(0)
     assert ws.get_bytes(100)[0] is c
+
+
+def test_kinds_of_calls_have_their_own_buffers():
+    ws = host_workspace()
+    ws._index = -1
+    a, b = ws.get_bytes(100, "paged")[0], ws.get_bytes(100, "logprobs")[0]
+    assert a is not b and ws.buf is b
+    assert ws.get_bytes(50, "paged")[0] is a and ws.buf is a
+    a.fill_(1)
+    b.fill_(1)
+    ws.zero()
+    assert not a.any() and not b.any()
+    assert ws.get_bytes(0, "paged") == (None, 0)
+
+
+def test_every_kind_of_call_names_its_kind(monkeypatch):
+    """One Workspace passed to calls of different kinds: none sees another's bytes.  (The calls
+    end at the lookup, before any launch.)"""
+    class Seen(Exception):
+        pass
+    kinds = []
+
+    class Ws:
+        def get(self, *a):
+            kinds.append("gemm")
+            raise Seen
+
+        def get_bytes(self, need, kind="gemm"):
+            kinds.append(kind)
+            raise Seen
+    monkeypatch.setattr(q, "_current_device", lambda: 0)
+    for name in ("paged", "logprobs"):
+        with pytest.raises(Seen):
+            q._scratch(Ws(), 0, 0, name, lambda *a: 1)
+    assert kinds == ["paged", "logprobs"]
