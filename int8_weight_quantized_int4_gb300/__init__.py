@@ -287,37 +287,48 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None                     # the buffer of the latest call
-        self._bufs = {}                     # by kind of call
+        self._bufs = {}                     # by kind of call: [buffer, its leading zero bytes], held by no graph
         self._index = self.device.index if self.device.type == "cuda" else -1    # -1: host memory
-        self._held = []                     # buffers that graphs were captured with
-        self._own = (0, {})                 # the latest capture and the buffers of its own, by kind
+        self._held = []                     # buffers that graphs were captured with,
+        self._fixed = {}                    # the newest of them by (kind, zero bytes)
+        self._own = (0, {})                 # the latest capture and the buffers of its own, likewise
 
     def get(self, mode: int, M: int, N: int, K: int):
         with torch.cuda.device(self.device):
             need = workspace_bytes(mode, M, N, K)
         return self.get_bytes(need)
 
-    def get_bytes(self, need: int, kind: str = "gemm"):
-        """A buffer of at least `need` bytes for calls of a kind (zero-filled when it is made)."""
+    def get_bytes(self, need: int, kind: str = "gemm", zero: int = 0):
+        """A buffer of at least `need` bytes for calls of a kind (zero-filled when it is made).
+        zero: the leading bytes that the call finds and leaves zero, for kinds where they depend
+        on its sizes; what a smaller call has written there is zero-filled again."""
         if need == 0:
             return None, 0
         index = self._index
         capture = _capture_id(_current_device() if index is None else index) if index != -1 else 0
-        buf = self._bufs.get(kind)
-        fits = buf is not None and buf.numel() >= need
-        if not capture:
-            if not fits:
-                buf = self._bufs[kind] = self._zeros(need)
-        elif fits:
-            if not any(x is buf for x in self._held):
-                self._held.append(buf)
-        else:
-            if self._own[0] != capture:
-                self._own = (capture, {})
-            buf = self._own[1].get(kind)
+        entry = self._bufs.get(kind)
+        if entry is not None and entry[0].numel() < need:
+            entry = None
+        if capture and entry is not None and entry[1] == zero:
+            buf = self._fixed[kind, zero] = self._bufs.pop(kind)[0]
+            self._held.append(buf)
+        elif entry is None or capture or entry[1] < zero:
+            buf = self._fixed.get((kind, zero))
             if buf is None or buf.numel() < need:
-                buf = self._own[1][kind] = self._zeros(need)
-            return buf, buf.numel()
+                if capture:
+                    if self._own[0] != capture:
+                        self._own = (capture, {})
+                    buf = self._own[1].get((kind, zero))
+                    if buf is None or buf.numel() < need:
+                        buf = self._own[1][kind, zero] = self._zeros(need)
+                    return buf, buf.numel()
+                if entry is None:
+                    entry = self._bufs[kind] = [self._zeros(need), zero]
+                buf = entry[0]
+                buf[entry[1]:zero].zero_()
+                entry[1] = zero
+        else:
+            buf, entry[1] = entry[0], zero
         self.buf = buf
         return buf, buf.numel()
 
@@ -326,7 +337,7 @@ class Workspace:
 
     def zero(self):
         """Zero-fill the buffers again (needed after a call that ended in QW_ERR_TIMEOUT)."""
-        for x in {id(x): x for x in (*self._bufs.values(), *self._held)}.values():
+        for x in [x for x, _ in self._bufs.values()] + self._held:
             x.zero_()
 
 
@@ -463,16 +474,13 @@ def attn_int8qk_intermediates(ws: Workspace, T: int, S: int, Hq: int, Hkv: int, 
     V^T [Hkv,d,S]); codes as fp16 tensors holding the int8 values."""
     off = (ctypes.c_size_t * 6)()
     _check(lib().attn_int8qk_workspace_layout(T, S, Hq, Hkv, d, off))
-    b = ws._bufs["int8qk"]
+    b = ws._bufs["int8qk"][0] if "int8qk" in ws._bufs else ws._fixed["int8qk", 0]
 
     def view(o, n, dt, shape):
         return b[o:o + n * torch.tensor([], dtype=dt).element_size()].view(dt).view(shape)
     return (view(off[0], Hq * T * d, torch.float16, (Hq, T, d)), view(off[1], Hq * T, torch.float32, (Hq, T)),
             view(off[2], Hkv * S * d, torch.float16, (Hkv, S, d)), view(off[3], Hkv * S, torch.float32, (Hkv, S)),
             view(off[4], Hkv * d * S, torch.float16, (Hkv, d, S)))
-
-
-_topk_ws = {}
 
 
 def qgemm_lm_head_topk(mode: int, x, packed, N: int, K: int, k: int, y=None, vals=None, idx=None,
@@ -500,7 +508,8 @@ def qgemm_lm_head_topk(mode: int, x, packed, N: int, K: int, k: int, y=None, val
         ws = _default_ws.setdefault(key, Workspace(x.device))
     with torch.cuda.device(x.device):
         need = int(lib().qgemm_lm_head_topk_workspace_bytes(mode, M, N, K, k))
-        wbuf, wbytes = ws.get_bytes(need, "lm_head_topk")
+        wbuf, wbytes = ws.get_bytes(need, "lm_head_topk",
+                                    int(lib().qgemm_lm_head_topk_workspace_zero_bytes(mode, M, N, K, k)))
         _check(lib().qgemm_lm_head_topk(mode, _ptr(x), _ptr(packed), M, N, K, k, _ptr(y), _ptr(vals),
                                         _ptr(idx), _ptr(wbuf), wbytes, _stream(x)))
     return y, vals, idx
@@ -513,14 +522,12 @@ def topk_logits(logits, k: int):
     M, N = logits.shape
     vals = torch.empty((M, k), dtype=torch.float16, device=logits.device)
     idx = torch.empty((M, k), dtype=torch.int32, device=logits.device)
-    need = int(lib().topk_workspace_bytes(M, N, k))
-    key = (logits.device, torch.cuda.current_stream(logits.device).cuda_stream)
-    buf = _topk_ws.get(key)
-    if buf is None or buf.numel() < need:
-        buf = torch.zeros(max(need, 256), dtype=torch.uint8, device=logits.device)
-        _topk_ws[key] = buf
+    key = (logits.device, torch.cuda.current_stream(logits.device).cuda_stream, "topk")
+    ws = _default_ws.setdefault(key, Workspace(logits.device))
     with torch.cuda.device(logits.device):
-        _check(lib().topk_logits(_ptr(logits), M, N, k, _ptr(vals), _ptr(idx), _ptr(buf), buf.numel(),
+        buf, nbytes = ws.get_bytes(int(lib().topk_workspace_bytes(M, N, k)), "topk",
+                                   int(lib().topk_workspace_zero_bytes(M, N, k)))
+        _check(lib().topk_logits(_ptr(logits), M, N, k, _ptr(vals), _ptr(idx), _ptr(buf), nbytes,
                                  _stream(logits)))
     return vals, idx
 

@@ -117,3 +117,29 @@ def test_lm_head_topk_zero_rows(q):
     assert (idx.cpu() == torch.arange(k, dtype=torch.int32)).all()
     assert np.array_equal(bits(vals), bits(y[:, :k]))
     _check_topk(y, vals, idx, k)
+
+
+def test_topk_of_changing_sizes(q):
+    """The workspace's zero bytes grow with M: after a small call, which leaves its candidates
+    right behind its own, a larger one must find all of its counters zero."""
+    gen = synth.generator(77)
+    rows = {M: torch.randn(M, 8192, generator=gen).to(torch.float16).to(DEV) for M in (1, 65, 300, 1000)}
+    for M in (1000, 1, 300, 65, 1000, 1, 65, 1, 1000):
+        x = rows[M]
+        vals, idx = q.topk_logits(x, 64)
+        want = torch.sort(-x.float(), dim=1, stable=True).indices[:, :64]
+        assert torch.equal(idx.long(), want) and torch.equal(vals, x.gather(1, want))
+    assert q.device_error() == 0
+
+
+def test_lm_head_topk_of_changing_sizes(q):
+    N, K, k = 4096, 256, 40
+    codes, scales, x = _tie_problem(150, N, K, seed=5)
+    packed, xd = q.qpack_w4(codes.to(DEV), scales.to(DEV)), x.to(DEV)
+    ws = q.Workspace(DEV)
+    for own in (None, ws):
+        for M in (150, 1, 64, 16, 150, 2, 150, 64, 1, 64):
+            y, vals, idx = q.qgemm_lm_head_topk(q.MODE_W4A16, xd[:M], packed, N, K, k, ws=own)
+            torch.cuda.synchronize()
+            _check_topk(y, vals, idx, k)
+    assert q.device_error() == 0

@@ -103,3 +103,28 @@ def test_every_kind_of_call_names_its_kind(monkeypatch):
         with pytest.raises(Seen):
             q._scratch(Ws(), 0, 0, name, lambda *a: 1)
     assert kinds == ["paged", "logprobs"]
+
+
+def test_leading_zero_bytes_that_depend_on_the_call(capture):
+    """A call leaves its own leading bytes zero and may write the others: a later call that needs
+    more of them zero finds them so, whatever ran between, and graphs keep theirs."""
+    ws = host_workspace()
+
+    def call(need, zero):
+        buf, n = ws.get_bytes(need, "topk", zero)
+        assert n >= need and not buf[:zero].any(), (need, zero)
+        buf[zero:need] = 7
+        return buf
+    a = call(1000, 300)
+    assert call(200, 50) is a and call(1000, 300) is a and call(800, 290) is a and call(900, 600) is a
+    capture(1)
+    g1 = call(900, 600)
+    own = call(900, 100)                                # a capture's own: its graph zero-fills it
+    assert g1 is a and own is not a
+    capture(0)
+    b = call(500, 100)                                  # others leave the graph's buffer alone
+    assert b is not a and call(900, 600) is a and call(500, 100) is b
+    capture(2)
+    assert call(900, 600) is a and call(500, 100) is b
+    capture(0)
+    assert call(500, 100) is b and call(400, 30) is not b and call(400, 30) is not a
