@@ -401,7 +401,7 @@ int kv_pool_free_pages(kv_pool_t *pool);
  *   logprob[m][c]   x[tokens[m][c]] - lse for C given tokens (a token outside [0, N): NaN,
  *                   and QW_ERR_BAD_INDEX)
  *   top_logprob, top_idx [m][k]   the k most likely tokens, most likely first, equal logits
- *                   by the smaller index (-0 equals +0)
+ *                   by the smaller index (-0 equals +0; NaN after every number)
  *   logits: fp16, bf16 or binary32 (dtype QW_F16, QW_BF16, QW_F32), row m at
  *   logits + m * row_stride elements; any alignment and any 1 <= N <= 2^30.  -inf is a
  *   probability of 0 (a mask of the type's lowest value likewise, but a row of nothing else

@@ -93,10 +93,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-// binary32 values as unsigned integers in the values' order; -0 as +0; no value gives 0
+// binary32 values as unsigned integers in the values' order; -0 as +0; NaN below every number
+// (a maximum leaves NaN out, so what it bounds must not lie above it); no value gives 0
 __device__ __forceinline__ unsigned order_key32(float x) {
   const unsigned u = __float_as_uint(x + 0.0f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return x == x ? u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u) : 1u;
 }
 __device__ __forceinline__ float key_value32(unsigned k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
@@ -158,7 +159,7 @@ __device__ __forceinline__ void lp_unpack(const uint4 &w, float (&x)[LpVec<T>::V
     }
   }
 }
-// The largest element of a vector (16-bit types: two at a time; NaN ignored).
+// The largest element of a vector (16-bit types: two at a time; NaN only where all are).
 template <typename T>
 __device__ __forceinline__ float lp_max(const uint4 &w) {
   if constexpr (sizeof(T) == 4) {
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(co
     // ---- the sums, over even and odd elements.  The reference starts at the largest of the
     // warp's first blocks and moves when a block passes it by 4 (y stays below 6: nothing
     // overflows, and little cancels in log2 s - t / s).
-    float top = -INFINITY, r = kNoRef;            // this thread's largest element
+    const float nothing = __uint_as_float(0x7fc00000u);        // (a maximum with NaN is the other)
+    float top = nothing, r = kNoRef;              // this thread's largest element
     unsigned long long nr2 = pair2(-kNoRef, -kNoRef), s2 = pair2(0.0f, 0.0f), t2 = s2;
     const unsigned long long e2 = pair2(kLog2e, kLog2e);
     auto raise = [&](float x) {
@@ -452,12 +454,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) token_logprobs_kernel(co
     int g = 0;                                    // log2 of the blocks behind a kept maximum
     if (TOP)
       while ((w1 - w0 - 1) / kLpBlock >> g >= kLpMaxima) ++g;
-    float run = -INFINITY;
+    float run = nothing;
 #pragma unroll 1
     for (int v = w0, blk = 0; v < w1; v += kLpBlock, ++blk) {
       uint4 x4[kLpUnroll];
       fetch(x4);
-      float bm = -INFINITY;
+      float bm = nothing;
 #pragma unroll
       for (int i = 0; i < kLpUnroll; ++i)
         if (v + tid + i * kLpThreads < w1) bm = fmaxf(bm, lp_max<T>(w[i]));

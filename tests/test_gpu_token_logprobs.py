@@ -214,6 +214,36 @@ def test_nan_and_inf(q):
     assert bool(torch.isnan(r.lse[:2]).all()) and bool(torch.isfinite(r.lse[2]))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,k", [(3, 20, 20), (2, 4097, 64), (1, 248320, 20), (800, 3000, 7)])
+@pytest.mark.parametrize("left", [0, 1, 5, 70])
+def test_indices_of_nan_rows_are_columns(q, dtype, M, N, k, left):
+    """Rows of NaN of either sign but for `left` logits: sums are NaN, and the indices are k
+    different columns, so that a gather with them stays inside the row."""
+    g = torch.Generator(device=DEV).manual_seed(left)
+    word = {2: torch.int16, 4: torch.int32}[torch.empty(0, dtype=dtype).element_size()]
+    for sign in (1.0, -1.0, 0.0):
+        nan = torch.full((M, N), float("nan"), dtype=dtype, device=DEV).view(word)
+        low = torch.iinfo(word).min
+        if sign < 0:
+            nan |= low
+        elif sign == 0:
+            nan |= torch.randint(0, 2, (M, N), generator=g, device=DEV).to(word) * low
+        x = nan.view(dtype)
+        at = torch.argsort(torch.rand(M, N, generator=g, device=DEV))[:, :min(left, N - 1)]
+        x.scatter_(1, at, torch.randn(M, N, generator=g, device=DEV).to(dtype)[:, :at.shape[1]])
+        r = q.token_logprobs(x, torch.zeros(M, dtype=torch.int32, device=DEV), k=k)
+        assert q.device_error() == 0
+        assert bool(torch.isnan(r.lse).all()) and bool(torch.isnan(r.top_logprob).all())
+        idx = torch.sort(r.top_idx, dim=1).values
+        assert int(idx.min()) >= 0 and int(idx.max()) < N, (sign, r.top_idx[0])
+        assert bool((idx[:, 1:] > idx[:, :-1]).all())
+        # the numbers first, largest first, then NaN by index
+        v = x.double()
+        order = torch.sort(torch.where(torch.isnan(v), float("inf"), -v), dim=1, stable=True).indices[:, :k]
+        assert torch.equal(r.top_idx.long(), order)
+
+
 def test_workspace_is_shared_by_calls_of_any_shape(q):
     ws = q.Workspace(torch.device("cuda:0"))
     for M, N, k in ((700, 3000, 64), (3, 248320, 20), (1, 50000, 64), (200, 9000, 5), (700, 3000, 1), (64, 128257, 20)):
