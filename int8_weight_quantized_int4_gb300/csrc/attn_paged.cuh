@@ -5,7 +5,7 @@
 // j < sinks):
 //   x_j = q . k_j * scale,  p_j = e^(x_j - m),  out = sum_j p_j v_j / sum_j p_j.
 // One pass over K and V: a running reference m of the exponents (moved only when a score
-// passes it by 2^8, which rescales the sums), the sums in binary32.
+// passes it by 2^8, in fp16 2^15, which rescales the sums), the sums in binary32.
 //
 // What bounds it: reading K and V, 2 S d e bytes a (sequence, KV head) for 4 S d flops a
 // query row -- a few rows a KV head (G x new tokens), so 1..64 flops a byte, far below the
@@ -49,7 +49,11 @@
 // Roundings: p is rounded to the values' 16-bit type for the P.V product (fp16 2^-11, bf16
 // 2^-8 relative, half a step; both sums are exact products accumulated in binary32) -- the
 // error of each p is independent, so it stays of the order of the output's own rounding; the
-// denominator sums the unrounded p.  With the int8 cache the value's scale joins its weight
+// denominator sums the unrounded p.  fp16 has no such relative bound below 2^-14, and rounds
+// what lies below 2^-25 to 0, always the same way: the reference starts 2^7 below the largest
+// score, so that only weights below 2^-32 of it are lost (131k of them hold 2^-15 of the mass;
+// with the reference at the largest it was 2^-8), and weights stay below 2^15.  bf16 has
+// binary32's exponents.  With the int8 cache the value's scale joins its weight
 // (w_j = p_j vs_j) and the reference follows w_j, not p_j, so that w keeps its bits whatever
 // the scales' size.
 #pragma once
@@ -657,6 +661,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
   constexpr int KW = P::kKW, NT = P::kThreads, ROWS = P::kRows, COLS = P::kCols, RB = P::kRowBytes;
   constexpr int R = P::kRing, SW = P::kSW, GW = P::kGW;
   constexpr int DT = D / 16 / GW;                       // 16-channel tiles a warp
+  // the reference lies kHead below a strip's largest score when it moves, and moves when one
+  // passes it by kRise (exponents of 2; fp16 weights reach 2^kRise)
+  constexpr float kHead = BF ? 0.0f : 7.0f, kRise = BF ? 8.0f : 15.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *fixed = smem + R * KW * P::kHalf;
   float *red = reinterpret_cast<float *>(fixed);                      // [KW][GW][COLS][SW + 4]
@@ -962,13 +969,13 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
             lvs[h] = fmaxf(paged_lg2(fabsf(vsc[h])), -64.0f);
           }
         }
-        // ---- weights.  The reference moves only when a weight passes it by 2^8 (a weight
-        // then still fits fp16), so the largest score of a strip is seldom needed exactly.
+        // ---- weights.  The reference moves only when a weight passes it by 2^kRise, so the
+        // largest score of a strip is seldom needed exactly.
         bool up = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up |= (I8 ? s[nb][e] + lvs[e >> 1] : s[nb][e]) > m[nb][e & 1] + 8.0f;
+          for (int e = 0; e < 4; ++e) up |= (I8 ? s[nb][e] + lvs[e >> 1] : s[nb][e]) > m[nb][e & 1] + kRise;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -978,7 +985,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               float f = 1.0f;
-              if (top > m[nb][e] + 8.0f) {
+              if (top > m[nb][e] + kRise) {
+                top -= kHead;
                 f = paged_ex2(m[nb][e] - top);
                 m[nb][e] = top;
               }

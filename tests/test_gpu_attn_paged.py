@@ -1,6 +1,8 @@
 """attn_paged on the GPU against its definition in binary64, with error bounds derived in
 _decode_ref.Cache.tolerances.  Every slot of the cache that holds no key of the batch is NaN
 (and, int8, has a NaN scale)."""
+import math
+
 import pytest
 import torch
 
@@ -230,6 +232,47 @@ def test_scores_near_the_lowest(q):
     tol = 2.0 ** -9 * ref[0].abs() * (1 + 2.0 ** -6) + 400 * 2.0 ** -24 * ref[3]
     assert bool(((out.double() - ref[0]).abs() <= 2 * tol).all())
     assert bool(((lse.double() / ref[1] - 1).abs() <= 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("kind", ["fp16", "int8", "bf16"])
+@pytest.mark.parametrize("new", [1, 5])
+@pytest.mark.parametrize("gap", [17.5, 18.0, 19.0])
+def test_weights_far_below_the_largest_count(q, kind, new, gap):
+    """Every 64th key scores `gap` above the others and has a value of 0: the row is what the
+    others' weights, e^-gap (2^-25.2 to 2^-27.4), leave of their values.  Per element: scores are
+    exact (one product); a weight's rounding u where the type is normal, and where it is not the
+    2^-25 of a weight whose largest is at least 2^7, 2^-32 n |v| in all; exponents 2^-22 + 64 steps of
+    binary32; one rounding of the output."""
+    d, n = 64, 4000
+    c = Cache([n], [new], 6, 1, d, 16, kind, seed=1)
+    v = torch.randint(1, 101, (n, d), generator=torch.Generator().manual_seed(9)).double().to(DEV)
+    v[::64] = 0.0
+    key = torch.arange(n, device=DEV)
+    pid, off = c.table[0].long()[key // 16], key % 16
+    if kind == "int8":
+        k8 = torch.zeros(n, d, dtype=torch.int8, device=DEV)
+        k8[::64, 0] = 64
+        c.k[pid, 0, off], c.v[pid, 0, off] = k8, v.to(torch.int8)
+        c.kw["k_scale"][pid, 0, off] = 2.0 ** -6
+        c.kw["v_scale"][pid, 0, off] = 1.0
+    else:
+        c.k[pid, 0, off] = 0.0
+        c.k[pid[::64], 0, off[::64], 0] = 1.0
+        c.v[pid, 0, off] = v.to(c.act)
+    c.q.zero_()
+    c.q[:, :, 0] = gap
+    out = q.attn_paged(c.q, *c.args(), max_new=new, scale=1.0, **c.kw).double()
+    assert q.device_error() == 0
+    u, e = torch.finfo(c.act).eps / 2, 2.0 ** -24
+    for t in range(new):
+        m = n - new + t + 1
+        p = torch.where(key[:m] % 64 == 0, 1.0, math.exp(-gap)).double()
+        p /= p.sum()
+        want = p @ v[:m]
+        tol = (2 * u + 2.0 ** -20 + 128 * e) * want + m * 2.0 ** -32 * 100 / (m // 64)
+        if c.act == torch.float16:
+            tol = tol + 2.0 ** -25
+        assert bool(((out[t] - want).abs() <= tol).all()), (t, float(out[t, 0, 0]), float(want[0]))
 
 
 @pytest.mark.parametrize("v_scale", [2.0 ** -13, 2.0 ** 8])
