@@ -24,10 +24,10 @@
 //     hide each other's waits where six could not.
 //   - More than 16 columns are dealt to the groups in blocks of 16: the groups of different
 //     blocks stream the same strips at the same time, the first from HBM and the others from
-//     L2.  (16 sequences of up to 16384, 6 to 36 columns, d = 256: 149 us.  As items of their
-//     own the blocks came too far apart, 5 % L2 hits and 21 us more; groups of two to four warps
-//     with 16 columns each, reading a strip once for all of them, took 188 to 421 us, rings
-//     shared through counting barriers 151 at best.)
+//     L2.  (16 sequences of up to 16384, 6 to 36 columns, d = 256, with one product a weight: 149
+//     us.  As items of their own the blocks came too far apart, 5 % L2 hits and 21 us more; groups
+//     of two to four warps with 16 columns each, reading a strip once for all of them, took 188
+//     to 421 us, rings shared through counting barriers 151 at best.)
 //   - Work is split evenly over the SMs whatever the lengths: the visible strips of every
 //     (sequence, column block, KV head) item are laid end to end and cut into one equal range
 //     a CTA (every CTA finds its own range from the lengths on the device, so a captured graph
@@ -38,24 +38,25 @@
 //     is being finished.
 //
 // Measured (K and V rows read / time): 64 ragged contexts of up to 8190, 32/8 heads of 128, bf16:
-// 176 to 181 us, 6.4 to 6.6 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 111 us, 6.0 TB/s (the
+// 177 to 183 us, 6.3 to 6.5 TB/s; 4 of up to 131071, 24/4 heads of 256, int8: 116 us, 5.75 TB/s (the
 // codes' conversion to fp16 takes half of the issue slots); 16 of up to 16384 with up to 6 new
-// tokens, fp16: 149 us, 4.74 TB/s (up to 36 columns: a strip is read once from HBM and up to
-// twice more from L2, whose 31 bytes a clock an SM are the bound); a window of
+// tokens, fp16: 157 us, 4.5 TB/s (up to 36 columns: a strip is read once from HBM and up to
+// twice more from L2, at 31 bytes a clock an SM with one product a weight); a window of
 // 1024, 48 contexts, 64/8 heads of 64, fp16: 26.9 us, 3.7 TB/s (items of 66 strips: their
 // starts and joins); one context of 1003, 24/4 heads of 256, fp16: 12.2 us, nearly all of it the
 // chain launch -> lengths -> page table -> keys -> exchange -> partial sums -> join.
 //
-// Roundings: p is rounded to the values' 16-bit type for the P.V product (fp16 2^-11, bf16
-// 2^-8 relative, half a step; both sums are exact products accumulated in binary32) -- the
-// error of each p is independent, so it stays of the order of the output's own rounding; the
-// denominator sums the unrounded p.  fp16 has no such relative bound below 2^-14, and rounds
-// what lies below 2^-25 to 0, always the same way: the reference starts 2^7 below the largest
-// score, so that only weights below 2^-32 of it are lost (131k of them hold 2^-15 of the mass;
-// with the reference at the largest it was 2^-8), and weights stay below 2^15.  bf16 has
-// binary32's exponents.  With the int8 cache the value's scale joins its weight
-// (w_j = p_j vs_j) and the reference follows w_j, not p_j, so that w keeps its bits whatever
-// the scales' size.
+// Roundings: each weight enters P.V as two terms of the values' 16-bit type, p rounded and what
+// that leaves, so it keeps 22 bits (bf16 16) where one term has 11 (8): all products are exact and
+// all sums binary32, and the output's own rounding is what remains (one term gave 1.32 times the
+// error of a binary32 softmax in fp16 and 1.26 in bf16, against binary64; two give 1.00).  The
+// second product costs nothing where 8 columns read at HBM's rate, 3.5 % for int8 and 6 % for up to
+// 36 columns of d = 256.  fp16 has no relative bound below 2^-14, and rounds what lies below 2^-25
+// to 0, always the same way: the reference starts 2^7 below the largest score, so that only
+// weights below 2^-32 of it are lost (131k of them hold 2^-15 of the mass; with the reference at
+// the largest it was 2^-8), and weights stay below 2^15.  bf16 has binary32's exponents.  With the
+// int8 cache the value's scale joins its weight (w_j = p_j vs_j) and the reference follows w_j,
+// not p_j, so that w keeps its bits whatever the scales' size.
 #pragma once
 #include <stdint.h>
 #include <cuda_bf16.h>
@@ -169,6 +170,11 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
     return *reinterpret_cast<const uint32_t *>(&v);
   }
 }
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(u32_as_h2(w));
+}
 // Two int8 codes of a word (xor 0x80 applied: u = code + 128) as an fp16 pair: 0x6400 | u
 // is 1024 + u exactly, minus 1152.  SEL picks the two bytes.
 template <uint32_t SEL>
@@ -213,22 +219,20 @@ __device__ __noinline__ bool strip_nonfinite(uint32_t vst, int lane) {
   return __any_sync(0xffffffffu, bad);
 }
 // acc += V^T P^T of one strip over the visible keys alone (score above -inf), term by term.
-// pk[nb][h]: the packed weights of keys r8 + 8 h and columns 2 c4, 2 c4 + 1; s: their scores.
+// s[nb]: the scores of keys r8 + 8 h and columns 2 c4, 2 c4 + 1; m: those columns' references.
 // n0: the warp's first chunk of 8 channels.
 template <int D, int DT, int NB, bool BF>
-__device__ __forceinline__ void add_visible(float (&acc)[DT][NB][4], const uint32_t (&pk)[NB][2],
-                                            const float (&s)[NB][4], uint32_t vst, int n0, int lane) {
+__device__ __forceinline__ void add_visible(float (&acc)[DT][NB][4], const float (&s)[NB][4], const float (&m)[NB][2],
+                                            uint32_t vst, int n0, int lane) {
   const int c4 = lane & 3, r8 = lane >> 2;
 #pragma unroll 1
   for (int j = 0; j < kStrip; ++j) {
     const int src = (j & 7) * 4 + c4, h = j >> 3;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const uint32_t pw = __shfl_sync(0xffffffffu, h ? pk[nb][1] : pk[nb][0], src);
       const float s0 = __shfl_sync(0xffffffffu, h ? s[nb][2] : s[nb][0], src);
       const float s1 = __shfl_sync(0xffffffffu, h ? s[nb][3] : s[nb][1], src);
-      const float w0 = BF ? __uint_as_float(pw << 16) : __half2float(__ushort_as_half((unsigned short)pw));
-      const float w1 = BF ? __uint_as_float(pw & 0xffff0000u) : __half2float(__ushort_as_half((unsigned short)(pw >> 16)));
+      const float w0 = paged_ex2(s0 - m[nb][0]), w1 = paged_ex2(s1 - m[nb][1]);
 #pragma unroll
       for (int n = 0; n < 2 * DT; ++n) {             // channel 8 n + r8: rows r8 (+ 8) of tile n / 2
         unsigned short v;
@@ -998,7 +1002,7 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
               }
             }
         }
-        uint32_t pk[NB][2];
+        uint32_t pf[2][NB][2];                             // the rounded weights, and what that leaves
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -1010,7 +1014,10 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
               p0 = s[nb][2 * h] == -INFINITY ? 0.0f : p0 * vsc[h];
               p1 = s[nb][2 * h + 1] == -INFINITY ? 0.0f : p1 * vsc[h];
             }
-            pk[nb][h] = pack2<BF>(p0, p1);
+            const uint32_t pk = pack2<BF>(p0, p1);
+            const float2 r = unpack2<BF>(pk);
+            pf[0][nb][h] = movm_t(pk);
+            pf[1][nb][h] = movm_t(pack2<BF>(p0 - r.x, p1 - r.y));
           }
         }
         // ---- O^T += V^T P^T
@@ -1022,14 +1029,8 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
           // products.
           odd = masked && mixed && strip_nonfinite<D, BF>(vst, lane);
         }
-        uint32_t pf[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          pf[nb][0] = movm_t(pk[nb][0]);
-          pf[nb][1] = movm_t(pk[nb][1]);
-        }
         if (!I8 && odd) {
-          if constexpr (!I8) add_visible<D, DT, NB, BF>(acc, pk, s, vst, gi * 2 * DT, lane);
+          if constexpr (!I8) add_visible<D, DT, NB, BF>(acc, s, m, vst, gi * 2 * DT, lane);
         } else if constexpr (!I8) {
           // A tile (transposed): (channels 0-7, 8-15) x (keys 0-7, 8-15)
 #pragma unroll
@@ -1037,7 +1038,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
             uint32_t vf[4];
             ldsm4_t(vf, vst + half + voff(dt));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<BF>(acc[dt][nb], vf, pf[nb][0], pf[nb][1]);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816<BF>(acc[dt][nb], vf, pf[i][nb][0], pf[i][nb][1]);
           }
         } else {
           // a transposed 16-bit element holds two channels: rows 0-7 of tile dt are the even
@@ -1051,7 +1054,9 @@ __global__ void __launch_bounds__(PagedShape<D, KV, NB, CTAS>::kThreads, CTAS)
               const uint32_t u0 = vf[h] ^ 0x80808080u, u1 = vf[2 + h] ^ 0x80808080u;
               const uint32_t af[4] = {codes_f16<0x4240>(u0), codes_f16<0x4341>(u0), codes_f16<0x4240>(u1), codes_f16<0x4341>(u1)};
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16816<false>(acc[2 * kk + h][nb], af, pf[nb][0], pf[nb][1]);
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16816<false>(acc[2 * kk + h][nb], af, pf[i][nb][0], pf[i][nb][1]);
             }
           }
         }

@@ -275,6 +275,45 @@ def test_weights_far_below_the_largest_count(q, kind, new, gap):
         assert bool(((out[t] - want).abs() <= tol).all()), (t, float(out[t, 0, 0]), float(want[0]))
 
 
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "int8"])
+@pytest.mark.parametrize("d,G,new", [(64, 6, 1), (128, 8, 2), (256, 8, 1), (256, 6, 2), (128, 16, 2), (64, 16, 4)])
+def test_weights_of_opposite_values(q, kind, d, G, new):
+    """Two keys with values A and -A and scores that differ by a little (exactly, one product):
+    A tanh of half the difference, 0 to 13 % of A.  What the weights lose shows beside
+    that: two terms of 16 bits hold a weight to u^2 of itself, exponents, sums and the quotient
+    2^-20 of A, and one rounding of the output.  With several tokens a later one's infinite
+    value lies in the strip (16-bit caches), which then is summed key by key."""
+    A = 1016.0
+    n = new + 1
+    c = Cache([n], [new], 2 * G, 2, d, 16, kind, seed=1)
+    pid = int(c.table[0, 0])
+    one = 64 if kind == "int8" else 1
+    c.k[pid, :, :n], c.v[pid, :, :n] = 0, 0
+    c.k[pid, :, 0, 0] = one
+    c.v[pid, :, 0], c.v[pid, :, 1] = (127, -127) if kind == "int8" else (A, -A)
+    if kind == "int8":
+        c.kw["k_scale"][pid], c.kw["v_scale"][pid] = 2.0 ** -6, 8.0
+    elif new > 1:
+        c.v[pid, :, 2:n] = float("inf")
+    c.q.zero_()
+    delta = torch.arange(c.T * 2 * G, device=DEV).view(c.T, 2 * G).double() % 64 / 256
+    c.q[:, :, 0] = delta.to(c.act)
+    out = q.attn_paged(c.q, *c.args(), max_new=new, scale=1.0, **c.kw).double()
+    assert q.device_error() == 0
+    want = (A * torch.tanh(delta / 2))[:, :, None]
+    u = torch.finfo(c.act).eps / 2
+    tol = A * (u * u + 2.0 ** -20) + u * want * (1 + 2.0 ** -6)
+    assert bool(((out[0] - want[0]).abs() <= tol[0]).all()), float(((out[0] - want[0]).abs() / tol[0]).max())
+    # later tokens: further keys of value 0 and score 0 (int8), or the infinity they see
+    for t in range(1, new):
+        if kind == "int8":
+            w = torch.exp(delta[t])
+            w = (A * (w - 1) / (w + 1 + t))[:, None]
+            assert bool(((out[t] - w).abs() <= A * (u * u + 2.0 ** -20) + u * w.abs() * (1 + 2.0 ** -6)).all())
+        else:
+            assert not bool(torch.isfinite(out[t]).any())
+
+
 @pytest.mark.parametrize("v_scale", [2.0 ** -13, 2.0 ** 8])
 def test_int8_values_of_any_size(q, v_scale):
     """The weight carries the value's scale: small scales must not lose its bits."""
