@@ -409,8 +409,8 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.npages = c->num_pages;
   a.max_pages = b->max_pages;
   a.cap = b->max_pages * c->page;
-  a.window = window;
-  a.sinks = window > 0 ? sinks : 0;
+  a.window = window < a.cap ? window : 0;        // (a window of all keys is none; and no sum with it overflows)
+  a.sinks = a.window > 0 ? sinks : 0;
   a.page_shift = (c->page & (c->page - 1)) == 0 ? 0 : -1;
   while (a.page_shift >= 0 && c->page >> a.page_shift > 1) ++a.page_shift;
   a.strip_pages = c->page % 16 == 0;

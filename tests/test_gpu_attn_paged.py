@@ -94,6 +94,17 @@ def test_long_context_of_one_head(q, kind, d, G, new):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("kind,d", [("fp16", 128), ("bf16", 256), ("int8", 64)])
+@pytest.mark.parametrize("window", [128, 129, 1 << 30, 2 ** 31 - 2, 2 ** 31 - 1])
+def test_windows_past_every_key(q, kind, d, window):
+    """A window that reaches every key hides none, however large, also where a sequence has more
+    new tokens than positions (those before the first see nothing)."""
+    c = Cache([3, 100, 60], [10, 2, 90], 8, 2, d, 16, kind, seed=3)
+    a, la = check(q, c, window=window)
+    b, lb = check(q, c)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
+
+
 def count_case(kind, d, lens, news, Hkv, G, page, seed=0):
     """A batch whose scores are all 0 and whose values count: strip s (16 keys) of a sequence is 1
     in channel s % d of even heads and s // d % d of odd ones, else 0.  Returns (q, args, scales)."""
