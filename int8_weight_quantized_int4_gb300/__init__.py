@@ -545,6 +545,14 @@ assert struct.calcsize("@PPPPiiiiiqqq") == ctypes.sizeof(KvCacheDesc)
 assert struct.calcsize("@PPPii0q") == ctypes.sizeof(KvBatchDesc)
 assert struct.calcsize("@Piiqqq") == ctypes.sizeof(PagePoolDesc)
 _i32, _f32 = torch.int32, torch.float32
+_INT_MAX = 0x7fffffff
+
+
+def _int(x):
+    """x as a C int; ctypes would take it modulo 2^32."""
+    if not -_INT_MAX <= x <= _INT_MAX:
+        raise ValueError(f"{x} is outside the 32-bit range")
+    return x
 
 
 _step = {}
@@ -708,6 +716,8 @@ def attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, max_new: in
     if lse is not None and (lse.dtype is not _f32 or lse.shape != (T, Hq) or lse.get_device() != index
                             or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor {(T, Hq)} on the cache's device")
+    if max(max_new, window, sinks) > _INT_MAX or min(max_new, window, sinks) < 0:
+        max_new, window, sinks = (max(min(x, _INT_MAX), -1) for x in (max_new, window, sinks))   # -1: refused below
     stream = _raw_stream(index)
     buf, pbuf, nbytes = _scratch(ws, index, stream, "paged", _step_fn("attn_paged_workspace_bytes"), d, Hq, heads,
                                  max_new)
@@ -724,7 +734,7 @@ class KvPool:
 
     def __init__(self, num_pages: int, page: int):
         h = ctypes.c_void_p()
-        _check(lib().kv_pool_create(num_pages, page, ctypes.byref(h)))
+        _check(lib().kv_pool_create(_int(num_pages), _int(page), ctypes.byref(h)))
         self._h = h
         self.num_pages, self.page = num_pages, page
 
@@ -741,35 +751,35 @@ class KvPool:
     def extend(self, seq: int, n_tokens: int) -> list:
         """Lengthens the sequence; returns the pages to copy first: [] or [[src, dst]]."""
         pair, n = (ctypes.c_int32 * 2)(), ctypes.c_int()
-        _check(lib().kv_pool_extend(self._h, seq, n_tokens, pair, ctypes.byref(n)))
+        _check(lib().kv_pool_extend(self._h, _int(seq), _int(n_tokens), pair, ctypes.byref(n)))
         return [list(pair)] if n.value else []
 
     def truncate(self, seq: int, length: int):
-        _check(lib().kv_pool_truncate(self._h, seq, length))
+        _check(lib().kv_pool_truncate(self._h, _int(seq), _int(length)))
 
     def fork(self, seq: int) -> int:
         s = ctypes.c_int()
-        _check(lib().kv_pool_fork(self._h, seq, ctypes.byref(s)))
+        _check(lib().kv_pool_fork(self._h, _int(seq), ctypes.byref(s)))
         return s.value
 
     def free(self, seq: int):
-        _check(lib().kv_pool_free(self._h, seq))
+        _check(lib().kv_pool_free(self._h, _int(seq)))
 
     def compact(self, most: int | None = None) -> list:
         """Moves live pages into the lowest free ones; returns the pages to copy."""
-        cap = self.num_pages if most is None else most
+        cap = self.num_pages if most is None else min(most, self.num_pages)
         pairs, n = (ctypes.c_int32 * (2 * max(cap, 1)))(), ctypes.c_int()
-        _check(lib().kv_pool_compact(self._h, pairs, cap, ctypes.byref(n)))
+        _check(lib().kv_pool_compact(self._h, pairs, _int(cap), ctypes.byref(n)))
         return [[pairs[2 * i], pairs[2 * i + 1]] for i in range(n.value)]
 
     def length(self, seq: int) -> int:
         n = ctypes.c_int()
-        _check(lib().kv_pool_pages(self._h, seq, ctypes.byref(n), None))
+        _check(lib().kv_pool_pages(self._h, _int(seq), ctypes.byref(n), None))
         return n.value
 
     def pages(self, seq: int) -> int:
         n = ctypes.c_int()
-        _check(lib().kv_pool_pages(self._h, seq, None, ctypes.byref(n)))
+        _check(lib().kv_pool_pages(self._h, _int(seq), None, ctypes.byref(n)))
         return n.value
 
     def free_pages(self) -> int:
@@ -780,7 +790,7 @@ class KvPool:
 
     def table(self, seqs, max_pages: int | None = None, pin: bool = False):
         """CPU int32 tensors (page_table [B, max_pages], seq_lens [B]) of the sequences."""
-        seqs = [int(s) for s in seqs]
+        seqs = [_int(int(s)) for s in seqs]
         width = max([self.pages(s) for s in seqs], default=0) if max_pages is None else max_pages
         table = torch.empty((len(seqs), width), dtype=torch.int32, pin_memory=pin)
         lens = torch.empty((len(seqs),), dtype=torch.int32, pin_memory=pin)

@@ -105,6 +105,19 @@ def test_windows_past_every_key(q, kind, d, window):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 70])
+def test_sizes_past_32_bits(q, past):
+    """Sizes that no C int holds count as the largest, not modulo 2^32; negative ones are refused."""
+    c = Cache([300, 40], [5, 1], 8, 2, 64, 16, "fp16", seed=3)
+    check(q, c, window=past)
+    check(q, c, window=past, sinks=past)
+    check(q, c, window=7, sinks=past)
+    check(q, c, max_new=past)
+    for kw in (dict(window=-past), dict(sinks=-past, window=5), dict(max_new=-past)):
+        with pytest.raises(q.QgemmError):
+            q.attn_paged(c.q, *c.args(), **kw)
+
+
 def count_case(kind, d, lens, news, Hkv, G, page, seed=0):
     """A batch whose scores are all 0 and whose values count: strip s (16 keys) of a sequence is 1
     in channel s % d of even heads and s // d % d of odd ones, else 0.  Returns (q, args, scales)."""

@@ -156,3 +156,16 @@ def test_refusals():
     s = empty.add()
     assert empty.extend(s, 0) == [] and empty.free_pages() == 0 and empty.compact() == []
     assert empty.table([s])[0].shape == (1, 0) and empty.table([])[1].shape == (0,)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """ctypes takes an int modulo 2^32: 2^32 + 3 tokens would be 3."""
+    pool = q.KvPool(10, 4)
+    s = pool.add()
+    assert pool.extend(s, 10) == []
+    for call in (lambda: q.KvPool(2 ** 32 + 5, 4), lambda: q.KvPool(5, 2 ** 32 + 4), lambda: pool.extend(s, 2 ** 32 + 3),
+                 lambda: pool.truncate(s, 2 ** 32 + 3), lambda: pool.length(2 ** 32 + s), lambda: pool.pages(2 ** 32 + s),
+                 lambda: pool.fork(2 ** 32 + s), lambda: pool.free(2 ** 32 + s), lambda: pool.table([2 ** 32 + s])):
+        with pytest.raises(ValueError):
+            call()
+    assert pool.length(s) == 10 and pool.pages(s) == 3 and pool.compact(2 ** 40) == []
