@@ -597,6 +597,11 @@ def _scratch(ws, index, stream, kind, query, *args):
     return buf, (None if buf is None else buf.data_ptr()), nbytes
 
 
+def _strides(t):
+    """The strides, 0 for dimensions of one element, where they mean nothing."""
+    return tuple(0 if n == 1 else st for n, st in zip(t.shape[:-1], t.stride())) + t.stride()[-1:]
+
+
 def _kv_cache(k_pages, v_pages, k_scale, v_scale, index):
     """(packed descriptor, cache type, Hkv, d) of one layer's cache, [pages, Hkv, page, d]."""
     dtype = _KV_TYPES.get(k_pages.dtype)
@@ -607,7 +612,9 @@ def _kv_cache(k_pages, v_pages, k_scale, v_scale, index):
     shape, stride = k_pages.shape, k_pages.stride()
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have one shape [pages, Hkv, page, d]")
-    if v_pages.stride() != stride or stride[3] != 1:
+    if 1 in shape:
+        stride = _strides(k_pages)
+    if (_strides(v_pages) if 1 in shape else v_pages.stride()) != stride or stride[3] != 1:
         raise ValueError("k_pages and v_pages must have the same strides, the last dimension contiguous")
     ks = vs = 0
     pages, heads, page, d = shape
@@ -645,7 +652,7 @@ def _rows(t, name, dtype, d, index, heads):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, {d}]")
     T, h, dt = t.shape
-    st, sh, sd = t.stride()
+    st, sh, sd = t.stride() if T > 1 and h > 1 else _strides(t)
     if dt != d or (heads and h != heads) or sd != 1:
         raise ValueError(f"{name} must be [T, {heads or 'Hq'}, {d}] with the last dimension contiguous")
     return T, h, st, sh
@@ -692,8 +699,9 @@ def kv_copy_pages(pairs, *pools):
             if n != 1 and st != dense:
                 raise ValueError(f"pool {i}: a page must be one dense block")
             dense *= n
-        desc += _pack_pool(x.data_ptr(), shape[0] if lead == 2 else 1, shape[lead - 1],
-                           stride[0] * es if lead == 2 else 0, stride[lead - 1] * es, dense * es)
+        layers, pages = shape[0] if lead == 2 else 1, shape[lead - 1]
+        desc += _pack_pool(x.data_ptr(), layers, pages, stride[0] * es if layers > 1 else 0,
+                           (stride[lead - 1] if pages > 1 else dense) * es, dense * es)
     _run(index, _step_fn("kv_copy_pages"), desc, len(pools), pairs.data_ptr(), pairs.shape[0], _raw_stream(index))
 
 

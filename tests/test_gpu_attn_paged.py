@@ -531,6 +531,44 @@ def test_another_stream(q):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("kind", ["fp16", "int8"])
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_strides_of_extents_of_one_mean_nothing(q, kind, dim):
+    """A dimension of one element may have any stride, in K another than in V."""
+    shape = [(1, 2, 16), (5, 1, 16), (20, 2, 1)][dim]
+    pages, Hkv, page = shape
+    n = min(pages * page, 16)
+    c = Cache([n], [1], 4 * Hkv, Hkv, 64, page, kind, seed=dim, spare=pages - -(-n // page))
+    assert tuple(c.k.shape[:3]) == shape
+    want = q.attn_paged(c.q, *c.args(), **c.kw)
+    odd = [list(c.k.stride()) for _ in range(2)]
+    odd[0][dim], odd[1][dim] = 7, 3
+
+    def restride(x, st):
+        return x.as_strided(x.shape, st)
+    k, v = restride(c.k, odd[0]), restride(c.v, odd[1])
+    qq = c.q.as_strided(c.q.shape, (5, 64, 1))                       # one token
+    got = q.attn_paged(qq, k, v, *c.args()[2:], **c.kw)
+    assert torch.equal(got, want)
+    new = torch.randn(1, Hkv, 64, device=DEV).half()
+    for x, y in ((c.k, c.v), (k, v)):
+        q.kv_append(new if x is c.k else new.as_strided(new.shape, (3, 64, 1)), new, x, y, *c.args()[2:], **c.kw)
+        pid, off = c.row(0, n - 1)
+        if kind == "fp16":
+            assert torch.equal(c.k[pid, :, off], new[0]) and torch.equal(c.v[pid, :, off], new[0])
+        c.k[pid, :, off] = 0
+    # copies: one layer, or one page
+    pool = torch.randn(1, 4, 2, 8, 64, device=DEV).half()
+    want = pool.clone()
+    want[:, 2] = want[:, 1]
+    pairs = torch.tensor([[1, 2]], dtype=torch.int32, device=DEV)
+    q.kv_copy_pages(pairs, pool.as_strided(pool.shape, (1, *pool.stride()[1:])))
+    assert torch.equal(pool, want)
+    one = pool[:, :1].as_strided((1, 1, 2, 8, 64), (1, 1, *pool.stride()[2:]))
+    q.kv_copy_pages(torch.zeros(1, 2, dtype=torch.int32, device=DEV), one)
+    assert torch.equal(pool, want) and q.device_error() == 0
+
+
 def test_binding_refusals(q):
     c = Cache([20], [1], 4, 2, 64, 16, "fp16")
     a = c.args()
