@@ -296,7 +296,8 @@ typedef struct {
  *   fp16; each row is quantized as quant_act_int8 does it: scale = amax / 127, code =
  *   rne(x / scale), a row of zeros scale 0), 16-byte aligned.
  * A token whose page is missing (a position before 0 or past the table, a page id outside
- * [0, num_pages)) is skipped and sets QW_ERR_BAD_INDEX.  One launch, async.  Returns QW_OK,
+ * [0, num_pages)) is skipped and sets QW_ERR_BAD_INDEX; so do offsets that descend or leave
+ * 0 .. T, whose tokens may be skipped or written at another position.  One launch, async.  Returns QW_OK,
  * QW_ERR_INVALID_ARG, QW_ERR_UNSUPPORTED_SHAPE, QW_ERR_ALIGNMENT, QW_ERR_ARCH or QW_ERR_CUDA.
  * ------------------------------------------------------------------------ */
 int kv_append(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const uint16_t *k, const uint16_t *v, int T,

@@ -65,7 +65,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps) kv_append_kernel(const __gr
   load(0);
   // the token's sequence: the last b with cu[b] <= t
   int b = t;
-  bool found = t < a.B && __ldg(a.cu + t) <= t && t < __ldg(a.cu + t + 1);
+  bool found = false;
+  if (t < a.B) {
+    const int c0 = __ldg(a.cu + t), c1 = __ldg(a.cu + t + 1);
+    found = c0 <= t && t < c1;
+    if (c0 < 0 || c1 < c0 || c1 > a.T) atomicCAS(a.err, 0, -9);      // offsets out of order
+  }
+  for (long long i = t + (lane + 1ll) * a.T; i < a.B; i += 32ll * a.T) {      // (sequences with no token)
+    const int c0 = __ldg(a.cu + i), c1 = __ldg(a.cu + i + 1);
+    if (c0 < 0 || c1 < c0 || c1 > a.T) atomicCAS(a.err, 0, -9);
+  }
   if (!found) {
     int lo = 0, hi = a.B;                        // the answer is in [lo, hi)
     while (hi - lo > 1) {

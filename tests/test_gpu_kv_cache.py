@@ -86,6 +86,24 @@ def test_append_bad_pages_are_skipped(q):
     assert torch.equal(bits(c.v), bits(before))
 
 
+@pytest.mark.parametrize("kind", ["fp16", "int8"])
+@pytest.mark.parametrize("cu", [[0, 2, 1, 6], [0, 900, 6, 6], [-1, 2, 4, 6], [0, 2, 4, 7], [5, 3, 1, 0], [0, 6, 6, 6, 6, 6, 6, 6, 5]])
+def test_append_offsets_out_of_order(q, kind, cu):
+    """Offsets that descend or leave 0 .. T are recorded; what is written stays in the named
+    sequences' pages, and those alone."""
+    B = len(cu) - 1
+    c = Cache([20] * B, [6] + [0] * (B - 1), 4, 2, 64, 16, kind, stale=0.25, spare=5)
+    c.cu.copy_(torch.tensor(cu, device=DEV))
+    before = c.k.clone(), c.v.clone()
+    q.kv_append(c.qkv[:, 4:6], c.qkv[:, 6:], *c.args(), **c.kw)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and q.device_error() == 0
+    spare = torch.ones(c.k.shape[0], dtype=torch.bool, device=DEV)
+    spare[c.table.flatten().long()] = False
+    assert int(spare.sum()) == 5
+    for x, w in zip((c.k, c.v), before):
+        assert torch.equal(bits(x[spare]), bits(w[spare]))
+
+
 def test_append_tokens_of_no_sequence(q):
     """Rows past cu_tokens[B] belong to nobody and are left out."""
     c = Cache([20], [3], 4, 2, 64, 16, stale=0.25)
