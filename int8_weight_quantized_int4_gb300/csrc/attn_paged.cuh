@@ -1234,16 +1234,16 @@ cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
 template <int KV>
 cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
   const bool many = 3ll * a.B * a.Hkv > sms;
-#define QW_PAGED(DD, C1, C2)                                               \
-  case DD:                                                                 \
-    return cols == 8 ? many ? paged_launch_one<DD, KV, 1, C1>(a, sms, st)  \
-                            : paged_launch_one<DD, KV, 1, 1>(a, sms, st)   \
-                     : many ? paged_launch_one<DD, KV, 2, C2>(a, sms, st)  \
+#define QW_PAGED(DD)                                                                       \
+  case DD:                                                                                  \
+    return cols == 8 ? many ? paged_launch_one<DD, KV, 1, paged_ctas(DD, 8)>(a, sms, st)    \
+                            : paged_launch_one<DD, KV, 1, 1>(a, sms, st)                    \
+                     : many ? paged_launch_one<DD, KV, 2, paged_ctas(DD, 64)>(a, sms, st)   \
                             : paged_launch_one<DD, KV, 2, 1>(a, sms, st);
   switch (d) {
-    QW_PAGED(64, 4, 4)
-    QW_PAGED(128, 4, 2)
-    QW_PAGED(256, 2, 1)
+    QW_PAGED(64)
+    QW_PAGED(128)
+    QW_PAGED(256)
   }
 #undef QW_PAGED
   return cudaErrorInvalidValue;

@@ -258,9 +258,8 @@ const void *append_kernel(int d) {
 // of 16.
 int paged_columns(int max_new, int G) { return (long long)max_new * G <= 8 ? 8 : 64; }
 constexpr size_t kPagedCounterBytes = 3 * kPagedMaxCtas * 4;   // three counters a CTA
-constexpr int kPagedCtas = 4;                    // CTAs an SM, at most
 size_t paged_ws(int d, int cols, int sms) {
-  return kPagedCounterBytes + (size_t)2 * kPagedCtas * sms * cols * (d + 2) * 4;
+  return kPagedCounterBytes + (size_t)2 * paged_ctas(d, cols) * sms * cols * (d + 2) * 4;
 }
 int check_heads(int d, int Hq, int Hkv, int max_new) {
   if (Hq < 1 || Hkv < 1 || max_new < 1) return bad(QW_ERR_INVALID_ARG, "Hq, Hkv and max_new must be positive");
@@ -392,7 +391,8 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
   a.G = Hq / c->Hkv;
   const int cols = paged_columns(max_new, a.G);
   const size_t need = paged_ws(c->d, cols, sms);
-  if (kPagedCtas * sms > kPagedMaxCtas) return bad(QW_ERR_ARCH, "more than %d SMs", kPagedMaxCtas / kPagedCtas);
+  const int most_sms = kPagedMaxCtas / paged_ctas(c->d, cols);
+  if (sms > most_sms) return bad(QW_ERR_ARCH, "more than %d SMs", most_sms);
   if (!ws || ws_bytes < need)
     return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
   a.q = q;

@@ -109,6 +109,8 @@ cudaError_t launch_attn(const AttnLaunch &L, cudaStream_t st);
 enum { kPagedF16 = 0, kPagedBf16 = 1, kPagedI8 = 2 };
 constexpr int kPagedMaxCtas = 1024;
 constexpr unsigned kPagedMaxPlaces = 1u << 30;   // of all items of a call
+// CTAs an SM where there are many items; cols: the columns of an item, 8 or up to 64
+constexpr int paged_ctas(int d, int cols) { return cols == 8 ? (d == 256 ? 2 : 4) : d == 64 ? 4 : d == 128 ? 2 : 1; }
 struct PagedArgs {
   const uint16_t *q;            // [T][Hq][d], token and head strides q_tok, q_head (elements)
   uint16_t *out;                // [T][Hq][d] dense
@@ -125,7 +127,7 @@ struct PagedArgs {
   int shift;                    // the schedule counts places (a strip of 16 keys for a block of columns) in 2^shift
   int min_places;               // fewest of those units a CTA takes
   float scale_log2;             // softmax scale * log2(e)
-  float *part;                  // [2 CTAs][rows (d + 2)] partial sums (workspace)
+  float *part;                  // [CTAs][2][rows (d + 2)] partial sums (workspace)
   int *counters;                // [kPagedMaxCtas] arrivals of an item's groups of parts, then [kPagedMaxCtas][2]
                                 //   of a group's parts; zero between calls (workspace)
   int *err;

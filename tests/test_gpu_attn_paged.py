@@ -569,6 +569,15 @@ def test_strides_of_extents_of_one_mean_nothing(q, kind, dim):
     assert torch.equal(pool, want) and q.device_error() == 0
 
 
+@pytest.mark.parametrize("d,new,ctas", [(64, 1, 4), (128, 1, 4), (256, 1, 2), (64, 2, 4), (128, 2, 2), (256, 2, 1)])
+def test_workspace_is_what_the_launch_can_use(q, d, new, ctas):
+    """Two partial sums (m, l and d channels a column) for each CTA that the widest launch has."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cols = 8 if new == 1 else 64
+    want = 12288 + 2 * ctas * sms * cols * (d + 2) * 4
+    assert q.lib().attn_paged_workspace_bytes(d, 12, 2, new) == want
+
+
 def test_binding_refusals(q):
     c = Cache([20], [1], 4, 2, 64, 16, "fp16")
     a = c.args()

@@ -74,7 +74,7 @@ def test_example_runs(ex, cache, capsys):
 def test_decode_and_verify_graphs_in_turn(ex, own, first):
     """A decode step and a verify step, each captured into a graph of its own, with no workspace
     given or with one that only the smaller step has sized, then replayed in turn: the eager
-    calls' bits.  The verify step's attention needs eight times the workspace."""
+    calls' bits.  The verify step's attention needs four times the workspace."""
     q, dev = ex.q, ex.DEV
     g = torch.Generator(device=dev).manual_seed(3)
     k, v = torch.randn(2, 400, 2, 16, 128, generator=g, device=dev).half()
