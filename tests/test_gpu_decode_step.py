@@ -142,3 +142,21 @@ def test_one_workspace_for_every_kind_of_call(ex):
             assert torch.equal(a, b), i
     torch.cuda.synchronize()
     assert q.device_error() == 0
+
+
+def test_captures_have_numbers(ex):
+    """0 outside a capture, one number in a capture, another in the next."""
+    q, dev = ex.q, ex.DEV
+    seen = []
+    x = torch.zeros(8, device=dev)
+
+    def number():
+        return int(q.lib().qw_stream_capture_id(torch.cuda.current_stream().cuda_stream))
+    for _ in range(2):
+        assert number() == 0
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            x += 1
+            seen.append(number())
+            x += 1
+            assert number() == seen[-1]
+    assert number() == 0 and seen[0] != seen[1] and all(seen)
