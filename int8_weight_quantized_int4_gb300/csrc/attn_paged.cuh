@@ -1225,12 +1225,12 @@ cudaError_t paged_launch_one(const PagedArgs &a, int sms, cudaStream_t st) {
 //
 // Several CTAs share an SM where there are many items (one CTA's exchange and join then overlap
 // the others' strips), one has it alone where there are few (a short call waits for one item,
-// which more warps finish sooner).  Measured, one against several: 64 x 8k of 8 heads of 128, bf16:
-// 192 and 181 us; 200 x 700: 82 and 58; 48 windows of 1024 of 8 heads of 64: 31.5 and 27.1; 64 x 3000
-// of 4 heads of 256: 74.2 and 71.1 (int8 49.5 and 45.2); and 16 x 3000 of 4 heads of 256 (64 items):
-// 28.5 and 26.8, 4 x 3000: 14.4 and 15.4; 2 x 3000 of 8 heads of 128: 11.3 and 12.9; 4 x 128k of 4
-// heads of 256, int8: 113.6 and 117.6.  Sixteen columns of d = 256 leave no registers for it
-// (48 x 16k, 24 columns: 299 and 382 us).
+// which more warps finish sooner).  Measured, one against several: 64 of 1000 to 8190 tokens, 32/8
+// heads of 128, bf16: 187.5 and 184.5 us; 200 x 700: 98.2 and 95.5; 48 windows of 1024, 64/8 heads of
+// 64: 32.7 and 27.9; 64 x 3000, 24/4 heads of 256: 126.3 and 127.6 (int8 81.6 and 76.4), 16 x 3000: 41.0 and
+// 40.3, 4 x 3000: 16.3 and 17.4; 2 x 3000 of 8 heads of 128: 12.5 and 13.0; 4 x 131071 of 4 heads of 256, int8:
+// 176 and 186; 32 x 16000, 24 columns of 8 heads of 128: 437 and 439.  Sixteen columns of d = 256 leave
+// no registers for it (48 x 16k, 24 columns, with one product a weight: 299 and 382 us).
 template <int KV>
 cudaError_t paged_launch(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st) {
   const bool many = 3ll * a.B * a.Hkv > sms;
