@@ -420,6 +420,79 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
                    int32_t *top_idx, void *ws, size_t ws_bytes, qw_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * A verify step over trees of drafted tokens: sample_tokens (a token for every node's row of
+ * logits), tree_accept, kv_keep_path.
+ *
+ * A sequence's new tokens are the nodes of a tree, written to the cache at its last positions
+ * in their order (kv_append).  parents [T] (int32, device) gives each node's parent as its place
+ * among the sequence's new tokens: an earlier node, or -1 for a root.  Node 0 is the token that
+ * the last step drew; a chain (parents -1, 0, 1, ..) is what attn_paged computes.
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * sample_tokens -- draws a token from each row of an [M, N] logit matrix.  With X the row's
+ * largest logit, token i weighs w_i = exp((x_i - X) / temperature).  In the order of the logits
+ * (larger first, equal ones by the smaller index):
+ *   top_k   leaves the first top_k (<= 0, or N and more: all);
+ *   top_p   of these the shortest beginning whose weights sum to at least top_p times their sum
+ *           (>= 1: all; <= 0: the first);
+ *   min_p   of these the ones with w_i >= min_p (<= 0: all).
+ * The first token always stays.  token[m] is the first token, in the order of the vocabulary, at
+ * which the running sum of the weights that stay passes u[m] times their sum (u in [0, 1));
+ * logprob[m] (may be NULL) the logarithm of its share of that sum.  A temperature that is not
+ * above 0 draws the first token, with logarithm 0.  NaN in top_p or min_p is none, in u 0.
+ *   logits: as token_logprobs, 1 <= N <= 2^20.  -inf and NaN weigh nothing; a row of nothing
+ *   else gives token -1 and -inf.  Rows with +inf draw among those.
+ *   settings: numbers for all rows, or per row [M] where the array is not NULL (device).
+ * Weights are compared and summed as whole numbers of 2^-40 (relative error 4e-9), so equal inputs
+ * give equal tokens; top-p's sum holds what lies far below the border in binary32.
+ * One launch, async, no workspace.  Returns as kv_append.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    float temperature, top_p, min_p;
+    int top_k;
+    const float *temperatures, *top_ps, *min_ps;
+    const int32_t *top_ks;
+} qw_sampling_t;
+int sample_tokens(const void *logits, int dtype, int M, int N, long long row_stride, const float *u,
+                  const qw_sampling_t *settings, int32_t *token, float *logprob, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tree_accept -- the path of each sequence's tree that the drawn tokens accept: node 0, and
+ * after a node its first child whose token is the one drawn at the node.
+ *   tokens, drawn, parents [T], cu_tokens [B + 1]: int32, device; drawn[t] is the token drawn from
+ *   node t's logits.
+ *   path [B][max_path] int32: the path's nodes (places among the sequence's new tokens), at most
+ *   max_path, -1 behind them; count [B] their number; next_token [B] the token drawn at the last of them
+ *   (-1 for a sequence without nodes).
+ * Offsets outside 0 .. T count as the nearest of these, a parent that is not an earlier node as
+ * none; both set QW_ERR_BAD_INDEX.  One launch, async.  Returns as kv_append.
+ * ------------------------------------------------------------------------ */
+int tree_accept(const int32_t *tokens, const int32_t *drawn, const int32_t *parents, const int32_t *cu_tokens, int B,
+                int T, int max_path, int32_t *path, int32_t *count, int32_t *next_token, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_keep_path -- moves the accepted nodes' rows together: with s the slot of a sequence's node
+ * 0, slot s + i takes the row of slot s + path[b][i], i < count[b], in every layer, head and pool;
+ * new_lens[b] (int32, may be NULL; not the batch's seq_lens) = s + count[b].
+ *   pools: up to four (K, V and their scales); token r of page p, head h, layer l is the
+ *   row_bytes bytes at base + l * layer_stride + p * page_stride + h * head_stride + r * token_stride
+ *   (strides in bytes, all multiples of 4; 16 bytes at a time where they and base allow).
+ *   batch, T: as kv_append; page the tokens of a page.  The pages that hold the nodes belong to one
+ *   sequence.  path [B][max_path], count [B]: as tree_accept gives them (entries ascend).
+ * An entry that does not ascend or names no node, a count outside 0 .. the nodes, or a page
+ * outside its pool moves nothing (the count taken as the nearest) and sets QW_ERR_BAD_INDEX.  One
+ * launch for all pools and layers, async.  Returns as kv_append.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *base;
+    int layers, num_pages, heads, row_bytes;
+    long long layer_stride, page_stride, head_stride, token_stride;
+} qw_row_pool_t;
+int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *batch, int T, int page,
+                 const int32_t *path, const int32_t *count, int max_path, int32_t *new_lens, qw_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * qgemm_w4a8_fused -- the W4A8 layer from fp16 activations: y is bit-identical
  * to quant_act_int8(x) followed by qgemm_w4a8 on the same weights ("In full"
  * item 4: activations quantized to int8 per token, int4 weights).

@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
     attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens) -> out
     kv_copy_pages(pairs, *pools)                     KvPool: pages of sequences, on the host
     token_logprobs(logits, tokens, k) -> TokenLogprobs
+    sample_tokens(logits, u, temperature, top_k, top_p, min_p) -> SampledTokens
+    tree_accept(tokens, drawn, parents, cu_tokens, max_path) -> TreePath
+    kv_keep_path(path, count, page_table, seq_lens, cu_tokens, *pools) -> new lengths
 """
 from __future__ import annotations
 
@@ -72,6 +75,16 @@ class PagePoolDesc(ctypes.Structure):
                 ("page_bytes", _ll)]
 
 
+class RowPoolDesc(ctypes.Structure):
+    _fields_ = [("base", _p), ("layers", _i), ("num_pages", _i), ("heads", _i), ("row_bytes", _i),
+                ("layer_stride", _ll), ("page_stride", _ll), ("head_stride", _ll), ("token_stride", _ll)]
+
+
+class SamplingDesc(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float), ("top_k", _i),
+                ("temperatures", _p), ("top_ps", _p), ("min_ps", _p), ("top_ks", _p)]
+
+
 _ip = ctypes.POINTER(ctypes.c_int)
 
 SIGNATURES = {
@@ -117,6 +130,9 @@ SIGNATURES = {
     "token_logprobs_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "token_logprobs_workspace_zero_bytes": (_sz, [_i, _i, _i, _i]),
     "token_logprobs": (_i, [_p, _i, _i, _i, _ll, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "sample_tokens": (_i, [_p, _i, _i, _i, _ll, _p, ctypes.POINTER(SamplingDesc), _p, _p, _p]),
+    "tree_accept": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p]),
+    "kv_keep_path": (_i, [ctypes.POINTER(RowPoolDesc), _i, ctypes.POINTER(KvBatchDesc), _i, _i, _p, _p, _i, _p, _p]),
     "qw_last_error_string": (ctypes.c_char_p, []),
     "qw_device_error": (_i, [_p]),
     "qw_num_kernel_launches": (_ll, []),
@@ -544,6 +560,10 @@ _pack_pool = struct.Struct("@Piiqqq").pack
 assert struct.calcsize("@PPPPiiiiiqqq") == ctypes.sizeof(KvCacheDesc)
 assert struct.calcsize("@PPPii0q") == ctypes.sizeof(KvBatchDesc)
 assert struct.calcsize("@Piiqqq") == ctypes.sizeof(PagePoolDesc)
+_pack_rows = struct.Struct("@Piiiiqqqq").pack
+_pack_sampling = struct.Struct("@fffiPPPP").pack
+assert struct.calcsize("@Piiiiqqqq") == ctypes.sizeof(RowPoolDesc)
+assert struct.calcsize("@fffiPPPP") == ctypes.sizeof(SamplingDesc)
 _i32, _f32 = torch.int32, torch.float32
 _INT_MAX = 0x7fffffff
 
@@ -856,6 +876,133 @@ def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> T
          4 if tt is _i32 else 8, C, k, logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), ptop, pidx, pbuf, nbytes,
          stream)
     return TokenLogprobs(logprob, entropy, lse, top, idx)
+
+
+# ------------------------------------------------- trees of drafted tokens --
+def _ints(t, name, n, index):
+    """Checks an int32 [n] (any length for n None) on device `index`; returns its length."""
+    if t.dtype is not _i32 or t.get_device() != index:
+        raise TypeError(f"{name} must be int32 on the device of the others, got {t.dtype} on {t.device}")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous [{'T' if n is None else n}], got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+class SampledTokens(NamedTuple):
+    token: torch.Tensor                 # [M] int32
+    logprob: torch.Tensor               # [M] of its share of what the filters leave
+
+
+def _setting(x, name, dtype, M, index):
+    """(number, pointer) of a sampler's setting: a number, or a tensor of one a row."""
+    if not isinstance(x, torch.Tensor):
+        return (_int(int(x)) if dtype is _i32 else x), 0
+    if x.dtype is not dtype or x.get_device() != index:
+        raise TypeError(f"{name} must be a number, or {dtype} on the logits' device")
+    if x.shape != (M,) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a number or a contiguous [{M}]")
+    return 0, x.data_ptr()
+
+
+def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0) -> SampledTokens:
+    """Draws a token from each row of logits [M, N] (fp16, bf16 or float32; rows may be strided)
+    with the uniform numbers u (float32 [M], in [0, 1)).  temperature (0: the most likely), top_k
+    (0: off), top_p (1: off, of what top_k leaves) and min_p (0: off, a share of the most likely
+    token's probability) are numbers, or tensors of one a row (float32; top_k int32)."""
+    dtype = _LOGIT_TYPES.get(logits.dtype)
+    index = logits.get_device()
+    if dtype is None or index < 0:
+        raise TypeError("logits must be a float16, bfloat16 or float32 CUDA tensor")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, N] with contiguous rows")
+    M, N = logits.shape
+    row, col = logits.stride()
+    if col != 1 and N > 1:
+        raise ValueError("logits must be [M, N] with contiguous rows")
+    if u.dtype is not _f32 or u.get_device() != index:
+        raise TypeError("u must be float32 on the logits' device")
+    if u.shape != (M,) or not u.is_contiguous():
+        raise ValueError(f"u must be a contiguous [{M}]")
+    t, pt = _setting(temperature, "temperature", _f32, M, index)
+    k, pk = _setting(top_k, "top_k", _i32, M, index)
+    p, pp = _setting(top_p, "top_p", _f32, M, index)
+    m, pm = _setting(min_p, "min_p", _f32, M, index)
+    token = torch.empty(M, dtype=_i32, device=logits.device)
+    logprob = torch.empty(M, dtype=_f32, device=logits.device)
+    _run(index, _step_fn("sample_tokens"), logits.data_ptr(), dtype, M, N, row if M > 1 else 0, u.data_ptr(),
+         _pack_sampling(t, p, m, k, pt, pp, pm, pk), token.data_ptr(), logprob.data_ptr(), _raw_stream(index))
+    return SampledTokens(token, logprob)
+
+
+class TreePath(NamedTuple):
+    path: torch.Tensor                  # [B, max_path] int32, the accepted nodes, -1 behind them
+    count: torch.Tensor                 # [B] int32, their number
+    next_token: torch.Tensor            # [B] int32, the token drawn at the last of them
+
+
+def tree_accept(tokens, drawn, parents, cu_tokens, max_path: int) -> TreePath:
+    """The path of each sequence's tree that the drawn tokens accept: node 0, and after a node
+    its first child whose token is the one drawn at the node.  tokens, drawn, parents int32 [T]."""
+    index = tokens.get_device()
+    if index < 0:
+        raise TypeError("tokens must be an int32 CUDA tensor")
+    T = _ints(tokens, "tokens", None, index)
+    _ints(drawn, "drawn", T, index)
+    _ints(parents, "parents", T, index)
+    B = _ints(cu_tokens, "cu_tokens", None, index) - 1
+    if B < 0:
+        raise ValueError("cu_tokens must be [B + 1]")
+    if not 1 <= max_path <= _INT_MAX:
+        raise ValueError("max_path must be positive")
+    out = torch.empty(B * (max_path + 2), dtype=_i32, device=tokens.device)
+    path, count, following = out[:B * max_path].view(B, max_path), out[B * max_path:B * max_path + B], out[B * max_path + B:]
+    at = out.data_ptr()
+    _run(index, _step_fn("tree_accept"), tokens.data_ptr(), drawn.data_ptr(), parents.data_ptr(), cu_tokens.data_ptr(), B,
+         T, max_path, at, at + 4 * B * max_path, at + 4 * B * (max_path + 1), _raw_stream(index))
+    return TreePath(path, count, following)
+
+
+def kv_keep_path(path, count, page_table, seq_lens, cu_tokens, *pools):
+    """Moves the rows of each sequence's accepted nodes (path int32 [B, max_path], count int32
+    [B], as tree_accept gives them) together behind the tokens before the tree, in every layer of
+    the pools: K and V [pages, Hkv, page, d] or [layers, pages, Hkv, page, d] (any strides with d
+    contiguous), the scales of an int8 cache [(layers,) pages, Hkv, page] float32.  seq_lens
+    counts all nodes; returns the lengths that remain, int32 [B]."""
+    index = path.get_device()
+    if index < 0 or path.dtype is not _i32:
+        raise TypeError("path must be an int32 CUDA tensor")
+    batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
+    B = page_table.shape[0]
+    if path.dim() != 2 or path.shape[0] != B or not path.is_contiguous():
+        raise ValueError("path must be a contiguous [B, max_path]")
+    _ints(count, "count", B, index)
+    if len(pools) > 4:
+        raise ValueError("at most four pools")
+    desc, page = b"", 0
+    for i, x in enumerate(pools):
+        if x.get_device() != index:
+            raise ValueError(f"pool {i} is on {x.device}, the path on {path.device}")
+        es, shape = x.element_size(), x.shape
+        stride = _strides(x) if 1 in shape else x.stride()
+        row = 1
+        if x.dtype is not _f32:
+            if len(shape) < 4 or stride[-1] != 1 and shape[-1] != 1:
+                raise ValueError(f"pool {i}: [(layers,) pages, Hkv, page, d] with d contiguous")
+            row, shape, stride = shape[-1], shape[:-1], stride[:-1]
+        elif 1 in shape[-1:]:
+            stride = (*stride[:-1], 0)
+        if len(shape) not in (3, 4):
+            raise ValueError(f"pool {i}: [(layers,) pages, Hkv, page, ...]")
+        if page and shape[-1] != page:
+            raise ValueError(f"pool {i} has pages of {shape[-1]} tokens, the others of {page}")
+        page = shape[-1]
+        lead = (shape[0], stride[0] * es) if len(shape) == 4 else (1, 0)
+        desc += _pack_rows(x.data_ptr(), lead[0], shape[-3], shape[-2], row * es, lead[1], stride[-3] * es, stride[-2] * es,
+                           stride[-1] * es)
+    lens = torch.empty(B, dtype=_i32, device=path.device)
+    _run(index, _step_fn("kv_keep_path"), desc or None, len(pools), batch, _INT_MAX, page or 1, path.data_ptr(),
+         count.data_ptr(), path.shape[1], lens.data_ptr(), _raw_stream(index))
+    return lens
 
 
 def qgemm_w4a16_noalloc(x, packed, N: int, K: int, y=None):

@@ -1,0 +1,1066 @@
+// sample.cu -- draws a token from each row of a logit matrix: temperature, top-k, top-p and
+// min-p, and one uniform number a row.
+//
+// With M the row's largest logit and t the temperature, token i weighs w_i = e^((x_i - M) / t).
+// In the order of the logits (larger first, equal ones by the index) top-k leaves the first k, of
+// these top-p the shortest beginning whose weights reach p times their sum, and of these min-p
+// the ones with w >= min_p; the first token always stays.  The draw is the first token, in the
+// order of the vocabulary, at which the running sum of what stays passes u times its total.
+//
+// A draw near a border of that sum is decided by the last digits, and there are as many borders
+// as tokens.  So the weights that decide are whole numbers, 2^40 w: x - M exactly (as two
+// binary32 terms), its product with log2(e) / t in two terms, 2^y = 2^n (1 + f ln 2 + f^2 q(f))
+// by the series of the exponential function, |f| <= 1/2, the first two terms exact: about 3e-9 of
+// w.  Whole numbers add up the same in any order, so atomics do not change a result.
+//
+// A cluster of 1 to 8 CTAs takes a row, as many as fill the GPU.
+//   1. One pass over the logits: the largest value of every block of 32 elements of a thread, and
+//      for top-p without top-k the block's sum of weights relative to it (binary32).
+//   2. A bound below which nothing can stay: for top-k, a warp's j-th largest block maximum is
+//      reached by j elements, so the least of these over all warps, j = ceil(k / warps), by k; for
+//      top-p the weight that N tokens together need to hold 1 - p of the sum; for min-p its own.
+//   3. Blocks that reach the bound are read again (from L2), their elements from the bound on
+//      listed; for top-p the rest's weights are summed, blocks that do not reach it as they are.
+//   4. The first CTA resolves the list (some hundreds): bins of a quarter of an octave hold
+//      counts and sums; a border falls in one bin, whose elements compare themselves with each other.
+// A list that overflows (flat rows), or no filter at all, goes over the whole row instead: bins
+// of an eighth of an octave, the border's bin refined by the digits of the values, and
+// the draw by sums of ever smaller ranges.
+#include <math.h>
+#include <stdarg.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "launch.h"
+#include "ptx.cuh"
+#include "qgemm.h"
+
+namespace qw {
+
+constexpr int kSmThreads = 256;
+constexpr int kSmWarps = kSmThreads / 32;
+constexpr int kSmBlocks = 8;                      // blocks a thread keeps the maxima of
+constexpr int kSmList = 1024;
+constexpr int kSmBins = 256;
+constexpr int kSmMaxCluster = 8;
+constexpr int kSmFix = 40;                        // weights in units of 2^-40
+
+typedef unsigned long long u64;
+
+struct SampleArgs {
+  const void *logits;
+  const float *u;
+  const float *temps, *top_ps, *min_ps;           // [M], or nullptr: the number below for every row
+  const int *top_ks;
+  float temp, top_p, min_p;
+  int top_k;
+  long long row_stride;                           // elements
+  int M, N;
+  int *token;
+  float *logprob;
+};
+
+struct SampleSmem {
+  float bmax[kSmBlocks][kSmThreads];
+  union {
+    float bsum[kSmBlocks][kSmThreads];
+    u64 w[kSmList];
+  };
+  u64 key[kSmList];                               // order key << 32 | ~index
+  union {
+    unsigned short work[kSmBlocks * kSmThreads];
+    unsigned short order[kSmList];
+  };
+  unsigned short start[kSmBins + 1];
+  unsigned cnt[kSmBins];                          // bins: elements,
+  unsigned limb[3][kSmBins];                      // and weights in three terms of 14 bits (a row's slice has below 2^18
+  u64 mass[kSmBins];                              // elements); or their sum
+  float red[kSmWarps];
+  unsigned rkey[kSmWarps];
+  u64 rsum[kSmWarps];
+  // read by the cluster's other CTAs
+  float xmax, xsum;
+  unsigned xkey;
+  u64 xtotal;
+  // written by them (first CTA)
+  unsigned n, gidx;
+  u64 tail[kSmMaxCluster];
+  // results of one thread or CTA for all
+  int bin, digit, found;
+  unsigned before;
+  u64 mbefore, total, top, thr;
+  float rowmax, rowsum;
+  unsigned rowkey;
+  int nwork;
+};
+
+// ------------------------------------------------------------------ clusters --
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer(const void *p, unsigned rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_ld32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ u64 peer_ld64(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_st32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_st64(uint32_t a, u64 v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned peer_add(uint32_t a, unsigned v) {
+  unsigned old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void peer_min(uint32_t a, unsigned v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// ------------------------------------------------------------------- numbers --
+__device__ __forceinline__ float sm_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sm_lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// binary32 values as unsigned integers in the values' order, -0 as +0, NaN below all (as -inf
+// it is never drawn)
+__device__ __forceinline__ unsigned sm_key(float x) {
+  const unsigned u = __float_as_uint(x + 0.0f);
+  return x == x ? u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float sm_value(unsigned k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// A row's scale: M and log2(e) / t = chi + clo.
+struct SampleScale {
+  float M, chi, clo;
+};
+// 2^40 e^((x - M) / t), rounded; 0 for -inf and NaN.  EXACT: x - M has no rounding (16-bit types).
+template <bool EXACT>
+__device__ __forceinline__ u64 sm_weight(float x, const SampleScale &c) {
+  if (x == c.M) return 1ull << kSmFix;            // (+inf too)
+  const float d = x - c.M;
+  float y = d * c.chi;
+  if (!(y > -60.0f)) return 0;                    // (and NaN)
+  float yl = fmaf(d, c.chi, -y) + d * c.clo;
+  if constexpr (!EXACT) {
+    const float b = d - x;                        // what the difference rounded off
+    yl = fmaf((x - (d - b)) + (-c.M - b), c.chi, yl);
+  }
+  const float n = rintf(y);
+  const float f = (y - n) + yl;
+  constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
+  const float p = f * L, pl = fmaf(f, L, -p) + f * Llo;
+  // (2^f - 1 - f ln 2) / f^2: ln(2)^k / k! f^(k - 2), k = 2 .. 8
+  float q = 1.3215487e-6f;
+  q = fmaf(q, f, 1.5252734e-5f);
+  q = fmaf(q, f, 1.5403530e-4f);
+  q = fmaf(q, f, 1.3333558e-3f);
+  q = fmaf(q, f, 9.6181291e-3f);
+  q = fmaf(q, f, 5.5504109e-2f);
+  q = fmaf(q, f, 0.24022651f);
+  const int i = __float2int_rn(p * 2147483648.0f) + __float2int_rn(fmaf(q, f * f, pl) * 2147483648.0f);
+  const unsigned m = 0x80000000u + (unsigned)i;   // 2^31 2^f: 0.7 .. 1.42
+  const int s = -(int)n;                          // (y <= 0; n up to 0)
+  return s <= 0 ? (u64)m << 9 : ((u64)m << 9) >> s;
+}
+
+// A row as 16-byte vectors: vector v holds columns v VE - pad .. + VE - 1, pad being how many
+// elements the row starts past a 16-byte boundary.  Places outside the row read as -inf.
+template <typename T>
+struct SampleRow {
+  static constexpr int VE = 16 / sizeof(T);
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr bool kBf = sizeof(T) == 2 && !__is_same(T, __half);
+  const T *row;
+  int pad, N, nvec, in0, in1;                     // whole vectors: [in0, in1)
+  __device__ __forceinline__ SampleRow(const T *r, int n) : row(r), N(n) {
+    pad = (int)((reinterpret_cast<uintptr_t>(r) / sizeof(T)) % VE);
+    nvec = (n + pad + VE - 1) / VE;
+    in0 = pad > 0 ? 1 : 0;
+    in1 = max((n + pad) / VE, in0);
+  }
+  __device__ __forceinline__ int col(int v) const { return v * VE - pad; }
+  static constexpr uint32_t kLowest = kF32 ? 0xff800000u : kBf ? 0xff80u : 0xfc00u;      // -inf
+  static __device__ __noinline__ uint4 edge(const T *row, int c, int N) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kF32) {
+        const int j = c + i;
+        w[i] = (unsigned)j < (unsigned)N ? __ldg(reinterpret_cast<const uint32_t *>(row) + j) : kLowest;
+      } else {
+        w[i] = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = c + 2 * i + h;
+          const uint32_t x = (unsigned)j < (unsigned)N ? __ldg(reinterpret_cast<const uint16_t *>(row) + j) : kLowest;
+          w[i] |= x << (16 * h);
+        }
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ uint4 load(int v) const {
+    return v >= in0 && v < in1 ? __ldg(reinterpret_cast<const uint4 *>(row + col(v))) : edge(row, col(v), N);
+  }
+  __device__ __forceinline__ static uint4 nothing() {
+    constexpr uint32_t w = kF32 ? kLowest : kLowest * 0x10001u;
+    return make_uint4(w, w, w, w);
+  }
+  __device__ __forceinline__ static void floats(const uint4 &r, float (&x)[VE]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kF32) {
+        x[i] = __uint_as_float(w[i]);
+      } else if constexpr (kBf) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(u32_as_h2(w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+  // the largest of a vector's elements so far (packed for 16-bit types; NaN left out)
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    if constexpr (kF32) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else if constexpr (kBf) {
+      const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+      return *reinterpret_cast<const uint32_t *>(&r);
+    } else return h2_as_u32(__hmax2(u32_as_h2(a), u32_as_h2(b)));
+  }
+  __device__ __forceinline__ static float max_of(uint32_t m) {
+    float r;
+    if constexpr (kF32) r = __uint_as_float(m);
+    else if constexpr (kBf) r = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    else {
+      const float2 f = __half22float2(u32_as_h2(m));
+      r = fmaxf(f.x, f.y);
+    }
+    return r == r ? r : -INFINITY;                // all NaN
+  }
+};
+
+// One CTA's place in the row's cluster.
+template <typename T>
+struct SampleCta {
+  static constexpr int VE = SampleRow<T>::VE;
+  static constexpr bool kExact = sizeof(T) == 2;
+  SampleSmem &s;
+  SampleRow<T> row;
+  int tid, warp, lane;
+  unsigned rank, size;
+  int v0, v1;                                     // its vectors
+  SampleScale sc;
+
+  __device__ __forceinline__ void sync() {        // the cluster's CTAs
+    if (size > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ u64 weight(float x) const { return sm_weight<kExact>(x, sc); }
+  // eighths (quarters) of an octave below the largest logit
+  __device__ __forceinline__ int bin_of(float x, float per) const {
+    if (x == sc.M) return 0;
+    const float y = (sc.M - x) * sc.chi * per;
+    return y < (float)(kSmBins - 1) ? (int)y : kSmBins - 1;        // (NaN: the last)
+  }
+
+  // Calls f(x, column) for every element of the CTA's vectors.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+    for (int v = v0 + tid; v < v1; v += kSmThreads) {
+      float x[VE];
+      SampleRow<T>::floats(row.load(v), x);
+      const int c = row.col(v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if ((unsigned)(c + e) < (unsigned)row.N) f(x[e], c + e);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ u64 warp_sum(F &f, int a, int b) {
+    u64 sum = 0;
+    for (int v = a + lane; v < b; v += 32) {
+      float x[VE];
+      SampleRow<T>::floats(row.load(v), x);
+      const int c = row.col(v);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if ((unsigned)(c + e) < (unsigned)row.N) sum += f(x[e], c + e);
+    }
+    return reduce(sum);
+  }
+  __device__ __forceinline__ static u64 reduce(u64 x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  }
+
+  // The first column, in order, at which the running sum of f over the whole row passes
+  // target(total): by the sums of the CTAs, of the warps' ranges and of pieces of one range.
+  // done(column, f there, total) is called by one thread of the CTA that holds it.
+  template <typename F, typename G, typename H>
+  __device__ __forceinline__ void find(F f, G target, H done) {
+    const int per = (v1 - v0 + kSmWarps - 1) / kSmWarps;
+    auto begin = [&](int w) { return min(v0 + w * per, v1); };
+    __syncthreads();
+    const u64 mine = warp_sum(f, begin(warp), begin(warp + 1));
+    if (lane == 0) s.rsum[warp] = mine;
+    __syncthreads();
+    if (tid == 0) {
+      u64 t = 0;
+      for (int w = 0; w < kSmWarps; ++w) t += s.rsum[w];
+      s.xtotal = t;
+    }
+    sync();
+    u64 total = 0, before = 0, own = 0;
+    for (unsigned r = 0; r < size; ++r) {
+      const u64 t = size > 1 ? peer_ld64(peer(&s.xtotal, r)) : s.xtotal;
+      if (r == rank) {
+        before = total;
+        own = t;
+      }
+      total += t;
+    }
+    u64 at = target(total);
+    const bool here = at >= before && at < before + own;
+    if (here) {                                   // (the whole CTA)
+      at -= before;
+      int w = 0;
+      while (w < kSmWarps - 1 && at >= s.rsum[w]) at -= s.rsum[w++];
+      const int a = begin(w), b = begin(w + 1), len = (b - a + kSmWarps - 1) / kSmWarps;
+      const int p0 = min(a + warp * len, b), p1 = min(p0 + len, b);
+      const u64 piece = warp_sum(f, p0, p1);
+      __syncthreads();
+      if (lane == 0) s.rsum[warp] = piece;
+      __syncthreads();
+      int q = 0;
+      while (q < kSmWarps - 1 && at >= s.rsum[q]) at -= s.rsum[q++];
+      if (q == warp) {
+        for (int v = p0; v < p1; v += 32) {       // 32 vectors at a time
+          float x[VE];
+          u64 sum = 0;
+          const int c = row.col(v + lane);
+          if (v + lane < p1) SampleRow<T>::floats(row.load(v + lane), x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (v + lane < p1 && (unsigned)(c + e) < (unsigned)row.N) sum += f(x[e], c + e);
+          u64 incl = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, incl > at);
+          if (past) {
+            if (lane == __ffs(past) - 1) {
+              u64 run = incl - sum;
+              bool got = false;
+#pragma unroll
+              for (int e = 0; e < VE; ++e) {
+                if (!got && (unsigned)(c + e) < (unsigned)row.N) {
+                  const u64 y = f(x[e], c + e);
+                  run += y;
+                  if (run > at) {
+                    got = true;
+                    done(c + e, y, total);
+                  }
+                }
+              }
+            }
+            break;
+          }
+          at -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void sample_write(const SampleArgs &a, int r, int token, u64 w, u64 total) {
+  a.token[r] = token;
+  if (a.logprob) a.logprob[r] = -log1pf((float)(total - w) / (float)w);
+}
+// floor(u total), below total
+__device__ __forceinline__ u64 sample_target(float u, u64 total) {
+  const double t = (double)u * (double)total;
+  return t > 0.0 ? min((u64)fmin(t, 1e19), total - 1) : 0;         // (NaN: 0)
+}
+// the least whole number that is not below p total
+__device__ __forceinline__ u64 sample_mass(float p, u64 total) {
+  return p > 0.0f ? (u64)ceil((double)p * (double)total) : 0;
+}
+
+// ------------------------------------------------------------------ the list --
+// Resolves the list of n elements (one CTA): which stay, and the draw among them.
+template <typename T>
+__device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
+                                            float u) {
+  SampleSmem &s = t.s;
+  constexpr int PER = kSmList / kSmThreads;
+  const int tid = t.tid, lane = t.lane;
+  for (int i = tid; i < kSmBins; i += kSmThreads) {
+    s.cnt[i] = 0;
+    s.mass[i] = 0;
+  }
+  if (tid == 0) {
+    s.top = 0;
+    s.total = 0;
+  }
+  __syncthreads();
+  u64 key[PER], w[PER];
+  int bin[PER];
+  unsigned nth[PER];
+  bool keep[PER];
+  u64 best = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid + i * kSmThreads;
+    keep[i] = e < n;
+    key[i] = w[i] = 0;
+    bin[i] = kSmBins;
+    if (!keep[i]) continue;
+    key[i] = s.key[e];
+    const float x = sm_value((unsigned)(key[i] >> 32));
+    w[i] = t.weight(x);
+    s.w[e] = w[i];
+    bin[i] = t.bin_of(x, 4.0f);
+    nth[i] = atomicAdd(&s.cnt[bin[i]], 1u);
+    atomicAdd(&s.mass[bin[i]], w[i]);
+    best = max(best, key[i]);
+  }
+  atomicMax(&s.top, best);
+  __syncthreads();
+  // the elements by their bins: bin b's are s.order[s.start[b]] .. [s.start[b + 1] - 1]
+  auto sort_bins = [&](auto on) {
+    unsigned incl = s.cnt[tid];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.rkey[t.warp] = incl;
+    __syncthreads();
+    for (int v = 0; v < t.warp; ++v) incl += s.rkey[v];
+    s.start[tid + 1] = (unsigned short)incl;
+    if (tid == 0) s.start[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (on(i)) s.order[s.start[bin[i]] + nth[i]] = (unsigned short)(tid + i * kSmThreads);
+    __syncthreads();
+  };
+  auto others = [&](int b, auto f) {
+    for (int q = s.start[b]; q < s.start[b + 1]; ++q) f(s.order[q]);
+  };
+  sort_bins([&](int i) { return keep[i]; });
+  // the first bin at which the running count (weights) reaches `need`, and what lies before it
+  auto border = [&](u64 need, bool by_mass) {
+    if (t.warp == 0) {
+      u64 v[kSmBins / 32], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kSmBins / 32; ++i) {
+        v[i] = by_mass ? s.mass[lane * (kSmBins / 32) + i] : s.cnt[lane * (kSmBins / 32) + i];
+        sum += v[i];
+      }
+      u64 incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned at = __ballot_sync(0xffffffffu, incl >= need);
+      if (lane == 0 && at == 0) s.bin = kSmBins;  // everything stays
+      if (at && lane == __ffs(at) - 1) {
+        u64 run = incl - sum;
+        int b = -1;
+#pragma unroll
+        for (int i = 0; i < kSmBins / 32; ++i) {
+          if (b < 0 && run + v[i] >= need) b = i;
+          if (b < 0) run += v[i];
+        }
+        s.bin = lane * (kSmBins / 32) + b;
+        s.mbefore = run;
+      }
+    }
+    __syncthreads();
+  };
+  if (k > 0 && n > k) {
+    border(k, false);
+    const int kb = s.bin;
+    const unsigned before = (unsigned)s.mbefore;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!keep[i] || bin[i] < kb) continue;
+      if (bin[i] == kb) {
+        unsigned rank = before;
+        others(kb, [&](int e) { rank += s.key[e] > key[i]; });
+        keep[i] = rank < (unsigned)k;
+      } else {
+        keep[i] = false;
+      }
+    }
+    __syncthreads();
+    // sums of what stays
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = tid + i * kSmThreads;
+      if (e < n && !keep[i]) {
+        atomicAdd(&s.mass[bin[i]], 0ull - w[i]);
+        s.w[e] = 0;
+      }
+    }
+    __syncthreads();
+  }
+  if (p < 1.0f) {
+    if (t.warp == 0) {
+      u64 sum = 0;
+      for (int i = lane; i < kSmBins; i += 32) sum += s.mass[i];
+      if (k == 0 && lane < (int)t.size) sum += s.tail[lane];
+      sum = SampleCta<T>::reduce(sum);
+      if (lane == 0) s.thr = sample_mass(p, sum);
+    }
+    __syncthreads();
+    const u64 thr = s.thr;
+    border(thr, true);
+    const int pb = s.bin;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!keep[i] || bin[i] < pb) continue;
+      if (bin[i] == pb) {
+        u64 above = s.mbefore;
+        others(pb, [&](int e) { if (s.key[e] > key[i]) above += s.w[e]; });
+        keep[i] = above < thr || key[i] == s.top;
+      } else {
+        keep[i] = key[i] == s.top;
+      }
+    }
+  }
+  if (mp > 0.0f) {
+    const u64 least = mp <= 1.0f ? (u64)ceil((double)mp * (double)(1ull << kSmFix)) : ~0ull;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) keep[i] = keep[i] && (w[i] >= least || key[i] == s.top);
+  }
+  // the draw, in the order of the vocabulary: bins of columns
+  __syncthreads();
+  for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = s.mass[i] = 0;
+  __syncthreads();
+  const int width = (t.row.N + kSmBins - 1) / kSmBins;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (!keep[i]) continue;
+    bin[i] = (int)(~(unsigned)key[i]) / width;
+    nth[i] = atomicAdd(&s.cnt[bin[i]], 1u);
+    atomicAdd(&s.mass[bin[i]], w[i]);
+  }
+  __syncthreads();
+  sort_bins([&](int i) { return keep[i]; });
+  if (t.warp == 0) {
+    u64 sum = 0;
+    for (int i = lane; i < kSmBins; i += 32) sum += s.mass[i];
+    sum = SampleCta<T>::reduce(sum);
+    if (lane == 0) {
+      s.total = sum;
+      s.thr = sample_target(u, sum) + 1;
+    }
+  }
+  __syncthreads();
+  border(s.thr, true);
+  const int vb = s.bin;
+  const u64 target = s.thr - 1;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const unsigned col = ~(unsigned)key[i];
+    if (!keep[i] || bin[i] != vb) continue;
+    u64 run = s.mbefore;
+    others(vb, [&](int e) { if (~(unsigned)s.key[e] < col) run += s.w[e]; });
+    if (run <= target && run + w[i] > target) sample_write(a, r, (int)col, w[i], s.total);
+  }
+}
+
+// --------------------------------------------------------------- whole rows --
+// What stays: keys above K, and those equal to it up to column I.
+struct SampleCut {
+  unsigned K;
+  int I;
+  __device__ __forceinline__ bool stays(unsigned key, int col) const { return key > K || (key == K && col <= I); }
+};
+
+// The cut that leaves the first `need` elements of those within `in` (need their number, or
+// their weights' sum: the shortest beginning that reaches it), one at least.
+template <typename T>
+__device__ __forceinline__ SampleCut sample_cut(SampleCta<T> &t, const SampleCut &in, u64 need, bool by_mass) {
+  SampleSmem &s = t.s;
+  unsigned prefix = 0, mask = 0;
+  int bin = -1;
+  u64 before = 0;
+  need = max(need, 1ull);
+  // bins of an eighth of an octave first, then the digits of the keys
+  constexpr int kDigits = sizeof(T) == 4 ? 4 : SampleRow<T>::kBf ? 2 : 3;      // (of 16-bit types the rest is all alike)
+  for (int round = 0; round <= kDigits; ++round) {
+    const int shift = 32 - 8 * round;
+    t.sync();                                     // the others have read the last round's bins
+    s.cnt[t.tid] = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s.limb[i][t.tid] = 0;
+    __syncthreads();
+    t.each([&](float x, int col) {
+      const unsigned key = sm_key(x);
+      if ((key & mask) != prefix || !in.stays(key, col)) return;
+      const int b = t.bin_of(x, 8.0f);
+      if (round > 0 && b != bin) return;
+      const int d = round == 0 ? b : 255 - (int)((key >> shift) & 255u);       // larger values first
+      if (by_mass) {
+        const u64 w = t.weight(x);
+        if (w == 0) return;
+        atomicAdd(&s.limb[0][d], (unsigned)w & 0x3fffu);
+        atomicAdd(&s.limb[1][d], (unsigned)(w >> 14) & 0x3fffu);
+        atomicAdd(&s.limb[2][d], (unsigned)(w >> 28));
+      } else {
+        atomicAdd(&s.cnt[d], 1u);
+      }
+    });
+    __syncthreads();
+    s.mass[t.tid] = by_mass ? (u64)s.limb[0][t.tid] + ((u64)s.limb[1][t.tid] << 14) + ((u64)s.limb[2][t.tid] << 28) : s.cnt[t.tid];
+    t.sync();
+    u64 v = s.mass[t.tid];
+    if (t.size > 1) {
+      v = 0;
+      for (unsigned r = 0; r < t.size; ++r) v += peer_ld64(peer(&s.mass[t.tid], r));
+    }
+    // running sums over the 256 bins, a bin a thread
+    u64 incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (t.lane >= o) incl += y;
+    }
+    if (t.lane == 31) s.rsum[t.warp] = incl;
+    if (t.tid == 0) s.digit = -1;
+    __syncthreads();
+    for (int w = 0; w < t.warp; ++w) incl += s.rsum[w];
+    incl += before;
+    if (incl >= need && incl - v < need) {        // one thread, or none where all stay
+      s.digit = t.tid;
+      s.mbefore = incl - v;
+    }
+    __syncthreads();
+    const int d = s.digit;
+    if (d < 0) return in;                         // (round 0 alone: together they do not reach it)
+    before = s.mbefore;
+    if (round == 0) {
+      bin = d;
+    } else {
+      prefix |= (unsigned)(255 - d) << shift;
+      mask |= 255u << shift;
+    }
+  }
+  // the low digits that all values of a 16-bit type share
+  if constexpr (sizeof(T) == 2) {
+    if (!(prefix >> 31)) prefix |= ~mask;
+  }
+  if (prefix <= 0x007fffffu) return in;           // -inf or NaN: they weigh nothing anyway
+  // how many of the equal ones stay
+  u64 ties = need - before;
+  if (by_mass) {
+    const u64 w = t.weight(sm_value(prefix));
+    ties = (ties + w - 1) / w;
+  }
+  if (t.tid == 0) s.found = 0x7fffffff;
+  __syncthreads();
+  t.find([&](float x, int col) { return (u64)(sm_key(x) == prefix && in.stays(prefix, col)); },
+         [&](u64) { return ties - 1; },
+         [&](int col, u64, u64) {
+           if (t.size > 1)
+             for (unsigned r = 0; r < t.size; ++r) peer_st32(peer(&s.found, r), (unsigned)col);
+           else
+             s.found = col;
+         });
+  t.sync();
+  return SampleCut{prefix, s.found};
+}
+
+template <typename T>
+__device__ __noinline__ void sample_row(const SampleArgs &a, SampleCta<T> t, int r, int k, float p, float mp, float u) {
+  SampleCut cut{0u, 0x7fffffff};
+  if (k > 0) cut = sample_cut(t, cut, (u64)k, false);
+  if (p < 1.0f) {
+    // the sum of what top-k left
+    const SampleCut in = cut;
+    t.find([&](float x, int col) { return in.stays(sm_key(x), col) ? t.weight(x) : 0ull; },
+           [&](u64 total) {
+             if (t.tid == 0) t.s.thr = sample_mass(p, total);
+             return ~0ull;                        // (no draw yet)
+           },
+           [](int, u64, u64) {});
+    __syncthreads();
+    const u64 need = t.s.thr;
+    cut = sample_cut(t, in, need, true);
+  }
+  const u64 least = !(mp > 0.0f) ? 0 : mp <= 1.0f ? (u64)ceil((double)mp * (double)(1ull << kSmFix)) : 1ull << kSmFix;
+  t.sync();
+  t.find(
+      [&](float x, int col) {
+        if (!cut.stays(sm_key(x), col)) return 0ull;
+        const u64 w = t.weight(x);
+        return w >= least ? w : 0ull;
+      },
+      [&](u64 total) { return sample_target(u, total); },
+      [&](int col, u64 w, u64 total) { sample_write(a, r, col, w, total); });
+}
+
+// ---------------------------------------------------------------- the kernel --
+template <typename T>
+__global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_constant__ SampleArgs a) {
+  __shared__ SampleSmem s;
+  constexpr int VE = SampleRow<T>::VE;
+  const unsigned rank = cluster_rank(), size = cluster_size();
+  const int r = (int)(blockIdx.x / size);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  const float tau = a.temps ? __ldg(a.temps + r) : a.temp;
+  int k = a.top_ks ? __ldg(a.top_ks + r) : a.top_k;
+  float p = a.top_ps ? __ldg(a.top_ps + r) : a.top_p;
+  float mp = a.min_ps ? __ldg(a.min_ps + r) : a.min_p;
+  const float u = __ldg(a.u + r);
+  const bool greedy = !(tau > 0.0f);
+  if (k <= 0 || k >= a.N) k = 0;
+  if (!(p < 1.0f)) p = 1.0f;
+  if (!(mp > 0.0f)) mp = 0.0f;
+  if (greedy) {
+    k = 0;
+    p = 1.0f;
+    mp = 0.0f;
+  }
+  const bool sums = p < 1.0f && k == 0;
+
+  SampleCta<T> t{s, SampleRow<T>(static_cast<const T *>(a.logits) + (long long)r * a.row_stride, a.N), tid, warp, lane, rank, size};
+  const int per = (t.row.nvec + (int)size - 1) / (int)size;
+  t.v0 = min((int)rank * per, t.row.nvec);
+  t.v1 = min(t.v0 + per, t.row.nvec);
+  // log2(e) / t in two terms: the quotient, and its remainder divided
+  constexpr float E = 1.44269504f, Elo = (float)(1.4426950408889634074 - (double)E);
+  t.sc.chi = fminf(__fdiv_rn(E, tau), 3.0e38f);
+  t.sc.clo = __fdiv_rn(fmaf(-t.sc.chi, tau, E) + Elo, tau);
+  if (greedy || !(fabsf(t.sc.clo) <= 1e-6f * t.sc.chi)) t.sc.clo = 0.0f;
+  const float c = t.sc.chi;
+
+  // ---- 1. blocks: U vectors of a thread, kSmThreads apart
+  constexpr int U0 = 32 / VE;
+  const int vecs = (t.v1 - t.v0 + kSmThreads - 1) / kSmThreads;
+  int U = U0, logU = U0 == 4 ? 2 : 3;
+  while (U * kSmBlocks < vecs) {
+    U *= 2;
+    ++logU;
+  }
+  const int nblk = (vecs + U - 1) / U;
+  if (tid == 0) {
+    s.n = s.nwork = 0;
+    s.gidx = 0xffffffffu;
+  }
+  float top = -INFINITY;
+  for (int b = 0; b < nblk; ++b) {
+    const int first = t.v0 + b * U * kSmThreads + tid;
+    float bm = -INFINITY, bs = 0.0f;
+    for (int g = 0; g < U && first + g * kSmThreads < t.v1; g += U0) {
+      uint4 raw[U0];
+#pragma unroll
+      for (int i = 0; i < U0; ++i) {
+        const int v = first + (g + i) * kSmThreads;
+        raw[i] = v < t.v1 ? t.row.load(v) : t.row.nothing();
+      }
+      uint32_t m = raw[0].x;
+#pragma unroll
+      for (int i = 0; i < U0; ++i) m = t.row.max2(m, t.row.max2(t.row.max2(raw[i].x, raw[i].y), t.row.max2(raw[i].z, raw[i].w)));
+      const float gm = t.row.max_of(m);
+      if (sums) {
+        const float nm = fmaxf(bm, gm), ref = nm == -INFINITY ? 0.0f : nm;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U0; ++i) {
+          float x[VE];
+          t.row.floats(raw[i], x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) sum += sm_ex2((x[e] - ref) * c);
+        }
+        if (!(sum < INFINITY)) {                  // NaN logits, or infinite ones
+          sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < U0; ++i) {
+            float x[VE];
+            t.row.floats(raw[i], x);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum += x[e] == ref ? 1.0f : x[e] > -INFINITY ? sm_ex2((x[e] - ref) * c) : 0.0f;
+          }
+        }
+        bs = (bs == 0.0f ? 0.0f : bs * sm_ex2((bm - nm) * c)) + sum;
+        bm = nm;
+      } else {
+        bm = fmaxf(bm, gm);
+      }
+    }
+    s.bmax[b][tid] = bm;
+    if (sums) s.bsum[b][tid] = bs;
+    top = fmaxf(top, bm);
+  }
+  // ---- 2. the row's largest logit, sum and bound
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s.red[warp] = top;
+  if (k > 0) {
+    // the j-th largest of the warp's block maxima, to 16 bits: by halving
+    const int j = (k + kSmWarps * (int)size - 1) / (kSmWarps * (int)size);
+    unsigned bound = 0;
+    if (j <= 32 * nblk) {
+      for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+        int n = 0;
+        for (int b = 0; b < nblk; ++b) n += __popc(__ballot_sync(0xffffffffu, sm_key(s.bmax[b][tid]) >= (bound | bit)));
+        if (n >= j) bound |= bit;
+      }
+    }
+    if (lane == 0) s.rkey[warp] = bound;
+  }
+  __syncthreads();
+  float cm = s.red[0];
+#pragma unroll
+  for (int w = 1; w < kSmWarps; ++w) cm = fmaxf(cm, s.red[w]);
+  auto rel = [&](float bm, float bs, float M) { return bs == 0.0f ? 0.0f : bm == M ? bs : bs * sm_ex2((bm - M) * c); };
+  if (sums) {
+    float sum = 0.0f;
+    for (int b = 0; b < nblk; ++b) sum += rel(s.bmax[b][tid], s.bsum[b][tid], cm);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
+    if (lane == 0) s.red[warp] = sum;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    float sum = 0.0f;
+    unsigned key = 0xffffffffu;
+    for (int w = 0; w < kSmWarps; ++w) {
+      if (sums) sum += s.red[w];
+      if (k > 0) key = min(key, s.rkey[w]);
+    }
+    s.xmax = cm;
+    s.xsum = sum;
+    s.xkey = key;
+  }
+  t.sync();
+  if (warp == 0) {
+    float m = -INFINITY, sum = 0.0f;
+    unsigned key = 0xffffffffu;
+    if (lane < (int)size) {
+      m = __uint_as_float(peer_ld32(peer(&s.xmax, lane)));
+      sum = __uint_as_float(peer_ld32(peer(&s.xsum, lane)));
+      key = peer_ld32(peer(&s.xkey, lane));
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    sum = rel(m, sum, M);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
+    }
+    if (lane == 0) {
+      s.rowmax = M;
+      s.rowsum = sum;
+      s.rowkey = key;
+    }
+  }
+  __syncthreads();
+  t.sc.M = s.rowmax;
+  const float M = t.sc.M;
+  if (M == -INFINITY) {                           // nothing to draw from
+    if (rank == 0 && tid == 0) {
+      a.token[r] = -1;
+      if (a.logprob) a.logprob[r] = -INFINITY;
+    }
+    t.sync();
+    return;
+  }
+  if (!greedy && k == 0 && p == 1.0f && mp == 0.0f) {
+    sample_row<T>(a, t, r, 0, 1.0f, 0.0f, u);
+    t.sync();                                     // (its sums have been read)
+    return;
+  }
+  // the bound, as an order key; a little lower where it is computed
+  unsigned T0 = k > 0 ? s.rowkey : 0u;
+  auto below = [&](float z) {                     // the key of M + z t ln 2, z <= 0
+    const float d = z / c;
+    return sm_key(M + d - (fabsf(d) * 1e-4f + fabsf(M) * 1e-6f));
+  };
+  if (sums) T0 = max(T0, below(fminf(sm_lg2((1.0f - p) * s.rowsum / (float)a.N) - 0.01f, 0.0f)));
+  if (mp > 0.0f && !(k > 0 && p < 1.0f)) T0 = max(T0, below(mp < 1.0f ? sm_lg2(mp) - 0.01f : 0.0f));
+  if (greedy) T0 = sm_key(M);
+  T0 = max(T0, 0x00800000u);                      // (the key of the lowest finite value: not -inf, not NaN)
+  if (M == INFINITY) T0 = sm_key(M);              // (weights of 0 beside it)
+
+  // ---- 3. the list
+  u64 tail = 0;
+  auto fixed = [&](float x) { return __float2ull_rn(x * (float)(1ull << kSmFix)); };
+  for (int b = 0; b < nblk; ++b) {
+    const float bm = s.bmax[b][tid];
+    const bool hit = sm_key(bm) >= T0;
+    const unsigned v = __ballot_sync(0xffffffffu, hit);
+    int at = 0;
+    if (v && lane == 0) at = atomicAdd(&s.nwork, __popc(v));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (hit) s.work[at + __popc(v & ((1u << lane) - 1u))] = (unsigned short)(b * kSmThreads + tid);
+    else if (sums) tail += fixed(rel(bm, s.bsum[b][tid], M));
+  }
+  __syncthreads();
+  const uint32_t lead_n = peer(&s.n, 0), lead_key = peer(&s.key[0], 0), lead_g = peer(&s.gidx, 0);
+  const int items = s.nwork * U;
+  for (int i = tid; i < items; i += kSmThreads) {
+    const int id = s.work[i >> logU], v = t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
+    if (v >= t.v1) continue;
+    float x[VE];
+    t.row.floats(t.row.load(v), x);
+    unsigned hits = 0;
+    float rest = 0.0f;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      if (sm_key(x[e]) >= T0) hits |= 1u << e;
+      else if (sums && x[e] > -INFINITY) rest += sm_ex2((x[e] - M) * c);
+    }
+    if (sums) tail += fixed(rest);
+    if (hits) {
+      const int col = t.row.col(v);               // (places outside the row are -inf)
+      if (greedy) {
+        peer_min(lead_g, (unsigned)(col + __ffs(hits) - 1));
+      } else {
+        unsigned at = peer_add(lead_n, __popc(hits));
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          if ((hits >> e & 1) && at < kSmList) peer_st64(lead_key + 8 * at, (u64)sm_key(x[e]) << 32 | (unsigned)~(col + e));
+          at += hits >> e & 1;
+        }
+      }
+    }
+  }
+  if (sums) {
+    tail = SampleCta<T>::reduce(tail);
+    if (lane == 0) s.rsum[warp] = tail;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kSmWarps; ++w) tail += s.rsum[w];
+      peer_st64(peer(&s.tail[rank], 0), tail);
+    }
+  }
+  t.sync();
+  if (greedy) {
+    if (rank == 0 && tid == 0) {
+      a.token[r] = (int)s.gidx;
+      if (a.logprob) a.logprob[r] = 0.0f;
+    }
+    return;                                       // (nobody reads another CTA's memory any more)
+  }
+  const unsigned n = peer_ld32(lead_n);
+  if (size > 1) {                                 // the first CTA's memory stays until all have read n
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (n <= kSmList) {
+    if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u);
+    return;
+  }
+  sample_row<T>(a, t, r, k, p, mp, u);
+  t.sync();
+}
+
+namespace {
+int bad(int code, const char *fmt, ...) {
+  char msg[400];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof msg, fmt, ap);
+  va_end(ap);
+  return set_last_error(code, msg);
+}
+bool at(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+}  // namespace
+}  // namespace qw
+
+using namespace qw;
+
+extern "C" int sample_tokens(const void *logits, int dtype, int M, int N, long long row_stride, const float *u,
+                             const qw_sampling_t *set, int32_t *token, float *logprob, qw_stream_t stream) {
+  if (M < 0 || row_stride < 0) return bad(QW_ERR_INVALID_ARG, "negative size");
+  if (dtype != QW_F16 && dtype != QW_BF16 && dtype != QW_F32) return bad(QW_ERR_INVALID_ARG, "logit type %d", dtype);
+  if (N < 1 || N > (1 << 20)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "1 <= N <= 2^20 (N=%d)", N);
+  if (!set) return bad(QW_ERR_INVALID_ARG, "null settings");
+  if (M == 0) return QW_OK;
+  if (!logits || !u || !token) return bad(QW_ERR_INVALID_ARG, "null tensor pointer");
+  if (!at(logits, dtype == QW_F32 ? 4 : 2) || !at(u, 4) || !at(token, 4) || !at(logprob, 4) || !at(set->temperatures, 4) ||
+      !at(set->top_ps, 4) || !at(set->min_ps, 4) || !at(set->top_ks, 4))
+    return bad(QW_ERR_ALIGNMENT, "arrays must be aligned to their elements");
+  int sms = 0, rc = device_info(&sms, nullptr);
+  if (rc) return rc;
+  SampleArgs a{logits,           u,          set->temperatures, set->top_ps, set->min_ps, set->top_ks, set->temperature,
+               set->top_p,       set->min_p, set->top_k,        row_stride,  M,           N,           token,
+               logprob};
+  // CTAs a row: as many as the GPU holds four an SM of, 2048 elements each at least, and so that
+  // a CTA's part has below 2^18 elements
+  int cluster = 1;
+  while (cluster < kSmMaxCluster && ((2ll * cluster * M <= 4ll * sms && 2 * cluster * 2048 <= N) || N / cluster >= (1 << 18) - 16))
+    cluster *= 2;
+  if ((long long)M * cluster > 0x7fffffffll) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many rows");
+  const void *f = dtype == QW_F16    ? reinterpret_cast<const void *>(sample_kernel<__half>)
+                  : dtype == QW_BF16 ? reinterpret_cast<const void *>(sample_kernel<__nv_bfloat16>)
+                                     : reinterpret_cast<const void *>(sample_kernel<float>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(M * cluster));
+  cfg.blockDim = dim3(kSmThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  void *argv[] = {&a};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, f, argv);
+  count_launch();
+  if (e != cudaSuccess) return bad(QW_ERR_CUDA, "sampling kernel launch: %s", cudaGetErrorString(e));
+  return QW_OK;
+}

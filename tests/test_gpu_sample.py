@@ -1,0 +1,207 @@
+"""sample_tokens against its definition in binary64 (tests/_tree_ref.py).
+
+Tolerances.  A weight is a whole number of 2^-40 within 4e-9 of its value, so a running sum is
+within 4e-9 (and N 2^-41 / total <= 2^20 2^-41 < 5e-7 only if all N weights were rounded the same
+way; independent, below 1e-9) of the total, and the sum that top-p takes its share of within 1e-7 of the
+part below the border.  So the draw has to be the definition's for some number within 1e-7 of u
+and of top_p (relative); its log probability, that answer's within 2^-22 (relative; absolute
+below 1): one rounding of the quotient, one of log1p (2 ulp), the weights."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import int8_weight_quantized_int4_gb300 as q
+from tests import _tree_ref as ref
+
+pytestmark = pytest.mark.gpu
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def check(logits, u, **kw):
+    r = q.sample_tokens(logits, u, **kw)
+    again = q.sample_tokens(logits, u, **kw)
+    assert torch.equal(r.token, again.token) and torch.equal(r.logprob, again.logprob)
+    assert q.device_error() == 0
+    x, uu = logits.double().cpu().numpy(), u.double().cpu().numpy()
+    rows = {n: v.double().cpu().numpy() if torch.is_tensor(v) else np.full(len(uu), np.float64(np.float32(v)))
+            for n, v in kw.items()}
+    token, lp = r.token.tolist(), r.logprob.double().tolist()
+    for i in range(len(uu)):
+        f = {n: (int(v[i]) if n == "top_k" else v[i]) for n, v in rows.items()}
+        ok = ref.draws(x[i], uu[i], **f)
+        assert token[i] in ok, (i, token[i], ok, f, uu[i])
+        assert any(lp[i] == e or abs(lp[i] - e) <= 2 ** -22 * max(1.0, abs(e)) for e in ok[token[i]]), (i, lp[i], ok, f)
+    return r
+
+
+def make(M, N, dtype, seed, spread=2.5, peaks=32):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, N, generator=g) * spread
+    if peaks:
+        at = torch.randint(0, N, (M, peaks), generator=g)
+        x.scatter_(1, at, torch.rand(M, peaks, generator=g) * 10 + 3)
+    return x.to(TYPES[dtype]).cuda(), torch.rand(M, generator=g).cuda()
+
+
+FILTERS = [dict(), dict(top_k=1), dict(top_k=40), dict(temperature=0.7, top_p=0.9), dict(min_p=0.03),
+           dict(temperature=1.3, top_k=100, top_p=0.8, min_p=0.02), dict(temperature=0.0), dict(top_p=0.999),
+           dict(top_k=3000, top_p=0.97), dict(temperature=2.0, top_k=700)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M,N", [(1, 1), (3, 2), (5, 7), (4, 33), (9, 1000), (6, 4097), (3, 50257), (700, 513), (2, 131073),
+                                 (1, 262144), (640, 2049)])
+def test_filters(M, N, dtype):
+    x, u = make(M, N, dtype, M * 7 + N)
+    for kw in FILTERS if M < 100 else FILTERS[:6]:
+        check(x, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_a_setting_a_row(dtype):
+    x, u = make(48, 6000, dtype, 3)
+    g = torch.Generator().manual_seed(4)
+
+    def pick(v, t=torch.float32):
+        return torch.tensor(v, dtype=t)[torch.randint(0, len(v), (48,), generator=g)].cuda()
+    check(x, u, temperature=pick([0.0, 0.5, 1.0, 1.7, -1.0]), top_k=pick([0, 1, 7, 300, 5999, 6000, 9000, -3], torch.int32),
+          top_p=pick([1.0, 0.9, 0.3, 0.0, 1.5]), min_p=pick([0.0, 0.1, 1.0, -0.5]))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N", [100, 3001, 40000])
+def test_flat_rows_and_ties(N, dtype):
+    """Lists that overflow: all equal, few values, a wide and flat distribution."""
+    g = torch.Generator().manual_seed(N)
+    few = torch.round(torch.randn(4, N, generator=g) * 2) / 2
+    flat = torch.randn(4, N, generator=g) * 0.05
+    same = torch.full((2, N), -7.25)
+    x = torch.cat([few, flat, same]).to(TYPES[dtype]).cuda()
+    u = torch.rand(10, generator=g).cuda()
+    for kw in (dict(), dict(top_k=N // 3), dict(top_p=0.6), dict(top_k=N // 2, top_p=0.5), dict(min_p=0.9), dict(temperature=0.0),
+               dict(top_k=5, top_p=0.5), dict(top_p=0.99, min_p=0.3), dict(top_k=N // 3, min_p=1.0)):
+        check(x, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N", [65, 20011])
+def test_masked_places(N, dtype):
+    x, u = make(12, N, dtype, N)
+    g = torch.Generator().manual_seed(9)
+    hide = (torch.rand(12, N, generator=g) < 0.97).cuda()
+    hide[:, 3] = False
+    low = torch.finfo(x.dtype).min
+    for v in (float("-inf"), low, float("nan")):
+        y = x.masked_fill(hide, v)
+        y[1] = v                                       # a row of nothing else
+        y[2, : N // 2] = v
+        y[3] = float("-inf")
+        y[4] = low
+        y[5] = float("nan")
+        for kw in (dict(), dict(top_k=20), dict(top_p=0.9), dict(min_p=0.05), dict(temperature=0.0),
+                   dict(top_k=50, top_p=0.7, min_p=0.01), dict(temperature=1e-3), dict(top_k=N - 1)):
+            check(y, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_infinite_logits(dtype):
+    x, u = make(6, 3000, dtype, 1)
+    x[0, 17] = x[0, 2900] = float("inf")
+    x[1, 5] = float("inf")
+    x[2, ::3] = float("inf")
+    x[3, 100] = float("inf")
+    x[3, 101] = float("-inf")
+    x[3, 102] = float("nan")
+    for kw in (dict(), dict(top_k=20), dict(top_p=0.9), dict(min_p=0.05), dict(temperature=0.0), dict(top_k=2, top_p=0.4)):
+        check(x, u, **kw)
+
+
+def test_strided_rows_and_borders_of_u():
+    x, _ = make(8, 5001, "bf16", 5)
+    wide = torch.zeros(8, 9001, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2001:7002] = x
+    u = torch.tensor([0.0, 1.0 - 2 ** -24, 0.5, 1e-30, 0.999, 0.25, 0.75, 1.0], device="cuda")
+    for kw in (dict(), dict(top_k=30), dict(top_p=0.8)):
+        r = check(wide[:, 2001:7002], u, **kw)
+        s = check(x, u, **kw)
+        assert torch.equal(r.token, s.token) and torch.equal(r.logprob, s.logprob)
+    one = q.sample_tokens(x[2:3], u[2:3], top_p=0.8)          # a row alone: spread over more CTAs
+    assert one.token.item() == s.token[2].item()
+    # out-of-range numbers draw the first or the last of what stays
+    odd = q.sample_tokens(x[:4], torch.tensor([-1.0, 2.0, float("nan"), float("inf")], device="cuda"), top_k=3)
+    best = torch.topk(x[:4].float(), 3).indices.sort(1).values
+    assert odd.token.tolist() == [best[0, 0], best[1, 2], best[2, 0], best[3, 2]]
+
+
+def test_greedy_takes_the_first_of_equals():
+    x = torch.zeros(3, 9000, device="cuda")
+    x[0, 8000] = x[0, 4000] = x[0, 4001] = 2.0
+    x[1, 1:] = -0.0
+    r = q.sample_tokens(x, torch.rand(3, device="cuda"), temperature=0)
+    assert r.token.tolist() == [4000, 0, 0] and r.logprob.tolist() == [0, 0, 0]
+
+
+def test_largest_row():
+    N = 1 << 20
+    x, u = make(2, N, "bf16", 8)
+    for kw in (dict(), dict(top_k=64), dict(top_p=0.9), dict(top_k=5000)):
+        check(x, u, **kw)
+
+
+def test_shares_follow_the_probabilities():
+    """The u's of an even grid draw each token as often as its probability says, within one."""
+    x, _ = make(1, 300, "fp32", 12, spread=1.0, peaks=0)
+    n = 4096
+    u = ((torch.arange(n, dtype=torch.float32) + 0.5) / n).cuda()
+    r = q.sample_tokens(x.expand(n, 300), u, top_k=50)
+    w = torch.softmax(torch.topk(x[0].double(), 50).values, 0)
+    got = torch.bincount(r.token.long(), minlength=300)[torch.topk(x[0], 50).indices]
+    assert (got - w * n).abs().max() <= 1.0 + 1e-3 and int(got.sum()) == n
+
+
+def test_streams_graphs_and_empty():
+    x, u = make(16, 7000, "fp16", 2)
+    want = q.sample_tokens(x, u, top_p=0.9)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = q.sample_tokens(x, u, top_p=0.9)
+    side.synchronize()
+    assert torch.equal(other.token, want.token)
+    p = torch.full((16,), 0.9, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = q.sample_tokens(x, u, top_p=p)
+    for _ in range(2):
+        g.replay()
+        assert torch.equal(r.token, want.token) and torch.equal(r.logprob, want.logprob)
+    x.copy_(make(16, 7000, "fp16", 77)[0])
+    p.fill_(0.5)
+    g.replay()
+    assert torch.equal(r.token, q.sample_tokens(x, u, top_p=0.5).token)
+    none = q.sample_tokens(x[:0], u[:0])
+    assert none.token.shape == (0,)
+
+
+def test_binding_refusals():
+    x, u = make(4, 50, "fp16", 2)
+    with pytest.raises(TypeError):
+        q.sample_tokens(x.double(), u)
+    with pytest.raises(TypeError):
+        q.sample_tokens(x.cpu(), u)
+    with pytest.raises(ValueError):
+        q.sample_tokens(x.T, u)
+    with pytest.raises(ValueError):
+        q.sample_tokens(x, u[:3])
+    with pytest.raises(TypeError):
+        q.sample_tokens(x, u.double())
+    with pytest.raises(TypeError):
+        q.sample_tokens(x, u, top_k=torch.ones(4, device="cuda"))
+    with pytest.raises(ValueError):
+        q.sample_tokens(x, u, top_p=torch.ones(5, device="cuda"))
+    with pytest.raises(ValueError):
+        q.sample_tokens(x, u, top_k=1 << 40)
+    with pytest.raises(q.QgemmError):
+        q.sample_tokens(x[:, :0], u)
