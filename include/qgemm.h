@@ -420,14 +420,33 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
                    int32_t *top_idx, void *ws, size_t ws_bytes, qw_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * A verify step over trees of drafted tokens: sample_tokens (a token for every node's row of
- * logits), tree_accept, kv_keep_path.
+ * A verify step over trees of drafted tokens: attn_tree, sample_tokens (a token for every
+ * node's row of logits), tree_accept, kv_keep_path.
  *
  * A sequence's new tokens are the nodes of a tree, written to the cache at its last positions
  * in their order (kv_append).  parents [T] (int32, device) gives each node's parent as its place
  * among the sequence's new tokens: an earlier node, or -1 for a root.  Node 0 is the token that
  * the last step drew; a chain (parents -1, 0, 1, ..) is what attn_paged computes.
  * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * attn_tree -- attn_paged for the nodes of a tree.  With s the slot of the sequence's node 0
+ * (its length minus its nodes), the node r at depth e (the number of its ancestors) is at
+ * position s + e; it sees the keys j < s and those of its ancestors and itself, with window > 0
+ * only the ones at positions above s + e - window or below `sinks`.
+ *   max_nodes: 1 .. 256, at least the nodes of any sequence (a sequence with more gives rows of
+ *   zeros and QW_ERR_BAD_INDEX; so does a parent that is not an earlier node, which counts as -1
+ *   then).  The workspace's size depends on it not at all.
+ *   ws: attn_tree_workspace_bytes(d, Hq, Hkv) bytes, 256-byte aligned, no zeroing needed; not
+ *   shared by calls that may run concurrently.
+ * Other arguments, masked values, bad pages and lengths as attn_paged.  Results are bit-identical
+ * between calls (on devices with the same number of SMs).  Two launches, async.  Returns as
+ * attn_paged.
+ * ------------------------------------------------------------------------ */
+size_t attn_tree_workspace_bytes(int d, int Hq, int Hkv);
+int attn_tree(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const int32_t *parents, const uint16_t *q, int T,
+              int Hq, long long q_token_stride, long long q_head_stride, int max_nodes, int window, int sinks,
+              float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes, qw_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * sample_tokens -- draws a token from each row of an [M, N] logit matrix.  With X the row's

@@ -14,6 +14,7 @@ Entry points (same names as the C ABI):
     attn_paged(q, k_pages, v_pages, page_table, seq_lens, cu_tokens) -> out
     kv_copy_pages(pairs, *pools)                     KvPool: pages of sequences, on the host
     token_logprobs(logits, tokens, k) -> TokenLogprobs
+    attn_tree(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, parents) -> out
     sample_tokens(logits, u, temperature, top_k, top_p, min_p) -> SampledTokens
     tree_accept(tokens, drawn, parents, cu_tokens, max_path) -> TreePath
     kv_keep_path(path, count, page_table, seq_lens, cu_tokens, *pools) -> new lengths
@@ -130,6 +131,9 @@ SIGNATURES = {
     "token_logprobs_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "token_logprobs_workspace_zero_bytes": (_sz, [_i, _i, _i, _i]),
     "token_logprobs": (_i, [_p, _i, _i, _i, _ll, _p, _i, _i, _i, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "attn_tree_workspace_bytes": (_sz, [_i, _i, _i]),
+    "attn_tree": (_i, [ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvBatchDesc), _p, _p, _i, _i, _ll, _ll, _i, _i, _i,
+                       ctypes.c_float, _p, _p, _p, _sz, _p]),
     "sample_tokens": (_i, [_p, _i, _i, _i, _ll, _p, ctypes.POINTER(SamplingDesc), _p, _p, _p]),
     "tree_accept": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p]),
     "kv_keep_path": (_i, [ctypes.POINTER(RowPoolDesc), _i, ctypes.POINTER(KvBatchDesc), _i, _i, _p, _p, _i, _p, _p]),
@@ -886,6 +890,35 @@ def _ints(t, name, n, index):
     if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be a contiguous [{'T' if n is None else n}], got {tuple(t.shape)}")
     return t.shape[0]
+
+
+def attn_tree(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, parents, max_nodes: int = 64, window: int = 0,
+              sinks: int = 0, scale: float | None = None, k_scale=None, v_scale=None, out=None, lse=None,
+              ws: Workspace | None = None):
+    """attn_paged for new tokens that are the nodes of a tree: parents (int32 [T]) gives each
+    node's parent as its place among the sequence's new tokens, an earlier one, or -1.  A node sees
+    the keys before the tree, its ancestors and itself; window counts positions, a node's being
+    the first node's slot plus its depth.  max_nodes (<= 256): at least the nodes of any sequence."""
+    index = k_pages.get_device()
+    cache, dtype, heads, d = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
+    T, Hq, qt, qh = _rows(q, "q", dtype, d, index, 0)
+    _ints(parents, "parents", T, index)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    elif out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != index or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor {tuple(q.shape)} on the cache's device")
+    if lse is not None and (lse.dtype is not _f32 or lse.shape != (T, Hq) or lse.get_device() != index
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor {(T, Hq)} on the cache's device")
+    if max(max_nodes, window, sinks) > _INT_MAX or min(max_nodes, window, sinks) < 0:
+        max_nodes, window, sinks = (max(min(x, _INT_MAX), -1) for x in (max_nodes, window, sinks))   # -1: refused below
+    stream = _raw_stream(index)
+    buf, pbuf, nbytes = _scratch(ws, index, stream, "tree", _step_fn("attn_tree_workspace_bytes"), d, Hq, heads)
+    _run(index, _step_fn("attn_tree"), cache, batch, parents.data_ptr(), q.data_ptr(), T, Hq, qt, qh, max_nodes, window,
+         sinks, d ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), pbuf,
+         nbytes, stream)
+    return out if lse is None else (out, lse)
 
 
 class SampledTokens(NamedTuple):

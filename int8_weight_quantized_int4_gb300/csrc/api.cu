@@ -269,6 +269,10 @@ namespace qw {
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
+unsigned long long wait_limit_ns() {
+  return 1000ull * (unsigned long long)g_opt_wait_limit_us.load(std::memory_order_relaxed);
+}
+
 int set_last_error(int code, const char *msg) { return fail(code, "%s", msg); }
 
 int device_info(int *sms, int **err) {

@@ -1,0 +1,1034 @@
+// attn_tree.cuh -- attention of the nodes of trees of drafted tokens over a paged key-value cache.
+//
+// A sequence of length n whose last m positions hold the nodes of a tree: with s = n - m, node r at
+// depth e (its ancestors) stands at position s + e and sees the keys j < s and those of its
+// ancestors and itself (with a window W only positions above s + e - W or below `sinks`).  For head h
+// of a node and KV head g = h / G,
+//   x_j = q . k_j * scale,  p_j = e^(x_j - m),  out = sum_j p_j v_j / sum_j p_j.
+//
+// The G heads and m nodes that share a KV head are the rows of a 128-row tile, tiles of 64 keys
+// stream past it: S = Q K^T and O += P V on tcgen05, S and O in TMEM, a row a thread in the
+// softmax.  Reading K and V takes 4 D bytes a key for 128 x 2 x 3 D flops (P enters P V as two
+// 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
+// of the 128 rows a small tree fills.
+//
+// Roles of a CTA's warps: 4 of softmax (warp w reads TMEM lanes 32 w ..), 1 issuing MMAs, 4 loading (2
+// with an int8 cache) and for an int8 cache 4 that widen codes to fp16 (exact).  A ring of stages, each
+// 64 rows of K or V, in the order K0 K1 V0 K2 V1 .. of a segment: scores of the next tile are
+// computed while the softmax works on the last.
+//   - Rows are loaded with cp.async, 16 bytes a thread, straight to the 128-byte swizzle: pages of
+//     any size and order, and rows that no node sees are zero-filled, not read.  K is the K-major
+//     operand and V, as it lies, the MN-major one, so nothing is transposed.
+//   - P goes back into TMEM over the scores it came from.
+//   - O is rescaled only when a score passes the reference by 2^8 (fp16: 2^15).
+//   - A tile that some rows see partly gets a 64-bit mask a row: the window's and the length's
+//     borders, and the bits of the row's ancestors (found by walking the parents once an item).
+//
+// Work: the tiles of every (sequence, KV head, block of 128 rows) item are laid end to end and cut into
+// one equal range a CTA; an item that a border cuts leaves (m, l, O) parts in the workspace, which a
+// second kernel joins.  Where sequences have several row blocks, R CTAs form a team that runs
+// one range, a row block each, so that K and V come from HBM once and from L2 for the others.
+//
+// Roundings: each weight enters P V as two terms of the values' 16-bit type, p rounded and what
+// that leaves, so the products keep 22 bits of it (bf16: 16), all sums are binary32 and the output's
+// rounding is what remains.  In fp16 the reference starts 2^7 below the largest score, so that
+// only weights below 2^-32 of it are lost.  With the int8 cache the value's scale joins its weight.
+#pragma once
+#include <stdint.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace qw {
+
+constexpr int kTreeKeys = 64;                     // keys of a tile
+constexpr int kTreeRows = 128;                    // rows (columns of a KV head: node x head) of an item
+constexpr int kTreeSegs = 32;                     // segments listed at a time
+constexpr int kTreeMaxTeam = 4;
+constexpr float kTreeNoScore = -3.402823466e38f;
+
+struct TreeSeg {
+  int b, g, rb;                                   // sequence, KV head, row block
+  int u0, u1;                                     // tiles [u0, u1) of the item's
+  int nsu, first;                                 // tiles of the sinks, tile of the first windowed key
+  int lo, len, pos0;                              // keys [lo, len) and below `sinks`; the slot of node 0
+  int tok0, nodes;
+  int slot;                                       // -1: the whole item; 0: begins inside it; 1: begins it
+  int parts;
+};
+
+struct TreeCtl {
+  int nseg, more, team, member, size;             // size: CTAs of a team
+  int b, dead;
+  long long off, pos, begin, end, share;
+  long long part[16][kTreeMaxTeam];
+  unsigned long long bad;                         // keys of a tile whose values are not finite
+  int zeroed;                                     // the segment (counted from 1) whose O was cleared before its first P V
+};
+
+template <int D, int KV>
+struct TreeShape {
+  static constexpr bool kI8 = KV == kPagedI8;
+  static constexpr int kLoaders = kI8 ? 2 : 4;    // warps
+  static constexpr int kWideners = kI8 ? 4 : 0;
+  static constexpr int kMmaWarp = 4, kLoad0 = 5, kWiden0 = kLoad0 + kLoaders;
+  static constexpr int kWarps = kWiden0 + kWideners;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = tree_ctas(D);
+  static constexpr int kStage = kTreeKeys * D * 2;
+  static constexpr int kStages = kI8 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : D == 64 ? 8 : 4;
+  static constexpr int kRaw = kI8 ? kTreeKeys * D : 0;                // a stage of codes
+  static constexpr int kRaws = !kI8 ? 0 : D == 256 ? 5 : D == 128 ? 3 : 8;
+  static constexpr int kScaleSlots = D == 64 ? 16 : 8;   // tiles whose scales are kept (more than can be under way)
+  static constexpr int kQ = kTreeRows * D * 2;
+  static constexpr uint32_t kTmem = D == 256 ? 512 : 256;
+  static constexpr uint32_t kSCol = D;            // O [0, D), then two buffers of 64 columns of S and P
+  static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 8 : 0;
+  static constexpr int kFixed = kScaleBytes + 512 /* barriers */ + 512 /* parents */ + kTreeSegs * (int)sizeof(TreeSeg) + (int)sizeof(TreeCtl) + 64;
+  static constexpr int kSmem = 1024 + kQ + kStages * kStage + kRaws * kRaw + kFixed;
+  static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024, "shared memory");
+  static_assert(kStages + kRaws + 4 < 2 * kScaleSlots - 2, "scales outlive their use");
+  // what an item costs beside its tiles, in tiles: about the time of 192 KB
+  static constexpr int kItemCost = 196608 / (2 * kStage / (kI8 ? 2 : 1));
+};
+
+__device__ __forceinline__ float tree_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float tree_lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// arrive on `bar` when the thread's cp.async copies so far have landed (counted as one arrival)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 32 bytes: a whole sector from one thread
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// MN-major operand in the 128-byte swizzle: 128-byte rows of 64 channels, a row a key; groups of
+// eight keys 1024 bytes apart, the next 64 channels a tile of keys further.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)(kTreeKeys * 128 >> 4) << 16;     // leading byte offset: along the channels
+  d |= (uint64_t)(1024 >> 4) << 32;                // stride byte offset: along the keys
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Instruction descriptor, kind::f16: D fp32, A and B both fp16 or both bf16, B MN-major or not.
+__host__ __device__ constexpr uint32_t tree_idesc(bool bf, bool b_mn, int M, int N) {
+  return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t tree_pack(float x, float y) {
+  if constexpr (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    return h2_as_u32(__floats2half2_rn(x, y));
+  }
+}
+template <bool BF>
+__device__ __forceinline__ float2 tree_unpack(uint32_t w) {
+  if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(u32_as_h2(w));
+}
+// Two int8 codes of a word (xor 0x80 applied: code + 128) as fp16: 0x6400 | u is 1024 + u.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t tree_widen(uint32_t u) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x64646464u), "n"(SEL));
+  return h2_as_u32(__hsub2(u32_as_h2(r), u32_as_h2(0x64806480u)));
+}
+
+// --------------------------------------------------------------- the schedule --
+struct TreeSeq {
+  int tok0, nodes, len;
+  bool fine;
+};
+// Sequence b's nodes and keys, clamped to what the buffers hold.
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
+  TreeSeq s;
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), n = __ldg(a.lens + b);
+  s.tok0 = min(max(c0, 0), a.T);
+  s.nodes = max(min(max(c1, 0), a.T) - s.tok0, 0);
+  s.len = min(max(n, 0), a.cap);
+  if (c0 != s.tok0 || c1 != s.tok0 + s.nodes || n != s.len || s.nodes > a.max_nodes) atomicCAS(a.err, 0, -9);
+  if (s.nodes > a.max_nodes) s.len = 0;           // rows of zeros
+  return s;
+}
+struct TreeSpan {
+  int lo, nsu, first, n, blocks;
+};
+__device__ __forceinline__ TreeSpan tree_span(const TreeArgs &a, const TreeSeq &s) {
+  TreeSpan p;
+  p.lo = a.window > 0 ? max(s.len - s.nodes - a.window + 1, 0) : 0;
+  p.first = p.lo / kTreeKeys;
+  p.nsu = min((min(a.sinks, s.len) + kTreeKeys - 1) / kTreeKeys, p.first);
+  p.n = max(p.nsu + (s.len + kTreeKeys - 1) / kTreeKeys - p.first, 1);       // an item without keys still writes its rows
+  p.blocks = (int)(((long long)s.nodes * a.G + kTreeRows - 1) / kTreeRows);
+  return p;
+}
+// places of a sequence for teams of R
+template <int IC>
+__device__ __forceinline__ long long tree_places(const TreeArgs &a, const TreeSpan &p, int R) {
+  return (long long)((p.blocks + R - 1) / R) * a.Hkv * (p.n + IC);
+}
+
+// Lists the range's next segments (one thread).
+template <int IC>
+__device__ __forceinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
+  int n = 0, b = ctl->b;
+  long long off = ctl->off, pos = ctl->pos;
+  const int R = ctl->size;
+#pragma unroll 1
+  while (pos < ctl->end && n < kTreeSegs) {
+    const TreeSeq s = tree_seq(a, b);
+    const TreeSpan p = tree_span(a, s);
+    const long long all = tree_places<IC>(a, p, R);
+    if (off >= all) {
+      ++b;
+      off = 0;
+      continue;
+    }
+    const int each = p.n + IC, groups = (p.blocks + R - 1) / R;
+    const int item = (int)(off / each), in = (int)(off - (long long)item * each);
+    const long long at = pos - in;                // the item's first place
+    const int g = item / groups, rb = (item - g * groups) * R + ctl->member;
+    const long long x0 = ctl->begin - at - IC, x1 = ctl->end - at - IC;
+    const int u0 = x0 > 0 ? (int)x0 : 0, u1 = x1 < p.n ? (int)x1 : p.n;
+    if (u0 < u1 && rb < p.blocks) {
+      TreeSeg &q = segs[n++];
+      q.b = b;
+      q.g = g;
+      q.rb = rb;
+      q.u0 = u0;
+      q.u1 = u1;
+      q.nsu = p.nsu;
+      q.first = p.first;
+      q.lo = p.lo;
+      q.len = s.len;
+      q.pos0 = s.len - s.nodes;
+      q.tok0 = s.tok0;
+      q.nodes = s.nodes;
+      q.slot = u0 == 0 && u1 == p.n ? -1 : u0 > 0 ? 0 : 1;
+      q.parts = (int)((at + IC + p.n - 1) / ctl->share - (at + IC) / ctl->share) + 1;
+    }
+    pos += each - in;
+    off += each - in;
+  }
+  ctl->nseg = n;
+  ctl->more = pos < ctl->end;
+  ctl->b = b;
+  ctl->off = off;
+  ctl->pos = pos;
+}
+
+// This CTA's team and range, and its first segments.  All threads.
+template <int IC, int NW>
+__device__ __forceinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
+  constexpr int NT = 32 * NW;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.B + NT - 1) / NT;
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  long long sum[kTreeMaxTeam] = {};
+  for (int b = b0; b < b1; ++b) {
+    const TreeSpan p = tree_span(a, tree_seq(a, b));
+#pragma unroll
+    for (int R = 1; R <= kTreeMaxTeam; ++R) sum[R - 1] += tree_places<IC>(a, p, R);
+  }
+  long long incl[kTreeMaxTeam];
+#pragma unroll
+  for (int k = 0; k < kTreeMaxTeam; ++k) {
+    incl[k] = sum[k];
+    if (a.B > 32 || warp == 0) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl[k], o);
+        if (lane >= o) incl[k] += y;
+      }
+    }
+    if (lane == 31) ctl->part[warp][k] = incl[k];
+  }
+  if (tid == 0) {
+    ctl->nseg = ctl->more = ctl->zeroed = 0;
+    ctl->bad = 0;
+  }
+  __syncthreads();
+  long long total[kTreeMaxTeam] = {}, before[kTreeMaxTeam] = {};
+  for (int w = 0; w < NW; ++w) {
+#pragma unroll
+    for (int k = 0; k < kTreeMaxTeam; ++k) {
+      if (w == warp) before[k] = total[k];
+      total[k] += ctl->part[w][k];
+    }
+  }
+  // The team: a row block more a team saves reading K and V again from HBM, but CTAs whose
+  // sequence has fewer blocks idle.  Compared: the tiles a CTA runs, times what a tile costs that
+  // is read for one row block alone (3) or for several (2; the MMAs bound it then).
+  int R = 1;
+  long long best = total[0] / gridDim.x * 3;
+#pragma unroll
+  for (int k = 1; k < kTreeMaxTeam; ++k) {
+    const long long cost = total[k] / max((int)gridDim.x / (k + 1), 1) * 2;
+    if (total[k] < total[0] && (int)gridDim.x >= k + 1 && cost < best) {
+      best = cost;
+      R = k + 1;
+    }
+  }
+  long long W = 0, start = 0, mine = 0;
+#pragma unroll
+  for (int k = 0; k < kTreeMaxTeam; ++k) {
+    if (k == R - 1) {
+      W = total[k];
+      mine = sum[k];
+      start = before[k] + incl[k] - sum[k];
+    }
+  }
+  const int teams = (int)gridDim.x / R;
+  const int team = (int)blockIdx.x / R;
+  long long share = (W + teams - 1) / teams;
+  share = max(share, (long long)a.min_tiles + IC);
+  const long long begin = team < teams ? min((long long)team * share, W) : W, end = min(begin + share, W);
+  if (begin < end && start <= begin && begin < start + mine) {      // one thread
+    ctl->size = R;
+    ctl->member = (int)blockIdx.x % R;
+    ctl->share = share;
+    ctl->begin = begin;
+    ctl->end = end;
+    int b = b0;
+    long long off = begin - start;
+    for (; b < b1; ++b) {
+      const long long c = tree_places<IC>(a, tree_span(a, tree_seq(a, b)), R);
+      if (off < c) break;
+      off -= c;
+    }
+    ctl->b = b;
+    ctl->off = off;
+    ctl->pos = begin;
+    tree_walk<IC>(a, segs, ctl);
+  }
+  __syncthreads();
+}
+
+// key base of tile u of a segment's item
+__device__ __forceinline__ int tree_base(const TreeSeg &s, int u) { return (u < s.nsu ? u : u - s.nsu + s.first) * kTreeKeys; }
+
+// The stage of a segment's K or V of its i-th tile of n, counted from the segment's first stage.
+__device__ __forceinline__ int tree_k_stage(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int tree_v_stage(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+
+// bits a .. b - 1 of a word (clamped to 0 .. 64)
+__device__ __forceinline__ unsigned long long tree_bits(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 64);
+  if (a >= b) return 0;
+  return (~0ull >> (64 - (b - a))) << a;
+}
+
+// 16-byte chunk c of row r of a stage
+__device__ __forceinline__ uint32_t tree_chunk(uint32_t stage, int r, int c) {
+  return stage + (c >> 3) * (kTreeKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+  tmem_wait_ld();
+  return __uint_as_float(r);
+}
+// O += p v for the keys of `found`, in the rows that see them; then their values are cleared.
+// The four softmax warps; fresh: O holds nothing yet.
+template <int D, bool BF>
+__device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t vst, unsigned long long found,
+                                          unsigned long long vis, float scale, float m, bool fresh) {
+#pragma unroll 1
+  for (int cc = 0; cc < D; cc += 32) {
+    uint32_t v[32];
+    if (fresh) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = 0u;
+    } else {
+      tmem_ld32(o + cc, v);
+      tmem_wait_ld();
+    }
+#pragma unroll 1
+    for (unsigned long long k = found; k; k &= k - 1) {
+      const int j = __ffsll((long long)k) - 1;
+      const float p = tree_ex2(tmem_ld1(scores + j) * scale - m);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(tree_chunk(vst, j, cc / 8 + q)) : "memory");
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float2 f = tree_unpack<BF>(w[h]);
+          float x = __uint_as_float(v[8 * q + 2 * h]), y = __uint_as_float(v[8 * q + 2 * h + 1]);
+          if (vis >> j & 1) {
+            x = fmaf(p, f.x, x);
+            y = fmaf(p, f.y, y);
+          }
+          v[8 * q + 2 * h] = __float_as_uint(x);
+          v[8 * q + 2 * h + 1] = __float_as_uint(y);
+        }
+      }
+    }
+    tmem_st32(o + cc, v);
+  }
+  tmem_wait_st();
+  named_bar_sync(1, 128);                         // everyone has read the values
+  for (unsigned long long k = found; k; k &= k - 1) {
+    const int j = __ffsll((long long)k) - 1;
+    if ((int)threadIdx.x < D / 8) {
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tree_chunk(vst, j, (int)threadIdx.x)), "r"(0) : "memory");
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// ---------------------------------------------------------------- the kernel --
+template <int D, int KV>
+__global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::kCtas) attn_tree_kernel(const __grid_constant__ TreeArgs a) {
+  using Sh = TreeShape<D, KV>;
+  constexpr bool kI8 = Sh::kI8, kBf = KV == kPagedBf16;
+  constexpr int F = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw0 = smem_u32(smem_raw);
+  const uint32_t sbase = (raw0 + 1023u) & ~1023u;
+  uint8_t *gbase = smem_raw + (sbase - raw0);
+  const uint32_t q_s = sbase, st_s = q_s + Sh::kQ, cd_s = st_s + F * Sh::kStage;
+  constexpr int kAt = Sh::kQ + F * Sh::kStage + Sh::kRaws * Sh::kRaw;
+  float *ksc = reinterpret_cast<float *>(gbase + kAt);                       // int8: [slots][64] K scales, then V scales
+  float *vsc = ksc + Sh::kScaleSlots * kTreeKeys;
+  const uint32_t bars = sbase + kAt + Sh::kScaleBytes;
+  short *par = reinterpret_cast<short *>(gbase + kAt + Sh::kScaleBytes + 512);   // parents of the segment's nodes (256)
+  TreeSeg *segs = reinterpret_cast<TreeSeg *>(gbase + kAt + Sh::kScaleBytes + 1024);
+  TreeCtl *ctl = reinterpret_cast<TreeCtl *>(reinterpret_cast<uint8_t *>(segs) + kTreeSegs * sizeof(TreeSeg));
+  volatile WaitBlock *wctl = reinterpret_cast<volatile WaitBlock *>(ctl + 1);
+  volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(const_cast<WaitBlock *>(wctl) + 1);
+  // barriers: full[F], empty[F], raw_full[], raw_empty[], then
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (8 + s); };
+  auto raw_full = [&](int s) { return bars + 8u * (16 + s); };
+  auto raw_empty = [&](int s) { return bars + 8u * (24 + s); };
+  auto s_full = [&](int b) { return bars + 8u * (32 + b); };
+  auto p_full = [&](int b) { return bars + 8u * (34 + b); };
+  const uint32_t q_full = bars + 8 * 36, q_empty = bars + 8 * 37, o_step = bars + 8 * 38, o_done = bars + 8 * 39, o_free = bars + 8 * 40,
+                 drain = bars + 8 * 41;
+  auto pwait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, wctl, a.wait_ns == 0); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F; ++s) {
+      mbar_init(full(s), kI8 ? 32 * Sh::kWideners : 32 * Sh::kLoaders);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < Sh::kRaws; ++s) {
+      mbar_init(raw_full(s), 32 * Sh::kLoaders);
+      mbar_init(raw_empty(s), Sh::kWideners);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(p_full(b), 4);
+    }
+    mbar_init(q_full, 32 * Sh::kLoaders);
+    mbar_init(q_empty, 1);
+    mbar_init(o_step, 1);
+    mbar_init(o_done, 1);
+    mbar_init(o_free, 4);
+    mbar_init(drain, 1);
+    wait_block_init(wctl, a.wait_ns, a.err);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(const_cast<uint32_t *>(tslot)), Sh::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  griddep_wait();
+  griddep_launch_dependents();
+  tree_schedule<Sh::kItemCost, Sh::kWarps>(a, segs, ctl);
+
+  // the roles' counters run over all segments of all lists
+  int stage = 0;                                  // stages filled / emptied
+  int tiles = 0;                                  // tiles
+  int nsegs = 0;                                  // segments
+  bool ok = true;
+  TreeDesc desc{};                                // the item whose first part this CTA leaves
+
+  for (;;) {
+    const int nseg = ctl->nseg;
+    if (warp >= Sh::kLoad0 && warp < Sh::kWiden0) {
+      // ------------------------------------------------------------ loading --
+      constexpr int RPW = kTreeKeys / Sh::kLoaders;               // rows of a tile a warp: 16 or 32
+      constexpr int RB = kI8 ? D : 2 * D;                         // bytes of a row
+      constexpr int CH = RB / 16;                                 // 16-byte chunks of it
+      constexpr int RPI = 32 / CH;                                // rows a step of the warp (CH <= 32)
+      const int lw = warp - Sh::kLoad0;
+      const int c = lane % CH, ro = lane / CH;
+      constexpr int kRing = kI8 ? Sh::kRaws : F;
+      for (int si = 0; si < nseg && ok; ++si) {
+        const TreeSeg &s = segs[si];
+        const int n = s.u1 - s.u0;
+        // lane l < RPW: where row RPW lw + l of a tile starts (elements), -1 where it is not read
+        auto page_of = [&](int i) {
+          const int j = tree_base(s, s.u0 + i) + RPW * lw + lane % RPW;
+          const bool see = j < s.len && (j >= s.lo || j < a.sinks);
+          const int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page;
+          return see ? __ldg(a.table + (long long)s.b * a.max_pages + pi) : -2;
+        };
+        auto start_of = [&](int i, int pid, long long &scale_at) -> long long {
+          const int j = tree_base(s, s.u0 + i) + RPW * lw + lane % RPW;
+          const int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page;
+          const int r = j - pi * a.page;
+          if ((unsigned)pid >= (unsigned)a.npages) {
+            if (pid != -2) atomicCAS(a.err, 0, -9);
+            scale_at = -1;
+            return -1;
+          }
+          scale_at = ((long long)pid * a.Hkv + s.g) * a.page + r;
+          return pid * a.page_stride + s.g * a.head_stride + r * a.tok_stride;
+        };
+        auto copy_rows = [&](const uint8_t *base, long long start) {
+          const int slot = stage % kRing;
+          if (stage >= kRing && ok) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((stage / kRing - 1) & 1)));
+          if (!ok) return;
+          const uint32_t dst = kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage;
+#pragma unroll
+          for (int k = 0; k < RPW / RPI; ++k) {
+            const int r = k * RPI + ro, row = RPW * lw + r;
+            const long long at = __shfl_sync(0xffffffffu, start, r);
+            const uint8_t *src = base + (at < 0 ? 0 : at * (kI8 ? 1 : 2) + 16 * c);
+            const uint32_t to = kI8 ? dst + row * RB + 16 * c : dst + (c >> 3) * (kTreeKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            cp_async16(to, src, at < 0 ? 0u : 16u);
+          }
+        };
+        auto done = [&]() {
+          const int slot = stage % kRing;
+          if (ok) cp_async_arrive(kI8 ? raw_full(slot) : full(slot));
+          ++stage;
+        };
+        int pid = page_of(0);
+        long long at_v = 0;
+        for (int i = 0; i <= n && ok; ++i) {
+          long long at_k = -1, sc_k = -1;
+          if (i < n) {
+            at_k = start_of(i, pid, sc_k);
+            if (i + 1 < n) pid = page_of(i + 1);
+            copy_rows(a.k, at_k);
+            if constexpr (kI8) {                  // the tile's scales come with its K
+              if (ok && lane < RPW) {
+                const int slot = (tiles + i) % Sh::kScaleSlots, row = RPW * lw + lane;
+                cp_async4_zfill(smem_u32(ksc + slot * kTreeKeys + row), a.ks + (sc_k < 0 ? 0 : sc_k), sc_k < 0 ? 0u : 4u);
+                cp_async4_zfill(smem_u32(vsc + slot * kTreeKeys + row), a.vs + (sc_k < 0 ? 0 : sc_k), sc_k < 0 ? 0u : 4u);
+              }
+            }
+            done();
+          }
+          if (i == 0 && ok) {
+            // Q: row r is column rb * 128 + r of the KV head: node column / G, head column % G
+            if (nsegs + si > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((nsegs + si - 1) & 1)));
+            if (ok) {
+              constexpr int QC = D / 8;           // chunks of a row
+              const int rows = s.nodes * a.G - s.rb * kTreeRows;
+#pragma unroll 4
+              for (int x = (warp - Sh::kLoad0) * 32 + lane; x < kTreeRows * QC; x += 32 * Sh::kLoaders) {
+                const int r = x / QC, cc = x % QC;
+                const int col = s.rb * kTreeRows + r, i2 = col / a.G, h = col - i2 * a.G;
+                const uint16_t *src = r < rows ? a.q + (long long)(s.tok0 + i2) * a.q_tok + (long long)(s.g * a.G + h) * a.q_head + 8 * cc : a.q;
+                cp_async16(q_s + (cc >> 3) * (kTreeRows * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4), src, r < rows ? 16u : 0u);
+              }
+              cp_async_arrive(q_full);
+            }
+          }
+          if (i > 0 && ok) {
+            copy_rows(a.v, at_v);
+            done();
+          }
+          at_v = at_k;
+        }
+        tiles += n;
+      }
+    } else if (kI8 && warp >= Sh::kWiden0) {
+      // ----------------------------------------------------------- widening --
+      const int t = threadIdx.x - 32 * Sh::kWiden0;
+      for (int si = 0; si < nseg && ok; ++si) {
+        const int n = segs[si].u1 - segs[si].u0;
+        for (int i = 0; i < 2 * n && ok; ++i, ++stage) {
+          const int rs = stage % (kI8 ? Sh::kRaws : 1), fs = stage % F;
+          ok = pwait(raw_full(rs), (uint32_t)((stage / (kI8 ? Sh::kRaws : 1)) & 1));
+          if (ok && stage >= F) ok = pwait(empty(fs), (uint32_t)((stage / F - 1) & 1));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          constexpr int CH = D / 16;
+          constexpr int PER = kTreeKeys * CH / 128;
+          uint4 x[PER];
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const uint32_t at = cd_s + rs * Sh::kRaw + 16 * (k * 128 + t);
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(at) : "memory");
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_empty(rs));
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int id = k * 128 + t, row = id / CH, cc = id % CH;
+            const uint32_t w[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u, x[k].w ^ 0x80808080u};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c8 = 2 * cc + h;
+              const uint32_t to = st_s + fs * Sh::kStage + (c8 >> 3) * (kTreeKeys * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(tree_widen<0x4140>(w[2 * h])),
+                           "r"(tree_widen<0x4342>(w[2 * h])), "r"(tree_widen<0x4140>(w[2 * h + 1])), "r"(tree_widen<0x4342>(w[2 * h + 1]))
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(full(fs));
+        }
+      }
+    } else if (warp == Sh::kMmaWarp) {
+      // ---------------------------------------------------------------- MMA --
+      // The whole warp runs the loop and the leader lane issues: see mma_f16_ts_w.
+      const uint32_t leader = elect_leader();
+      auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, pwait(bar, parity)); };
+      constexpr uint32_t kIdS = tree_idesc(kBf, false, kTreeRows, kTreeKeys), kIdO = tree_idesc(kBf, true, kTreeRows, D);
+      for (int si = 0; si < nseg && ok; ++si) {
+        const int n = segs[si].u1 - segs[si].u0;
+        const int seg = nsegs + si;
+        if (!wwait(q_full, (uint32_t)(seg & 1))) { ok = false; break; }
+        for (int i = 0; i <= n; ++i) {
+          if (i < n) {
+            const int st = stage + tree_k_stage(i), slot = st % F, b = (tiles + i) & 1;
+            if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
+            fence_proxy_async_smem();             // the copies' writes, seen through the barrier
+            tc_fence_after();
+            const uint32_t ks = st_s + slot * Sh::kStage;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_f16_ss_w(leader, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys), smem_desc_sw128(q_s + (kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32),
+                           smem_desc_sw128(ks + (kk >> 2) * (kTreeKeys * 128) + (kk & 3) * 32), kIdS, kk > 0 ? 1u : 0u);
+            mma_commit_w(leader, s_full(b));
+            mma_commit_w(leader, empty(slot));
+            if (i == n - 1) mma_commit_w(leader, q_empty);
+          }
+          if (i > 0) {
+            const int j = i - 1, st = stage + tree_v_stage(j, n), slot = st % F, gt = tiles + j, b = gt & 1;
+            if (!wwait(p_full(b), (uint32_t)((gt >> 1) & 1))) { ok = false; break; }
+            if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint32_t vs = st_s + slot * Sh::kStage;
+            // (O of the segment before has been read; a tile with values that are not finite starts it at 0)
+            if (j == 0 && seg > 0 && !wwait(o_free, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
+            const uint32_t more = j > 0 || *static_cast<volatile int *>(&ctl->zeroed) == seg + 1;
+#pragma unroll
+            for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+                mma_f16_ts_w(leader, tmem, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys + (kk >> 1) * 32 + term * 16 + (kk & 1) * 8),
+                             smem_desc_sw128_mn(vs + kk * 2048), kIdO, (kk > 0 || term > 0) ? 1u : more);
+            }
+            mma_commit_w(leader, empty(slot));
+            mma_commit_w(leader, o_step);
+            if (j == n - 1) mma_commit_w(leader, o_done);
+          }
+        }
+        if (!ok) break;
+        stage += 2 * n;
+        tiles += n;
+      }
+    } else if (warp < 4) {
+      // ------------------------------------------------------------ softmax --
+      const int row = threadIdx.x;                // of the 128 (TMEM lane)
+      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+      constexpr float kHead = kBf ? 0.0f : 7.0f, kPass = kBf ? 8.0f : 15.0f;
+      bool aborted = !ok;
+      for (int si = 0; si < nseg && !aborted; ++si) {
+        const TreeSeg s = segs[si];
+        const int n = s.u1 - s.u0, seg = nsegs + si;
+        const int col = s.rb * kTreeRows + row, node = col / a.G, head = s.g * a.G + col - node * a.G;
+        const bool real = node < s.nodes;
+        // the row's ancestors, as bits over the nodes; its depth; the first key its window holds
+        unsigned anc[8] = {};
+        int lo = s.lo, depth = 0;
+        const bool tree = tree_base(s, s.u1 - 1) + kTreeKeys > s.pos0 || a.window > 0;       // (segments that never meet the tree need no mask)
+        named_bar_sync(1, 128);                   // the last segment's parents have been read
+        if (tree && s.nodes <= 256) {
+          for (int i = row; i < s.nodes; i += 128) {
+            int p = __ldg(a.parents + s.tok0 + i);
+            if (p < -1 || p >= i) {
+              atomicCAS(a.err, 0, -9);
+              p = -1;
+            }
+            par[i] = (short)p;
+          }
+          named_bar_sync(1, 128);
+          if (real && s.len > 0) {
+            if (a.window > 0) {
+              for (int i = par[node]; i >= 0; i = par[i]) ++depth;
+              lo = max(s.pos0 + depth - a.window + 1, 0);
+            }
+            int e = 0;
+            for (int i = node; i >= 0; i = par[i], ++e) {
+              if (a.window == 0 || e < a.window || s.pos0 + depth - e < a.sinks) {
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                  if (i >> 5 == w) anc[w] |= 1u << (i & 31);
+              }
+            }
+          }
+        }
+        // the keys before this one are seen by every row, from `whole` on (without the sinks)
+        const int whole = a.window > 0 ? s.pos0 + s.nodes - a.window : 0;
+        float m_ref = kTreeNoScore, l = 0.0f;
+        float mp = kTreeNoScore;                  // int8: the reference of the weights with their values' scales
+        for (int i = 0; i < n; ++i) {
+          const int gt = tiles + i, b = gt & 1;
+          const int base = tree_base(s, s.u0 + i);
+          const bool masked = base + kTreeKeys > s.pos0 || (base < whole && base + kTreeKeys > a.sinks);
+          unsigned long long vis = ~0ull;
+          if (masked) {
+            vis = tree_bits(lo - base, s.pos0 - base) | tree_bits(0, min(a.sinks, s.pos0) - base);
+            const int at = base - s.pos0;         // the tile's first key among the nodes
+            if (at > -kTreeKeys && at < 256) {
+              unsigned long long t = 0;
+#pragma unroll
+              for (int w = 0; w < 8; ++w) {
+                const int sh = 32 * w - at;       // where word w starts in the tile
+                if (sh > -32 && sh < 64) t |= sh >= 0 ? (unsigned long long)anc[w] << sh : (unsigned long long)anc[w] >> -sh;
+              }
+              if (s.len - base < 64) t &= tree_bits(0, s.len - base);
+              vis |= t;
+            }
+            if (!real) vis = 0;
+          }
+          const bool got = pwait(s_full(b), (uint32_t)((gt >> 1) & 1));
+          if (named_bar_or(1, 128, !got || wctl->abort)) { aborted = true; break; }
+          tc_fence_after();
+          const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys);
+          const float *kss = ksc + (gt % Sh::kScaleSlots) * kTreeKeys, *vss = vsc + (gt % Sh::kScaleSlots) * kTreeKeys;
+          float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t v[32];
+            tmem_ld32(sadr + 32u * hh, v);
+            tmem_wait_ld();
+            const uint32_t vm = (uint32_t)(vis >> (32 * hh));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float t = __uint_as_float(v[c]) * a.scale_log2;
+              if constexpr (kI8) t *= kss[32 * hh + c];
+              if (masked && !(vm >> c & 1)) t = -INFINITY;
+              mx = fmaxf(mx, t);
+              if constexpr (kI8) my = fmaxf(my, t + tree_lg2(fabsf(vss[32 * hh + c])));
+            }
+          }
+          // The references move only when a score passes them by 2^kPass; then O and l are
+          // rescaled, once the previous P V is done.
+          float fl = 1.0f, fo = 1.0f;
+          if (kI8) {
+            if (mx > m_ref + 8.0f) {
+              fl = tree_ex2(m_ref - mx);
+              m_ref = mx;
+            }
+            if (my > mp + kPass) {
+              fo = tree_ex2(mp - (my - kHead));
+              mp = my - kHead;
+            }
+          } else if (mx > m_ref + kPass) {
+            fl = fo = tree_ex2(m_ref - (mx - kHead));
+            m_ref = mx - kHead;
+          }
+          l *= fl;
+          const bool resc = fo != 1.0f && i > 0;
+          if (__any_sync(0xffffffffu, resc)) {
+            if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) {
+              aborted = true;
+            } else {
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + lane_base + cc, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * fo);
+                tmem_st32(tmem + lane_base + cc, v);
+              }
+              tmem_wait_st();
+            }
+          }
+          // the weights, half a tile at a time: 16 columns of rounded pairs, 16 of what they leave
+          const float fw = kI8 ? (mp == kTreeNoScore ? 0.0f : tree_ex2(m_ref - mp)) : 1.0f;
+          if constexpr (!kI8) {
+            // A value that is not finite would reach the rows that do not see its key (0 times it is NaN),
+            // so tiles seen partly are searched for such keys.  They are added here, to the rows
+            // that see them, and cleared for the MMA.
+            if (masked && !aborted) {
+              const int st = stage + tree_v_stage(i, n);
+              const uint32_t vst = st_s + (st % F) * Sh::kStage;
+              if (!pwait(full(st % F), (uint32_t)((st / F) & 1))) aborted = true;
+              if (row == 0) ctl->bad = 0;
+              if (named_bar_or(1, 128, aborted)) aborted = true;
+              if (!aborted) {
+                constexpr uint32_t e = kBf ? 0x7f807f80u : 0x7c007c00u;
+                bool bad = false;
+#pragma unroll 4
+                for (int c = 0; c < D / 16; ++c) {
+                  const uint32_t at = tree_chunk(vst, row >> 1, (row & 1) * (D / 16) + c);
+                  uint4 x;
+                  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+                  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) bad |= (w[k] & (e & 0xffffu)) == (e & 0xffffu) || (w[k] & (e & 0xffff0000u)) == (e & 0xffff0000u);
+                }
+                if (bad) atomicOr(&ctl->bad, 1ull << (row >> 1));
+                named_bar_sync(1, 128);
+                const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad);
+                if (found) {
+                  aborted = !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
+                  if (named_bar_or(1, 128, aborted)) aborted = true;
+                  if (!aborted) {
+                    tc_fence_after();
+                    tree_add_bad<D, kBf>(tmem + lane_base, sadr, vst, found, vis, a.scale_log2, m_ref, i == 0);
+                    if (row == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
+                  }
+                }
+              }
+            }
+          }
+          if (!aborted) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t v[32], hi[16], lw[16];
+              tmem_ld32(sadr + 32u * hh, v);
+              tmem_wait_ld();
+              const uint32_t vm = (uint32_t)(vis >> (32 * hh));
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float t = __uint_as_float(v[c + e]) * a.scale_log2;
+                  if constexpr (kI8) t *= kss[32 * hh + c + e];
+                  const bool hide = masked && !(vm >> (c + e) & 1);
+                  const float p = hide ? 0.0f : tree_ex2(t - m_ref);
+                  l += p;
+                  w[e] = kI8 ? (hide ? 0.0f : p * fw * vss[32 * hh + c + e]) : p;
+                }
+                hi[c / 2] = tree_pack<kBf>(w[0], w[1]);
+                const float2 f = tree_unpack<kBf>(hi[c / 2]);
+                lw[c / 2] = tree_pack<kBf>(w[0] - f.x, w[1] - f.y);
+              }
+              tmem_st16(sadr + 32u * hh, hi);
+              tmem_st16(sadr + 32u * hh + 16u, lw);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && !aborted) mbar_arrive(p_full(b));
+          if (__any_sync(0xffffffffu, aborted)) {
+            aborted = true;
+            if (lane == 0) wctl->abort = 1;
+          }
+        }
+        // ---- the rows, or their parts
+        const bool got = !aborted && pwait(o_done, (uint32_t)(seg & 1));
+        if (named_bar_or(1, 128, !got || wctl->abort)) { aborted = true; break; }
+        tc_fence_after();
+        if (s.slot < 0) {
+          const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
+          const float fin = kI8 ? inv * tree_ex2(mp - m_ref) : inv;
+          const long long at = (long long)(s.tok0 + node) * a.Hq + head;
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + cc, v);
+            tmem_wait_ld();
+            if (real) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t o[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const float x = l == 0.0f ? 0.0f : __uint_as_float(v[16 * h + 2 * c]) * fin, y = l == 0.0f ? 0.0f : __uint_as_float(v[16 * h + 2 * c + 1]) * fin;
+                  o[c] = tree_pack<kBf>(x, y);
+                }
+                uint4 *to = reinterpret_cast<uint4 *>(a.out + at * D + cc + 16 * h);
+                to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+            }
+          }
+          if (real && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.693147180559945309f;
+        } else {
+          const int ps = 2 * (int)blockIdx.x + s.slot;
+          float *part = a.part + (size_t)ps * tree_part_floats(D) + (size_t)row * D;
+          const float fin = kI8 ? tree_ex2(mp - m_ref) : 1.0f;
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + cc, v);
+            tmem_wait_ld();
+            if (real) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                uint32_t o[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o[c] = l == 0.0f ? 0u : kI8 ? __float_as_uint(__uint_as_float(v[8 * h + c]) * fin) : v[8 * h + c];
+                st_global_v8(part + cc + 8 * h, o);
+              }
+            }
+          }
+          float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)ps * tree_part_floats(D) + (size_t)kTreeRows * D) + row;
+          if (real) *ml = make_float2(m_ref, l);
+          if (s.slot == 1) {
+            desc.tok0 = s.tok0;
+            desc.col0 = s.rb * kTreeRows;
+            desc.cols = min(s.nodes * a.G - s.rb * kTreeRows, kTreeRows);
+            desc.g = s.g;
+            desc.parts = s.parts;
+            desc.step = ctl->size;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+        tiles += n;
+        stage += 2 * n;
+      }
+      ok = !aborted;
+    }
+    nsegs += nseg;
+    if (!ctl->more) break;
+    __syncthreads();                              // everyone has done the list
+    if (threadIdx.x == 0) tree_walk<Sh::kItemCost>(a, segs, ctl);
+    __syncthreads();
+    if (ctl->nseg == 0 && !ctl->more) break;
+  }
+
+  // what was started ends before the CTA does
+  if (warp >= Sh::kLoad0 && warp < Sh::kWiden0) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (warp == Sh::kMmaWarp) {
+    const uint32_t leader = elect_leader();
+    mma_commit_w(leader, drain);
+    mbar_drain(drain, 0u, wctl);
+  }
+  if (threadIdx.x == 0) a.desc[blockIdx.x] = desc;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Sh::kTmem);
+  }
+}
+
+// ------------------------------------------------------------------ the join --
+// A CTA 32 rows of the item whose first part CTA blockIdx.x of attn_tree_kernel left: its parts are
+// that CTA's second slot and the first slots of the same member of the next teams.
+constexpr int kJoinWarps = 8;
+template <int D, bool BF>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  const TreeDesc d = a.desc[blockIdx.x];
+  const size_t size = tree_part_floats(D);
+  auto part = [&](int k) { return a.part + (size_t)(k == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + k * d.step)) * size; };
+  for (int r = blockIdx.y * 32 + warp; r < min(d.cols, (int)blockIdx.y * 32 + 32); r += kJoinWarps) {
+    float m = kTreeNoScore;
+    for (int k = lane; k < d.parts; k += 32) m = fmaxf(m, reinterpret_cast<const float2 *>(part(k) + (size_t)kTreeRows * D)[r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f, acc[PER] = {};
+    for (int k0 = 0; k0 < d.parts; k0 += 32) {
+      float w = 0.0f, lk = 0.0f;
+      if (k0 + lane < d.parts) {
+        const float2 ml = reinterpret_cast<const float2 *>(part(k0 + lane) + (size_t)kTreeRows * D)[r];
+        w = tree_ex2(ml.x - m);
+        lk = ml.y * w;
+      }
+      const int n = min(d.parts - k0, 32);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float *p = part(k0 + k) + (size_t)r * D + lane * PER;
+        const float f = __shfl_sync(0xffffffffu, w, k);
+        l += __shfl_sync(0xffffffffu, lk, k);
+        float x[PER];
+        if constexpr (PER == 2) {
+          const float2 v = *reinterpret_cast<const float2 *>(p);
+          x[0] = v.x;
+          x[1] = v.y;
+        } else {
+#pragma unroll
+          for (int q = 0; q < PER / 4; ++q) {
+            const float4 v = reinterpret_cast<const float4 *>(p)[q];
+            x[4 * q] = v.x;
+            x[4 * q + 1] = v.y;
+            x[4 * q + 2] = v.z;
+            x[4 * q + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < PER; ++c) acc[c] = fmaf(f, x[c], acc[c]);
+      }
+    }
+    const int col = d.col0 + r, node = col / a.G, head = d.g * a.G + col - node * a.G;
+    const long long at = (long long)(d.tok0 + node) * a.Hq + head;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t o[PER / 2];
+#pragma unroll
+    for (int c = 0; c < PER / 2; ++c) o[c] = tree_pack<BF>(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    uint32_t *to = reinterpret_cast<uint32_t *>(a.out + at * D) + lane * (PER / 2);
+    if constexpr (PER == 8) *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+    else if constexpr (PER == 4) *reinterpret_cast<uint2 *>(to) = make_uint2(o[0], o[1]);
+    else *to = o[0];
+    if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+  }
+}
+
+template <int D, int KV>
+cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t st) {
+  using Sh = TreeShape<D, KV>;
+  const void *f = reinterpret_cast<const void *>(attn_tree_kernel<D, KV>);
+  cudaError_t e = ensure_smem_attr(f, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(f, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, a);
+  count_launch();
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(reinterpret_cast<const void *>(attn_tree_join_kernel<D, KV == kPagedBf16>), dim3(grid, kTreeRows / 32), dim3(32 * kJoinWarps),
+                 0, st, a);
+  count_launch();
+  return e;
+}
+template <int KV>
+cudaError_t launch_tree_kv(const TreeArgs &a, int d, int grid, cudaStream_t st) {
+  return d == 64 ? launch_tree<64, KV>(a, grid, st) : d == 128 ? launch_tree<128, KV>(a, grid, st) : launch_tree<256, KV>(a, grid, st);
+}
+
+}  // namespace qw

@@ -261,6 +261,8 @@ constexpr size_t kPagedCounterBytes = 3 * kPagedMaxCtas * 4;   // three counters
 size_t paged_ws(int d, int cols, int sms) {
   return kPagedCounterBytes + (size_t)2 * paged_ctas(d, cols) * sms * cols * (d + 2) * 4;
 }
+constexpr size_t kTreeDescBytes = kPagedMaxCtas * sizeof(TreeDesc);
+size_t tree_ws(int d, int sms) { return kTreeDescBytes + (size_t)2 * tree_ctas(d) * sms * tree_part_floats(d) * 4; }
 int check_heads(int d, int Hq, int Hkv, int max_new) {
   if (Hq < 1 || Hkv < 1 || max_new < 1) return bad(QW_ERR_INVALID_ARG, "Hq, Hkv and max_new must be positive");
   if (d != 64 && d != 128 && d != 256)
@@ -443,6 +445,79 @@ int attn_paged(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const uint16_t *q
                   : c->dtype == QW_KV_BF16 ? launch_attn_paged_bf16(a, c->d, cols, sms, st)
                                            : launch_attn_paged_i8(a, c->d, cols, sms, st);
   if (e != cudaSuccess) return bad(QW_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
+  return QW_OK;
+}
+
+size_t attn_tree_workspace_bytes(int d, int Hq, int Hkv) {
+  int sms = 0;
+  if (check_heads(d, Hq, Hkv, 1) || device_info(&sms, nullptr)) return 0;
+  return tree_ws(d, sms);
+}
+
+int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *parents, const uint16_t *q, int T, int Hq,
+              long long q_token_stride, long long q_head_stride, int max_nodes, int window, int sinks, float scale,
+              uint16_t *out, float *lse, void *ws, size_t ws_bytes, qw_stream_t stream) {
+  int rc = check_cache(c);
+  if (rc) return rc;
+  if ((rc = check_batch(b, c->page, T))) return rc;
+  if ((rc = check_heads(c->d, Hq, c->Hkv, max_nodes))) return rc;
+  if (max_nodes > 256) return bad(QW_ERR_UNSUPPORTED_SHAPE, "max_nodes %d: at most 256", max_nodes);
+  if (window < 0 || sinks < 0) return bad(QW_ERR_INVALID_ARG, "negative window or sinks");
+  if (!isfinite(scale)) return bad(QW_ERR_INVALID_ARG, "scale is not finite");
+  if ((long long)T * Hq > 0x7fffffffll) return bad(QW_ERR_UNSUPPORTED_SHAPE, "T * Hq above 2^31 - 1");
+  if (T == 0 || b->B == 0) return QW_OK;
+  if (!parents || !q || !out) return bad(QW_ERR_INVALID_ARG, "null tensor pointer");
+  if (!at(q, 16) || !at(out, 16) || q_token_stride % 8 || q_head_stride % 8 || !at(parents, 4) || (lse && !at(lse, 4)) ||
+      (ws && !at(ws, 256)))
+    return bad(QW_ERR_ALIGNMENT, "q rows and out must start on 16-byte boundaries, the workspace on a 256-byte one");
+  TreeArgs a{};
+  int sms = 0;
+  if ((rc = device_info(&sms, &a.err))) return rc;
+  const int grid = tree_ctas(c->d) * sms;
+  if (grid > kPagedMaxCtas) return bad(QW_ERR_ARCH, "more than %d SMs", kPagedMaxCtas / tree_ctas(c->d));
+  const size_t need = tree_ws(c->d, sms);
+  if (!ws || ws_bytes < need)
+    return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.k = static_cast<const uint8_t *>(c->k);
+  a.v = static_cast<const uint8_t *>(c->v);
+  a.ks = c->k_scale;
+  a.vs = c->v_scale;
+  a.table = b->page_table;
+  a.lens = b->seq_lens;
+  a.cu = b->cu_tokens;
+  a.parents = parents;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.page_stride = c->page_stride;
+  a.head_stride = c->head_stride;
+  a.tok_stride = c->token_stride;
+  a.B = b->B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = c->Hkv;
+  a.G = Hq / c->Hkv;
+  a.page = c->page;
+  a.npages = c->num_pages;
+  a.max_pages = b->max_pages;
+  a.cap = b->max_pages * c->page;
+  a.window = window < a.cap ? window : 0;
+  a.sinks = a.window > 0 ? sinks : 0;
+  a.page_shift = (c->page & (c->page - 1)) == 0 ? 0 : -1;
+  while (a.page_shift >= 0 && c->page >> a.page_shift > 1) ++a.page_shift;
+  a.max_nodes = max_nodes;
+  a.min_tiles = 1;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.desc = static_cast<TreeDesc *>(ws);
+  a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kTreeDescBytes);
+  a.wait_ns = wait_limit_ns();
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = c->dtype == QW_KV_F16    ? launch_attn_tree_f16(a, c->d, grid, st)
+                  : c->dtype == QW_KV_BF16 ? launch_attn_tree_bf16(a, c->d, grid, st)
+                                           : launch_attn_tree_i8(a, c->d, grid, st);
+  if (e != cudaSuccess) return bad(QW_ERR_CUDA, "tree attention kernel launch: %s", cudaGetErrorString(e));
   return QW_OK;
 }
 

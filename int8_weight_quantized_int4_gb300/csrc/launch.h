@@ -31,6 +31,8 @@ struct GemmArgs {
 };
 
 void count_launch();
+// QW_OPT_WAIT_LIMIT_US in nanoseconds
+unsigned long long wait_limit_ns();
 // Record a host-side error for qw_last_error_string(); returns `code`.
 int set_last_error(int code, const char *msg);
 // Check the current device (sm_103) and return its SM count and the address of its
@@ -135,6 +137,34 @@ struct PagedArgs {
 cudaError_t launch_attn_paged_f16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
 cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
 cudaError_t launch_attn_paged_i8(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
+
+// Attention of trees over the paged cache (attn_tree*.cu)
+struct TreeDesc {               // an item that several CTAs share, left by the first of them
+  int tok0, col0, cols, g;      // its first row in q, first column, columns (0: none), KV head
+  int parts, step;              // parts; CTAs from one to the next
+};
+struct TreeArgs {
+  const uint16_t *q;            // as PagedArgs
+  uint16_t *out;
+  float *lse;
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int *table, *lens, *cu, *parents;
+  long long q_tok, q_head, page_stride, head_stride, tok_stride;
+  int B, T, Hq, Hkv, G, page, npages, max_pages, cap, window, sinks, page_shift;
+  int max_nodes, min_tiles;     // fewest tiles of keys a CTA takes
+  float scale_log2;
+  float *part;                  // [CTAs][2][128 (d + 2)] partial sums (workspace)
+  TreeDesc *desc;               // [CTAs] (workspace)
+  int *err;
+  unsigned long long wait_ns;
+};
+// CTAs an SM: TMEM holds O and two buffers of scores of two CTAs up to d = 128
+constexpr int tree_ctas(int d) { return d == 256 ? 1 : 2; }
+__host__ __device__ constexpr size_t tree_part_floats(int d) { return (size_t)128 * (d + 2); }
+cudaError_t launch_attn_tree_f16(const TreeArgs &a, int d, int grid, cudaStream_t st);
+cudaError_t launch_attn_tree_bf16(const TreeArgs &a, int d, int grid, cudaStream_t st);
+cudaError_t launch_attn_tree_i8(const TreeArgs &a, int d, int grid, cudaStream_t st);
 
 cudaError_t launch_gemm_w4a16(const GemmArgs &a, cudaStream_t st);
 // W4A8 (token scales in the epilogue): act8, int8 codes widened in the kernel (token
