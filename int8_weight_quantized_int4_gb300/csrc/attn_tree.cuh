@@ -12,8 +12,8 @@
 // 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
 // of the 128 rows a small tree fills.
 //
-// Roles of a CTA's warps: 4 of softmax (warp w reads TMEM lanes 32 w ..), 1 issuing MMAs, 4 loading (2
-// with an int8 cache) and for an int8 cache 4 that widen codes to fp16 (exact).  A ring of stages, each
+// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 2
+// loading and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  A ring of stages, each
 // 64 rows of K or V, in the order K0 K1 V0 K2 V1 .. of a segment: scores of the next tile are
 // computed while the softmax works on the last.
 //   - Rows are loaded with cp.async, 16 bytes a thread, straight to the 128-byte swizzle: pages of
@@ -35,6 +35,7 @@
 // only weights below 2^-32 of it are lost.  With the int8 cache the value's scale joins its weight.
 #pragma once
 #include <stdint.h>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "launch.h"
@@ -70,29 +71,59 @@ struct TreeCtl {
 template <int D, int KV>
 struct TreeShape {
   static constexpr bool kI8 = KV == kPagedI8;
-  static constexpr int kLoaders = kI8 ? 2 : 4;    // warps
-  static constexpr int kWideners = kI8 ? 4 : 0;
-  static constexpr int kMmaWarp = 4, kLoad0 = 5, kWiden0 = kLoad0 + kLoaders;
+  static constexpr int kLoaders = 2;              // warps
+  static constexpr int kWideners = !kI8 ? 0 : D == 256 ? 4 : 2;
+  static constexpr int kMmaWarp = 8, kLoad0 = 9, kWiden0 = kLoad0 + kLoaders;
   static constexpr int kWarps = kWiden0 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
   static constexpr int kStage = kTreeKeys * D * 2;
-  static constexpr int kStages = kI8 ? (D == 256 ? 2 : D == 128 ? 3 : 4) : D == 64 ? 8 : 4;
+  static constexpr int kStages = kI8 ? (D == 64 ? 4 : 2) : D == 64 ? 8 : 4;
   static constexpr int kRaw = kI8 ? kTreeKeys * D : 0;                // a stage of codes
   static constexpr int kRaws = !kI8 ? 0 : D == 256 ? 5 : D == 128 ? 3 : 8;
   static constexpr int kScaleSlots = D == 64 ? 16 : 8;   // tiles whose scales are kept (more than can be under way)
   static constexpr int kQ = kTreeRows * D * 2;
   static constexpr uint32_t kTmem = D == 256 ? 512 : 256;
   static constexpr uint32_t kSCol = D;            // O [0, D), then two buffers of 64 columns of S and P
-  static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 8 : 0;
-  static constexpr int kFixed = kScaleBytes + 512 /* barriers */ + 512 /* parents */ + kTreeSegs * (int)sizeof(TreeSeg) + (int)sizeof(TreeCtl) + 64;
-  static constexpr int kSmem = 1024 + kQ + kStages * kStage + kRaws * kRaw + kFixed;
-  static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024, "shared memory");
+  static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 16 : 0;
+  static constexpr int kMaskWords = 9;            // a row's ancestors (256 bits) and the first key of its window
+  // barriers, parents, masks, an exchange between the groups, the segments
+  static constexpr int kFixed = 512 + 512 + kTreeRows * kMaskWords * 4 + 2 * kTreeRows * 4 + kTreeSegs * (int)sizeof(TreeSeg) +
+                                (int)sizeof(TreeCtl) + 64;
+  static constexpr int kSmem = 1024 + kQ + kStages * kStage + kRaws * kRaw + kScaleBytes + kFixed;
+  static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages + kRaws + 4 < 2 * kScaleSlots - 2, "scales outlive their use");
   // what an item costs beside its tiles, in tiles: about the time of 192 KB
   static constexpr int kItemCost = 196608 / (2 * kStage / (kI8 ? 2 : 1));
 };
 
+// Pairs of binary32, two to an instruction.
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float tree_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -110,12 +141,10 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 __device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // 32 bytes: a whole sector from one thread
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&r)[8]) {
@@ -135,6 +164,7 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr) {
   return d;
 }
 // Instruction descriptor, kind::f16: D fp32, A and B both fp16 or both bf16, B MN-major or not.
+// (bit 13 negates A.)
 __host__ __device__ constexpr uint32_t tree_idesc(bool bf, bool b_mn, int M, int N) {
   return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
@@ -357,12 +387,13 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
   return __uint_as_float(r);
 }
 // O += p v for the keys of `found`, in the rows that see them; then their values are cleared.
-// The four softmax warps; fresh: O holds nothing yet.
+// The softmax warps, each group half of the channels; fresh: O holds nothing yet.
 template <int D, bool BF>
 __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t vst, unsigned long long found,
                                           unsigned long long vis, float scale, float m, bool fresh) {
+  const int c0 = (int)(threadIdx.x >> 7) * (D / 2);
 #pragma unroll 1
-  for (int cc = 0; cc < D; cc += 32) {
+  for (int cc = c0; cc < c0 + D / 2; cc += 32) {
     uint32_t v[32];
     if (fresh) {
 #pragma unroll
@@ -395,7 +426,7 @@ __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t 
     tmem_st32(o + cc, v);
   }
   tmem_wait_st();
-  named_bar_sync(1, 128);                         // everyone has read the values
+  named_bar_sync(1, 256);                         // everyone has read the values
   for (unsigned long long k = found; k; k &= k - 1) {
     const int j = __ffsll((long long)k) - 1;
     if ((int)threadIdx.x < D / 8) {
@@ -417,11 +448,15 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   uint8_t *gbase = smem_raw + (sbase - raw0);
   const uint32_t q_s = sbase, st_s = q_s + Sh::kQ, cd_s = st_s + F * Sh::kStage;
   constexpr int kAt = Sh::kQ + F * Sh::kStage + Sh::kRaws * Sh::kRaw;
-  float *ksc = reinterpret_cast<float *>(gbase + kAt);                       // int8: [slots][64] K scales, then V scales
-  float *vsc = ksc + Sh::kScaleSlots * kTreeKeys;
+  // int8, by tile: [slots][64] of K's scales times the softmax's, V's scales vs, log2 |vs| and 1 / |vs|
+  float *ksc = reinterpret_cast<float *>(gbase + kAt);
+  float *vsc = ksc + Sh::kScaleSlots * kTreeKeys, *vlog = vsc + Sh::kScaleSlots * kTreeKeys, *vinv = vlog + Sh::kScaleSlots * kTreeKeys;
   const uint32_t bars = sbase + kAt + Sh::kScaleBytes;
-  short *par = reinterpret_cast<short *>(gbase + kAt + Sh::kScaleBytes + 512);   // parents of the segment's nodes (256)
-  TreeSeg *segs = reinterpret_cast<TreeSeg *>(gbase + kAt + Sh::kScaleBytes + 1024);
+  uint8_t *fixed = gbase + kAt + Sh::kScaleBytes;
+  short *par = reinterpret_cast<short *>(fixed + 512);                       // parents of the segment's nodes (256)
+  uint32_t *masks = reinterpret_cast<uint32_t *>(fixed + 1024);              // [128][kMaskWords]
+  float *xch = reinterpret_cast<float *>(masks + kTreeRows * Sh::kMaskWords);   // [2][128]
+  TreeSeg *segs = reinterpret_cast<TreeSeg *>(xch + 2 * kTreeRows);
   TreeCtl *ctl = reinterpret_cast<TreeCtl *>(reinterpret_cast<uint8_t *>(segs) + kTreeSegs * sizeof(TreeSeg));
   volatile WaitBlock *wctl = reinterpret_cast<volatile WaitBlock *>(ctl + 1);
   volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(const_cast<WaitBlock *>(wctl) + 1);
@@ -448,13 +483,13 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(p_full(b), 4);
+      mbar_init(p_full(b), 8);
     }
     mbar_init(q_full, 32 * Sh::kLoaders);
     mbar_init(q_empty, 1);
     mbar_init(o_step, 1);
     mbar_init(o_done, 1);
-    mbar_init(o_free, 4);
+    mbar_init(o_free, 8);
     mbar_init(drain, 1);
     wait_block_init(wctl, a.wait_ns, a.err);
     fence_mbar_init();
@@ -582,19 +617,30 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           if (ok && stage >= F) ok = pwait(empty(fs), (uint32_t)((stage / F - 1) & 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          constexpr int WT = 32 * (kI8 ? Sh::kWideners : 1);
+          // a tile's scales, with its K: logarithm and inverse of V's (of 0: of 2^-100, which times
+          // vs is 0 again)
+          if ((i == 0 || (i & 1)) && i < 2 * n - 1 && t < kTreeKeys) {
+            const int at = ((tiles + (i + 1) / 2) % Sh::kScaleSlots) * kTreeKeys + t;
+            const float v = fabsf(vsc[at]);
+            const float lv = v < INFINITY ? fmaxf(tree_lg2(v), -100.0f) : 0.0f;
+            vlog[at] = lv;
+            vinv[at] = tree_ex2(-lv);
+            ksc[at] *= a.scale_log2;
+          }
           constexpr int CH = D / 16;
-          constexpr int PER = kTreeKeys * CH / 128;
+          constexpr int PER = kTreeKeys * CH / WT;
           uint4 x[PER];
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const uint32_t at = cd_s + rs * Sh::kRaw + 16 * (k * 128 + t);
+            const uint32_t at = cd_s + rs * Sh::kRaw + 16 * (k * WT + t);
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(at) : "memory");
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(raw_empty(rs));
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const int id = k * 128 + t, row = id / CH, cc = id % CH;
+            const int id = k * WT + t, row = id / CH, cc = id % CH;
             const uint32_t w[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u, x[k].w ^ 0x80808080u};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -608,13 +654,15 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           fence_proxy_async_smem();
           mbar_arrive(full(fs));
         }
+        tiles += n;
       }
     } else if (warp == Sh::kMmaWarp) {
       // ---------------------------------------------------------------- MMA --
       // The whole warp runs the loop and the leader lane issues: see mma_f16_ts_w.
       const uint32_t leader = elect_leader();
       auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, pwait(bar, parity)); };
-      constexpr uint32_t kIdS = tree_idesc(kBf, false, kTreeRows, kTreeKeys), kIdO = tree_idesc(kBf, true, kTreeRows, D);
+      constexpr uint32_t kIdO = tree_idesc(kBf, true, kTreeRows, D);
+      const uint32_t kIdS = tree_idesc(kBf, false, kTreeRows, kTreeKeys) | (a.scale_log2 < 0.0f && !kI8 ? 1u << 13 : 0u);
       for (int si = 0; si < nseg && ok; ++si) {
         const int n = segs[si].u1 - segs[si].u0;
         const int seg = nsegs + si;
@@ -660,24 +708,28 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         stage += 2 * n;
         tiles += n;
       }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
       // ------------------------------------------------------------ softmax --
-      const int row = threadIdx.x;                // of the 128 (TMEM lane)
-      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+      // Group grp = 0, 1 of four warps takes keys 32 grp .. of a tile and half of O's columns; a
+      // thread a row.  Warps whose rows are all beyond the item's only keep the barriers going.
+      constexpr int ST = 256;
+      const int grp = warp >> 2, row = threadIdx.x & 127;              // (TMEM lane)
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       constexpr float kHead = kBf ? 0.0f : 7.0f, kPass = kBf ? 8.0f : 15.0f;
+      constexpr int DH = D / 2;
+      const float scale = fabsf(a.scale_log2);    // (a negative one negates Q)
       bool aborted = !ok;
       for (int si = 0; si < nseg && !aborted; ++si) {
-        const TreeSeg s = segs[si];
+        const TreeSeg &s = segs[si];
         const int n = s.u1 - s.u0, seg = nsegs + si;
         const int col = s.rb * kTreeRows + row, node = col / a.G, head = s.g * a.G + col - node * a.G;
         const bool real = node < s.nodes;
-        // the row's ancestors, as bits over the nodes; its depth; the first key its window holds
-        unsigned anc[8] = {};
-        int lo = s.lo, depth = 0;
-        const bool tree = tree_base(s, s.u1 - 1) + kTreeKeys > s.pos0 || a.window > 0;       // (segments that never meet the tree need no mask)
-        named_bar_sync(1, 128);                   // the last segment's parents have been read
-        if (tree && s.nodes <= 256) {
-          for (int i = row; i < s.nodes; i += 128) {
+        const bool busy = __any_sync(0xffffffffu, real);
+        // the row's ancestors, as bits over the nodes, and the first key its window holds
+        uint32_t *mine = masks + row * Sh::kMaskWords;
+        if ((tree_base(s, s.u1 - 1) + kTreeKeys > s.pos0 || a.window > 0) && s.nodes <= 256) {   // (else none is needed)
+          named_bar_sync(1, ST);                  // the last segment's have been read
+          for (int i = threadIdx.x; i < s.nodes; i += ST) {
             int p = __ldg(a.parents + s.tok0 + i);
             if (p < -1 || p >= i) {
               atomicCAS(a.err, 0, -9);
@@ -685,187 +737,212 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             par[i] = (short)p;
           }
-          named_bar_sync(1, 128);
-          if (real && s.len > 0) {
-            if (a.window > 0) {
+          named_bar_sync(1, ST);
+          if (grp == 0) {
+            int depth = 0;
+            if (real && a.window > 0)
               for (int i = par[node]; i >= 0; i = par[i]) ++depth;
-              lo = max(s.pos0 + depth - a.window + 1, 0);
-            }
-            int e = 0;
-            for (int i = node; i >= 0; i = par[i], ++e) {
-              if (a.window == 0 || e < a.window || s.pos0 + depth - e < a.sinks) {
 #pragma unroll
-                for (int w = 0; w < 8; ++w)
-                  if (i >> 5 == w) anc[w] |= 1u << (i & 31);
-              }
+            for (int w = 0; w < 8; ++w) mine[w] = 0u;
+            mine[8] = (uint32_t)(a.window > 0 ? max(s.pos0 + depth - a.window + 1, 0) : 0);
+            if (real && s.len > 0) {
+              int e = 0;
+              for (int i = node; i >= 0; i = par[i], ++e)
+                if (a.window == 0 || e < a.window || s.pos0 + depth - e < a.sinks) mine[i >> 5] |= 1u << (i & 31);
             }
           }
+          named_bar_sync(1, ST);
         }
-        // the keys before this one are seen by every row, from `whole` on (without the sinks)
+        // keys from this one on (before the tree) are in every row's window
         const int whole = a.window > 0 ? s.pos0 + s.nodes - a.window : 0;
         float m_ref = kTreeNoScore, l = 0.0f;
-        float mp = kTreeNoScore;                  // int8: the reference of the weights with their values' scales
         for (int i = 0; i < n; ++i) {
           const int gt = tiles + i, b = gt & 1;
           const int base = tree_base(s, s.u0 + i);
           const bool masked = base + kTreeKeys > s.pos0 || (base < whole && base + kTreeKeys > a.sinks);
           unsigned long long vis = ~0ull;
           if (masked) {
+            const int lo = a.window > 0 ? (int)mine[8] : 0;
             vis = tree_bits(lo - base, s.pos0 - base) | tree_bits(0, min(a.sinks, s.pos0) - base);
             const int at = base - s.pos0;         // the tile's first key among the nodes
             if (at > -kTreeKeys && at < 256) {
               unsigned long long t = 0;
-#pragma unroll
-              for (int w = 0; w < 8; ++w) {
+              for (int w = max(at, 0) >> 5; w < 8 && 32 * w - at < 64; ++w) {
                 const int sh = 32 * w - at;       // where word w starts in the tile
-                if (sh > -32 && sh < 64) t |= sh >= 0 ? (unsigned long long)anc[w] << sh : (unsigned long long)anc[w] >> -sh;
+                t |= sh >= 0 ? (unsigned long long)mine[w] << sh : (unsigned long long)mine[w] >> -sh;
               }
-              if (s.len - base < 64) t &= tree_bits(0, s.len - base);
-              vis |= t;
+              vis |= t & tree_bits(0, s.len - base);
             }
             if (!real) vis = 0;
           }
-          const bool got = pwait(s_full(b), (uint32_t)((gt >> 1) & 1));
-          if (named_bar_or(1, 128, !got || wctl->abort)) { aborted = true; break; }
+          const uint32_t vm = (uint32_t)(vis >> (32 * grp));
+          bool stop = !pwait(s_full(b), (uint32_t)((gt >> 1) & 1));
           tc_fence_after();
-          const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys);
-          const float *kss = ksc + (gt % Sh::kScaleSlots) * kTreeKeys, *vss = vsc + (gt % Sh::kScaleSlots) * kTreeKeys;
-          float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys + 32 * grp);
+          const int sc = (gt % Sh::kScaleSlots) * kTreeKeys + 32 * grp;
+          F2 x[16];
+          float top = -INFINITY;
+          if (busy) {
             uint32_t v[32];
-            tmem_ld32(sadr + 32u * hh, v);
+            tmem_ld32(sadr, v);
             tmem_wait_ld();
-            const uint32_t vm = (uint32_t)(vis >> (32 * hh));
+            if constexpr (kI8) {                  // log2 of the weight times its value's scale
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float t = __uint_as_float(v[c]) * a.scale_log2;
-              if constexpr (kI8) t *= kss[32 * hh + c];
-              if (masked && !(vm >> c & 1)) t = -INFINITY;
-              mx = fmaxf(mx, t);
-              if constexpr (kI8) my = fmaxf(my, t + tree_lg2(fabsf(vss[32 * hh + c])));
-            }
-          }
-          // The references move only when a score passes them by 2^kPass; then O and l are
-          // rescaled, once the previous P V is done.
-          float fl = 1.0f, fo = 1.0f;
-          if (kI8) {
-            if (mx > m_ref + 8.0f) {
-              fl = tree_ex2(m_ref - mx);
-              m_ref = mx;
-            }
-            if (my > mp + kPass) {
-              fo = tree_ex2(mp - (my - kHead));
-              mp = my - kHead;
-            }
-          } else if (mx > m_ref + kPass) {
-            fl = fo = tree_ex2(m_ref - (mx - kHead));
-            m_ref = mx - kHead;
-          }
-          l *= fl;
-          const bool resc = fo != 1.0f && i > 0;
-          if (__any_sync(0xffffffffu, resc)) {
-            if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) {
-              aborted = true;
+              for (int c = 0; c < 32; c += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(ksc + sc + c), e = *reinterpret_cast<const float4 *>(vlog + sc + c);
+                x[c / 2] = fma2(F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), F2(k.x, k.y), F2(e.x, e.y));
+                x[c / 2 + 1] = fma2(F2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), F2(k.z, k.w), F2(e.z, e.w));
+              }
             } else {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            }
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float p, r;
+                x[c / 2].get(p, r);
+                x[c / 2] = F2(vm >> c & 1 ? p : -INFINITY, vm >> (c + 1) & 1 ? r : -INFINITY);
+              }
+            }
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              float p, r;
+              x[c].get(p, r);
+              t0 = max3(t0, p, r);
+              x[c + 1].get(p, r);
+              t1 = max3(t1, p, r);
+            }
+            top = fmaxf(t0, t1);
+            if (!kI8) top = top == -INFINITY ? top : top * scale;
+          }
+          // The reference moves only when a score passes it by 2^kPass (both groups decide together);
+          // then O and l are rescaled, once the previous P V is done.
+          stop = stop || wctl->abort;
+          if (named_bar_or(1, ST, stop || top > m_ref + kPass)) {
+            xch[grp * kTreeRows + row] = top;
+            if (named_bar_or(1, ST, stop)) {
+              aborted = true;
+              break;
+            }
+            top = fmaxf(top, xch[(grp ^ 1) * kTreeRows + row]);
+            float f = 1.0f;
+            if (top > m_ref + kPass) {
+              f = tree_ex2(m_ref - (top - kHead));
+              m_ref = top - kHead;
+            }
+            l *= f;
+            if (__any_sync(0xffffffffu, f != 1.0f) && i > 0) {
+              if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) stop = true;
               tc_fence_after();
 #pragma unroll 1
-              for (int cc = 0; cc < D; cc += 32) {
+              for (int cc = grp * DH; cc < (stop ? 0 : grp * DH + DH); cc += 32) {
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_base + cc, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * fo);
+                for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
                 tmem_st32(tmem + lane_base + cc, v);
               }
               tmem_wait_st();
             }
           }
-          // the weights, half a tile at a time: 16 columns of rounded pairs, 16 of what they leave
-          const float fw = kI8 ? (mp == kTreeNoScore ? 0.0f : tree_ex2(m_ref - mp)) : 1.0f;
           if constexpr (!kI8) {
             // A value that is not finite would reach the rows that do not see its key (0 times it is NaN),
             // so tiles seen partly are searched for such keys.  They are added here, to the rows
             // that see them, and cleared for the MMA.
-            if (masked && !aborted) {
+            if (masked) {
               const int st = stage + tree_v_stage(i, n);
               const uint32_t vst = st_s + (st % F) * Sh::kStage;
-              if (!pwait(full(st % F), (uint32_t)((st / F) & 1))) aborted = true;
-              if (row == 0) ctl->bad = 0;
-              if (named_bar_or(1, 128, aborted)) aborted = true;
-              if (!aborted) {
-                constexpr uint32_t e = kBf ? 0x7f807f80u : 0x7c007c00u;
-                bool bad = false;
-#pragma unroll 4
-                for (int c = 0; c < D / 16; ++c) {
-                  const uint32_t at = tree_chunk(vst, row >> 1, (row & 1) * (D / 16) + c);
-                  uint4 x;
-                  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
-                  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              stop = stop || !pwait(full(st % F), (uint32_t)((st / F) & 1));
+              if (threadIdx.x == 0) ctl->bad = 0;
+              named_bar_sync(1, ST);
+              constexpr uint32_t e = kBf ? 0x7f80u : 0x7c00u;
+              bool bad = false;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) bad |= (w[k] & (e & 0xffffu)) == (e & 0xffffu) || (w[k] & (e & 0xffff0000u)) == (e & 0xffff0000u);
+              for (int c = 0; c < D / 32; ++c) {
+                const uint32_t at = tree_chunk(vst, threadIdx.x >> 2, (threadIdx.x & 3) * (D / 32) + c);
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bad |= (w[k] & e) == e || (w[k] >> 16 & e) == e;
+              }
+              if (bad) atomicOr(&ctl->bad, 1ull << (threadIdx.x >> 2));
+              named_bar_sync(1, ST);
+              const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad);
+              if (found) {
+                stop = stop || !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
+                tc_fence_after();
+                if (named_bar_or(1, ST, stop)) {
+                  aborted = true;
+                  break;
                 }
-                if (bad) atomicOr(&ctl->bad, 1ull << (row >> 1));
-                named_bar_sync(1, 128);
-                const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad);
-                if (found) {
-                  aborted = !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
-                  if (named_bar_or(1, 128, aborted)) aborted = true;
-                  if (!aborted) {
-                    tc_fence_after();
-                    tree_add_bad<D, kBf>(tmem + lane_base, sadr, vst, found, vis, a.scale_log2, m_ref, i == 0);
-                    if (row == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
-                  }
-                }
+                tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, scale, m_ref, i == 0);
+                if (threadIdx.x == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
+                named_bar_sync(1, ST);            // (all scores have been read)
               }
             }
           }
-          if (!aborted) {
+          // the weights: 16 columns of rounded pairs, 16 of what they leave
+          auto weights = [&](auto partly) {
+            uint32_t hi[8], lw[8];
+            F2 sum(0.0f, 0.0f);
+            const F2 sc2(scale, scale), neg(-m_ref, -m_ref), minus(-1.0f, -1.0f);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t v[32], hi[16], lw[16];
-              tmem_ld32(sadr + 32u * hh, v);
-              tmem_wait_ld();
-              const uint32_t vm = (uint32_t)(vis >> (32 * hh));
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                float w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float t = __uint_as_float(v[c + e]) * a.scale_log2;
-                  if constexpr (kI8) t *= kss[32 * hh + c + e];
-                  const bool hide = masked && !(vm >> (c + e) & 1);
-                  const float p = hide ? 0.0f : tree_ex2(t - m_ref);
-                  l += p;
-                  w[e] = kI8 ? (hide ? 0.0f : p * fw * vss[32 * hh + c + e]) : p;
-                }
-                hi[c / 2] = tree_pack<kBf>(w[0], w[1]);
-                const float2 f = tree_unpack<kBf>(hi[c / 2]);
-                lw[c / 2] = tree_pack<kBf>(w[0] - f.x, w[1] - f.y);
+            for (int c = 0; c < 16; ++c) {
+              F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
+              float p, r;
+              w.get(p, r);
+              w = F2(tree_ex2(p), tree_ex2(r));
+              if constexpr (kI8) {
+                w = mul2(w, *reinterpret_cast<const F2 *>(vinv + sc + 2 * c));
+                sum = add2(sum, w);
+                w = mul2(w, *reinterpret_cast<const F2 *>(vsc + sc + 2 * c));
               }
-              tmem_st16(sadr + 32u * hh, hi);
-              tmem_st16(sadr + 32u * hh + 16u, lw);
+              w.get(p, r);
+              if constexpr (decltype(partly)::value) {      // (hidden: also with scores or scales that are not finite)
+                p = vm >> (2 * c) & 1 ? p : 0.0f;
+                r = vm >> (2 * c + 1) & 1 ? r : 0.0f;
+                w = F2(p, r);
+              }
+              if constexpr (!kI8) sum = add2(sum, w);
+              hi[c & 7] = tree_pack<kBf>(p, r);
+              const float2 h = tree_unpack<kBf>(hi[c & 7]);
+              fma2(F2(h.x, h.y), minus, w).get(p, r);
+              lw[c & 7] = tree_pack<kBf>(p, r);
+              if ((c & 7) == 7) {
+                tmem_st8(sadr + (uint32_t)(c - 7), hi);
+                tmem_st8(sadr + (uint32_t)(c + 9), lw);
+              }
             }
+            float p, r;
+            sum.get(p, r);
+            l += p + r;
             tmem_wait_st();
+          };
+          if (busy) {
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0 && !aborted) mbar_arrive(p_full(b));
-          if (__any_sync(0xffffffffu, aborted)) {
-            aborted = true;
-            if (lane == 0) wctl->abort = 1;
+          if (lane == 0) {
+            if (stop) wctl->abort = 1;
+            mbar_arrive(p_full(b));
           }
         }
         // ---- the rows, or their parts
         const bool got = !aborted && pwait(o_done, (uint32_t)(seg & 1));
-        if (named_bar_or(1, 128, !got || wctl->abort)) { aborted = true; break; }
+        xch[grp * kTreeRows + row] = l;
+        if (named_bar_or(1, ST, !got || wctl->abort)) { aborted = true; break; }
         tc_fence_after();
+        l += xch[(grp ^ 1) * kTreeRows + row];
         if (s.slot < 0) {
-          const float inv = l > 0.0f || !(l == l) ? 1.0f / l : 0.0f;
-          const float fin = kI8 ? inv * tree_ex2(mp - m_ref) : inv;
+          const float inv = 1.0f / l;
           const long long at = (long long)(s.tok0 + node) * a.Hq + head;
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 32) {
+          for (int cc = grp * DH; cc < grp * DH + DH; cc += 32) {
             uint32_t v[32];
             tmem_ld32(tmem + lane_base + cc, v);
             tmem_wait_ld();
@@ -874,23 +951,20 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               for (int h = 0; h < 2; ++h) {
                 uint32_t o[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const float x = l == 0.0f ? 0.0f : __uint_as_float(v[16 * h + 2 * c]) * fin, y = l == 0.0f ? 0.0f : __uint_as_float(v[16 * h + 2 * c + 1]) * fin;
-                  o[c] = tree_pack<kBf>(x, y);
-                }
+                for (int c = 0; c < 8; ++c)
+                  o[c] = l == 0.0f ? 0u : tree_pack<kBf>(__uint_as_float(v[16 * h + 2 * c]) * inv, __uint_as_float(v[16 * h + 2 * c + 1]) * inv);
                 uint4 *to = reinterpret_cast<uint4 *>(a.out + at * D + cc + 16 * h);
                 to[0] = make_uint4(o[0], o[1], o[2], o[3]);
                 to[1] = make_uint4(o[4], o[5], o[6], o[7]);
               }
             }
           }
-          if (real && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.693147180559945309f;
+          if (real && grp == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.693147180559945309f;
         } else {
           const int ps = 2 * (int)blockIdx.x + s.slot;
           float *part = a.part + (size_t)ps * tree_part_floats(D) + (size_t)row * D;
-          const float fin = kI8 ? tree_ex2(mp - m_ref) : 1.0f;
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 32) {
+          for (int cc = grp * DH; cc < grp * DH + DH; cc += 32) {
             uint32_t v[32];
             tmem_ld32(tmem + lane_base + cc, v);
             tmem_wait_ld();
@@ -899,13 +973,13 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               for (int h = 0; h < 4; ++h) {
                 uint32_t o[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) o[c] = l == 0.0f ? 0u : kI8 ? __float_as_uint(__uint_as_float(v[8 * h + c]) * fin) : v[8 * h + c];
+                for (int c = 0; c < 8; ++c) o[c] = l == 0.0f ? 0u : v[8 * h + c];
                 st_global_v8(part + cc + 8 * h, o);
               }
             }
           }
           float2 *ml = reinterpret_cast<float2 *>(a.part + (size_t)ps * tree_part_floats(D) + (size_t)kTreeRows * D) + row;
-          if (real) *ml = make_float2(m_ref, l);
+          if (real && grp == 0) *ml = make_float2(m_ref, l);
           if (s.slot == 1) {
             desc.tok0 = s.tok0;
             desc.col0 = s.rb * kTreeRows;
