@@ -267,6 +267,34 @@ int pack_common(int bits, const int8_t *codes, const uint16_t *scales, int N, in
 
 namespace qw {
 
+int encode_row_map(CUtensorMap *map, const void *base, long long rows, int d, long long pitch, bool int8, bool bf16) {
+  if (!load_encoder()) return fail(QW_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t estride[2] = {1, 1};
+  const cuuint64_t gdim[2] = {(cuuint64_t)d, (cuuint64_t)rows}, gstride[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {int8 ? (cuuint32_t)d : 64u, 1u};
+  const CUresult r = g_encode(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              2, const_cast<void *>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              int8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QW_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", (int)r);
+  return QW_OK;
+}
+
+int encode_page_map(CUtensorMap *map, const void *base, const long long (&dim)[3], const long long (&stride)[3], int d, int box,
+                    int box2, bool int8, bool bf16) {
+  if (!load_encoder()) return fail(QW_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t estride[4] = {1, 1, 1, 1};
+  const cuuint64_t gdim[4] = {(cuuint64_t)d, (cuuint64_t)dim[0], (cuuint64_t)dim[1], (cuuint64_t)dim[2]};
+  const cuuint64_t gstride[3] = {(cuuint64_t)stride[0], (cuuint64_t)stride[1], (cuuint64_t)stride[2]};
+  const cuuint32_t boxes[4] = {int8 ? (cuuint32_t)d : 64u, (cuuint32_t)box, 1u, (cuuint32_t)box2};
+  const CUresult r = g_encode(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              4, const_cast<void *>(base), gdim, gstride, boxes, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              int8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QW_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", (int)r);
+  return QW_OK;
+}
+
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 unsigned long long wait_limit_ns() {

@@ -12,12 +12,14 @@
 // 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
 // of the 128 rows a small tree fills.
 //
-// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 2
+// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 1
 // loading and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  A ring of stages, each
 // 64 rows of K or V, in the order K0 K1 V0 K2 V1 .. of a segment: scores of the next tile are
 // computed while the softmax works on the last.
-//   - Rows are loaded with cp.async, 16 bytes a thread, straight to the 128-byte swizzle: pages of
-//     any size and order, and rows that no node sees are zero-filled, not read.  K is the K-major
+//   - Rows come by TMA straight to the 128-byte swizzle: pages of a multiple of 8 rows in boxes of up
+//     to 64, other pages four rows a gather, from a map of rows one common divisor of the cache's
+//     strides apart (rows outside it are zeros).  (Gathers move 6 to 9 bytes a clock an SM; cp.async
+//     by two warps a CTA moved 10.)  Boxes without a row that a node sees are not read.  K is the K-major
 //     operand and V, as it lies, the MN-major one, so nothing is transposed.
 //   - P goes back into TMEM over the scores it came from.
 //   - O is rescaled only when a score passes the reference by 2^8 (fp16: 2^15).
@@ -71,9 +73,8 @@ struct TreeCtl {
 template <int D, int KV>
 struct TreeShape {
   static constexpr bool kI8 = KV == kPagedI8;
-  static constexpr int kLoaders = 2;              // warps
   static constexpr int kWideners = !kI8 ? 0 : D == 256 ? 4 : 2;
-  static constexpr int kMmaWarp = 8, kLoad0 = 9, kWiden0 = kLoad0 + kLoaders;
+  static constexpr int kMmaWarp = 8, kLoadWarp = 9, kWiden0 = 10;
   static constexpr int kWarps = kWiden0 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
@@ -137,6 +138,20 @@ __device__ __forceinline__ float tree_lg2(float x) {
 // arrive on `bar` when the thread's cp.async copies so far have landed (counted as one arrival)
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Four rows of a 2-D tensor map (box one row high), row after row, from column x; rows outside the
+// tensor are zero-filled.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int x, const int (&r)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+      : "memory");
+}
+// The box at (x, y, z, w) of a 4-D tensor map.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -216,7 +231,7 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs &a, const TreeSeq &
   p.first = p.lo / kTreeKeys;
   p.nsu = min((min(a.sinks, s.len) + kTreeKeys - 1) / kTreeKeys, p.first);
   p.n = max(p.nsu + (s.len + kTreeKeys - 1) / kTreeKeys - p.first, 1);       // an item without keys still writes its rows
-  p.blocks = (int)(((long long)s.nodes * a.G + kTreeRows - 1) / kTreeRows);
+  p.blocks = (int)(((long long)s.nodes * a.G + a.block_rows - 1) / a.block_rows);
   return p;
 }
 // places of a sequence for teams of R
@@ -405,6 +420,7 @@ __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t 
 #pragma unroll 1
     for (unsigned long long k = found; k; k &= k - 1) {
       const int j = __ffsll((long long)k) - 1;
+      if (!__any_sync(0xffffffffu, (vis >> j & 1) != 0)) continue;
       const float p = tree_ex2(tmem_ld1(scores + j) * scale - m);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -474,18 +490,18 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < F; ++s) {
-      mbar_init(full(s), kI8 ? 32 * Sh::kWideners : 32 * Sh::kLoaders);
+      mbar_init(full(s), kI8 ? 32 * Sh::kWideners : 1);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < Sh::kRaws; ++s) {
-      mbar_init(raw_full(s), 32 * Sh::kLoaders);
+      mbar_init(raw_full(s), 33);
       mbar_init(raw_empty(s), Sh::kWideners);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(p_full(b), 8);
     }
-    mbar_init(q_full, 32 * Sh::kLoaders);
+    mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(o_step, 1);
     mbar_init(o_done, 1);
@@ -515,94 +531,144 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 
   for (;;) {
     const int nseg = ctl->nseg;
-    if (warp >= Sh::kLoad0 && warp < Sh::kWiden0) {
+    if (warp == Sh::kLoadWarp) {
       // ------------------------------------------------------------ loading --
-      constexpr int RPW = kTreeKeys / Sh::kLoaders;               // rows of a tile a warp: 16 or 32
-      constexpr int RB = kI8 ? D : 2 * D;                         // bytes of a row
-      constexpr int CH = RB / 16;                                 // 16-byte chunks of it
-      constexpr int RPI = 32 / CH;                                // rows a step of the warp (CH <= 32)
-      const int lw = warp - Sh::kLoad0;
-      const int c = lane % CH, ro = lane / CH;
+      // Pages of whole boxes (8 to 64 rows, a.box): box b of a tile is rows box * (b % boxes) .. of 128
+      // bytes b / boxes (int8: of whole rows), and lane b's.  Other pages: a tile's 64 rows are sixteen gathers of four rows, and as many
+      // for each 128 bytes; lane l finds the rows of quad l % 16.
+      constexpr int CW = kI8 ? 1 : D / 64;                        // boxes or gathers side by side
       constexpr int kRing = kI8 ? Sh::kRaws : F;
+      const int quad = lane & 15;
+      const int boxes = a.box ? kTreeKeys / a.box : 16;           // down a tile; a power of two
+      const int first = a.box ? (lane & (boxes - 1)) * a.box : 4 * quad;       // this lane's first row
+      const int chunk = lane / boxes;                             // its 128 bytes (box: the only ones)
+      const int nrows = a.box ? a.box : 4;
       for (int si = 0; si < nseg && ok; ++si) {
         const TreeSeg &s = segs[si];
         const int n = s.u1 - s.u0;
-        // lane l < RPW: where row RPW lw + l of a tile starts (elements), -1 where it is not read
-        auto page_of = [&](int i) {
-          const int j = tree_base(s, s.u0 + i) + RPW * lw + lane % RPW;
-          const bool see = j < s.len && (j >= s.lo || j < a.sinks);
-          const int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page;
-          return see ? __ldg(a.table + (long long)s.b * a.max_pages + pi) : -2;
-        };
-        auto start_of = [&](int i, int pid, long long &scale_at) -> long long {
-          const int j = tree_base(s, s.u0 + i) + RPW * lw + lane % RPW;
-          const int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page;
-          const int r = j - pi * a.page;
-          if ((unsigned)pid >= (unsigned)a.npages) {
-            if (pid != -2) atomicCAS(a.err, 0, -9);
-            scale_at = -1;
-            return -1;
-          }
-          scale_at = ((long long)pid * a.Hkv + s.g) * a.page + r;
-          return pid * a.page_stride + s.g * a.head_stride + r * a.tok_stride;
-        };
-        auto copy_rows = [&](const uint8_t *base, long long start) {
-          const int slot = stage % kRing;
-          if (stage >= kRing && ok) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((stage / kRing - 1) & 1)));
-          if (!ok) return;
-          const uint32_t dst = kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage;
+        auto seen = [&](int j) { return j < s.len && (j >= s.lo || j < a.sinks); };
+        auto page_at = [&](int j) { return a.page_shift >= 0 ? j >> a.page_shift : j / a.page; };
+        // the pages of the lane's rows of tile i (a box: of all of them), -2 where none is needed
+        auto pages_of = [&](int i, int (&pid)[4]) {
+          const int j = tree_base(s, s.u0 + i) + first;
+          const int *t = a.table + (long long)s.b * a.max_pages;
+          if (a.box) {
+            pid[0] = j < s.len && (j + a.box > s.lo || j < a.sinks) ? __ldg(t + page_at(j)) : -2;
+          } else {
+            int pi = page_at(j), r = j - pi * a.page;
 #pragma unroll
-          for (int k = 0; k < RPW / RPI; ++k) {
-            const int r = k * RPI + ro, row = RPW * lw + r;
-            const long long at = __shfl_sync(0xffffffffu, start, r);
-            const uint8_t *src = base + (at < 0 ? 0 : at * (kI8 ? 1 : 2) + 16 * c);
-            const uint32_t to = kI8 ? dst + row * RB + 16 * c : dst + (c >> 3) * (kTreeKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-            cp_async16(to, src, at < 0 ? 0u : 16u);
-          }
-        };
-        auto done = [&]() {
-          const int slot = stage % kRing;
-          if (ok) cp_async_arrive(kI8 ? raw_full(slot) : full(slot));
-          ++stage;
-        };
-        int pid = page_of(0);
-        long long at_v = 0;
-        for (int i = 0; i <= n && ok; ++i) {
-          long long at_k = -1, sc_k = -1;
-          if (i < n) {
-            at_k = start_of(i, pid, sc_k);
-            if (i + 1 < n) pid = page_of(i + 1);
-            copy_rows(a.k, at_k);
-            if constexpr (kI8) {                  // the tile's scales come with its K
-              if (ok && lane < RPW) {
-                const int slot = (tiles + i) % Sh::kScaleSlots, row = RPW * lw + lane;
-                cp_async4_zfill(smem_u32(ksc + slot * kTreeKeys + row), a.ks + (sc_k < 0 ? 0 : sc_k), sc_k < 0 ? 0u : 4u);
-                cp_async4_zfill(smem_u32(vsc + slot * kTreeKeys + row), a.vs + (sc_k < 0 ? 0 : sc_k), sc_k < 0 ? 0u : 4u);
+            for (int e = 0; e < 4; ++e) {
+              pid[e] = seen(j + e) ? __ldg(t + pi) : -2;
+              if (++r == a.page) {
+                r = 0;
+                ++pi;
               }
             }
-            done();
+          }
+        };
+        auto page_ok = [&](int pid) {
+          if ((unsigned)pid < (unsigned)a.npages) return true;
+          if (pid != -2) atomicCAS(a.err, 0, -9);
+          return false;
+        };
+        // copies the lane's part of tile i to the ring's next stage
+        auto copy = [&](const void *boxmap, const void *rowmap, int i, const int (&pid)[4]) {
+          const int slot = stage % kRing;
+          if (stage >= kRing) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((stage / kRing - 1) & 1)));
+          if (!ok) return;
+          const uint32_t bar = kI8 ? raw_full(slot) : full(slot);
+          const uint32_t dst = (kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage) + first * (kI8 ? D : 128);
+          const int j = tree_base(s, s.u0 + i) + first;
+          const int r0 = j - page_at(j) * a.page;
+          constexpr int kRowBytes = kI8 ? D : 128;
+          // boxes that no node sees a row of stay what they are: their keys are masked
+          const bool on = chunk < CW && (!a.box || pid[0] != -2);
+          const unsigned parts = __ballot_sync(0xffffffffu, on);
+          if (lane == 0) mbar_arrive_expect_tx(bar, a.box ? __popc(parts) * a.box * kRowBytes : kI8 ? Sh::kRaw : Sh::kStage);
+          __syncwarp();
+          if (!on) return;
+          if (a.box && page_ok(pid[0])) {
+            tma_load_4d(dst + (kI8 ? 0 : chunk * (kTreeKeys * 128)), boxmap, 64 * (kI8 ? 0 : chunk), r0, s.g, pid[0], bar);
+            return;
+          }
+          for (int q = 0; q < nrows; q += 4) {    // (a box of a page that is none: zeros)
+            int row[4];
+            int r = r0 + q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              row[e] = !a.box && seen(j + e) && page_ok(pid[e]) ? pid[e] * a.page_rows + s.g * a.head_rows + r * a.tok_rows : -1;
+              if (++r == a.page) r = 0;
+            }
+            for (int c = chunk; c < CW; c += a.box ? CW : 2)
+              tma_gather4(dst + q * kRowBytes + (kI8 ? 0 : c * (kTreeKeys * 128)), rowmap, kI8 ? 0 : 64 * c, row, bar);
+          }
+        };
+        // the page table, far ahead of its use: lines of 32 entries from tile i on
+        auto fetch_ahead = [&](int i, int line) {
+          const int j = tree_base(s, s.u0 + min(i, n - 1)), pi = page_at(j) + 32 * line;
+          if (pi <= page_at(max(s.len - 1, 0)) && pi < a.max_pages) prefetch_l1(a.table + (long long)s.b * a.max_pages + pi);
+        };
+        fetch_ahead(0, lane);
+        int pid[4], vpid[4];
+        pages_of(0, pid);
+        for (int i = 0; i <= n && ok; ++i) {
+          int kpid[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) kpid[e] = pid[e];
+          if (i < n) {
+            if (i + 1 < n) pages_of(i + 1, pid);
+            if (lane < 2) fetch_ahead(i + 16, lane);
+            copy(&a.kbox, &a.kmap, i, kpid);
+            if constexpr (kI8) {                  // the tile's scales come with its K: lanes 0 .. 15 K's, the others V's
+              const int other = __shfl_sync(0xffffffffu, kpid[0], a.box ? 4 * quad / a.box : 0);
+              if (ok) {
+                const int slot = (tiles + i) % Sh::kScaleSlots, j = tree_base(s, s.u0 + i) + 4 * quad;
+                const float *from = lane < 16 ? a.ks : a.vs;
+                float *to = (lane < 16 ? ksc : vsc) + slot * kTreeKeys + 4 * quad;
+                int r = j - page_at(j) * a.page;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int p = a.box ? other : kpid[e];
+                  const bool on = seen(j + e) && (unsigned)p < (unsigned)a.npages;
+                  cp_async4_zfill(smem_u32(to + e), from + (on ? ((long long)p * a.Hkv + s.g) * a.page + r : 0), on ? 4u : 0u);
+                  if (++r == a.page) r = 0;
+                }
+                cp_async_arrive(raw_full(stage % kRing));
+              }
+            }
+            ++stage;
           }
           if (i == 0 && ok) {
             // Q: row r is column rb * 128 + r of the KV head: node column / G, head column % G
             if (nsegs + si > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((nsegs + si - 1) & 1)));
             if (ok) {
-              constexpr int QC = D / 8;           // chunks of a row
-              const int rows = s.nodes * a.G - s.rb * kTreeRows;
-#pragma unroll 4
-              for (int x = (warp - Sh::kLoad0) * 32 + lane; x < kTreeRows * QC; x += 32 * Sh::kLoaders) {
-                const int r = x / QC, cc = x % QC;
-                const int col = s.rb * kTreeRows + r, i2 = col / a.G, h = col - i2 * a.G;
-                const uint16_t *src = r < rows ? a.q + (long long)(s.tok0 + i2) * a.q_tok + (long long)(s.g * a.G + h) * a.q_head + 8 * cc : a.q;
-                cp_async16(q_s + (cc >> 3) * (kTreeRows * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4), src, r < rows ? 16u : 0u);
+              if (a.G <= kTreeRows) {             // whole nodes: one box (rows beyond the sequence's are never written)
+                if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
+                __syncwarp();
+                if (lane < D / 64)
+                  tma_load_4d(q_s + lane * (kTreeRows * 128), &a.qbox, 64 * lane, 0, s.g, s.tok0 + s.rb * (a.block_rows / a.G), q_full);
+              } else {
+                if (lane == 0) mbar_arrive_expect_tx(q_full, Sh::kQ);
+                __syncwarp();
+                int row[4];
+                const int cols = s.nodes * a.G;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int col = s.rb * kTreeRows + 4 * lane + e, node = col / a.G;
+                  row[e] = col < cols ? (s.tok0 + node) * a.q_tok_rows + (s.g * a.G + col - node * a.G) * a.q_head_rows : -1;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) tma_gather4(q_s + c * (kTreeRows * 128) + lane * 512, &a.qmap, 64 * c, row, q_full);
               }
-              cp_async_arrive(q_full);
             }
           }
           if (i > 0 && ok) {
-            copy_rows(a.v, at_v);
-            done();
+            copy(&a.vbox, &a.vmap, i - 1, vpid);
+            if (kI8 && ok) cp_async_arrive(raw_full(stage % kRing));
+            ++stage;
           }
-          at_v = at_k;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vpid[e] = kpid[e];
         }
         tiles += n;
       }
@@ -671,7 +737,6 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           if (i < n) {
             const int st = stage + tree_k_stage(i), slot = st % F, b = (tiles + i) & 1;
             if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
-            fence_proxy_async_smem();             // the copies' writes, seen through the barrier
             tc_fence_after();
             const uint32_t ks = st_s + slot * Sh::kStage;
 #pragma unroll
@@ -686,7 +751,6 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             const int j = i - 1, st = stage + tree_v_stage(j, n), slot = st % F, gt = tiles + j, b = gt & 1;
             if (!wwait(p_full(b), (uint32_t)((gt >> 1) & 1))) { ok = false; break; }
             if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
-            fence_proxy_async_smem();
             tc_fence_after();
             const uint32_t vs = st_s + slot * Sh::kStage;
             // (O of the segment before has been read; a tile with values that are not finite starts it at 0)
@@ -722,8 +786,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       for (int si = 0; si < nseg && !aborted; ++si) {
         const TreeSeg &s = segs[si];
         const int n = s.u1 - s.u0, seg = nsegs + si;
-        const int col = s.rb * kTreeRows + row, node = col / a.G, head = s.g * a.G + col - node * a.G;
-        const bool real = node < s.nodes;
+        const int col = s.rb * a.block_rows + row, node = col / a.G, head = s.g * a.G + col - node * a.G;
+        const bool real = node < s.nodes && row < a.block_rows;
         const bool busy = __any_sync(0xffffffffu, real);
         // the row's ancestors, as bits over the nodes, and the first key its window holds
         uint32_t *mine = masks + row * Sh::kMaskWords;
@@ -982,8 +1046,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           if (real && grp == 0) *ml = make_float2(m_ref, l);
           if (s.slot == 1) {
             desc.tok0 = s.tok0;
-            desc.col0 = s.rb * kTreeRows;
-            desc.cols = min(s.nodes * a.G - s.rb * kTreeRows, kTreeRows);
+            desc.col0 = s.rb * a.block_rows;
+            desc.cols = min(s.nodes * a.G - s.rb * a.block_rows, a.block_rows);
             desc.g = s.g;
             desc.parts = s.parts;
             desc.step = ctl->size;
@@ -1006,7 +1070,13 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   }
 
   // what was started ends before the CTA does
-  if (warp >= Sh::kLoad0 && warp < Sh::kWiden0) asm volatile("cp.async.wait_all;" ::: "memory");
+  if (warp == Sh::kLoadWarp) {
+    constexpr int kRing = kI8 ? Sh::kRaws : F;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int st = max(stage - kRing, 0); st < stage && lane == 0; ++st)
+      mbar_drain(kI8 ? raw_full(st % kRing) : full(st % kRing), (uint32_t)((st / kRing) & 1), wctl);
+    if (nsegs > 0 && lane == 0) mbar_drain(q_full, (uint32_t)((nsegs - 1) & 1), wctl);
+  }
   if (warp == Sh::kMmaWarp) {
     const uint32_t leader = elect_leader();
     mma_commit_w(leader, drain);

@@ -261,6 +261,30 @@ constexpr size_t kPagedCounterBytes = 3 * kPagedMaxCtas * 4;   // three counters
 size_t paged_ws(int d, int cols, int sms) {
   return kPagedCounterBytes + (size_t)2 * paged_ctas(d, cols) * sms * cols * (d + 2) * 4;
 }
+// Rows at i * stride[0] + j * stride[1] + k * stride[2] (bytes, multiples of 16) as the rows of one
+// map, `pitch` bytes apart.
+struct RowView {
+  long long rows, pitch;
+  int step[3];
+};
+RowView row_view(long long n0, long long s0, long long n1, long long s1, long long n2, long long s2, long long row) {
+  const long long n[3] = {n0, n1, n2}, s[3] = {s0, s1, s2};
+  long long g = 0, last = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] < 1) return RowView{0, row, {0, 0, 0}};
+    if (n[i] == 1) continue;                      // (a stride of one element means nothing)
+    for (long long x = s[i]; x;) {
+      const long long y = g % x;
+      g = x;
+      x = y;
+    }
+    last += (n[i] - 1) * s[i];
+  }
+  if (g == 0) g = row;
+  RowView v{last / g + 1, g, {0, 0, 0}};
+  for (int i = 0; i < 3; ++i) v.step[i] = n[i] == 1 || s[i] / g > 0x7fffffffll ? 0 : (int)(s[i] / g);
+  return v;
+}
 constexpr size_t kTreeDescBytes = kPagedMaxCtas * sizeof(TreeDesc);
 size_t tree_ws(int d, int sms) { return kTreeDescBytes + (size_t)2 * tree_ctas(d) * sms * tree_part_floats(d) * 4; }
 int check_heads(int d, int Hq, int Hkv, int max_new) {
@@ -478,27 +502,51 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   const size_t need = tree_ws(c->d, sms);
   if (!ws || ws_bytes < need)
     return bad(QW_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
-  a.q = q;
+  // the cache and q as rows: their strides' greatest common divisor apart
+  const bool i8 = c->dtype == QW_KV_INT8, bf = c->dtype == QW_KV_BF16;
+  const int es = i8 ? 1 : 2;
+  RowView kv = row_view(c->num_pages, c->page_stride * es, c->Hkv, c->head_stride * es, c->page, c->token_stride * es, c->d * es);
+  RowView qv = row_view(1, 0, T, q_token_stride * 2, Hq, q_head_stride * 2, c->d * 2);
+  if (kv.rows > 0x7fffffffll || qv.rows > 0x7fffffffll)
+    return bad(QW_ERR_UNSUPPORTED_SHAPE, "more than 2^31 rows of the strides' greatest common divisor");
+  const bool none = kv.rows == 0;                // no pages: every row is outside a map of one row
+  if ((rc = encode_row_map(&a.kmap, none ? q : c->k, none ? 1 : kv.rows, c->d, kv.pitch, i8, bf))) return rc;
+  if ((rc = encode_row_map(&a.vmap, none ? q : c->v, none ? 1 : kv.rows, c->d, kv.pitch, i8, bf))) return rc;
+  if ((rc = encode_row_map(&a.qmap, q, qv.rows, c->d, qv.pitch, false, bf))) return rc;
+  // boxes of the rows of a tile that lie in one page, where that are 8 or more
+  a.box = none ? 0 : c->page & -c->page;
+  a.box = a.box < 8 ? 0 : a.box < 64 ? a.box : 64;
+  if (a.box) {
+    const long long dim[3] = {c->page, c->Hkv, c->num_pages};
+    const long long stride[3] = {c->token_stride * es, c->Hkv > 1 ? c->head_stride * es : 16, c->num_pages > 1 ? c->page_stride * es : 16};
+    if ((rc = encode_page_map(&a.kbox, c->k, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
+    if ((rc = encode_page_map(&a.vbox, c->v, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
+  }
+  const int G = Hq / c->Hkv;
+  a.block_rows = G <= 128 ? 128 / G * G : 128;
+  if (G <= 128) {
+    const long long dim[3] = {G, c->Hkv, T};
+    const long long stride[3] = {G > 1 ? q_head_stride * 2 : 16, c->Hkv > 1 ? G * q_head_stride * 2 : 16, T > 1 ? q_token_stride * 2 : 16};
+    if ((rc = encode_page_map(&a.qbox, q, dim, stride, c->d, G, 128 / G, false, bf))) return rc;
+  }
+  a.page_rows = kv.step[0];
+  a.head_rows = kv.step[1];
+  a.tok_rows = kv.step[2];
+  a.q_tok_rows = qv.step[1];
+  a.q_head_rows = qv.step[2];
   a.out = out;
   a.lse = lse;
-  a.k = static_cast<const uint8_t *>(c->k);
-  a.v = static_cast<const uint8_t *>(c->v);
   a.ks = c->k_scale;
   a.vs = c->v_scale;
   a.table = b->page_table;
   a.lens = b->seq_lens;
   a.cu = b->cu_tokens;
   a.parents = parents;
-  a.q_tok = q_token_stride;
-  a.q_head = q_head_stride;
-  a.page_stride = c->page_stride;
-  a.head_stride = c->head_stride;
-  a.tok_stride = c->token_stride;
   a.B = b->B;
   a.T = T;
   a.Hq = Hq;
   a.Hkv = c->Hkv;
-  a.G = Hq / c->Hkv;
+  a.G = G;
   a.page = c->page;
   a.npages = c->num_pages;
   a.max_pages = b->max_pages;

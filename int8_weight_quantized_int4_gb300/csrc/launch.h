@@ -144,13 +144,17 @@ struct TreeDesc {               // an item that several CTAs share, left by the 
   int parts, step;              // parts; CTAs from one to the next
 };
 struct TreeArgs {
-  const uint16_t *q;            // as PagedArgs
-  uint16_t *out;
+  CUtensorMap qmap, kmap, vmap; // rows of d elements, boxes of 64 elements (int8: d) and one row
+  CUtensorMap kbox, vbox;       // [pages][Hkv][page][d], boxes of 64 elements (int8: d) and `box` rows
+  int box;                      // 0: the pages are no multiple of 8 rows
+  CUtensorMap qbox;             // [T][Hkv][G][d], boxes of 64 elements and block_rows rows (G <= 128)
+  int block_rows;               // rows of an item: whole nodes, up to 128
+  uint16_t *out;                // as PagedArgs
   float *lse;
-  const uint8_t *k, *v;
   const float *ks, *vs;
   const int *table, *lens, *cu, *parents;
-  long long q_tok, q_head, page_stride, head_stride, tok_stride;
+  int q_tok_rows, q_head_rows;  // strides in rows of the maps
+  int page_rows, head_rows, tok_rows;
   int B, T, Hq, Hkv, G, page, npages, max_pages, cap, window, sinks, page_shift;
   int max_nodes, min_tiles;     // fewest tiles of keys a CTA takes
   float scale_log2;
@@ -159,6 +163,13 @@ struct TreeArgs {
   int *err;
   unsigned long long wait_ns;
 };
+// A tensor map of `rows` rows of d elements `pitch` bytes apart, in boxes of one row (int8: whole
+// rows, unswizzled; 16 bits: 64 elements, 128-byte swizzle), for gathers.
+int encode_row_map(CUtensorMap *map, const void *base, long long rows, int d, long long pitch, bool int8, bool bf16);
+// [dim[2]][dim[1]][dim[0]][d] (strides in bytes), in boxes of `box` by 1 by `box2` rows: the cache as
+// pages, heads and tokens, q as nodes, KV heads and the heads of each.
+int encode_page_map(CUtensorMap *map, const void *base, const long long (&dim)[3], const long long (&stride)[3], int d, int box,
+                    int box2, bool int8, bool bf16);
 // CTAs an SM: TMEM holds O and two buffers of scores of two CTAs up to d = 128
 constexpr int tree_ctas(int d) { return d == 256 ? 1 : 2; }
 __host__ __device__ constexpr size_t tree_part_floats(int d) { return (size_t)128 * (d + 2); }

@@ -115,7 +115,7 @@ def same(a, b):
 
 SHAPES = [("fp16", 128, 16, 4, 16, False), ("fp16", 256, 24, 4, 16, False), ("bf16", 128, 32, 8, 64, True),
           ("int8", 256, 24, 4, 16, False), ("fp16", 64, 64, 8, 1, False), ("bf16", 256, 8, 8, 48, False),
-          ("int8", 128, 16, 1, 7, False), ("int8", 64, 6, 2, 32, True), ("fp16", 128, 40, 10, 33, True),
+          ("int8", 128, 16, 1, 7, False), ("int8", 64, 6, 2, 32, True), ("fp16", 128, 40, 10, 33, True), ("bf16", 128, 160, 1, 16, False), ("fp16", 64, 100, 2, 8, True),
           ("bf16", 64, 16, 1, 128, False)]
 
 
@@ -294,6 +294,26 @@ def test_pages_outside_the_window_are_not_read():
 def test_fewer_positions_than_nodes():
     """Nodes before the first position have no slot; others see what there is."""
     check(Case([3, 100, 60], [10, 2, 90], 8, 2, 128, 16, "bf16", seed=14))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "int8"])
+def test_padded_strides_and_no_pages(kind):
+    """Rows, heads and pages any multiple of 16 bytes apart; a cache of one page, and of none."""
+    c = Case([300, 40], [20, 9], 8, 2, 128, 16, kind, seed=21)
+    want = run(c)
+    for pad in ((0, 0, 16), (0, 3, 0), (2, 0, 48), (1, 5, 16)):
+        shape = [n + p for n, p in zip(c.k.shape[1:], pad)]
+        both = torch.full((2, c.k.shape[0], *shape), 7, dtype=c.k.dtype, device=DEV)
+        k, v = (x[:, :2, :16, :128] for x in both)
+        k.copy_(c.k)
+        v.copy_(c.v)
+        assert same(want, (q.attn_tree(c.q, k, v, *c.args()[2:], c.parents, lse=torch.empty_like(want[1]), **c.kw)))
+    one = Case([16], [5], 8, 2, 64, 16, kind, seed=22, spare=0)
+    assert one.k.shape[0] == 1
+    check(one)
+    e = {n: v[:0] for n, v in c.kw.items()}
+    out, lse = q.attn_tree(c.q, c.k[:0], c.v[:0], *c.args()[2:], c.parents, lse=torch.empty_like(want[1]), **e)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and bool((out == 0).all())
 
 
 def test_streams_graphs_and_workspaces():
