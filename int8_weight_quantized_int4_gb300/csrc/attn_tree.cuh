@@ -12,7 +12,7 @@
 // 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
 // of the 128 rows a small tree fills.
 //
-// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 1
+// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 2
 // loading and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  A ring of stages, each
 // 64 rows of K or V, in the order K0 K1 V0 K2 V1 .. of a segment: scores of the next tile are
 // computed while the softmax works on the last.
@@ -74,7 +74,7 @@ template <int D, int KV>
 struct TreeShape {
   static constexpr bool kI8 = KV == kPagedI8;
   static constexpr int kWideners = !kI8 ? 0 : D == 256 ? 4 : 2;
-  static constexpr int kMmaWarp = 8, kLoadWarp = 9, kWiden0 = 10;
+  static constexpr int kMmaWarp = 8, kLoadWarp = 9, kWiden0 = 11;   // loading: K and Q, V
   static constexpr int kWarps = kWiden0 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < Sh::kRaws; ++s) {
-      mbar_init(raw_full(s), 33);
+      mbar_init(raw_full(s), a.scale_boxes ? 1 : 33);
       mbar_init(raw_empty(s), Sh::kWideners);
     }
     for (int b = 0; b < 2; ++b) {
@@ -527,17 +527,22 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   int tiles = 0;                                  // tiles
   int nsegs = 0;                                  // segments
   bool ok = true;
+  int last = -1, queries = 0;                     // loading: the last stage copied to slot `lane`; Qs copied
   TreeDesc desc{};                                // the item whose first part this CTA leaves
 
   for (;;) {
     const int nseg = ctl->nseg;
-    if (warp == Sh::kLoadWarp) {
+    if (warp == Sh::kLoadWarp || warp == Sh::kLoadWarp + 1) {
       // ------------------------------------------------------------ loading --
       // Pages of whole boxes (8 to 64 rows, a.box): box b of a tile is rows box * (b % boxes) .. of 128
       // bytes b / boxes (int8: of whole rows), and lane b's.  Other pages: a tile's 64 rows are sixteen gathers of four rows, and as many
       // for each 128 bytes; lane l finds the rows of quad l % 16.
+      // One warp loads K and Q, the other V (a box holds its warp about 70 cycles).
       constexpr int CW = kI8 ? 1 : D / 64;                        // boxes or gathers side by side
       constexpr int kRing = kI8 ? Sh::kRaws : F;
+      constexpr int kRowBytes = kI8 ? D : 128;
+      const bool isv = warp != Sh::kLoadWarp;
+      const void *boxmap = isv ? &a.vbox : &a.kbox, *rowmap = isv ? &a.vmap : &a.kmap;
       const int quad = lane & 15;
       const int boxes = a.box ? kTreeKeys / a.box : 16;           // down a tile; a power of two
       const int first = a.box ? (lane & (boxes - 1)) * a.box : 4 * quad;       // this lane's first row
@@ -546,19 +551,40 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       for (int si = 0; si < nseg && ok; ++si) {
         const TreeSeg &s = segs[si];
         const int n = s.u1 - s.u0;
+        const int *table = a.table + (long long)s.b * a.max_pages;
         auto seen = [&](int j) { return j < s.len && (j >= s.lo || j < a.sinks); };
         auto page_at = [&](int j) { return a.page_shift >= 0 ? j >> a.page_shift : j / a.page; };
+        auto page_ok = [&](int pid) {
+          if ((unsigned)pid < (unsigned)a.npages) return true;
+          if (pid != -2) atomicCAS(a.err, 0, -9);
+          return false;
+        };
+        // Boxes: a window of 64 entries of the page table, 32 of them ahead of their use.
+        int wbase = -64, win = 0, ahead = 0;
+        auto entry = [&](int e) { return e + lane < a.max_pages ? __ldg(table + e + lane) : 0; };
         // the pages of the lane's rows of tile i (a box: of all of them), -2 where none is needed
         auto pages_of = [&](int i, int (&pid)[4]) {
-          const int j = tree_base(s, s.u0 + i) + first;
-          const int *t = a.table + (long long)s.b * a.max_pages;
+          const int base = tree_base(s, s.u0 + i), j = base + first;
           if (a.box) {
-            pid[0] = j < s.len && (j + a.box > s.lo || j < a.sinks) ? __ldg(t + page_at(j)) : -2;
+            const int e0 = page_at(base);         // (the tile's first; it has at most 8)
+            if (e0 - wbase >= 64 || e0 < wbase) {
+              wbase = e0;
+              win = entry(wbase);
+              ahead = entry(wbase + 32);
+            } else if (e0 - wbase >= 32) {
+              wbase += 32;
+              win = ahead;
+              ahead = entry(wbase + 32);
+            }
+            const int at = page_at(j) - wbase;
+            const int p0 = __shfl_sync(0xffffffffu, win, at & 31);
+            const int p1 = __any_sync(0xffffffffu, at >= 32) ? __shfl_sync(0xffffffffu, ahead, at & 31) : 0;
+            pid[0] = j < s.len && (j + a.box > s.lo || j < a.sinks) ? (at < 32 ? p0 : p1) : -2;
           } else {
             int pi = page_at(j), r = j - pi * a.page;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              pid[e] = seen(j + e) ? __ldg(t + pi) : -2;
+              pid[e] = seen(j + e) ? __ldg(table + pi) : -2;
               if (++r == a.page) {
                 r = 0;
                 ++pi;
@@ -566,111 +592,90 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
           }
         };
-        auto page_ok = [&](int pid) {
-          if ((unsigned)pid < (unsigned)a.npages) return true;
-          if (pid != -2) atomicCAS(a.err, 0, -9);
-          return false;
-        };
-        // copies the lane's part of tile i to the ring's next stage
-        auto copy = [&](const void *boxmap, const void *rowmap, int i, const int (&pid)[4]) {
-          const int slot = stage % kRing;
-          if (stage >= kRing) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((stage / kRing - 1) & 1)));
-          if (!ok) return;
+        int pid[4];
+        pages_of(0, pid);
+        for (int i = 0; i < n && ok; ++i) {
+          const int st = stage + (isv ? tree_v_stage(i, n) : tree_k_stage(i)), slot = st % kRing;
+          if (st >= kRing) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((st / kRing - 1) & 1)));
+          if (!ok) break;
+          if (lane == slot) last = st;
           const uint32_t bar = kI8 ? raw_full(slot) : full(slot);
-          const uint32_t dst = (kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage) + first * (kI8 ? D : 128);
+          const uint32_t dst = (kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage) + first * kRowBytes;
           const int j = tree_base(s, s.u0 + i) + first;
           const int r0 = j - page_at(j) * a.page;
-          constexpr int kRowBytes = kI8 ? D : 128;
           // boxes that no node sees a row of stay what they are: their keys are masked
           const bool on = chunk < CW && (!a.box || pid[0] != -2);
-          const unsigned parts = __ballot_sync(0xffffffffu, on);
-          if (lane == 0) mbar_arrive_expect_tx(bar, a.box ? __popc(parts) * a.box * kRowBytes : kI8 ? Sh::kRaw : Sh::kStage);
+          const bool page = on && (!a.box || page_ok(pid[0]));
+          const int parts = __popc(__ballot_sync(0xffffffffu, on)), pages = __popc(__ballot_sync(0xffffffffu, page));
+          if (lane == 0)                          // (int8: the tile's scales come with its K)
+            mbar_arrive_expect_tx(bar, (a.box ? parts * a.box * kRowBytes : kI8 ? Sh::kRaw : Sh::kStage) + (kI8 && !isv && a.scale_boxes ? pages * a.box * 8 : 0));
           __syncwarp();
-          if (!on) return;
-          if (a.box && page_ok(pid[0])) {
+          if (a.box && page) {
             tma_load_4d(dst + (kI8 ? 0 : chunk * (kTreeKeys * 128)), boxmap, 64 * (kI8 ? 0 : chunk), r0, s.g, pid[0], bar);
-            return;
-          }
-          for (int q = 0; q < nrows; q += 4) {    // (a box of a page that is none: zeros)
-            int row[4];
-            int r = r0 + q;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              row[e] = !a.box && seen(j + e) && page_ok(pid[e]) ? pid[e] * a.page_rows + s.g * a.head_rows + r * a.tok_rows : -1;
-              if (++r == a.page) r = 0;
+            if (kI8 && !isv && a.scale_boxes) {
+              const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + first;
+              const long long from = ((long long)pid[0] * a.Hkv + s.g) * a.page + r0;
+              bulk_g2s_nohint(smem_u32(ksc + to), a.ks + from, a.box * 4, bar);
+              bulk_g2s_nohint(smem_u32(vsc + to), a.vs + from, a.box * 4, bar);
             }
-            for (int c = chunk; c < CW; c += a.box ? CW : 2)
-              tma_gather4(dst + q * kRowBytes + (kI8 ? 0 : c * (kTreeKeys * 128)), rowmap, kI8 ? 0 : 64 * c, row, bar);
+          } else if (on) {
+            for (int q = 0; q < nrows; q += 4) {  // (a box of a page that is none: zeros)
+              int row[4];
+              int r = r0 + q;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                row[e] = !a.box && seen(j + e) && page_ok(pid[e]) ? pid[e] * a.page_rows + s.g * a.head_rows + r * a.tok_rows : -1;
+                if (++r == a.page) r = 0;
+              }
+              for (int c = chunk; c < CW; c += a.box ? CW : 2)
+                tma_gather4(dst + q * kRowBytes + (kI8 ? 0 : c * (kTreeKeys * 128)), rowmap, kI8 ? 0 : 64 * c, row, bar);
+            }
           }
-        };
-        // the page table, far ahead of its use: lines of 32 entries from tile i on
-        auto fetch_ahead = [&](int i, int line) {
-          const int j = tree_base(s, s.u0 + min(i, n - 1)), pi = page_at(j) + 32 * line;
-          if (pi <= page_at(max(s.len - 1, 0)) && pi < a.max_pages) prefetch_l1(a.table + (long long)s.b * a.max_pages + pi);
-        };
-        fetch_ahead(0, lane);
-        int pid[4], vpid[4];
-        pages_of(0, pid);
-        for (int i = 0; i <= n && ok; ++i) {
-          int kpid[4];
+          if (kI8 && !a.scale_boxes) {            // row by row: lanes 0 .. 15 K's scales, the others V's
+            const int other = __shfl_sync(0xffffffffu, pid[0], a.box ? 4 * quad / a.box : 0);
+            if (!isv) {
+              const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + 4 * quad, j4 = tree_base(s, s.u0 + i) + 4 * quad;
+              const float *from = lane < 16 ? a.ks : a.vs;
+              int r = j4 - page_at(j4) * a.page;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) kpid[e] = pid[e];
-          if (i < n) {
-            if (i + 1 < n) pages_of(i + 1, pid);
-            if (lane < 2) fetch_ahead(i + 16, lane);
-            copy(&a.kbox, &a.kmap, i, kpid);
-            if constexpr (kI8) {                  // the tile's scales come with its K: lanes 0 .. 15 K's, the others V's
-              const int other = __shfl_sync(0xffffffffu, kpid[0], a.box ? 4 * quad / a.box : 0);
-              if (ok) {
-                const int slot = (tiles + i) % Sh::kScaleSlots, j = tree_base(s, s.u0 + i) + 4 * quad;
-                const float *from = lane < 16 ? a.ks : a.vs;
-                float *to = (lane < 16 ? ksc : vsc) + slot * kTreeKeys + 4 * quad;
-                int r = j - page_at(j) * a.page;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int p = a.box ? other : kpid[e];
-                  const bool on = seen(j + e) && (unsigned)p < (unsigned)a.npages;
-                  cp_async4_zfill(smem_u32(to + e), from + (on ? ((long long)p * a.Hkv + s.g) * a.page + r : 0), on ? 4u : 0u);
-                  if (++r == a.page) r = 0;
-                }
-                cp_async_arrive(raw_full(stage % kRing));
+              for (int e = 0; e < 4; ++e) {
+                const int p = a.box ? other : pid[e];
+                const bool here = seen(j4 + e) && (unsigned)p < (unsigned)a.npages;
+                cp_async4_zfill(smem_u32((lane < 16 ? ksc : vsc) + to + e), from + (here ? ((long long)p * a.Hkv + s.g) * a.page + r : 0), here ? 4u : 0u);
+                if (++r == a.page) r = 0;
               }
             }
-            ++stage;
+            cp_async_arrive(bar);
           }
-          if (i == 0 && ok) {
-            // Q: row r is column rb * 128 + r of the KV head: node column / G, head column % G
-            if (nsegs + si > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((nsegs + si - 1) & 1)));
-            if (ok) {
-              if (a.G <= kTreeRows) {             // whole nodes: one box (rows beyond the sequence's are never written)
-                if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
-                __syncwarp();
-                if (lane < D / 64)
-                  tma_load_4d(q_s + lane * (kTreeRows * 128), &a.qbox, 64 * lane, 0, s.g, s.tok0 + s.rb * (a.block_rows / a.G), q_full);
-              } else {
-                if (lane == 0) mbar_arrive_expect_tx(q_full, Sh::kQ);
-                __syncwarp();
-                int row[4];
-                const int cols = s.nodes * a.G;
+          if (i + 1 < n) pages_of(i + 1, pid);
+          if (i == 0 && !isv) {
+            // Q: row r is column rb * block_rows + r of the KV head: node column / G, head column % G
+            const int seg = nsegs + si;
+            if (seg > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((seg - 1) & 1)));
+            if (!ok) break;
+            if (a.G <= kTreeRows) {               // whole nodes: one box (rows beyond the sequence's are never written)
+              if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
+              __syncwarp();
+              if (lane < D / 64)
+                tma_load_4d(q_s + lane * (kTreeRows * 128), &a.qbox, 64 * lane, 0, s.g, s.tok0 + s.rb * (a.block_rows / a.G), q_full);
+            } else {
+              if (lane == 0) mbar_arrive_expect_tx(q_full, Sh::kQ);
+              __syncwarp();
+              int row[4];
+              const int cols = s.nodes * a.G;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int col = s.rb * kTreeRows + 4 * lane + e, node = col / a.G;
-                  row[e] = col < cols ? (s.tok0 + node) * a.q_tok_rows + (s.g * a.G + col - node * a.G) * a.q_head_rows : -1;
-                }
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) tma_gather4(q_s + c * (kTreeRows * 128) + lane * 512, &a.qmap, 64 * c, row, q_full);
+              for (int e = 0; e < 4; ++e) {
+                const int col = s.rb * kTreeRows + 4 * lane + e, node = col / a.G;
+                row[e] = col < cols ? (s.tok0 + node) * a.q_tok_rows + (s.g * a.G + col - node * a.G) * a.q_head_rows : -1;
               }
-            }
-          }
-          if (i > 0 && ok) {
-            copy(&a.vbox, &a.vmap, i - 1, vpid);
-            if (kI8 && ok) cp_async_arrive(raw_full(stage % kRing));
-            ++stage;
-          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vpid[e] = kpid[e];
+              for (int c = 0; c < D / 64; ++c) tma_gather4(q_s + c * (kTreeRows * 128) + lane * 512, &a.qmap, 64 * c, row, q_full);
+            }
+            queries = seg + 1;
+          }
         }
         tiles += n;
+        stage += 2 * n;
       }
     } else if (kI8 && warp >= Sh::kWiden0) {
       // ----------------------------------------------------------- widening --
@@ -1070,12 +1075,12 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   }
 
   // what was started ends before the CTA does
-  if (warp == Sh::kLoadWarp) {
-    constexpr int kRing = kI8 ? Sh::kRaws : F;
+  // (the MMAs have waited for all copies, unless a wait gave up)
+  if ((warp == Sh::kLoadWarp || warp == Sh::kLoadWarp + 1) && wctl->abort) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int st = max(stage - kRing, 0); st < stage && lane == 0; ++st)
-      mbar_drain(kI8 ? raw_full(st % kRing) : full(st % kRing), (uint32_t)((st / kRing) & 1), wctl);
-    if (nsegs > 0 && lane == 0) mbar_drain(q_full, (uint32_t)((nsegs - 1) & 1), wctl);
+    constexpr int kRing = kI8 ? Sh::kRaws : F;
+    if (last >= 0) mbar_drain(kI8 ? raw_full(lane) : full(lane), (uint32_t)((last / kRing) & 1), wctl);
+    if (lane == 0 && queries > 0) mbar_drain(q_full, (uint32_t)((queries - 1) & 1), wctl);
   }
   if (warp == Sh::kMmaWarp) {
     const uint32_t leader = elect_leader();

@@ -522,6 +522,7 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
     if ((rc = encode_page_map(&a.kbox, c->k, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
     if ((rc = encode_page_map(&a.vbox, c->v, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
   }
+  a.scale_boxes = i8 && a.box && at(c->k_scale, 16) && at(c->v_scale, 16);
   const int G = Hq / c->Hkv;
   a.block_rows = G <= 128 ? 128 / G * G : 128;
   if (G <= 128) {

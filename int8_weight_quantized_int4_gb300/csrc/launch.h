@@ -148,6 +148,7 @@ struct TreeArgs {
   CUtensorMap kbox, vbox;       // [pages][Hkv][page][d], boxes of 64 elements (int8: d) and `box` rows
   int box;                      // 0: the pages are no multiple of 8 rows
   CUtensorMap qbox;             // [T][Hkv][G][d], boxes of 64 elements and block_rows rows (G <= 128)
+  int scale_boxes;              // int8: a box's scales are a multiple of 16 bytes, so aligned
   int block_rows;               // rows of an item: whole nodes, up to 128
   uint16_t *out;                // as PagedArgs
   float *lse;
