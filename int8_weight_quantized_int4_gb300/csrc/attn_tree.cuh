@@ -125,6 +125,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// mbar_wait without a call: one would keep a role's values in memory around it.
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile WaitBlock *w, bool no_limit) {
+  if (no_limit ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (w->abort) return false;
+    if (globaltimer_ns() - t0 >= w->limit_ns) {
+      w->abort = 1;
+      atomicCAS(w->err, 0, -7);
+      return false;
+    }
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+  }
+}
+
 __device__ __forceinline__ float tree_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -242,7 +257,7 @@ __device__ __forceinline__ long long tree_places(const TreeArgs &a, const TreeSp
 
 // Lists the range's next segments (one thread).
 template <int IC>
-__device__ __forceinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
+__device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
   int n = 0, b = ctl->b;
   long long off = ctl->off, pos = ctl->pos;
   const int R = ctl->size;
@@ -291,7 +306,7 @@ __device__ __forceinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, Tree
 
 // This CTA's team and range, and its first segments.  All threads.
 template <int IC, int NW>
-__device__ __forceinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
+__device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
   constexpr int NT = 32 * NW;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + NT - 1) / NT;
@@ -395,17 +410,17 @@ __device__ __forceinline__ unsigned long long tree_bits(int a, int b) {
 __device__ __forceinline__ uint32_t tree_chunk(uint32_t stage, int r, int c) {
   return stage + (c >> 3) * (kTreeKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
   tmem_wait_ld();
-  return __uint_as_float(r);
+  return r;
 }
 // O += p v for the keys of `found`, in the rows that see them; then their values are cleared.
 // The softmax warps, each group half of the channels; fresh: O holds nothing yet.
 template <int D, bool BF>
-__device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t vst, unsigned long long found,
-                                          unsigned long long vis, float scale, float m, bool fresh) {
+__device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t weights, uint32_t vst, unsigned long long found,
+                                          unsigned long long vis, bool fresh) {
   const int c0 = (int)(threadIdx.x >> 7) * (D / 2);
 #pragma unroll 1
   for (int cc = c0; cc < c0 + D / 2; cc += 32) {
@@ -421,7 +436,9 @@ __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t scores, uint32_t 
     for (unsigned long long k = found; k; k &= k - 1) {
       const int j = __ffsll((long long)k) - 1;
       if (!__any_sync(0xffffffffu, (vis >> j & 1) != 0)) continue;
-      const float p = tree_ex2(tmem_ld1(scores + j) * scale - m);
+      const uint32_t at = weights + (j & ~15) + (j & 15) / 2;     // its two terms
+      const float2 hi = tree_unpack<BF>(tmem_ld1(at)), lw = tree_unpack<BF>(tmem_ld1(at + 8));
+      const float p = j & 1 ? hi.y + lw.y : hi.x + lw.x;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t w[4];
@@ -485,7 +502,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   auto p_full = [&](int b) { return bars + 8u * (34 + b); };
   const uint32_t q_full = bars + 8 * 36, q_empty = bars + 8 * 37, o_step = bars + 8 * 38, o_done = bars + 8 * 39, o_free = bars + 8 * 40,
                  drain = bars + 8 * 41;
-  auto pwait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, wctl, a.wait_ns == 0); };
+  auto pwait = [&](uint32_t bar, uint32_t parity) { return tree_wait(bar, parity, wctl, a.wait_ns == 0); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -765,7 +782,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
 #pragma unroll
               for (int term = 0; term < 2; ++term)
-                mma_f16_ts_w(leader, tmem, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys + (kk >> 1) * 32 + term * 16 + (kk & 1) * 8),
+                mma_f16_ts_w(leader, tmem, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys + kk * 16 + term * 8),
                              smem_desc_sw128_mn(vs + kk * 2048), kIdO, (kk > 0 || term > 0) ? 1u : more);
             }
             mma_commit_w(leader, empty(slot));
@@ -849,41 +866,43 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           tc_fence_after();
           const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys + 32 * grp);
           const int sc = (gt % Sh::kScaleSlots) * kTreeKeys + 32 * grp;
-          F2 x[16];
-          float top = -INFINITY;
-          if (busy) {
-            uint32_t v[32];
-            tmem_ld32(sadr, v);
+          // 16 scores of the row; int8: log2 of the weight times its value's scale
+          auto scores = [&](int c0, F2 (&x)[8]) {
+            uint32_t v[16];
+            tmem_ld16(sadr + (uint32_t)c0, v);
             tmem_wait_ld();
-            if constexpr (kI8) {                  // log2 of the weight times its value's scale
-#pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 k = *reinterpret_cast<const float4 *>(ksc + sc + c), e = *reinterpret_cast<const float4 *>(vlog + sc + c);
-                x[c / 2] = fma2(F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), F2(k.x, k.y), F2(e.x, e.y));
-                x[c / 2 + 1] = fma2(F2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), F2(k.z, k.w), F2(e.z, e.w));
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            }
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                float p, r;
-                x[c / 2].get(p, r);
-                x[c / 2] = F2(vm >> c & 1 ? p : -INFINITY, vm >> (c + 1) & 1 ? r : -INFINITY);
-              }
-            }
-            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              float p, r;
-              x[c].get(p, r);
-              t0 = max3(t0, p, r);
-              x[c + 1].get(p, r);
-              t1 = max3(t1, p, r);
+              x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+              if constexpr (kI8) x[c / 2] = fma2(x[c / 2], *reinterpret_cast<const F2 *>(ksc + sc + c0 + c), *reinterpret_cast<const F2 *>(vlog + sc + c0 + c));
             }
-            top = fmaxf(t0, t1);
+          };
+          float top = -INFINITY;
+          if (busy) {
+#pragma unroll
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+              F2 x[8];
+              scores(c0, x);
+              float t0 = -INFINITY, t1 = -INFINITY;
+              if (masked) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  float p, r;
+                  x[c].get(p, r);
+                  t0 = max3(t0, vm >> (c0 + 2 * c) & 1 ? p : -INFINITY, vm >> (c0 + 2 * c + 1) & 1 ? r : -INFINITY);
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                  float p, r;
+                  x[c].get(p, r);
+                  t0 = max3(t0, p, r);
+                  x[c + 1].get(p, r);
+                  t1 = max3(t1, p, r);
+                }
+              }
+              top = max3(top, t0, t1);
+            }
             if (!kI8) top = top == -INFINITY ? top : top * scale;
           }
           // The reference moves only when a score passes it by 2^kPass (both groups decide together);
@@ -917,6 +936,54 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               tmem_wait_st();
             }
           }
+          // the weights of 16 keys over their scores: 8 columns of rounded pairs, 8 of what they leave
+          auto weights = [&](auto partly) {
+            const F2 sc2(scale, scale), neg(-m_ref, -m_ref), minus(-1.0f, -1.0f);
+            F2 sum(0.0f, 0.0f);
+#pragma unroll
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+              uint32_t hi[8], lw[8];
+              F2 x[8];
+              scores(c0, x);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
+                float p, r;
+                w.get(p, r);
+                w = F2(tree_ex2(p), tree_ex2(r));
+                if constexpr (kI8) {
+                  w = mul2(w, *reinterpret_cast<const F2 *>(vinv + sc + c0 + 2 * c));
+                  if constexpr (decltype(partly)::value) {
+                    w.get(p, r);
+                    w = F2(vm >> (c0 + 2 * c) & 1 ? p : 0.0f, vm >> (c0 + 2 * c + 1) & 1 ? r : 0.0f);
+                  }
+                  sum = add2(sum, w);
+                  w = mul2(w, *reinterpret_cast<const F2 *>(vsc + sc + c0 + 2 * c));
+                }
+                w.get(p, r);
+                if constexpr (decltype(partly)::value) {      // (hidden: also with scores or scales that are not finite)
+                  p = vm >> (c0 + 2 * c) & 1 ? p : 0.0f;
+                  r = vm >> (c0 + 2 * c + 1) & 1 ? r : 0.0f;
+                  w = F2(p, r);
+                }
+                if constexpr (!kI8) sum = add2(sum, w);
+                hi[c] = tree_pack<kBf>(p, r);
+                const float2 h = tree_unpack<kBf>(hi[c]);
+                fma2(F2(h.x, h.y), minus, w).get(p, r);
+                lw[c] = tree_pack<kBf>(p, r);
+              }
+              tmem_st8(sadr + (uint32_t)c0, hi);
+              tmem_st8(sadr + (uint32_t)c0 + 8u, lw);
+            }
+            float p, r;
+            sum.get(p, r);
+            l += p + r;
+            tmem_wait_st();
+          };
+          if (busy) {
+            if (masked) weights(std::true_type{});
+            else weights(std::false_type{});
+          }
           if constexpr (!kI8) {
             // A value that is not finite would reach the rows that do not see its key (0 times it is NaN),
             // so tiles seen partly are searched for such keys.  They are added here, to the rows
@@ -947,52 +1014,10 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
                   aborted = true;
                   break;
                 }
-                tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, scale, m_ref, i == 0);
+                tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0);
                 if (threadIdx.x == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
-                named_bar_sync(1, ST);            // (all scores have been read)
               }
             }
-          }
-          // the weights: 16 columns of rounded pairs, 16 of what they leave
-          auto weights = [&](auto partly) {
-            uint32_t hi[8], lw[8];
-            F2 sum(0.0f, 0.0f);
-            const F2 sc2(scale, scale), neg(-m_ref, -m_ref), minus(-1.0f, -1.0f);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
-              float p, r;
-              w.get(p, r);
-              w = F2(tree_ex2(p), tree_ex2(r));
-              if constexpr (kI8) {
-                w = mul2(w, *reinterpret_cast<const F2 *>(vinv + sc + 2 * c));
-                sum = add2(sum, w);
-                w = mul2(w, *reinterpret_cast<const F2 *>(vsc + sc + 2 * c));
-              }
-              w.get(p, r);
-              if constexpr (decltype(partly)::value) {      // (hidden: also with scores or scales that are not finite)
-                p = vm >> (2 * c) & 1 ? p : 0.0f;
-                r = vm >> (2 * c + 1) & 1 ? r : 0.0f;
-                w = F2(p, r);
-              }
-              if constexpr (!kI8) sum = add2(sum, w);
-              hi[c & 7] = tree_pack<kBf>(p, r);
-              const float2 h = tree_unpack<kBf>(hi[c & 7]);
-              fma2(F2(h.x, h.y), minus, w).get(p, r);
-              lw[c & 7] = tree_pack<kBf>(p, r);
-              if ((c & 7) == 7) {
-                tmem_st8(sadr + (uint32_t)(c - 7), hi);
-                tmem_st8(sadr + (uint32_t)(c + 9), lw);
-              }
-            }
-            float p, r;
-            sum.get(p, r);
-            l += p + r;
-            tmem_wait_st();
-          };
-          if (busy) {
-            if (masked) weights(std::true_type{});
-            else weights(std::false_type{});
           }
           tc_fence_before();
           __syncwarp();
