@@ -74,7 +74,8 @@ template <int D, int KV>
 struct TreeShape {
   static constexpr bool kI8 = KV == kPagedI8;
   static constexpr int kWideners = !kI8 ? 0 : D == 256 ? 4 : 2;
-  static constexpr int kMmaWarp = 8, kLoadWarp = 9, kWiden0 = 11;   // loading: K and Q, V
+  static constexpr int kLoaders = D == 256 ? 2 : 1;       // two: one for K and Q, one for V
+  static constexpr int kMmaWarp = 8, kLoadWarp = 9, kWiden0 = kLoadWarp + kLoaders;
   static constexpr int kWarps = kWiden0 + kWideners;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
@@ -249,6 +250,10 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs &a, const TreeSeq &
   p.blocks = (int)(((long long)s.nodes * a.G + a.block_rows - 1) / a.block_rows);
   return p;
 }
+// a / b, 0 <= a, 0 < b: of 32 bits where they are (a third of the latency)
+__device__ __forceinline__ long long tree_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 // places of a sequence for teams of R
 template <int IC>
 __device__ __forceinline__ long long tree_places(const TreeArgs &a, const TreeSpan &p, int R) {
@@ -272,7 +277,7 @@ __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl
       continue;
     }
     const int each = p.n + IC, groups = (p.blocks + R - 1) / R;
-    const int item = (int)(off / each), in = (int)(off - (long long)item * each);
+    const int item = (int)tree_div(off, each), in = (int)(off - (long long)item * each);
     const long long at = pos - in;                // the item's first place
     const int g = item / groups, rb = (item - g * groups) * R + ctl->member;
     const long long x0 = ctl->begin - at - IC, x1 = ctl->end - at - IC;
@@ -292,7 +297,7 @@ __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl
       q.tok0 = s.tok0;
       q.nodes = s.nodes;
       q.slot = u0 == 0 && u1 == p.n ? -1 : u0 > 0 ? 0 : 1;
-      q.parts = (int)((at + IC + p.n - 1) / ctl->share - (at + IC) / ctl->share) + 1;
+      q.parts = q.slot != 1 ? 0 : (int)(tree_div(at + IC + p.n - 1, ctl->share) - tree_div(at + IC, ctl->share)) + 1;
     }
     pos += each - in;
     off += each - in;
@@ -347,11 +352,12 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   // sequence has fewer blocks idle.  Compared: the tiles a CTA runs, times what a tile costs that
   // is read for one row block alone (3) or for several (2; the MMAs bound it then).
   int R = 1;
-  long long best = total[0] / gridDim.x * 3;
+  long long best = tree_div(total[0], gridDim.x) * 3;
 #pragma unroll
   for (int k = 1; k < kTreeMaxTeam; ++k) {
-    const long long cost = total[k] / max((int)gridDim.x / (k + 1), 1) * 2;
-    if (total[k] < total[0] && (int)gridDim.x >= k + 1 && cost < best) {
+    if (total[k] == total[0] || (int)gridDim.x < k + 1) continue;
+    const long long cost = tree_div(total[k], (int)gridDim.x / (k + 1)) * 2;
+    if (cost < best) {
       best = cost;
       R = k + 1;
     }
@@ -367,7 +373,7 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   }
   const int teams = (int)gridDim.x / R;
   const int team = (int)blockIdx.x / R;
-  long long share = (W + teams - 1) / teams;
+  long long share = tree_div(W + teams - 1, teams);
   share = max(share, (long long)a.min_tiles + IC);
   const long long begin = team < teams ? min((long long)team * share, W) : W, end = min(begin + share, W);
   if (begin < end && start <= begin && begin < start + mine) {      // one thread
@@ -549,17 +555,17 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 
   for (;;) {
     const int nseg = ctl->nseg;
-    if (warp == Sh::kLoadWarp || warp == Sh::kLoadWarp + 1) {
+    if (warp >= Sh::kLoadWarp && warp < Sh::kWiden0) {
       // ------------------------------------------------------------ loading --
       // Pages of whole boxes (8 to 64 rows, a.box): box b of a tile is rows box * (b % boxes) .. of 128
       // bytes b / boxes (int8: of whole rows), and lane b's.  Other pages: a tile's 64 rows are sixteen gathers of four rows, and as many
       // for each 128 bytes; lane l finds the rows of quad l % 16.
-      // One warp loads K and Q, the other V (a box holds its warp about 70 cycles).
+      // A box holds its warp about 70 cycles, so where a tile has most of them one warp loads K and
+      // Q and the other V.
       constexpr int CW = kI8 ? 1 : D / 64;                        // boxes or gathers side by side
       constexpr int kRing = kI8 ? Sh::kRaws : F;
       constexpr int kRowBytes = kI8 ? D : 128;
-      const bool isv = warp != Sh::kLoadWarp;
-      const void *boxmap = isv ? &a.vbox : &a.kbox, *rowmap = isv ? &a.vmap : &a.kmap;
+      const int role = Sh::kLoaders == 2 ? warp - Sh::kLoadWarp : 2;      // 0: K and Q, 1: V, 2: all
       const int quad = lane & 15;
       const int boxes = a.box ? kTreeKeys / a.box : 16;           // down a tile; a power of two
       const int first = a.box ? (lane & (boxes - 1)) * a.box : 4 * quad;       // this lane's first row
@@ -609,10 +615,29 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
           }
         };
-        int pid[4];
-        pages_of(0, pid);
-        for (int i = 0; i < n && ok; ++i) {
-          const int st = stage + (isv ? tree_v_stage(i, n) : tree_k_stage(i)), slot = st % kRing;
+        int pid[4], vpid[4];
+        if (role != 2) pages_of(0, pid);
+        // stages in their order: K0 K1 V0 K2 V1 ..
+        for (int x = 0; x < 2 * n && ok; ++x) {
+          const bool isv = n == 1 ? x == 1 : x == 2 * n - 1 || (x >= 2 && !(x & 1));
+          if (role != 2 && isv != (role == 1)) continue;
+          const int i = isv ? (x == 2 * n - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2;
+          if (role == 2) {                        // (V of a tile comes after K of the next)
+            if (!isv) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) vpid[e] = pid[e];
+              pages_of(i, pid);
+            } else if (i < n - 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int t = pid[e];
+                pid[e] = vpid[e];
+                vpid[e] = t;
+              }
+            }
+          }
+          const void *boxmap = isv ? &a.vbox : &a.kbox, *rowmap = isv ? &a.vmap : &a.kmap;
+          const int st = stage + x, slot = st % kRing;
           if (st >= kRing) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((st / kRing - 1) & 1)));
           if (!ok) break;
           if (lane == slot) last = st;
@@ -664,13 +689,18 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             cp_async_arrive(bar);
           }
-          if (i + 1 < n) pages_of(i + 1, pid);
-          if (i == 0 && !isv) {
+          if (role != 2) {
+            if (i + 1 < n) pages_of(i + 1, pid);
+          } else if (isv && i < n - 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pid[e] = vpid[e];
+          }
+          if (x == 0) {
             // Q: row r is column rb * block_rows + r of the KV head: node column / G, head column % G
             const int seg = nsegs + si;
             if (seg > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((seg - 1) & 1)));
             if (!ok) break;
-            if (a.G <= kTreeRows) {               // whole nodes: one box (rows beyond the sequence's are never written)
+            if (a.q_box) {                        // whole nodes: one box (rows beyond the sequence's are never written)
               if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
               __syncwarp();
               if (lane < D / 64)
@@ -866,13 +896,17 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           tc_fence_after();
           const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys + 32 * grp);
           const int sc = (gt % Sh::kScaleSlots) * kTreeKeys + 32 * grp;
-          // 16 scores of the row; int8: log2 of the weight times its value's scale
-          auto scores = [&](int c0, F2 (&x)[8]) {
-            uint32_t v[16];
-            tmem_ld16(sadr + (uint32_t)c0, v);
+          // Scores from c0 on; int8: log2 of the weight times its value's scale.  Up to d = 128 (two CTAs an
+          // SM) they are read twice, 16 at a time: 32 would not fit the registers.
+          constexpr int NX = D == 256 ? 32 : 16;
+          F2 x[NX / 2];
+          auto scores = [&](int c0) {
+            uint32_t v[NX];
+            if constexpr (NX == 32) tmem_ld32(sadr, v);
+            else tmem_ld16(sadr + (uint32_t)c0, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
+            for (int c = 0; c < NX; c += 2) {
               x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
               if constexpr (kI8) x[c / 2] = fma2(x[c / 2], *reinterpret_cast<const F2 *>(ksc + sc + c0 + c), *reinterpret_cast<const F2 *>(vlog + sc + c0 + c));
             }
@@ -880,20 +914,19 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           float top = -INFINITY;
           if (busy) {
 #pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += 16) {
-              F2 x[8];
-              scores(c0, x);
+            for (int c0 = 0; c0 < 32; c0 += NX) {
+              scores(c0);
               float t0 = -INFINITY, t1 = -INFINITY;
               if (masked) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < NX / 2; ++c) {
                   float p, r;
                   x[c].get(p, r);
                   t0 = max3(t0, vm >> (c0 + 2 * c) & 1 ? p : -INFINITY, vm >> (c0 + 2 * c + 1) & 1 ? r : -INFINITY);
                 }
               } else {
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
+                for (int c = 0; c < NX / 2; c += 2) {
                   float p, r;
                   x[c].get(p, r);
                   t0 = max3(t0, p, r);
@@ -905,15 +938,12 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             if (!kI8) top = top == -INFINITY ? top : top * scale;
           }
-          // The reference moves only when a score passes it by 2^kPass (both groups decide together);
+          // The reference moves only when a score passes it by 2^kPass (both warps of a row decide together);
           // then O and l are rescaled, once the previous P V is done.
           stop = stop || wctl->abort;
-          if (named_bar_or(1, ST, stop || top > m_ref + kPass)) {
+          if (named_bar_or(2 + (warp & 3), 64, stop || top > m_ref + kPass)) {
             xch[grp * kTreeRows + row] = top;
-            if (named_bar_or(1, ST, stop)) {
-              aborted = true;
-              break;
-            }
+            named_bar_sync(2 + (warp & 3), 64);
             top = fmaxf(top, xch[(grp ^ 1) * kTreeRows + row]);
             float f = 1.0f;
             if (top > m_ref + kPass) {
@@ -943,11 +973,11 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 #pragma unroll
             for (int c0 = 0; c0 < 32; c0 += 16) {
               uint32_t hi[8], lw[8];
-              F2 x[8];
-              scores(c0, x);
+              if constexpr (NX == 16) scores(c0);
+              const int x0 = NX == 16 ? 0 : c0 / 2;
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
+                F2 w = kI8 ? add2(x[x0 + c], neg) : fma2(x[x0 + c], sc2, neg);
                 float p, r;
                 w.get(p, r);
                 w = F2(tree_ex2(p), tree_ex2(r));
@@ -1010,11 +1040,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               if (found) {
                 stop = stop || !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
                 tc_fence_after();
-                if (named_bar_or(1, ST, stop)) {
-                  aborted = true;
-                  break;
-                }
-                tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0);
+                // (after a wait that gave up everyone goes on to the segment's end without waiting)
+                if (!named_bar_or(1, ST, stop)) tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0);
                 if (threadIdx.x == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
               }
             }
@@ -1101,7 +1128,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 
   // what was started ends before the CTA does
   // (the MMAs have waited for all copies, unless a wait gave up)
-  if ((warp == Sh::kLoadWarp || warp == Sh::kLoadWarp + 1) && wctl->abort) {
+  if (warp >= Sh::kLoadWarp && warp < Sh::kWiden0 && wctl->abort) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     constexpr int kRing = kI8 ? Sh::kRaws : F;
     if (last >= 0) mbar_drain(kI8 ? raw_full(lane) : full(lane), (uint32_t)((last / kRing) & 1), wctl);

@@ -524,8 +524,12 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   }
   a.scale_boxes = i8 && a.box && at(c->k_scale, 16) && at(c->v_scale, 16);
   const int G = Hq / c->Hkv;
+  // Row blocks of whole nodes, whose Q is one box (a gather of 128 rows takes 2 to 5 us), unless
+  // that makes more of them than 128 rows of any nodes do, for a sequence of max_nodes.
   a.block_rows = G <= 128 ? 128 / G * G : 128;
-  if (G <= 128) {
+  a.q_box = G <= 128 && (max_nodes * G + a.block_rows - 1) / a.block_rows == (max_nodes * G + 127) / 128;
+  if (!a.q_box) a.block_rows = 128;
+  if (a.q_box) {
     const long long dim[3] = {G, c->Hkv, T};
     const long long stride[3] = {G > 1 ? q_head_stride * 2 : 16, c->Hkv > 1 ? G * q_head_stride * 2 : 16, T > 1 ? q_token_stride * 2 : 16};
     if ((rc = encode_page_map(&a.qbox, q, dim, stride, c->d, G, 128 / G, false, bf))) return rc;

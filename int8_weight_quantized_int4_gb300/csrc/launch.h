@@ -149,7 +149,8 @@ struct TreeArgs {
   int box;                      // 0: the pages are no multiple of 8 rows
   CUtensorMap qbox;             // [T][Hkv][G][d], boxes of 64 elements and block_rows rows (G <= 128)
   int scale_boxes;              // int8: a box's scales are a multiple of 16 bytes, so aligned
-  int block_rows;               // rows of an item: whole nodes, up to 128
+  int block_rows;               // rows of an item: whole nodes (q_box), or 128
+  int q_box;
   uint16_t *out;                // as PagedArgs
   float *lse;
   const float *ks, *vs;
