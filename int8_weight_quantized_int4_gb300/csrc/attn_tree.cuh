@@ -558,38 +558,78 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
     if (warp >= Sh::kLoadWarp && warp < Sh::kWiden0) {
       // ------------------------------------------------------------ loading --
       // Pages of whole boxes (8 to 64 rows, a.box): box b of a tile is rows box * (b % boxes) .. of 128
-      // bytes b / boxes (int8: of whole rows), and lane b's.  Other pages: a tile's 64 rows are sixteen gathers of four rows, and as many
-      // for each 128 bytes; lane l finds the rows of quad l % 16.
-      // A box holds its warp about 70 cycles, so where a tile has most of them one warp loads K and
-      // Q and the other V.
+      // bytes b / boxes (int8: of whole rows), and lane b's.  Other pages: a tile's 64 rows are
+      // sixteen gathers of four rows, and as many for each 128 bytes; lane l finds the rows of quad
+      // l % 16.  A box holds its warp about 70 cycles, so where a tile has most of them one warp
+      // loads K and Q and the other V.  The loop over boxes is kept short: a warp that comes round
+      // once a stage finds its instructions gone from the caches near it (250 of them took 1500
+      // cycles).
       constexpr int CW = kI8 ? 1 : D / 64;                        // boxes or gathers side by side
       constexpr int kRing = kI8 ? Sh::kRaws : F;
       constexpr int kRowBytes = kI8 ? D : 128;
+      constexpr uint32_t kSlotBytes = kI8 ? Sh::kRaw : Sh::kStage;
+      const uint32_t ring = kI8 ? cd_s : st_s, full0 = kI8 ? raw_full(0) : full(0), empty0 = kI8 ? raw_empty(0) : empty(0);
       const int role = Sh::kLoaders == 2 ? warp - Sh::kLoadWarp : 2;      // 0: K and Q, 1: V, 2: all
-      const int quad = lane & 15;
       const int boxes = a.box ? kTreeKeys / a.box : 16;           // down a tile; a power of two
-      const int first = a.box ? (lane & (boxes - 1)) * a.box : 4 * quad;       // this lane's first row
-      const int chunk = lane / boxes;                             // its 128 bytes (box: the only ones)
-      const int nrows = a.box ? a.box : 4;
+      const int chunk = lane / boxes;                             // this lane's 128 bytes (box: the only ones)
+      const int first = a.box ? (lane & (boxes - 1)) * a.box : 4 * (lane & 15);        // its first row
+      const uint32_t mine = (uint32_t)(first * kRowBytes + (a.box && !kI8 ? chunk * (kTreeKeys * 128) : 0));
       for (int si = 0; si < nseg && ok; ++si) {
         const TreeSeg &s = segs[si];
-        const int n = s.u1 - s.u0;
+        const int n = s.u1 - s.u0, seg = nsegs + si;
         const int *table = a.table + (long long)s.b * a.max_pages;
-        auto seen = [&](int j) { return j < s.len && (j >= s.lo || j < a.sinks); };
-        auto page_at = [&](int j) { return a.page_shift >= 0 ? j >> a.page_shift : j / a.page; };
-        auto page_ok = [&](int pid) {
-          if ((unsigned)pid < (unsigned)a.npages) return true;
-          if (pid != -2) atomicCAS(a.err, 0, -9);
-          return false;
+        // waits for stage st's slot; false: give up
+        auto room = [&](int st, int slot) {
+          if (st >= kRing) ok = __all_sync(0xffffffffu, pwait(empty0 + 8u * slot, (uint32_t)((st / kRing - 1) & 1)));
+          if (ok && lane == slot) last = st;
+          return ok;
         };
-        // Boxes: a window of 64 entries of the page table, 32 of them ahead of their use.
-        int wbase = -64, win = 0, ahead = 0;
-        auto entry = [&](int e) { return e + lane < a.max_pages ? __ldg(table + e + lane) : 0; };
-        // the pages of the lane's rows of tile i (a box: of all of them), -2 where none is needed
-        auto pages_of = [&](int i, int (&pid)[4]) {
-          const int base = tree_base(s, s.u0 + i), j = base + first;
-          if (a.box) {
-            const int e0 = page_at(base);         // (the tile's first; it has at most 8)
+        auto queries_in = [&] {
+          // Q: row r is column rb * block_rows + r of the KV head: node column / G, head column % G
+          if (seg > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((seg - 1) & 1)));
+          if (!ok) return;
+          if (a.q_box) {                          // whole nodes: one box (rows beyond the sequence's are never written)
+            if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
+            __syncwarp();
+            if (lane < D / 64)
+              tma_load_4d(q_s + lane * (kTreeRows * 128), &a.qbox, 64 * lane, 0, s.g, s.tok0 + s.rb * (a.block_rows / a.G), q_full);
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(q_full, Sh::kQ);
+            __syncwarp();
+            int row[4];
+            const int cols = s.nodes * a.G;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = s.rb * kTreeRows + 4 * lane + e, node = col / a.G;
+              row[e] = col < cols ? (s.tok0 + node) * a.q_tok_rows + (s.g * a.G + col - node * a.G) * a.q_head_rows : -1;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) tma_gather4(q_s + c * (kTreeRows * 128) + lane * 512, &a.qmap, 64 * c, row, q_full);
+          }
+          queries = seg + 1;
+        };
+        if (a.box) {
+          // Tile t's box of this lane: page table entry pi, row r of it; advanced a tile at a time.
+          // The table comes through a window of 64 entries, 32 ahead of their use.
+          const int dpi = kTreeKeys / a.page, dr = kTreeKeys % a.page;
+          int t = s.u0 - 1, j = 0, pi = 0, r = 0, wbase = -64, win = 0, ahead = 0;
+          auto entry = [&](int e) { return e + lane < a.max_pages ? __ldg(table + e + lane) : 0; };
+          int pid = -2, row = 0, vpid = -2, vrow = 0;             // of the tile whose K, V is next
+          auto next = [&] {
+            ++t;
+            j += kTreeKeys;
+            pi += dpi;
+            r += dr;
+            if (r >= a.page) {
+              r -= a.page;
+              ++pi;
+            }
+            if (t == s.u0 || t == s.nsu) {        // (the windowed tiles follow the sinks')
+              j = tree_base(s, t) + first;
+              pi = j / a.page;
+              r = j - pi * a.page;
+            }
+            const int e0 = __shfl_sync(0xffffffffu, pi, 0);       // the tile's first entry; it has at most 8
             if (e0 - wbase >= 64 || e0 < wbase) {
               wbase = e0;
               win = entry(wbase);
@@ -599,126 +639,106 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               win = ahead;
               ahead = entry(wbase + 32);
             }
-            const int at = page_at(j) - wbase;
-            const int p0 = __shfl_sync(0xffffffffu, win, at & 31);
-            const int p1 = __any_sync(0xffffffffu, at >= 32) ? __shfl_sync(0xffffffffu, ahead, at & 31) : 0;
-            pid[0] = j < s.len && (j + a.box > s.lo || j < a.sinks) ? (at < 32 ? p0 : p1) : -2;
-          } else {
-            int pi = page_at(j), r = j - pi * a.page;
+            const int at = pi - wbase;
+            pid = __shfl_sync(0xffffffffu, win, at & 31);
+            if (__any_sync(0xffffffffu, at >= 32)) {
+              const int p = __shfl_sync(0xffffffffu, ahead, at & 31);
+              pid = at >= 32 ? p : pid;
+            }
+            row = r;
+            // boxes that no node sees a row of stay what they are: their keys are masked
+            if (chunk >= CW || j >= s.len || (j + a.box <= s.lo && j >= a.sinks)) pid = -2;
+          };
+          const int stages = role == 2 ? 2 * n : n;
+#pragma unroll 1
+          for (int x = 0; x < stages; ++x) {      // K0 K1 V0 K2 V1 .., or a role's share of it
+            const bool isv = role == 2 ? x == stages - 1 || (x >= 2 && !(x & 1)) : role == 1;
+            const int st = stage + (role == 2 ? x : role == 1 ? tree_v_stage(x, n) : tree_k_stage(x)), slot = st % kRing;
+            if (role != 2 || !isv) {
+              vpid = pid;
+              vrow = row;
+              next();
+            } else if (x == stages - 1) {
+              vpid = pid;
+              vrow = row;
+            }
+            const int p = role == 2 && isv ? vpid : pid, r0 = role == 2 && isv ? vrow : row;
+            if (!room(st, slot)) break;
+            const uint32_t bar = full0 + 8u * slot, dst = ring + slot * kSlotBytes + mine;
+            const bool page = (unsigned)p < (unsigned)a.npages, on = p != -2;
+            const int parts = __popc(__ballot_sync(0xffffffffu, on)), pages = kI8 ? __popc(__ballot_sync(0xffffffffu, page)) : 0;
+            if (lane == 0)                        // (int8: the tile's scales come with its K)
+              mbar_arrive_expect_tx(bar, parts * a.box * kRowBytes + (kI8 && !isv && a.scale_boxes ? pages * a.box * 8 : 0));
+            __syncwarp();
+            if (page) tma_load_4d(dst, isv ? &a.vbox : &a.kbox, kI8 ? 0 : 64 * chunk, r0, s.g, p, bar);
+            if (on && !page) {                    // a page that is none: zeros
+              atomicCAS(a.err, 0, -9);
+              const int none[4] = {-1, -1, -1, -1};
+              for (int q = 0; q < a.box; q += 4) tma_gather4(dst + q * kRowBytes, isv ? &a.vmap : &a.kmap, 0, none, bar);
+            }
+            if constexpr (kI8) {
+              if (a.scale_boxes) {
+                if (!isv && page) {
+                  const int to = ((tiles + (t - s.u0)) % Sh::kScaleSlots) * kTreeKeys + first;
+                  const long long from = ((long long)p * a.Hkv + s.g) * a.page + r0;
+                  bulk_g2s_nohint(smem_u32(ksc + to), a.ks + from, a.box * 4, bar);
+                  bulk_g2s_nohint(smem_u32(vsc + to), a.vs + from, a.box * 4, bar);
+                }
+              } else {                            // (scales that are not aligned: one by one)
+                for (int q = 0; q < a.box && !isv && on; ++q) {
+                  const int to = ((tiles + (t - s.u0)) % Sh::kScaleSlots) * kTreeKeys + first + q;
+                  const long long from = page ? ((long long)p * a.Hkv + s.g) * a.page + r0 + q : 0;
+                  cp_async4_zfill(smem_u32(ksc + to), a.ks + from, page ? 4u : 0u);
+                  cp_async4_zfill(smem_u32(vsc + to), a.vs + from, page ? 4u : 0u);
+                }
+                cp_async_arrive(bar);
+              }
+            }
+            if (x == 0 && role != 1) queries_in();
+          }
+        } else {
+          const int quad = lane & 15;
+          auto seen = [&](int j) { return j < s.len && (j >= s.lo || j < a.sinks); };
+#pragma unroll 1
+          for (int x = 0; x < 2 * n; ++x) {
+            const bool isv = x == 2 * n - 1 || (x >= 2 && !(x & 1));
+            if (role != 2 && isv != (role == 1)) continue;
+            const int i = isv ? (x == 2 * n - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2, st = stage + x, slot = st % kRing;
+            const int j = tree_base(s, s.u0 + i) + 4 * quad;
+            int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page, r = j - pi * a.page;
+            int row[4], pid[4], at[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               pid[e] = seen(j + e) ? __ldg(table + pi) : -2;
+              at[e] = r;
               if (++r == a.page) {
                 r = 0;
                 ++pi;
               }
             }
-          }
-        };
-        int pid[4], vpid[4];
-        if (role != 2) pages_of(0, pid);
-        // stages in their order: K0 K1 V0 K2 V1 ..
-        for (int x = 0; x < 2 * n && ok; ++x) {
-          const bool isv = n == 1 ? x == 1 : x == 2 * n - 1 || (x >= 2 && !(x & 1));
-          if (role != 2 && isv != (role == 1)) continue;
-          const int i = isv ? (x == 2 * n - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2;
-          if (role == 2) {                        // (V of a tile comes after K of the next)
-            if (!isv) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) vpid[e] = pid[e];
-              pages_of(i, pid);
-            } else if (i < n - 1) {
+            for (int e = 0; e < 4; ++e) {
+              const bool page = (unsigned)pid[e] < (unsigned)a.npages;
+              if (!page && pid[e] != -2) atomicCAS(a.err, 0, -9);
+              row[e] = page ? pid[e] * a.page_rows + s.g * a.head_rows + at[e] * a.tok_rows : -1;
+            }
+            if (!room(st, slot)) break;
+            const uint32_t bar = full0 + 8u * slot, dst = ring + slot * kSlotBytes + mine;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes);
+            __syncwarp();
+            for (int c = chunk; c < CW; c += 2)
+              tma_gather4(dst + c * (kTreeKeys * 128), isv ? &a.vmap : &a.kmap, kI8 ? 0 : 64 * c, row, bar);
+            if constexpr (kI8) {                  // lanes 0 .. 15 K's scales, the others V's
+              if (!isv) {
+                const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + 4 * quad;
+                const float *from = lane < 16 ? a.ks : a.vs;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int t = pid[e];
-                pid[e] = vpid[e];
-                vpid[e] = t;
+                for (int e = 0; e < 4; ++e)
+                  cp_async4_zfill(smem_u32((lane < 16 ? ksc : vsc) + to + e), from + (row[e] < 0 ? 0 : ((long long)pid[e] * a.Hkv + s.g) * a.page + at[e]), row[e] < 0 ? 0u : 4u);
               }
+              cp_async_arrive(bar);
             }
-          }
-          const void *boxmap = isv ? &a.vbox : &a.kbox, *rowmap = isv ? &a.vmap : &a.kmap;
-          const int st = stage + x, slot = st % kRing;
-          if (st >= kRing) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(slot) : empty(slot), (uint32_t)((st / kRing - 1) & 1)));
-          if (!ok) break;
-          if (lane == slot) last = st;
-          const uint32_t bar = kI8 ? raw_full(slot) : full(slot);
-          const uint32_t dst = (kI8 ? cd_s + slot * Sh::kRaw : st_s + slot * Sh::kStage) + first * kRowBytes;
-          const int j = tree_base(s, s.u0 + i) + first;
-          const int r0 = j - page_at(j) * a.page;
-          // boxes that no node sees a row of stay what they are: their keys are masked
-          const bool on = chunk < CW && (!a.box || pid[0] != -2);
-          const bool page = on && (!a.box || page_ok(pid[0]));
-          const int parts = __popc(__ballot_sync(0xffffffffu, on)), pages = __popc(__ballot_sync(0xffffffffu, page));
-          if (lane == 0)                          // (int8: the tile's scales come with its K)
-            mbar_arrive_expect_tx(bar, (a.box ? parts * a.box * kRowBytes : kI8 ? Sh::kRaw : Sh::kStage) + (kI8 && !isv && a.scale_boxes ? pages * a.box * 8 : 0));
-          __syncwarp();
-          if (a.box && page) {
-            tma_load_4d(dst + (kI8 ? 0 : chunk * (kTreeKeys * 128)), boxmap, 64 * (kI8 ? 0 : chunk), r0, s.g, pid[0], bar);
-            if (kI8 && !isv && a.scale_boxes) {
-              const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + first;
-              const long long from = ((long long)pid[0] * a.Hkv + s.g) * a.page + r0;
-              bulk_g2s_nohint(smem_u32(ksc + to), a.ks + from, a.box * 4, bar);
-              bulk_g2s_nohint(smem_u32(vsc + to), a.vs + from, a.box * 4, bar);
-            }
-          } else if (on) {
-            for (int q = 0; q < nrows; q += 4) {  // (a box of a page that is none: zeros)
-              int row[4];
-              int r = r0 + q;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                row[e] = !a.box && seen(j + e) && page_ok(pid[e]) ? pid[e] * a.page_rows + s.g * a.head_rows + r * a.tok_rows : -1;
-                if (++r == a.page) r = 0;
-              }
-              for (int c = chunk; c < CW; c += a.box ? CW : 2)
-                tma_gather4(dst + q * kRowBytes + (kI8 ? 0 : c * (kTreeKeys * 128)), rowmap, kI8 ? 0 : 64 * c, row, bar);
-            }
-          }
-          if (kI8 && !a.scale_boxes) {            // row by row: lanes 0 .. 15 K's scales, the others V's
-            const int other = __shfl_sync(0xffffffffu, pid[0], a.box ? 4 * quad / a.box : 0);
-            if (!isv) {
-              const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + 4 * quad, j4 = tree_base(s, s.u0 + i) + 4 * quad;
-              const float *from = lane < 16 ? a.ks : a.vs;
-              int r = j4 - page_at(j4) * a.page;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int p = a.box ? other : pid[e];
-                const bool here = seen(j4 + e) && (unsigned)p < (unsigned)a.npages;
-                cp_async4_zfill(smem_u32((lane < 16 ? ksc : vsc) + to + e), from + (here ? ((long long)p * a.Hkv + s.g) * a.page + r : 0), here ? 4u : 0u);
-                if (++r == a.page) r = 0;
-              }
-            }
-            cp_async_arrive(bar);
-          }
-          if (role != 2) {
-            if (i + 1 < n) pages_of(i + 1, pid);
-          } else if (isv && i < n - 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pid[e] = vpid[e];
-          }
-          if (x == 0) {
-            // Q: row r is column rb * block_rows + r of the KV head: node column / G, head column % G
-            const int seg = nsegs + si;
-            if (seg > 0) ok = __all_sync(0xffffffffu, pwait(q_empty, (uint32_t)((seg - 1) & 1)));
-            if (!ok) break;
-            if (a.q_box) {                        // whole nodes: one box (rows beyond the sequence's are never written)
-              if (lane == 0) mbar_arrive_expect_tx(q_full, a.block_rows * 2 * D);
-              __syncwarp();
-              if (lane < D / 64)
-                tma_load_4d(q_s + lane * (kTreeRows * 128), &a.qbox, 64 * lane, 0, s.g, s.tok0 + s.rb * (a.block_rows / a.G), q_full);
-            } else {
-              if (lane == 0) mbar_arrive_expect_tx(q_full, Sh::kQ);
-              __syncwarp();
-              int row[4];
-              const int cols = s.nodes * a.G;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int col = s.rb * kTreeRows + 4 * lane + e, node = col / a.G;
-                row[e] = col < cols ? (s.tok0 + node) * a.q_tok_rows + (s.g * a.G + col - node * a.G) * a.q_head_rows : -1;
-              }
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c) tma_gather4(q_s + c * (kTreeRows * 128) + lane * 512, &a.qmap, 64 * c, row, q_full);
-            }
-            queries = seg + 1;
+            if (x == 0) queries_in();
           }
         }
         tiles += n;
