@@ -810,11 +810,14 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             const int st = stage + tree_k_stage(i), slot = st % F, b = (tiles + i) & 1;
             if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
             tc_fence_after();
-            const uint32_t ks = st_s + slot * Sh::kStage;
+            // (descriptors count 16 bytes; the loops are kept rolled: see the loading loop)
+            uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(st_s + slot * Sh::kStage);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c, qd += kTreeRows * 8, kd += kTreeKeys * 8) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_f16_ss_w(leader, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys), smem_desc_sw128(q_s + (kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32),
-                           smem_desc_sw128(ks + (kk >> 2) * (kTreeKeys * 128) + (kk & 3) * 32), kIdS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_ss_w(leader, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys), qd + 2 * kk, kd + 2 * kk, kIdS, (uint32_t)(c + kk));
+            }
             mma_commit_w(leader, s_full(b));
             mma_commit_w(leader, empty(slot));
             if (i == n - 1) mma_commit_w(leader, q_empty);
@@ -824,16 +827,15 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             if (!wwait(p_full(b), (uint32_t)((gt >> 1) & 1))) { ok = false; break; }
             if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
             tc_fence_after();
-            const uint32_t vs = st_s + slot * Sh::kStage;
             // (O of the segment before has been read; a tile with values that are not finite starts it at 0)
             if (j == 0 && seg > 0 && !wwait(o_free, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
             const uint32_t more = j > 0 || *static_cast<volatile int *>(&ctl->zeroed) == seg + 1;
-#pragma unroll
-            for (int kk = 0; kk < kTreeKeys / 16; ++kk) {
-#pragma unroll
-              for (int term = 0; term < 2; ++term)
-                mma_f16_ts_w(leader, tmem, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys + kk * 16 + term * 8),
-                             smem_desc_sw128_mn(vs + kk * 2048), kIdO, (kk > 0 || term > 0) ? 1u : more);
+            uint64_t vd = smem_desc_sw128_mn(st_s + slot * Sh::kStage);
+            uint32_t pt = tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys);
+#pragma unroll 1
+            for (int kk = 0; kk < kTreeKeys / 16; ++kk, vd += 128, pt += 16) {
+              mma_f16_ts_w(leader, tmem, pt, vd, kIdO, more | (uint32_t)kk);
+              mma_f16_ts_w(leader, tmem, pt + 8, vd, kIdO, 1u);
             }
             mma_commit_w(leader, empty(slot));
             mma_commit_w(leader, o_step);
@@ -916,37 +918,35 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           tc_fence_after();
           const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys + 32 * grp);
           const int sc = (gt % Sh::kScaleSlots) * kTreeKeys + 32 * grp;
-          // Scores from c0 on; int8: log2 of the weight times its value's scale.  Up to d = 128 (two CTAs an
-          // SM) they are read twice, 16 at a time: 32 would not fit the registers.
-          constexpr int NX = D == 256 ? 32 : 16;
-          F2 x[NX / 2];
+          // 16 scores from c0 on; int8: log2 of the weight times its value's scale.  They are read twice:
+          // 32 would not fit the registers of two CTAs an SM.
+          F2 x[8];
           auto scores = [&](int c0) {
-            uint32_t v[NX];
-            if constexpr (NX == 32) tmem_ld32(sadr, v);
-            else tmem_ld16(sadr + (uint32_t)c0, v);
+            uint32_t v[16];
+            tmem_ld16(sadr + (uint32_t)c0, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < NX; c += 2) {
+            for (int c = 0; c < 16; c += 2) {
               x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
               if constexpr (kI8) x[c / 2] = fma2(x[c / 2], *reinterpret_cast<const F2 *>(ksc + sc + c0 + c), *reinterpret_cast<const F2 *>(vlog + sc + c0 + c));
             }
           };
           float top = -INFINITY;
           if (busy) {
-#pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += NX) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < 32; c0 += 16) {
               scores(c0);
               float t0 = -INFINITY, t1 = -INFINITY;
               if (masked) {
 #pragma unroll
-                for (int c = 0; c < NX / 2; ++c) {
+                for (int c = 0; c < 8; ++c) {
                   float p, r;
                   x[c].get(p, r);
                   t0 = max3(t0, vm >> (c0 + 2 * c) & 1 ? p : -INFINITY, vm >> (c0 + 2 * c + 1) & 1 ? r : -INFINITY);
                 }
               } else {
 #pragma unroll
-                for (int c = 0; c < NX / 2; c += 2) {
+                for (int c = 0; c < 8; c += 2) {
                   float p, r;
                   x[c].get(p, r);
                   t0 = max3(t0, p, r);
@@ -990,14 +990,13 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           auto weights = [&](auto partly) {
             const F2 sc2(scale, scale), neg(-m_ref, -m_ref), minus(-1.0f, -1.0f);
             F2 sum(0.0f, 0.0f);
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < 32; c0 += 16) {
               uint32_t hi[8], lw[8];
-              if constexpr (NX == 16) scores(c0);
-              const int x0 = NX == 16 ? 0 : c0 / 2;
+              scores(c0);
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                F2 w = kI8 ? add2(x[x0 + c], neg) : fma2(x[x0 + c], sc2, neg);
+                F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
                 float p, r;
                 w.get(p, r);
                 w = F2(tree_ex2(p), tree_ex2(r));
