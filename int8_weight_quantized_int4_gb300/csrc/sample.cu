@@ -79,6 +79,7 @@ struct SampleSmem {
   float red[kSmWarps];
   unsigned rkey[kSmWarps];
   u64 rsum[kSmWarps];
+  float rsum3[3][kSmWarps];
   // read by the cluster's other CTAs
   float xmax, xsum;
   unsigned xkey;
@@ -148,6 +149,16 @@ __device__ __forceinline__ float sm_lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// (x - r) c, two at a time
+__device__ __forceinline__ void pair_scaled(float x0, float x1, float r, float c, float &y0, float &y1) {
+  u64 x, n, s;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(n) : "f"(-r));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "f"(c));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(n));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(x));
 }
 // binary32 values as unsigned integers in the values' order, -0 as +0, NaN below all (as -inf
 // it is never drawn)
@@ -300,29 +311,35 @@ struct SampleCta {
     return y < (float)(kSmBins - 1) ? (int)y : kSmBins - 1;        // (NaN: the last)
   }
 
-  // Calls f(x, column) for every element of the CTA's vectors.
+  // Calls f(x, column) for the elements of vectors a, a + step, .. < b; four loads at a time.  Places
+  // outside the row are -inf.
+  template <typename F>
+  __device__ __forceinline__ void walk(int a, int b, int step, F f) {
+    for (int v = a; v < b; v += 4 * step) {
+      uint4 raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = v + i * step < b ? row.load(v + i * step) : SampleRow<T>::nothing();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        float x[VE];
+        SampleRow<T>::floats(raw[0], x);
+        raw[0] = raw[1];
+        raw[1] = raw[2];
+        raw[2] = raw[3];
+        const int c = row.col(v + i * step);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f(x[e], c + e);
+      }
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void each(F f) {
-    for (int v = v0 + tid; v < v1; v += kSmThreads) {
-      float x[VE];
-      SampleRow<T>::floats(row.load(v), x);
-      const int c = row.col(v);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if ((unsigned)(c + e) < (unsigned)row.N) f(x[e], c + e);
-    }
+    walk(v0 + tid, v1, kSmThreads, f);
   }
   template <typename F>
   __device__ __forceinline__ u64 warp_sum(F &f, int a, int b) {
     u64 sum = 0;
-    for (int v = a + lane; v < b; v += 32) {
-      float x[VE];
-      SampleRow<T>::floats(row.load(v), x);
-      const int c = row.col(v);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if ((unsigned)(c + e) < (unsigned)row.N) sum += f(x[e], c + e);
-    }
+    walk(a + lane, b, 32, [&](float x, int col) { sum += f(x, col); });
     return reduce(sum);
   }
   __device__ __forceinline__ static u64 reduce(u64 x) {
@@ -376,10 +393,9 @@ struct SampleCta {
           float x[VE];
           u64 sum = 0;
           const int c = row.col(v + lane);
-          if (v + lane < p1) SampleRow<T>::floats(row.load(v + lane), x);
+          SampleRow<T>::floats(v + lane < p1 ? row.load(v + lane) : SampleRow<T>::nothing(), x);
 #pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (v + lane < p1 && (unsigned)(c + e) < (unsigned)row.N) sum += f(x[e], c + e);
+          for (int e = 0; e < VE; ++e) sum += f(x[e], c + e);
           u64 incl = sum;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -393,7 +409,7 @@ struct SampleCta {
               bool got = false;
 #pragma unroll
               for (int e = 0; e < VE; ++e) {
-                if (!got && (unsigned)(c + e) < (unsigned)row.N) {
+                if (!got) {
                   const u64 y = f(x[e], c + e);
                   run += y;
                   if (run > at) {
@@ -642,6 +658,7 @@ __device__ __forceinline__ SampleCut sample_cut(SampleCta<T> &t, const SampleCut
     t.each([&](float x, int col) {
       const unsigned key = sm_key(x);
       if ((key & mask) != prefix || !in.stays(key, col)) return;
+      if ((unsigned)col >= (unsigned)t.row.N) return;
       const int b = t.bin_of(x, 8.0f);
       if (round > 0 && b != bin) return;
       const int d = round == 0 ? b : 255 - (int)((key >> shift) & 255u);       // larger values first
@@ -811,14 +828,20 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       const float gm = t.row.max_of(m);
       if (sums) {
         const float nm = fmaxf(bm, gm), ref = nm == -INFINITY ? 0.0f : nm;
-        float sum = 0.0f;
+        float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < U0; ++i) {
           float x[VE];
           t.row.floats(raw[i], x);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) sum += sm_ex2((x[e] - ref) * c);
+          for (int e = 0; e < VE; e += 2) {
+            float y0, y1;
+            pair_scaled(x[e], x[e + 1], ref, c, y0, y1);
+            sum += sm_ex2(y0);
+            sum1 += sm_ex2(y1);
+          }
         }
+        sum += sum1;
         if (!(sum < INFINITY)) {                  // NaN logits, or infinite ones
           sum = 0.0f;
 #pragma unroll
@@ -927,7 +950,49 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     const float d = z / c;
     return sm_key(M + d - (fabsf(d) * 1e-4f + fabsf(M) * 1e-6f));
   };
-  if (sums) T0 = max(T0, below(fminf(sm_lg2((1.0f - p) * s.rowsum / (float)a.N) - 0.01f, 0.0f)));
+  if (sums) {
+    const float most = (1.0f - p) * s.rowsum * 0.99f;             // what may be left out
+    float z = fminf(sm_lg2(most / (float)a.N), 0.0f);
+    if (size == 1) {
+      // Higher, from the blocks: with a bound of 2^z those below it leave out their sums and each
+      // other at most 31 elements of weight 2^z.  Tried: sixteenths of the way, four at a time.
+      const float step = -z * (1.0f / 16.0f), each = (float)(U * VE - 1);
+      int lo = 16;
+      for (int round = 0; round < 2; ++round) {
+        const int at = round == 0 ? 4 : 1, from = round == 0 ? 0 : lo - 4;     // tried: from + at, from + 2 at, ..
+        float sum[3] = {}, zt[3], wt[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          zt[i] = -step * (float)(from + at * (i + 1));
+          wt[i] = each * sm_ex2(zt[i]);
+        }
+        for (int b = 0; b < nblk; ++b) {
+          const float bm = s.bmax[b][tid], y = bm == M ? 0.0f : (bm - M) * c, bs = rel(bm, s.bsum[b][tid], M);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) sum[i] += y < zt[i] ? bs : fminf(bs, wt[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+          if (lane == 0) s.rsum3[i][warp] = sum[i];
+        }
+        __syncthreads();
+        int best = from + 4 * at;
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+          float total = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kSmWarps; ++w) total += s.rsum3[i][w];
+          if (total <= most) best = from + at * (i + 1);
+        }
+        lo = best;
+      }
+      z = -step * (float)lo;
+    }
+    T0 = max(T0, below(z - 0.01f));
+  }
   if (mp > 0.0f && !(k > 0 && p < 1.0f)) T0 = max(T0, below(mp < 1.0f ? sm_lg2(mp) - 0.01f : 0.0f));
   if (greedy) T0 = sm_key(M);
   T0 = max(T0, 0x00800000u);                      // (the key of the lowest finite value: not -inf, not NaN)
