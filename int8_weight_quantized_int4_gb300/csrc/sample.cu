@@ -30,6 +30,7 @@
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "launch.h"
@@ -43,7 +44,7 @@ constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBlocks = 8;                      // blocks a thread keeps the maxima of
 constexpr int kSmList = 1024;
 constexpr int kSmBins = 256;
-constexpr int kSmMaxCluster = 8;
+constexpr int kSmMaxCluster = 16;
 constexpr int kSmFix = 40;                        // weights in units of 2^-40
 
 typedef unsigned long long u64;
@@ -81,9 +82,9 @@ struct SampleSmem {
   u64 rsum[kSmWarps];
   float rsum3[3][kSmWarps];
   // read by the cluster's other CTAs
-  float xmax, xsum;
+  float xmax, xsum, xsum3[2][3];
   unsigned xkey;
-  u64 xtotal;
+  u64 xtotal, xkept;
   // written by them (first CTA)
   unsigned n, gidx;
   u64 tail[kSmMaxCluster];
@@ -174,34 +175,44 @@ __device__ __forceinline__ float sm_value(unsigned k) {
 struct SampleScale {
   float M, chi, clo;
 };
-// 2^40 e^((x - M) / t), rounded; 0 for -inf and NaN.  EXACT: x - M has no rounding (16-bit types).
+// 2^40 2^(k / 16), k = -8 .. 8
+static __device__ const u64 kSmPowers[17] = {
+    777472127994ull,  811893759832ull,  847839367509ull,  885376423200ull,  924575386327ull,  965509835819ull,
+    1008256608221ull, 1052895941925ull, 1099511627776ull, 1148191166361ull, 1199025932245ull, 1252111345494ull,
+    1307547050779ull, 1365437104419ull, 1425890169699ull, 1489019720837ull, 1554944255988ull};
+constexpr float kSmLight = -12.0f;                // log2 of the weight from which on it is computed exactly
+
+// 2^40 2^y for y = (x - M) chi, -12 < y <= 0, to 2e-11: y in two terms, the nearest sixteenth of an
+// octave from a table, and the rest's exponential by its series, whose first term is exact.
+// EXACT: x - M has no rounding (16-bit types).
+template <bool EXACT>
+__device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float clo) {
+  const float d = x - M, y = d * chi;
+  float yl = fmaf(d, chi, -y) + d * clo;
+  if constexpr (!EXACT) {
+    const float b = d - x;                        // what the difference rounded off
+    yl = fmaf((x - (d - b)) + (-M - b), chi, yl);
+  }
+  const float n = rintf(y), f = y - n;
+  const float k = rintf(f * 16.0f), s = fmaf(k, -0.0625f, f);
+  constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
+  const float p = s * L, pl = fmaf(s, L, -p) + s * Llo + yl * L;
+  // (2^s - 1 - s ln 2) / s^2: ln(2)^k / k! s^(k - 2), k = 2 .. 5
+  float q = fmaf(1.33335581e-3f, s, 9.61812911e-3f);
+  q = fmaf(q, s, 5.55041087e-2f);
+  q = fmaf(q, s, 0.240226507f);
+  const long long t = (long long)__float2int_rn(p * 68719476736.0f) + __float2int_rn(fmaf(q, s * s, pl) * 68719476736.0f);
+  const u64 w = kSmPowers[(int)k + 8];
+  return (w + (u64)__mul64hi((long long)(w << 22), t << 6)) >> -(int)n;
+}
+// 2^40 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32 (1e-6 of the weight, without
+// a common sign).
 template <bool EXACT>
 __device__ __forceinline__ u64 sm_weight(float x, const SampleScale &c) {
   if (x == c.M) return 1ull << kSmFix;            // (+inf too)
-  const float d = x - c.M;
-  float y = d * c.chi;
-  if (!(y > -60.0f)) return 0;                    // (and NaN)
-  float yl = fmaf(d, c.chi, -y) + d * c.clo;
-  if constexpr (!EXACT) {
-    const float b = d - x;                        // what the difference rounded off
-    yl = fmaf((x - (d - b)) + (-c.M - b), c.chi, yl);
-  }
-  const float n = rintf(y);
-  const float f = (y - n) + yl;
-  constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
-  const float p = f * L, pl = fmaf(f, L, -p) + f * Llo;
-  // (2^f - 1 - f ln 2) / f^2: ln(2)^k / k! f^(k - 2), k = 2 .. 8
-  float q = 1.3215487e-6f;
-  q = fmaf(q, f, 1.5252734e-5f);
-  q = fmaf(q, f, 1.5403530e-4f);
-  q = fmaf(q, f, 1.3333558e-3f);
-  q = fmaf(q, f, 9.6181291e-3f);
-  q = fmaf(q, f, 5.5504109e-2f);
-  q = fmaf(q, f, 0.24022651f);
-  const int i = __float2int_rn(p * 2147483648.0f) + __float2int_rn(fmaf(q, f * f, pl) * 2147483648.0f);
-  const unsigned m = 0x80000000u + (unsigned)i;   // 2^31 2^f: 0.7 .. 1.42
-  const int s = -(int)n;                          // (y <= 0; n up to 0)
-  return s <= 0 ? (u64)m << 9 : ((u64)m << 9) >> s;
+  const float y = (x - c.M) * c.chi;
+  if (y > kSmLight) return sm_heavy<EXACT>(x, c.M, c.chi, c.clo);
+  return y > -60.0f ? (u64)__float2uint_rn(sm_ex2(y) * (float)(1ull << kSmFix)) : 0;      // (and NaN)
 }
 
 // A row as 16-byte vectors: vector v holds columns v VE - pad .. + VE - 1, pad being how many
@@ -332,14 +343,59 @@ struct SampleCta {
       }
     }
   }
+  // The weights of one vector's elements, in sum: the light ones in binary32.
+  __device__ __forceinline__ u64 vector_weight(const uint4 &raw) const {
+    float x[VE], y[VE], top = -INFINITY, sum = 0.0f, sum1 = 0.0f;
+    SampleRow<T>::floats(raw, x);
+#pragma unroll
+    for (int e = 0; e < VE; e += 2) {
+      pair_scaled(x[e], x[e + 1], sc.M, sc.chi, y[e], y[e + 1]);
+      top = fmaxf(top, fmaxf(y[e], y[e + 1]));
+      sum += sm_ex2(y[e]);
+      sum1 += sm_ex2(y[e + 1]);
+    }
+    sum += sum1;
+    if (top <= kSmLight && sum == sum) return __float2uint_rn(sum * (float)(1ull << kSmFix));
+    u64 total = 0;
+    unsigned heavy = 0;
+    sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      if (y[e] > kSmLight || x[e] == sc.M) heavy |= 1u << e;
+      else sum += y[e] > -60.0f ? sm_ex2(y[e]) : 0.0f;
+    }
+    for (; heavy; heavy &= heavy - 1) {
+      const int k = __ffs(heavy) - 1;
+      float v = x[0];
+#pragma unroll
+      for (int e = 1; e < VE; ++e) v = e == k ? x[e] : v;
+      total += weight(v);
+    }
+    return total + __float2uint_rn(sum * (float)(1ull << kSmFix));
+  }
   template <typename F>
   __device__ __forceinline__ void each(F f) {
     walk(v0 + tid, v1, kSmThreads, f);
   }
-  template <typename F>
+  template <bool ALL, typename F>
   __device__ __forceinline__ u64 warp_sum(F &f, int a, int b) {
     u64 sum = 0;
-    walk(a + lane, b, 32, [&](float x, int col) { sum += f(x, col); });
+    if constexpr (ALL) {
+      for (int v = a + lane; v < b; v += 128) {
+        uint4 raw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = v + i * 32 < b ? row.load(v + i * 32) : SampleRow<T>::nothing();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          sum += vector_weight(raw[0]);
+          raw[0] = raw[1];
+          raw[1] = raw[2];
+          raw[2] = raw[3];
+        }
+      }
+    } else {
+      walk(a + lane, b, 32, [&](float x, int col) { sum += f(x, col); });
+    }
     return reduce(sum);
   }
   __device__ __forceinline__ static u64 reduce(u64 x) {
@@ -351,12 +407,13 @@ struct SampleCta {
   // The first column, in order, at which the running sum of f over the whole row passes
   // target(total): by the sums of the CTAs, of the warps' ranges and of pieces of one range.
   // done(column, f there, total) is called by one thread of the CTA that holds it.
-  template <typename F, typename G, typename H>
+  // ALL: f is every element's weight.
+  template <bool ALL, typename F, typename G, typename H>
   __device__ __forceinline__ void find(F f, G target, H done) {
     const int per = (v1 - v0 + kSmWarps - 1) / kSmWarps;
     auto begin = [&](int w) { return min(v0 + w * per, v1); };
     __syncthreads();
-    const u64 mine = warp_sum(f, begin(warp), begin(warp + 1));
+    const u64 mine = warp_sum<ALL>(f, begin(warp), begin(warp + 1));
     if (lane == 0) s.rsum[warp] = mine;
     __syncthreads();
     if (tid == 0) {
@@ -382,7 +439,7 @@ struct SampleCta {
       while (w < kSmWarps - 1 && at >= s.rsum[w]) at -= s.rsum[w++];
       const int a = begin(w), b = begin(w + 1), len = (b - a + kSmWarps - 1) / kSmWarps;
       const int p0 = min(a + warp * len, b), p1 = min(p0 + len, b);
-      const u64 piece = warp_sum(f, p0, p1);
+      const u64 piece = warp_sum<ALL>(f, p0, p1);
       __syncthreads();
       if (lane == 0) s.rsum[warp] = piece;
       __syncthreads();
@@ -393,9 +450,14 @@ struct SampleCta {
           float x[VE];
           u64 sum = 0;
           const int c = row.col(v + lane);
-          SampleRow<T>::floats(v + lane < p1 ? row.load(v + lane) : SampleRow<T>::nothing(), x);
+          const uint4 raw = v + lane < p1 ? row.load(v + lane) : SampleRow<T>::nothing();
+          SampleRow<T>::floats(raw, x);
+          if constexpr (ALL) {
+            sum = vector_weight(raw);
+          } else {
 #pragma unroll
-          for (int e = 0; e < VE; ++e) sum += f(x[e], c + e);
+            for (int e = 0; e < VE; ++e) sum += f(x[e], c + e);
+          }
           u64 incl = sum;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -405,19 +467,31 @@ struct SampleCta {
           const unsigned past = __ballot_sync(0xffffffffu, incl > at);
           if (past) {
             if (lane == __ffs(past) - 1) {
-              u64 run = incl - sum;
-              bool got = false;
+              // (one by one the elements may round to a little less than together: then the last, or
+              // where all round to 0 the largest)
+              u64 run = incl - sum, w = 0;
+              int found = -1;
 #pragma unroll
               for (int e = 0; e < VE; ++e) {
-                if (!got) {
-                  const u64 y = f(x[e], c + e);
-                  run += y;
-                  if (run > at) {
-                    got = true;
-                    done(c + e, y, total);
+                const u64 y = f(x[e], c + e);
+                if (run <= at && y > 0) {
+                  found = c + e;
+                  w = y;
+                }
+                run += y;
+              }
+              if (found < 0) {
+                float best = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                  if (x[e] > best) {
+                    best = x[e];
+                    found = c + e;
                   }
                 }
+                w = 1;
               }
+              done(found, w, total);
             }
             break;
           }
@@ -588,7 +662,7 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
     }
   }
   if (mp > 0.0f) {
-    const u64 least = mp <= 1.0f ? (u64)ceil((double)mp * (double)(1ull << kSmFix)) : ~0ull;
+    const u64 least = (u64)ceil((double)mp * (double)(1ull << kSmFix));
 #pragma unroll
     for (int i = 0; i < PER; ++i) keep[i] = keep[i] && (w[i] >= least || key[i] == s.top);
   }
@@ -720,7 +794,7 @@ __device__ __forceinline__ SampleCut sample_cut(SampleCta<T> &t, const SampleCut
   }
   if (t.tid == 0) s.found = 0x7fffffff;
   __syncthreads();
-  t.find([&](float x, int col) { return (u64)(sm_key(x) == prefix && in.stays(prefix, col)); },
+  t.template find<false>([&](float x, int col) { return (u64)(sm_key(x) == prefix && in.stays(prefix, col)); },
          [&](u64) { return ties - 1; },
          [&](int col, u64, u64) {
            if (t.size > 1)
@@ -732,6 +806,21 @@ __device__ __forceinline__ SampleCut sample_cut(SampleCta<T> &t, const SampleCut
   return SampleCut{prefix, s.found};
 }
 
+// The draw among what the cut and min-p leave.
+template <typename T, bool ALL>
+__device__ __forceinline__ void sample_draw(const SampleArgs &a, SampleCta<T> &t, int r, const SampleCut &cut, float mp, float u) {
+  const u64 least = (u64)ceil((double)mp * (double)(1ull << kSmFix));
+  t.sync();
+  t.template find<ALL>(
+      [&](float x, int col) {
+        if (!ALL && !cut.stays(sm_key(x), col)) return 0ull;
+        const u64 w = t.weight(x);
+        return ALL || w >= least ? w : 0ull;
+      },
+      [&](u64 total) { return sample_target(u, total); },
+      [&](int col, u64 w, u64 total) { sample_write(a, r, col, w, total); });
+}
+// Without bounds or lists: what a flat row's borders come to when even one bin overflows.
 template <typename T>
 __device__ __noinline__ void sample_row(const SampleArgs &a, SampleCta<T> t, int r, int k, float p, float mp, float u) {
   SampleCut cut{0u, 0x7fffffff};
@@ -739,7 +828,7 @@ __device__ __noinline__ void sample_row(const SampleArgs &a, SampleCta<T> t, int
   if (p < 1.0f) {
     // the sum of what top-k left
     const SampleCut in = cut;
-    t.find([&](float x, int col) { return in.stays(sm_key(x), col) ? t.weight(x) : 0ull; },
+    t.template find<false>([&](float x, int col) { return in.stays(sm_key(x), col) ? t.weight(x) : 0ull; },
            [&](u64 total) {
              if (t.tid == 0) t.s.thr = sample_mass(p, total);
              return ~0ull;                        // (no draw yet)
@@ -749,16 +838,127 @@ __device__ __noinline__ void sample_row(const SampleArgs &a, SampleCta<T> t, int
     const u64 need = t.s.thr;
     cut = sample_cut(t, in, need, true);
   }
-  const u64 least = !(mp > 0.0f) ? 0 : mp <= 1.0f ? (u64)ceil((double)mp * (double)(1ull << kSmFix)) : 1ull << kSmFix;
+  sample_draw<T, false>(a, t, r, cut, mp, u);
+}
+
+// The list that overflowed, by bins of an eighth of an octave: their counts and sums, the list of
+// the border's bin alone.  items(f): calls f(key, x, column) for the CTA's elements from the bound on.
+// false: that list overflows too.
+template <typename T, typename I>
+__device__ __forceinline__ bool sample_flat(SampleCta<T> &t, int k, float p, u64 tail, I items, SampleCut &cut) {
+  SampleSmem &s = t.s;
+  const int tid = t.tid, lane = t.lane, warp = t.warp;
+  s.cnt[tid] = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) s.limb[i][tid] = 0;
+  __syncthreads();
+  items([&](unsigned, float x, int) {
+    const int b = t.bin_of(x, 8.0f);
+    const u64 w = t.weight(x);
+    atomicAdd(&s.cnt[b], 1u);
+    atomicAdd(&s.limb[0][b], (unsigned)w & 0x3fffu);
+    atomicAdd(&s.limb[1][b], (unsigned)(w >> 14) & 0x3fffu);
+    atomicAdd(&s.limb[2][b], (unsigned)(w >> 28));
+  });
+  __syncthreads();
+  s.mass[tid] = (u64)s.limb[0][tid] + ((u64)s.limb[1][tid] << 14) + ((u64)s.limb[2][tid] << 28);
   t.sync();
-  t.find(
-      [&](float x, int col) {
-        if (!cut.stays(sm_key(x), col)) return 0ull;
-        const u64 w = t.weight(x);
-        return w >= least ? w : 0ull;
-      },
-      [&](u64 total) { return sample_target(u, total); },
-      [&](int col, u64 w, u64 total) { sample_write(a, r, col, w, total); });
+  // bin tid's and the running sums, of the whole row
+  u64 mass = 0, number = 0;
+  for (unsigned r = 0; r < t.size; ++r) {
+    mass += t.size > 1 ? peer_ld64(peer(&s.mass[tid], r)) : s.mass[tid];
+    number += t.size > 1 ? peer_ld32(peer(&s.cnt[tid], r)) : s.cnt[tid];
+  }
+  auto running = [&](u64 v, u64 &total) {
+    u64 incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) s.rsum[warp] = incl;
+    __syncthreads();
+    total = 0;
+    u64 before = 0;
+    for (int w = 0; w < kSmWarps; ++w) {
+      if (w == warp) before = total;
+      total += s.rsum[w];
+    }
+    return incl + before;
+  };
+  // The element of bin b up to which `need` more are reached (by number, or by weight among those
+  // from `floor` on): its composite key to everyone, and what stays of the bin weighs `kept`.
+  auto border = [&](int b, u64 need, bool by_mass, u64 floor, u64 &found, u64 &kept) {
+    t.sync();                                     // the last list, or its number, has been read
+    if (tid == 0) s.n = 0;
+    t.sync();
+    const uint32_t lead_n = peer(&s.n, 0), lead_key = peer(&s.key[0], 0);
+    items([&](unsigned key, float x, int col) {
+      if (t.bin_of(x, 8.0f) != b) return;
+      const u64 c = (u64)key << 32 | (unsigned)~col;
+      if (c < floor) return;
+      const unsigned at = peer_add(lead_n, 1u);
+      if (at < kSmList) peer_st64(lead_key + 8 * at, c);
+    });
+    t.sync();
+    const int n = (int)peer_ld32(lead_n);
+    if (n > kSmList) return false;
+    if (t.rank == 0) {
+      if (tid == 0) s.total = 0;
+      for (int e = tid; e < n; e += kSmThreads) s.w[e] = t.weight(sm_value((unsigned)(s.key[e] >> 32)));
+      __syncthreads();
+      for (int e = tid; e < n; e += kSmThreads) {
+        const u64 mine = s.key[e];
+        u64 above = 0;
+        for (int o = 0; o < n; ++o)
+          if (s.key[o] > mine) above += by_mass ? s.w[o] : 1ull;
+        if (above < need) atomicAdd(&s.total, s.w[e]);
+        if (above < need && above + (by_mass ? s.w[e] : 1ull) >= need)
+          for (unsigned r = 0; r < t.size; ++r) peer_st64(peer(&s.top, r), mine);
+      }
+      __syncthreads();
+      if (tid == 0)
+        for (unsigned r = 0; r < t.size; ++r) peer_st64(peer(&s.xkept, r), s.total);
+    }
+    t.sync();
+    found = s.top;
+    kept = s.xkept;
+    return true;
+  };
+  u64 total, floor = 0;
+  auto pick = [&](bool here, u64 before) {        // one thread's bin and what lies before it, to all
+    __syncthreads();
+    if (tid == 0) s.bin = -1;
+    __syncthreads();
+    if (here) {
+      s.bin = tid;
+      s.mbefore = before;
+    }
+    __syncthreads();
+    return s.bin;
+  };
+  if (tid == 0) s.top = 0;
+  if (k > 0) {
+    const u64 incl = running(number, total);
+    const int kb = pick(incl >= (u64)k && incl - number < (u64)k, incl - number);
+    if (kb >= 0) {
+      u64 kept;
+      if (!border(kb, (u64)k - s.mbefore, false, 0, floor, kept)) return false;
+      mass = tid < kb ? mass : tid == kb ? kept : 0;
+    }
+  }
+  if (p < 1.0f) {
+    const u64 incl = running(mass, total);
+    const u64 need = max(sample_mass(p, total + (k > 0 ? 0 : tail)), 1ull);
+    const int pb = pick(incl >= need && incl - mass < need, incl - mass);
+    if (pb >= 0) {
+      u64 kept;
+      if (!border(pb, need - s.mbefore, true, floor, floor, kept)) return false;
+    }
+  }
+  cut = SampleCut{(unsigned)(floor >> 32), floor == 0 ? 0x7fffffff : (int)~(unsigned)floor};
+  return true;
 }
 
 // ---------------------------------------------------------------- the kernel --
@@ -780,6 +980,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   if (k <= 0 || k >= a.N) k = 0;
   if (!(p < 1.0f)) p = 1.0f;
   if (!(mp > 0.0f)) mp = 0.0f;
+  if (mp > 1.0f) {                                // the first alone
+    k = a.N > 1 ? 1 : 0;
+    mp = 0.0f;
+  }
   if (greedy) {
     k = 0;
     p = 1.0f;
@@ -863,18 +1067,28 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     top = fmaxf(top, bm);
   }
   // ---- 2. the row's largest logit, sum and bound
+  const float mine = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s.red[warp] = top;
   if (k > 0) {
-    // the j-th largest of the warp's block maxima, to 16 bits: by halving
+    // the j-th largest of the warp's block maxima (of its threads' where that will do), to 16 bits: by halving
     const int j = (k + kSmWarps * (int)size - 1) / (kSmWarps * (int)size);
     unsigned bound = 0;
-    if (j <= 32 * nblk) {
+    if (j <= 12) {
+      const unsigned key = sm_key(mine);
+      for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+        if (__popc(__ballot_sync(0xffffffffu, key >= (bound | bit))) >= j) bound |= bit;
+    } else if (j <= 32 * nblk) {
+      unsigned key[kSmBlocks];
+#pragma unroll
+      for (int b = 0; b < kSmBlocks; ++b) key[b] = b < nblk ? sm_key(s.bmax[b][tid]) : 0u;
+#pragma unroll 1
       for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
         int n = 0;
-        for (int b = 0; b < nblk; ++b) n += __popc(__ballot_sync(0xffffffffu, sm_key(s.bmax[b][tid]) >= (bound | bit)));
-        if (n >= j) bound |= bit;
+#pragma unroll
+        for (int b = 0; b < kSmBlocks; ++b) n += key[b] >= (bound | bit);
+        if (__reduce_add_sync(0xffffffffu, n) >= j) bound |= bit;
       }
     }
     if (lane == 0) s.rkey[warp] = bound;
@@ -915,10 +1129,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     float M = m;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     sum = rel(m, sum, M);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
+    for (int o = 8; o > 0; o >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
       key = min(key, __shfl_xor_sync(0xffffffffu, key, o));
     }
@@ -940,7 +1154,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     return;
   }
   if (!greedy && k == 0 && p == 1.0f && mp == 0.0f) {
-    sample_row<T>(a, t, r, 0, 1.0f, 0.0f, u);
+    sample_draw<T, true>(a, t, r, SampleCut{0u, 0x7fffffff}, 0.0f, u);
     t.sync();                                     // (its sums have been read)
     return;
   }
@@ -953,7 +1167,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   if (sums) {
     const float most = (1.0f - p) * s.rowsum * 0.99f;             // what may be left out
     float z = fminf(sm_lg2(most / (float)a.N), 0.0f);
-    if (size == 1) {
+    {
       // Higher, from the blocks: with a bound of 2^z those below it leave out their sums and each
       // other at most 31 elements of weight 2^z.  Tried: sixteenths of the way, four at a time.
       const float step = -z * (1.0f / 16.0f), each = (float)(U * VE - 1);
@@ -979,12 +1193,22 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
           if (lane == 0) s.rsum3[i][warp] = sum[i];
         }
         __syncthreads();
+        if (size > 1) {
+          if (tid < 3) {
+            float total = 0.0f;
+            for (int w = 0; w < kSmWarps; ++w) total += s.rsum3[tid][w];
+            s.xsum3[round][tid] = total;
+          }
+          t.sync();
+        }
         int best = from + 4 * at;
 #pragma unroll
         for (int i = 2; i >= 0; --i) {
           float total = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kSmWarps; ++w) total += s.rsum3[i][w];
+          if (size > 1)
+            for (unsigned q = 0; q < size; ++q) total += __uint_as_float(peer_ld32(peer(&s.xsum3[round][i], q)));
+          else
+            for (int w = 0; w < kSmWarps; ++w) total += s.rsum3[i][w];
           if (total <= most) best = from + at * (i + 1);
         }
         lo = best;
@@ -1067,7 +1291,29 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u);
     return;
   }
-  sample_row<T>(a, t, r, k, p, mp, u);
+  // ---- flat rows
+  u64 rest = 0;
+  if (sums)
+    for (unsigned q = 0; q < size; ++q) rest += peer_ld64(peer(&s.tail[q], 0));
+  SampleCut cut;
+  const bool fine = sample_flat<T>(
+      t, k, p, rest,
+      [&](auto f) {
+        for (int i = tid; i < items; i += kSmThreads) {
+          const int id = s.work[i >> logU], v = t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
+          if (v >= t.v1) continue;
+          float x[VE];
+          t.row.floats(t.row.load(v), x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const unsigned key = sm_key(x[e]);
+            if (key >= T0) f(key, x[e], t.row.col(v) + e);
+          }
+        }
+      },
+      cut);
+  if (fine) sample_draw<T, false>(a, t, r, cut, mp, u);
+  else sample_row<T>(a, t, r, k, p, mp, u);
   t.sync();
 }
 
@@ -1105,12 +1351,23 @@ extern "C" int sample_tokens(const void *logits, int dtype, int M, int N, long l
   // CTAs a row: as many as the GPU holds four an SM of, 2048 elements each at least, and so that
   // a CTA's part has below 2^18 elements
   int cluster = 1;
-  while (cluster < kSmMaxCluster && ((2ll * cluster * M <= 4ll * sms && 2 * cluster * 2048 <= N) || N / cluster >= (1 << 18) - 16))
+  const int most = M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8;     // (16 have to fit one part of the GPU)
+  while (cluster < most && ((2ll * cluster * M <= 4ll * sms && 2 * cluster * 2048 <= N) || N / cluster >= (1 << 18) - 16))
     cluster *= 2;
   if ((long long)M * cluster > 0x7fffffffll) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many rows");
   const void *f = dtype == QW_F16    ? reinterpret_cast<const void *>(sample_kernel<__half>)
                   : dtype == QW_BF16 ? reinterpret_cast<const void *>(sample_kernel<__nv_bfloat16>)
                                      : reinterpret_cast<const void *>(sample_kernel<float>);
+  if (cluster > 8) {                              // (once a kernel and device)
+    static std::atomic<unsigned long long> allowed[3];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(allowed[dtype].load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess && dev < 64) allowed[dtype].fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    if (e != cudaSuccess) return bad(QW_ERR_CUDA, "cluster size: %s", cudaGetErrorString(e));
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(M * cluster));
   cfg.blockDim = dim3(kSmThreads);
