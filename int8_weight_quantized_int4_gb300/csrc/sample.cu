@@ -79,6 +79,7 @@ struct SampleSmem {
   u64 mass[kSmBins];                              // elements); or their sum
   float red[kSmWarps];
   unsigned rkey[kSmWarps];
+  int nkey[2][kSmWarps];
   u64 rsum[kSmWarps];
   float rsum3[3][kSmWarps];
   // read by the cluster's other CTAs
@@ -315,6 +316,22 @@ struct SampleCta {
     }
   }
   __device__ __forceinline__ u64 weight(float x) const { return sm_weight<kExact>(x, sc); }
+  // The CTAs' lists, one behind the other in the first CTA's; their number (above kSmList: not
+  // joined).  After a sync(), and ends with one.
+  __device__ __forceinline__ unsigned join_lists() {
+    if (size == 1) return s.n;
+    unsigned n = 0, before = 0;
+    for (unsigned r = 0; r < size; ++r) {
+      if (r == rank) before = n;
+      n += peer_ld32(peer(&s.n, r));
+    }
+    if (n <= kSmList && rank > 0) {
+      const uint32_t to = peer(&s.key[0], 0) + 8 * before;
+      for (unsigned e = tid; e < s.n; e += kSmThreads) peer_st64(to + 8 * e, s.key[e]);
+    }
+    sync();
+    return n;
+  }
   // eighths (quarters) of an octave below the largest logit
   __device__ __forceinline__ int bin_of(float x, float per) const {
     if (x == sc.M) return 0;
@@ -890,28 +907,28 @@ __device__ __forceinline__ bool sample_flat(SampleCta<T> &t, int k, float p, u64
   // The element of bin b up to which `need` more are reached (by number, or by weight among those
   // from `floor` on): its composite key to everyone, and what stays of the bin weighs `kept`.
   auto border = [&](int b, u64 need, bool by_mass, u64 floor, u64 &found, u64 &kept) {
-    t.sync();                                     // the last list, or its number, has been read
+    t.sync();                                     // the last list, and its number, have been read
     if (tid == 0) s.n = 0;
-    t.sync();
-    const uint32_t lead_n = peer(&s.n, 0), lead_key = peer(&s.key[0], 0);
+    __syncthreads();
     items([&](unsigned key, float x, int col) {
       if (t.bin_of(x, 8.0f) != b) return;
       const u64 c = (u64)key << 32 | (unsigned)~col;
       if (c < floor) return;
-      const unsigned at = peer_add(lead_n, 1u);
-      if (at < kSmList) peer_st64(lead_key + 8 * at, c);
+      const unsigned at = *static_cast<volatile unsigned *>(&s.n) > kSmList ? kSmList : atomicAdd(&s.n, 1u);
+      if (at < kSmList) s.key[at] = c;
     });
     t.sync();
-    const int n = (int)peer_ld32(lead_n);
+    const unsigned n = t.join_lists();
     if (n > kSmList) return false;
     if (t.rank == 0) {
       if (tid == 0) s.total = 0;
-      for (int e = tid; e < n; e += kSmThreads) s.w[e] = t.weight(sm_value((unsigned)(s.key[e] >> 32)));
+      for (unsigned e = tid; e < n; e += kSmThreads) s.w[e] = t.weight(sm_value((unsigned)(s.key[e] >> 32)));
       __syncthreads();
-      for (int e = tid; e < n; e += kSmThreads) {
+      for (unsigned e = tid; e < n; e += kSmThreads) {
         const u64 mine = s.key[e];
         u64 above = 0;
-        for (int o = 0; o < n; ++o)
+#pragma unroll 4
+        for (unsigned o = 0; o < n; ++o)
           if (s.key[o] > mine) above += by_mass ? s.w[o] : 1ull;
         if (above < need) atomicAdd(&s.total, s.w[e]);
         if (above < need && above + (by_mass ? s.w[e] : 1ull) >= need)
@@ -1072,26 +1089,35 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s.red[warp] = top;
   if (k > 0) {
-    // the j-th largest of the warp's block maxima (of its threads' where that will do), to 16 bits: by halving
-    const int j = (k + kSmWarps * (int)size - 1) / (kSmWarps * (int)size);
+    // the j-th largest of the CTA's thread maxima, or for many of its block maxima, to 16 bits: by
+    // halving
+    const int j = (k + (int)size - 1) / (int)size;
     unsigned bound = 0;
-    if (j <= 12) {
+    if (j <= kSmThreads / 2) {
       const unsigned key = sm_key(mine);
+#pragma unroll 1
       for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-        if (__popc(__ballot_sync(0xffffffffu, key >= (bound | bit))) >= j) bound |= bit;
-    } else if (j <= 32 * nblk) {
+        if (__syncthreads_count(key >= (bound | bit)) >= j) bound |= bit;
+    } else if (j <= kSmThreads * nblk) {
       unsigned key[kSmBlocks];
 #pragma unroll
       for (int b = 0; b < kSmBlocks; ++b) key[b] = b < nblk ? sm_key(s.bmax[b][tid]) : 0u;
+      int round = 0;
 #pragma unroll 1
-      for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1) {
+      for (unsigned bit = 0x80000000u; bit >= 0x10000u; bit >>= 1, round ^= 1) {
         int n = 0;
 #pragma unroll
         for (int b = 0; b < kSmBlocks; ++b) n += key[b] >= (bound | bit);
-        if (__reduce_add_sync(0xffffffffu, n) >= j) bound |= bit;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) s.nkey[round][warp] = n;
+        __syncthreads();
+        n = 0;
+#pragma unroll
+        for (int w = 0; w < kSmWarps; ++w) n += s.nkey[round][w];
+        if (n >= j) bound |= bit;
       }
     }
-    if (lane == 0) s.rkey[warp] = bound;
+    if (tid == 0) s.xkey = bound;
   }
   __syncthreads();
   float cm = s.red[0];
@@ -1109,14 +1135,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   }
   if (tid == 0) {
     float sum = 0.0f;
-    unsigned key = 0xffffffffu;
-    for (int w = 0; w < kSmWarps; ++w) {
-      if (sums) sum += s.red[w];
-      if (k > 0) key = min(key, s.rkey[w]);
-    }
+    if (sums)
+      for (int w = 0; w < kSmWarps; ++w) sum += s.red[w];
     s.xmax = cm;
     s.xsum = sum;
-    s.xkey = key;
   }
   t.sync();
   if (warp == 0) {
@@ -1236,7 +1258,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     else if (sums) tail += fixed(rel(bm, s.bsum[b][tid], M));
   }
   __syncthreads();
-  const uint32_t lead_n = peer(&s.n, 0), lead_key = peer(&s.key[0], 0), lead_g = peer(&s.gidx, 0);
+  const uint32_t lead_g = peer(&s.gidx, 0);
   const int items = s.nwork * U;
   for (int i = tid; i < items; i += kSmThreads) {
     const int id = s.work[i >> logU], v = t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
@@ -1256,10 +1278,11 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
       if (greedy) {
         peer_min(lead_g, (unsigned)(col + __ffs(hits) - 1));
       } else {
-        unsigned at = peer_add(lead_n, __popc(hits));
+        // (a list that is full already is left alone: thousands would queue for its number)
+        unsigned at = *static_cast<volatile unsigned *>(&s.n) > kSmList ? kSmList : atomicAdd(&s.n, __popc(hits));
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          if ((hits >> e & 1) && at < kSmList) peer_st64(lead_key + 8 * at, (u64)sm_key(x[e]) << 32 | (unsigned)~(col + e));
+          if ((hits >> e & 1) && at < kSmList) s.key[at] = (u64)sm_key(x[e]) << 32 | (unsigned)~(col + e);
           at += hits >> e & 1;
         }
       }
@@ -1282,11 +1305,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     return;                                       // (nobody reads another CTA's memory any more)
   }
-  const unsigned n = peer_ld32(lead_n);
-  if (size > 1) {                                 // the first CTA's memory stays until all have read n
-    cluster_arrive();
-    cluster_wait();
-  }
+  const unsigned n = t.join_lists();
   if (n <= kSmList) {
     if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u);
     return;
