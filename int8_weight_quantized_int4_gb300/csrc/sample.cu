@@ -23,9 +23,9 @@
 //      listed; for top-p the rest's weights are summed, blocks that do not reach it as they are.
 //   4. The first CTA resolves the list (some hundreds): bins of a quarter of an octave hold
 //      counts and sums; a border falls in one bin, whose elements compare themselves with each other.
-// A list that overflows (flat rows), or no filter at all, goes over the whole row instead: bins
-// of an eighth of an octave, the border's bin refined by the digits of the values, and
-// the draw by sums of ever smaller ranges.
+// A list that overflows (flat rows), or no filter at all, goes over the row instead: 256 bins of keys
+// with counts and weights, the border's bin refined until it fits a list, and the draw by sums
+// of ever smaller ranges.
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
@@ -42,7 +42,8 @@ namespace qw {
 constexpr int kSmThreads = 256;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBlocks = 8;                      // blocks a thread keeps the maxima of
-constexpr int kSmList = 1024;
+constexpr int kSmList = 2048;                     // elements a CTA lists
+constexpr int kSmShort = 1024;                    // of all CTAs of a row: the first one's alone
 constexpr int kSmBins = 256;
 constexpr int kSmMaxCluster = 16;
 constexpr int kSmFix = 40;                        // weights in units of 2^-40
@@ -63,35 +64,34 @@ struct SampleArgs {
 };
 
 struct SampleSmem {
-  float bmax[kSmBlocks][kSmThreads];
   union {
-    float bsum[kSmBlocks][kSmThreads];
-    u64 w[kSmList];
+    struct {
+      float bmax[kSmBlocks][kSmThreads], bsum[kSmBlocks][kSmThreads];
+    };
+    u64 w[kSmList];                               // (the blocks are done with when elements are weighed)
   };
   u64 key[kSmList];                               // order key << 32 | ~index
   union {
     unsigned short work[kSmBlocks * kSmThreads];
-    unsigned short order[kSmList];
+    unsigned short order[kSmShort];
   };
   unsigned short start[kSmBins + 1];
   unsigned cnt[kSmBins];                          // bins: elements,
   unsigned limb[3][kSmBins];                      // and weights in three terms of 14 bits (a row's slice has below 2^18
   u64 mass[kSmBins];                              // elements); or their sum
   float red[kSmWarps];
-  unsigned rkey[kSmWarps];
   int nkey[2][kSmWarps];
   u64 rsum[kSmWarps];
   float rsum3[3][kSmWarps];
   // read by the cluster's other CTAs
   float xmax, xsum, xsum3[2][3];
   unsigned xkey;
-  u64 xtotal, xkept;
+  u64 xtotal;
   // written by them (first CTA)
   unsigned n, gidx;
   u64 tail[kSmMaxCluster];
   // results of one thread or CTA for all
-  int bin, digit, found;
-  unsigned before;
+  int bin;
   u64 mbefore, total, top, thr;
   float rowmax, rowsum;
   unsigned rowkey;
@@ -131,11 +131,6 @@ __device__ __forceinline__ void peer_st32(uint32_t a, uint32_t v) {
 }
 __device__ __forceinline__ void peer_st64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned peer_add(uint32_t a, unsigned v) {
-  unsigned old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(a), "r"(v) : "memory");
-  return old;
 }
 __device__ __forceinline__ void peer_min(uint32_t a, unsigned v) {
   asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -295,6 +290,8 @@ struct SampleRow {
   }
 };
 
+__device__ __forceinline__ int sm_bin_shift(u64 range) { return max(0, 56 - __clzll((long long)range)); }      // range >> it <= 255
+
 // One CTA's place in the row's cluster.
 template <typename T>
 struct SampleCta {
@@ -316,18 +313,20 @@ struct SampleCta {
     }
   }
   __device__ __forceinline__ u64 weight(float x) const { return sm_weight<kExact>(x, sc); }
-  // The CTAs' lists, one behind the other in the first CTA's; their number (above kSmList: not
-  // joined).  After a sync(), and ends with one.
-  __device__ __forceinline__ unsigned join_lists() {
-    if (size == 1) return s.n;
+  // The CTAs' lists at `list`, one behind the other in the first CTA's, if they are `most` together or
+  // fewer; their number.  After a sync(), and ends with one.
+  __device__ __forceinline__ unsigned join_lists(u64 *list, unsigned most, bool &full) {
     unsigned n = 0, before = 0;
+    full = false;
     for (unsigned r = 0; r < size; ++r) {
       if (r == rank) before = n;
-      n += peer_ld32(peer(&s.n, r));
+      const unsigned m = size > 1 ? peer_ld32(peer(&s.n, r)) : s.n;
+      full |= m > kSmList;
+      n += m;
     }
-    if (n <= kSmList && rank > 0) {
-      const uint32_t to = peer(&s.key[0], 0) + 8 * before;
-      for (unsigned e = tid; e < s.n; e += kSmThreads) peer_st64(to + 8 * e, s.key[e]);
+    if (n <= most && rank > 0) {
+      const uint32_t to = peer(list, 0) + 8 * before;
+      for (unsigned e = tid; e < s.n; e += kSmThreads) peer_st64(to + 8 * e, list[e]);
     }
     sync();
     return n;
@@ -339,6 +338,33 @@ struct SampleCta {
     return y < (float)(kSmBins - 1) ? (int)y : kSmBins - 1;        // (NaN: the last)
   }
 
+  // bin tid's count or weight `v`: the first bin at which `need` is reached (-1: none; before it:
+  // s.mbefore), and the sum of all bins
+  __device__ __forceinline__ int pick(u64 v, u64 need, u64 &total) {
+    u64 incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) s.rsum[warp] = incl;
+    if (tid == 0) s.bin = -1;
+    __syncthreads();
+    total = 0;
+    u64 before = 0;
+    for (int w = 0; w < kSmWarps; ++w) {
+      if (w == warp) before = total;
+      total += s.rsum[w];
+    }
+    incl += before;
+    if (incl >= need && incl - v < need) {
+      s.bin = tid;
+      s.mbefore = incl - v;
+    }
+    __syncthreads();
+    return s.bin;
+  }
   // Calls f(x, column) for the elements of vectors a, a + step, .. < b; four loads at a time.  Places
   // outside the row are -inf.
   template <typename F>
@@ -539,7 +565,7 @@ template <typename T>
 __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
                                             float u) {
   SampleSmem &s = t.s;
-  constexpr int PER = kSmList / kSmThreads;
+  constexpr int PER = kSmShort / kSmThreads;
   const int tid = t.tid, lane = t.lane;
   for (int i = tid; i < kSmBins; i += kSmThreads) {
     s.cnt[i] = 0;
@@ -581,9 +607,9 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
       const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) s.rkey[t.warp] = incl;
+    if (lane == 31) s.nkey[0][t.warp] = (int)incl;
     __syncthreads();
-    for (int v = 0; v < t.warp; ++v) incl += s.rkey[v];
+    for (int v = 0; v < t.warp; ++v) incl += (unsigned)s.nkey[0][v];
     s.start[tid + 1] = (unsigned short)incl;
     if (tid == 0) s.start[0] = 0;
     __syncthreads();
@@ -728,101 +754,6 @@ struct SampleCut {
   __device__ __forceinline__ bool stays(unsigned key, int col) const { return key > K || (key == K && col <= I); }
 };
 
-// The cut that leaves the first `need` elements of those within `in` (need their number, or
-// their weights' sum: the shortest beginning that reaches it), one at least.
-template <typename T>
-__device__ __forceinline__ SampleCut sample_cut(SampleCta<T> &t, const SampleCut &in, u64 need, bool by_mass) {
-  SampleSmem &s = t.s;
-  unsigned prefix = 0, mask = 0;
-  int bin = -1;
-  u64 before = 0;
-  need = max(need, 1ull);
-  // bins of an eighth of an octave first, then the digits of the keys
-  constexpr int kDigits = sizeof(T) == 4 ? 4 : SampleRow<T>::kBf ? 2 : 3;      // (of 16-bit types the rest is all alike)
-  for (int round = 0; round <= kDigits; ++round) {
-    const int shift = 32 - 8 * round;
-    t.sync();                                     // the others have read the last round's bins
-    s.cnt[t.tid] = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) s.limb[i][t.tid] = 0;
-    __syncthreads();
-    t.each([&](float x, int col) {
-      const unsigned key = sm_key(x);
-      if ((key & mask) != prefix || !in.stays(key, col)) return;
-      if ((unsigned)col >= (unsigned)t.row.N) return;
-      const int b = t.bin_of(x, 8.0f);
-      if (round > 0 && b != bin) return;
-      const int d = round == 0 ? b : 255 - (int)((key >> shift) & 255u);       // larger values first
-      if (by_mass) {
-        const u64 w = t.weight(x);
-        if (w == 0) return;
-        atomicAdd(&s.limb[0][d], (unsigned)w & 0x3fffu);
-        atomicAdd(&s.limb[1][d], (unsigned)(w >> 14) & 0x3fffu);
-        atomicAdd(&s.limb[2][d], (unsigned)(w >> 28));
-      } else {
-        atomicAdd(&s.cnt[d], 1u);
-      }
-    });
-    __syncthreads();
-    s.mass[t.tid] = by_mass ? (u64)s.limb[0][t.tid] + ((u64)s.limb[1][t.tid] << 14) + ((u64)s.limb[2][t.tid] << 28) : s.cnt[t.tid];
-    t.sync();
-    u64 v = s.mass[t.tid];
-    if (t.size > 1) {
-      v = 0;
-      for (unsigned r = 0; r < t.size; ++r) v += peer_ld64(peer(&s.mass[t.tid], r));
-    }
-    // running sums over the 256 bins, a bin a thread
-    u64 incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (t.lane >= o) incl += y;
-    }
-    if (t.lane == 31) s.rsum[t.warp] = incl;
-    if (t.tid == 0) s.digit = -1;
-    __syncthreads();
-    for (int w = 0; w < t.warp; ++w) incl += s.rsum[w];
-    incl += before;
-    if (incl >= need && incl - v < need) {        // one thread, or none where all stay
-      s.digit = t.tid;
-      s.mbefore = incl - v;
-    }
-    __syncthreads();
-    const int d = s.digit;
-    if (d < 0) return in;                         // (round 0 alone: together they do not reach it)
-    before = s.mbefore;
-    if (round == 0) {
-      bin = d;
-    } else {
-      prefix |= (unsigned)(255 - d) << shift;
-      mask |= 255u << shift;
-    }
-  }
-  // the low digits that all values of a 16-bit type share
-  if constexpr (sizeof(T) == 2) {
-    if (!(prefix >> 31)) prefix |= ~mask;
-  }
-  if (prefix <= 0x007fffffu) return in;           // -inf or NaN: they weigh nothing anyway
-  // how many of the equal ones stay
-  u64 ties = need - before;
-  if (by_mass) {
-    const u64 w = t.weight(sm_value(prefix));
-    ties = (ties + w - 1) / w;
-  }
-  if (t.tid == 0) s.found = 0x7fffffff;
-  __syncthreads();
-  t.template find<false>([&](float x, int col) { return (u64)(sm_key(x) == prefix && in.stays(prefix, col)); },
-         [&](u64) { return ties - 1; },
-         [&](int col, u64, u64) {
-           if (t.size > 1)
-             for (unsigned r = 0; r < t.size; ++r) peer_st32(peer(&s.found, r), (unsigned)col);
-           else
-             s.found = col;
-         });
-  t.sync();
-  return SampleCut{prefix, s.found};
-}
-
 // The draw among what the cut and min-p leave.
 template <typename T, bool ALL>
 __device__ __forceinline__ void sample_draw(const SampleArgs &a, SampleCta<T> &t, int r, const SampleCut &cut, float mp, float u) {
@@ -837,145 +768,151 @@ __device__ __forceinline__ void sample_draw(const SampleArgs &a, SampleCta<T> &t
       [&](u64 total) { return sample_target(u, total); },
       [&](int col, u64 w, u64 total) { sample_write(a, r, col, w, total); });
 }
-// Without bounds or lists: what a flat row's borders come to when even one bin overflows.
+// The same from the CTAs' lists (n of them in this one).
 template <typename T>
-__device__ __noinline__ void sample_row(const SampleArgs &a, SampleCta<T> t, int r, int k, float p, float mp, float u) {
-  SampleCut cut{0u, 0x7fffffff};
-  if (k > 0) cut = sample_cut(t, cut, (u64)k, false);
-  if (p < 1.0f) {
-    // the sum of what top-k left
-    const SampleCut in = cut;
-    t.template find<false>([&](float x, int col) { return in.stays(sm_key(x), col) ? t.weight(x) : 0ull; },
-           [&](u64 total) {
-             if (t.tid == 0) t.s.thr = sample_mass(p, total);
-             return ~0ull;                        // (no draw yet)
-           },
-           [](int, u64, u64) {});
-    __syncthreads();
-    const u64 need = t.s.thr;
-    cut = sample_cut(t, in, need, true);
+__device__ __forceinline__ void sample_draw_listed(const SampleArgs &a, SampleCta<T> &t, int r, int n, const SampleCut &cut, float mp, float u) {
+  SampleSmem &s = t.s;
+  const u64 least = (u64)ceil((double)mp * (double)(1ull << kSmFix));
+  u64 sum = 0;
+  t.sync();                                       // (the border's list, at the same place, has been read)
+  for (int e = t.tid; e < n; e += kSmThreads) {
+    const unsigned key = (unsigned)(s.key[e] >> 32);
+    u64 w = 0;
+    if (cut.stays(key, (int)~(unsigned)s.key[e])) w = t.weight(sm_value(key));
+    if (w < least) w = 0;
+    s.w[e] = w;
+    sum += w;
   }
-  sample_draw<T, false>(a, t, r, cut, mp, u);
+  u64 own;
+  (void)t.pick(sum, ~0ull, own);
+  if (t.tid == 0) s.xtotal = own;
+  t.sync();
+  u64 total = 0, before = 0;
+  for (unsigned q = 0; q < t.size; ++q) {
+    if (q == t.rank) before = total;
+    total += t.size > 1 ? peer_ld64(peer(&s.xtotal, q)) : s.xtotal;
+  }
+  const u64 target = sample_target(u, total);
+  if (target < before || target >= before + own) return;
+  u64 need = target - before + 1;
+  unsigned lo = 0, hi = (unsigned)t.row.N - 1;    // its column, refined by 256 bins a round
+  while (lo != hi) {
+    const int shift = sm_bin_shift(hi - lo);
+    s.mass[t.tid] = 0;
+    __syncthreads();
+    for (int e = t.tid; e < n; e += kSmThreads) {
+      const unsigned c = ~(unsigned)s.key[e];
+      if (c >= lo && c <= hi && s.w[e]) atomicAdd(&s.mass[(c - lo) >> shift], s.w[e]);
+    }
+    __syncthreads();
+    u64 all;
+    const int b = max(t.pick(s.mass[t.tid], need, all), 0);
+    need -= s.mbefore;
+    lo += (unsigned)b << shift;
+    hi = min(hi, lo + ((1u << shift) - 1));
+    __syncthreads();
+  }
+  for (int e = t.tid; e < n; e += kSmThreads)
+    if (~(unsigned)s.key[e] == lo) sample_write(a, r, (int)lo, s.w[e], total);
 }
 
-// The list that overflowed, by bins of an eighth of an octave: their counts and sums, the list of
-// the border's bin alone.  items(f): calls f(key, x, column) for the CTA's elements from the bound on.
-// false: that list overflows too.
+// The list that overflowed: composite keys (value, then column) refined by 256 bins a round, all from
+// one number of leading bits on, until the border's bin fits a list, which the first CTA refines
+// further.  items(f): calls f(composite, x) for the CTA's elements from the bound on, whose composites are
+// `lowest` at least.
 template <typename T, typename I>
-__device__ __forceinline__ bool sample_flat(SampleCta<T> &t, int k, float p, u64 tail, I items, SampleCut &cut) {
+__device__ __forceinline__ SampleCut sample_flat(SampleCta<T> &t, int k, float p, u64 tail, u64 lowest, I items) {
   SampleSmem &s = t.s;
-  const int tid = t.tid, lane = t.lane, warp = t.warp;
-  s.cnt[tid] = 0;
+  const int tid = t.tid;
+  auto pick = [&](u64 v, u64 need, u64 &total) { return t.pick(v, need, total); };
+  // The composite of the element up to which `need` is reached, in descending order from `high` down
+  // to `low`: a number of elements, or (by_mass) a weight; share >= 0: that share of all weights and `tail`.
+  auto border = [&](u64 high, u64 low, u64 need, bool by_mass, float share, u64 &found) {
+    const u64 all = low;
+    for (;;) {
+      const u64 range = high - low;
+      const int shift = sm_bin_shift(range);
+      t.sync();                                   // the last round's bins have been read
+      s.cnt[tid] = 0;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) s.limb[i][tid] = 0;
-  __syncthreads();
-  items([&](unsigned, float x, int) {
-    const int b = t.bin_of(x, 8.0f);
-    const u64 w = t.weight(x);
-    atomicAdd(&s.cnt[b], 1u);
-    atomicAdd(&s.limb[0][b], (unsigned)w & 0x3fffu);
-    atomicAdd(&s.limb[1][b], (unsigned)(w >> 14) & 0x3fffu);
-    atomicAdd(&s.limb[2][b], (unsigned)(w >> 28));
-  });
-  __syncthreads();
-  s.mass[tid] = (u64)s.limb[0][tid] + ((u64)s.limb[1][tid] << 14) + ((u64)s.limb[2][tid] << 28);
-  t.sync();
-  // bin tid's and the running sums, of the whole row
-  u64 mass = 0, number = 0;
-  for (unsigned r = 0; r < t.size; ++r) {
-    mass += t.size > 1 ? peer_ld64(peer(&s.mass[tid], r)) : s.mass[tid];
-    number += t.size > 1 ? peer_ld32(peer(&s.cnt[tid], r)) : s.cnt[tid];
-  }
-  auto running = [&](u64 v, u64 &total) {
-    u64 incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int i = 0; i < 3; ++i) s.limb[i][tid] = 0;
+      if (tid == 0) s.n = 0;
+      __syncthreads();
+      items([&](u64 c, float x) {
+        if (c < low || c > high) return;
+        const int b = (int)((high - c) >> shift);
+        atomicAdd(&s.cnt[b], 1u);
+        if (by_mass) {
+          const u64 w = t.weight(x);
+          atomicAdd(&s.limb[0][b], (unsigned)w & 0x3fffu);
+          atomicAdd(&s.limb[1][b], (unsigned)(w >> 14) & 0x3fffu);
+          atomicAdd(&s.limb[2][b], (unsigned)(w >> 28));
+        }
+      });
+      __syncthreads();
+      s.mass[tid] = (u64)s.limb[0][tid] + ((u64)s.limb[1][tid] << 14) + ((u64)s.limb[2][tid] << 28);
+      t.sync();
+      u64 mass = 0, number = 0, total;
+      for (unsigned r = 0; r < t.size; ++r) {
+        number += t.size > 1 ? peer_ld32(peer(&s.cnt[tid], r)) : s.cnt[tid];
+        if (by_mass) mass += t.size > 1 ? peer_ld64(peer(&s.mass[tid], r)) : s.mass[tid];
+      }
+      if (share >= 0.0f) {
+        (void)pick(mass, 0, total);
+        need = max(sample_mass(share, total + tail), 1ull);
+        share = -1.0f;
+      }
+      const int b = pick(by_mass ? mass : number, need, total);
+      if (b < 0) {                                // all of them stay
+        found = all;
+        return;
+      }
+      need -= s.mbefore;
+      if (tid == b) s.total = number;
+      high -= (u64)b << shift;
+      low = max(low, high - min(high, (1ull << shift) - 1));
+      __syncthreads();
+      if (s.total <= kSmList) break;
     }
-    __syncthreads();
-    if (lane == 31) s.rsum[warp] = incl;
-    __syncthreads();
-    total = 0;
-    u64 before = 0;
-    for (int w = 0; w < kSmWarps; ++w) {
-      if (w == warp) before = total;
-      total += s.rsum[w];
-    }
-    return incl + before;
-  };
-  // The element of bin b up to which `need` more are reached (by number, or by weight among those
-  // from `floor` on): its composite key to everyone, and what stays of the bin weighs `kept`.
-  auto border = [&](int b, u64 need, bool by_mass, u64 floor, u64 &found, u64 &kept) {
-    t.sync();                                     // the last list, and its number, have been read
-    if (tid == 0) s.n = 0;
-    __syncthreads();
-    items([&](unsigned key, float x, int col) {
-      if (t.bin_of(x, 8.0f) != b) return;
-      const u64 c = (u64)key << 32 | (unsigned)~col;
-      if (c < floor) return;
-      const unsigned at = *static_cast<volatile unsigned *>(&s.n) > kSmList ? kSmList : atomicAdd(&s.n, 1u);
-      if (at < kSmList) s.key[at] = c;
+    // the list of the border's bin
+    items([&](u64 c, float) {
+      if (c < low || c > high) return;
+      s.w[atomicAdd(&s.n, 1u)] = c;
     });
     t.sync();
-    const unsigned n = t.join_lists();
-    if (n > kSmList) return false;
+    bool full;
+    const int n = (int)t.join_lists(s.w, kSmList, full);
     if (t.rank == 0) {
-      if (tid == 0) s.total = 0;
-      for (unsigned e = tid; e < n; e += kSmThreads) s.w[e] = t.weight(sm_value((unsigned)(s.key[e] >> 32)));
-      __syncthreads();
-      for (unsigned e = tid; e < n; e += kSmThreads) {
-        const u64 mine = s.key[e];
-        u64 above = 0;
-#pragma unroll 4
-        for (unsigned o = 0; o < n; ++o)
-          if (s.key[o] > mine) above += by_mass ? s.w[o] : 1ull;
-        if (above < need) atomicAdd(&s.total, s.w[e]);
-        if (above < need && above + (by_mass ? s.w[e] : 1ull) >= need)
-          for (unsigned r = 0; r < t.size; ++r) peer_st64(peer(&s.top, r), mine);
+      while (high != low) {
+        const int shift = sm_bin_shift(high - low);
+        __syncthreads();
+        s.mass[tid] = 0;
+        __syncthreads();
+        for (int e = tid; e < n; e += kSmThreads)
+          if (s.w[e] >= low && s.w[e] <= high)
+            atomicAdd(&s.mass[(int)((high - s.w[e]) >> shift)], by_mass ? t.weight(sm_value((unsigned)(s.w[e] >> 32))) : 1ull);
+        __syncthreads();
+        u64 total;
+        const int b = max(pick(s.mass[tid], need, total), 0);
+        need -= s.mbefore;
+        high -= (u64)b << shift;
+        low = max(low, high - min(high, (1ull << shift) - 1));
       }
-      __syncthreads();
       if (tid == 0)
-        for (unsigned r = 0; r < t.size; ++r) peer_st64(peer(&s.xkept, r), s.total);
+        for (unsigned r = 0; r < t.size; ++r) peer_st64(peer(&s.top, r), high);
     }
     t.sync();
     found = s.top;
-    kept = s.xkept;
-    return true;
   };
-  u64 total, floor = 0;
-  auto pick = [&](bool here, u64 before) {        // one thread's bin and what lies before it, to all
-    __syncthreads();
-    if (tid == 0) s.bin = -1;
-    __syncthreads();
-    if (here) {
-      s.bin = tid;
-      s.mbefore = before;
-    }
-    __syncthreads();
-    return s.bin;
-  };
-  if (tid == 0) s.top = 0;
-  if (k > 0) {
-    const u64 incl = running(number, total);
-    const int kb = pick(incl >= (u64)k && incl - number < (u64)k, incl - number);
-    if (kb >= 0) {
-      u64 kept;
-      if (!border(kb, (u64)k - s.mbefore, false, 0, floor, kept)) return false;
-      mass = tid < kb ? mass : tid == kb ? kept : 0;
-    }
-  }
+  const u64 highest = (u64)sm_key(t.sc.M) << 32 | 0xffffffffu;
+  u64 floor = lowest;
+  if (k > 0) border(highest, floor, (u64)k, false, -1.0f, floor);
   if (p < 1.0f) {
-    const u64 incl = running(mass, total);
-    const u64 need = max(sample_mass(p, total + (k > 0 ? 0 : tail)), 1ull);
-    const int pb = pick(incl >= need && incl - mass < need, incl - mass);
-    if (pb >= 0) {
-      u64 kept;
-      if (!border(pb, need - s.mbefore, true, floor, floor, kept)) return false;
-    }
+    u64 found;
+    border(highest, floor, 0, true, p, found);    // (of what top-k left, or with the tail of all)
+    floor = found;
   }
-  cut = SampleCut{(unsigned)(floor >> 32), floor == 0 ? 0x7fffffff : (int)~(unsigned)floor};
-  return true;
+  return SampleCut{(unsigned)(floor >> 32), (int)min(~(unsigned)floor, 0x7fffffffu)};
 }
 
 // ---------------------------------------------------------------- the kernel --
@@ -1305,8 +1242,9 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     }
     return;                                       // (nobody reads another CTA's memory any more)
   }
-  const unsigned n = t.join_lists();
-  if (n <= kSmList) {
+  bool full;
+  const unsigned n = t.join_lists(s.key, kSmShort, full);
+  if (n <= kSmShort) {
     if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u);
     return;
   }
@@ -1314,25 +1252,47 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   u64 rest = 0;
   if (sums)
     for (unsigned q = 0; q < size; ++q) rest += peer_ld64(peer(&s.tail[q], 0));
-  SampleCut cut;
-  const bool fine = sample_flat<T>(
-      t, k, p, rest,
-      [&](auto f) {
-        for (int i = tid; i < items; i += kSmThreads) {
-          const int id = s.work[i >> logU], v = t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
-          if (v >= t.v1) continue;
-          float x[VE];
-          t.row.floats(t.row.load(v), x);
+  if (!full) {                                    // every CTA's list holds its elements
+    const int own = (int)s.n;
+    const SampleCut cut = sample_flat<T>(t, k, p, rest, (u64)T0 << 32, [&](auto f) {
+      for (int e = tid; e < own; e += kSmThreads) f(s.key[e], sm_value((unsigned)(s.key[e] >> 32)));
+    });
+    sample_draw_listed<T>(a, t, r, own, cut, mp, u);
+    t.sync();
+    return;
+  }
+  const SampleCut cut = sample_flat<T>(t, k, p, rest, (u64)T0 << 32, [&](auto f) {
+    auto at = [&](int i) {
+      const int id = s.work[i >> logU];
+      return t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
+    };
+    for (int i = tid; i < items; i += 4 * kSmThreads) {
+      uint4 raw[4];
+      int v[4];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const unsigned key = sm_key(x[e]);
-            if (key >= T0) f(key, x[e], t.row.col(v) + e);
-          }
+      for (int q = 0; q < 4; ++q) {
+        v[q] = i + q * kSmThreads < items ? at(i + q * kSmThreads) : t.v1;
+        raw[q] = v[q] < t.v1 ? t.row.load(v[q]) : t.row.nothing();
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float x[VE];
+        t.row.floats(raw[0], x);
+        const int col = t.row.col(v[0]);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const unsigned key = sm_key(x[e]);
+          if (key >= T0) f((u64)key << 32 | (unsigned)~(col + e), x[e]);
         }
-      },
-      cut);
-  if (fine) sample_draw<T, false>(a, t, r, cut, mp, u);
-  else sample_row<T>(a, t, r, k, p, mp, u);
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+          raw[z] = raw[z + 1];
+          v[z] = v[z + 1];
+        }
+      }
+    }
+  });
+  sample_draw<T, false>(a, t, r, cut, mp, u);
   t.sync();
 }
 
@@ -1367,12 +1327,18 @@ extern "C" int sample_tokens(const void *logits, int dtype, int M, int N, long l
   SampleArgs a{logits,           u,          set->temperatures, set->top_ps, set->min_ps, set->top_ks, set->temperature,
                set->top_p,       set->min_p, set->top_k,        row_stride,  M,           N,           token,
                logprob};
-  // CTAs a row: as many as the GPU holds four an SM of, 2048 elements each at least, and so that
-  // a CTA's part has below 2^18 elements
   int cluster = 1;
-  const int most = M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8;     // (16 have to fit one part of the GPU)
-  while (cluster < most && ((2ll * cluster * M <= 4ll * sms && 2 * cluster * 2048 <= N) || N / cluster >= (1 << 18) - 16))
-    cluster *= 2;
+  // CTAs a row: the waves of CTAs (four an SM) times a CTA's elements, a row's steps counted as
+  // 32768 (768 x 50257: 46 us with one CTA a row, 64 with two).  16 have to fit one part of the GPU; a CTA's part
+  // has below 2^18 elements.
+  long long best = 0;
+  for (int c = 1; c <= (M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8); c *= 2) {
+    const long long cost = ((long long)M * c + 4 * sms - 1) / (4 * sms) * (N / c + 32768);
+    if (N / c < (1 << 18) - 16 && (best == 0 || cost < best)) {
+      best = cost;
+      cluster = c;
+    }
+  }
   if ((long long)M * cluster > 0x7fffffffll) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many rows");
   const void *f = dtype == QW_F16    ? reinterpret_cast<const void *>(sample_kernel<__half>)
                   : dtype == QW_BF16 ? reinterpret_cast<const void *>(sample_kernel<__nv_bfloat16>)
