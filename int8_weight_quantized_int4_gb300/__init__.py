@@ -883,13 +883,13 @@ def token_logprobs(logits, tokens, k: int = 0, ws: Workspace | None = None) -> T
 
 
 # ------------------------------------------------- trees of drafted tokens --
-def _ints(t, name, n, index):
-    """Checks an int32 [n] (any length for n None) on device `index`; returns its length."""
-    if t.dtype is not _i32 or t.get_device() != index:
-        raise TypeError(f"{name} must be int32 on the device of the others, got {t.dtype} on {t.device}")
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous [{'T' if n is None else n}], got {tuple(t.shape)}")
-    return t.shape[0]
+def _need_ints(index, *named):
+    """Raises for what is no contiguous int32 vector of the given length on device `index`; named: (tensor, name, length)."""
+    for t, name, n in named:
+        if t.dtype is not _i32 or t.get_device() != index or index < 0:
+            raise TypeError(f"{name} must be int32 on one CUDA device with the others, got {t.dtype} on {t.device}")
+        if t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{n}], got {tuple(t.shape)}")
 
 
 def attn_tree(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, parents, max_nodes: int = 64, window: int = 0,
@@ -903,7 +903,8 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, parents, max
     cache, dtype, heads, d = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
     batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
     T, Hq, qt, qh = _rows(q, "q", dtype, d, index, 0)
-    _ints(parents, "parents", T, index)
+    if parents.dtype is not _i32 or parents.get_device() != index or parents.shape != (T,) or not parents.is_contiguous():
+        _need_ints(index, (parents, "parents", T))
     if out is None:
         out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
     elif out.dtype is not q.dtype or out.shape != q.shape or out.get_device() != index or not out.is_contiguous():
@@ -946,22 +947,23 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0) -> 
     index = logits.get_device()
     if dtype is None or index < 0:
         raise TypeError("logits must be a float16, bfloat16 or float32 CUDA tensor")
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [M, N] with contiguous rows")
-    M, N = logits.shape
+    M, N = shape
     row, col = logits.stride()
     if col != 1 and N > 1:
         raise ValueError("logits must be [M, N] with contiguous rows")
     if u.dtype is not _f32 or u.get_device() != index:
         raise TypeError("u must be float32 on the logits' device")
-    if u.shape != (M,) or not u.is_contiguous():
+    if u.shape != shape[:1] or not u.is_contiguous():
         raise ValueError(f"u must be a contiguous [{M}]")
     t, pt = _setting(temperature, "temperature", _f32, M, index)
     k, pk = _setting(top_k, "top_k", _i32, M, index)
     p, pp = _setting(top_p, "top_p", _f32, M, index)
     m, pm = _setting(min_p, "min_p", _f32, M, index)
-    token = torch.empty(M, dtype=_i32, device=logits.device)
-    logprob = torch.empty(M, dtype=_f32, device=logits.device)
+    logprob = torch.empty_like(u)
+    token = torch.empty_like(u, dtype=_i32)
     _run(index, _step_fn("sample_tokens"), logits.data_ptr(), dtype, M, N, row if M > 1 else 0, u.data_ptr(),
          _pack_sampling(t, p, m, k, pt, pp, pm, pk), token.data_ptr(), logprob.data_ptr(), _raw_stream(index))
     return SampledTokens(token, logprob)
@@ -977,21 +979,20 @@ def tree_accept(tokens, drawn, parents, cu_tokens, max_path: int) -> TreePath:
     """The path of each sequence's tree that the drawn tokens accept: node 0, and after a node
     its first child whose token is the one drawn at the node.  tokens, drawn, parents int32 [T]."""
     index = tokens.get_device()
-    if index < 0:
-        raise TypeError("tokens must be an int32 CUDA tensor")
-    T = _ints(tokens, "tokens", None, index)
-    _ints(drawn, "drawn", T, index)
-    _ints(parents, "parents", T, index)
-    B = _ints(cu_tokens, "cu_tokens", None, index) - 1
-    if B < 0:
-        raise ValueError("cu_tokens must be [B + 1]")
+    shape, cu = tokens.shape, cu_tokens.shape
+    if not (tokens.dtype is drawn.dtype is parents.dtype is cu_tokens.dtype is _i32 and shape == drawn.shape == parents.shape
+            and index == drawn.get_device() == parents.get_device() == cu_tokens.get_device() >= 0
+            and len(shape) == len(cu) == 1 and cu[0] > 0 and tokens.is_contiguous() and drawn.is_contiguous()
+            and parents.is_contiguous() and cu_tokens.is_contiguous()):
+        T = shape[0] if len(shape) else 0
+        _need_ints(index, (tokens, "tokens", T), (drawn, "drawn", T), (parents, "parents", T),
+                   (cu_tokens, "cu_tokens", max(cu[0] if len(cu) else 1, 1)))
     if not 1 <= max_path <= _INT_MAX:
         raise ValueError("max_path must be positive")
-    out = torch.empty(B * (max_path + 2), dtype=_i32, device=tokens.device)
-    path, count, following = out[:B * max_path].view(B, max_path), out[B * max_path:B * max_path + B], out[B * max_path + B:]
-    at = out.data_ptr()
+    B, dev, empty = cu[0] - 1, tokens.device, torch.empty
+    path, count, following = empty((B, max_path), dtype=_i32, device=dev), empty(B, dtype=_i32, device=dev), empty(B, dtype=_i32, device=dev)
     _run(index, _step_fn("tree_accept"), tokens.data_ptr(), drawn.data_ptr(), parents.data_ptr(), cu_tokens.data_ptr(), B,
-         T, max_path, at, at + 4 * B * max_path, at + 4 * B * (max_path + 1), _raw_stream(index))
+         shape[0], max_path, path.data_ptr(), count.data_ptr(), following.data_ptr(), _raw_stream(index))
     return TreePath(path, count, following)
 
 
@@ -1005,36 +1006,44 @@ def kv_keep_path(path, count, page_table, seq_lens, cu_tokens, *pools):
     if index < 0 or path.dtype is not _i32:
         raise TypeError("path must be an int32 CUDA tensor")
     batch = _kv_batch(page_table, seq_lens, cu_tokens, index)
-    B = page_table.shape[0]
-    if path.dim() != 2 or path.shape[0] != B or not path.is_contiguous():
+    shape = path.shape
+    if len(shape) != 2 or shape[0] != page_table.shape[0] or not path.is_contiguous():
         raise ValueError("path must be a contiguous [B, max_path]")
-    _ints(count, "count", B, index)
+    if count.dtype is not _i32 or count.get_device() != index or count.shape != shape[:1] or not count.is_contiguous():
+        _need_ints(index, (count, "count", shape[0]))
     if len(pools) > 4:
         raise ValueError("at most four pools")
-    desc, page = b"", 0
+    desc, page = [], 0
     for i, x in enumerate(pools):
         if x.get_device() != index:
             raise ValueError(f"pool {i} is on {x.device}, the path on {path.device}")
-        es, shape = x.element_size(), x.shape
-        stride = _strides(x) if 1 in shape else x.stride()
-        row = 1
-        if x.dtype is not _f32:
-            if len(shape) < 4 or stride[-1] != 1 and shape[-1] != 1:
+        dims, es = x.shape, x.element_size()
+        if x.dtype is _f32:                       # scales: a row is one number
+            if 1 in dims:
+                stride = _strides(x.unsqueeze(-1))[:-1]
+            else:
+                stride = x.stride()
+            row = 1
+        else:
+            stride = _strides(x) if 1 in dims else x.stride()
+            if len(dims) < 4 or stride[-1] != 1 and dims[-1] != 1:
                 raise ValueError(f"pool {i}: [(layers,) pages, Hkv, page, d] with d contiguous")
-            row, shape, stride = shape[-1], shape[:-1], stride[:-1]
-        elif 1 in shape[-1:]:
-            stride = (*stride[:-1], 0)
-        if len(shape) not in (3, 4):
+            row, dims, stride = dims[-1], dims[:-1], stride[:-1]
+        if len(dims) == 4:
+            layers, pages, heads, tokens = dims
+            sl, sp, sh, st = stride
+        elif len(dims) == 3:
+            layers, (pages, heads, tokens) = 1, dims
+            sl, (sp, sh, st) = 0, stride
+        else:
             raise ValueError(f"pool {i}: [(layers,) pages, Hkv, page, ...]")
-        if page and shape[-1] != page:
-            raise ValueError(f"pool {i} has pages of {shape[-1]} tokens, the others of {page}")
-        page = shape[-1]
-        lead = (shape[0], stride[0] * es) if len(shape) == 4 else (1, 0)
-        desc += _pack_rows(x.data_ptr(), lead[0], shape[-3], shape[-2], row * es, lead[1], stride[-3] * es, stride[-2] * es,
-                           stride[-1] * es)
-    lens = torch.empty(B, dtype=_i32, device=path.device)
-    _run(index, _step_fn("kv_keep_path"), desc or None, len(pools), batch, _INT_MAX, page or 1, path.data_ptr(),
-         count.data_ptr(), path.shape[1], lens.data_ptr(), _raw_stream(index))
+        if page and tokens != page:
+            raise ValueError(f"pool {i} has pages of {tokens} tokens, the others of {page}")
+        page = tokens
+        desc.append(_pack_rows(x.data_ptr(), layers, pages, heads, row * es, sl * es, sp * es, sh * es, st * es))
+    lens = torch.empty_like(count)
+    _run(index, _step_fn("kv_keep_path"), b"".join(desc) or None, len(desc), batch, _INT_MAX, page or 1, path.data_ptr(),
+         count.data_ptr(), shape[1], lens.data_ptr(), _raw_stream(index))
     return lens
 
 
