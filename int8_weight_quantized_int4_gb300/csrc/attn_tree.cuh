@@ -62,10 +62,10 @@ struct TreeSeg {
 };
 
 struct TreeCtl {
-  int nseg, more, team, member, size;             // size: CTAs of a team
-  int b, dead;
-  long long off, pos, begin, end, share;
-  long long part[16][kTreeMaxTeam];
+  int nseg, more, member, size;                   // size: CTAs of a team
+  int b, cost;                                    // cost: what an item takes beside its tiles
+  unsigned off, pos, begin, end, share;
+  unsigned part[16][kTreeMaxTeam], bare[16];
   unsigned long long bad;                         // keys of a tile whose values are not finite
   int zeroed;                                     // the segment (counted from 1) whose O was cleared before its first P V
 };
@@ -250,37 +250,33 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs &a, const TreeSeq &
   p.blocks = (int)(((long long)s.nodes * a.G + a.block_rows - 1) / a.block_rows);
   return p;
 }
-// a / b, 0 <= a, 0 < b: of 32 bits where they are (a third of the latency)
-__device__ __forceinline__ long long tree_div(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-// places of a sequence for teams of R
-template <int IC>
-__device__ __forceinline__ long long tree_places(const TreeArgs &a, const TreeSpan &p, int R) {
-  return (long long)((p.blocks + R - 1) / R) * a.Hkv * (p.n + IC);
+// Places of a sequence for teams of R: a tile takes one, an item `cost` more by itself.  All of a
+// call's stay below 2^32 (the host's bound).
+__device__ __forceinline__ unsigned tree_places(const TreeArgs &a, const TreeSpan &p, int R, int cost) {
+  return (unsigned)((p.blocks + R - 1) / R) * (unsigned)a.Hkv * (unsigned)(p.n + cost);
 }
 
 // Lists the range's next segments (one thread).
-template <int IC>
-__device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
+static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
   int n = 0, b = ctl->b;
-  long long off = ctl->off, pos = ctl->pos;
-  const int R = ctl->size;
+  unsigned off = ctl->off, pos = ctl->pos;
+  const unsigned begin = ctl->begin, end = ctl->end;
+  const int R = ctl->size, cost = ctl->cost;
 #pragma unroll 1
-  while (pos < ctl->end && n < kTreeSegs) {
+  while (pos < end && n < kTreeSegs) {
     const TreeSeq s = tree_seq(a, b);
     const TreeSpan p = tree_span(a, s);
-    const long long all = tree_places<IC>(a, p, R);
-    if (off >= all) {
+    if (off >= tree_places(a, p, R, cost)) {
       ++b;
       off = 0;
       continue;
     }
-    const int each = p.n + IC, groups = (p.blocks + R - 1) / R;
-    const int item = (int)tree_div(off, each), in = (int)(off - (long long)item * each);
-    const long long at = pos - in;                // the item's first place
-    const int g = item / groups, rb = (item - g * groups) * R + ctl->member;
-    const long long x0 = ctl->begin - at - IC, x1 = ctl->end - at - IC;
+    const unsigned each = (unsigned)(p.n + cost);
+    const int groups = (p.blocks + R - 1) / R;
+    const unsigned item = off / each, in = off - item * each;
+    const int g = groups == 1 ? (int)item : (int)item / groups, rb = ((int)item - g * groups) * R + ctl->member;
+    // the item's first place is pos - in, its first tile's `cost` further
+    const long long x0 = (long long)begin - pos + in - cost, x1 = (long long)end - pos + in - cost;
     const int u0 = x0 > 0 ? (int)x0 : 0, u1 = x1 < p.n ? (int)x1 : p.n;
     if (u0 < u1 && rb < p.blocks) {
       TreeSeg &q = segs[n++];
@@ -297,13 +293,14 @@ __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl
       q.tok0 = s.tok0;
       q.nodes = s.nodes;
       q.slot = u0 == 0 && u1 == p.n ? -1 : u0 > 0 ? 0 : 1;
-      q.parts = q.slot != 1 ? 0 : (int)(tree_div(at + IC + p.n - 1, ctl->share) - tree_div(at + IC, ctl->share)) + 1;
+      // (begun here: the tiles that are left, in shares)
+      q.parts = q.slot != 1 ? 0 : 1 + (int)((unsigned)(p.n - u1 + ctl->share - 1) / ctl->share);
     }
     pos += each - in;
     off += each - in;
   }
   ctl->nseg = n;
-  ctl->more = pos < ctl->end;
+  ctl->more = pos < end;
   ctl->b = b;
   ctl->off = off;
   ctl->pos = pos;
@@ -316,83 +313,123 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  long long sum[kTreeMaxTeam] = {};
+  const int most = a.blocks > 1 ? kTreeMaxTeam : 1;               // (one row block a sequence: no teams)
+  unsigned sum[kTreeMaxTeam] = {}, bare = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeSpan p = tree_span(a, tree_seq(a, b));
+    sum[0] += tree_places(a, p, 1, IC);
+    bare += tree_places(a, p, 1, 0);
+    if (most > 1) {
 #pragma unroll
-    for (int R = 1; R <= kTreeMaxTeam; ++R) sum[R - 1] += tree_places<IC>(a, p, R);
-  }
-  long long incl[kTreeMaxTeam];
-#pragma unroll
-  for (int k = 0; k < kTreeMaxTeam; ++k) {
-    incl[k] = sum[k];
-    if (a.B > 32 || warp == 0) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl[k], o);
-        if (lane >= o) incl[k] += y;
-      }
+      for (int R = 2; R <= kTreeMaxTeam; ++R) sum[R - 1] += tree_places(a, p, R, IC);
     }
-    if (lane == 31) ctl->part[warp][k] = incl[k];
   }
   if (tid == 0) {
     ctl->nseg = ctl->more = ctl->zeroed = 0;
     ctl->bad = 0;
   }
-  __syncthreads();
-  long long total[kTreeMaxTeam] = {}, before[kTreeMaxTeam] = {};
-  for (int w = 0; w < NW; ++w) {
+  // totals; up to 32 sequences are the first warp's
+  unsigned total[kTreeMaxTeam] = {};
+  auto over_warp = [&](unsigned v) { return __reduce_add_sync(0xffffffffu, v); };
+  if (a.B <= 32) {
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 0; k < kTreeMaxTeam; ++k) {
+        const unsigned v = k < most ? over_warp(sum[k]) : 0u;
+        if (lane == 0) ctl->part[0][k] = v;
+      }
+      const unsigned v = over_warp(bare);
+      if (lane == 0) ctl->bare[0] = v;
+    }
+  } else {
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k) {
-      if (w == warp) before[k] = total[k];
-      total[k] += ctl->part[w][k];
+      const unsigned v = k < most ? over_warp(sum[k]) : 0u;
+      if (lane == 0) ctl->part[warp][k] = v;
     }
+    const unsigned v = over_warp(bare);
+    if (lane == 0) ctl->bare[warp] = v;
+  }
+  __syncthreads();
+  unsigned tiles = 0;
+  for (int w = 0; w < (a.B <= 32 ? 1 : NW); ++w) {
+    tiles += ctl->bare[w];
+#pragma unroll
+    for (int k = 0; k < kTreeMaxTeam; ++k) total[k] += ctl->part[w][k];
   }
   // The team: a row block more a team saves reading K and V again from HBM, but CTAs whose
   // sequence has fewer blocks idle.  Compared: the tiles a CTA runs, times what a tile costs that
   // is read for one row block alone (3) or for several (2; the MMAs bound it then).
-  int R = 1;
-  long long best = tree_div(total[0], gridDim.x) * 3;
+  const unsigned grid = gridDim.x;
+  int R = 1, cost = IC;
+  unsigned W = total[0];
+  if (most > 1) {
+    unsigned best = total[0] / grid * 3;
 #pragma unroll
-  for (int k = 1; k < kTreeMaxTeam; ++k) {
-    if (total[k] == total[0] || (int)gridDim.x < k + 1) continue;
-    const long long cost = tree_div(total[k], (int)gridDim.x / (k + 1)) * 2;
-    if (cost < best) {
-      best = cost;
-      R = k + 1;
+    for (int k = 1; k < kTreeMaxTeam; ++k) {
+      if (total[k] == total[0] || grid < k + 1u) continue;
+      const unsigned c = total[k] / (grid / (k + 1u)) * 2;
+      if (c < best) {
+        best = c;
+        R = k + 1;
+        W = total[k];
+      }
     }
   }
-  long long W = 0, start = 0, mine = 0;
+  // few tiles: one or two a CTA, whatever an item costs
+  if (tiles <= 2 * grid) {
+    R = 1;
+    cost = 0;
+    W = tiles;
+  }
+  const unsigned teams = R == 1 ? grid : grid / (unsigned)R;
+  const unsigned team = R == 1 ? blockIdx.x : blockIdx.x / (unsigned)R;
+  const unsigned share = W == 0 ? 1 : (W - 1) / teams + 1;
+  const unsigned begin = team < teams && (unsigned long long)team * share < W ? team * share : W;
+  const unsigned end = W - begin < share ? W : begin + share;
+  // the sequence that the range begins in: running sums of its own team size
+  unsigned mine = 0, incl;
+  if (cost == 0) mine = bare;
+  else {
 #pragma unroll
-  for (int k = 0; k < kTreeMaxTeam; ++k) {
-    if (k == R - 1) {
-      W = total[k];
-      mine = sum[k];
-      start = before[k] + incl[k] - sum[k];
+    for (int k = 0; k < kTreeMaxTeam; ++k) mine = k == R - 1 ? sum[k] : mine;
+  }
+  incl = mine;
+  if (a.B > 32 || warp == 0) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
   }
-  const int teams = (int)gridDim.x / R;
-  const int team = (int)blockIdx.x / R;
-  long long share = tree_div(W + teams - 1, teams);
-  share = max(share, (long long)a.min_tiles + IC);
-  const long long begin = team < teams ? min((long long)team * share, W) : W, end = min(begin + share, W);
-  if (begin < end && start <= begin && begin < start + mine) {      // one thread
+  if (a.B > 32) {
+    for (int w = 0; w < warp; ++w) {
+      if (cost == 0) incl += ctl->bare[w];
+      else {
+#pragma unroll
+        for (int k = 0; k < kTreeMaxTeam; ++k) incl += k == R - 1 ? ctl->part[w][k] : 0u;
+      }
+    }
+  }
+  const unsigned start = incl - mine;
+  if (begin < end && start <= begin && begin - start < mine) {     // one thread
     ctl->size = R;
-    ctl->member = (int)blockIdx.x % R;
+    ctl->cost = cost;
+    ctl->member = R == 1 ? 0 : (int)blockIdx.x % R;
     ctl->share = share;
     ctl->begin = begin;
     ctl->end = end;
     int b = b0;
-    long long off = begin - start;
-    for (; b < b1; ++b) {
-      const long long c = tree_places<IC>(a, tree_span(a, tree_seq(a, b)), R);
+    unsigned off = begin - start;
+    for (; b + 1 < b1; ++b) {
+      const unsigned c = tree_places(a, tree_span(a, tree_seq(a, b)), R, cost);
       if (off < c) break;
       off -= c;
     }
     ctl->b = b;
     ctl->off = off;
     ctl->pos = begin;
-    tree_walk<IC>(a, segs, ctl);
+    tree_walk(a, segs, ctl);
   }
   __syncthreads();
 }
@@ -1140,7 +1177,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
     nsegs += nseg;
     if (!ctl->more) break;
     __syncthreads();                              // everyone has done the list
-    if (threadIdx.x == 0) tree_walk<Sh::kItemCost>(a, segs, ctl);
+    if (threadIdx.x == 0) tree_walk(a, segs, ctl);
     __syncthreads();
     if (ctl->nseg == 0 && !ctl->more) break;
   }
@@ -1168,7 +1205,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 }
 
 // ------------------------------------------------------------------ the join --
-// A CTA 32 rows of the item whose first part CTA blockIdx.x of attn_tree_kernel left: its parts are
+// A warp a row of the item whose first part CTA blockIdx.x of attn_tree_kernel left: its parts are
 // that CTA's second slot and the first slots of the same member of the next teams.
 constexpr int kJoinWarps = 8;
 template <int D, bool BF>
@@ -1180,21 +1217,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
   const TreeDesc d = a.desc[blockIdx.x];
   const size_t size = tree_part_floats(D);
   auto part = [&](int k) { return a.part + (size_t)(k == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + k * d.step)) * size; };
-  for (int r = blockIdx.y * 32 + warp; r < min(d.cols, (int)blockIdx.y * 32 + 32); r += kJoinWarps) {
-    float m = kTreeNoScore;
-    for (int k = lane; k < d.parts; k += 32) m = fmaxf(m, reinterpret_cast<const float2 *>(part(k) + (size_t)kTreeRows * D)[r].x);
+  const int r = blockIdx.y * kJoinWarps + warp;
+  if (r < d.cols) {
+    // the parts' references and sums, 32 at a time
+    auto head_of = [&](int k) { return k < d.parts ? reinterpret_cast<const float2 *>(part(k) + (size_t)kTreeRows * D)[r] : make_float2(kTreeNoScore, 0.0f); };
+    const float2 first = head_of(lane);
+    float m = first.x;
+    for (int k = lane + 32; k < d.parts; k += 32) m = fmaxf(m, head_of(k).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.0f, acc[PER] = {};
     for (int k0 = 0; k0 < d.parts; k0 += 32) {
-      float w = 0.0f, lk = 0.0f;
-      if (k0 + lane < d.parts) {
-        const float2 ml = reinterpret_cast<const float2 *>(part(k0 + lane) + (size_t)kTreeRows * D)[r];
-        w = tree_ex2(ml.x - m);
-        lk = ml.y * w;
-      }
+      const float2 ml = k0 == 0 ? first : head_of(k0 + lane);
+      const float w = k0 + lane < d.parts ? tree_ex2(ml.x - m) : 0.0f, lk = ml.y * w;
       const int n = min(d.parts - k0, 32);
-#pragma unroll 4
+#pragma unroll 8
       for (int k = 0; k < n; ++k) {
         const float *p = part(k0 + k) + (size_t)r * D + lane * PER;
         const float f = __shfl_sync(0xffffffffu, w, k);
@@ -1241,7 +1278,7 @@ cudaError_t launch_tree(const TreeArgs &a, int grid, cudaStream_t st) {
   e = launch_pdl(f, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, a);
   count_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(reinterpret_cast<const void *>(attn_tree_join_kernel<D, KV == kPagedBf16>), dim3(grid, kTreeRows / 32), dim3(32 * kJoinWarps),
+  e = launch_pdl(reinterpret_cast<const void *>(attn_tree_join_kernel<D, KV == kPagedBf16>), dim3(grid, kTreeRows / kJoinWarps), dim3(32 * kJoinWarps),
                  0, st, a);
   count_launch();
   return e;

@@ -158,7 +158,7 @@ struct TreeArgs {
   int q_tok_rows, q_head_rows;  // strides in rows of the maps
   int page_rows, head_rows, tok_rows;
   int B, T, Hq, Hkv, G, page, npages, max_pages, cap, window, sinks, page_shift;
-  int max_nodes, min_tiles;     // fewest tiles of keys a CTA takes
+  int max_nodes, blocks;        // row blocks of a sequence of max_nodes
   float scale_log2;
   float *part;                  // [CTAs][2][128 (d + 2)] partial sums (workspace)
   TreeDesc *desc;               // [CTAs] (workspace)
