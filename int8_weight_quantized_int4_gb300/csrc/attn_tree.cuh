@@ -66,7 +66,7 @@ struct TreeCtl {
   int b, cost;                                    // cost: what an item takes beside its tiles
   unsigned off, pos, begin, end, share;
   unsigned part[16][kTreeMaxTeam], bare[16];
-  unsigned long long bad;                         // keys of a tile whose values are not finite
+  unsigned long long bad[2];                      // keys of a group's tile whose values are not finite
   int zeroed;                                     // the segment (counted from 1) whose O was cleared before its first P V
 };
 
@@ -90,7 +90,7 @@ struct TreeShape {
   static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 16 : 0;
   static constexpr int kMaskWords = 9;            // a row's ancestors (256 bits) and the first key of its window
   // barriers, parents, masks, an exchange between the groups, the segments
-  static constexpr int kFixed = 512 + 512 + kTreeRows * kMaskWords * 4 + 2 * kTreeRows * 4 + kTreeSegs * (int)sizeof(TreeSeg) +
+  static constexpr int kFixed = 512 + 512 + kTreeRows * kMaskWords * 4 + 4 * kTreeRows * 4 + kTreeSegs * (int)sizeof(TreeSeg) +
                                 (int)sizeof(TreeCtl) + 64;
   static constexpr int kSmem = 1024 + kQ + kStages * kStage + kRaws * kRaw + kScaleBytes + kFixed;
   static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory");
@@ -326,7 +326,7 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   }
   if (tid == 0) {
     ctl->nseg = ctl->more = ctl->zeroed = 0;
-    ctl->bad = 0;
+    ctl->bad[0] = ctl->bad[1] = 0;
   }
   // totals; up to 32 sequences are the first warp's
   unsigned total[kTreeMaxTeam] = {};
@@ -460,13 +460,12 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   return r;
 }
 // O += p v for the keys of `found`, in the rows that see them; then their values are cleared.
-// The softmax warps, each group half of the channels; fresh: O holds nothing yet.
+// The warps of group grp; fresh: O holds nothing yet.
 template <int D, bool BF>
 __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t weights, uint32_t vst, unsigned long long found,
-                                          unsigned long long vis, bool fresh) {
-  const int c0 = (int)(threadIdx.x >> 7) * (D / 2);
+                                          unsigned long long vis, bool fresh, int grp) {
 #pragma unroll 1
-  for (int cc = c0; cc < c0 + D / 2; cc += 32) {
+  for (int cc = 0; cc < D; cc += 32) {
     uint32_t v[32];
     if (fresh) {
 #pragma unroll
@@ -502,12 +501,11 @@ __device__ __noinline__ void tree_add_bad(uint32_t o, uint32_t weights, uint32_t
     tmem_st32(o + cc, v);
   }
   tmem_wait_st();
-  named_bar_sync(1, 256);                         // everyone has read the values
+  named_bar_sync(10 + grp, 128);                  // everyone has read the values
   for (unsigned long long k = found; k; k &= k - 1) {
     const int j = __ffsll((long long)k) - 1;
-    if ((int)threadIdx.x < D / 8) {
-      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tree_chunk(vst, j, (int)threadIdx.x)), "r"(0) : "memory");
-    }
+    if ((int)(threadIdx.x & 127) < D / 8)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tree_chunk(vst, j, (int)(threadIdx.x & 127))), "r"(0) : "memory");
   }
   fence_proxy_async_smem();
 }
@@ -531,8 +529,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   uint8_t *fixed = gbase + kAt + Sh::kScaleBytes;
   short *par = reinterpret_cast<short *>(fixed + 512);                       // parents of the segment's nodes (256)
   uint32_t *masks = reinterpret_cast<uint32_t *>(fixed + 1024);              // [128][kMaskWords]
-  float *xch = reinterpret_cast<float *>(masks + kTreeRows * Sh::kMaskWords);   // [2][128]
-  TreeSeg *segs = reinterpret_cast<TreeSeg *>(xch + 2 * kTreeRows);
+  float *xch = reinterpret_cast<float *>(masks + kTreeRows * Sh::kMaskWords);   // [2][128], then [2][128] references
+  TreeSeg *segs = reinterpret_cast<TreeSeg *>(xch + 4 * kTreeRows);
   TreeCtl *ctl = reinterpret_cast<TreeCtl *>(reinterpret_cast<uint8_t *>(segs) + kTreeSegs * sizeof(TreeSeg));
   volatile WaitBlock *wctl = reinterpret_cast<volatile WaitBlock *>(ctl + 1);
   volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(const_cast<WaitBlock *>(wctl) + 1);
@@ -559,7 +557,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(p_full(b), 8);
+      mbar_init(p_full(b), 4);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -885,8 +883,11 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       }
     } else if (warp < 8) {
       // ------------------------------------------------------------ softmax --
-      // Group grp = 0, 1 of four warps takes keys 32 grp .. of a tile and half of O's columns; a
-      // thread a row.  Warps whose rows are all beyond the item's only keep the barriers going.
+      // Two groups of four warps take tiles in turn, a thread a row: while one group's weights are
+      // under way the other finds the next tile's largest scores (loads and stores of TMEM take
+      // hundreds of cycles beside the MMAs; with both groups on one tile, half the keys each, a tile
+      // took 2700 cycles, 3600 with int8).  The reference passes from tile to tile through shared memory.
+      // Warps whose rows are all beyond the item's only keep the barriers going.
       constexpr int ST = 256;
       const int grp = warp >> 2, row = threadIdx.x & 127;              // (TMEM lane)
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -930,9 +931,11 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         }
         // keys from this one on (before the tree) are in every row's window
         const int whole = a.window > 0 ? s.pos0 + s.nodes - a.window : 0;
-        float m_ref = kTreeNoScore, l = 0.0f;
-        for (int i = 0; i < n; ++i) {
-          const int gt = tiles + i, b = gt & 1;
+        float m_ref = kTreeNoScore, l = 0.0f;     // the group's sum, to the reference of its latest tile
+        float *refs = xch + 2 * kTreeRows + row;  // [2][128]: of the latest tiles
+        const int pass_on = 2 + 4 * grp + (warp & 3), take_over = 2 + 4 * (grp ^ 1) + (warp & 3);      // barriers of a row's two warps
+        for (int i = (tiles & 1) == grp ? 0 : 1; i < n; i += 2) {
+          const int gt = tiles + i, b = grp;
           const int base = tree_base(s, s.u0 + i);
           const bool masked = base + kTreeKeys > s.pos0 || (base < whole && base + kTreeKeys > a.sinks);
           unsigned long long vis = ~0ull;
@@ -950,20 +953,25 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             if (!real) vis = 0;
           }
-          const uint32_t vm = (uint32_t)(vis >> (32 * grp));
           bool stop = !pwait(s_full(b), (uint32_t)((gt >> 1) & 1));
           tc_fence_after();
-          const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys + 32 * grp);
-          const int sc = (gt % Sh::kScaleSlots) * kTreeKeys + 32 * grp;
-          // 16 scores from c0 on; int8: log2 of the weight times its value's scale.  They are read twice:
-          // 32 would not fit the registers of two CTAs an SM.
-          F2 x[8];
+          const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys);
+          const int sc = (gt % Sh::kScaleSlots) * kTreeKeys;
+          // NX scores from c0 on; int8: log2 of the weight times its value's scale.  Where the registers
+          // do not hold all 64 they are read twice.
+          constexpr int NX = D < 256 ? 16 : kI8 ? 32 : 64;
+          F2 x[NX / 2];
           auto scores = [&](int c0) {
-            uint32_t v[16];
-            tmem_ld16(sadr + (uint32_t)c0, v);
+            uint32_t v[NX];
+            if constexpr (NX == 16) tmem_ld16(sadr + (uint32_t)c0, v);
+            else if constexpr (NX == 32) tmem_ld32(sadr + (uint32_t)c0, v);
+            else {
+              tmem_ld32(sadr, *reinterpret_cast<uint32_t(*)[32]>(v));
+              tmem_ld32(sadr + 32u, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            }
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
+            for (int c = 0; c < NX; c += 2) {
               x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
               if constexpr (kI8) x[c / 2] = fma2(x[c / 2], *reinterpret_cast<const F2 *>(ksc + sc + c0 + c), *reinterpret_cast<const F2 *>(vlog + sc + c0 + c));
             }
@@ -971,19 +979,20 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           float top = -INFINITY;
           if (busy) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < 32; c0 += 16) {
+            for (int c0 = 0; c0 < kTreeKeys; c0 += NX) {
               scores(c0);
               float t0 = -INFINITY, t1 = -INFINITY;
               if (masked) {
+                const unsigned long long vm = vis >> c0;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < NX / 2; ++c) {
                   float p, r;
                   x[c].get(p, r);
-                  t0 = max3(t0, vm >> (c0 + 2 * c) & 1 ? p : -INFINITY, vm >> (c0 + 2 * c + 1) & 1 ? r : -INFINITY);
+                  t0 = max3(t0, vm >> (2 * c) & 1 ? p : -INFINITY, vm >> (2 * c + 1) & 1 ? r : -INFINITY);
                 }
               } else {
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
+                for (int c = 0; c < NX / 2; c += 2) {
                   float p, r;
                   x[c].get(p, r);
                   t0 = max3(t0, p, r);
@@ -995,71 +1004,79 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             if (!kI8) top = top == -INFINITY ? top : top * scale;
           }
-          // The reference moves only when a score passes it by 2^kPass (both warps of a row decide together);
-          // then O and l are rescaled, once the previous P V is done.
+          // The reference of the tile before, which moves only when a score passes it by 2^kPass; then O
+          // is rescaled, once the previous P V is done.
           stop = stop || wctl->abort;
-          if (named_bar_or(2 + (warp & 3), 64, stop || top > m_ref + kPass)) {
-            xch[grp * kTreeRows + row] = top;
-            named_bar_sync(2 + (warp & 3), 64);
-            top = fmaxf(top, xch[(grp ^ 1) * kTreeRows + row]);
-            float f = 1.0f;
-            if (top > m_ref + kPass) {
-              f = tree_ex2(m_ref - (top - kHead));
-              m_ref = top - kHead;
-            }
-            l *= f;
-            if (__any_sync(0xffffffffu, f != 1.0f) && i > 0) {
-              if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) stop = true;
-              tc_fence_after();
+          float before = kTreeNoScore;
+          if (i > 0) {
+            named_bar_sync(take_over, 64);
+            before = refs[(grp ^ 1) * kTreeRows];
+          }
+          const bool moves = top > before + kPass;
+          const float now = moves ? top - kHead : before;
+          if (i + 1 < n) {
+            refs[grp * kTreeRows] = now;
+            asm volatile("bar.arrive %0, %1;" ::"r"(pass_on), "r"(64) : "memory");
+          }
+          l *= tree_ex2(m_ref - now);
+          m_ref = now;
+          if (__any_sync(0xffffffffu, moves) && i > 0) {
+            const float f = tree_ex2(before - now);
+            if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) stop = true;
+            tc_fence_after();
 #pragma unroll 1
-              for (int cc = grp * DH; cc < (stop ? 0 : grp * DH + DH); cc += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + lane_base + cc, v);
-                tmem_wait_ld();
+            for (int cc = 0; cc < (stop ? 0 : D); cc += 32) {
+              uint32_t v[32];
+              tmem_ld32(tmem + lane_base + cc, v);
+              tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
-                tmem_st32(tmem + lane_base + cc, v);
-              }
-              tmem_wait_st();
+              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * f);
+              tmem_st32(tmem + lane_base + cc, v);
             }
+            tmem_wait_st();
           }
           // the weights of 16 keys over their scores: 8 columns of rounded pairs, 8 of what they leave
           auto weights = [&](auto partly) {
             const F2 sc2(scale, scale), neg(-m_ref, -m_ref), minus(-1.0f, -1.0f);
             F2 sum(0.0f, 0.0f);
 #pragma unroll 1
-            for (int c0 = 0; c0 < 32; c0 += 16) {
-              uint32_t hi[8], lw[8];
-              scores(c0);
+            for (int c0 = 0; c0 < kTreeKeys; c0 += NX) {
+              if constexpr (NX < kTreeKeys) scores(c0);
+              const unsigned long long vm = vis >> c0;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                F2 w = kI8 ? add2(x[c], neg) : fma2(x[c], sc2, neg);
-                float p, r;
-                w.get(p, r);
-                w = F2(tree_ex2(p), tree_ex2(r));
-                if constexpr (kI8) {
-                  w = mul2(w, *reinterpret_cast<const F2 *>(vinv + sc + c0 + 2 * c));
-                  if constexpr (decltype(partly)::value) {
-                    w.get(p, r);
-                    w = F2(vm >> (c0 + 2 * c) & 1 ? p : 0.0f, vm >> (c0 + 2 * c + 1) & 1 ? r : 0.0f);
+              for (int h = 0; h < NX; h += 16) {
+                uint32_t hi[8], lw[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  F2 w = kI8 ? add2(x[h / 2 + c], neg) : fma2(x[h / 2 + c], sc2, neg);
+                  float p, r;
+                  w.get(p, r);
+                  w = F2(tree_ex2(p), tree_ex2(r));
+                  const int at = sc + c0 + h + 2 * c;
+                  if constexpr (kI8) {
+                    w = mul2(w, *reinterpret_cast<const F2 *>(vinv + at));
+                    if constexpr (decltype(partly)::value) {
+                      w.get(p, r);
+                      w = F2(vm >> (h + 2 * c) & 1 ? p : 0.0f, vm >> (h + 2 * c + 1) & 1 ? r : 0.0f);
+                    }
+                    sum = add2(sum, w);
+                    w = mul2(w, *reinterpret_cast<const F2 *>(vsc + at));
                   }
-                  sum = add2(sum, w);
-                  w = mul2(w, *reinterpret_cast<const F2 *>(vsc + sc + c0 + 2 * c));
+                  w.get(p, r);
+                  if constexpr (decltype(partly)::value) {    // (hidden: also with scores or scales that are not finite)
+                    p = vm >> (h + 2 * c) & 1 ? p : 0.0f;
+                    r = vm >> (h + 2 * c + 1) & 1 ? r : 0.0f;
+                    w = F2(p, r);
+                  }
+                  if constexpr (!kI8) sum = add2(sum, w);
+                  hi[c] = tree_pack<kBf>(p, r);
+                  const float2 q = tree_unpack<kBf>(hi[c]);
+                  fma2(F2(q.x, q.y), minus, w).get(p, r);
+                  lw[c] = tree_pack<kBf>(p, r);
                 }
-                w.get(p, r);
-                if constexpr (decltype(partly)::value) {      // (hidden: also with scores or scales that are not finite)
-                  p = vm >> (c0 + 2 * c) & 1 ? p : 0.0f;
-                  r = vm >> (c0 + 2 * c + 1) & 1 ? r : 0.0f;
-                  w = F2(p, r);
-                }
-                if constexpr (!kI8) sum = add2(sum, w);
-                hi[c] = tree_pack<kBf>(p, r);
-                const float2 h = tree_unpack<kBf>(hi[c]);
-                fma2(F2(h.x, h.y), minus, w).get(p, r);
-                lw[c] = tree_pack<kBf>(p, r);
+                tmem_st8(sadr + (uint32_t)(c0 + h), hi);
+                tmem_st8(sadr + (uint32_t)(c0 + h) + 8u, lw);
               }
-              tmem_st8(sadr + (uint32_t)c0, hi);
-              tmem_st8(sadr + (uint32_t)c0 + 8u, lw);
             }
             float p, r;
             sum.get(p, r);
@@ -1078,27 +1095,27 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               const int st = stage + tree_v_stage(i, n);
               const uint32_t vst = st_s + (st % F) * Sh::kStage;
               stop = stop || !pwait(full(st % F), (uint32_t)((st / F) & 1));
-              if (threadIdx.x == 0) ctl->bad = 0;
-              named_bar_sync(1, ST);
+              if (row == 0) ctl->bad[grp] = 0;
+              named_bar_sync(10 + grp, 128);
               constexpr uint32_t e = kBf ? 0x7f80u : 0x7c00u;
               bool bad = false;
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                const uint32_t at = tree_chunk(vst, threadIdx.x >> 2, (threadIdx.x & 3) * (D / 32) + c);
+              for (int c = 0; c < D / 16; ++c) {
+                const uint32_t at = tree_chunk(vst, row >> 1, (row & 1) * (D / 16) + c);
                 uint32_t w[4];
                 asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 #pragma unroll
                 for (int k = 0; k < 4; ++k) bad |= (w[k] & e) == e || (w[k] >> 16 & e) == e;
               }
-              if (bad) atomicOr(&ctl->bad, 1ull << (threadIdx.x >> 2));
-              named_bar_sync(1, ST);
-              const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad);
+              if (bad) atomicOr(&ctl->bad[grp], 1ull << (row >> 1));
+              named_bar_sync(10 + grp, 128);
+              const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad[grp]);
               if (found) {
                 stop = stop || !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
                 tc_fence_after();
                 // (after a wait that gave up everyone goes on to the segment's end without waiting)
-                if (!named_bar_or(1, ST, stop)) tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0);
-                if (threadIdx.x == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
+                if (!named_bar_or(10 + grp, 128, stop)) tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0, grp);
+                if (row == 0 && i == 0) *static_cast<volatile int *>(&ctl->zeroed) = seg + 1;
               }
             }
           }
@@ -1112,9 +1129,15 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         // ---- the rows, or their parts
         const bool got = !aborted && pwait(o_done, (uint32_t)(seg & 1));
         xch[grp * kTreeRows + row] = l;
+        refs[grp * kTreeRows] = m_ref;
         if (named_bar_or(1, ST, !got || wctl->abort)) { aborted = true; break; }
         tc_fence_after();
-        l += xch[(grp ^ 1) * kTreeRows + row];
+        {
+          const float other = refs[(grp ^ 1) * kTreeRows], m = fmaxf(m_ref, other);      // (the latest tile's)
+          l = l * tree_ex2(m_ref - m) + xch[(grp ^ 1) * kTreeRows + row] * tree_ex2(other - m);
+          m_ref = m;
+        }
+        named_bar_sync(1, ST);                    // (both have read them)
         if (s.slot < 0) {
           const float inv = 1.0f / l;
           const long long at = (long long)(s.tok0 + node) * a.Hq + head;
