@@ -28,8 +28,8 @@
 //
 // Work: the tiles of every (sequence, KV head, block of 128 rows) item are laid end to end and cut into
 // one equal range a CTA; an item that a border cuts leaves (m, l, O) parts in the workspace, which a
-// second kernel joins.  Where sequences have several row blocks, R CTAs form a team that runs
-// one range, a row block each, so that K and V come from HBM once and from L2 for the others.
+// second kernel joins.  Where sequences have several row blocks, teams of CTAs run one range, a
+// row block each (tree_schedule).
 //
 // Roundings: each weight enters P V as two terms of the values' 16-bit type, p rounded and what
 // that leaves, so the products keep 22 bits of it (bf16: 16), all sums are binary32 and the output's
@@ -63,7 +63,7 @@ struct TreeSeg {
 
 struct TreeCtl {
   int nseg, more, member, size;                   // size: CTAs of a team
-  int b, cost;                                    // cost: what an item takes beside its tiles
+  int b, cost, all;                               // cost: what an item takes beside its tiles; all: one class alone
   unsigned off, pos, begin, end, share;
   unsigned part[16][kTreeMaxTeam], bare[16];
   unsigned long long bad[2];                      // keys of a group's tile whose values are not finite
@@ -80,9 +80,9 @@ struct TreeShape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
   static constexpr int kStage = kTreeKeys * D * 2;
-  static constexpr int kStages = kI8 ? (D == 64 ? 4 : 2) : D == 64 ? 8 : 4;
+  static constexpr int kStages = kI8 ? (D == 64 ? 4 : D == 256 ? 3 : 2) : D == 64 ? 8 : 4;
   static constexpr int kRaw = kI8 ? kTreeKeys * D : 0;                // a stage of codes
-  static constexpr int kRaws = !kI8 ? 0 : D == 256 ? 5 : D == 128 ? 3 : 8;
+  static constexpr int kRaws = !kI8 ? 0 : D == 256 ? 3 : D == 128 ? 3 : 8;
   static constexpr int kScaleSlots = D == 64 ? 16 : 8;   // tiles whose scales are kept (more than can be under way)
   static constexpr int kQ = kTreeRows * D * 2;
   static constexpr uint32_t kTmem = D == 256 ? 512 : 256;
@@ -256,6 +256,9 @@ __device__ __forceinline__ unsigned tree_places(const TreeArgs &a, const TreeSpa
   return (unsigned)((p.blocks + R - 1) / R) * (unsigned)a.Hkv * (unsigned)(p.n + cost);
 }
 
+// CTAs that share the row blocks of a sequence: one for each block, up to four
+__device__ __forceinline__ int tree_team(const TreeSpan &p) { return min(max(p.blocks, 1), kTreeMaxTeam); }
+
 // Lists the range's next segments (one thread).
 static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
   int n = 0, b = ctl->b;
@@ -266,7 +269,7 @@ static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, 
   while (pos < end && n < kTreeSegs) {
     const TreeSeq s = tree_seq(a, b);
     const TreeSpan p = tree_span(a, s);
-    if (off >= tree_places(a, p, R, cost)) {
+    if ((!ctl->all && tree_team(p) != R) || off >= tree_places(a, p, R, cost)) {
       ++b;
       off = 0;
       continue;
@@ -306,91 +309,98 @@ static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, 
   ctl->pos = pos;
 }
 
-// This CTA's team and range, and its first segments.  All threads.
+// This CTA's team and range, and its first segments.  All threads.  Sequences of as many row
+// blocks form a class, the CTAs are shared among the classes by their work, and a class's CTAs form
+// teams of one CTA a block that run one range of tiles together: K and V then come from HBM once
+// for all blocks, and no CTA idles beside a sequence of fewer.  (Teams of three for all, 12
+// sequences of two and three blocks: 216 us, a quarter of the CTAs' time idle.)
 template <int IC, int NW>
 __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
   constexpr int NT = 32 * NW;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + NT - 1) / NT;
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  const int most = a.blocks > 1 ? kTreeMaxTeam : 1;               // (one row block a sequence: no teams)
+  const int classes = a.blocks > 1 ? kTreeMaxTeam : 1;
   unsigned sum[kTreeMaxTeam] = {}, bare = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeSpan p = tree_span(a, tree_seq(a, b));
-    sum[0] += tree_places(a, p, 1, IC);
-    bare += tree_places(a, p, 1, 0);
-    if (most > 1) {
+    const int R = tree_team(p);
 #pragma unroll
-      for (int R = 2; R <= kTreeMaxTeam; ++R) sum[R - 1] += tree_places(a, p, R, IC);
-    }
+    for (int k = 0; k < kTreeMaxTeam; ++k)
+      if (k == R - 1) sum[k] += tree_places(a, p, R, IC);
+    bare += tree_places(a, p, 1, 0);
   }
   if (tid == 0) {
     ctl->nseg = ctl->more = ctl->zeroed = 0;
     ctl->bad[0] = ctl->bad[1] = 0;
   }
   // totals; up to 32 sequences are the first warp's
-  unsigned total[kTreeMaxTeam] = {};
   auto over_warp = [&](unsigned v) { return __reduce_add_sync(0xffffffffu, v); };
-  if (a.B <= 32) {
-    if (warp == 0) {
-#pragma unroll
-      for (int k = 0; k < kTreeMaxTeam; ++k) {
-        const unsigned v = k < most ? over_warp(sum[k]) : 0u;
-        if (lane == 0) ctl->part[0][k] = v;
-      }
-      const unsigned v = over_warp(bare);
-      if (lane == 0) ctl->bare[0] = v;
-    }
-  } else {
+  if (a.B > 32 || warp == 0) {
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k) {
-      const unsigned v = k < most ? over_warp(sum[k]) : 0u;
+      const unsigned v = k < classes ? over_warp(sum[k]) : 0u;
       if (lane == 0) ctl->part[warp][k] = v;
     }
     const unsigned v = over_warp(bare);
     if (lane == 0) ctl->bare[warp] = v;
   }
   __syncthreads();
-  unsigned tiles = 0;
+  unsigned total[kTreeMaxTeam] = {}, tiles = 0;
   for (int w = 0; w < (a.B <= 32 ? 1 : NW); ++w) {
     tiles += ctl->bare[w];
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k) total[k] += ctl->part[w][k];
   }
-  // The team: a row block more a team saves reading K and V again from HBM, but CTAs whose
-  // sequence has fewer blocks idle.  Compared: the tiles a CTA runs, times what a tile costs that
-  // is read for one row block alone (3) or for several (2; the MMAs bound it then).
   const unsigned grid = gridDim.x;
   int R = 1, cost = IC;
-  unsigned W = total[0];
-  if (most > 1) {
-    unsigned best = total[0] / grid * 3;
-#pragma unroll
-    for (int k = 1; k < kTreeMaxTeam; ++k) {
-      if (total[k] == total[0] || grid < k + 1u) continue;
-      const unsigned c = total[k] / (grid / (k + 1u)) * 2;
-      if (c < best) {
-        best = c;
-        R = k + 1;
-        W = total[k];
-      }
-    }
-  }
-  // few tiles: one or two a CTA, whatever an item costs
-  if (tiles <= 2 * grid) {
-    R = 1;
+  unsigned W = total[0], teams = grid, from = 0;          // the class's work, teams and first CTA
+  bool all = true;                                        // every sequence is of the class
+  if (tiles <= 2 * grid) {                                // few tiles: one or two a CTA, whatever an item costs
     cost = 0;
     W = tiles;
+  } else if (classes > 1) {
+    // CTAs of each class: its share of the work (a class of R: R a place), whole teams; what is left
+    // over goes to the class with most
+    float work[kTreeMaxTeam], sums = 0.0f;
+    int most = 0;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxTeam; ++k) {
+      work[k] = (float)total[k] * (float)(k + 1);
+      sums += work[k];
+      if (k > 0 && work[k] > work[most]) most = k;
+    }
+    unsigned n[kTreeMaxTeam], used = 0, big = 1;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxTeam; ++k) {
+      n[k] = total[k] == 0 ? 0u : max(1u, (unsigned)(work[k] / sums * (float)grid / (float)(k + 1)));       // teams
+      used += n[k] * (unsigned)(k + 1);
+      if (k == most) big = n[k];
+    }
+    const unsigned spare = grid - min(used, grid), over = used - min(used, grid);
+    unsigned at = 0;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxTeam; ++k) {
+      if (k == most) n[k] = max(big + spare / (unsigned)(k + 1), (over + k) / (unsigned)(k + 1) + 1) - (over + k) / (unsigned)(k + 1);
+      const unsigned end = at + n[k] * (unsigned)(k + 1);
+      if (blockIdx.x >= at && blockIdx.x < end) {
+        R = k + 1;
+        W = total[k];
+        teams = n[k];
+        from = at;
+      }
+      at = end;
+    }
+    if (blockIdx.x >= at) W = 0;                          // (fewer CTAs than a team are left over)
+    all = false;
   }
-  const unsigned teams = R == 1 ? grid : grid / (unsigned)R;
-  const unsigned team = R == 1 ? blockIdx.x : blockIdx.x / (unsigned)R;
+  const unsigned team = R == 1 ? blockIdx.x - from : (blockIdx.x - from) / (unsigned)R;
   const unsigned share = W == 0 ? 1 : (W - 1) / teams + 1;
   const unsigned begin = team < teams && (unsigned long long)team * share < W ? team * share : W;
   const unsigned end = W - begin < share ? W : begin + share;
-  // the sequence that the range begins in: running sums of its own team size
-  unsigned mine = 0, incl;
-  if (cost == 0) mine = bare;
-  else {
+  // the sequence that the range begins in: running sums of the class
+  unsigned mine = cost == 0 ? bare : 0u, incl;
+  if (cost != 0) {
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k) mine = k == R - 1 ? sum[k] : mine;
   }
@@ -403,26 +413,23 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
     }
   }
   if (a.B > 32) {
-    for (int w = 0; w < warp; ++w) {
-      if (cost == 0) incl += ctl->bare[w];
-      else {
-#pragma unroll
-        for (int k = 0; k < kTreeMaxTeam; ++k) incl += k == R - 1 ? ctl->part[w][k] : 0u;
-      }
-    }
+    for (int w = 0; w < warp; ++w) incl += cost == 0 ? ctl->bare[w] : ctl->part[w][R - 1];
   }
   const unsigned start = incl - mine;
   if (begin < end && start <= begin && begin - start < mine) {     // one thread
     ctl->size = R;
+    ctl->all = all;
     ctl->cost = cost;
-    ctl->member = R == 1 ? 0 : (int)blockIdx.x % R;
+    ctl->member = R == 1 ? 0 : (int)((blockIdx.x - from) % (unsigned)R);
     ctl->share = share;
     ctl->begin = begin;
     ctl->end = end;
     int b = b0;
     unsigned off = begin - start;
     for (; b + 1 < b1; ++b) {
-      const unsigned c = tree_places(a, tree_span(a, tree_seq(a, b)), R, cost);
+      const TreeSpan p = tree_span(a, tree_seq(a, b));
+      if (!all && tree_team(p) != R) continue;
+      const unsigned c = tree_places(a, p, R, cost);
       if (off < c) break;
       off -= c;
     }
