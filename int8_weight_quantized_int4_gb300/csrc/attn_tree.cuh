@@ -14,8 +14,8 @@
 //
 // Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 2
 // loading and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  A ring of stages, each
-// 64 rows of K or V, in the order K0 K1 V0 K2 V1 .. of a segment: scores of the next tile are
-// computed while the softmax works on the last.
+// 64 rows of K or V: the scores of the next tile (d = 256: two) are computed while the softmax works on
+// the last.
 //   - Rows come by TMA straight to the 128-byte swizzle: pages of a multiple of 8 rows in boxes of up
 //     to 64, other pages four rows a gather, from a map of rows one common divisor of the cache's
 //     strides apart (rows outside it are zeros).  (Gathers move 6 to 9 bytes a clock an SM; cp.async
@@ -47,7 +47,7 @@ namespace qw {
 
 constexpr int kTreeKeys = 64;                     // keys of a tile
 constexpr int kTreeRows = 128;                    // rows (columns of a KV head: node x head) of an item
-constexpr int kTreeSegs = 32;                     // segments listed at a time
+constexpr int kTreeSegs = 16;                     // segments listed at a time
 constexpr int kTreeMaxTeam = 4;
 constexpr float kTreeNoScore = -3.402823466e38f;
 
@@ -80,21 +80,24 @@ struct TreeShape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = tree_ctas(D);
   static constexpr int kStage = kTreeKeys * D * 2;
-  static constexpr int kStages = kI8 ? (D == 64 ? 4 : D == 256 ? 3 : 2) : D == 64 ? 8 : 4;
+  // tiles of K, and of V, in shared memory: rings of their own, each filled in the tiles' order by one
+  // warp and emptied by another, so that a wait's parity names one phase
+  static constexpr int kTiles = kI8 ? (D == 64 ? 2 : 1) : D == 64 ? 4 : 2;
   static constexpr int kRaw = kI8 ? kTreeKeys * D : 0;                // a stage of codes
-  static constexpr int kRaws = !kI8 ? 0 : D == 256 ? 3 : D == 128 ? 3 : 8;
-  static constexpr int kScaleSlots = D == 64 ? 16 : 8;   // tiles whose scales are kept (more than can be under way)
+  static constexpr int kRawK = !kI8 ? 0 : D == 256 ? 3 : D == 128 ? 2 : 4, kRawV = !kI8 ? 0 : D == 64 ? 4 : 2;
+  static constexpr int kScaleSlots = D == 64 ? 16 : D == 128 ? 6 : 8;     // tiles whose scales are kept (more than can be under way)
   static constexpr int kQ = kTreeRows * D * 2;
+  static constexpr int kAhead = D == 256 ? 2 : 1, kBufs = kAhead + 1;     // tiles whose scores are computed before P V of one
   static constexpr uint32_t kTmem = D == 256 ? 512 : 256;
-  static constexpr uint32_t kSCol = D;            // O [0, D), then two buffers of 64 columns of S and P
+  static constexpr uint32_t kSCol = D;            // O [0, D), then kBufs buffers of 64 columns of S and P
   static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 16 : 0;
   static constexpr int kMaskWords = 9;            // a row's ancestors (256 bits) and the first key of its window
   // barriers, parents, masks, an exchange between the groups, the segments
   static constexpr int kFixed = 512 + 512 + kTreeRows * kMaskWords * 4 + 4 * kTreeRows * 4 + kTreeSegs * (int)sizeof(TreeSeg) +
                                 (int)sizeof(TreeCtl) + 64;
-  static constexpr int kSmem = 1024 + kQ + kStages * kStage + kRaws * kRaw + kScaleBytes + kFixed;
+  static constexpr int kSmem = 1024 + kQ + 2 * kTiles * kStage + (kRawK + kRawV) * kRaw + kScaleBytes + kFixed;
   static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory");
-  static_assert(kStages + kRaws + 4 < 2 * kScaleSlots - 2, "scales outlive their use");
+  static_assert(kAhead + kTiles + kRawK + 2 <= kScaleSlots, "scales outlive their use");
   // what an item costs beside its tiles, in tiles: about the time of 192 KB
   static constexpr int kItemCost = 196608 / (2 * kStage / (kI8 ? 2 : 1));
 };
@@ -105,6 +108,9 @@ struct F2 {
   __device__ __forceinline__ F2() {}
   __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
   __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+struct alignas(16) F4 {
+  F2 a, b;
 };
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
@@ -444,10 +450,6 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
 // key base of tile u of a segment's item
 __device__ __forceinline__ int tree_base(const TreeSeg &s, int u) { return (u < s.nsu ? u : u - s.nsu + s.first) * kTreeKeys; }
 
-// The stage of a segment's K or V of its i-th tile of n, counted from the segment's first stage.
-__device__ __forceinline__ int tree_k_stage(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int tree_v_stage(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
-
 // bits a .. b - 1 of a word (clamped to 0 .. 64)
 __device__ __forceinline__ unsigned long long tree_bits(int a, int b) {
   a = max(a, 0);
@@ -522,13 +524,13 @@ template <int D, int KV>
 __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::kCtas) attn_tree_kernel(const __grid_constant__ TreeArgs a) {
   using Sh = TreeShape<D, KV>;
   constexpr bool kI8 = Sh::kI8, kBf = KV == kPagedBf16;
-  constexpr int F = Sh::kStages;
+  constexpr int F = Sh::kTiles;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw0 = smem_u32(smem_raw);
   const uint32_t sbase = (raw0 + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (sbase - raw0);
-  const uint32_t q_s = sbase, st_s = q_s + Sh::kQ, cd_s = st_s + F * Sh::kStage;
-  constexpr int kAt = Sh::kQ + F * Sh::kStage + Sh::kRaws * Sh::kRaw;
+  const uint32_t q_s = sbase, k_s = q_s + Sh::kQ, v_s = k_s + F * Sh::kStage, kc_s = v_s + F * Sh::kStage, vc_s = kc_s + Sh::kRawK * Sh::kRaw;      // (kc, vc: codes)
+  constexpr int kAt = Sh::kQ + 2 * F * Sh::kStage + (Sh::kRawK + Sh::kRawV) * Sh::kRaw;
   // int8, by tile: [slots][64] of K's scales times the softmax's, V's scales vs, log2 |vs| and 1 / |vs|
   float *ksc = reinterpret_cast<float *>(gbase + kAt);
   float *vsc = ksc + Sh::kScaleSlots * kTreeKeys, *vlog = vsc + Sh::kScaleSlots * kTreeKeys, *vinv = vlog + Sh::kScaleSlots * kTreeKeys;
@@ -541,34 +543,40 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   TreeCtl *ctl = reinterpret_cast<TreeCtl *>(reinterpret_cast<uint8_t *>(segs) + kTreeSegs * sizeof(TreeSeg));
   volatile WaitBlock *wctl = reinterpret_cast<volatile WaitBlock *>(ctl + 1);
   volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(const_cast<WaitBlock *>(wctl) + 1);
-  // barriers: full[F], empty[F], raw_full[], raw_empty[], then
-  auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (8 + s); };
-  auto raw_full = [&](int s) { return bars + 8u * (16 + s); };
-  auto raw_empty = [&](int s) { return bars + 8u * (24 + s); };
+  // barriers: of K's and V's rings ([4] each; int8 also of the codes'), then
+  auto full = [&](int isv, int slot) { return bars + 8u * (8 * isv + slot); };
+  auto empty = [&](int isv, int slot) { return bars + 8u * (8 * isv + 4 + slot); };
+  auto raw_full = [&](int isv, int slot) { return bars + 8u * (16 + 8 * isv + slot); };
+  auto raw_empty = [&](int isv, int slot) { return bars + 8u * (20 + 8 * isv + slot); };
   auto s_full = [&](int b) { return bars + 8u * (32 + b); };
-  auto p_full = [&](int b) { return bars + 8u * (34 + b); };
-  const uint32_t q_full = bars + 8 * 36, q_empty = bars + 8 * 37, o_step = bars + 8 * 38, o_done = bars + 8 * 39, o_free = bars + 8 * 40,
-                 drain = bars + 8 * 41;
+  auto p_full = [&](int b) { return bars + 8u * (36 + b); };
+  const uint32_t q_full = bars + 8 * 40, q_empty = bars + 8 * 41, o_done = bars + 8 * 43, o_free = bars + 8 * 44,
+                 drain = bars + 8 * 45;
+  // P V of tile gt is done.  One barrier a buffer: scores of tile gt follow P V of tile gt - kBufs, so
+  // a wait for the tile before names one phase.
+  auto o_step = [&](int gt) { return bars + 8u * (46 + gt % Sh::kBufs); };
+  auto o_phase = [&](int gt) { return (uint32_t)((gt / Sh::kBufs) & 1); };
   auto pwait = [&](uint32_t bar, uint32_t parity) { return tree_wait(bar, parity, wctl, a.wait_ns == 0); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < F; ++s) {
-      mbar_init(full(s), kI8 ? 32 * Sh::kWideners : 1);
-      mbar_init(empty(s), 1);
+    for (int v = 0; v < 2; ++v) {
+      for (int i = 0; i < F; ++i) {
+        mbar_init(full(v, i), kI8 ? 16 * Sh::kWideners : 1);
+        mbar_init(empty(v, i), 1);
+      }
+      for (int i = 0; i < (v ? Sh::kRawV : Sh::kRawK); ++i) {
+        mbar_init(raw_full(v, i), a.scale_boxes ? 1 : 33);
+        mbar_init(raw_empty(v, i), Sh::kWideners / 2);
+      }
     }
-    for (int s = 0; s < Sh::kRaws; ++s) {
-      mbar_init(raw_full(s), a.scale_boxes ? 1 : 33);
-      mbar_init(raw_empty(s), Sh::kWideners);
-    }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < Sh::kBufs; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(p_full(b), 4);
+      mbar_init(o_step(b), 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(o_step, 1);
     mbar_init(o_done, 1);
     mbar_init(o_free, 8);
     mbar_init(drain, 1);
@@ -588,11 +596,10 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   tree_schedule<Sh::kItemCost, Sh::kWarps>(a, segs, ctl);
 
   // the roles' counters run over all segments of all lists
-  int stage = 0;                                  // stages filled / emptied
   int tiles = 0;                                  // tiles
   int nsegs = 0;                                  // segments
   bool ok = true;
-  int last = -1, queries = 0;                     // loading: the last stage copied to slot `lane`; Qs copied
+  int last = -1, queries = 0;                     // loading: the last tile copied to slot `lane` (V: lane - 8); Qs copied
   TreeDesc desc{};                                // the item whose first part this CTA leaves
 
   for (;;) {
@@ -607,10 +614,9 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       // once a stage finds its instructions gone from the caches near it (250 of them took 1500
       // cycles).
       constexpr int CW = kI8 ? 1 : D / 64;                        // boxes or gathers side by side
-      constexpr int kRing = kI8 ? Sh::kRaws : F;
+      constexpr int NK = kI8 ? Sh::kRawK : F, NV = kI8 ? Sh::kRawV : F;
       constexpr int kRowBytes = kI8 ? D : 128;
       constexpr uint32_t kSlotBytes = kI8 ? Sh::kRaw : Sh::kStage;
-      const uint32_t ring = kI8 ? cd_s : st_s, full0 = kI8 ? raw_full(0) : full(0), empty0 = kI8 ? raw_empty(0) : empty(0);
       const int role = Sh::kLoaders == 2 ? warp - Sh::kLoadWarp : 2;      // 0: K and Q, 1: V, 2: all
       const int boxes = a.box ? kTreeKeys / a.box : 16;           // down a tile; a power of two
       const int chunk = lane / boxes;                             // this lane's 128 bytes (box: the only ones)
@@ -620,10 +626,13 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         const TreeSeg &s = segs[si];
         const int n = s.u1 - s.u0, seg = nsegs + si;
         const int *table = a.table + (long long)s.b * a.max_pages;
-        // waits for stage st's slot; false: give up
-        auto room = [&](int st, int slot) {
-          if (st >= kRing) ok = __all_sync(0xffffffffu, pwait(empty0 + 8u * slot, (uint32_t)((st / kRing - 1) & 1)));
-          if (ok && lane == slot) last = st;
+        // waits for the slot of tile gt of K or V; its barrier, and where it lies (false: give up)
+        auto room = [&](bool isv, int gt, uint32_t &bar, uint32_t &dst) {
+          const int ring = isv ? NV : NK, slot = gt % ring;
+          if (gt >= ring) ok = __all_sync(0xffffffffu, pwait(kI8 ? raw_empty(isv, slot) : empty(isv, slot), (uint32_t)((gt / ring - 1) & 1)));
+          if (ok && lane == slot + (isv ? 8 : 0)) last = gt;
+          bar = kI8 ? raw_full(isv, slot) : full(isv, slot);
+          dst = (kI8 ? isv ? vc_s : kc_s : isv ? v_s : k_s) + slot * kSlotBytes + mine;
           return ok;
         };
         auto queries_in = [&] {
@@ -695,7 +704,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 #pragma unroll 1
           for (int x = 0; x < stages; ++x) {      // K0 K1 V0 K2 V1 .., or a role's share of it
             const bool isv = role == 2 ? x == stages - 1 || (x >= 2 && !(x & 1)) : role == 1;
-            const int st = stage + (role == 2 ? x : role == 1 ? tree_v_stage(x, n) : tree_k_stage(x)), slot = st % kRing;
+            const int i = role != 2 ? x : isv ? (x == stages - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2;
             if (role != 2 || !isv) {
               vpid = pid;
               vrow = row;
@@ -705,8 +714,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               vrow = row;
             }
             const int p = role == 2 && isv ? vpid : pid, r0 = role == 2 && isv ? vrow : row;
-            if (!room(st, slot)) break;
-            const uint32_t bar = full0 + 8u * slot, dst = ring + slot * kSlotBytes + mine;
+            uint32_t bar, dst;
+            if (!room(isv, tiles + i, bar, dst)) break;
             const bool page = (unsigned)p < (unsigned)a.npages, on = p != -2;
             const int parts = __popc(__ballot_sync(0xffffffffu, on)), pages = kI8 ? __popc(__ballot_sync(0xffffffffu, page)) : 0;
             if (lane == 0)                        // (int8: the tile's scales come with its K)
@@ -721,14 +730,14 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             if constexpr (kI8) {
               if (a.scale_boxes) {
                 if (!isv && page) {
-                  const int to = ((tiles + (t - s.u0)) % Sh::kScaleSlots) * kTreeKeys + first;
+                  const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + first;
                   const long long from = ((long long)p * a.Hkv + s.g) * a.page + r0;
                   bulk_g2s_nohint(smem_u32(ksc + to), a.ks + from, a.box * 4, bar);
                   bulk_g2s_nohint(smem_u32(vsc + to), a.vs + from, a.box * 4, bar);
                 }
               } else {                            // (scales that are not aligned: one by one)
                 for (int q = 0; q < a.box && !isv && on; ++q) {
-                  const int to = ((tiles + (t - s.u0)) % Sh::kScaleSlots) * kTreeKeys + first + q;
+                  const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + first + q;
                   const long long from = page ? ((long long)p * a.Hkv + s.g) * a.page + r0 + q : 0;
                   cp_async4_zfill(smem_u32(ksc + to), a.ks + from, page ? 4u : 0u);
                   cp_async4_zfill(smem_u32(vsc + to), a.vs + from, page ? 4u : 0u);
@@ -745,7 +754,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           for (int x = 0; x < 2 * n; ++x) {
             const bool isv = x == 2 * n - 1 || (x >= 2 && !(x & 1));
             if (role != 2 && isv != (role == 1)) continue;
-            const int i = isv ? (x == 2 * n - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2, st = stage + x, slot = st % kRing;
+            const int i = isv ? (x == 2 * n - 1 ? n - 1 : x / 2 - 1) : (x + 1) / 2;
             const int j = tree_base(s, s.u0 + i) + 4 * quad;
             int pi = a.page_shift >= 0 ? j >> a.page_shift : j / a.page, r = j - pi * a.page;
             int row[4], pid[4], at[4];
@@ -764,8 +773,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               if (!page && pid[e] != -2) atomicCAS(a.err, 0, -9);
               row[e] = page ? pid[e] * a.page_rows + s.g * a.head_rows + at[e] * a.tok_rows : -1;
             }
-            if (!room(st, slot)) break;
-            const uint32_t bar = full0 + 8u * slot, dst = ring + slot * kSlotBytes + mine;
+            uint32_t bar, dst;
+            if (!room(isv, tiles + i, bar, dst)) break;
             if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes);
             __syncwarp();
             for (int c = chunk; c < CW; c += 2)
@@ -784,55 +793,62 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           }
         }
         tiles += n;
-        stage += 2 * n;
       }
     } else if (kI8 && warp >= Sh::kWiden0) {
       // ----------------------------------------------------------- widening --
-      const int t = threadIdx.x - 32 * Sh::kWiden0;
+      // Half of the warps widen K, the others V.
+      constexpr int WT = 16 * (kI8 ? Sh::kWideners : 2);          // threads a half
+      const int isv = warp >= Sh::kWiden0 + Sh::kWideners / 2;
+      const int t = threadIdx.x - 32 * Sh::kWiden0 - isv * WT;
+      const int ring = isv ? max(Sh::kRawV, 1) : max(Sh::kRawK, 1);
+      const uint32_t from_s = isv ? vc_s : kc_s, to_s = isv ? v_s : k_s;
       for (int si = 0; si < nseg && ok; ++si) {
         const int n = segs[si].u1 - segs[si].u0;
-        for (int i = 0; i < 2 * n && ok; ++i, ++stage) {
-          const int rs = stage % (kI8 ? Sh::kRaws : 1), fs = stage % F;
-          ok = pwait(raw_full(rs), (uint32_t)((stage / (kI8 ? Sh::kRaws : 1)) & 1));
-          if (ok && stage >= F) ok = pwait(empty(fs), (uint32_t)((stage / F - 1) & 1));
+        for (int i = 0; i < n && ok; ++i) {
+          const int gt = tiles + i, rs = gt % ring, fs = gt % F;
+          ok = pwait(raw_full(isv, rs), (uint32_t)((gt / ring) & 1));
+          if (ok && gt >= F) ok = pwait(empty(isv, fs), (uint32_t)((gt / F - 1) & 1));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          constexpr int WT = 32 * (kI8 ? Sh::kWideners : 1);
           // a tile's scales, with its K: logarithm and inverse of V's (of 0: of 2^-100, which times
           // vs is 0 again)
-          if ((i == 0 || (i & 1)) && i < 2 * n - 1 && t < kTreeKeys) {
-            const int at = ((tiles + (i + 1) / 2) % Sh::kScaleSlots) * kTreeKeys + t;
-            const float v = fabsf(vsc[at]);
-            const float lv = v < INFINITY ? fmaxf(tree_lg2(v), -100.0f) : 0.0f;
-            vlog[at] = lv;
-            vinv[at] = tree_ex2(-lv);
-            ksc[at] *= a.scale_log2;
+          if (!isv) {
+            for (int e = t; e < kTreeKeys; e += WT) {
+              const int at = (gt % Sh::kScaleSlots) * kTreeKeys + e;
+              const float v = fabsf(vsc[at]);
+              const float lv = v < INFINITY ? fmaxf(tree_lg2(v), -100.0f) : 0.0f;
+              vlog[at] = lv;
+              vinv[at] = tree_ex2(-lv);
+              ksc[at] *= a.scale_log2;
+            }
           }
-          constexpr int CH = D / 16;
-          constexpr int PER = kTreeKeys * CH / WT;
-          uint4 x[PER];
+          constexpr int CH = D / 16, PER = kTreeKeys * CH / WT, STEP = PER < 4 ? PER : 4;
+#pragma unroll 1
+          for (int k0 = 0; k0 < PER; k0 += STEP) {
+            uint4 x[STEP];
 #pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const uint32_t at = cd_s + rs * Sh::kRaw + 16 * (k * WT + t);
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(at) : "memory");
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(raw_empty(rs));
+            for (int k = 0; k < STEP; ++k) {
+              const uint32_t at = from_s + rs * Sh::kRaw + 16 * ((k0 + k) * WT + t);
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(at) : "memory");
+            }
+            if (k0 + STEP == PER) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(raw_empty(isv, rs));
+            }
 #pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const int id = k * WT + t, row = id / CH, cc = id % CH;
-            const uint32_t w[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u, x[k].w ^ 0x80808080u};
+            for (int k = 0; k < STEP; ++k) {
+              const int id = (k0 + k) * WT + t, row = id / CH, cc = id % CH;
+              const uint32_t w[4] = {x[k].x ^ 0x80808080u, x[k].y ^ 0x80808080u, x[k].z ^ 0x80808080u, x[k].w ^ 0x80808080u};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c8 = 2 * cc + h;
-              const uint32_t to = st_s + fs * Sh::kStage + (c8 >> 3) * (kTreeKeys * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4);
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(tree_widen<0x4140>(w[2 * h])),
-                           "r"(tree_widen<0x4342>(w[2 * h])), "r"(tree_widen<0x4140>(w[2 * h + 1])), "r"(tree_widen<0x4342>(w[2 * h + 1]))
-                           : "memory");
+              for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tree_chunk(to_s + fs * Sh::kStage, row, 2 * cc + h)),
+                             "r"(tree_widen<0x4140>(w[2 * h])), "r"(tree_widen<0x4342>(w[2 * h])), "r"(tree_widen<0x4140>(w[2 * h + 1])),
+                             "r"(tree_widen<0x4342>(w[2 * h + 1]))
+                             : "memory");
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(full(fs));
+          mbar_arrive(full(isv, fs));
         }
         tiles += n;
       }
@@ -847,13 +863,14 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         const int n = segs[si].u1 - segs[si].u0;
         const int seg = nsegs + si;
         if (!wwait(q_full, (uint32_t)(seg & 1))) { ok = false; break; }
-        for (int i = 0; i <= n; ++i) {
-          if (i < n) {
-            const int st = stage + tree_k_stage(i), slot = st % F, b = (tiles + i) & 1;
-            if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
+        for (int i = -Sh::kAhead; i < n; ++i) {   // scores of tile i + kAhead, then P V of tile i
+          const int k = i + Sh::kAhead;
+          if (k < n) {
+            const int gt = tiles + k, slot = gt % F, b = gt % Sh::kBufs;
+            if (!wwait(full(0, slot), (uint32_t)((gt / F) & 1))) { ok = false; break; }
             tc_fence_after();
             // (descriptors count 16 bytes; the loops are kept rolled: see the loading loop)
-            uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(st_s + slot * Sh::kStage);
+            uint64_t qd = smem_desc_sw128(q_s), kd = smem_desc_sw128(k_s + slot * Sh::kStage);
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c, qd += kTreeRows * 8, kd += kTreeKeys * 8) {
 #pragma unroll
@@ -861,31 +878,30 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
                 mma_f16_ss_w(leader, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys), qd + 2 * kk, kd + 2 * kk, kIdS, (uint32_t)(c + kk));
             }
             mma_commit_w(leader, s_full(b));
-            mma_commit_w(leader, empty(slot));
-            if (i == n - 1) mma_commit_w(leader, q_empty);
+            mma_commit_w(leader, empty(0, slot));
+            if (k == n - 1) mma_commit_w(leader, q_empty);
           }
-          if (i > 0) {
-            const int j = i - 1, st = stage + tree_v_stage(j, n), slot = st % F, gt = tiles + j, b = gt & 1;
-            if (!wwait(p_full(b), (uint32_t)((gt >> 1) & 1))) { ok = false; break; }
-            if (!wwait(full(slot), (uint32_t)((st / F) & 1))) { ok = false; break; }
+          if (i >= 0) {
+            const int gt = tiles + i, slot = gt % F, b = gt % Sh::kBufs;
+            if (!wwait(p_full(b), (uint32_t)((gt / Sh::kBufs) & 1))) { ok = false; break; }
+            if (!wwait(full(1, slot), (uint32_t)((gt / F) & 1))) { ok = false; break; }
             tc_fence_after();
             // (O of the segment before has been read; a tile with values that are not finite starts it at 0)
-            if (j == 0 && seg > 0 && !wwait(o_free, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
-            const uint32_t more = j > 0 || *static_cast<volatile int *>(&ctl->zeroed) == seg + 1;
-            uint64_t vd = smem_desc_sw128_mn(st_s + slot * Sh::kStage);
+            if (i == 0 && seg > 0 && !wwait(o_free, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
+            const uint32_t more = i > 0 || *static_cast<volatile int *>(&ctl->zeroed) == seg + 1;
+            uint64_t vd = smem_desc_sw128_mn(v_s + slot * Sh::kStage);
             uint32_t pt = tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys);
 #pragma unroll 1
             for (int kk = 0; kk < kTreeKeys / 16; ++kk, vd += 128, pt += 16) {
               mma_f16_ts_w(leader, tmem, pt, vd, kIdO, more | (uint32_t)kk);
               mma_f16_ts_w(leader, tmem, pt + 8, vd, kIdO, 1u);
             }
-            mma_commit_w(leader, empty(slot));
-            mma_commit_w(leader, o_step);
-            if (j == n - 1) mma_commit_w(leader, o_done);
+            mma_commit_w(leader, empty(1, slot));
+            mma_commit_w(leader, o_step(gt));
+            if (i == n - 1) mma_commit_w(leader, o_done);
           }
         }
         if (!ok) break;
-        stage += 2 * n;
         tiles += n;
       }
     } else if (warp < 8) {
@@ -942,7 +958,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         float *refs = xch + 2 * kTreeRows + row;  // [2][128]: of the latest tiles
         const int pass_on = 2 + 4 * grp + (warp & 3), take_over = 2 + 4 * (grp ^ 1) + (warp & 3);      // barriers of a row's two warps
         for (int i = (tiles & 1) == grp ? 0 : 1; i < n; i += 2) {
-          const int gt = tiles + i, b = grp;
+          const int gt = tiles + i, b = gt % Sh::kBufs;
           const int base = tree_base(s, s.u0 + i);
           const bool masked = base + kTreeKeys > s.pos0 || (base < whole && base + kTreeKeys > a.sinks);
           unsigned long long vis = ~0ull;
@@ -960,7 +976,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             if (!real) vis = 0;
           }
-          bool stop = !pwait(s_full(b), (uint32_t)((gt >> 1) & 1));
+          bool stop = !pwait(s_full(b), (uint32_t)((gt / Sh::kBufs) & 1));
           tc_fence_after();
           const uint32_t sadr = tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys);
           const int sc = (gt % Sh::kScaleSlots) * kTreeKeys;
@@ -978,9 +994,14 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             }
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < NX; c += 2) {
+            for (int c = 0; c < NX; c += 4) {
               x[c / 2] = F2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-              if constexpr (kI8) x[c / 2] = fma2(x[c / 2], *reinterpret_cast<const F2 *>(ksc + sc + c0 + c), *reinterpret_cast<const F2 *>(vlog + sc + c0 + c));
+              x[c / 2 + 1] = F2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+              if constexpr (kI8) {                // (16 bytes a load: the loads of scales alone are 1500 cycles a tile by 8)
+                const F4 k = *reinterpret_cast<const F4 *>(ksc + sc + c0 + c), e = *reinterpret_cast<const F4 *>(vlog + sc + c0 + c);
+                x[c / 2] = fma2(x[c / 2], k.a, e.a);
+                x[c / 2 + 1] = fma2(x[c / 2 + 1], k.b, e.b);
+              }
             }
           };
           float top = -INFINITY;
@@ -1029,7 +1050,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           m_ref = now;
           if (__any_sync(0xffffffffu, moves) && i > 0) {
             const float f = tree_ex2(before - now);
-            if (!__all_sync(0xffffffffu, pwait(o_step, (uint32_t)((gt - 1) & 1)))) stop = true;
+            if (!__all_sync(0xffffffffu, pwait(o_step(gt - 1), o_phase(gt - 1)))) stop = true;
             tc_fence_after();
 #pragma unroll 1
             for (int cc = 0; cc < (stop ? 0 : D); cc += 32) {
@@ -1053,21 +1074,27 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 #pragma unroll
               for (int h = 0; h < NX; h += 16) {
                 uint32_t hi[8], lw[8];
+                F4 iv, vs;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
+                  if constexpr (kI8) {
+                    if (!(c & 1)) {
+                      iv = *reinterpret_cast<const F4 *>(vinv + sc + c0 + h + 2 * c);
+                      vs = *reinterpret_cast<const F4 *>(vsc + sc + c0 + h + 2 * c);
+                    }
+                  }
                   F2 w = kI8 ? add2(x[h / 2 + c], neg) : fma2(x[h / 2 + c], sc2, neg);
                   float p, r;
                   w.get(p, r);
                   w = F2(tree_ex2(p), tree_ex2(r));
-                  const int at = sc + c0 + h + 2 * c;
                   if constexpr (kI8) {
-                    w = mul2(w, *reinterpret_cast<const F2 *>(vinv + at));
+                    w = mul2(w, c & 1 ? iv.b : iv.a);
                     if constexpr (decltype(partly)::value) {
                       w.get(p, r);
                       w = F2(vm >> (h + 2 * c) & 1 ? p : 0.0f, vm >> (h + 2 * c + 1) & 1 ? r : 0.0f);
                     }
                     sum = add2(sum, w);
-                    w = mul2(w, *reinterpret_cast<const F2 *>(vsc + at));
+                    w = mul2(w, c & 1 ? vs.b : vs.a);
                   }
                   w.get(p, r);
                   if constexpr (decltype(partly)::value) {    // (hidden: also with scores or scales that are not finite)
@@ -1099,9 +1126,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             // so tiles seen partly are searched for such keys.  They are added here, to the rows
             // that see them, and cleared for the MMA.
             if (masked) {
-              const int st = stage + tree_v_stage(i, n);
-              const uint32_t vst = st_s + (st % F) * Sh::kStage;
-              stop = stop || !pwait(full(st % F), (uint32_t)((st / F) & 1));
+              const uint32_t vst = v_s + (gt % F) * Sh::kStage;
+              stop = stop || !pwait(full(1, gt % F), (uint32_t)((gt / F) & 1));
               if (row == 0) ctl->bad[grp] = 0;
               named_bar_sync(10 + grp, 128);
               constexpr uint32_t e = kBf ? 0x7f80u : 0x7c00u;
@@ -1118,7 +1144,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               named_bar_sync(10 + grp, 128);
               const unsigned long long found = *static_cast<volatile unsigned long long *>(&ctl->bad[grp]);
               if (found) {
-                stop = stop || !__all_sync(0xffffffffu, i == 0 || pwait(o_step, (uint32_t)((gt - 1) & 1)));
+                stop = stop || !__all_sync(0xffffffffu, i == 0 || pwait(o_step(gt - 1), o_phase(gt - 1)));
                 tc_fence_after();
                 // (after a wait that gave up everyone goes on to the segment's end without waiting)
                 if (!named_bar_or(10 + grp, 128, stop)) tree_add_bad<D, kBf>(tmem + lane_base, tmem + lane_base + Sh::kSCol + (uint32_t)(b * kTreeKeys), vst, found, vis, i == 0, grp);
@@ -1200,7 +1226,6 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
         tiles += n;
-        stage += 2 * n;
       }
       ok = !aborted;
     }
@@ -1216,8 +1241,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
   // (the MMAs have waited for all copies, unless a wait gave up)
   if (warp >= Sh::kLoadWarp && warp < Sh::kWiden0 && wctl->abort) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    constexpr int kRing = kI8 ? Sh::kRaws : F;
-    if (last >= 0) mbar_drain(kI8 ? raw_full(lane) : full(lane), (uint32_t)((last / kRing) & 1), wctl);
+    const int isv = lane >= 8, ring = max(kI8 ? isv ? Sh::kRawV : Sh::kRawK : F, 1);
+    if (last >= 0) mbar_drain(kI8 ? raw_full(isv, lane & 7) : full(isv, lane & 7), (uint32_t)((last / ring) & 1), wctl);
     if (lane == 0 && queries > 0) mbar_drain(q_full, (uint32_t)((queries - 1) & 1), wctl);
   }
   if (warp == Sh::kMmaWarp) {
