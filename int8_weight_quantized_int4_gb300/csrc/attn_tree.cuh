@@ -82,14 +82,18 @@ struct TreeShape {
   static constexpr int kStage = kTreeKeys * D * 2;
   // tiles of K, and of V, in shared memory: rings of their own, each filled in the tiles' order by one
   // warp and emptied by another, so that a wait's parity names one phase
-  static constexpr int kTiles = kI8 ? (D == 64 ? 2 : 1) : D == 64 ? 4 : 2;
+  static constexpr int kTiles = kI8 ? (D == 128 ? 1 : 2) : D == 64 ? 4 : D == 256 ? 3 : 2;
   static constexpr int kRaw = kI8 ? kTreeKeys * D : 0;                // a stage of codes
-  static constexpr int kRawK = !kI8 ? 0 : D == 256 ? 3 : D == 128 ? 2 : 4, kRawV = !kI8 ? 0 : D == 64 ? 4 : 2;
+  static constexpr int kRawK = !kI8 ? 0 : D == 64 ? 4 : 2, kRawV = kRawK;
   static constexpr int kScaleSlots = D == 64 ? 16 : D == 128 ? 6 : 8;     // tiles whose scales are kept (more than can be under way)
-  static constexpr int kQ = kTreeRows * D * 2;
-  static constexpr int kAhead = D == 256 ? 2 : 1, kBufs = kAhead + 1;     // tiles whose scores are computed before P V of one
+  // d = 256 (one CTA an SM): Q in TMEM.  From shared memory it would be read again for every 64 keys,
+  // 64 KB beside the tile's 64, and shared memory's bandwidth bound the tile (Q there: 194 us for 12 x
+  // 16k of 64 nodes); and it leaves 64 KB for tiles.
+  static constexpr bool kQTmem = D == 256;
+  static constexpr int kQ = kQTmem ? 0 : kTreeRows * D * 2;
+  static constexpr int kAhead = 1, kBufs = kAhead + 1;    // tiles whose scores are computed before P V of one
   static constexpr uint32_t kTmem = D == 256 ? 512 : 256;
-  static constexpr uint32_t kSCol = D;            // O [0, D), then kBufs buffers of 64 columns of S and P
+  static constexpr uint32_t kQCol = D, kSCol = kQTmem ? D + D / 2 : D;    // O [0, D), Q, then kBufs buffers of 64 columns of S and P
   static constexpr int kScaleBytes = kI8 ? kScaleSlots * kTreeKeys * 16 : 0;
   static constexpr int kMaskWords = 9;            // a row's ancestors (256 bits) and the first key of its window
   // barriers, parents, masks, an exchange between the groups, the segments
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
       mbar_init(p_full(b), 4);
       mbar_init(o_step(b), 1);
     }
-    mbar_init(q_full, 1);
+    mbar_init(q_full, Sh::kQTmem ? 8 : 1);
     mbar_init(q_empty, 1);
     mbar_init(o_done, 1);
     mbar_init(o_free, 8);
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
                 cp_async_arrive(bar);
               }
             }
-            if (x == 0 && role != 1) queries_in();
+            if (!Sh::kQTmem && x == 0 && role != 1) queries_in();
           }
         } else {
           const int quad = lane & 15;
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               }
               cp_async_arrive(bar);
             }
-            if (x == 0) queries_in();
+            if (!Sh::kQTmem && x == 0) queries_in();
           }
         }
         tiles += n;
@@ -874,12 +878,15 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c, qd += kTreeRows * 8, kd += kTreeKeys * 8) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss_w(leader, tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys), qd + 2 * kk, kd + 2 * kk, kIdS, (uint32_t)(c + kk));
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t to = tmem + Sh::kSCol + (uint32_t)(b * kTreeKeys);
+                if constexpr (Sh::kQTmem) mma_f16_ts_w(leader, to, tmem + Sh::kQCol + (uint32_t)(32 * c + 8 * kk), kd + 2 * kk, kIdS, (uint32_t)(c + kk));
+                else mma_f16_ss_w(leader, to, qd + 2 * kk, kd + 2 * kk, kIdS, (uint32_t)(c + kk));
+              }
             }
             mma_commit_w(leader, s_full(b));
             mma_commit_w(leader, empty(0, slot));
-            if (k == n - 1) mma_commit_w(leader, q_empty);
+            if (!Sh::kQTmem && k == n - 1) mma_commit_w(leader, q_empty);
           }
           if (i >= 0) {
             const int gt = tiles + i, slot = gt % F, b = gt % Sh::kBufs;
@@ -924,6 +931,23 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
         const int col = s.rb * a.block_rows + row, node = col / a.G, head = s.g * a.G + col - node * a.G;
         const bool real = node < s.nodes && row < a.block_rows;
         const bool busy = __any_sync(0xffffffffu, real);
+        if constexpr (Sh::kQTmem) {
+          // the row of Q, a group half of it: two elements a column (the segment before has its scores)
+          uint4 v[D / 16];
+          const uint16_t *from = a.q + (long long)(s.tok0 + (real ? node : 0)) * a.q_tok + (long long)head * a.q_head + grp * (D / 2);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) v[c] = real ? __ldg(reinterpret_cast<const uint4 *>(from) + c) : make_uint4(0u, 0u, 0u, 0u);
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; c += 2) {
+            const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+            tmem_st8(tmem + lane_base + Sh::kQCol + (uint32_t)(grp * (D / 4) + 4 * c), w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
         // the row's ancestors, as bits over the nodes, and the first key its window holds
         uint32_t *mine = masks + row * Sh::kMaskWords;
         if ((tree_base(s, s.u1 - 1) + kTreeKeys > s.pos0 || a.window > 0) && s.nodes <= 256) {   // (else none is needed)

@@ -526,8 +526,9 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   const int G = Hq / c->Hkv;
   // Row blocks of whole nodes, whose Q is one box (a gather of 128 rows takes 2 to 5 us), unless
   // that makes more of them than 128 rows of any nodes do, for a sequence of max_nodes.
-  a.block_rows = G <= 128 ? 128 / G * G : 128;
-  a.q_box = G <= 128 && (max_nodes * G + a.block_rows - 1) / a.block_rows == (max_nodes * G + 127) / 128;
+  // (d = 256 reads its rows one by one).
+  a.block_rows = G <= 128 && c->d < 256 ? 128 / G * G : 128;
+  a.q_box = G <= 128 && c->d < 256 && (max_nodes * G + a.block_rows - 1) / a.block_rows == (max_nodes * G + 127) / 128;
   if (!a.q_box) a.block_rows = 128;
   if (a.q_box) {
     const long long dim[3] = {G, c->Hkv, T};
@@ -539,6 +540,9 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   a.tok_rows = kv.step[2];
   a.q_tok_rows = qv.step[1];
   a.q_head_rows = qv.step[2];
+  a.q = q;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
   a.out = out;
   a.lse = lse;
   a.ks = c->k_scale;

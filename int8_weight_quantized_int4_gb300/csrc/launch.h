@@ -151,10 +151,12 @@ struct TreeArgs {
   int scale_boxes;              // int8: a box's scales are a multiple of 16 bytes, so aligned
   int block_rows;               // rows of an item: whole nodes (q_box), or 128
   int q_box;
-  uint16_t *out;                // as PagedArgs
+  const uint16_t *q;            // as PagedArgs
+  uint16_t *out;
   float *lse;
   const float *ks, *vs;
   const int *table, *lens, *cu, *parents;
+  long long q_tok, q_head;
   int q_tok_rows, q_head_rows;  // strides in rows of the maps
   int page_rows, head_rows, tok_rows;
   int B, T, Hq, Hkv, G, page, npages, max_pages, cap, window, sinks, page_shift;
