@@ -43,6 +43,7 @@ constexpr int kSmThreads = 256;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBlocks = 8;                      // blocks a thread keeps the maxima of
 constexpr int kSmList = 2048;                     // elements a CTA lists
+constexpr int kSmPairs = 256;                     // a list whose elements are compared each with each
 constexpr int kSmShort = 1024;                    // of all CTAs of a row: the first one's alone
 constexpr int kSmBins = 256;
 constexpr int kSmMaxCluster = 16;
@@ -560,13 +561,132 @@ __device__ __forceinline__ u64 sample_mass(float p, u64 total) {
 }
 
 // ------------------------------------------------------------------ the list --
-// Resolves the list of n elements (one CTA): which stay, and the draw among them.
+// Keeps of a list what is not surely below its k-th element (k > 0): the key reached by k elements at
+// least is raised by halving, until few more than k reach it.  Returns how many are left.
+template <typename T>
+__device__ __forceinline__ int sample_shrink(SampleCta<T> &t, int n, int k, unsigned low) {
+  SampleSmem &s = t.s;
+  constexpr int PER = kSmShort / kSmThreads;
+  u64 key[PER];
+  unsigned high = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t.tid + i * kSmThreads;
+    key[i] = e < n ? s.key[e] : 0;
+    high = max(high, (unsigned)(key[i] >> 32));
+  }
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (t.lane == 0) s.cnt[t.warp] = high;
+  if (t.tid == 0) s.nwork = 0;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kSmWarps; ++v) high = max(high, s.cnt[v]);
+  const int per = (n + kSmThreads - 1) / kSmThreads, enough = k + max(k / 4, 16);
+  int left = n;
+#pragma unroll 1
+  for (int round = 0; round < 16 && left > enough && low < high; ++round) {
+    const unsigned mid = low + (high - low) / 2 + 1;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i < per) c += __syncthreads_count((unsigned)(key[i] >> 32) >= mid);
+    if (c >= k) {
+      low = mid;
+      left = c;
+    } else {
+      high = mid - 1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if ((unsigned)(key[i] >> 32) >= low && key[i]) s.key[atomicAdd(&s.nwork, 1)] = key[i];
+  __syncthreads();
+  return left;
+}
+
+// A list of kSmPairs elements at most: sorted by comparing each with each, by a thread or a few an
+// element; every filter then leaves a first part of it.
+template <typename T>
+__device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
+                                             float u) {
+  SampleSmem &s = t.s;
+  const int tid = t.tid, lane = t.lane, warp = t.warp;
+  auto threads = [](int n) { return n <= 32 ? 3 : n <= 64 ? 2 : n <= 128 ? 1 : 0; };       // an element, log2
+  u64 *const sorted = s.key + kSmPairs + 2;
+  {
+    const int lg = threads(n), e = tid >> lg, first = tid & ((1 << lg) - 1);
+    if (tid < 2) s.key[n + tid] = 0;              // (below all)
+    u64 tails = 0;
+    if (p < 1.0f && k == 0 && tid < (int)t.size) tails = s.tail[tid];
+    if (warp == 0) {
+      tails = SampleCta<T>::reduce(tails);
+      if (lane == 0) s.thr = tails;
+    }
+    __syncthreads();
+    const u64 key = e < n ? s.key[e] : ~0ull;
+    int above = 0;
+#pragma unroll 4
+    for (int q = 2 * first; q < n; q += 2 << lg) above += (s.key[q] > key) + (s.key[q + 1] > key);
+    for (int o = 1; o < 1 << lg; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (e < n && first == 0) sorted[above] = key;
+    __syncthreads();
+  }
+  const u64 key = tid < n ? sorted[tid] : 0;
+  bool keep = tid < n && (k == 0 || tid < k);
+  const u64 w = keep ? t.weight(sm_value((unsigned)(key >> 32))) : 0;
+  if (p < 1.0f) {
+    u64 incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.mass[warp] = incl;
+    __syncthreads();
+    u64 all = s.thr, before = incl - w;
+#pragma unroll
+    for (int v = 0; v < kSmWarps; ++v) {
+      all += s.mass[v];
+      if (v < warp) before += s.mass[v];
+    }
+    keep = keep && (before < sample_mass(p, all) || tid == 0);
+  }
+  if (mp > 0.0f) {
+    const u64 least = (u64)ceil((double)mp * (double)(1ull << kSmFix));
+    keep = keep && (w >= least || tid == 0);
+  }
+  // the draw among what stays, in the order of the vocabulary
+  s.cnt[tid] = keep ? ~(unsigned)key : 0xffffffffu;
+  s.w[tid] = keep ? w : 0;
+  const u64 part = SampleCta<T>::reduce(keep ? w : 0);
+  if (lane == 0) s.rsum[warp] = part;
+  const int m = __syncthreads_count(keep), lg = threads(m), e = tid >> lg;
+  u64 all = 0, before = 0;
+#pragma unroll
+  for (int v = 0; v < kSmWarps; ++v) all += s.rsum[v];
+  const unsigned col = s.cnt[e];
+#pragma unroll 4
+  for (int q = tid & ((1 << lg) - 1); q < m; q += 1 << lg) {
+    const u64 other = s.w[q];
+    before += s.cnt[q] < col ? other : 0;
+  }
+  for (int o = 1; o < 1 << lg; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  const u64 target = sample_target(u, all), mine = s.w[e];
+  if ((tid & ((1 << lg) - 1)) == 0 && e < m && before <= target && before + mine > target) sample_write(a, r, (int)col, mine, all);
+}
+
+// Resolves the list of n elements from the key `low` on (one CTA): which stay, and the draw among them.
 template <typename T>
 __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
-                                            float u) {
+                                            float u, unsigned low) {
   SampleSmem &s = t.s;
   constexpr int PER = kSmShort / kSmThreads;
   const int tid = t.tid, lane = t.lane;
+  if (k > 0 && n > 64 && n > k) n = sample_shrink(t, n, k, low);
+  if (n <= kSmPairs) {
+    sample_pairs(a, t, r, n, k, p, mp, u);
+    return;
+  }
   for (int i = tid; i < kSmBins; i += kSmThreads) {
     s.cnt[i] = 0;
     s.mass[i] = 0;
@@ -1245,7 +1365,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   bool full;
   const unsigned n = t.join_lists(s.key, kSmShort, full);
   if (n <= kSmShort) {
-    if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u);
+    if (rank == 0) sample_list<T>(a, t, r, (int)n, k, p, mp, u, T0);
     return;
   }
   // ---- flat rows
