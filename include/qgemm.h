@@ -436,12 +436,17 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
  * only the ones at positions above s + e - window or below `sinks`.
  *   max_nodes: 1 .. 256, at least the nodes of any sequence (a sequence with more gives rows of
  *   zeros and QW_ERR_BAD_INDEX; so does a parent that is not an earlier node, which counts as -1
- *   then).  The workspace's size depends on it not at all.
+ *   then).
  *   ws: attn_tree_workspace_bytes(d, Hq, Hkv) bytes, 256-byte aligned, no zeroing needed; not
  *   shared by calls that may run concurrently.
- * Other arguments, masked values, bad pages and lengths as attn_paged.  Results are bit-identical
- * between calls (on devices with the same number of SMs).  Two launches, async.  Returns as
- * attn_paged.
+ * Other arguments, masked values, bad pages and lengths as attn_paged; strides of q are not negative
+ * (0: broadcast).  A value of V that a node sees and that is not finite makes its channel of the
+ * node's output not finite.  QW_ERR_UNSUPPORTED_SHAPE: more than 2^31 rows of the cache's (or q's)
+ * strides' greatest common divisor; query columns times the page table's keys past 2^32 schedule
+ * entries ((T Hq / Hkv / 128 + B) Hkv (keys / 64 + 25) > 4e9).  A wait inside the kernel that
+ * passes QW_OPT_WAIT_LIMIT_US ends it with QW_ERR_TIMEOUT and undefined results; the workspace
+ * needs nothing then.  Results are bit-identical between calls (on devices with the same number of
+ * SMs).  Two launches, async.  Returns as attn_paged.
  * ------------------------------------------------------------------------ */
 size_t attn_tree_workspace_bytes(int d, int Hq, int Hkv);
 int attn_tree(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const int32_t *parents, const uint16_t *q, int T,
@@ -463,8 +468,9 @@ int attn_tree(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const int3
  *   logits: as token_logprobs, 1 <= N <= 2^20.  -inf and NaN weigh nothing; a row of nothing
  *   else gives token -1 and -inf.  Rows with +inf draw among those.
  *   settings: numbers for all rows, or per row [M] where the array is not NULL (device).
- * Weights are compared and summed as whole numbers of 2^-40 (relative error 4e-9), so equal inputs
- * give equal tokens; top-p's sum holds what lies far below the border in binary32.
+ * Weights are compared and summed as whole numbers of 2^-40, so equal inputs give equal tokens:
+ * from 2^-12 on with a relative error of 2e-11, below that of 4e-6 (binary32); top-p's sum holds
+ * what lies far below the border in binary32.
  * One launch, async, no workspace.  Returns as kv_append.
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -496,7 +502,8 @@ int tree_accept(const int32_t *tokens, const int32_t *drawn, const int32_t *pare
  * new_lens[b] (int32, may be NULL; not the batch's seq_lens) = s + count[b].
  *   pools: up to four (K, V and their scales); token r of page p, head h, layer l is the
  *   row_bytes bytes at base + l * layer_stride + p * page_stride + h * head_stride + r * token_stride
- *   (strides in bytes, all multiples of 4; 16 bytes at a time where they and base allow).
+ *   (strides in bytes, all multiples of 4; 16 bytes at a time where they and base allow).  Rows
+ *   that overlap and a base given twice are refused.
  *   batch, T: as kv_append; page the tokens of a page.  The pages that hold the nodes belong to one
  *   sequence.  path [B][max_path], count [B]: as tree_accept gives them (entries ascend).
  * An entry that does not ascend or names no node, a count outside 0 .. the nodes, or a page
@@ -571,8 +578,8 @@ int qgemm_w4a16_noalloc(const uint16_t *x, const void *packed_w4, int M, int N, 
  *   qpack_*) may directly precede a GEMM on the same stream.
  *
  *   QW_OPT_WAIT_LIMIT_US (default 4000000, i.e. 4 s; 0 .. 4000000).  The time
- *   limit, in microseconds, of every wait inside a GEMM kernel (a pipeline stage
- *   waiting for another).  A wait that runs past it ends the kernel early with
+ *   limit, in microseconds, of every wait inside a GEMM kernel or attn_tree's (a
+ *   pipeline stage waiting for another).  A wait that runs past it ends the kernel early with
  *   QW_ERR_TIMEOUT in the device error word (qw_device_error) and an undefined
  *   y; the workspace must then be zero-filled again.  A test hook: lowering it
  *   (0 makes every wait that is not already satisfied when first checked give

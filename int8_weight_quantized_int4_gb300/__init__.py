@@ -1086,8 +1086,8 @@ DEFAULT_WAIT_LIMIT_US = 4_000_000
 
 
 def set_wait_limit_us(us: int | None = None):
-    """Test hook: the time limit of every wait inside the GEMM kernels launched from now
-    on, in microseconds (None restores the 4 s default).  A kernel whose wait runs past
+    """Test hook: the time limit of every wait inside the GEMM kernels and attn_tree's launched
+    from now on, in microseconds (None restores the 4 s default).  A kernel whose wait runs past
     it ends early with QW_ERR_TIMEOUT in the device error word."""
     _check(lib().qw_set_option(QW_OPT_WAIT_LIMIT_US, DEFAULT_WAIT_LIMIT_US if us is None else int(us)))
 

@@ -266,8 +266,11 @@ __device__ __forceinline__ unsigned tree_places(const TreeArgs &a, const TreeSpa
   return (unsigned)((p.blocks + R - 1) / R) * (unsigned)a.Hkv * (unsigned)(p.n + cost);
 }
 
-// CTAs that share the row blocks of a sequence: one for each block, up to four
-__device__ __forceinline__ int tree_team(const TreeSpan &p) { return min(max(p.blocks, 1), kTreeMaxTeam); }
+// CTAs that share the row blocks of a sequence: one for each block, up to four; one where max_nodes
+// says that every sequence has one block (whatever a sequence that breaks its word has)
+__device__ __forceinline__ int tree_team(const TreeArgs &a, const TreeSpan &p) {
+  return a.blocks > 1 ? min(max(p.blocks, 1), kTreeMaxTeam) : 1;
+}
 
 // Lists the range's next segments (one thread).
 static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, TreeCtl *ctl) {
@@ -276,10 +279,10 @@ static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, 
   const unsigned begin = ctl->begin, end = ctl->end;
   const int R = ctl->size, cost = ctl->cost;
 #pragma unroll 1
-  while (pos < end && n < kTreeSegs) {
+  while (pos < end && n < kTreeSegs && b < a.B) {
     const TreeSeq s = tree_seq(a, b);
     const TreeSpan p = tree_span(a, s);
-    if ((!ctl->all && tree_team(p) != R) || off >= tree_places(a, p, R, cost)) {
+    if ((!ctl->all && tree_team(a, p) != R) || off >= tree_places(a, p, R, cost)) {
       ++b;
       off = 0;
       continue;
@@ -313,7 +316,7 @@ static __device__ __noinline__ void tree_walk(const TreeArgs &a, TreeSeg *segs, 
     off += each - in;
   }
   ctl->nseg = n;
-  ctl->more = pos < end;
+  ctl->more = pos < end && b < a.B;
   ctl->b = b;
   ctl->off = off;
   ctl->pos = pos;
@@ -334,7 +337,7 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   unsigned sum[kTreeMaxTeam] = {}, bare = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeSpan p = tree_span(a, tree_seq(a, b));
-    const int R = tree_team(p);
+    const int R = tree_team(a, p);
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k)
       if (k == R - 1) sum[k] += tree_places(a, p, R, IC);
@@ -438,7 +441,7 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
     unsigned off = begin - start;
     for (; b + 1 < b1; ++b) {
       const TreeSpan p = tree_span(a, tree_seq(a, b));
-      if (!all && tree_team(p) != R) continue;
+      if (!all && tree_team(a, p) != R) continue;
       const unsigned c = tree_places(a, p, R, cost);
       if (off < c) break;
       off -= c;

@@ -489,6 +489,7 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   if (window < 0 || sinks < 0) return bad(QW_ERR_INVALID_ARG, "negative window or sinks");
   if (!isfinite(scale)) return bad(QW_ERR_INVALID_ARG, "scale is not finite");
   if ((long long)T * Hq > 0x7fffffffll) return bad(QW_ERR_UNSUPPORTED_SHAPE, "T * Hq above 2^31 - 1");
+  if (q_token_stride < 0 || q_head_stride < 0) return bad(QW_ERR_INVALID_ARG, "negative q stride");
   if (T == 0 || b->B == 0) return QW_OK;
   if (!parents || !q || !out) return bad(QW_ERR_INVALID_ARG, "null tensor pointer");
   if (!at(q, 16) || !at(out, 16) || q_token_stride % 8 || q_head_stride % 8 || !at(parents, 4) || (lse && !at(lse, 4)) ||
@@ -513,12 +514,15 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   if ((rc = encode_row_map(&a.kmap, none ? q : c->k, none ? 1 : kv.rows, c->d, kv.pitch, i8, bf))) return rc;
   if ((rc = encode_row_map(&a.vmap, none ? q : c->v, none ? 1 : kv.rows, c->d, kv.pitch, i8, bf))) return rc;
   if ((rc = encode_row_map(&a.qmap, q, qv.rows, c->d, qv.pitch, false, bf))) return rc;
-  // boxes of the rows of a tile that lie in one page, where that are 8 or more
-  a.box = none ? 0 : c->page & -c->page;
+  // boxes of the rows of a tile that lie in one page, where that are 8 or more; not of a broadcast
+  // cache or q (a stride of 0 in a map's dimension), whose rows are gathered
+  auto lies = [](long long n, long long stride) { return n <= 1 || stride > 0; };
+  a.box = none || !lies(c->page, c->token_stride) || !lies(c->Hkv, c->head_stride) || !lies(c->num_pages, c->page_stride)
+              ? 0 : c->page & -c->page;
   a.box = a.box < 8 ? 0 : a.box < 64 ? a.box : 64;
   if (a.box) {
     const long long dim[3] = {c->page, c->Hkv, c->num_pages};
-    const long long stride[3] = {c->token_stride * es, c->Hkv > 1 ? c->head_stride * es : 16, c->num_pages > 1 ? c->page_stride * es : 16};
+    const long long stride[3] = {c->page > 1 ? c->token_stride * es : 16, c->Hkv > 1 ? c->head_stride * es : 16, c->num_pages > 1 ? c->page_stride * es : 16};
     if ((rc = encode_page_map(&a.kbox, c->k, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
     if ((rc = encode_page_map(&a.vbox, c->v, dim, stride, c->d, a.box, 1, i8, bf))) return rc;
   }
@@ -529,6 +533,7 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   // (d = 256 reads its rows one by one).
   a.block_rows = G <= 128 && c->d < 256 ? 128 / G * G : 128;
   a.q_box = G <= 128 && c->d < 256 && (max_nodes * G + a.block_rows - 1) / a.block_rows == (max_nodes * G + 127) / 128;
+  a.q_box = a.q_box && lies(Hq, q_head_stride) && lies(T, q_token_stride);
   if (!a.q_box) a.block_rows = 128;
   if (a.q_box) {
     const long long dim[3] = {G, c->Hkv, T};

@@ -263,7 +263,11 @@ int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *b
     if (!p.base) return bad(QW_ERR_INVALID_ARG, "null pool pointer");
     if (!at(p.base, 4) || p.layer_stride % 4 || p.page_stride % 4 || p.head_stride % 4 || p.token_stride % 4)
       return bad(QW_ERR_ALIGNMENT, "rows start on 4-byte boundaries");
-    if (page > 1 && p.token_stride < p.row_bytes) return bad(QW_ERR_INVALID_ARG, "rows overlap");
+    if ((page > 1 && p.token_stride < p.row_bytes) || (p.heads > 1 && p.head_stride < p.row_bytes) ||
+        (p.num_pages > 1 && p.page_stride < p.row_bytes) || (p.layers > 1 && p.layer_stride < p.row_bytes))
+      return bad(QW_ERR_INVALID_ARG, "rows overlap");
+    for (int j = 0; j < a.npools; ++j)
+      if (a.pool[j].base == p.base) return bad(QW_ERR_INVALID_ARG, "a pool given twice");
     KeepPool &q = a.pool[a.npools++];
     q.base = static_cast<uint8_t *>(p.base);
     q.layer_stride = p.layer_stride;
@@ -287,6 +291,7 @@ int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *b
   if (!at(path, 4) || !at(count, 4) || !at(batch->page_table, 4) || !at(batch->seq_lens, 4) || !at(batch->cu_tokens, 4) ||
       !at(new_lens, 4))
     return bad(QW_ERR_ALIGNMENT, "int32 arrays must be 4-byte aligned");
+  if (new_lens && new_lens == batch->seq_lens) return bad(QW_ERR_INVALID_ARG, "new_lens is the batch's seq_lens");
   if (a.npools == 0 && !new_lens) return QW_OK;
   a.warps = (int)(warps > 0 ? warps : 1);
   const long long grid = ((long long)a.warps * batch->B + kKeepWarps - 1) / kKeepWarps;

@@ -368,3 +368,104 @@ def test_binding_refusals():
         q.attn_tree(c.q, *a, c.parents, out=torch.empty(3, 8, 128, dtype=torch.float16, device=DEV))
     with pytest.raises(TypeError):
         q.attn_tree(c.q.bfloat16(), *a, c.parents)
+
+
+@pytest.mark.parametrize("kind,d,Hq,Hkv", [("fp16", 256, 160, 1), ("int8", 256, 160, 1), ("bf16", 256, 512, 2), ("fp16", 64, 1024, 1)])
+def test_more_heads_than_rows_of_a_block(kind, d, Hq, Hkv):
+    check(Case([200, 5, 70], [3, 5, 1], Hq, Hkv, d, 16, kind, seed=31))
+
+
+@pytest.mark.parametrize("kind", ["fp16", "int8"])
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 7), (256, 32)])
+def test_broadcast_tensors(kind, d, page):
+    """One query row for all nodes or heads, one KV head for all: strides of 0."""
+    c = Case([300, 40], [20, 9], 8, 4, d, page, kind, seed=32)
+    lse = torch.empty(c.T, 8, device=DEV)
+    call = lambda qq, k=c.k, v=c.v, kw=c.kw: q.attn_tree(qq, k, v, *c.args()[2:], c.parents, lse=lse.clone(), **kw)
+    for qq in (c.q[:1].expand_as(c.q), c.q[:, :1].expand_as(c.q), c.q[:1, :1].expand_as(c.q)):
+        assert same(call(qq), call(qq.contiguous()))
+    k, v = (x[:, :1].expand_as(x) for x in (c.k, c.v))
+    kw = {n: x[:, :1].expand_as(x).contiguous() for n, x in c.kw.items()}
+    assert same(call(c.q, k, v, kw), call(c.q, k.contiguous(), v.contiguous(), kw))
+    assert q.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 64, 48])
+def test_scales_at_any_address(d, page):
+    c = Case([300, 40, 1000], [20, 9, 64], 8, 2, d, page, "int8", seed=33)
+    want = check(c)
+    for off in (1, 2, 3):
+        both = torch.full((2, c.kw["k_scale"].numel() + 4), math.nan, device=DEV)
+        kw = {}
+        for x, (n, s) in zip(both, c.kw.items()):
+            kw[n] = x[off:off + s.numel()].view(s.shape)
+            kw[n].copy_(s)
+        assert same(want, q.attn_tree(c.q, *c.args(), c.parents, lse=torch.empty_like(want[1]), **kw))
+
+
+@pytest.mark.parametrize("Hq", [8, 64])
+def test_a_sequence_of_more_nodes_than_said(Hq):
+    """It gets rows of zeros and the flag, whatever blocks it would take; the others their own."""
+    c = Case([500, 1000, 64, 900, 30], [9, 256, 5, 70, 3], Hq, 2, 128, 16, "fp16", seed=34)
+    want = run(c)
+    assert q.device_error() == 0
+    out, lse = run(c, max_nodes=9)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX
+    t = 0
+    for m in c.news:
+        rows = slice(t, t + m)
+        if m > 9:
+            assert bool((out[rows] == 0).all()) and bool(torch.isneginf(lse[rows]).all())
+        else:
+            r = c.reference()
+            assert bool(((out.double() - r[0]).abs() <= c.tolerances(r)[0])[rows].all())
+        t += m
+
+
+def test_two_calls_at_once():
+    """Calls of two streams with workspaces of their own, none waiting for another; and two captured graphs."""
+    c = [Case([9000, 700], [30, 64], 24, 4, 256, 16, "fp16", seed=35), Case([5000, 3, 800], [64, 3, 20], 16, 4, 128, 16, "int8", seed=36)]
+    want = [run(x) for x in c]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(c[i]))
+    torch.cuda.synchronize()
+    assert all(same(w, x) for w, g in zip(want, got) for x in g)
+    graphs, outs = [], []
+    for x in c:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([run(x) for _ in range(4)])
+        graphs.append(g)
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(same(w, x) for w, g in zip(want, outs) for x in g) and q.device_error() == 0
+
+
+@pytest.mark.parametrize("kind,d,page", [("fp16", 64, 16), ("bf16", 128, 8), ("fp16", 256, 64), ("int8", 64, 16), ("int8", 128, 7),
+                                         ("int8", 256, 16), ("fp16", 128, 5)])
+def test_wait_limit_ends_the_kernel(kind, d, page):
+    """At a limit of 0 every wait that is not over when first looked at gives up, in unmodified kernels;
+    afterwards the same workspace serves as before."""
+    c = Case([3000, 40, 700], [40, 9, 64], 8, 2, d, page, kind, seed=37)
+    ws = q.Workspace()
+    want = run(c, ws=ws)
+    assert q.device_error() == 0
+    q.set_wait_limit_us(0)
+    errs = []
+    try:
+        for _ in range(3):
+            run(c, ws=ws)
+            errs.append(q.device_error())
+    finally:
+        q.set_wait_limit_us(None)
+    assert errs == [q.QW_ERR_TIMEOUT] * 3
+    assert same(want, run(c, ws=ws)) and q.device_error() == 0

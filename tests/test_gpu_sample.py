@@ -1,9 +1,10 @@
 """sample_tokens against its definition in binary64 (tests/_tree_ref.py).
 
-Tolerances.  A weight is a whole number of 2^-40 within 4e-9 of its value, so a running sum is
-within 4e-9 (and N 2^-41 / total <= 2^20 2^-41 < 5e-7 only if all N weights were rounded the same
-way; independent, below 1e-9) of the total, and the sum that top-p takes its share of within 1e-7 of the
-part below the border.  So the draw has to be the definition's for some number within 1e-7 of u
+Tolerances.  A weight from 2^-12 on is a whole number of 2^-40 within 2e-11 of its value, a lighter
+one within 4e-6 of it (binary32; thousands of them that round differently, so that less than
+1e-7 of their sum is left), and so is a running sum of the total (N 2^-41 / total <= 2^20 2^-41 <
+5e-7 only if all N weights were rounded to whole numbers the same way; independent, below 1e-9);
+the sum that top-p takes its share of is within 1e-7 of the part below the border.  So the draw has to be the definition's for some number within 1e-7 of u
 and of top_p (relative); its log probability, that answer's within 2^-22 (relative; absolute
 below 1): one rounding of the quotient, one of log1p (2 ulp), the weights."""
 import ctypes
@@ -205,3 +206,39 @@ def test_binding_refusals():
         q.sample_tokens(x, u, top_k=1 << 40)
     with pytest.raises(q.QgemmError):
         q.sample_tokens(x[:, :0], u)
+
+
+@pytest.mark.parametrize("N", [33, 50257])
+def test_one_row_for_all(N):
+    """Logits broadcast over the rows (a stride of 0), in two streams at once."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(1, N, generator=g, device="cuda").half() * 3
+    u = torch.rand(40, generator=g, device="cuda")
+    kw = dict(temperature=0.9, top_k=100, top_p=0.9, min_p=0.01)
+    want = q.sample_tokens(x.repeat(40, 1), u, **kw)
+    got = [q.sample_tokens(x.expand(40, N), u, **kw)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(q.sample_tokens(x.expand(40, N), u, **kw))
+    torch.cuda.synchronize()
+    assert all(torch.equal(want.token, y.token) and torch.equal(want.logprob, y.logprob) for y in got)
+
+
+@pytest.mark.parametrize("n", [30, 63, 64, 65, 127, 128, 129, 255, 256, 257, 400, 1023, 1024, 1025])
+@pytest.mark.parametrize("ties", [False, True])
+def test_lists_of_every_length(n, ties):
+    """n logits far above the rest, all different or many alike, cut in every way."""
+    rng = np.random.default_rng(n)
+    N, M = 20000, 24
+    x = np.full((M, N), -40.0)
+    for r in range(M):
+        at = rng.choice(N, n, replace=False)
+        x[r, at] = rng.choice([0.0, 0.5, 1.0], n) if ties else rng.permutation(n) / n * 3
+    x = torch.tensor(x, dtype=torch.float32, device="cuda")
+    u = torch.tensor(rng.random(M), dtype=torch.float32, device="cuda")
+    for kw in (dict(top_k=n), dict(top_k=max(n // 2, 1)), dict(top_k=7), dict(top_k=max(n - 1, 1), top_p=0.7), dict(top_p=0.5),
+               dict(top_p=0.97), dict(min_p=0.2), dict(top_k=n // 3, top_p=0.9, min_p=0.3)):
+        check(x, u, **kw)

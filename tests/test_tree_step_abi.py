@@ -94,6 +94,22 @@ def test_keep_refusals():
     assert q.lib().kv_keep_path(None, 0, None, 5, 16, P, P, 3, P, N0) == q.QW_ERR_INVALID_ARG
 
 
+def test_strides_that_make_no_sense_are_refused():
+    c, b = cache(), batch()
+    assert tree(c, b, st=(-1024, 128)) == tree(c, b, st=(1024, -128)) == q.QW_ERR_INVALID_ARG
+    sizes = dict(base=B, layers=2, num_pages=4, heads=2, row_bytes=256, layer_stride=1 << 16, page_stride=8192, head_stride=4096,
+                 token_stride=256)
+    names = [k for k, _ in q.RowPoolDesc._fields_]
+
+    def keep(n=1, lens=ctypes.c_void_p(B + 64), **kw):
+        pools = (q.RowPoolDesc * n)(*[q.RowPoolDesc(*[{**sizes, **kw}[k] for k in names]) for _ in range(n)])
+        return q.lib().kv_keep_path(pools, n, batch(), 5, 16, P, P, 3, lens, N0)
+    for name in ("layer_stride", "page_stride", "head_stride", "token_stride"):      # rows that overlap would be moved twice
+        assert keep(**{name: 0}) == keep(**{name: 128}) == q.QW_ERR_INVALID_ARG, name
+    assert keep(n=2) == q.QW_ERR_INVALID_ARG                                         # as would a pool given twice
+    assert keep(lens=ctypes.c_void_p(batch().seq_lens)) == q.QW_ERR_INVALID_ARG      # lengths that other warps still read
+
+
 def test_definitions():
     """The plain forms that the GPU tests compare with, on cases that can be seen."""
     import math
