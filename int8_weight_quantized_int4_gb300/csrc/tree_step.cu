@@ -126,31 +126,36 @@ struct KeepArgs {
   int *err;
 };
 constexpr int kKeepWarps = 8;
-constexpr int kKeepRows = 8;                     // rows in flight a lane
+// Rows in flight a lane.  Warps, not rows, hide the latency: with 8 rows and 100 registers 23 % of
+// an SM's warps were active and 64 sequences of 48 int8 layers (62 MB in all) took 33 us, now 18.
+// (2 rows: 17, and twice the round trips of a long path.)
+constexpr int kKeepRows = 4;
 
+// Moves a lane's column of the rows that lanes hold offsets of (from: -1 none), in the lanes' order.
 template <typename V>
-__device__ __forceinline__ void move_rows(uint8_t *at, bool on, const KeepPool &q, int n, int sp, int so, int dp, int dof) {
-  for (int i = 0; i < n; i += kKeepRows) {
+__device__ __forceinline__ void move_rows(uint8_t *at, bool on, long long from, long long to) {
+  unsigned left = __ballot_sync(0xffffffffu, from >= 0);
+  while (left) {
     V r[kKeepRows];
+    unsigned rows = left;
 #pragma unroll
     for (int k = 0; k < kKeepRows; ++k) {
-      const int p = __shfl_sync(0xffffffffu, sp, (i + k) & 31), o = __shfl_sync(0xffffffffu, so, (i + k) & 31);
-      if (on && i + k < n && (unsigned)p < (unsigned)q.npages)
-        r[k] = *reinterpret_cast<const V *>(at + p * q.page_stride + o * q.token_stride);
+      const long long x = __shfl_sync(0xffffffffu, from, (__ffs(rows) - 1) & 31);
+      if (on && rows) r[k] = *reinterpret_cast<const V *>(at + x);
+      rows &= rows - 1;
     }
 #pragma unroll
     for (int k = 0; k < kKeepRows; ++k) {
-      const int s = __shfl_sync(0xffffffffu, sp, (i + k) & 31);
-      const int p = __shfl_sync(0xffffffffu, dp, (i + k) & 31), o = __shfl_sync(0xffffffffu, dof, (i + k) & 31);
-      if (on && i + k < n && (unsigned)s < (unsigned)q.npages && (unsigned)p < (unsigned)q.npages)
-        *reinterpret_cast<V *>(at + p * q.page_stride + o * q.token_stride) = r[k];
+      const long long x = __shfl_sync(0xffffffffu, to, (__ffs(left) - 1) & 31);
+      if (on && left) *reinterpret_cast<V *>(at + x) = r[k];
+      left &= left - 1;
     }
   }
 }
 
 // One warp 32 columns of a sequence: a column is 16 bytes (4 for scales) of a row's bytes in one
 // layer and head.  Lane i looks up the i-th row's slots; eight rows are read before they are written.
-__global__ void __launch_bounds__(32 * kKeepWarps) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
+__global__ void __launch_bounds__(32 * kKeepWarps, 4) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * kKeepWarps + (threadIdx.x >> 5);
   griddep_wait();
@@ -183,7 +188,8 @@ __global__ void __launch_bounds__(32 * kKeepWarps) kv_keep_kernel(const __grid_c
     int prev = __shfl_up_sync(0xffffffffu, src, 1);
     if (lane == 0) prev = before;
     before = __shfl_sync(0xffffffffu, src, 31);
-    int sp = -1, so = 0, dp = -1, dof = 0;
+    int sp = -1, so = 0, dp = -1, dof = 0;      // pages and rows of them
+    long long from = -1, to = 0;
     if (i < m && src != i) {                     // (a row in its place stays)
       const long long s = (long long)pos0 + src, d = (long long)pos0 + i;
       const bool fine = src > prev && src >= i && src < n && pos0 >= 0;
@@ -194,11 +200,15 @@ __global__ void __launch_bounds__(32 * kKeepWarps) kv_keep_kernel(const __grid_c
         so = (int)(s - (long long)ps * a.page);
         dof = (int)(d - (long long)pd * a.page);
       }
-      if (!fine || (unsigned)sp >= (unsigned)q.npages || (unsigned)dp >= (unsigned)q.npages) atomicCAS(a.err, 0, -9);
+      if ((unsigned)sp >= (unsigned)q.npages || (unsigned)dp >= (unsigned)q.npages) {
+        atomicCAS(a.err, 0, -9);
+      } else {
+        from = sp * q.page_stride + so * q.token_stride;
+        to = dp * q.page_stride + dof * q.token_stride;
+      }
     }
-    const int rows = min(m - i0, 32);
-    if (q.wide) move_rows<uint4>(at, on, q, rows, sp, so, dp, dof);
-    else move_rows<uint32_t>(at, on, q, rows, sp, so, dp, dof);
+    if (q.wide) move_rows<uint4>(at, on, from, to);
+    else move_rows<uint32_t>(at, on, from, to);
   }
 }
 
