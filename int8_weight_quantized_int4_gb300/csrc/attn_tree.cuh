@@ -12,10 +12,9 @@
 // 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
 // of the 128 rows a small tree fills.
 //
-// Roles of a CTA's warps: 8 of softmax (two groups, each half the keys of a tile), 1 issuing MMAs, 2
-// loading and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  A ring of stages, each
-// 64 rows of K or V: the scores of the next tile (d = 256: two) are computed while the softmax works on
-// the last.
+// Roles of a CTA's warps: 8 of softmax (two groups that take tiles in turn), 1 issuing MMAs, 1 loading
+// (d = 256: 2) and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  Rings of K and of V
+// tiles, each 64 rows: the scores of the next tile are computed while the softmax works on the last.
 //   - Rows come by TMA straight to the 128-byte swizzle: pages of a multiple of 8 rows in boxes of up
 //     to 64, other pages four rows a gather, from a map of rows one common divisor of the cache's
 //     strides apart (rows outside it are zeros).  (Gathers move 6 to 9 bytes a clock an SM; cp.async
@@ -30,6 +29,12 @@
 // one equal range a CTA; an item that a border cuts leaves (m, l, O) parts in the workspace, which a
 // second kernel joins.  Where sequences have several row blocks, teams of CTAs run one range, a
 // row block each (tree_schedule).
+//
+// Measured (a graph of calls, inputs larger than L2): 40 contexts of up to 8190, 24 nodes of 32/8 heads
+// of 128, bf16: 114 us, 585 MB, 75 % of the copy rate of HBM.  12 of up to 16384, 64 nodes of 24/4
+// heads of 256, fp16: 195 us; a full row block's tile takes 2730 cycles, of which the MMAs are 1930
+// (two terms of P), and the softmax of a tile bounds it.  5 of up to 65535 int8, 13 nodes: 153 us, 376
+// MB: the same softmax, with scales, and shared memory (codes in, halves out, halves read) bound it.
 //
 // Roundings: each weight enters P V as two terms of the values' 16-bit type, p rounded and what
 // that leaves, so the products keep 22 bits of it (bf16: 16), all sums are binary32 and the output's

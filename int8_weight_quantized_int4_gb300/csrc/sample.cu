@@ -9,23 +9,30 @@
 //
 // A draw near a border of that sum is decided by the last digits, and there are as many borders
 // as tokens.  So the weights that decide are whole numbers, 2^40 w: x - M exactly (as two
-// binary32 terms), its product with log2(e) / t in two terms, 2^y = 2^n (1 + f ln 2 + f^2 q(f))
-// by the series of the exponential function, |f| <= 1/2, the first two terms exact: about 3e-9 of
-// w.  Whole numbers add up the same in any order, so atomics do not change a result.
+// binary32 terms), its product with log2(e) / t in two terms, 2^y
+// from a table of sixteenths of an octave and the series of the exponential function: 2e-11 of w.
+// Weights below 2^-12 are computed in binary32 (4e-6 of w).  Whole numbers add up the same in any order, so atomics do not change a result.
 //
-// A cluster of 1 to 8 CTAs takes a row, as many as fill the GPU.
+// A cluster of 1 to 16 CTAs takes a row, as many as fill the GPU.
 //   1. One pass over the logits: the largest value of every block of 32 elements of a thread, and
 //      for top-p without top-k the block's sum of weights relative to it (binary32).
-//   2. A bound below which nothing can stay: for top-k, a warp's j-th largest block maximum is
-//      reached by j elements, so the least of these over all warps, j = ceil(k / warps), by k; for
-//      top-p the weight that N tokens together need to hold 1 - p of the sum; for min-p its own.
+//   2. A bound below which nothing can stay: for top-k, a CTA's j-th largest thread (or block)
+//      maximum is reached by j elements, so the least of these over the row's CTAs, j = ceil(k /
+//      CTAs), by k; for top-p the largest tried below which the blocks' sums hold no more than 1 - p
+//      of all; for min-p its own.
 //   3. Blocks that reach the bound are read again (from L2), their elements from the bound on
 //      listed; for top-p the rest's weights are summed, blocks that do not reach it as they are.
-//   4. The first CTA resolves the list (some hundreds): bins of a quarter of an octave hold
-//      counts and sums; a border falls in one bin, whose elements compare themselves with each other.
+//   4. The first CTA resolves the list (some hundreds).  Up to 256 elements (a longer list of a top-k is
+//      cut down first) are ranked by comparing each with each; longer lists go to bins of a quarter
+//      of an octave with counts and sums, a border falls in one bin, whose elements compare themselves.
 // A list that overflows (flat rows), or no filter at all, goes over the row instead: 256 bins of keys
 // with counts and weights, the border's bin refined until it fits a list, and the draw by sums
 // of ever smaller ranges.
+//
+// Measured (a graph of calls): one row of 248320 fp16 with top-k 200, top-p and min-p 12.6 us, 768 rows of
+// 50257 bf16 with top-p 42 us (77 MB, 27 % of the copy rate of HBM: after the pass, 8 us of a CTA's 20,
+// three short phases of block-wide steps follow, and 768 rows are 1.3 waves), 200 rows of 32000 with no
+// filter 18.6 us.  Flat rows cost more: 64 x 128257 with a top-p of 0.95 that leaves thousands 57 us.
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
