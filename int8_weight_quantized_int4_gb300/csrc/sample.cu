@@ -51,7 +51,7 @@ constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBlocks = 8;                      // blocks a thread keeps the maxima of
 constexpr int kSmList = 2048;                     // elements a CTA lists
 constexpr int kSmPairs = 256;                     // a list whose elements are compared each with each
-constexpr int kSmShort = 1024;                    // of all CTAs of a row: the first one's alone
+constexpr int kSmShort = 2048;                    // of all CTAs of a row: the first one's alone
 constexpr int kSmBins = 256;
 constexpr int kSmMaxCluster = 16;
 constexpr int kSmFix = 40;                        // weights in units of 2^-40
@@ -133,9 +133,6 @@ __device__ __forceinline__ u64 peer_ld64(uint32_t a) {
   u64 v;
   asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ void peer_st32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void peer_st64(uint32_t a, u64 v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
@@ -338,12 +335,6 @@ struct SampleCta {
     }
     sync();
     return n;
-  }
-  // eighths (quarters) of an octave below the largest logit
-  __device__ __forceinline__ int bin_of(float x, float per) const {
-    if (x == sc.M) return 0;
-    const float y = (sc.M - x) * sc.chi * per;
-    return y < (float)(kSmBins - 1) ? (int)y : kSmBins - 1;        // (NaN: the last)
   }
 
   // bin tid's count or weight `v`: the first bin at which `need` is reached (-1: none; before it:
@@ -683,52 +674,55 @@ __device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &
 }
 
 // Resolves the list of n elements from the key `low` on (one CTA): which stay, and the draw among them.
+// The elements are sorted into 256 bins, by their values for the filters' borders, by their columns
+// for the draw; a border falls in one bin, whose elements compare themselves with each other.
 template <typename T>
 __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
                                             float u, unsigned low) {
   SampleSmem &s = t.s;
-  constexpr int PER = kSmShort / kSmThreads;
   const int tid = t.tid, lane = t.lane;
   if (k > 0 && n > 64 && n > k) n = sample_shrink(t, n, k, low);
   if (n <= kSmPairs) {
     sample_pairs(a, t, r, n, k, p, mp, u);
     return;
   }
-  for (int i = tid; i < kSmBins; i += kSmThreads) {
-    s.cnt[i] = 0;
-    s.mass[i] = 0;
+  unsigned keep = 0;                              // bit i: element tid + i kSmThreads stays
+  u64 best = 0, least = ~0ull;
+  for (int e = tid, i = 0; e < n; e += kSmThreads, ++i) {
+    const u64 key = s.key[e];
+    s.w[e] = t.weight(sm_value((unsigned)(key >> 32)));
+    keep |= 1u << i;
+    best = max(best, key);
+    least = min(least, key);
   }
-  if (tid == 0) {
-    s.top = 0;
-    s.total = 0;
-  }
-  __syncthreads();
-  u64 key[PER], w[PER];
-  int bin[PER];
-  unsigned nth[PER];
-  bool keep[PER];
-  u64 best = 0;
+  const unsigned k0 = __reduce_min_sync(0xffffffffu, (unsigned)(least >> 32));
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid + i * kSmThreads;
-    keep[i] = e < n;
-    key[i] = w[i] = 0;
-    bin[i] = kSmBins;
-    if (!keep[i]) continue;
-    key[i] = s.key[e];
-    const float x = sm_value((unsigned)(key[i] >> 32));
-    w[i] = t.weight(x);
-    s.w[e] = w[i];
-    bin[i] = t.bin_of(x, 4.0f);
-    nth[i] = atomicAdd(&s.cnt[bin[i]], 1u);
-    atomicAdd(&s.mass[bin[i]], w[i]);
-    best = max(best, key[i]);
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) {
+    s.rsum[t.warp] = best;
+    s.nkey[0][t.warp] = (int)k0;
   }
-  atomicMax(&s.top, best);
   __syncthreads();
-  // the elements by their bins: bin b's are s.order[s.start[b]] .. [s.start[b + 1] - 1]
-  auto sort_bins = [&](auto on) {
-    unsigned incl = s.cnt[tid];
+  unsigned last = ~0u;
+#pragma unroll
+  for (int v = 0; v < kSmWarps; ++v) {
+    best = max(best, s.rsum[v]);
+    last = min(last, (unsigned)s.nkey[0][v]);
+  }
+  // bins of equal width from the largest value to the smallest (a NaN, as of infinities, is bin 0)
+  const float from = sm_value((unsigned)(best >> 32)), per = (float)kSmBins * 0.9999f / (from - sm_value(last));
+  auto value_bin = [&](u64 key) { return min(max((int)((from - sm_value((unsigned)(key >> 32))) * per), 0), kSmBins - 1); };
+  const int width = (t.row.N + kSmBins - 1) / kSmBins;
+  auto column_bin = [&](u64 key) { return (int)(~(unsigned)key) / width; };
+  // what stays, by its bins: bin b's are s.order[s.start[b]] .. [s.start[b + 1] - 1]
+  auto sort = [&](auto bin) {
+    s.cnt[tid] = 0;
+    __syncthreads();
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i)
+      if (keep >> i & 1) atomicAdd(&s.cnt[bin(s.key[e])], 1u);
+    __syncthreads();
+    const unsigned own = s.cnt[tid];
+    unsigned incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -739,137 +733,106 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
     for (int v = 0; v < t.warp; ++v) incl += (unsigned)s.nkey[0][v];
     s.start[tid + 1] = (unsigned short)incl;
     if (tid == 0) s.start[0] = 0;
+    s.cnt[tid] = incl - own;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (on(i)) s.order[s.start[bin[i]] + nth[i]] = (unsigned short)(tid + i * kSmThreads);
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i)
+      if (keep >> i & 1) s.order[atomicAdd(&s.cnt[bin(s.key[e])], 1u)] = (unsigned short)e;
     __syncthreads();
   };
   auto others = [&](int b, auto f) {
     for (int q = s.start[b]; q < s.start[b + 1]; ++q) f(s.order[q]);
   };
-  sort_bins([&](int i) { return keep[i]; });
-  // the first bin at which the running count (weights) reaches `need`, and what lies before it
-  auto border = [&](u64 need, bool by_mass) {
-    if (t.warp == 0) {
-      u64 v[kSmBins / 32], sum = 0;
+  // the first bin at which the running weight (or number) of what stays reaches `need`: s.bin
+  // (kSmBins: none), and what lies before it: s.mbefore.  need(total): from all of it.
+  auto border = [&](bool by_mass, auto need) {
+    u64 own = s.start[tid + 1] - s.start[tid];
+    if (by_mass) {
+      own = 0;
+      others(tid, [&](int e) { own += s.w[e]; });
+    }
+    u64 incl = own;
 #pragma unroll
-      for (int i = 0; i < kSmBins / 32; ++i) {
-        v[i] = by_mass ? s.mass[lane * (kSmBins / 32) + i] : s.cnt[lane * (kSmBins / 32) + i];
-        sum += v[i];
-      }
-      u64 incl = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s.rsum[t.warp] = incl;
+    if (tid == 0) s.bin = kSmBins;
+    __syncthreads();
+    u64 total = 0, before = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned at = __ballot_sync(0xffffffffu, incl >= need);
-      if (lane == 0 && at == 0) s.bin = kSmBins;  // everything stays
-      if (at && lane == __ffs(at) - 1) {
-        u64 run = incl - sum;
-        int b = -1;
-#pragma unroll
-        for (int i = 0; i < kSmBins / 32; ++i) {
-          if (b < 0 && run + v[i] >= need) b = i;
-          if (b < 0) run += v[i];
-        }
-        s.bin = lane * (kSmBins / 32) + b;
-        s.mbefore = run;
-      }
+    for (int v = 0; v < kSmWarps; ++v) {
+      if (v == t.warp) before = total;
+      total += s.rsum[v];
+    }
+    incl += before;
+    const u64 at = need(total);
+    if (incl >= at && (incl - own < at || (at == 0 && tid == 0))) {        // (one thread)
+      s.bin = tid;
+      s.mbefore = incl - own;
     }
     __syncthreads();
+    return at;
   };
+  if ((k > 0 && n > k) || p < 1.0f) sort(value_bin);
   if (k > 0 && n > k) {
-    border(k, false);
+    (void)border(false, [&](u64) { return (u64)k; });
     const int kb = s.bin;
     const unsigned before = (unsigned)s.mbefore;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (!keep[i] || bin[i] < kb) continue;
-      if (bin[i] == kb) {
-        unsigned rank = before;
-        others(kb, [&](int e) { rank += s.key[e] > key[i]; });
-        keep[i] = rank < (unsigned)k;
-      } else {
-        keep[i] = false;
-      }
+    unsigned out = 0;
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i) {
+      const u64 key = s.key[e];
+      const int b = value_bin(key);
+      if (b < kb) continue;
+      unsigned rank = before;
+      if (b == kb) others(kb, [&](int o) { rank += s.key[o] > key; });
+      if (b > kb || rank >= (unsigned)k) out |= 1u << i;
     }
     __syncthreads();
-    // sums of what stays
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = tid + i * kSmThreads;
-      if (e < n && !keep[i]) {
-        atomicAdd(&s.mass[bin[i]], 0ull - w[i]);
-        s.w[e] = 0;
-      }
-    }
+    keep &= ~out;
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i)
+      if (out >> i & 1) s.w[e] = 0;
     __syncthreads();
   }
   if (p < 1.0f) {
-    if (t.warp == 0) {
-      u64 sum = 0;
-      for (int i = lane; i < kSmBins; i += 32) sum += s.mass[i];
-      if (k == 0 && lane < (int)t.size) sum += s.tail[lane];
-      sum = SampleCta<T>::reduce(sum);
-      if (lane == 0) s.thr = sample_mass(p, sum);
-    }
-    __syncthreads();
-    const u64 thr = s.thr;
-    border(thr, true);
+    u64 tails = 0;
+    if (k == 0)
+      for (unsigned q = 0; q < t.size; ++q) tails += s.tail[q];
+    const u64 thr = border(true, [&](u64 total) { return sample_mass(p, total + tails); });
     const int pb = s.bin;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (!keep[i] || bin[i] < pb) continue;
-      if (bin[i] == pb) {
-        u64 above = s.mbefore;
-        others(pb, [&](int e) { if (s.key[e] > key[i]) above += s.w[e]; });
-        keep[i] = above < thr || key[i] == s.top;
-      } else {
-        keep[i] = key[i] == s.top;
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i) {
+      const u64 key = s.key[e];
+      const int b = value_bin(key);
+      if (!(keep >> i & 1) || b < pb || key == best) continue;
+      u64 above = thr;
+      if (b == pb) {
+        above = s.mbefore;
+        others(pb, [&](int o) { if (s.key[o] > key) above += s.w[o]; });
       }
+      if (above >= thr) keep &= ~(1u << i);
     }
   }
   if (mp > 0.0f) {
-    const u64 least = (u64)ceil((double)mp * (double)(1ull << kSmFix));
-#pragma unroll
-    for (int i = 0; i < PER; ++i) keep[i] = keep[i] && (w[i] >= least || key[i] == s.top);
+    const u64 bar = (u64)ceil((double)mp * (double)(1ull << kSmFix));
+    for (int e = tid, i = 0; e < n; e += kSmThreads, ++i)
+      if (s.w[e] < bar && s.key[e] != best) keep &= ~(1u << i);
   }
-  // the draw, in the order of the vocabulary: bins of columns
+  // the draw, in the order of the vocabulary
   __syncthreads();
-  for (int i = tid; i < kSmBins; i += kSmThreads) s.cnt[i] = s.mass[i] = 0;
-  __syncthreads();
-  const int width = (t.row.N + kSmBins - 1) / kSmBins;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (!keep[i]) continue;
-    bin[i] = (int)(~(unsigned)key[i]) / width;
-    nth[i] = atomicAdd(&s.cnt[bin[i]], 1u);
-    atomicAdd(&s.mass[bin[i]], w[i]);
-  }
-  __syncthreads();
-  sort_bins([&](int i) { return keep[i]; });
-  if (t.warp == 0) {
-    u64 sum = 0;
-    for (int i = lane; i < kSmBins; i += 32) sum += s.mass[i];
-    sum = SampleCta<T>::reduce(sum);
-    if (lane == 0) {
-      s.total = sum;
-      s.thr = sample_target(u, sum) + 1;
-    }
-  }
-  __syncthreads();
-  border(s.thr, true);
+  sort(column_bin);
+  u64 all = 0;
+  const u64 target = border(true, [&](u64 total) {
+    all = total;
+    return sample_target(u, total) + 1;
+  }) - 1;
   const int vb = s.bin;
-  const u64 target = s.thr - 1;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const unsigned col = ~(unsigned)key[i];
-    if (!keep[i] || bin[i] != vb) continue;
+  for (int e = tid, i = 0; e < n; e += kSmThreads, ++i) {
+    const u64 key = s.key[e];
+    if (!(keep >> i & 1) || column_bin(key) != vb) continue;
+    const unsigned col = ~(unsigned)key;
     u64 run = s.mbefore;
-    others(vb, [&](int e) { if (~(unsigned)s.key[e] < col) run += s.w[e]; });
-    if (run <= target && run + w[i] > target) sample_write(a, r, (int)col, w[i], s.total);
+    others(vb, [&](int o) { if (~(unsigned)s.key[o] < col) run += s.w[o]; });
+    if (run <= target && run + s.w[e] > target) sample_write(a, r, (int)col, s.w[e], all);
   }
 }
 
