@@ -1287,11 +1287,22 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   __syncthreads();
   const uint32_t lead_g = peer(&s.gidx, 0);
   const int items = s.nwork * U;
+  auto item = [&](int i) {                        // vector of work item i (t.v1: none)
+    if (i >= items) return t.v1;
+    const int id = s.work[i >> logU];
+    return min(t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads, t.v1);
+  };
+  // (the next vector is loaded while one is looked through)
+  int vn = item(tid);
+  uint4 next = vn < t.v1 ? t.row.load(vn) : t.row.nothing();
   for (int i = tid; i < items; i += kSmThreads) {
-    const int id = s.work[i >> logU], v = t.v0 + ((id / kSmThreads) * U + (i & (U - 1))) * kSmThreads + id % kSmThreads;
+    const int v = vn;
+    const uint4 raw = next;
+    vn = item(i + kSmThreads);
+    next = vn < t.v1 ? t.row.load(vn) : t.row.nothing();
     if (v >= t.v1) continue;
     float x[VE];
-    t.row.floats(t.row.load(v), x);
+    t.row.floats(raw, x);
     unsigned hits = 0;
     float rest = 0.0f;
 #pragma unroll
