@@ -579,15 +579,20 @@ __device__ __forceinline__ int sample_shrink(SampleCta<T> &t, int n, int k, unsi
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < kSmWarps; ++v) high = max(high, s.cnt[v]);
-  const int per = (n + kSmThreads - 1) / kSmThreads, enough = k + max(k / 4, 16);
+  const int enough = k + max(k / 4, 16);
   int left = n;
 #pragma unroll 1
   for (int round = 0; round < 16 && left > enough && low < high; ++round) {
     const unsigned mid = low + (high - low) / 2 + 1;
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i < per) c += __syncthreads_count((unsigned)(key[i] >> 32) >= mid);
+    for (int i = 0; i < PER; ++i) c += (unsigned)(key[i] >> 32) >= mid;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (t.lane == 0) s.nkey[round & 1][t.warp] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int v = 0; v < kSmWarps; ++v) c += s.nkey[round & 1][v];
     if (c >= k) {
       low = mid;
       left = c;
@@ -740,7 +745,9 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
     __syncthreads();
   };
   auto others = [&](int b, auto f) {
-    for (int q = s.start[b]; q < s.start[b + 1]; ++q) f(s.order[q]);
+    const int end = s.start[b + 1];
+#pragma unroll 4
+    for (int q = s.start[b]; q < end; ++q) f(s.order[q]);
   };
   // the first bin at which the running weight (or number) of what stays reaches `need`: s.bin
   // (kSmBins: none), and what lies before it: s.mbefore.  need(total): from all of it.
