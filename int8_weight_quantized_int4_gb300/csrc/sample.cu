@@ -23,16 +23,16 @@
 //   3. Blocks that reach the bound are read again (from L2), their elements from the bound on
 //      listed; for top-p the rest's weights are summed, blocks that do not reach it as they are.
 //   4. The first CTA resolves the list (some hundreds).  Up to 256 elements (a longer list of a top-k is
-//      cut down first) are ranked by comparing each with each; longer lists go to bins of a quarter
-//      of an octave with counts and sums, a border falls in one bin, whose elements compare themselves.
-// A list that overflows (flat rows), or no filter at all, goes over the row instead: 256 bins of keys
-// with counts and weights, the border's bin refined until it fits a list, and the draw by sums
-// of ever smaller ranges.
+//      cut down first) are ranked by comparing each with each; up to 2048 are sorted into 256 bins
+//      by value, and by column for the draw: a border falls in one bin, whose elements compare themselves.
+// A list that overflows (flat rows), or no filter at all, goes over the row (or the CTAs' lists)
+// instead: 256 bins with counts and weights, the border's bin refined until it fits a list, and the
+// draw by sums of ever smaller ranges.
 //
 // Measured (a graph of calls): one row of 248320 fp16 with top-k 200, top-p and min-p 12.6 us, 768 rows of
 // 50257 bf16 with top-p 42 us (77 MB, 27 % of the copy rate of HBM: after the pass, 8 us of a CTA's 20,
 // three short phases of block-wide steps follow, and 768 rows are 1.3 waves), 200 rows of 32000 with no
-// filter 18.6 us.  Flat rows cost more: 64 x 128257 with a top-p of 0.95 that leaves thousands 57 us.
+// filter 18.7 us.  Flat rows cost more: 64 x 128257 with a top-p of 0.95 that leaves thousands 48 us.
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>

@@ -8,6 +8,7 @@ the sum that top-p takes its share of is within 1e-7 of the part below the borde
 and of top_p (relative); its log probability, that answer's within 2^-22 (relative; absolute
 below 1): one rounding of the quotient, one of log1p (2 ulp), the weights."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -242,3 +243,13 @@ def test_lists_of_every_length(n, ties):
     for kw in (dict(top_k=n), dict(top_k=max(n // 2, 1)), dict(top_k=7), dict(top_k=max(n - 1, 1), top_p=0.7), dict(top_p=0.5),
                dict(top_p=0.97), dict(min_p=0.2), dict(top_k=n // 3, top_p=0.9, min_p=0.3)):
         check(x, u, **kw)
+
+
+@pytest.mark.parametrize("temperature", [1e-38, 1e-30, 1e-6, 1e6, 1e30, float("inf")])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_extreme_temperatures(temperature, dtype):
+    """From the largest logit alone to equal weights, which no list holds; a tenth of the places masked."""
+    x, u = make(7, 20011, dtype, 41)
+    x[:, ::10] = -math.inf
+    for kw in (dict(), dict(top_k=700), dict(top_k=5000), dict(top_p=0.9), dict(top_k=9000, top_p=0.7), dict(min_p=0.5)):
+        check(x, u, temperature=temperature, **kw)
