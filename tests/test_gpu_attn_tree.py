@@ -469,3 +469,43 @@ def test_wait_limit_ends_the_kernel(kind, d, page):
         q.set_wait_limit_us(None)
     assert errs == [q.QW_ERR_TIMEOUT] * 3
     assert same(want, run(c, ws=ws)) and q.device_error() == 0
+
+
+@pytest.mark.parametrize("kind,page", [("fp16", 16), ("fp16", 12), ("int8", 16), ("int8", 7)])
+def test_pages_far_into_a_large_cache(kind, page):
+    """Pools of over 2^32 bytes: the pages at their end, as those of a small cache."""
+    c = Case([400, 60], [20, 9], 8, 4, 256, page, kind, seed=38)
+    want = run(c)
+    n = c.k.shape[0]
+    total = (5 << 30) // (4 * page * 256 * c.k.element_size()) + n
+    k, v = (torch.empty((total, *c.k.shape[1:]), dtype=c.k.dtype, device=DEV) for _ in range(2))
+    k[-n:], v[-n:] = c.k, c.v
+    kw = {}
+    for name, s in c.kw.items():
+        kw[name] = torch.zeros((total, *s.shape[1:]), device=DEV)
+        kw[name][-n:] = s
+    table = c.table + (total - n)
+    assert same(want, q.attn_tree(c.q, k, v, table, c.lens, c.cu, c.parents, lse=torch.empty_like(want[1]), **kw))
+    assert q.device_error() == 0
+    # and its rows moved
+    path, count = torch.tensor([[0, 4, 9], [2, 8, -1]], dtype=torch.int32, device=DEV), torch.tensor([3, 2], dtype=torch.int32, device=DEV)
+    small = q.kv_keep_path(path, count, c.table, c.lens, c.cu, c.k, c.v, *c.kw.values())
+    large = q.kv_keep_path(path, count, table, c.lens, c.cu, k, v, *kw.values())
+    assert torch.equal(small, large) and q.device_error() == 0
+    used = c.table.long().unique()
+    for x, y in zip((c.k, c.v, *c.kw.values()), (k, v, *kw.values())):
+        assert torch.equal(x[used].nan_to_num(7), y[-n:][used].nan_to_num(7))
+
+
+def test_nothing_to_do():
+    """No new tokens, and no sequences."""
+    c = Case([100, 50], [10, 5], 8, 2, 128, 16, "fp16", seed=39)
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    out, lse = q.attn_tree(c.q[:0], c.k, c.v, c.table, c.lens, zero, c.parents[:0], lse=torch.empty(0, 8, device=DEV))
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8)
+    out = torch.full_like(c.q.contiguous(), 3.0)
+    q.attn_tree(c.q, c.k, c.v, c.table[:0], c.lens[:0], zero[:1], c.parents, out=out)
+    assert bool((out == 3).all())
+    path = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
+    assert q.kv_keep_path(path, zero[:0], c.table[:0], c.lens[:0], zero[:1], c.k, c.v).shape == (0,)
+    assert q.device_error() == 0
