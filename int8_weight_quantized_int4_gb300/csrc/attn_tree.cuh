@@ -843,10 +843,6 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
               const uint32_t at = from_s + rs * Sh::kRaw + 16 * ((k0 + k) * WT + t);
               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w) : "r"(at) : "memory");
             }
-            if (k0 + STEP == PER) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(raw_empty(isv, rs));
-            }
 #pragma unroll
             for (int k = 0; k < STEP; ++k) {
               const int id = (k0 + k) * WT + t, row = id / CH, cc = id % CH;
@@ -859,6 +855,10 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
                              : "memory");
             }
           }
+          // (the codes' slot is given back only here, where every load's value has been used: an arrival
+          // right behind the loads let the next copy overtake them)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(raw_empty(isv, rs));
           fence_proxy_async_smem();
           mbar_arrive(full(isv, fs));
         }

@@ -509,3 +509,14 @@ def test_nothing_to_do():
     path = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
     assert q.kv_keep_path(path, zero[:0], c.table[:0], c.lens[:0], zero[:1], c.k, c.v).shape == (0,)
     assert q.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [1, 7, 16])
+def test_int8_tiles_that_wait_for_values(d, page):
+    """Large trees over pages that are gathered: the loads bound the call, so a slot of codes is filled
+    again as soon as it is given back.  Every run the same."""
+    c = Case([2653, 4761, 3900, 1135, 3167], [1, 130, 224, 1, 250], 24, 4, d, page, "int8", seed=40)
+    want = check(c)
+    for _ in range(10):
+        assert same(want, run(c))
