@@ -33,7 +33,7 @@
 // Measured (a graph of calls, inputs larger than L2): 40 contexts of up to 8190, 24 nodes of 32/8 heads
 // of 128, bf16: 114 us, 585 MB, 75 % of the copy rate of HBM.  12 of up to 16384, 64 nodes of 24/4
 // heads of 256, fp16: 195 us; a full row block's tile takes 2730 cycles, of which the MMAs are 1930
-// (two terms of P), and the softmax of a tile bounds it.  5 of up to 65535 int8, 13 nodes: 153 us, 376
+// (two terms of P), and the softmax of a tile bounds it.  5 of up to 65535 int8, 13 nodes: 155 us, 376
 // MB: the same softmax, with scales, and shared memory (codes in, halves out, halves read) bound it.
 //
 // Roundings: each weight enters P V as two terms of the values' 16-bit type, p rounded and what
