@@ -443,7 +443,8 @@ int token_logprobs(const void *logits, int dtype, int M, int N, long long row_st
  * (0: broadcast).  A value of V that a node sees and that is not finite makes its channel of the
  * node's output not finite.  QW_ERR_UNSUPPORTED_SHAPE: more than 2^31 rows of the cache's (or q's)
  * strides' greatest common divisor; query columns times the page table's keys past 2^32 schedule
- * entries ((T Hq / Hkv / 128 + B) Hkv (keys / 64 + 25) > 4e9).  A wait inside the kernel that
+ * entries ((T Hq / Hkv / 128 + B) Hkv (keys / 64 + 25) > 4e9; a call whose offsets descend, so that its
+ * sequences together pass that, computes nothing).  A wait inside the kernel that
  * passes QW_OPT_WAIT_LIMIT_US ends it with QW_ERR_TIMEOUT and undefined results; the workspace
  * needs nothing then.  Results are bit-identical between calls (on devices with the same number of
  * SMs).  Two launches, async.  Returns as attn_paged.

@@ -240,7 +240,7 @@ __device__ __forceinline__ uint32_t tree_widen(uint32_t u) {
 // --------------------------------------------------------------- the schedule --
 struct TreeSeq {
   int tok0, nodes, len;
-  bool fine;
+  bool descends;                                  // its offsets do: its rows may be other sequences' too
 };
 // Sequence b's nodes and keys, clamped to what the buffers hold.
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
@@ -248,6 +248,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
   const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), n = __ldg(a.lens + b);
   s.tok0 = min(max(c0, 0), a.T);
   s.nodes = max(min(max(c1, 0), a.T) - s.tok0, 0);
+  s.descends = c1 < c0;
   s.len = min(max(n, 0), a.cap);
   if (c0 != s.tok0 || c1 != s.tok0 + s.nodes || n != s.len || s.nodes > a.max_nodes) atomicCAS(a.err, 0, -9);
   if (s.nodes > a.max_nodes) s.len = 0;           // rows of zeros
@@ -265,8 +266,8 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs &a, const TreeSeq &
   p.blocks = (int)(((long long)s.nodes * a.G + a.block_rows - 1) / a.block_rows);
   return p;
 }
-// Places of a sequence for teams of R: a tile takes one, an item `cost` more by itself.  All of a
-// call's stay below 2^32 (the host's bound).
+// Places of a sequence for teams of R: a tile takes one, an item `cost` more by itself.  A
+// sequence's stay below kTreeMaxPlaces, and so do all of a call's whose offsets ascend (the host's bound).
 __device__ __forceinline__ unsigned tree_places(const TreeArgs &a, const TreeSpan &p, int R, int cost) {
   return (unsigned)((p.blocks + R - 1) / R) * (unsigned)a.Hkv * (unsigned)(p.n + cost);
 }
@@ -340,13 +341,17 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   const int classes = a.blocks > 1 ? kTreeMaxTeam : 1;
   unsigned sum[kTreeMaxTeam] = {}, bare = 0;
+  bool descends = false;
+  auto add = [](unsigned x, unsigned y) { return y > kTreeMaxPlaces - min(x, kTreeMaxPlaces) ? kTreeMaxPlaces + 1u : x + y; };
   for (int b = b0; b < b1; ++b) {
-    const TreeSpan p = tree_span(a, tree_seq(a, b));
+    const TreeSeq s = tree_seq(a, b);
+    const TreeSpan p = tree_span(a, s);
     const int R = tree_team(a, p);
 #pragma unroll
     for (int k = 0; k < kTreeMaxTeam; ++k)
-      if (k == R - 1) sum[k] += tree_places(a, p, R, IC);
-    bare += tree_places(a, p, 1, 0);
+      if (k == R - 1) sum[k] = add(sum[k], tree_places(a, p, R, IC));
+    bare = add(bare, tree_places(a, p, 1, 0));
+    descends |= s.descends;
   }
   if (tid == 0) {
     ctl->nseg = ctl->more = ctl->zeroed = 0;
@@ -363,7 +368,17 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
     const unsigned v = over_warp(bare);
     if (lane == 0) ctl->bare[warp] = v;
   }
-  __syncthreads();
+  // Offsets that descend (recorded by tree_seq) can name every node many times.  The sums above are
+  // those of the call only if those in 64 bits stay below the limit; else nothing is computed.
+  if (__syncthreads_or(descends)) {
+    atomicAdd(&ctl->bad[0], (unsigned long long)sum[0] + sum[1] + sum[2] + sum[3]);
+    atomicAdd(&ctl->bad[1], (unsigned long long)bare);
+    __syncthreads();
+    const unsigned long long most = max(ctl->bad[0], ctl->bad[1]);
+    __syncthreads();
+    if (tid == 0) ctl->bad[0] = ctl->bad[1] = 0;
+    if (most > kTreeMaxPlaces) return;            // (the whole CTA; its list is empty)
+  }
   unsigned total[kTreeMaxTeam] = {}, tiles = 0;
   for (int w = 0; w < (a.B <= 32 ? 1 : NW); ++w) {
     tiles += ctl->bare[w];

@@ -572,7 +572,7 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   a.max_nodes = max_nodes;
   a.blocks = (max_nodes * G + a.block_rows - 1) / a.block_rows;
   // every item's places, were all contexts as long as the page table: 64 keys each and up to 24 more
-  if (((double)T * G / a.block_rows + b->B) * c->Hkv * (a.cap / 64 + 25) > 4.0e9)
+  if (((double)T * G / a.block_rows + b->B) * c->Hkv * (a.cap / 64 + 25) > (double)kTreeMaxPlaces)
     return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns for a page table so wide");
   a.scale_log2 = scale * 1.4426950408889634f;
   a.desc = static_cast<TreeDesc *>(ws);

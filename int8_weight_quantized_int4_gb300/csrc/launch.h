@@ -139,6 +139,7 @@ cudaError_t launch_attn_paged_bf16(const PagedArgs &a, int d, int cols, int sms,
 cudaError_t launch_attn_paged_i8(const PagedArgs &a, int d, int cols, int sms, cudaStream_t st);
 
 // Attention of trees over the paged cache (attn_tree*.cu)
+constexpr unsigned kTreeMaxPlaces = 4000000000u;   // of all items of a call (sums of 32 bits)
 struct TreeDesc {               // an item that several CTAs share, left by the first of them
   int tok0, col0, cols, g;      // its first row in q, first column, columns (0: none), KV head
   int parts, step;              // parts; CTAs from one to the next

@@ -520,3 +520,44 @@ def test_int8_tiles_that_wait_for_values(d, page):
     want = check(c)
     for _ in range(10):
         assert same(want, run(c))
+
+
+@pytest.mark.parametrize("cu,left", [([1, 3, 2, 4], [0, 4, 5]), ([-7, 1, 1, 2], [2, 3, 4, 5]),
+                                     ([5, 900, 900, 900], [0, 1, 2, 3, 4]), ([6, -2, -2, 0], [0, 1, 2, 3, 4, 5])])
+def test_offsets_stay_inside(cu, left):
+    """Offsets that descend or leave 0 .. T write no row outside q's nor one of no sequence."""
+    c = Case([40, 40, 40], [2, 2, 2], 4, 2, 64, 16, "fp16", seed=44)
+    c.cu.copy_(torch.tensor(cu, device=DEV))
+    c.parents.fill_(-1)
+    big = torch.full((c.T + 16, 4, 64), 3.0, dtype=torch.float16, device=DEV)
+    lse = torch.full((c.T + 16, 4), 3.0, device=DEV)
+    q.attn_tree(c.q, *c.args(), c.parents, max_nodes=2, out=big[8:8 + c.T], lse=lse[8:8 + c.T])
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and q.device_error() == 0
+    keep = torch.ones(c.T + 16, dtype=torch.bool, device=DEV)
+    keep[8:8 + c.T] = False
+    keep[[8 + t for t in left]] = True
+    assert bool((big[keep] == 3.0).all()) and bool((lse[keep] == 3.0).all())
+    assert bool(torch.isfinite(big.float()).all()) and not bool((big[~keep] == 3.0).any())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_overlapping_offsets_past_2_to_32_places(d):
+    """Offsets that descend can name each node many times: 8200 sequences of all 256 nodes, 64 KV heads of 1024 tiles,
+    would be more than 2^32 places.  Nothing is computed, and the next call, with the same workspace, is right.
+    Fewer of them are computed."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    T, H, B = 256, 64, 16400
+    k = torch.randn(1, H, 1024, d, device=DEV).half()
+    table, lens = torch.zeros(B, 64, **i32), torch.full((B,), 65536, **i32)
+    cu = torch.tensor([0, T] * (B // 2) + [0], **i32)
+    qq, parents = torch.randn(T, 16 * H, d, device=DEV).half(), torch.full((T,), -1, **i32)
+    ws = q.Workspace(torch.device("cuda:0"))
+    out = torch.full_like(qq, 3.0)
+    q.attn_tree(qq, k, k, table, lens, cu, parents, max_nodes=256, out=out, ws=ws)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX and bool((out == 3.0).all())
+    check(Case([40, 3000], [1, 20], 64, 64, d, 16, "fp16", seed=45), ws=ws)
+    few = torch.tensor([0, 2, 0, 2, 2], **i32)            # the first and third sequence alike
+    got = q.attn_tree(qq[:2, :H], k, k, table[:4, :1].contiguous(), torch.full((4,), 500, **i32), few, parents[:2], ws=ws)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX
+    want = q.attn_tree(qq[:2, :H], k, k, table[:1, :1].contiguous(), torch.full((1,), 500, **i32), few[:2], parents[:2], ws=ws)
+    assert q.device_error() == 0 and float((got - want).abs().max()) <= 2 ** -9 * float(want.abs().max())
