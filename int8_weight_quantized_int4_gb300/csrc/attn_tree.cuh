@@ -745,6 +745,16 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
             if (!room(isv, tiles + i, bar, dst)) break;
             const bool page = (unsigned)p < (unsigned)a.npages, on = p != -2;
             const int parts = __popc(__ballot_sync(0xffffffffu, on)), pages = kI8 ? __popc(__ballot_sync(0xffffffffu, page)) : 0;
+            if constexpr (kI8) {
+              // (scales of a page that is none are 0, not the tile's before: written ahead of lane 0's arrival)
+              if (pages < parts && !isv && a.scale_boxes) {
+                for (int q = 0; q < a.box && on && !page; ++q) {
+                  const int to = ((tiles + i) % Sh::kScaleSlots) * kTreeKeys + first + q;
+                  ksc[to] = vsc[to] = 0.0f;
+                }
+                __syncwarp();
+              }
+            }
             if (lane == 0)                        // (int8: the tile's scales come with its K)
               mbar_arrive_expect_tx(bar, parts * a.box * kRowBytes + (kI8 && !isv && a.scale_boxes ? pages * a.box * 8 : 0));
             __syncwarp();

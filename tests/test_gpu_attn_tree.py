@@ -561,3 +561,43 @@ def test_overlapping_offsets_past_2_to_32_places(d):
     assert q.device_error() == q.QW_ERR_BAD_INDEX
     want = q.attn_tree(qq[:2, :H], k, k, table[:1, :1].contiguous(), torch.full((1,), 500, **i32), few[:2], parents[:2], ws=ws)
     assert q.device_error() == 0 and float((got - want).abs().max()) <= 2 ** -9 * float(want.abs().max())
+
+
+@pytest.mark.parametrize("kind,d,page", [("fp16", 64, 16), ("bf16", 128, 7), ("fp16", 256, 48), ("int8", 64, 16), ("int8", 128, 16),
+                                         ("int8", 256, 64), ("int8", 128, 7), ("int8", 64, 1)])
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+def test_pages_outside_the_pool_are_rows_of_zeros(kind, d, page, bad):
+    """Compared with the definition, whose cache has a page of zeros there."""
+    c = Case([700, 90], [20, 9], 8, 2, d, page, kind, seed=41)
+    for x in ("k64", "v64"):
+        setattr(c, x, torch.cat([getattr(c, x), torch.zeros_like(getattr(c, x)[:1])]))
+    places = [(0, 3), (0, 5), (0, (700 - 1) // page), (1, 0)]
+    for b, i in places:
+        c.table[b, i] = c.k64.shape[0] - 1
+    r = c.reference()
+    for b, i in places:
+        c.table[b, i] = bad
+    out, lse = run(c)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX
+    tol, lse_tol = c.tolerances(r)
+    assert bool(((out.double() - r[0]).abs() <= tol).all()) and bool(((lse.double() - r[1]).abs() <= lse_tol).all())
+
+
+@pytest.mark.parametrize("d,ctas", [(64, 2), (128, 2), (256, 1)])
+def test_a_page_outside_the_pool_has_no_scales(d, ctas):
+    """Twenty tiles a CTA, every third of a page that is none: its scores are 0, whatever scales the tiles before had (large ones,
+    with codes of 0)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 64 * 20 * ctas * sms
+    k, v = torch.zeros(1, 1, 64, d, dtype=torch.int8, device=DEV), torch.ones(1, 1, 64, d, dtype=torch.int8, device=DEV)
+    ks, vs = torch.full((1, 1, 64), 5e37, device=DEV), torch.ones(1, 1, 64, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.where(torch.arange(n // 64, device=DEV) % 3 == 2, -1, 0).int()[None]
+    qq = torch.randn(1, 1, d, device=DEV).half()
+    lse = torch.empty(1, 1, device=DEV)
+    out, lse = q.attn_tree(qq, k, v, table, torch.tensor([n], **i32), torch.tensor([0, 1], **i32), torch.tensor([-1], **i32), scale=4.0,
+                           k_scale=ks, v_scale=vs, lse=lse)
+    assert q.device_error() == q.QW_ERR_BAD_INDEX
+    share = float((table == 0).sum()) / table.numel()
+    assert bool(((out.double() - share).abs() <= 2.0 ** -10).all())      # (fp16's rounding: 2^-12)
+    assert abs(float(lse) - math.log(n)) <= 2.0 ** -20 * math.log(n)
