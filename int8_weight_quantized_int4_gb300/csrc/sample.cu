@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   const float u = __ldg(a.u + r);
   const bool greedy = !(tau > 0.0f);
   if (k <= 0 || k >= a.N) k = 0;
-  if (!(p < 1.0f)) p = 1.0f;
+  p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;         // (NaN: none)
   if (!(mp > 0.0f)) mp = 0.0f;
   if (mp > 1.0f) {                                // the first alone
     k = a.N > 1 ? 1 : 0;

@@ -253,3 +253,17 @@ def test_extreme_temperatures(temperature, dtype):
     x[:, ::10] = -math.inf
     for kw in (dict(), dict(top_k=700), dict(top_k=5000), dict(top_p=0.9), dict(top_k=9000, top_p=0.7), dict(min_p=0.5)):
         check(x, u, temperature=temperature, **kw)
+
+
+@pytest.mark.parametrize("top_p", [0.0, -0.1, -math.inf])
+def test_a_top_p_not_above_0_leaves_the_first(top_p):
+    """Also of rows that no list holds."""
+    g = torch.Generator().manual_seed(50)
+    x = torch.cat([torch.full((2, 40000), 1.5), torch.randn(2, 40000, generator=g) * 0.01]).half().cuda()
+    x[1, :7] = 0.0
+    u = torch.tensor([0.3, 0.9, 0.0, 0.999], device="cuda")
+    for kw in (dict(), dict(top_k=30), dict(top_k=3000), dict(top_k=30000, min_p=0.5)):
+        r = check(x, u, top_p=top_p, **kw)
+        assert r.token.tolist() == [0, 7, *x[2:].float().argmax(1).tolist()]
+        per_row = torch.full((4,), top_p, device="cuda")
+        assert torch.equal(q.sample_tokens(x, u, top_p=per_row, **kw).token, r.token)
