@@ -608,7 +608,8 @@ __device__ __forceinline__ int sample_shrink(SampleCta<T> &t, int n, int k, unsi
 }
 
 // A list of kSmPairs elements at most: sorted by comparing each with each, by a thread or a few an
-// element; every filter then leaves a first part of it.
+// element; every filter then leaves a first part of it.  (min-p almost: weights of logits next to each
+// other may round the other way round, so what stays is looked for up to the last of it.)
 template <typename T>
 __device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &t, int r, int n, int k, float p, float mp,
                                              float u) {
@@ -662,11 +663,20 @@ __device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &
   s.cnt[tid] = keep ? ~(unsigned)key : 0xffffffffu;
   s.w[tid] = keep ? w : 0;
   const u64 part = SampleCta<T>::reduce(keep ? w : 0);
-  if (lane == 0) s.rsum[warp] = part;
-  const int m = __syncthreads_count(keep), lg = threads(m), e = tid >> lg;
+  const unsigned stay = __ballot_sync(0xffffffffu, keep);
+  if (lane == 0) {
+    s.rsum[warp] = part;
+    s.nkey[0][warp] = stay ? 32 * warp + 32 - __clz(stay) : 0;
+  }
+  __syncthreads();
   u64 all = 0, before = 0;
+  int m = 0;
 #pragma unroll
-  for (int v = 0; v < kSmWarps; ++v) all += s.rsum[v];
+  for (int v = 0; v < kSmWarps; ++v) {
+    all += s.rsum[v];
+    m = max(m, s.nkey[0][v]);
+  }
+  const int lg = threads(m), e = tid >> lg;
   const unsigned col = s.cnt[e];
 #pragma unroll 4
   for (int q = tid & ((1 << lg) - 1); q < m; q += 1 << lg) {

@@ -267,3 +267,26 @@ def test_a_top_p_not_above_0_leaves_the_first(top_p):
         assert r.token.tolist() == [0, 7, *x[2:].float().argmax(1).tolist()]
         per_row = torch.full((4,), top_p, device="cuda")
         assert torch.equal(q.sample_tokens(x, u, top_p=per_row, **kw).token, r.token)
+
+
+def test_every_row_is_drawn_where_weights_lie_at_the_bar_of_min_p():
+    """200 logits within 1e-5 to 1e-9 of where the weight is min_p: some weights of logits next to each other
+    round the other way round there.  Every row's token is written, and its weight reaches min_p within 4e-6."""
+    g = torch.Generator().manual_seed(60)
+    M, N = 1 << 17, 200
+    for width in (1e-6, 1e-8, 1e-9):
+        mp = torch.exp(torch.rand(M, generator=g, dtype=torch.float64) * -8.3).float()
+        t = (torch.rand(M, generator=g) * 3 + 0.2)
+        top = -t.double() * mp.double().log()
+        x = torch.randn(M, N, generator=g) * width - (top - top.float().double()).float()[:, None]
+        x[:, 0] = top.float()
+        u = torch.rand(M, generator=g)
+        x, u, t, mp = (v.cuda() for v in (x, u, t, mp))
+        token, lp = torch.full((M,), -7777, dtype=torch.int32, device="cuda"), torch.full((M,), 1.0, device="cuda")
+        s = q.SamplingDesc(temperature=1.0, top_p=1.0, temperatures=t.data_ptr(), min_ps=mp.data_ptr())
+        ptr = [ctypes.c_void_p(v.data_ptr()) for v in (x, u, token, lp)]
+        assert q.lib().sample_tokens(ptr[0], q.QW_F32, M, N, N, ptr[1], s, *ptr[2:], ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+        torch.cuda.synchronize()
+        assert bool(((token >= 0) & (token < N)).all()) and bool((lp <= 0).all())
+        w = torch.exp((x.gather(1, token.long()[:, None])[:, 0].double() - x[:, 0].double()) / t.double())
+        assert bool((w >= mp.double() * (1 - 4e-6)).all())
