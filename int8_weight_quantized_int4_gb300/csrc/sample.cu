@@ -448,7 +448,7 @@ struct SampleCta {
 
   // The first column, in order, at which the running sum of f over the whole row passes
   // target(total): by the sums of the CTAs, of the warps' ranges and of pieces of one range.
-  // done(column, f there, total) is called by one thread of the CTA that holds it.
+  // done(column, logit, total) is called by one thread of the CTA that holds it.
   // ALL: f is every element's weight.
   template <bool ALL, typename F, typename G, typename H>
   __device__ __forceinline__ void find(F f, G target, H done) {
@@ -511,29 +511,28 @@ struct SampleCta {
             if (lane == __ffs(past) - 1) {
               // (one by one the elements may round to a little less than together: then the last, or
               // where all round to 0 the largest)
-              u64 run = incl - sum, w = 0;
+              u64 run = incl - sum;
               int found = -1;
+              float logit = -INFINITY;
 #pragma unroll
               for (int e = 0; e < VE; ++e) {
                 const u64 y = f(x[e], c + e);
                 if (run <= at && y > 0) {
                   found = c + e;
-                  w = y;
+                  logit = x[e];
                 }
                 run += y;
               }
               if (found < 0) {
-                float best = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                  if (x[e] > best) {
-                    best = x[e];
+                  if (x[e] > logit) {
+                    logit = x[e];
                     found = c + e;
                   }
                 }
-                w = 1;
               }
-              done(found, w, total);
+              done(found, logit, total);
             }
             break;
           }
@@ -544,9 +543,22 @@ struct SampleCta {
   }
 };
 
-__device__ __forceinline__ void sample_write(const SampleArgs &a, int r, int token, u64 w, u64 total) {
+// The token of logit x, and the logarithm of its share: (x - M) / t less that of the total, which is 1
+// and more.  Neither is above 0, so nothing cancels (a far token's weight has few bits left of its
+// units: from the quotient of weights the logarithm was off by 1e-3 at 2^-30).
+static __device__ __noinline__ void sample_write(const SampleArgs &a, int r, int token, float x, float M, u64 total) {
   a.token[r] = token;
-  if (a.logprob) a.logprob[r] = -log1pf((float)(total - w) / (float)w);
+  if (!a.logprob) return;
+  const float t = a.temps ? __ldg(a.temps + r) : a.temp;
+  float q = 0.0f, rest = 0.0f;
+  if (x != M) {                                   // (not both infinite)
+    const float d = x - M, b = d - x;
+    q = __fdiv_rn(d, t);
+    rest = __fdiv_rn(fmaf(-q, t, d) + ((x - (d - b)) + (-M - b)), t);
+    if (!(fabsf(rest) <= 1e-6f * fabsf(q))) rest = 0.0f;          // (t infinite)
+  }
+  constexpr u64 one = 1ull << kSmFix;
+  a.logprob[r] = q - log1pf((float)(total - one) * (1.0f / (float)one)) + rest;
 }
 // floor(u total), below total
 __device__ __forceinline__ u64 sample_target(float u, u64 total) {
@@ -685,7 +697,8 @@ __device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &
   }
   for (int o = 1; o < 1 << lg; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   const u64 target = sample_target(u, all), mine = s.w[e];
-  if ((tid & ((1 << lg) - 1)) == 0 && e < m && before <= target && before + mine > target) sample_write(a, r, (int)col, mine, all);
+  if ((tid & ((1 << lg) - 1)) == 0 && e < m && before <= target && before + mine > target)
+    sample_write(a, r, (int)col, sm_value((unsigned)(sorted[e] >> 32)), t.sc.M, all);
 }
 
 // Resolves the list of n elements from the key `low` on (one CTA): which stay, and the draw among them.
@@ -849,7 +862,7 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
     const unsigned col = ~(unsigned)key;
     u64 run = s.mbefore;
     others(vb, [&](int o) { if (~(unsigned)s.key[o] < col) run += s.w[o]; });
-    if (run <= target && run + s.w[e] > target) sample_write(a, r, (int)col, s.w[e], all);
+    if (run <= target && run + s.w[e] > target) sample_write(a, r, (int)col, sm_value((unsigned)(key >> 32)), t.sc.M, all);
   }
 }
 
@@ -873,7 +886,7 @@ __device__ __forceinline__ void sample_draw(const SampleArgs &a, SampleCta<T> &t
         return ALL || w >= least ? w : 0ull;
       },
       [&](u64 total) { return sample_target(u, total); },
-      [&](int col, u64 w, u64 total) { sample_write(a, r, col, w, total); });
+      [&](int col, float x, u64 total) { sample_write(a, r, col, x, t.sc.M, total); });
 }
 // The same from the CTAs' lists (n of them in this one).
 template <typename T>
@@ -920,7 +933,7 @@ __device__ __forceinline__ void sample_draw_listed(const SampleArgs &a, SampleCt
     __syncthreads();
   }
   for (int e = t.tid; e < n; e += kSmThreads)
-    if (~(unsigned)s.key[e] == lo) sample_write(a, r, (int)lo, s.w[e], total);
+    if (~(unsigned)s.key[e] == lo) sample_write(a, r, (int)lo, sm_value((unsigned)(s.key[e] >> 32)), t.sc.M, total);
 }
 
 // A number in the elements' order: 4095 less the distance from the largest in steps of the first

@@ -290,3 +290,33 @@ def test_every_row_is_drawn_where_weights_lie_at_the_bar_of_min_p():
         assert bool(((token >= 0) & (token < N)).all()) and bool((lp <= 0).all())
         w = torch.exp((x.gather(1, token.long()[:, None])[:, 0].double() - x[:, 0].double()) / t.double())
         assert bool((w >= mp.double() * (1 - 4e-6)).all())
+
+
+def log_shares(x, token, temperature=1.0, top_k=0):
+    """Log probabilities of the tokens (one a row of x, binary64) among the top_k."""
+    t = float(np.float32(temperature))
+    w = np.exp((x - x.max(1, keepdims=True)) / t)
+    total = np.sort(w, 1)[:, -top_k:].sum(1) if top_k else w.sum(1)
+    at = np.arange(len(x)), token
+    return (x[at] - x.max(1)) / t - np.log(total)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kw", [dict(), dict(temperature=1.1), dict(top_k=149999), dict(temperature=0.9, top_k=100000)])
+def test_log_probabilities_of_far_tokens(dtype, kw):
+    """A vocabulary far below one logit, drawn from.  The logarithm: the distance of the logit (exact), its
+    quotient and log1p of the total (an ulp each) and their difference, all below 2^-22 of the result."""
+    N, gaps, parts = 150000, (12.0, 17.0, 19.0, 20.5), (0.02, 0.2, 0.45, 0.7, 0.95)
+    g = torch.Generator().manual_seed(51)
+    x = (torch.randn(len(gaps), N, generator=g) * 0.5).to(TYPES[dtype])
+    x[:, 70000] = torch.tensor(gaps)
+    x = x.repeat_interleave(len(parts), 0)
+    y = x.double().numpy()
+    w = np.exp((y - y.max(1, keepdims=True)) / float(np.float32(kw.get("temperature", 1.0))))
+    far = w[:, 70001:].sum(1) / w.sum(1)
+    u = torch.tensor(1 - far * np.tile(parts, len(gaps)), dtype=torch.float32).cuda()
+    r = q.sample_tokens(x.cuda(), u, **kw)
+    want = log_shares(y, r.token.cpu().numpy(), **kw)
+    err = np.abs(r.logprob.double().cpu().numpy() - want)
+    assert q.device_error() == 0 and (want < -12).sum() >= 15
+    assert (err <= 2 ** -22 * np.maximum(1, np.abs(want))).all(), (err / np.abs(want)).max()
