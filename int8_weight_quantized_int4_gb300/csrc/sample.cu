@@ -185,15 +185,11 @@ constexpr float kSmLight = -12.0f;                // log2 of the weight from whi
 
 // 2^40 2^y for y = (x - M) chi, -12 < y <= 0, to 2e-11: y in two terms, the nearest sixteenth of an
 // octave from a table, and the rest's exponential by its series, whose first term is exact.
-// EXACT: x - M has no rounding (16-bit types).
-template <bool EXACT>
-__device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float clo) {
-  const float d = x - M, y = d * chi;
-  float yl = fmaf(d, chi, -y) + d * clo;
-  if constexpr (!EXACT) {
-    const float b = d - x;                        // what the difference rounded off
-    yl = fmaf((x - (d - b)) + (-M - b), chi, yl);
-  }
+// x - M is rounded for 16-bit types too: fp16 values span 40 bits, and a logit of 2.4e-4 under a largest
+// of 7.9 loses 2.4e-7 of its weight.
+static __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float clo) {
+  const float d = x - M, y = d * chi, b = d - x;  // (x - (d - b)) + (-M - b): what the difference rounded off
+  const float yl = fmaf((x - (d - b)) + (-M - b), chi, fmaf(d, chi, -y) + d * clo);
   const float n = rintf(y), f = y - n;
   const float k = rintf(f * 16.0f), s = fmaf(k, -0.0625f, f);
   constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
@@ -208,11 +204,10 @@ __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float clo) {
 }
 // 2^40 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32 (1e-6 of the weight, without
 // a common sign).
-template <bool EXACT>
 __device__ __forceinline__ u64 sm_weight(float x, const SampleScale &c) {
   if (x == c.M) return 1ull << kSmFix;            // (+inf too)
   const float y = (x - c.M) * c.chi;
-  if (y > kSmLight) return sm_heavy<EXACT>(x, c.M, c.chi, c.clo);
+  if (y > kSmLight) return sm_heavy(x, c.M, c.chi, c.clo);
   return y > -60.0f ? (u64)__float2uint_rn(sm_ex2(y) * (float)(1ull << kSmFix)) : 0;      // (and NaN)
 }
 
@@ -301,7 +296,6 @@ __device__ __forceinline__ int sm_bin_shift(u64 range) { return max(0, 56 - __cl
 template <typename T>
 struct SampleCta {
   static constexpr int VE = SampleRow<T>::VE;
-  static constexpr bool kExact = sizeof(T) == 2;
   SampleSmem &s;
   SampleRow<T> row;
   int tid, warp, lane;
@@ -317,7 +311,7 @@ struct SampleCta {
       __syncthreads();
     }
   }
-  __device__ __forceinline__ u64 weight(float x) const { return sm_weight<kExact>(x, sc); }
+  __device__ __forceinline__ u64 weight(float x) const { return sm_weight(x, sc); }
   // The CTAs' lists at `list`, one behind the other in the first CTA's, if they are `most` together or
   // fewer; their number.  After a sync(), and ends with one.
   __device__ __forceinline__ unsigned join_lists(u64 *list, unsigned most, bool &full) {

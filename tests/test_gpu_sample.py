@@ -320,3 +320,41 @@ def test_log_probabilities_of_far_tokens(dtype, kw):
     err = np.abs(r.logprob.double().cpu().numpy() - want)
     assert q.device_error() == 0 and (want < -12).sum() >= 15
     assert (err <= 2 ** -22 * np.maximum(1, np.abs(want))).all(), (err / np.abs(want)).max()
+
+
+def beside_borders(x, lo, hi, inside=(0.0, 1.0), temperature=1.0, most=400):
+    """Numbers (float32) whose nearest border between two tokens' shares of the row x (binary64) is between lo
+    and hi away, within `inside`; and the tokens that they draw."""
+    w = np.exp((x - x.max()) / float(np.float32(temperature)))
+    sums = np.cumsum(w.astype(np.longdouble))
+    sums = (sums / sums[-1]).astype(np.float64)
+    b = sums[(sums > inside[0]) & (sums < inside[1])]
+    near = b.astype(np.float32)
+    step = int(math.ceil(hi / 2 ** -25))
+    grid = np.unique(np.concatenate([near + np.float32(i * 2 ** -25) for i in range(-step, step + 1)]).astype(np.float32)).astype(np.float64)
+    at = np.searchsorted(sums, grid)
+    gap = np.minimum(np.abs(sums[np.minimum(at, len(sums) - 1)] - grid), np.abs(grid - sums[np.maximum(at - 1, 0)]))
+    grid = grid[(gap >= lo) & (gap <= hi)]
+    grid = grid[np.random.default_rng(0).permutation(len(grid))[:most]]
+    return torch.tensor(grid, dtype=torch.float32), torch.tensor(np.searchsorted(sums, grid, side="right"), dtype=torch.int32)
+
+
+def check_borders(x, lo, hi, fewest, temperature=1.0, inside=(0.35, 0.65), filters=(dict(), dict(min_p=1e-9))):
+    u, want = beside_borders(x.double().numpy(), lo, hi, inside, temperature)
+    assert len(u) >= fewest, len(u)
+    rows = x.cuda()[None].expand(len(u), -1)
+    for kw in filters:
+        got = q.sample_tokens(rows, u.cuda(), temperature=temperature, **kw).token.cpu()
+        assert torch.equal(got, want), (kw, int((got != want).sum()), len(u))
+    assert q.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,top,rest", [("fp16", 7.8984375, 2.4438e-4), ("fp16", 4.5, 3 * 2.0 ** -24), ("bf16", 7.90625, 0.9 * 2.0 ** -22),
+                                            ("fp32", 7.8984375, 2.4438e-4)])
+def test_weights_of_logits_near_zero(dtype, top, rest):
+    """A difference from the largest logit that binary32 does not hold: draws 3e-9 from a border, where weights within
+    2e-11 and half a unit (1.2e-13 of the largest) move it by 1e-10."""
+    n = int(round(math.exp(top)))
+    x = torch.full((n + 1,), rest).to(TYPES[dtype])
+    x[0] = top
+    check_borders(x, 3e-9, 2.5e-8, 10)
