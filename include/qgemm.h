@@ -470,7 +470,7 @@ int attn_tree(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const int3
  *   else gives token -1 and -inf.  Rows with +inf draw among those.
  *   settings: numbers for all rows, or per row [M] where the array is not NULL (device).
  * Weights are compared and summed as whole numbers of 2^-40, so equal inputs give equal tokens:
- * from 2^-12 on with a relative error of 2e-11, below that of 4e-6 (binary32); top-p's sum holds
+ * from 2^-12 on with a relative error of 4e-11, below that of 4e-6 (binary32); top-p's sum holds
  * what lies far below the border in binary32.
  * One launch, async, no workspace.  Returns as kv_append.
  * ------------------------------------------------------------------------ */

@@ -10,7 +10,7 @@
 // A draw near a border of that sum is decided by the last digits, and there are as many borders
 // as tokens.  So the weights that decide are whole numbers, 2^40 w: x - M exactly (as two
 // binary32 terms), its product with log2(e) / t in two terms, 2^y
-// from a table of sixteenths of an octave and the series of the exponential function: 2e-11 of w.
+// from a table of sixteenths of an octave and the series of the exponential function: 4e-11 of w.
 // Weights below 2^-12 are computed in binary32 (4e-6 of w).  Whole numbers add up the same in any order, so atomics do not change a result.
 //
 // A cluster of 1 to 16 CTAs takes a row, as many as fill the GPU.
@@ -183,8 +183,9 @@ static __device__ const u64 kSmPowers[17] = {
     1307547050779ull, 1365437104419ull, 1425890169699ull, 1489019720837ull, 1554944255988ull};
 constexpr float kSmLight = -12.0f;                // log2 of the weight from which on it is computed exactly
 
-// 2^40 2^y for y = (x - M) chi, -12 < y <= 0, to 2e-11: y in two terms, the nearest sixteenth of an
-// octave from a table, and the rest's exponential by its series, whose first term is exact.
+// 2^40 2^y for y = (x - M) chi, -12 < y <= 0, to 4e-11: y in two terms, the nearest sixteenth of an
+// octave from a table, and the rest's exponential by its series, whose first term is exact; the low
+// term's enters with the rest's exponential as its factor (without, it is 1e-8 off).
 // x - M is rounded for 16-bit types too: fp16 values span 40 bits, and a logit of 2.4e-4 under a largest
 // of 7.9 loses 2.4e-7 of its weight.
 static __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float clo) {
@@ -193,12 +194,13 @@ static __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float c
   const float n = rintf(y), f = y - n;
   const float k = rintf(f * 16.0f), s = fmaf(k, -0.0625f, f);
   constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
-  const float p = s * L, pl = fmaf(s, L, -p) + s * Llo + yl * L;
+  const float p = s * L, pl = fmaf(s, L, -p) + s * Llo, low = yl * L;
   // (2^s - 1 - s ln 2) / s^2: ln(2)^k / k! s^(k - 2), k = 2 .. 5
   float q = fmaf(1.33335581e-3f, s, 9.61812911e-3f);
   q = fmaf(q, s, 5.55041087e-2f);
   q = fmaf(q, s, 0.240226507f);
-  const long long t = (long long)__float2int_rn(p * 68719476736.0f) + __float2int_rn(fmaf(q, s * s, pl) * 68719476736.0f);
+  const float z = q * (s * s), rest = fmaf(low, p + z, low) + (z + pl);
+  const long long t = (long long)__float2int_rn(p * 68719476736.0f) + __float2int_rn(rest * 68719476736.0f);
   const u64 w = kSmPowers[(int)k + 8];
   return (w + (u64)__mul64hi((long long)(w << 22), t << 6)) >> -(int)n;
 }

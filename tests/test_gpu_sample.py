@@ -358,3 +358,13 @@ def test_weights_of_logits_near_zero(dtype, top, rest):
     x = torch.full((n + 1,), rest).to(TYPES[dtype])
     x[0] = top
     check_borders(x, 3e-9, 2.5e-8, 10)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("gap", [6.5625, 6.4375, 6.0, 5.875])
+def test_weights_of_a_rounded_exponent(dtype, gap):
+    """Differences whose product with log2(e) is rounded far: draws 2.5e-10 from a border, where weights of 1.4e-3
+    within 4e-11 and a unit of 2^-40 (6.5e-10 of them) move it by 1.8e-10."""
+    x = torch.zeros(int(round(math.exp(gap))) + 1).to(TYPES[dtype])
+    x[0] = gap
+    check_borders(x, 2.5e-10, 1.5e-9, 2)
