@@ -8,9 +8,10 @@
 // order of the vocabulary, at which the running sum of what stays passes u times its total.
 //
 // A draw near a border of that sum is decided by the last digits, and there are as many borders
-// as tokens.  So the weights that decide are whole numbers, 2^40 w: x - M exactly (as two
+// as tokens.  So the weights that decide are whole numbers, 2^42 w: x - M exactly (as two
 // binary32 terms), its product with log2(e) / t in two terms, 2^y
-// from a table of sixteenths of an octave and the series of the exponential function: 4e-11 of w.
+// from a table of sixteenths of an octave and the series of the exponential function: 4e-11 of w, and
+// half a unit (as fine as sums of 2^20 of them in 64 bits, and of a CTA's in bins of 32, allow).
 // Weights below 2^-12 are computed in binary32 (4e-6 of w).  Whole numbers add up the same in any order, so atomics do not change a result.
 //
 // A cluster of 1 to 16 CTAs takes a row, as many as fill the GPU.
@@ -54,7 +55,7 @@ constexpr int kSmPairs = 256;                     // a list whose elements are c
 constexpr int kSmShort = 2048;                    // of all CTAs of a row: the first one's alone
 constexpr int kSmBins = 256;
 constexpr int kSmMaxCluster = 16;
-constexpr int kSmFix = 40;                        // weights in units of 2^-40
+constexpr int kSmFix = 42;                        // weights in units of 2^-42
 
 typedef unsigned long long u64;
 
@@ -85,7 +86,7 @@ struct SampleSmem {
   };
   unsigned short start[kSmBins + 1];
   unsigned cnt[kSmBins];                          // bins: elements,
-  unsigned limb[3][kSmBins];                      // and weights in three terms of 14 bits (a row's slice has below 2^18
+  unsigned limb[3][kSmBins];                      // and weights in three terms of 14 bits (the last up to 2^14; a row's slice has below 2^18
   u64 mass[kSmBins];                              // elements); or their sum
   float red[kSmWarps];
   int nkey[2][kSmWarps];
@@ -176,14 +177,14 @@ __device__ __forceinline__ float sm_value(unsigned k) {
 struct SampleScale {
   float M, chi, clo;
 };
-// 2^40 2^(k / 16), k = -8 .. 8
+// 2^42 2^(k / 16), k = -8 .. 8
 static __device__ const u64 kSmPowers[17] = {
-    777472127994ull,  811893759832ull,  847839367509ull,  885376423200ull,  924575386327ull,  965509835819ull,
-    1008256608221ull, 1052895941925ull, 1099511627776ull, 1148191166361ull, 1199025932245ull, 1252111345494ull,
-    1307547050779ull, 1365437104419ull, 1425890169699ull, 1489019720837ull, 1554944255988ull};
+    3109888511975ull, 3247575039328ull, 3391357470036ull, 3541505692798ull, 3698301545306ull, 3862039343274ull,
+    4033026432885ull, 4211583767698ull, 4398046511104ull, 4592764665442ull, 4796103728980ull, 5008445381977ull,
+    5230188203118ull, 5461748417677ull, 5703560678795ull, 5956078883349ull, 6219777023951ull};
 constexpr float kSmLight = -12.0f;                // log2 of the weight from which on it is computed exactly
 
-// 2^40 2^y for y = (x - M) chi, -12 < y <= 0, to 4e-11: y in two terms, the nearest sixteenth of an
+// 2^42 2^y for y = (x - M) chi, -12 < y <= 0, to 4e-11 and half a unit: y in two terms, the nearest sixteenth of an
 // octave from a table, and the rest's exponential by its series, whose first term is exact; the low
 // term's enters with the rest's exponential as its factor (without, it is 1e-8 off).
 // x - M is rounded for 16-bit types too: fp16 values span 40 bits, and a logit of 2.4e-4 under a largest
@@ -202,9 +203,11 @@ static __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float c
   const float z = q * (s * s), rest = fmaf(low, p + z, low) + (z + pl);
   const long long t = (long long)__float2int_rn(p * 68719476736.0f) + __float2int_rn(rest * 68719476736.0f);
   const u64 w = kSmPowers[(int)k + 8];
-  return (w + (u64)__mul64hi((long long)(w << 22), t << 6)) >> -(int)n;
+  const u64 v = w + (u64)__mul64hi((long long)(w << 20), t << 8);
+  const int r = -(int)n;
+  return (v + ((1ull << r) >> 1)) >> r;
 }
-// 2^40 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32 (1e-6 of the weight, without
+// 2^42 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32 (1e-6 of the weight, without
 // a common sign).
 __device__ __forceinline__ u64 sm_weight(float x, const SampleScale &c) {
   if (x == c.M) return 1ull << kSmFix;            // (+inf too)
@@ -393,7 +396,7 @@ struct SampleCta {
       sum1 += sm_ex2(y[e + 1]);
     }
     sum += sum1;
-    if (top <= kSmLight && sum == sum) return __float2uint_rn(sum * (float)(1ull << kSmFix));
+    if (top <= kSmLight && sum == sum) return __float2ull_rn(sum * (float)(1ull << kSmFix));
     u64 total = 0;
     unsigned heavy = 0;
     sum = 0.0f;
@@ -409,7 +412,7 @@ struct SampleCta {
       for (int e = 1; e < VE; ++e) v = e == k ? x[e] : v;
       total += weight(v);
     }
-    return total + __float2uint_rn(sum * (float)(1ull << kSmFix));
+    return total + __float2ull_rn(sum * (float)(1ull << kSmFix));
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) {

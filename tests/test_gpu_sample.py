@@ -368,3 +368,34 @@ def test_weights_of_a_rounded_exponent(dtype, gap):
     x = torch.zeros(int(round(math.exp(gap))) + 1).to(TYPES[dtype])
     x[0] = gap
     check_borders(x, 2.5e-10, 1.5e-9, 2)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("gap", [8.25, 7.5])
+def test_weights_are_rounded_to_fine_units(dtype, gap):
+    """Thousands of equal weights, all rounded alike: draws 1.5e-10 from a border, where weights of 2^-12 within 4e-11
+    and half a unit of 2^-42 (4.4e-10 of them) move it by a quarter of that, 1.2e-10."""
+    x = torch.zeros(int(round(math.exp(gap))) + 1).to(TYPES[dtype])
+    x[0] = gap
+    check_borders(x, 1.5e-10, 4.5e-10, 6)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("gap", [18.0, 22.0])
+def test_a_flat_vocabulary_far_below_one_logit(dtype, gap):
+    """2^20 - 1 equal tokens: the draw is the definition's for some number within 1e-7 (weights within 3e-7 of an even
+    part of all) and half a unit of 2^-42 a token (1.2e-7) of u."""
+    N = 1 << 20
+    x = torch.zeros(1, N)
+    x[0, 0] = gap
+    x = x.to(TYPES[dtype])
+    w = math.exp(-gap)
+    share = (N - 1) * w / (1 + (N - 1) * w)
+    u = torch.tensor([1 - share * f for f in (0.999, 0.97, 0.8, 0.5, 0.1)], dtype=torch.float32)
+    eps = 1e-7 + N * 2.0 ** -43
+    for kw in (dict(), dict(top_k=N - 1)):
+        r = q.sample_tokens(x.cuda().expand(5, N), u.cuda(), **kw)
+        total = 1 + (N - 1 - bool(kw)) * w
+        for token, lp, v in zip(r.token.tolist(), r.logprob.tolist(), u.double().tolist()):
+            assert token >= 1 and v - eps < (1 + token * w) / total and v + eps >= (1 + (token - 1) * w) / total, (kw, token, v)
+            assert abs(lp + gap + math.log(total)) <= 2 ** -22 * gap
