@@ -470,7 +470,7 @@ int attn_tree(const qw_kv_cache_t *cache, const qw_kv_batch_t *batch, const int3
  *   else gives token -1 and -inf.  Rows with +inf draw among those.
  *   settings: numbers for all rows, or per row [M] where the array is not NULL (device).
  * Weights are compared and summed as whole numbers of 2^-42, so equal inputs give equal tokens:
- * within half a unit, and beside it from 2^-12 on a relative error of 4e-11, below that of 4e-6
+ * within half a unit, and beside it from 2^-12 on a relative error of 4e-11, below that of 5e-7
  * (binary32); top-p's sum holds what lies far below the border in binary32.
  * One launch, async, no workspace.  Returns as kv_append.
  * ------------------------------------------------------------------------ */

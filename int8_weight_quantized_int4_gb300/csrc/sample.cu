@@ -12,7 +12,8 @@
 // binary32 terms), its product with log2(e) / t in two terms, 2^y
 // from a table of sixteenths of an octave and the series of the exponential function: 4e-11 of w, and
 // half a unit (as fine as sums of 2^20 of them in 64 bits, and of a CTA's in bins of 32, allow).
-// Weights below 2^-12 are computed in binary32 (4e-6 of w).  Whole numbers add up the same in any order, so atomics do not change a result.
+// Weights below 2^-12 are computed in binary32 (3e-7 of w, 5e-7 of their sums).  Whole numbers add up the same in any order, so
+// atomics do not change a result.
 //
 // A cluster of 1 to 16 CTAs takes a row, as many as fill the GPU.
 //   1. One pass over the logits: the largest value of every block of 32 elements of a thread, and
@@ -163,6 +164,28 @@ __device__ __forceinline__ void pair_scaled(float x0, float x1, float r, float c
   asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(s));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(x));
 }
+// Pairs of binary32, two to an instruction.
+struct F2 {
+  u64 v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ void get(float &x, float &y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 // binary32 values as unsigned integers in the values' order, -0 as +0, NaN below all (as -inf
 // it is never drawn)
 __device__ __forceinline__ unsigned sm_key(float x) {
@@ -182,7 +205,8 @@ static __device__ const u64 kSmPowers[17] = {
     3109888511975ull, 3247575039328ull, 3391357470036ull, 3541505692798ull, 3698301545306ull, 3862039343274ull,
     4033026432885ull, 4211583767698ull, 4398046511104ull, 4592764665442ull, 4796103728980ull, 5008445381977ull,
     5230188203118ull, 5461748417677ull, 5703560678795ull, 5956078883349ull, 6219777023951ull};
-constexpr float kSmLight = -12.0f;                // log2 of the weight from which on it is computed exactly
+constexpr float kSmLight = -12.0f;                // log2 of the weight from which on it is computed by sm_heavy
+constexpr float kSmLn2 = 0.693147181f;
 
 // 2^42 2^y for y = (x - M) chi, -12 < y <= 0, to 4e-11 and half a unit: y in two terms, the nearest sixteenth of an
 // octave from a table, and the rest's exponential by its series, whose first term is exact; the low
@@ -207,13 +231,20 @@ static __device__ __noinline__ u64 sm_heavy(float x, float M, float chi, float c
   const int r = -(int)n;
   return (v + ((1ull << r) >> 1)) >> r;
 }
-// 2^42 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32 (1e-6 of the weight, without
-// a common sign).
+// e^((x - M) / t) in binary32, 0 below 2^-125 (and for NaN): 2^y, and times what y and x - M round off.
+// (From y alone the weights of a row would all be off the same way, by up to 1.6e-6.)
+__device__ __forceinline__ float sm_light(float x, const SampleScale &c) {
+  const float d = x - c.M, y = d * c.chi, b = d - x;
+  if (!(y > -125.0f)) return 0.0f;
+  const float e = sm_ex2(y);
+  return fmaf(e, kSmLn2 * fmaf((x - (d - b)) + (-c.M - b), c.chi, fmaf(d, c.chi, -y) + d * c.clo), e);
+}
+// 2^42 e^((x - M) / t), rounded; 0 for -inf and NaN.  Below 2^-12 in binary32: ex2's 2^-22 of the weight
+// and 2^-24.
 __device__ __forceinline__ u64 sm_weight(float x, const SampleScale &c) {
   if (x == c.M) return 1ull << kSmFix;            // (+inf too)
-  const float y = (x - c.M) * c.chi;
-  if (y > kSmLight) return sm_heavy(x, c.M, c.chi, c.clo);
-  return y > -60.0f ? (u64)__float2uint_rn(sm_ex2(y) * (float)(1ull << kSmFix)) : 0;      // (and NaN)
+  if ((x - c.M) * c.chi > kSmLight) return sm_heavy(x, c.M, c.chi, c.clo);
+  return __float2uint_rn(sm_light(x, c) * (float)(1ull << kSmFix));
 }
 
 // A row as 16-byte vectors: vector v holds columns v VE - pad .. + VE - 1, pad being how many
@@ -283,6 +314,16 @@ struct SampleRow {
       return *reinterpret_cast<const uint32_t *>(&r);
     } else return h2_as_u32(__hmax2(u32_as_h2(a), u32_as_h2(b)));
   }
+  // elements below `low` (or NaN) raised to it
+  __device__ __forceinline__ static uint4 raised(const uint4 &r, uint32_t low) {
+    return make_uint4(max2(r.x, low), max2(r.y, low), max2(r.z, low), max2(r.w, low));
+  }
+  // the value next below x, or x, twice for 16-bit types
+  __device__ __forceinline__ static uint32_t packed(float x) {
+    if constexpr (kF32) return __float_as_uint(x);
+    else if constexpr (kBf) return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(x)) * 0x10001u;
+    else return (uint32_t)__half_as_ushort(__float2half_rd(x)) * 0x10001u;
+  }
   __device__ __forceinline__ static float max_of(uint32_t m) {
     float r;
     if constexpr (kF32) r = __uint_as_float(m);
@@ -307,6 +348,7 @@ struct SampleCta {
   unsigned rank, size;
   int v0, v1;                                     // its vectors
   SampleScale sc;
+  uint32_t lowest;                                // as vector_weight's, twice for 16-bit types
 
   __device__ __forceinline__ void sync() {        // the cluster's CTAs
     if (size > 1) {
@@ -384,35 +426,55 @@ struct SampleCta {
       }
     }
   }
-  // The weights of one vector's elements, in sum: the light ones in binary32.
-  __device__ __forceinline__ u64 vector_weight(const uint4 &raw) const {
-    float x[VE], y[VE], top = -INFINITY, sum = 0.0f, sum1 = 0.0f;
+  // The weights of one vector's elements, in sum: the light ones in binary32, as sm_light's, two at a
+  // time.  (Of 16-bit types without what x - M rounds off, half a step of it: logits below 2^-9 in size
+  // alone have bits there.)  Elements below `lowest` (also -inf and NaN) count as that, 2^-100.
+  __device__ __forceinline__ u64 vector_weight(uint4 raw) const {
+    raw = row.raised(raw, lowest);
+    float x[VE];
     SampleRow<T>::floats(raw, x);
+    const float top = row.max_of(row.max2(row.max2(raw.x, raw.y), row.max2(raw.z, raw.w)));
+    u64 total = 0;
+    if ((top - sc.M) * sc.chi > kSmLight) {
+      const float low = row.max_of(lowest);
+      unsigned heavy = 0;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) heavy |= (x[e] - sc.M) * sc.chi > kSmLight ? 1u << e : 0u;
+      for (; heavy; heavy &= heavy - 1) {
+        const int k = __ffs(heavy) - 1;
+        float v = x[0];
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          v = e == k ? x[e] : v;
+          x[e] = e == k ? low : x[e];
+        }
+        total += weight(v);
+      }
+    }
+    const F2 to(-sc.M, -sc.M), chi(sc.chi, sc.chi), less(-sc.chi, -sc.chi), clo(sc.clo, sc.clo);
+    F2 w[VE / 2], off(0.0f, 0.0f);
 #pragma unroll
     for (int e = 0; e < VE; e += 2) {
-      pair_scaled(x[e], x[e + 1], sc.M, sc.chi, y[e], y[e + 1]);
-      top = fmaxf(top, fmaxf(y[e], y[e + 1]));
-      sum += sm_ex2(y[e]);
-      sum1 += sm_ex2(y[e + 1]);
+      const F2 v(x[e], x[e + 1]), d = add2(v, to), y = mul2(d, less);        // (-y)
+      F2 r = fma2(d, clo, fma2(d, chi, y));
+      if constexpr (SampleRow<T>::kF32) {         // what the difference rounded off
+        const F2 minus(-1.0f, -1.0f), b = fma2(v, minus, d);
+        r = fma2(add2(fma2(fma2(b, minus, d), minus, v), fma2(b, minus, to)), chi, r);
+      }
+      float y0, y1;
+      y.get(y0, y1);
+      w[e / 2] = F2(sm_ex2(-y0), sm_ex2(-y1));
+      off = fma2(w[e / 2], r, off);
     }
-    sum += sum1;
-    if (top <= kSmLight && sum == sum) return __float2ull_rn(sum * (float)(1ull << kSmFix));
-    u64 total = 0;
-    unsigned heavy = 0;
-    sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      if (y[e] > kSmLight || x[e] == sc.M) heavy |= 1u << e;
-      else sum += y[e] > -60.0f ? sm_ex2(y[e]) : 0.0f;
+    if constexpr (VE == 8) {
+      w[0] = add2(w[0], w[1]);
+      w[1] = add2(w[2], w[3]);
     }
-    for (; heavy; heavy &= heavy - 1) {
-      const int k = __ffs(heavy) - 1;
-      float v = x[0];
-#pragma unroll
-      for (int e = 1; e < VE; ++e) v = e == k ? x[e] : v;
-      total += weight(v);
-    }
-    return total + __float2ull_rn(sum * (float)(1ull << kSmFix));
+    float s0, s1, o0, o1;
+    add2(w[0], w[1]).get(s0, s1);
+    off.get(o0, o1);
+    const float sum = fmaf(kSmLn2, o0 + o1, s0 + s1);
+    return total + ((u64)__float2uint_rn(sum * (float)(1ull << (kSmFix - 2))) << 2);       // (half of four units is at most half of one an element)
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) {
@@ -545,16 +607,15 @@ struct SampleCta {
 // The token of logit x, and the logarithm of its share: (x - M) / t less that of the total, which is 1
 // and more.  Neither is above 0, so nothing cancels (a far token's weight has few bits left of its
 // units: from the quotient of weights the logarithm was off by 1e-3 at 2^-30).
-static __device__ __noinline__ void sample_write(const SampleArgs &a, int r, int token, float x, float M, u64 total) {
+__device__ __forceinline__ void sample_write(const SampleArgs &a, int r, int token, float x, const SampleScale &c, u64 total) {
   a.token[r] = token;
   if (!a.logprob) return;
-  const float t = a.temps ? __ldg(a.temps + r) : a.temp;
   float q = 0.0f, rest = 0.0f;
-  if (x != M) {                                   // (not both infinite)
-    const float d = x - M, b = d - x;
-    q = __fdiv_rn(d, t);
-    rest = __fdiv_rn(fmaf(-q, t, d) + ((x - (d - b)) + (-M - b)), t);
-    if (!(fabsf(rest) <= 1e-6f * fabsf(q))) rest = 0.0f;          // (t infinite)
+  if (x != c.M) {                                 // (not both infinite)
+    constexpr float L = 0.693147180559945f, Llo = (float)(0.69314718055994530942 - (double)L);
+    const float d = x - c.M, y = d * c.chi, b = d - x;
+    q = y * L;
+    rest = fmaf(y, L, -q) + y * Llo + L * fmaf((x - (d - b)) + (-c.M - b), c.chi, fmaf(d, c.chi, -y) + d * c.clo);
   }
   constexpr u64 one = 1ull << kSmFix;
   a.logprob[r] = q - log1pf((float)(total - one) * (1.0f / (float)one)) + rest;
@@ -697,7 +758,7 @@ __device__ __forceinline__ void sample_pairs(const SampleArgs &a, SampleCta<T> &
   for (int o = 1; o < 1 << lg; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   const u64 target = sample_target(u, all), mine = s.w[e];
   if ((tid & ((1 << lg) - 1)) == 0 && e < m && before <= target && before + mine > target)
-    sample_write(a, r, (int)col, sm_value((unsigned)(sorted[e] >> 32)), t.sc.M, all);
+    sample_write(a, r, (int)col, sm_value((unsigned)(sorted[e] >> 32)), t.sc, all);
 }
 
 // Resolves the list of n elements from the key `low` on (one CTA): which stay, and the draw among them.
@@ -861,7 +922,7 @@ __device__ __forceinline__ void sample_list(const SampleArgs &a, SampleCta<T> &t
     const unsigned col = ~(unsigned)key;
     u64 run = s.mbefore;
     others(vb, [&](int o) { if (~(unsigned)s.key[o] < col) run += s.w[o]; });
-    if (run <= target && run + s.w[e] > target) sample_write(a, r, (int)col, sm_value((unsigned)(key >> 32)), t.sc.M, all);
+    if (run <= target && run + s.w[e] > target) sample_write(a, r, (int)col, sm_value((unsigned)(key >> 32)), t.sc, all);
   }
 }
 
@@ -885,7 +946,7 @@ __device__ __forceinline__ void sample_draw(const SampleArgs &a, SampleCta<T> &t
         return ALL || w >= least ? w : 0ull;
       },
       [&](u64 total) { return sample_target(u, total); },
-      [&](int col, float x, u64 total) { sample_write(a, r, col, x, t.sc.M, total); });
+      [&](int col, float x, u64 total) { sample_write(a, r, col, x, t.sc, total); });
 }
 // The same from the CTAs' lists (n of them in this one).
 template <typename T>
@@ -932,7 +993,7 @@ __device__ __forceinline__ void sample_draw_listed(const SampleArgs &a, SampleCt
     __syncthreads();
   }
   for (int e = t.tid; e < n; e += kSmThreads)
-    if (~(unsigned)s.key[e] == lo) sample_write(a, r, (int)lo, sm_value((unsigned)(s.key[e] >> 32)), t.sc.M, total);
+    if (~(unsigned)s.key[e] == lo) sample_write(a, r, (int)lo, sm_value((unsigned)(s.key[e] >> 32)), t.sc, total);
 }
 
 // A number in the elements' order: 4095 less the distance from the largest in steps of the first
@@ -1266,7 +1327,10 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     t.sync();
     return;
   }
-  if (!greedy && k == 0 && p == 1.0f && mp == 0.0f) {
+  // (2^-100 of the largest, if the type and the temperature have such a value; else as with filters)
+  t.lowest = t.row.packed(M - 100.0f / c);
+  const float low = t.row.max_of(t.lowest), far = (M - low) * c;
+  if (!greedy && k == 0 && p == 1.0f && mp == 0.0f && low > -INFINITY && far > 60.0f && far < 1e4f) {
     sample_draw<T, true>(a, t, r, SampleCut{0u, 0x7fffffff}, 0.0f, u);
     t.sync();                                     // (its sums have been read)
     return;

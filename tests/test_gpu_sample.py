@@ -399,3 +399,15 @@ def test_a_flat_vocabulary_far_below_one_logit(dtype, gap):
         for token, lp, v in zip(r.token.tolist(), r.logprob.tolist(), u.double().tolist()):
             assert token >= 1 and v - eps < (1 + token * w) / total and v + eps >= (1 + (token - 1) * w) / total, (kw, token, v)
             assert abs(lp + gap + math.log(total)) <= 2 ** -22 * gap
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_light_weights_have_no_common_error(dtype):
+    """Half of the sum in weights of 2^-17 to 2^-20, at a temperature whose log2(e) / t rounds far: within 2^-22 (ex2)
+    and four sums' 2^-24, all alike at the worst, they move a border by a quarter of 4.8e-7, and rounding 320,000 of
+    them to units of 2^-42 by 3.6e-8."""
+    g = torch.Generator().manual_seed(53)
+    n = 320000
+    x = -1.1 * math.log(2) * (17 + 3 * torch.rand(n + 1, generator=g))
+    x[0] = 0.0
+    check_borders(x.to(TYPES[dtype]), 1.58e-7, 1.78e-7, 50, temperature=1.1)
