@@ -411,3 +411,31 @@ def test_light_weights_have_no_common_error(dtype):
     x = -1.1 * math.log(2) * (17 + 3 * torch.rand(n + 1, generator=g))
     x[0] = 0.0
     check_borders(x.to(TYPES[dtype]), 1.58e-7, 1.78e-7, 50, temperature=1.1)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_top_p_counts_what_lies_far_below(dtype):
+    """Half of the sum in 320,000 tokens far below the border of top_p, the other in 30: which of these stay.  An
+    error that the far ones' weights share (log2(e) / t rounded: 5.5e-7) would move the border by a quarter of it; ex2's
+    2^-22, and what sums of independent roundings leave of 2^-24 a step (1e-7), by 8e-8."""
+    g = torch.Generator().manual_seed(54)
+    n, few, t = 320000, 30, 1.1
+    x = torch.cat([-torch.arange(few) * 0.03125, -t * math.log(2) * (13.5 + torch.rand(n, generator=g))]).to(TYPES[dtype])
+    y = x.double().numpy()
+    w = np.exp((y - y.max()) / float(np.float32(t)))
+    total = w.sum()
+    assert 0.35 < w[few:].sum() / total < 0.65
+    sums = np.cumsum(w[:few]) / total
+    p, want = [], []
+    for j, s in enumerate(sums):
+        if 0.3 < s < 0.5:
+            near = np.float32(s)
+            for i in range(-8, 9):
+                v = float(near + np.float32(i * 2 ** -25))
+                if 0.8e-7 <= abs(v - s) <= 1.3e-7:
+                    p.append(v)
+                    want.append(j + (v > s))
+    assert len(p) >= 10
+    u = torch.full((len(p),), 1 - 2 ** -24, device="cuda")
+    got = q.sample_tokens(x.cuda()[None].expand(len(p), -1), u, temperature=t, top_p=torch.tensor(p, device="cuda")).token.tolist()
+    assert got == want
