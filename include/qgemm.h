@@ -504,7 +504,9 @@ int tree_accept(const int32_t *tokens, const int32_t *drawn, const int32_t *pare
  *   pools: up to four (K, V and their scales); token r of page p, head h, layer l is the
  *   row_bytes bytes at base + l * layer_stride + p * page_stride + h * head_stride + r * token_stride
  *   (strides in bytes, all multiples of 4; 16 bytes at a time where they and base allow).  Rows
- *   that overlap and a base given twice are refused.
+ *   that overlap would be moved in no order: a pool's strides nest (of the dimensions with several
+ *   entries, each is at least what those of smaller strides span), and no two pools share bytes of
+ *   a row (they may be laced, as K and V in one allocation); else QW_ERR_INVALID_ARG.
  *   batch, T: as kv_append; page the tokens of a page.  The pages that hold the nodes belong to one
  *   sequence.  path [B][max_path], count [B]: as tree_accept gives them (entries ascend).
  * An entry that does not ascend or names no node, a count outside 0 .. the nodes, or a page

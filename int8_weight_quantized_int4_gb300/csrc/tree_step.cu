@@ -222,6 +222,80 @@ int bad(int code, const char *fmt, ...) {
   return set_last_error(code, msg);
 }
 bool at(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// A pool's rows start at base + sum i_k stride_k, i_k < n_k: its dimensions of several entries, the
+// largest stride first.
+struct RowDims {
+  int count;
+  long long n[4], stride[4];
+};
+RowDims row_dims(const qw_row_pool_t &p, int page) {
+  const long long n[4] = {p.layers, p.num_pages, p.heads, page}, s[4] = {p.layer_stride, p.page_stride, p.head_stride, p.token_stride};
+  RowDims d{};
+  for (int i = 0; i < 4; ++i) {
+    if (n[i] < 2) continue;
+    int k = d.count++;
+    for (; k > 0 && d.stride[k - 1] < s[i]; --k) {
+      d.n[k] = d.n[k - 1];
+      d.stride[k] = d.stride[k - 1];
+    }
+    d.n[k] = n[i];
+    d.stride[k] = s[i];
+  }
+  return d;
+}
+typedef __int128 wide;                            // (products of sizes and strides pass 64 bits)
+wide row_span(const RowDims &d, int from, long long row) {
+  wide span = row;
+  for (int i = from; i < d.count; ++i) span += (wide)(d.n[i] - 1) * d.stride[i];
+  return span;
+}
+// Rows that overlap: strides that do not nest, each at least what the smaller ones span.
+bool rows_overlap(const RowDims &d, long long row) {
+  for (int i = 0; i < d.count; ++i)
+    if (d.stride[i] < row_span(d, i + 1, row)) return true;
+  return false;
+}
+// Whether x + sum k_i stride_i lies between -below and above (both excluded) for some lo_i <= k_i <= hi_i:
+// the largest stride's k_i are those from which the others' reach it, one to three where strides nest.
+struct RowGap {
+  int count;
+  long long lo[8], hi[8], stride[8];
+  long long below, above;
+  int left;                                       // more steps than these count as found
+};
+bool row_meets(RowGap &g, wide x, int i) {
+  if (--g.left < 0) return true;
+  wide least = 0, most = 0;                       // of what the later ones add
+  for (int k = i + 1; k < g.count; ++k) {
+    least += (wide)g.lo[k] * g.stride[k];
+    most += (wide)g.hi[k] * g.stride[k];
+  }
+  if (i >= g.count) return x > -(wide)g.below && x < (wide)g.above;
+  const wide s = g.stride[i];
+  auto down = [&](wide a) { return a / s - (a % s != 0 && a < 0); };      // floor(a / s)
+  const wide from = -down(x + g.below - 1 + most), to = down(g.above - 1 - x - least);
+  for (wide k = from < g.lo[i] ? (wide)g.lo[i] : from; k <= g.hi[i] && k <= to; ++k)
+    if (row_meets(g, x + k * s, i + 1)) return true;
+  return false;
+}
+// Pools that share bytes of a row, or are laced in a way that 65536 steps do not tell apart.
+bool pools_meet(const qw_row_pool_t &p, const RowDims &a, const qw_row_pool_t &q, const RowDims &b) {
+  const wide x = (wide)reinterpret_cast<uintptr_t>(p.base) - (wide)reinterpret_cast<uintptr_t>(q.base);
+  if (x + row_span(a, 0, p.row_bytes) <= 0 || x >= row_span(b, 0, q.row_bytes)) return false;
+  RowGap g{0, {}, {}, {}, p.row_bytes, q.row_bytes, 65536};
+  for (int i = 0, j = 0; i < a.count || j < b.count;) {       // equal strides together, largest first
+    const bool first = j >= b.count || (i < a.count && a.stride[i] >= b.stride[j]);
+    const bool both = first && j < b.count && a.stride[i] == b.stride[j];
+    g.stride[g.count] = first ? a.stride[i] : b.stride[j];
+    g.hi[g.count] = first ? a.n[i] - 1 : 0;
+    g.lo[g.count] = !first || both ? 1 - b.n[j] : 0;
+    ++g.count;
+    i += first;
+    j += !first || both;
+  }
+  return row_meets(g, x, 0);
+}
 }  // namespace
 }  // namespace qw
 
@@ -262,6 +336,8 @@ int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *b
     return bad(QW_ERR_UNSUPPORTED_SHAPE, "a page table names at most 2^30 keys");
   KeepArgs a{};
   long long warps = 0;
+  RowDims dims[kMaxRowPools];
+  const qw_row_pool_t *given[kMaxRowPools];
   for (int i = 0; i < n_pools; ++i) {
     const qw_row_pool_t &p = pools[i];
     if (p.layers < 0 || p.num_pages < 0 || p.heads < 0 || p.row_bytes < 0 || p.layer_stride < 0 || p.page_stride < 0 ||
@@ -273,12 +349,7 @@ int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *b
     if (!p.base) return bad(QW_ERR_INVALID_ARG, "null pool pointer");
     if (!at(p.base, 4) || p.layer_stride % 4 || p.page_stride % 4 || p.head_stride % 4 || p.token_stride % 4)
       return bad(QW_ERR_ALIGNMENT, "rows start on 4-byte boundaries");
-    if ((page > 1 && p.token_stride < p.row_bytes) || (p.heads > 1 && p.head_stride < p.row_bytes) ||
-        (p.num_pages > 1 && p.page_stride < p.row_bytes) || (p.layers > 1 && p.layer_stride < p.row_bytes))
-      return bad(QW_ERR_INVALID_ARG, "rows overlap");
-    for (int j = 0; j < a.npools; ++j)
-      if (a.pool[j].base == p.base) return bad(QW_ERR_INVALID_ARG, "a pool given twice");
-    KeepPool &q = a.pool[a.npools++];
+    KeepPool &q = a.pool[a.npools];
     q.base = static_cast<uint8_t *>(p.base);
     q.layer_stride = p.layer_stride;
     q.page_stride = p.page_stride;
@@ -291,6 +362,11 @@ int kv_keep_path(const qw_row_pool_t *pools, int n_pools, const qw_kv_batch_t *b
     q.vecs = p.row_bytes / (q.wide ? 16 : 4);
     const long long columns = (long long)p.layers * p.heads * q.vecs;
     if (columns > (1ll << 30)) return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many rows a token");
+    dims[a.npools] = row_dims(p, page);
+    if (rows_overlap(dims[a.npools], p.row_bytes)) return bad(QW_ERR_INVALID_ARG, "rows overlap: a stride below what the smaller ones span");
+    for (int j = 0; j < a.npools; ++j)
+      if (pools_meet(p, dims[a.npools], *given[j], dims[j])) return bad(QW_ERR_INVALID_ARG, "pools %d and %d share rows", (int)(given[j] - pools), i);
+    given[a.npools++] = &p;
     q.columns = (int)columns;
     q.first = (int)warps;
     warps += (columns + 31) / 32;

@@ -129,3 +129,83 @@ def test_definitions():
     assert ref.accept([9, 5, 5, 7], [5, 7, 7, 1], [-1, 0, 0, 1], 2) == ([0, 1], 7)
     assert ref.accept([], [], [], 2) == ([], -1)
     assert ref.ancestors([-1, 0, 0, 2], 3) == [0, 2, 3]
+
+
+def row_pool(base, shape, strides, row):
+    return q.RowPoolDesc(base, shape[0], shape[1], shape[2], row, strides[0], strides[1], strides[2], strides[3])
+
+
+def keep_pools(*pools, page=16):
+    """What kv_keep_path says of the pools: no offsets are given, so what passes ends with an aligned pointer's refusal."""
+    a = (q.RowPoolDesc * len(pools))(*pools)
+    return q.lib().kv_keep_path(a, len(pools), batch(), 5, page, ODD, P, 3, P, N0)
+
+
+def test_rows_that_overlap_are_refused():
+    """Strides that are fine one by one."""
+    page, heads, row = 16, 4, 256
+    good, bad = q.QW_ERR_ALIGNMENT, q.QW_ERR_INVALID_ARG
+    hnd, nhd = (4 * 16384, 16384, 4096, 256), (4 * 16384, 16384, 256, 1024)
+    for st in (hnd, nhd, (1 << 40, 16384 + 64, 4096 + 16, 256), (16384, 2 * 16384, 256, 1024), (256, 512, 2048, 8192 * 4)):
+        assert keep_pools(row_pool(B, (2, 4, heads), st, row)) == good, st
+    for st in ((4 * 16384, 16384, 256, 256), (4 * 16384, 16384, 256, 1020), (4 * 16384, 16380, 4096, 256), (16384, 16384, 4096, 256),
+               (3 * 16384, 16384, 4096, 256), (4 * 16384, 16384, 4092, 256), (1 << 62, 1 << 62, 1 << 62, 1 << 62)):
+        assert keep_pools(row_pool(B, (2, 4, heads), st, row)) == bad, st
+    # dimensions of one entry mean nothing
+    assert keep_pools(row_pool(B, (1, 4, 1), (0, 4096, 0, 256), row)) == good
+    assert keep_pools(row_pool(B, (2, 4, heads), (1024, 2048, 256, 0), row), page=1) == good
+
+
+def test_pools_that_share_rows_are_refused():
+    good, bad = q.QW_ERR_ALIGNMENT, q.QW_ERR_INVALID_ARG
+    hnd, shape = (4 * 16384, 16384, 4096, 256), (2, 4, 4)
+    size = 2 * 4 * 16384
+    k = row_pool(B, shape, hnd, 256)
+    assert keep_pools(k, row_pool(B + size, shape, hnd, 256)) == good                       # one after the other
+    assert keep_pools(k, row_pool(B + size - 256, shape, hnd, 256)) == bad                  # by its last row
+    assert keep_pools(k, row_pool(B + 4, shape, hnd, 256)) == bad
+    assert keep_pools(k, row_pool(B + 4 * 16384, (1, 4, 4), hnd, 256)) == bad               # pools[0] and pools[0][1:]
+    assert keep_pools(row_pool(B, (1, 4, 4), hnd, 256), row_pool(B + 4 * 16384, (1, 4, 4), hnd, 256)) == good      # its layers
+    # K and V laced by layer, page, head or token
+    for st, gap in (((8 * 16384, 16384, 4096, 256), 4 * 16384), ((8 * 16384, 32768, 4096, 256), 16384), ((8 * 16384, 32768, 8192, 256), 4096),
+                    ((8 * 16384, 32768, 8192, 512), 256)):
+        assert keep_pools(row_pool(B, shape, st, 256), row_pool(B + gap, shape, st, 256)) == good, st
+        assert keep_pools(row_pool(B + gap, shape, st, 256), row_pool(B, shape, st, 256)) == good, st
+        assert keep_pools(row_pool(B, shape, st, 256), row_pool(B + gap - 16, shape, st, 256)) == bad, st
+    # codes and scales in one page: 16 rows of 256 bytes, then 16 numbers
+    st = (4 * 4 * 4160, 4 * 4160, 4160)
+    codes, scales = row_pool(B, shape, (*st, 256), 256), row_pool(B + 4096, shape, (*st, 4), 4)
+    assert keep_pools(codes, scales) == keep_pools(scales, codes) == good
+    assert keep_pools(codes, row_pool(B + 4092, shape, (*st, 4), 4)) == bad
+    # a row's scale behind its codes
+    st = (16 * 4 * 4 * 260, 16 * 4 * 260, 16 * 260, 260)
+    assert keep_pools(row_pool(B, shape, st, 256), row_pool(B + 256, shape, st, 4)) == good
+    assert keep_pools(row_pool(B, shape, st, 260), row_pool(B + 256, shape, st, 4)) == bad
+    # four pools, and one without rows
+    four = [row_pool(B + i * size, shape, hnd, 256) for i in range(4)]
+    assert keep_pools(*four) == good and keep_pools(*four[:3], four[1]) == bad
+    assert keep_pools(k, row_pool(B, (0, 4, 4), hnd, 256)) == good
+
+
+def test_pools_that_meet_by_chance():
+    """Random strides, compared with all rows laid out."""
+    import random
+    rng = random.Random(3)
+    seen = [0, 0]
+    for _ in range(400):
+        pools, rows = [], []
+        for _ in range(2):
+            n = [rng.randint(1, 3) for _ in range(3)] + [2]
+            row, order, st, span = 4 * rng.randint(1, 3), rng.sample(range(4), 4), [0] * 4, 0
+            span = row
+            for i in order:
+                st[i] = span + 4 * rng.choice([0, 0, 0, 1, 2, 8])
+                span += (n[i] - 1) * st[i]
+            base = 4 * rng.randint(0, 60)
+            pools.append(row_pool(B + base, n[:3], st, row))
+            rows.append({base + a * st[0] + b * st[1] + c * st[2] + d * st[3] + e for a in range(n[0]) for b in range(n[1])
+                         for c in range(n[2]) for d in range(n[3]) for e in range(row)})
+        meet = bool(rows[0] & rows[1])
+        seen[meet] += 1
+        assert keep_pools(*pools, page=2) == (q.QW_ERR_INVALID_ARG if meet else q.QW_ERR_ALIGNMENT)
+    assert min(seen) > 60
