@@ -190,19 +190,20 @@ __global__ void __launch_bounds__(32 * kKeepWarps, 4) kv_keep_kernel(const __gri
     before = __shfl_sync(0xffffffffu, src, 31);
     int sp = -1, so = 0, dp = -1, dof = 0;      // pages and rows of them
     long long from = -1, to = 0;
-    if (i < m && src != i) {                     // (a row in its place stays)
+    if (i < m) {
       const long long s = (long long)pos0 + src, d = (long long)pos0 + i;
       const bool fine = src > prev && src >= i && src < n && pos0 >= 0;
+      const bool moves = fine && src != i;        // (a row in its place stays)
       const int ps = (int)(s / a.page), pd = (int)(d / a.page);
-      if (fine && ps < a.max_pages) {
+      if (moves && ps < a.max_pages) {
         sp = __ldg(a.table + (long long)b * a.max_pages + ps);
         dp = __ldg(a.table + (long long)b * a.max_pages + pd);
         so = (int)(s - (long long)ps * a.page);
         dof = (int)(d - (long long)pd * a.page);
       }
-      if ((unsigned)sp >= (unsigned)q.npages || (unsigned)dp >= (unsigned)q.npages) {
+      if (!fine || (moves && ((unsigned)sp >= (unsigned)q.npages || (unsigned)dp >= (unsigned)q.npages))) {
         atomicCAS(a.err, 0, -9);
-      } else {
+      } else if (moves) {
         from = sp * q.page_stride + so * q.token_stride;
         to = dp * q.page_stride + dof * q.token_stride;
       }

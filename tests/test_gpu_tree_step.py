@@ -168,3 +168,15 @@ def test_keep_binding_refusals():
         q.tree_accept(i32([1, 2, 3]), i32([1, 2]), i32([-1, 0, 0]), i32([0, 3]), max_path=2)
     with pytest.raises(ValueError):
         q.tree_accept(i32([1]), i32([1]), i32([-1]), i32([0, 1]), max_path=0)
+
+
+def test_keep_entries_in_their_place_that_do_not_ascend():
+    """Entry 1 names slot 1, where it is, after an entry that did so already."""
+    x = torch.arange(4 * 1 * 4 * 64, dtype=torch.float16, device="cuda").view(4, 1, 4, 64)
+    table, lens, cu = i32([[0, 1, 2]]), i32([9]), i32([0, 6])             # slots 3 .. 8
+    y = x.clone()
+    y[0, 0, 3] = y[1, 0, 0]                                               # slot 3 takes slot 4
+    new = q.kv_keep_path(i32([[1, 1]]), i32([2]), table, lens, cu, x)
+    assert new.tolist() == [5] and torch.equal(x, y) and q.device_error() == q.QW_ERR_BAD_INDEX
+    q.kv_keep_path(i32([[0, 1, 2]]), i32([3]), table, lens, cu, x)        # all in their place
+    assert torch.equal(x, y) and q.device_error() == 0
