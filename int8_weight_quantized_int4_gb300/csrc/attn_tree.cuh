@@ -848,12 +848,12 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           // a tile's scales, with its K: logarithm and inverse of V's (of 0: of 2^-100, which times
-          // vs is 0 again)
+          // vs is 0 again; at most 2^126, whose inverse is normal)
           if (!isv) {
             for (int e = t; e < kTreeKeys; e += WT) {
               const int at = (gt % Sh::kScaleSlots) * kTreeKeys + e;
               const float v = fabsf(vsc[at]);
-              const float lv = v < INFINITY ? fmaxf(tree_lg2(v), -100.0f) : 0.0f;
+              const float lv = v < INFINITY ? fminf(fmaxf(tree_lg2(v), -100.0f), 126.0f) : 0.0f;
               vlog[at] = lv;
               vinv[at] = tree_ex2(-lv);
               ksc[at] *= a.scale_log2;

@@ -601,3 +601,16 @@ def test_a_page_outside_the_pool_has_no_scales(d, ctas):
     share = float((table == 0).sum()) / table.numel()
     assert bool(((out.double() - share).abs() <= 2.0 ** -10).all())      # (fp16's rounding: 2^-12)
     assert abs(float(lse) - math.log(n)) <= 2.0 ** -20 * math.log(n)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_largest_scales(d):
+    """Value scales up to 2^127: the outputs pass fp16, the sum of exponentials does not care."""
+    c = Case([300, 70], [20, 9], 8, 2, d, 16, "int8", seed=42)
+    want = run(c)
+    for s in (2.0 ** 125, 2.0 ** 126, 2.0 ** 127):
+        c.kw["v_scale"].fill_(s)
+        c.v.fill_(3)
+        out, lse = run(c)
+        tol = c.tolerances(c.reference())[1]
+        assert q.device_error() == 0 and bool(torch.isposinf(out).all()) and bool(((lse - want[1]).abs() <= 2 * tol).all())
