@@ -1181,8 +1181,9 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
           if constexpr (!kI8) {
             // A value that is not finite would reach the rows that do not see its key (0 times it is NaN),
             // so tiles seen partly are searched for such keys.  They are added here, to the rows
-            // that see them, and cleared for the MMA.
-            if (masked) {
+            // that see them, and cleared for the MMA.  (Not where no row sees anything: a sequence of more nodes
+            // than are allowed has no masks, so no barrier between this and the other group's rows of the last segment.)
+            if (masked && s.len > 0) {
               const uint32_t vst = v_s + (gt % F) * Sh::kStage;
               stop = stop || !pwait(full(1, gt % F), (uint32_t)((gt / F) & 1));
               if (row == 0) ctl->bad[grp] = 0;

@@ -614,3 +614,30 @@ def test_the_largest_scales(d):
         out, lse = run(c)
         tol = c.tolerances(c.reference())[1]
         assert q.device_error() == 0 and bool(torch.isposinf(out).all()) and bool(((lse - want[1]).abs() <= 2 * tol).all())
+
+
+def test_sequences_of_more_nodes_than_any():
+    """Between others, in CTAs whose shared memory holds NaN from the call before: rows of zeros, the others their own."""
+    lens, news = [60, 400, 33] * 150, [5, 300, 7] * 150
+    for kind, d in (("fp16", 128), ("bf16", 64), ("fp16", 256)):
+        c = Case(lens, news, 8, 8, d, 16, kind, seed=43)
+        small = [b for b, m in enumerate(news) if m < 100]
+        rows = torch.cat([torch.arange(int(c.cu[b]), int(c.cu[b + 1]), device=DEV) for b in small])
+        nan = torch.full_like(c.k, math.nan)
+        want = None
+        for _ in range(3):
+            q.attn_paged(c.q[:450], nan, nan, c.table, c.lens, torch.arange(451, dtype=torch.int32, device=DEV))
+            out, lse = run(c, max_nodes=8)
+            assert q.device_error() == q.QW_ERR_BAD_INDEX
+            alone = torch.ones(c.T, dtype=torch.bool, device=DEV)
+            alone[rows] = False
+            assert bool((out[alone] == 0).all()) and bool(torch.isneginf(lse[alone]).all())
+            want = want or (out, lse)
+            assert same(want, (out, lse))
+        s = Case([lens[b] for b in small[:6]], [news[b] for b in small[:6]], 8, 8, d, 16, kind, seed=43)
+        s.k, s.v, s.k64, s.v64 = c.k, c.v, c.k64, c.v64
+        s.table, s.q = c.table[small[:6]], c.q[rows[:s.T]]
+        s.trees = [c.trees[b] for b in small[:6]]
+        r = s.reference()
+        tol, lse_tol = s.tolerances(r)
+        assert bool(((out[rows[:s.T]].double() - r[0]).abs() <= tol).all()) and bool(((lse[rows[:s.T]].double() - r[1]).abs() <= lse_tol).all())
