@@ -1560,7 +1560,7 @@ extern "C" int sample_tokens(const void *logits, int dtype, int M, int N, long l
   // 32768 (768 x 50257: 46 us with one CTA a row, 64 with two).  16 have to fit one part of the GPU; a CTA's part
   // has below 2^18 elements.
   long long best = 0;
-  for (int c = 1; c <= (M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8); c *= 2) {
+  for (int c = 1; c <= ((long long)M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8); c *= 2) {
     const long long cost = ((long long)M * c + 4 * sms - 1) / (4 * sms) * (N / c + 32768);
     if (N / c < (1 << 18) - 16 && (best == 0 || cost < best)) {
       best = cost;
