@@ -3,6 +3,7 @@
 //
 // Both kernels only move bytes (2 d e a row, read and written), so what bounds them is HBM
 // for large calls and the launch with its chain of dependent reads for small ones.
+#include <algorithm>
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
@@ -532,7 +533,8 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   // that makes more of them than 128 rows of any nodes do, for a sequence of max_nodes.
   // (d = 256 reads its rows one by one).
   a.block_rows = G <= 128 && c->d < 256 ? 128 / G * G : 128;
-  a.q_box = G <= 128 && c->d < 256 && (max_nodes * G + a.block_rows - 1) / a.block_rows == (max_nodes * G + 127) / 128;
+  auto blocks = [&](int rows) { return ((long long)max_nodes * G + rows - 1) / rows; };
+  a.q_box = G <= 128 && c->d < 256 && blocks(a.block_rows) == blocks(128);
   a.q_box = a.q_box && lies(Hq, q_head_stride) && lies(T, q_token_stride);
   if (!a.q_box) a.block_rows = 128;
   if (a.q_box) {
@@ -570,7 +572,7 @@ int attn_tree(const qw_kv_cache_t *c, const qw_kv_batch_t *b, const int32_t *par
   a.page_shift = (c->page & (c->page - 1)) == 0 ? 0 : -1;
   while (a.page_shift >= 0 && c->page >> a.page_shift > 1) ++a.page_shift;
   a.max_nodes = max_nodes;
-  a.blocks = (max_nodes * G + a.block_rows - 1) / a.block_rows;
+  a.blocks = (int)std::min(blocks(a.block_rows), 0x7fffffffll);
   // every item's places, were all contexts as long as the page table: 64 keys each and up to 24 more
   if (((double)T * G / a.block_rows + b->B) * c->Hkv * (a.cap / 64 + 25) > (double)kTreeMaxPlaces)
     return bad(QW_ERR_UNSUPPORTED_SHAPE, "too many query columns for a page table so wide");
