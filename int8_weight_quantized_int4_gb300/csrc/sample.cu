@@ -1396,6 +1396,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
 
   // ---- 3. the list
   u64 tail = 0;
+  const bool counts = sums && M < INFINITY;       // (beside infinite logits the others weigh nothing)
   auto fixed = [&](float x) { return __float2ull_rn(x * (float)(1ull << kSmFix)); };
   for (int b = 0; b < nblk; ++b) {
     const float bm = s.bmax[b][tid];
@@ -1405,7 +1406,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
     if (v && lane == 0) at = atomicAdd(&s.nwork, __popc(v));
     at = __shfl_sync(0xffffffffu, at, 0);
     if (hit) s.work[at + __popc(v & ((1u << lane) - 1u))] = (unsigned short)(b * kSmThreads + tid);
-    else if (sums) tail += fixed(rel(bm, s.bsum[b][tid], M));
+    else if (counts) tail += fixed(rel(bm, s.bsum[b][tid], M));
   }
   __syncthreads();
   const uint32_t lead_g = peer(&s.gidx, 0);
@@ -1431,7 +1432,7 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       if (sm_key(x[e]) >= T0) hits |= 1u << e;
-      else if (sums && x[e] > -INFINITY) rest += power(x[e] - M);
+      else if (counts && x[e] > -INFINITY) rest += power(x[e] - M);
     }
     if (sums) tail += fixed(rest);
     if (hits) {

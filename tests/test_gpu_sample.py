@@ -439,3 +439,17 @@ def test_top_p_counts_what_lies_far_below(dtype):
     u = torch.full((len(p),), 1 - 2 ** -24, device="cuda")
     got = q.sample_tokens(x.cuda()[None].expand(len(p), -1), u, temperature=t, top_p=torch.tensor(p, device="cuda")).token.tolist()
     assert got == want
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("temperature", [0.8, 1.1, 3.0, math.inf])
+def test_infinite_logits_at_any_temperature(dtype, temperature):
+    """Two of three weights of 1 stay, or one: nothing else counts towards top_p."""
+    x, _ = make(8, 3000, dtype, 61)
+    x[:, 17] = x[:, 1500] = x[:, 2900] = math.inf
+    u = torch.tensor([0.0, 0.2, 0.4, 0.6, 0.8, 0.9, 0.95, 0.999], device="cuda")
+    for p, n in ((0.5, 2), (0.3, 1), (0.9, 3)):
+        for kw in (dict(), dict(min_p=0.1), dict(top_k=2999)):
+            r = q.sample_tokens(x, u, temperature=temperature, top_p=p, **kw)
+            assert r.token.tolist() == [(17, 1500, 2900)[int(v * n)] for v in u.tolist()]
+            assert bool(((r.logprob.double() + math.log(n)).abs() <= 2 ** -22 * max(1.0, math.log(n))).all())
