@@ -1163,7 +1163,8 @@ __global__ void __launch_bounds__(kSmThreads, 4) sample_kernel(const __grid_cons
   // e^(d / t) for the sums of what lies below top-p's bound; the low term takes away an error that all would
   // share (7e-7 of them at 2^-18 and t = 1.1).  The pass goes without: what counts in a block lies a few octaves
   // below its largest, where it is 2e-7 (with it 768 x 50257 take 46.8 us, so 42.4).
-  auto power = [&](float d) { return sm_ex2(fmaf(d, c, d * clo)); };
+  // (The distance of finite logits can be infinite too.)
+  auto power = [&](float d) { return sm_ex2(fmaf(d, c, fmaxf(d, -3.0e38f) * clo)); };
 
   // ---- 1. blocks: U vectors of a thread, kSmThreads apart
   constexpr int U0 = 32 / VE;

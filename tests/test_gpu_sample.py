@@ -453,3 +453,19 @@ def test_infinite_logits_at_any_temperature(dtype, temperature):
             r = q.sample_tokens(x, u, temperature=temperature, top_p=p, **kw)
             assert r.token.tolist() == [(17, 1500, 2900)[int(v * n)] for v in u.tolist()]
             assert bool(((r.logprob.double() + math.log(n)).abs() <= 2 ** -22 * max(1.0, math.log(n))).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("temperature", [0.8, 1.1, 1e30])
+@pytest.mark.parametrize("N", [65, 3000])
+def test_logits_further_apart_than_any_number(dtype, temperature, N):
+    """The largest finite value beside the lowest."""
+    x = torch.full((8, N), torch.finfo(TYPES[dtype]).min, dtype=TYPES[dtype], device="cuda")
+    x[:, 17] = x[:, 30] = x[:, 60] = torch.finfo(TYPES[dtype]).max
+    x[:, 40:50] = 0.0
+    u = torch.tensor([0.0, 0.2, 0.4, 0.6, 0.8, 0.9, 0.95, 0.999], device="cuda")
+    for kw in (dict(top_p=0.5), dict(top_p=0.3), dict(top_p=0.9), dict(), dict(min_p=0.1), dict(top_k=2), dict(top_k=20, top_p=0.6)):
+        r = q.sample_tokens(x, u, temperature=temperature, **kw)
+        n = kw.get("top_k", 3) if kw.get("top_k", 3) < 3 else {0.5: 2, 0.3: 1, 0.6: 2}.get(kw.get("top_p"), 3)
+        assert r.token.tolist() == [(17, 30, 60)[int(v * n)] for v in u.tolist()], kw
+        assert bool(((r.logprob.double() + math.log(n)).abs() <= 2 ** -22 * max(1.0, math.log(n))).all())
