@@ -8,9 +8,10 @@
 //
 // The G heads and m nodes that share a KV head are the rows of a 128-row tile, tiles of 64 keys
 // stream past it: S = Q K^T and O += P V on tcgen05, S and O in TMEM, a row a thread in the
-// softmax.  Reading K and V takes 4 D bytes a key for 128 x 2 x 3 D flops (P enters P V as two
-// 16-bit terms, below): 192 flops a byte, which HBM still bounds (the ridge lies at 281), however few
-// of the 128 rows a small tree fills.
+// softmax.  Reading K and V takes 4 D bytes a key (int8: 2 D) for 128 x 2 x 3 D flops (P enters P V as
+// two 16-bit terms, below) whatever rows a small tree fills: 192 flops a byte a row block, int8 384, where
+// the ridge lies at 281.  So HBM can bound one 16-bit row block alone; it does at d = 128 (74 % of its copy
+// rate), while at d = 256, with several blocks and with int8 the softmax of a tile comes first.
 //
 // Roles of a CTA's warps: 8 of softmax (two groups that take tiles in turn), 1 issuing MMAs, 1 loading
 // (d = 256: 2) and for an int8 cache 2 or 4 that widen codes to fp16 (exact).  Rings of K and of V
@@ -31,8 +32,8 @@
 // row block each (tree_schedule).
 //
 // Measured (a graph of calls, inputs larger than L2): 40 contexts of up to 8190, 24 nodes of 32/8 heads
-// of 128, bf16: 114 us, 585 MB, 75 % of the copy rate of HBM.  12 of up to 16384, 64 nodes of 24/4
-// heads of 256, fp16: 195 us; a full row block's tile takes 2730 cycles, of which the MMAs are 1930
+// of 128, bf16: 117 us, 585 MB, 74 % of the copy rate of HBM.  12 of up to 16384, 64 nodes of 24/4
+// heads of 256, fp16: 197 us; a full row block's tile takes 2730 cycles, of which the MMAs are 1930
 // (two terms of P), and the softmax of a tile bounds it.  5 of up to 65535 int8, 13 nodes: 155 us, 376
 // MB: the same softmax, with scales, and shared memory (codes in, halves out, halves read) bound it.
 //
@@ -107,7 +108,9 @@ struct TreeShape {
   static constexpr int kSmem = 1024 + kQ + 2 * kTiles * kStage + (kRawK + kRawV) * kRaw + kScaleBytes + kFixed;
   static_assert(kSmem * kCtas + 1024 * kCtas <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory");
   static_assert(kAhead + kTiles + kRawK + 2 <= kScaleSlots, "scales outlive their use");
-  // what an item costs beside its tiles, in tiles: about the time of 192 KB
+  // What an item costs beside its tiles, in tiles: about the time of 192 KB.  (us with none, 96, 192 and 384
+  // KB: 40 x 8k bf16, 24 nodes 145, 115, 117, 121; with d = 64 117, 87, 92, 104; 12 x 16k fp16, 64 nodes 165, 201,
+  // 196, 188; with d = 128 115, 114, 113, 116; 1 x 10k 32, 35, 27, 31; 40 windows of 1k 82, 56, 56, 55.)
   static constexpr int kItemCost = 196608 / (2 * kStage / (kI8 ? 2 : 1));
 };
 
@@ -389,7 +392,9 @@ __device__ __noinline__ void tree_schedule(const TreeArgs &a, TreeSeg *segs, Tre
   int R = 1, cost = IC;
   unsigned W = total[0], teams = grid, from = 0;          // the class's work, teams and first CTA
   bool all = true;                                        // every sequence is of the class
-  if (tiles <= 2 * grid) {                                // few tiles: one or two a CTA, whatever an item costs
+  // Few tiles: one or two a CTA, whatever an item costs.  (One context of 100 keys 14.5 us, with items' costs
+  // counted 15.2; 1003 keys 18.5 either way, and a limit of 1 or 4 tiles a CTA changes no form timed.)
+  if (tiles <= 2 * grid) {
     cost = 0;
     W = tiles;
   } else if (classes > 1) {
@@ -880,8 +885,8 @@ __global__ void __launch_bounds__(TreeShape<D, KV>::kThreads, TreeShape<D, KV>::
                              : "memory");
             }
           }
-          // (the codes' slot is given back only here, where every load's value has been used: an arrival
-          // right behind the loads let the next copy overtake them)
+          // (the codes' slot is given back only here, where every load's value has been used; right behind the
+          // loads, whose values need not have arrived, the next copy was seen in them)
           __syncwarp();
           if (lane == 0) mbar_arrive(raw_empty(isv, rs));
           fence_proxy_async_smem();

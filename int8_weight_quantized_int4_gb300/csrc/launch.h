@@ -147,7 +147,7 @@ struct TreeDesc {               // an item that several CTAs share, left by the 
 struct TreeArgs {
   CUtensorMap qmap, kmap, vmap; // rows of d elements, boxes of 64 elements (int8: d) and one row
   CUtensorMap kbox, vbox;       // [pages][Hkv][page][d], boxes of 64 elements (int8: d) and `box` rows
-  int box;                      // 0: the pages are no multiple of 8 rows
+  int box;                      // 0: gathers (pages of no multiple of 8 rows, a broadcast cache, no pages)
   CUtensorMap qbox;             // [T][Hkv][G][d], boxes of 64 elements and block_rows rows (G <= 128)
   int scale_boxes;              // int8: a box's scales are a multiple of 16 bytes, so aligned
   int block_rows;               // rows of an item: whole nodes (q_box), or 128

@@ -31,10 +31,11 @@
 // instead: 256 bins with counts and weights, the border's bin refined until it fits a list, and the
 // draw by sums of ever smaller ranges.
 //
-// Measured (a graph of calls): one row of 248320 fp16 with top-k 200, top-p and min-p 12.6 us, 768 rows of
-// 50257 bf16 with top-p 42 us (77 MB, 27 % of the copy rate of HBM: after the pass, 8 us of a CTA's 20,
+// Measured (a graph of calls): one row of 248320 fp16 with top-k 200, top-p and min-p 12.9 us, 768 rows of
+// 50257 bf16 with top-p 42.7 us (77 MB, 27 % of the copy rate of HBM: after the pass, 8 us of a CTA's 20,
 // three short phases of block-wide steps follow, and 768 rows are 1.3 waves), 200 rows of 32000 with no
-// filter 18.7 us.  Flat rows cost more: 64 x 128257 with a top-p of 0.95 that leaves thousands 48 us.
+// filter 20.3 us.  Flat rows cost more: 64 x 128257 fp32 with a top-p of 0.95 22.6 us at a temperature of 0.8
+// and 97 at 1, where it leaves thousands.
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
@@ -989,7 +990,8 @@ __device__ __forceinline__ void sample_draw_listed(const SampleArgs &a, SampleCt
 // A number in the elements' order: 4095 less the distance from the largest in steps of the first
 // 41 octaves' (or of the bound's) 4095th part, the order key, the column backwards (N <= 2^20).  The
 // first 12 bits spread the elements over bins, where the key alone crowds them into a few exponents
-// (64 rows of 128257 fp32, top-p 0.95: 55 us by keys, 48 so).
+// (64 rows of 128257 fp32, top-p 0.95, nine tenths masked, temperatures of 0.8, 1 and 1.2: 44, 53 and 61 us, by keys
+// 50, 59 and 67; unmasked, so with tens of thousands of them, 23, 97 and 147, by keys 24, 93 and 135).
 struct SampleOrder {
   float M, steps;
   __device__ __forceinline__ SampleOrder(const SampleScale &c, unsigned T0)
@@ -1559,8 +1561,10 @@ extern "C" int sample_tokens(const void *logits, int dtype, int M, int N, long l
                logprob};
   int cluster = 1;
   // CTAs a row: the waves of CTAs (four an SM) times a CTA's elements, a row's steps counted as
-  // 32768 (768 x 50257: 46 us with one CTA a row, 64 with two).  16 have to fit one part of the GPU; a CTA's part
-  // has below 2^18 elements.
+  // 32768.  16 have to fit one part of the GPU; a CTA's part has below 2^18 elements.  (us with 1, 2, 4, 8 and 16
+  // CTAs: 1 x 248320 31.5, 21.1, 16.0, 13.4, 12.9*; 16 x 128257 fp32 33.3, 21.6, 16.7, 14.6*; 64 x 128257 40.7, 26.4,
+  // 21.3, 22.7*; 128 x 50257 16.2, 16.4, 18.4*, 32.1; 300 x 50257 21.2, 23.2*, 42.1; 768 x 50257 42.3*, 58.9;
+  // *: the rule's.  Rows of a few thousand would do with fewer: 1 x 4096 8.5 us with one, 14.4 with the rule's 16.)
   long long best = 0;
   for (int c = 1; c <= ((long long)M * kSmMaxCluster <= sms / 2 ? kSmMaxCluster : 8); c *= 2) {
     const long long cost = ((long long)M * c + 4 * sms - 1) / (4 * sms) * (N / c + 32768);

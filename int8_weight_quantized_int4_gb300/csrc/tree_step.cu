@@ -127,7 +127,7 @@ struct KeepArgs {
 };
 constexpr int kKeepWarps = 8;
 // Rows in flight a lane.  Warps, not rows, hide the latency: with 8 rows and 100 registers 23 % of
-// an SM's warps were active and 64 sequences of 48 int8 layers (62 MB in all) took 33 us, now 18.
+// an SM's warps were active and 64 sequences of 48 int8 layers (62 MB in all) took 33 us, now 18.1.
 // (2 rows: 17, and twice the round trips of a long path.)
 constexpr int kKeepRows = 4;
 
@@ -154,7 +154,7 @@ __device__ __forceinline__ void move_rows(uint8_t *at, bool on, long long from, 
 }
 
 // One warp 32 columns of a sequence: a column is 16 bytes (4 for scales) of a row's bytes in one
-// layer and head.  Lane i looks up the i-th row's slots; eight rows are read before they are written.
+// layer and head.  Lane i looks up the i-th row's slots; kKeepRows rows are read before they are written.
 __global__ void __launch_bounds__(32 * kKeepWarps, 4) kv_keep_kernel(const __grid_constant__ KeepArgs a) {
   const int lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * kKeepWarps + (threadIdx.x >> 5);
